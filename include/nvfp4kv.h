@@ -407,6 +407,146 @@ int nvfp4kv_decode_attention_variant(int variant, const nvfp4kv_cache* cache, co
                                      float softmax_scale, void* workspace, size_t workspace_bytes,
                                      int32_t* device_status, nvfp4kv_stream_t stream);
 
+/* What happens to a score between q . k and the softmax in the scored
+ * attention calls below, for models whose attention is not the plain causal
+ * one.  With x = softmax_scale * q . khat_j, the query at position p of its
+ * sequence and the key at position j:
+ *     x <- softcap * tanh(x / softcap)          if softcap > 0
+ *     x <- x - slopes[h] * |p - j|              if slopes is not NULL
+ * and with window > 0 only keys with p - j < window, and the first `sinks`
+ * ones, are visible.  The struct itself is read on the host only; a NULL
+ * nvfp4kv_scoring pointer means none of the three. */
+typedef struct nvfp4kv_scoring {
+  float softcap;       /* 0 (no cap), or in [2^-20, 2^20] */
+  int32_t window;      /* 0 (no window), or > 0 */
+  int32_t sinks;       /* >= 0; only looked at with a window */
+  const float* slopes; /* device, finite fp32 [num_q_heads], or NULL (no bias) */
+} nvfp4kv_scoring;
+
+/*
+ * nvfp4kv_decode_attention with a scoring, a bf16 output and the log-sum-exp.
+ * The query of sequence b is its last token (position seq_lens[b] - 1).
+ *   out        device bf16 [batch][num_q_heads][head_dim], rounded once from
+ *              fp32; zeros for a sequence of length 0
+ *   lse        device fp32 [batch][num_q_heads], or NULL: the natural
+ *              logarithm of sum_j exp(x_j) over the visible tokens, -inf where
+ *              there are none (two results over disjoint keys join by it)
+ *   scoring    host struct, or NULL
+ * Pages that hold no visible token are not read, and neither are their
+ * page-table entries: the pages between the sinks and the window may have been
+ * freed or given to another sequence.  Positions are indices into the cached
+ * sequence.  |x| <= softcap is computed to about fp32's accuracy, as is the
+ * rest.  Other arguments, the workspace and errors as in
+ * nvfp4kv_decode_attention.
+ */
+int nvfp4kv_decode_attention_scored(const nvfp4kv_cache* cache, const void* q, void* out, float* lse,
+                                    const int32_t* page_table, int32_t max_pages_per_seq,
+                                    const int32_t* seq_lens, int32_t batch, int32_t num_q_heads,
+                                    float softmax_scale, const nvfp4kv_scoring* scoring, void* workspace,
+                                    size_t workspace_bytes, int32_t* device_status, nvfp4kv_stream_t stream);
+
+/*
+ * nvfp4kv_decode_attention_scored that also sums up how much attention each
+ * cached token gets, for nvfp4kv_evict.  For every sequence b, KV head hk and
+ * token t < seq_lens[b]:
+ *     weights[b][hk][t] <- decay * weights[b][hk][t]
+ *                          + sum over the head's G query heads of softmax(x)_t
+ * (tokens out of sight get 0 added); entries from seq_lens[b] on are not
+ * touched.  A new token's entry must be set (to 0) before its first step.
+ *   weights          device fp32 [batch][num_kv_heads][weight_stride]
+ *   weight_stride    >= max_pages_per_seq * page_size, or >= every seq_lens[b]
+ *                    if the caller vouches for them: it bounds the tokens
+ *                    whose sums are written (a longer sequence is an error,
+ *                    NVFP4KV_DEVERR_LENGTH, and its tokens from weight_stride
+ *                    on get no sum)
+ *   decay            finite, >= 0; 1 sums up, 0 keeps the last step's alone
+ *                    (and does not read weights)
+ *   max_total_pages  a bound of the batch's cached pages, sum over b of
+ *                    ceil(seq_lens[b] / page_size); num_pages of the cache
+ *                    serves where no page is shared.  If the batch has more,
+ *                    weights are left alone with NVFP4KV_DEVERR_LENGTH (out
+ *                    and lse are valid)
+ *   workspace        >= nvfp4kv_decode_weights_workspace_size() bytes,
+ *                    256-byte aligned: the decode's, and the visited tokens'
+ *                    scores (512 bytes per page and KV head for G > 4, 256 for
+ *                    G > 2, else 128)
+ * Other arguments and errors as in nvfp4kv_decode_attention_scored.  Enqueues
+ * three kernels.
+ */
+int nvfp4kv_decode_attention_weights(const nvfp4kv_cache* cache, const void* q, void* out, float* lse,
+                                     const int32_t* page_table, int32_t max_pages_per_seq,
+                                     const int32_t* seq_lens, int32_t batch, int32_t num_q_heads,
+                                     float softmax_scale, const nvfp4kv_scoring* scoring, float* weights,
+                                     int64_t weight_stride, float decay, int64_t max_total_pages,
+                                     void* workspace, size_t workspace_bytes, int32_t* device_status,
+                                     nvfp4kv_stream_t stream);
+
+/* Bytes of workspace of nvfp4kv_decode_attention_weights on the current CUDA
+ * device.  Host only; max_total_pages >= 0. */
+int nvfp4kv_decode_weights_workspace_size(const nvfp4kv_cache* cache, int32_t batch, int32_t num_q_heads,
+                                          int64_t max_total_pages, size_t* bytes);
+
+/* nvfp4kv_extend_attention with a scoring, further masks, a bf16 output and
+ * the log-sum-exp.  Chunk token t of sequence b has position
+ * p = prefix_lens[b] + t; its keys are low <= j <= high with
+ *     high = p, or max(p, full_lens[b] - 1) with full_lens: the sequence's
+ *            first full_lens[b] positions are seen by every query (a prefix
+ *            seen from both sides); keys past the chunk's end never are
+ *     low  = 0, or doc_starts[cu_q[b] + t] with doc_starts: the position at
+ *            which the token's document starts, for documents packed into one
+ *            sequence
+ * limited, with a window, to p - j < window or j < low + sinks.
+ *   full_lens    device int32 [batch], or NULL
+ *   doc_starts   device int32 [total_q], or NULL; values outside [0, high]
+ *                are allowed (below 0 they hide nothing)
+ *   out          device bf16 [total_q][num_q_heads][head_dim]; a row with no
+ *                visible key is zeros
+ *   lse          device fp32 [total_q][num_q_heads], or NULL; -inf for such a row
+ * Key tiles that no query of a block of rows sees are not read.  Other
+ * arguments, limits and errors as in nvfp4kv_extend_attention. */
+int nvfp4kv_extend_attention_scored(const void* q_bf16, const int64_t* cu_q, int32_t max_q_len,
+                                    const uint8_t* ws_k, const uint8_t* ws_v, const int64_t* cu_prefix,
+                                    const int32_t* prefix_lens, int32_t batch, int64_t total_rows,
+                                    int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
+                                    float k_ws_scale, float v_ws_scale, float softmax_scale,
+                                    const nvfp4kv_scoring* scoring, const int32_t* full_lens,
+                                    const int32_t* doc_starts, void* out, float* lse, int32_t* device_status,
+                                    nvfp4kv_stream_t stream);
+
+/* Eviction: keep `budget` tokens of every (sequence, KV head) and pack them
+ * into other pages of the same cache.  n = min(seq_lens[b], budget) tokens
+ * stay: all of them if there are no more, else the first `first`, the last
+ * `recent`, and of those between the budget - first - recent with the largest
+ * weights (equal weights: the lower index; a NaN counts as larger than any
+ * number).  They keep their order: token i of the packed sequence is token
+ * kept[b][hk][i] of the old one, its K and V bytes moved as they are; each KV
+ * head keeps its own tokens.  Keys carry their positions with them only if the
+ * model rotated them in; a scoring's distances count packed positions.
+ *   page_table      device int32 [batch][max_pages_per_seq], the old pages
+ *   seq_lens        device int32 [batch]
+ *   weights         device fp32 [batch][num_kv_heads][weight_stride], weight_stride
+ *                   >= max_pages_per_seq * page_size or >= every seq_lens[b]
+ *                   (longer ones are cut there, NVFP4KV_DEVERR_LENGTH)
+ *   budget, first, recent   budget > 0, first >= 0, recent >= 0, first + recent <= budget
+ *   dst_page_table  device int32 [batch][dst_max_pages_per_seq], dst_max_pages_per_seq
+ *                   >= ceil(budget / page_size); its first ceil(n / page_size)
+ *                   pages are written whole (rows past n as zeros).  They must
+ *                   differ from each other and from every page that page_table
+ *                   lists for the call
+ *   kept            device int32 [batch][num_kv_heads][budget]; -1 from n on
+ *   kept_weights    device fp32 [batch][num_kv_heads][kept_stride], or NULL:
+ *                   weights[kept], zeros from n to budget; kept_stride >= budget.
+ *                   Must not overlap weights
+ *   new_lens        device int32 [batch], or NULL: n.  May be seq_lens itself
+ * A source page id out of range reads as zeros, a destination page id out of
+ * range is not written, both with NVFP4KV_DEVERR_PAGE.  Enqueues two kernels;
+ * needs no workspace. */
+int nvfp4kv_evict(const nvfp4kv_cache* cache, const int32_t* page_table, int32_t max_pages_per_seq,
+                  const int32_t* seq_lens, int32_t batch, const float* weights, int64_t weight_stride,
+                  int32_t budget, int32_t first, int32_t recent, const int32_t* dst_page_table,
+                  int32_t dst_max_pages_per_seq, int32_t* kept, float* kept_weights, int64_t kept_stride,
+                  int32_t* new_lens, int32_t* device_status, nvfp4kv_stream_t stream);
+
 /* Global-scale calibration ("nvfp4-kv-cache-memory-wall", section 2: the
  * FP32 per-tensor scale is 1 in the uncalibrated public setting; a calibrated
  * scale maps the tensor's largest magnitude onto the largest NVFP4 magnitude,

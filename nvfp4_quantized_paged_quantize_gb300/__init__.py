@@ -64,6 +64,11 @@ class _CCache(ctypes.Structure):
     ]
 
 
+class _CScoring(ctypes.Structure):
+    _fields_ = [("softcap", ctypes.c_float), ("window", ctypes.c_int32), ("sinks", ctypes.c_int32),
+                ("slopes", ctypes.c_void_p)]
+
+
 def load(path: str | None = None, build_if_missing: bool = True):
     """Load libnvfp4kv.so (building it in-tree first if it is missing or stale).
 
@@ -103,6 +108,14 @@ def load(path: str | None = None, build_if_missing: bool = True):
     L.nvfp4kv_stream_probe.argtypes = [pc, vp, i32, vp, i32, ctypes.c_int, vp, vp, vp]
     L.nvfp4kv_decode_attention_variant.argtypes = [ctypes.c_int, pc, vp, vp, vp, i32, vp, i32, i32, f32, vp, sz, vp,
                                                    vp]
+    ps = ctypes.POINTER(_CScoring)
+    L.nvfp4kv_decode_attention_scored.argtypes = [pc, vp, vp, vp, vp, i32, vp, i32, i32, f32, ps, vp, sz, vp, vp]
+    L.nvfp4kv_decode_weights_workspace_size.argtypes = [pc, i32, i32, i64, ctypes.POINTER(sz)]
+    L.nvfp4kv_decode_attention_weights.argtypes = [pc, vp, vp, vp, vp, i32, vp, i32, i32, f32, ps, vp, i64, f32, i64,
+                                                   vp, sz, vp, vp]
+    L.nvfp4kv_extend_attention_scored.argtypes = [vp, vp, i32, vp, vp, vp, vp, i32, i64, i32, i32, i32, f32, f32, f32,
+                                                  ps, vp, vp, vp, vp, vp, vp]
+    L.nvfp4kv_evict.argtypes = [pc, vp, i32, vp, i32, vp, i64, i32, i32, i32, vp, i32, vp, vp, i64, vp, vp, vp]
     L.nvfp4kv_last_cuda_error.argtypes = []
     L.nvfp4kv_last_cuda_error.restype = ctypes.c_char_p
     L.nvfp4kv_status_string.argtypes = [ctypes.c_int]
@@ -112,7 +125,9 @@ def load(path: str | None = None, build_if_missing: bool = True):
                  "nvfp4kv_decode_attention_static", "nvfp4kv_append_decode_attention",
                  "nvfp4kv_tensor_amax", "nvfp4kv_calibrated_global_scale", "nvfp4kv_bf16_to_fp8_workspace",
                  "nvfp4kv_extend_attention", "nvfp4kv_quantize_append_fp8", "nvfp4kv_quantize_append_variant",
-                 "nvfp4kv_stream_probe", "nvfp4kv_decode_attention_variant"):
+                 "nvfp4kv_stream_probe", "nvfp4kv_decode_attention_variant", "nvfp4kv_decode_attention_scored",
+                 "nvfp4kv_decode_weights_workspace_size", "nvfp4kv_decode_attention_weights",
+                 "nvfp4kv_extend_attention_scored", "nvfp4kv_evict"):
         getattr(L, name).restype = ctypes.c_int
     _lib = L
     return L
@@ -231,6 +246,159 @@ class Cache:
     def c_struct(self) -> _CCache:
         return _CCache(_ptr(self.pages), int(self.num_pages), int(self.num_kv_heads), int(self.head_dim),
                        int(self.page_size), float(self.k_global_scale), float(self.v_global_scale))
+
+
+@dataclass
+class Scoring:
+    """What happens to a score before the softmax in the scored attention calls (include/nvfp4kv.h): a cap
+    softcap * tanh(x / softcap), a bias of -slopes[h] * distance (fp32 device tensor [Hq]), and a window of the
+    last `window` keys with the first `sinks` ones left visible.  The defaults change nothing."""
+    softcap: float = 0.0
+    window: int = 0
+    sinks: int = 0
+    slopes: object = None
+
+    def c_struct(self) -> _CScoring:
+        return _CScoring(float(self.softcap), int(self.window), int(self.sinks), _ptr(self.slopes))
+
+
+def _scoring(scoring, hq: int):
+    """The C struct of a Scoring (None stays NULL); its slopes are checked against the query heads."""
+    if scoring is None:
+        return None
+    if scoring.slopes is not None:
+        _check_tensor("slopes", scoring.slopes, "float32", (hq,))
+    return ctypes.byref(scoring.c_struct())
+
+
+def _check_tensor(name: str, x, dtype: str, shape, optional: bool = False) -> None:
+    """x is a contiguous GPU tensor of this dtype and shape (None in `shape`: any size); raises ValueError."""
+    import torch
+
+    if x is None and optional:
+        return
+    if (x is None or x.dtype is not getattr(torch, dtype) or not x.is_cuda or x.dim() != len(shape)
+            or not x.is_contiguous() or any(want is not None and got != want for got, want in zip(x.shape, shape))):
+        what = "None" if x is None else (f"{x.dtype} {tuple(x.shape)} on {x.device}"
+                                         f"{'' if x.is_contiguous() else ' (not contiguous)'}")
+        raise ValueError(f"{name}: expected a contiguous {dtype} GPU tensor of shape "
+                         f"{tuple('*' if d is None else d for d in shape)}, got {what}")
+
+
+def _check_decode(cache: "Cache", q, out, page_table, seq_lens, lse):
+    """Shapes and types of a scored decode's tensors; returns (batch, query heads, page-table columns)."""
+    if cache.mxfp4:
+        raise ValueError("the cache holds MXFP4 page-heads; the scored decodes read NVFP4 ones")
+    _check_tensor("q", q, "bfloat16", (None, None, HEAD_DIM))
+    B, Hq = int(q.shape[0]), int(q.shape[1])
+    _check_tensor("out", out, "bfloat16", (B, Hq, HEAD_DIM))
+    _check_tensor("page_table", page_table, "int32", (B, None))
+    _check_tensor("seq_lens", seq_lens, "int32", (B,))
+    _check_tensor("lse", lse, "float32", (B, Hq), optional=True)
+    return B, Hq, int(page_table.shape[1])
+
+
+def nvfp4kv_decode_attention_scored(cache: "Cache", q, out, page_table, seq_lens, softmax_scale: float, workspace,
+                                    scoring: Scoring | None = None, lse=None, device_status=None, stream=None,
+                                    workspace_bytes: int | None = None) -> None:
+    """Paged decode attention with a scoring (cap, distance bias, window with sinks): q bf16 [B, Hq, 128], out
+    bf16 [B, Hq, 128], lse fp32 [B, Hq] or None; the rest as nvfp4kv_decode_attention."""
+    B, Hq, maxp = _check_decode(cache, q, out, page_table, seq_lens, lse)
+    if workspace_bytes is None:
+        workspace_bytes = workspace.numel() * workspace.element_size()
+    c = cache.c_struct()
+    _check("nvfp4kv_decode_attention_scored",
+           _L().nvfp4kv_decode_attention_scored(ctypes.byref(c), _ptr(q), _ptr(out), _ptr(lse), _ptr(page_table), maxp,
+                                                _ptr(seq_lens), B, Hq, float(softmax_scale), _scoring(scoring, Hq),
+                                                _ptr(workspace), workspace_bytes, _ptr(device_status),
+                                                _stream(stream)))
+
+
+def nvfp4kv_decode_weights_workspace_size(cache: "Cache", batch: int, num_q_heads: int, max_total_pages: int) -> int:
+    """Workspace bytes of nvfp4kv_decode_attention_weights for a batch of at most max_total_pages cached pages."""
+    n = ctypes.c_size_t()
+    c = cache.c_struct()
+    _check("nvfp4kv_decode_weights_workspace_size",
+           _L().nvfp4kv_decode_weights_workspace_size(ctypes.byref(c), batch, num_q_heads, max_total_pages,
+                                                      ctypes.byref(n)))
+    return n.value
+
+
+def nvfp4kv_decode_attention_weights(cache: "Cache", q, out, page_table, seq_lens, softmax_scale: float, weights,
+                                     workspace, scoring: Scoring | None = None, decay: float = 1.0, lse=None,
+                                     max_total_pages: int | None = None, device_status=None, stream=None,
+                                     workspace_bytes: int | None = None) -> None:
+    """nvfp4kv_decode_attention_scored that also updates weights (fp32 [B, Hkv, tokens]): each cached token's
+    sum becomes decay * sum + the softmax weight it got from the KV head's query heads.  max_total_pages bounds
+    the batch's cached pages (default: the cache's num_pages, right where sequences share no page)."""
+    B, Hq, maxp = _check_decode(cache, q, out, page_table, seq_lens, lse)
+    _check_tensor("weights", weights, "float32", (B, cache.num_kv_heads, None))
+    if workspace_bytes is None:
+        workspace_bytes = workspace.numel() * workspace.element_size()
+    if max_total_pages is None:
+        max_total_pages = cache.num_pages
+    c = cache.c_struct()
+    _check("nvfp4kv_decode_attention_weights",
+           _L().nvfp4kv_decode_attention_weights(ctypes.byref(c), _ptr(q), _ptr(out), _ptr(lse), _ptr(page_table),
+                                                 maxp, _ptr(seq_lens), B, Hq, float(softmax_scale),
+                                                 _scoring(scoring, Hq), _ptr(weights), int(weights.shape[2]),
+                                                 float(decay), int(max_total_pages), _ptr(workspace), workspace_bytes,
+                                                 _ptr(device_status), _stream(stream)))
+
+
+def nvfp4kv_extend_attention_scored(q, cu_q, max_q_len: int, ws_k, ws_v, cu_prefix, prefix_lens, out,
+                                    softmax_scale: float, k_ws_scale: float = 1.0, v_ws_scale: float = 1.0,
+                                    scoring: Scoring | None = None, full_lens=None, doc_starts=None, lse=None,
+                                    device_status=None, stream=None) -> None:
+    """nvfp4kv_extend_attention with a scoring, a prefix mask (full_lens, int32 [B]: leading positions that every
+    query sees) and a document mask (doc_starts, int32 [total_q]: where each query's document starts); out bf16
+    [total_q, Hq, 128], lse fp32 [total_q, Hq] or None."""
+    _check_tensor("q", q, "bfloat16", (None, None, HEAD_DIM))
+    n, hq = int(q.shape[0]), int(q.shape[1])
+    _check_tensor("prefix_lens", prefix_lens, "int32", (None,))
+    B = int(prefix_lens.shape[0])
+    _check_tensor("cu_q", cu_q, "int64", (B + 1,))
+    _check_tensor("cu_prefix", cu_prefix, "int64", (None,))
+    if int(cu_prefix.shape[0]) < B:
+        raise ValueError(f"cu_prefix: {int(cu_prefix.shape[0])} entries for {B} sequences")
+    _check_tensor("ws_k", ws_k, "uint8", (None, None, HEAD_DIM))
+    _check_tensor("ws_v", ws_v, "uint8", tuple(ws_k.shape))
+    _check_tensor("out", out, "bfloat16", (n, hq, HEAD_DIM))
+    _check_tensor("full_lens", full_lens, "int32", (B,), optional=True)
+    _check_tensor("doc_starts", doc_starts, "int32", (n,), optional=True)
+    _check_tensor("lse", lse, "float32", (n, hq), optional=True)
+    _check("nvfp4kv_extend_attention_scored",
+           _L().nvfp4kv_extend_attention_scored(_ptr(q), _ptr(cu_q), int(max_q_len), _ptr(ws_k), _ptr(ws_v),
+                                                _ptr(cu_prefix), _ptr(prefix_lens), B, int(ws_k.shape[0]), hq,
+                                                int(ws_k.shape[1]), HEAD_DIM, float(k_ws_scale), float(v_ws_scale),
+                                                float(softmax_scale), _scoring(scoring, hq), _ptr(full_lens),
+                                                _ptr(doc_starts), _ptr(out), _ptr(lse), _ptr(device_status),
+                                                _stream(stream)))
+
+
+def nvfp4kv_evict(cache: "Cache", page_table, seq_lens, weights, budget: int, first: int, recent: int,
+                  dst_page_table, kept, kept_weights=None, new_lens=None, device_status=None, stream=None) -> None:
+    """Keep `budget` tokens of every (sequence, KV head) -- the first `first`, the last `recent`, and those of
+    largest weights (fp32 [B, Hkv, tokens]) -- and pack them into the pages of dst_page_table (int32 [B, >=
+    ceil(budget / 16)]).  kept: int32 [B, Hkv, budget] old indices, -1 past the end; kept_weights: fp32
+    [B, Hkv, >= budget] or None; new_lens: int32 [B] or None."""
+    if cache.mxfp4:
+        raise ValueError("the cache holds MXFP4 page-heads; eviction moves NVFP4 ones")
+    _check_tensor("seq_lens", seq_lens, "int32", (None,))
+    B, hkv = int(seq_lens.shape[0]), int(cache.num_kv_heads)
+    _check_tensor("page_table", page_table, "int32", (B, None))
+    _check_tensor("weights", weights, "float32", (B, hkv, None))
+    _check_tensor("dst_page_table", dst_page_table, "int32", (B, None))
+    _check_tensor("kept", kept, "int32", (B, hkv, int(budget)))
+    _check_tensor("kept_weights", kept_weights, "float32", (B, hkv, None), optional=True)
+    _check_tensor("new_lens", new_lens, "int32", (B,), optional=True)
+    c = cache.c_struct()
+    _check("nvfp4kv_evict",
+           _L().nvfp4kv_evict(ctypes.byref(c), _ptr(page_table), int(page_table.shape[1]), _ptr(seq_lens), B,
+                              _ptr(weights), int(weights.shape[2]), int(budget), int(first), int(recent),
+                              _ptr(dst_page_table), int(dst_page_table.shape[1]), _ptr(kept), _ptr(kept_weights),
+                              0 if kept_weights is None else int(kept_weights.shape[2]), _ptr(new_lens),
+                              _ptr(device_status), _stream(stream)))
 
 
 def nvfp4kv_status_string(status: int) -> str:
@@ -433,4 +601,6 @@ __all__ = ["Cache", "Nvfp4kvError", "load", "NVFP4KV_PAGE_HEAD_BYTES", "NVFP4KV_
            "nvfp4kv_tensor_amax", "nvfp4kv_calibrated_global_scale", "nvfp4kv_bf16_to_fp8_workspace",
            "nvfp4kv_extend_attention", "nvfp4kv_quantize_append_fp8", "nvfp4kv_quantize_append_variant",
            "nvfp4kv_stream_probe", "NVFP4KV_PROBE_DECODE_PATTERN", "NVFP4KV_PROBE_WHOLE_PAGES",
-           "nvfp4kv_decode_attention_variant"]
+           "nvfp4kv_decode_attention_variant", "Scoring", "nvfp4kv_decode_attention_scored",
+           "nvfp4kv_decode_weights_workspace_size", "nvfp4kv_decode_attention_weights",
+           "nvfp4kv_extend_attention_scored", "nvfp4kv_evict"]

@@ -215,6 +215,89 @@ int nvfp4kv_decode_attention_variant(int variant, const nvfp4kv_cache* cache, co
                                                     reinterpret_cast<cudaStream_t>(stream)));
 }
 
+// Host checks of a scoring (nullptr: none); *sc gets its value.
+static int check_scoring(const nvfp4kv_scoring* scoring, nvfp4kv_scoring* sc) {
+  *sc = nvfp4kv_scoring{0.0f, 0, 0, nullptr};
+  if (scoring == nullptr) return NVFP4KV_OK;
+  *sc = *scoring;
+  if (sc->softcap != 0.0f && !(sc->softcap >= 0x1p-20f && sc->softcap <= 0x1p+20f))
+    return NVFP4KV_ERR_INVALID_ARGUMENT;
+  if (sc->window < 0 || sc->sinks < 0 || !aligned(sc->slopes, 4)) return NVFP4KV_ERR_INVALID_ARGUMENT;
+  return NVFP4KV_OK;
+}
+
+int nvfp4kv_decode_attention_scored(const nvfp4kv_cache* cache, const void* q, void* out, float* lse,
+                                    const int32_t* page_table, int32_t max_pages_per_seq, const int32_t* seq_lens,
+                                    int32_t batch, int32_t num_q_heads, float softmax_scale,
+                                    const nvfp4kv_scoring* scoring, void* workspace, size_t workspace_bytes,
+                                    int32_t* device_status, nvfp4kv_stream_t stream) {
+  nvfp4kv_scoring sc;
+  int st = check_scoring(scoring, &sc);
+  if (st != NVFP4KV_OK) return st;
+  int nsm = 0;
+  st = check_decode(cache, q, static_cast<float*>(out), page_table, max_pages_per_seq, seq_lens, batch, num_q_heads,
+                    softmax_scale, workspace, workspace_bytes, device_status, &nsm);
+  if (st != NVFP4KV_OK) return st;
+  if (!aligned(lse, 4)) return NVFP4KV_ERR_INVALID_ARGUMENT;
+  if (batch == 0) return NVFP4KV_OK;
+  return cuda_status(nvfp4kv::launch_decode_scored(*cache, static_cast<const uint16_t*>(q),
+                                                   static_cast<uint16_t*>(out), lse, page_table, max_pages_per_seq,
+                                                   seq_lens, batch, num_q_heads, softmax_scale, sc, nullptr, workspace,
+                                                   device_status, nsm, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+// Checks of the sizes that the weights' workspace depends on, and its bytes.
+static int weights_workspace(const nvfp4kv_cache* cache, int32_t batch, int32_t num_q_heads, int64_t max_total_pages,
+                             int nsm, size_t* bytes) {
+  if (cache == nullptr || cache->num_kv_heads <= 0 || batch < 0 || num_q_heads <= 0 || max_total_pages < 0)
+    return NVFP4KV_ERR_INVALID_ARGUMENT;
+  if (num_q_heads % cache->num_kv_heads != 0) return NVFP4KV_ERR_INVALID_ARGUMENT;
+  if (num_q_heads / cache->num_kv_heads > 8) return NVFP4KV_ERR_UNSUPPORTED;
+  // page-heads of a batch stay below 2^31 (so the size below does not overflow)
+  if (max_total_pages > (int64_t(1) << 31) / cache->num_kv_heads) return NVFP4KV_ERR_UNSUPPORTED;
+  *bytes = nvfp4kv::decode_weights_workspace_bytes(nsm, batch, num_q_heads, cache->num_kv_heads, max_total_pages);
+  return NVFP4KV_OK;
+}
+
+int nvfp4kv_decode_weights_workspace_size(const nvfp4kv_cache* cache, int32_t batch, int32_t num_q_heads,
+                                          int64_t max_total_pages, size_t* bytes) {
+  if (bytes == nullptr) return NVFP4KV_ERR_INVALID_ARGUMENT;
+  size_t n = 0;
+  int st = weights_workspace(cache, batch, num_q_heads, max_total_pages, 1, &n);  // the checks, before any CUDA call
+  int nsm = 0;
+  if (st != NVFP4KV_OK || (st = current_num_sms(&nsm)) != NVFP4KV_OK) return st;
+  return weights_workspace(cache, batch, num_q_heads, max_total_pages, nsm, bytes);
+}
+
+int nvfp4kv_decode_attention_weights(const nvfp4kv_cache* cache, const void* q, void* out, float* lse,
+                                     const int32_t* page_table, int32_t max_pages_per_seq, const int32_t* seq_lens,
+                                     int32_t batch, int32_t num_q_heads, float softmax_scale,
+                                     const nvfp4kv_scoring* scoring, float* weights, int64_t weight_stride,
+                                     float decay, int64_t max_total_pages, void* workspace, size_t workspace_bytes,
+                                     int32_t* device_status, nvfp4kv_stream_t stream) {
+  nvfp4kv_scoring sc;
+  int st = check_scoring(scoring, &sc);
+  if (st != NVFP4KV_OK) return st;
+  if (weight_stride <= 0 || !std::isfinite(decay) || decay < 0.0f || max_total_pages < 0)
+    return NVFP4KV_ERR_INVALID_ARGUMENT;
+  int nsm = 0;
+  st = check_decode(cache, q, static_cast<float*>(out), page_table, max_pages_per_seq, seq_lens, batch, num_q_heads,
+                    softmax_scale, workspace, workspace_bytes, device_status, &nsm);
+  if (st != NVFP4KV_OK) return st;
+  if (!aligned(lse, 4)) return NVFP4KV_ERR_INVALID_ARGUMENT;
+  if (batch == 0) return NVFP4KV_OK;
+  if (weights == nullptr || !aligned(weights, 4)) return NVFP4KV_ERR_INVALID_ARGUMENT;
+  if (weight_stride > (int64_t(1) << 40)) return NVFP4KV_ERR_UNSUPPORTED;
+  size_t need = 0;
+  if ((st = weights_workspace(cache, batch, num_q_heads, max_total_pages, nsm, &need)) != NVFP4KV_OK) return st;
+  if (workspace_bytes < need) return NVFP4KV_ERR_WORKSPACE;
+  const nvfp4kv::DecodeWeights w = {weights, weight_stride, decay, max_total_pages};
+  return cuda_status(nvfp4kv::launch_decode_scored(*cache, static_cast<const uint16_t*>(q),
+                                                   static_cast<uint16_t*>(out), lse, page_table, max_pages_per_seq,
+                                                   seq_lens, batch, num_q_heads, softmax_scale, sc, &w, workspace,
+                                                   device_status, nsm, reinterpret_cast<cudaStream_t>(stream)));
+}
+
 int nvfp4kv_append_decode_attention(const nvfp4kv_cache* cache, const void* k, const void* v,
                                     const int64_t* slot_mapping, int64_t num_tokens, const void* q, float* out,
                                     const int32_t* page_table, int32_t max_pages_per_seq,
@@ -266,11 +349,12 @@ int nvfp4kv_bf16_to_fp8_workspace(const void* k_bf16, const void* v_bf16, const 
                                                  device_status, nsm, reinterpret_cast<cudaStream_t>(stream)));
 }
 
-int nvfp4kv_extend_attention(const void* q_bf16, const int64_t* cu_q, int32_t max_q_len, const uint8_t* ws_k,
-                             const uint8_t* ws_v, const int64_t* cu_prefix, const int32_t* prefix_lens,
-                             int32_t batch, int64_t total_rows, int32_t num_q_heads, int32_t num_kv_heads,
-                             int32_t head_dim, float k_ws_scale, float v_ws_scale, float softmax_scale,
-                             float* out, int32_t* device_status, nvfp4kv_stream_t stream) {
+// Host checks of extend arguments (nothing is enqueued); out is fp32 or bf16.
+static int check_extend(const void* q_bf16, const int64_t* cu_q, int32_t max_q_len, const uint8_t* ws_k,
+                        const uint8_t* ws_v, const int64_t* cu_prefix, const int32_t* prefix_lens, int32_t batch,
+                        int64_t total_rows, int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
+                        float k_ws_scale, float v_ws_scale, float softmax_scale, const void* out,
+                        const int32_t* device_status) {
   if (batch < 0 || max_q_len < 0 || total_rows < 0 || num_q_heads <= 0 || num_kv_heads <= 0)
     return NVFP4KV_ERR_INVALID_ARGUMENT;
   if (num_q_heads % num_kv_heads != 0) return NVFP4KV_ERR_INVALID_ARGUMENT;
@@ -287,10 +371,73 @@ int nvfp4kv_extend_attention(const void* q_bf16, const int64_t* cu_q, int32_t ma
       !aligned(cu_prefix, 8) || !aligned(prefix_lens, 4))
     return NVFP4KV_ERR_INVALID_ARGUMENT;
   if ((int64_t)max_q_len * group > (int64_t)INT32_MAX) return NVFP4KV_ERR_UNSUPPORTED;
+  return NVFP4KV_OK;
+}
+
+int nvfp4kv_extend_attention(const void* q_bf16, const int64_t* cu_q, int32_t max_q_len, const uint8_t* ws_k,
+                             const uint8_t* ws_v, const int64_t* cu_prefix, const int32_t* prefix_lens,
+                             int32_t batch, int64_t total_rows, int32_t num_q_heads, int32_t num_kv_heads,
+                             int32_t head_dim, float k_ws_scale, float v_ws_scale, float softmax_scale,
+                             float* out, int32_t* device_status, nvfp4kv_stream_t stream) {
+  const int st = check_extend(q_bf16, cu_q, max_q_len, ws_k, ws_v, cu_prefix, prefix_lens, batch, total_rows,
+                              num_q_heads, num_kv_heads, head_dim, k_ws_scale, v_ws_scale, softmax_scale, out,
+                              device_status);
+  if (st != NVFP4KV_OK || batch == 0 || max_q_len == 0) return st;
   return cuda_status(nvfp4kv::launch_extend_attention(
       static_cast<const uint16_t*>(q_bf16), cu_q, max_q_len, ws_k, ws_v, cu_prefix, prefix_lens, batch,
       total_rows, num_q_heads, num_kv_heads, k_ws_scale, v_ws_scale, softmax_scale, out, device_status,
       reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int nvfp4kv_extend_attention_scored(const void* q_bf16, const int64_t* cu_q, int32_t max_q_len, const uint8_t* ws_k,
+                                    const uint8_t* ws_v, const int64_t* cu_prefix, const int32_t* prefix_lens,
+                                    int32_t batch, int64_t total_rows, int32_t num_q_heads, int32_t num_kv_heads,
+                                    int32_t head_dim, float k_ws_scale, float v_ws_scale, float softmax_scale,
+                                    const nvfp4kv_scoring* scoring, const int32_t* full_lens,
+                                    const int32_t* doc_starts, void* out, float* lse, int32_t* device_status,
+                                    nvfp4kv_stream_t stream) {
+  nvfp4kv_scoring sc;
+  int st = check_scoring(scoring, &sc);
+  if (st != NVFP4KV_OK) return st;
+  st = check_extend(q_bf16, cu_q, max_q_len, ws_k, ws_v, cu_prefix, prefix_lens, batch, total_rows, num_q_heads,
+                    num_kv_heads, head_dim, k_ws_scale, v_ws_scale, softmax_scale, out, device_status);
+  if (st != NVFP4KV_OK) return st;
+  if (!aligned(full_lens, 4) || !aligned(doc_starts, 4) || !aligned(lse, 4)) return NVFP4KV_ERR_INVALID_ARGUMENT;
+  if (batch == 0 || max_q_len == 0) return NVFP4KV_OK;
+  return cuda_status(nvfp4kv::launch_extend_scored(
+      static_cast<const uint16_t*>(q_bf16), cu_q, max_q_len, ws_k, ws_v, cu_prefix, prefix_lens, batch, total_rows,
+      num_q_heads, num_kv_heads, k_ws_scale, v_ws_scale, softmax_scale, sc, full_lens, doc_starts,
+      static_cast<uint16_t*>(out), lse, device_status, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int nvfp4kv_evict(const nvfp4kv_cache* cache, const int32_t* page_table, int32_t max_pages_per_seq,
+                  const int32_t* seq_lens, int32_t batch, const float* weights, int64_t weight_stride,
+                  int32_t budget, int32_t first, int32_t recent, const int32_t* dst_page_table,
+                  int32_t dst_max_pages_per_seq, int32_t* kept, float* kept_weights, int64_t kept_stride,
+                  int32_t* new_lens, int32_t* device_status, nvfp4kv_stream_t stream) {
+  int st = check_cache(cache);
+  if (st != NVFP4KV_OK) return st;
+  if (batch < 0 || max_pages_per_seq <= 0 || weight_stride <= 0 || dst_max_pages_per_seq <= 0)
+    return NVFP4KV_ERR_INVALID_ARGUMENT;
+  if (budget <= 0 || first < 0 || recent < 0 || (int64_t)first + recent > budget) return NVFP4KV_ERR_INVALID_ARGUMENT;
+  const int64_t dst_pages = ((int64_t)budget + kPageSize - 1) / kPageSize;
+  if (dst_max_pages_per_seq < dst_pages || (kept_weights && kept_stride < budget)) return NVFP4KV_ERR_INVALID_ARGUMENT;
+  if (batch == 0) return NVFP4KV_OK;
+  const int64_t pairs = (int64_t)batch * cache->num_kv_heads;
+  if ((int64_t)max_pages_per_seq * kPageSize >= (int64_t(1) << 31) || weight_stride > (int64_t(1) << 40) ||
+      kept_stride > (int64_t(1) << 40) || pairs >= (int64_t(1) << 27) || pairs * dst_pages >= (int64_t(1) << 31))
+    return NVFP4KV_ERR_UNSUPPORTED;
+  if (!page_table || !seq_lens || !weights || !dst_page_table || !kept) return NVFP4KV_ERR_INVALID_ARGUMENT;
+  for (const void* ptr : {(const void*)page_table, (const void*)seq_lens, (const void*)weights,
+                          (const void*)dst_page_table, (const void*)kept, (const void*)kept_weights,
+                          (const void*)new_lens, (const void*)device_status})
+    if (!aligned(ptr, 4)) return NVFP4KV_ERR_INVALID_ARGUMENT;
+  int nsm = 0;
+  if ((st = current_num_sms(&nsm)) != NVFP4KV_OK) return st;
+  return cuda_status(nvfp4kv::launch_evict(*cache, page_table, max_pages_per_seq, seq_lens, batch, weights,
+                                           weight_stride, budget, first, recent, dst_page_table,
+                                           dst_max_pages_per_seq, kept, kept_weights, kept_stride, new_lens,
+                                           device_status, nsm, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 int nvfp4kv_tensor_amax(const void* x_bf16, int64_t n, float* amax, int accumulate,

@@ -42,6 +42,7 @@
 
 #include "nvfp4kv_device.cuh"
 #include "nvfp4kv_launch.h"
+#include "scoring.cuh"
 
 namespace nvfp4kv {
 namespace {
@@ -68,6 +69,15 @@ constexpr float kLazy = 8.0f;   // running-max slack (log2 units): P <= 2^8 in f
 // rotated on the way in and the output rotated back, both exact orthonormal
 // transforms); MXFP4 (blocks of 32 with E8M0 scales, 4 per row).
 enum : int { kFmtNvfp4 = 0, kFmtHadamard = 1, kFmtMxfp4 = 2 };
+
+// Scored decode (nvfp4kv_decode_attention_scored / _weights): bit flags of the
+// kernels' second template argument; 0 is the plain decode.
+enum : int {
+  kScored = 1,   // bf16 output, log-sum-exp, a window with sinks (both run-time: they touch no inner loop)
+  kCapped = 2,   // scores through cap * tanh(s / cap)
+  kBiased = 4,   // minus slope * distance
+  kStored = 8    // the scores of every visited token are kept for weights_kernel
+};
 
 // stage layout: the page-head as stored (K data | K scales | V data | V scales)
 constexpr int kOffKD = kOffKData;
@@ -105,6 +115,20 @@ struct DecodeParams {
   int32_t* cu_pages;  // [batch + 1], written by CTA 0: pages of the sequences before each, then of all
   int32_t ncta;       // CTAs of the decode grid (its split, rederived by the combine)
   int32_t comb_heads; // query heads per combine block
+  // scored decode only
+  float cap_scale;       // kCapped: softmax_scale * g_K / cap (score_scale is then cap * log2(e))
+  int32_t window;        // a query sees the last `window` tokens (0: all of them)
+  int32_t sinks;         // and the first `sinks`
+  const float* slopes;   // [hq], kBiased
+  uint16_t* out16;       // bf16 output
+  float* lse;            // natural log-sum-exp [batch][hq], or null
+  float* lse2;           // kStored: base-2 log-sum-exp [batch][hq]
+  float* scores;         // kStored: base-2 scores [items][16 tokens][score_heads]
+  int32_t score_heads;   // 2, 4 or 8: the group rounded up
+  long long score_items; // page-heads that `scores` has room for
+  float* weights;        // [batch][hkv][weight_stride]
+  long long weight_stride;
+  float decay;
 };
 
 // ---------------------------------------------------------------------------
@@ -121,8 +145,36 @@ __device__ __forceinline__ int clamp_len(const DecodeParams& p, int b) {
   return L;
 }
 
+// The pages of a sequence of L tokens that hold visible ones.  Without a
+// window: all of them.  With one: the pages of the first `sinks` tokens and
+// those from the window's first token on, the pages between left out (their
+// page-table entries are not read).
+struct VisiblePages {
+  int count;   // pages visited
+  int lead;    // the first `lead` of them are pages 0 .. lead - 1 ...
+  int skip;    // ... and the others come this many pages later than their index
+};
+
+template <int M>
+__device__ __forceinline__ VisiblePages visible_pages(const DecodeParams& p, int L) {
+  VisiblePages v;
+  v.count = (L + kPage - 1) / kPage;
+  v.lead = v.count;
+  v.skip = 0;
+  if constexpr (M != 0) {
+    if (p.window > 0 && L > p.window) {
+      const int first = (L - p.window) / kPage;  // page of the window's first token
+      v.lead = min(first, p.sinks / kPage + (p.sinks % kPage != 0));
+      v.skip = first - v.lead;
+      v.count -= v.skip;
+    }
+  }
+  return v;
+}
+
+template <int M>
 __device__ __forceinline__ int pages_of(const DecodeParams& p, int b) {
-  return (clamp_len(p, b) + kPage - 1) / kPage;
+  return visible_pages<M>(p, clamp_len(p, b)).count;
 }
 
 __device__ __forceinline__ float ex2(float x) {
@@ -206,6 +258,8 @@ struct ItemMap {
   int np;      // pages of the pair
   int lastnv;  // valid tokens in the pair's last page (1..16)
   int nv;      // after resolve_chunk: valid tokens of the item's page (0 for an invalid id or past the range)
+  int hole;    // scored: rows [hole & 255, hole >> 8) of the page are out of sight (0: none)
+  int dist;    // scored: the position of the page's first token minus the query's
 };
 
 // The sequence a chunk walk starts from: its index, its first page (in units
@@ -221,6 +275,7 @@ struct SeqCursor {
 // later, so the load latency is hidden behind the pages already staged.
 // `sc` is a sequence whose first page-head is <= the chunk's first item; on
 // return it is the sequence of the chunk's last valid item.
+template <int M>
 __device__ __forceinline__ ItemMap map_chunk(const DecodeParams& p, long long wr0, int i0, int n, SeqCursor& sc,
                                              int lane) {
   ItemMap m;
@@ -231,17 +286,20 @@ __device__ __forceinline__ ItemMap map_chunk(const DecodeParams& p, long long wr
   m.np = 1;
   m.lastnv = kPage;
   m.nv = 0;
+  m.hole = 0;
+  m.dist = 0;
   const int i = i0 + lane;
   int b = sc.b, cu = sc.cu, L = sc.L;
   if (i < n) {
     const long long r = wr0 + i;
-    int np = (L + kPage - 1) / kPage;
-    while (r >= (long long)(cu + np) * p.hkv) {
-      cu += np;
+    VisiblePages v = visible_pages<M>(p, L);
+    while (r >= (long long)(cu + v.count) * p.hkv) {
+      cu += v.count;
       ++b;
       L = clamp_len(p, b);
-      np = (L + kPage - 1) / kPage;
+      v = visible_pages<M>(p, L);
     }
+    const int np = v.count;
     const int local = (int)(r - (long long)cu * p.hkv);
     const int h = local / np;
     const int page = local - h * np;
@@ -249,8 +307,17 @@ __device__ __forceinline__ ItemMap map_chunk(const DecodeParams& p, long long wr
     m.pair = b * p.hkv + h;
     m.page = page;
     m.np = np;
-    m.lastnv = L - (np - 1) * kPage;
-    m.row = __ldg(p.page_table + (long long)b * p.max_pages + page);
+    m.lastnv = L - (np + v.skip - 1) * kPage;
+    const int at = page < v.lead ? page : page + v.skip;  // the page within the sequence
+    if constexpr (M != 0) {
+      const int t0 = at * kPage;
+      m.dist = t0 - (L - 1);
+      if (p.window > 0 && L > p.window) {
+        const int lo = min(max(p.sinks - t0, 0), kPage), hi = min(max(L - p.window - t0, 0), kPage);
+        if (lo < hi) m.hole = lo | (hi << 8);
+      }
+    }
+    m.row = __ldg(p.page_table + (long long)b * p.max_pages + at);
   }
   const int last = min(31, n - 1 - i0);
   sc.b = __shfl_sync(0xFFFFFFFFu, b, last);
@@ -311,10 +378,12 @@ __device__ __forceinline__ bool stage_wait(uint32_t bar, uint32_t parity) {
 
 // An item of a warp's range as the loop uses it: the byte offset of its
 // page-head in the pool and its valid tokens (0: nothing to copy or attend).
+// Scored: bits 8 and up of nv hold ItemMap::hole, so a page seen whole is
+// still nv == 16.
 struct alignas(16) ItemEntry {
   long long off;
   int nv;
-  int pad;
+  int dist;  // ItemMap::dist
 };
 
 // cp.async staging of one page-head at byte offset `off` of the pool: lane l
@@ -384,6 +453,8 @@ struct WarpState {
   float m0, m1;     // running max (base 2) of heads 2t, 2t+1
   float l0, l1;     // this lane's partial sums of P over its tokens
   float c0, c1;     // score multipliers of heads 2t, 2t+1
+  float x0, x1;     // kCapped: multipliers of the scores inside the tanh (c0, c1 come after it)
+  float b0, b1;     // kBiased: base-2 bias per token of distance
 };
 
 // Orthonormal Walsh-Hadamard transform (Sylvester order) of the 128 values of
@@ -452,8 +523,8 @@ __device__ __forceinline__ QRaw fetch_q(const DecodeParams& p, int pair, int g, 
 
 // Turn fetched q into B-fragments with a per-head power-of-two prescale and
 // reset the pair's softmax state.
-template <int F>
-__device__ __forceinline__ void load_q(const DecodeParams& p, const QRaw& raw, WarpState& s, int g, int t) {
+template <int F, int M>
+__device__ __forceinline__ void load_q(const DecodeParams& p, const QRaw& raw, WarpState& s, int pair, int g, int t) {
   float qv[32];
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
@@ -490,14 +561,57 @@ __device__ __forceinline__ void load_q(const DecodeParams& p, const QRaw& raw, W
     s.qf[i][1] = pack_f16x2(qv[4 * i + 2] * pre, qv[4 * i + 3] * pre);
   }
   const float c = p.score_scale * inv;  // score multiplier of head g
-  s.c0 = __shfl_sync(0xFFFFFFFFu, c, (2 * t) * 4);
-  s.c1 = __shfl_sync(0xFFFFFFFFu, c, (2 * t + 1) * 4);
+  if constexpr ((M & kCapped) != 0) {
+    const float x = p.cap_scale * inv;
+    s.x0 = __shfl_sync(0xFFFFFFFFu, x, (2 * t) * 4);
+    s.x1 = __shfl_sync(0xFFFFFFFFu, x, (2 * t + 1) * 4);
+    s.c0 = s.c1 = p.score_scale;
+  } else {
+    s.c0 = __shfl_sync(0xFFFFFFFFu, c, (2 * t) * 4);
+    s.c1 = __shfl_sync(0xFFFFFFFFu, c, (2 * t + 1) * 4);
+  }
+  if constexpr ((M & kBiased) != 0) {
+    const float* sl = p.slopes + (long long)(pair % p.hkv) * p.group;
+    s.b0 = 2 * t < p.group ? __ldg(sl + 2 * t) * kLog2e : 0.0f;
+    s.b1 = 2 * t + 1 < p.group ? __ldg(sl + 2 * t + 1) * kLog2e : 0.0f;
+  }
 #pragma unroll
   for (int i = 0; i < 8; ++i)
 #pragma unroll
     for (int j = 0; j < 4; ++j) s.o[i][j] = 0.0f;
   s.m0 = s.m1 = -INFINITY;
   s.l0 = s.l1 = 0.0f;
+}
+
+__device__ __forceinline__ bool in_hole(int hole, int row) { return row >= (hole & 255) && row < (hole >> 8); }
+
+// Sixteen fp32 -> bf16 (round to nearest even) at a 16-byte boundary.
+__device__ __forceinline__ void store_bf16x16(uint16_t* dst, const float (&v)[16]) {
+#pragma unroll
+  for (int j = 0; j < 2; ++j)
+    reinterpret_cast<uint4*>(dst)[j] =
+        make_uint4(pack_bf16x2(v[8 * j], v[8 * j + 1]), pack_bf16x2(v[8 * j + 2], v[8 * j + 3]),
+                   pack_bf16x2(v[8 * j + 4], v[8 * j + 5]), pack_bf16x2(v[8 * j + 6], v[8 * j + 7]));
+}
+
+// The log-sum-exp of one (sequence, query head) from its base-2 running max
+// and sum; -inf when nothing was visible.
+template <int M>
+__device__ __forceinline__ void store_lse(const DecodeParams& p, long long row, float m, float l) {
+  const float v = l > 0.0f ? m + log2f(l) : -INFINITY;
+  if (p.lse != nullptr) p.lse[row] = v * kLn2;
+  if constexpr ((M & kStored) != 0) p.lse2[row] = v;
+}
+
+// Keep a page's base-2 scores (masked ones are -inf): [16 tokens][score_heads]
+// floats, the lane's heads 2t and 2t + 1 of tokens g and g + 8; the warp's
+// stores of eight heads cover 512 contiguous bytes.
+__device__ __forceinline__ void store_scores(const DecodeParams& p, float* dst, const float (&S)[4], float c0,
+                                             float c1, int g, int t) {
+  if (dst != nullptr && 2 * t < p.score_heads) {
+    *reinterpret_cast<float2*>(dst + g * p.score_heads + 2 * t) = make_float2(S[0] * c0, S[1] * c1);
+    *reinterpret_cast<float2*>(dst + (g + 8) * p.score_heads + 2 * t) = make_float2(S[2] * c0, S[3] * c1);
+  }
 }
 
 // Phase 1 of a step: S^T = Khat q^T for NP pages (16 tokens x G heads each),
@@ -576,18 +690,52 @@ __device__ __forceinline__ void qk_phase(const uint8_t* const (&stage)[NP], cons
 
 // Phase 2: online softmax (base 2) over the NP pages' scores, one running-max
 // check for all of them; returns P^T as mma B fragments (k = tokens, n = heads).
-template <int NP, bool kFull, int F>
-__device__ __forceinline__ void softmax_phase(const float (&sc)[NP][2][4], const PageExp (&pe)[NP],
-                                              const int (&nvalid)[NP], WarpState& s, uint32_t (&pb)[NP][2], int g) {
+// Scored: S becomes the score in units of c0 / c1 -- the product itself, its
+// tanh, or (with a bias) the base-2 score, c0 = c1 = 1 from there on.
+template <int NP, bool kFull, int F, int M>
+__device__ __forceinline__ void softmax_phase(const DecodeParams& p, const float (&sc)[NP][2][4],
+                                              const PageExp (&pe)[NP], const int (&nvalid)[NP],
+                                              const int (&hole)[NP], const int (&dist)[NP], float* (&keep)[NP],
+                                              WarpState& s, uint32_t (&pb)[NP][2], int g, int t) {
   // raw scores; the running max is kept in scaled (base-2) units: max(S c) = c max(S), c > 0.
   // MXFP4: page k's weights carry 2^ve[k] (its V exponent), folded into the
   // exponent so that P stays within f16; the sums l take it out again.
   float S[NP][4];
   float mx0 = -INFINITY, mx1 = -INFINITY;
+  const float c0 = (M & kBiased) != 0 ? 1.0f : s.c0, c1 = (M & kBiased) != 0 ? 1.0f : s.c1;
+  if constexpr ((M & kCapped) != 0) {
+    float2 x[2 * NP];
+#pragma unroll
+    for (int k = 0; k < NP; ++k)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        x[2 * k + j].x = (NVFP4KV_DECODE_QK_CHAINS == 2 ? sc[k][0][2 * j] + sc[k][1][2 * j] : sc[k][0][2 * j]) * s.x0;
+        x[2 * k + j].y =
+            (NVFP4KV_DECODE_QK_CHAINS == 2 ? sc[k][0][2 * j + 1] + sc[k][1][2 * j + 1] : sc[k][0][2 * j + 1]) * s.x1;
+      }
+    tanh_warp(x);
+#pragma unroll
+    for (int k = 0; k < NP; ++k) {
+      S[k][0] = x[2 * k].x;
+      S[k][1] = x[2 * k].y;
+      S[k][2] = x[2 * k + 1].x;
+      S[k][3] = x[2 * k + 1].y;
+    }
+  }
 #pragma unroll
   for (int k = 0; k < NP; ++k) {
+    if constexpr ((M & kCapped) == 0) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) S[k][j] = NVFP4KV_DECODE_QK_CHAINS == 2 ? sc[k][0][j] + sc[k][1][j] : sc[k][0][j];
+      for (int j = 0; j < 4; ++j) S[k][j] = NVFP4KV_DECODE_QK_CHAINS == 2 ? sc[k][0][j] + sc[k][1][j] : sc[k][0][j];
+    }
+    if constexpr ((M & kBiased) != 0) {
+      // tokens g and g + 8 of the page lie dist + g and dist + g + 8 (<= 0) from the query
+      const float d0 = (float)(dist[k] + g), d1 = (float)(dist[k] + g + 8);
+      S[k][0] = fmaf(S[k][0], s.c0, s.b0 * d0);
+      S[k][1] = fmaf(S[k][1], s.c1, s.b1 * d0);
+      S[k][2] = fmaf(S[k][2], s.c0, s.b0 * d1);
+      S[k][3] = fmaf(S[k][3], s.c1, s.b1 * d1);
+    }
     if constexpr (F == kFmtMxfp4) {
 #pragma unroll
       for (int j = 0; j < 4; ++j) S[k][j] *= pe[k].kx;
@@ -596,7 +744,14 @@ __device__ __forceinline__ void softmax_phase(const float (&sc)[NP][2][4], const
       if (g >= nvalid[k]) S[k][0] = S[k][1] = -INFINITY;
       if (g + 8 >= nvalid[k]) S[k][2] = S[k][3] = -INFINITY;
     }
-    float a0 = fmaxf(S[k][0], S[k][2]) * s.c0, a1 = fmaxf(S[k][1], S[k][3]) * s.c1;
+    if constexpr (M != 0) {
+      if (!kFull && hole[k]) {  // between the sinks and the window
+        if (in_hole(hole[k], g)) S[k][0] = S[k][1] = -INFINITY;
+        if (in_hole(hole[k], g + 8)) S[k][2] = S[k][3] = -INFINITY;
+      }
+    }
+    if constexpr ((M & kStored) != 0) store_scores(p, keep[k], S[k], c0, c1, g, t);
+    float a0 = fmaxf(S[k][0], S[k][2]) * c0, a1 = fmaxf(S[k][1], S[k][3]) * c1;
     if constexpr (F == kFmtMxfp4) {
       a0 += (float)pe[k].ve;
       a1 += (float)pe[k].ve;
@@ -630,8 +785,15 @@ __device__ __forceinline__ void softmax_phase(const float (&sc)[NP][2][4], const
       o0 += (float)pe[k].ve;
       o1 += (float)pe[k].ve;
     }
-    const float p0 = ex2(fmaf(S[k][0], s.c0, o0)), p1 = ex2(fmaf(S[k][1], s.c1, o1));
-    const float p2 = ex2(fmaf(S[k][2], s.c0, o0)), p3 = ex2(fmaf(S[k][3], s.c1, o1));
+    float p0, p1, p2, p3;
+    if constexpr (M != 0 && (!kFull || (M & kBiased) != 0)) {
+      // nothing may have shown yet (rows in the hole, a bias of -inf): a maximum
+      // of -inf gives zeros
+      o0 = s.m0 == -INFINITY ? -INFINITY : o0;
+      o1 = s.m1 == -INFINITY ? -INFINITY : o1;
+    }
+    p0 = ex2(fmaf(S[k][0], c0, o0)), p1 = ex2(fmaf(S[k][1], c1, o1));
+    p2 = ex2(fmaf(S[k][2], c0, o0)), p3 = ex2(fmaf(S[k][3], c1, o1));
     if constexpr (F == kFmtMxfp4) {
       const float un = exp2_f32(-pe[k].ve);  // 2^-ve: the sum counts the plain weights
       s.l0 += (p0 + p2) * un;
@@ -647,9 +809,9 @@ __device__ __forceinline__ void softmax_phase(const float (&sc)[NP][2][4], const
 }
 
 // Phase 3: O^T += Vhat^T P^T for the NP pages.
-template <int NP, bool kFull, int F>
+template <int NP, bool kFull, int F, int M>
 __device__ __forceinline__ void pv_phase(const uint8_t* const (&stage)[NP], const int (&nvalid)[NP],
-                                         const PageExp (&pe)[NP], const uint32_t (&pb)[NP][2], WarpState& s, int g,
+                                         const int (&hole)[NP], const PageExp (&pe)[NP], const uint32_t (&pb)[NP][2], WarpState& s, int g,
                                          int t) {
 #pragma unroll
   for (int k = 0; k < NP; ++k) {
@@ -677,6 +839,14 @@ __device__ __forceinline__ void pv_phase(const uint8_t* const (&stage)[NP], cons
         if (t1 >= nvalid[k]) p01 &= 0x00FFu;
         if (t8 >= nvalid[k]) p89 &= 0xFF00u;
         if (t9 >= nvalid[k]) p89 &= 0x00FFu;
+      }
+      if constexpr (M != 0) {
+        if (!kFull && hole[k]) {
+          if (in_hole(hole[k], t0)) p01 &= 0xFF00u;
+          if (in_hole(hole[k], t1)) p01 &= 0x00FFu;
+          if (in_hole(hole[k], t8)) p89 &= 0xFF00u;
+          if (in_hole(hole[k], t9)) p89 &= 0x00FFu;
+        }
       }
       sv01 = e4m3x2_to_f16x2(p01);
       sv89 = e4m3x2_to_f16x2(p89);
@@ -713,20 +883,27 @@ __device__ __forceinline__ void pv_phase(const uint8_t* const (&stage)[NP], cons
 // NP pages of one KV head (16 tokens each, nvalid[k] of them valid) from ring
 // stages, folded into the warp's running softmax state with one max update.
 // kFull: every page has all 16 tokens (no masking code).
-template <int NP, bool kFull, int F>
-__device__ __forceinline__ void process_pages(const uint8_t* const (&stage)[NP], const int (&nvalid)[NP],
+template <int NP, bool kFull, int F, int M>
+__device__ __forceinline__ void process_pages(const DecodeParams& p, const uint8_t* const (&stage)[NP],
+                                              const int (&nv)[NP], const int (&dist)[NP], float* (&keep)[NP],
                                               WarpState& s, int g, int t) {
   float sc[NP][2][4];
   uint32_t pb[NP][2];
   PageExp pe[NP];
+  int nvalid[NP], hole[NP];
+#pragma unroll
+  for (int k = 0; k < NP; ++k) {
+    nvalid[k] = M != 0 ? nv[k] & 255 : nv[k];
+    hole[k] = M != 0 ? nv[k] >> 8 : 0;
+  }
   qk_phase<NP, F>(stage, nvalid, s, sc, pe, g, t);
-  softmax_phase<NP, kFull, F>(sc, pe, nvalid, s, pb, g);
-  pv_phase<NP, kFull, F>(stage, nvalid, pe, pb, s, g, t);
+  softmax_phase<NP, kFull, F, M>(p, sc, pe, nvalid, hole, dist, keep, s, pb, g, t);
+  pv_phase<NP, kFull, F, M>(stage, nvalid, hole, pe, pb, s, g, t);
 }
 
 // Finish a warp's piece of a pair: total l over the lanes, then either write
 // the final output (complete pair) or store the piece's record at `slot`.
-template <int F>
+template <int F, int M>
 __device__ __forceinline__ void finish_piece(const DecodeParams& p, WarpState& s, int pair, bool complete,
                                              float* slot, int g, int t) {
 #pragma unroll
@@ -737,7 +914,7 @@ __device__ __forceinline__ void finish_piece(const DecodeParams& p, WarpState& s
   const int h0 = 2 * t, h1 = 2 * t + 1;
   if (complete) {
     const int b = pair / p.hkv, h = pair - (pair / p.hkv) * p.hkv;
-    float* base = p.out + ((long long)b * p.hq + (long long)h * p.group) * kHeadDim;
+    const long long row0 = (long long)b * p.hq + (long long)h * p.group;
     const float r0 = s.l0 > 0.0f ? p.v_gscale / s.l0 : 0.0f;
     const float r1 = s.l1 > 0.0f ? p.v_gscale / s.l1 : 0.0f;
     // the lane's values of heads 2t and 2t + 1: d = 16 g + k, k = 0 .. 15
@@ -753,15 +930,23 @@ __device__ __forceinline__ void finish_piece(const DecodeParams& p, WarpState& s
       hadamard_lanes<16, 3>(v0, xs, (g << 2) | t);
       hadamard_lanes<16, 3>(v1, xs, (g << 2) | t);
     }
-    if (h0 < p.group) {
-      float4* dst = reinterpret_cast<float4*>(base + h0 * kHeadDim + 16 * g);
+    if constexpr (M != 0) {
+      if (h0 < p.group) store_bf16x16(p.out16 + (row0 + h0) * kHeadDim + 16 * g, v0);
+      if (h1 < p.group) store_bf16x16(p.out16 + (row0 + h1) * kHeadDim + 16 * g, v1);
+      if (g == 0 && h0 < p.group) store_lse<M>(p, row0 + h0, s.m0, s.l0);
+      if (g == 0 && h1 < p.group) store_lse<M>(p, row0 + h1, s.m1, s.l1);
+    } else {
+      float* base = p.out + row0 * kHeadDim;
+      if (h0 < p.group) {
+        float4* dst = reinterpret_cast<float4*>(base + h0 * kHeadDim + 16 * g);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) dst[j] = make_float4(v0[4 * j], v0[4 * j + 1], v0[4 * j + 2], v0[4 * j + 3]);
-    }
-    if (h1 < p.group) {
-      float4* dst = reinterpret_cast<float4*>(base + h1 * kHeadDim + 16 * g);
+        for (int j = 0; j < 4; ++j) dst[j] = make_float4(v0[4 * j], v0[4 * j + 1], v0[4 * j + 2], v0[4 * j + 3]);
+      }
+      if (h1 < p.group) {
+        float4* dst = reinterpret_cast<float4*>(base + h1 * kHeadDim + 16 * g);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) dst[j] = make_float4(v1[4 * j], v1[4 * j + 1], v1[4 * j + 2], v1[4 * j + 3]);
+        for (int j = 0; j < 4; ++j) dst[j] = make_float4(v1[4 * j], v1[4 * j + 1], v1[4 * j + 2], v1[4 * j + 3]);
+      }
     }
   } else {
     float4* d0 = reinterpret_cast<float4*>(slot + h0 * kHeadDim + 16 * g);
@@ -792,7 +977,20 @@ __device__ __forceinline__ long long block_sum_ll(long long v, long long* red, i
   return total;
 }
 
-template <int F>
+// The output rows of an empty sequence: zeros (and a log-sum-exp of -inf).
+template <int M>
+__device__ __forceinline__ void zero_sequence(const DecodeParams& p, int b) {
+  if constexpr (M != 0) {
+    uint4* o = reinterpret_cast<uint4*>(p.out16 + (long long)b * p.hq * kHeadDim);
+    for (int j = 0; j < p.hq * kHeadDim / 8; ++j) o[j] = make_uint4(0u, 0u, 0u, 0u);
+    for (int j = 0; j < p.hq; ++j) store_lse<M>(p, (long long)b * p.hq + j, 0.0f, 0.0f);
+  } else {
+    float4* o = reinterpret_cast<float4*>(p.out + (long long)b * p.hq * kHeadDim);
+    for (int j = 0; j < p.hq * kHeadDim / 4; ++j) o[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+  }
+}
+
+template <int F, int M>
 __global__ void __launch_bounds__(kNW * 32, kCtasPerSm) decode_kernel(const DecodeParams p) {
   extern __shared__ __align__(128) uint8_t smem[];
   uint8_t* ring = smem;
@@ -831,11 +1029,8 @@ __global__ void __launch_bounds__(kNW * 32, kCtasPerSm) decode_kernel(const Deco
     int np = 0;
     if (b < p.batch) {
       const int L = clamp_len(p, b);
-      np = (L + kPage - 1) / kPage;
-      if (L == 0 && (b % (int)gridDim.x) == (int)blockIdx.x) {
-        float4* o = reinterpret_cast<float4*>(p.out + (long long)b * p.hq * kHeadDim);
-        for (int j = 0; j < p.hq * kHeadDim / 4; ++j) o[j] = make_float4(0.f, 0.f, 0.f, 0.f);
-      }
+      np = visible_pages<M>(p, L).count;
+      if (L == 0 && (b % (int)gridDim.x) == (int)blockIdx.x) zero_sequence<M>(p, b);
     }
     int incl = np;
 #pragma unroll
@@ -852,7 +1047,10 @@ __global__ void __launch_bounds__(kNW * 32, kCtasPerSm) decode_kernel(const Deco
       total += red[w];
     }
     W = total * p.hkv;
-    if (W == 0) return;
+    if (W == 0) {
+      if ((M & kStored) != 0 && blockIdx.x == 0 && tid == 0) p.cu_pages[p.batch] = 0;
+      return;
+    }
     r0 = cta_start(blockIdx.x, W, N);
     r1 = cta_start((long long)blockIdx.x + 1, W, N);
     const int excl = (int)before + incl - np;
@@ -872,14 +1070,14 @@ __global__ void __launch_bounds__(kNW * 32, kCtasPerSm) decode_kernel(const Deco
     long long pages_local = 0;
     for (int b = tid; b < p.batch; b += kNW * 32) {
       const int L = clamp_len(p, b);
-      pages_local += (L + kPage - 1) / kPage;
-      if (L == 0 && (b % (int)gridDim.x) == (int)blockIdx.x) {
-        float4* o = reinterpret_cast<float4*>(p.out + (long long)b * p.hq * kHeadDim);
-        for (int j = 0; j < p.hq * kHeadDim / 4; ++j) o[j] = make_float4(0.f, 0.f, 0.f, 0.f);
-      }
+      pages_local += visible_pages<M>(p, L).count;
+      if (L == 0 && (b % (int)gridDim.x) == (int)blockIdx.x) zero_sequence<M>(p, b);
     }
     W = block_sum_ll(pages_local, red, warp, lane) * p.hkv;
-    if (W == 0) return;
+    if (W == 0) {
+      if ((M & kStored) != 0 && blockIdx.x == 0 && tid == 0) p.cu_pages[p.batch] = 0;
+      return;
+    }
     r0 = cta_start(blockIdx.x, W, N);
     r1 = cta_start((long long)blockIdx.x + 1, W, N);
 
@@ -887,7 +1085,7 @@ __global__ void __launch_bounds__(kNW * 32, kCtasPerSm) decode_kernel(const Deco
     int carry = 0;
     for (int base = 0; base < p.batch; base += kNW * 32) {
       const int b = base + tid;
-      const int np = b < p.batch ? pages_of(p, b) : 0;
+      const int np = b < p.batch ? pages_of<M>(p, b) : 0;
       int incl = np;
 #pragma unroll
       for (int off = 1; off < 32; off <<= 1) {
@@ -943,14 +1141,15 @@ __global__ void __launch_bounds__(kNW * 32, kCtasPerSm) decode_kernel(const Deco
     seq.b = wstart_b[warp];
     seq.cu = wstart_cu[warp];
     seq.L = clamp_len(p, seq.b);
-    ItemMap cur = map_chunk(p, wr0, 0, n, seq, lane);
+    ItemMap cur = map_chunk<M>(p, wr0, 0, n, seq, lane);
     // the first piece's q goes out before the ring prefill, so it does not
     // queue behind the pages
-    const QRaw q_first = fetch_q(p, __shfl_sync(0xFFFFFFFFu, cur.pair, 0), g, t);
+    const int pair_first = __shfl_sync(0xFFFFFFFFu, cur.pair, 0);
+    const QRaw q_first = fetch_q(p, pair_first, g, t);
     ItemMap nxt = cur;
     bool nres = true;  // nxt has been resolved (or is not used)
     if (n > 32) {
-      nxt = map_chunk(p, wr0, 32, n, seq, lane);
+      nxt = map_chunk<M>(p, wr0, 32, n, seq, lane);
       nres = false;
     }
     ItemEntry* const tab = s_items[warp];
@@ -958,8 +1157,8 @@ __global__ void __launch_bounds__(kNW * 32, kCtasPerSm) decode_kernel(const Deco
     auto entry_of = [&](const ItemMap& m) {
       ItemEntry e;
       e.off = m.row < 0 ? 0 : (long long)m.row * ph_bytes(F);
-      e.nv = m.nv;
-      e.pad = 0;
+      e.nv = M != 0 && m.nv > 0 ? m.nv | (m.hole << 8) : m.nv;
+      e.dist = M != 0 ? m.dist : 0;
       return e;
     };
     resolve_chunk(p, cur);
@@ -983,9 +1182,13 @@ __global__ void __launch_bounds__(kNW * 32, kCtasPerSm) decode_kernel(const Deco
     int st = 0;      // ring stage of the next item
     uint32_t ph = 0; // its mbarrier phase parity
     WarpState s;
-    load_q<F>(p, q_first, s, g, t);  // the first piece's q, fetched before the prefill
+    load_q<F, M>(p, q_first, s, pair_first, g, t);  // the first piece's q, fetched before the prefill
     int nseg = 0;
     int i = 0;
+    // where the scores of the warp's item k are kept (null: no room for this batch)
+    auto score_row = [&](int k) -> float* {
+      return W <= p.score_items ? p.scores + (wr0 + k) * (long long)(kPage * p.score_heads) : nullptr;
+    };
     // resolve the next chunk's map into the item table
 #define NVFP4KV_RESOLVE_NXT()                                          \
   {                                                                     \
@@ -1001,7 +1204,7 @@ __global__ void __launch_bounds__(kNW * 32, kCtasPerSm) decode_kernel(const Deco
     ++chunk;                                                    \
     nres = true;                                                \
     if ((chunk + 1) * 32 < n) {                                 \
-      nxt = map_chunk(p, wr0, (chunk + 1) * 32, n, seq, lane);  \
+      nxt = map_chunk<M>(p, wr0, (chunk + 1) * 32, n, seq, lane); \
       nres = false;                                             \
     }                                                           \
   }
@@ -1014,7 +1217,7 @@ __global__ void __launch_bounds__(kNW * 32, kCtasPerSm) decode_kernel(const Deco
       const int np = __shfl_sync(0xFFFFFFFFu, cur.np, li);
       const int iend = min(n, i + (np - page0));
       ++nseg;
-      if (nseg > 1) load_q<F>(p, fetch_q(p, pair, g, t), s, g, t);
+      if (nseg > 1) load_q<F, M>(p, fetch_q(p, pair, g, t), s, pair, g, t);
       int j = i;
       // the next item at which the chunk maps need work: the next chunk's start,
       // or half way through this chunk while the next one's rows are unresolved
@@ -1041,10 +1244,20 @@ __global__ void __launch_bounds__(kNW * 32, kCtasPerSm) decode_kernel(const Deco
           const int nv0 = tab[j & 63].nv, nv1 = tab[(j + 1) & 63].nv;
           const uint8_t* const stg[2] = {wring + st * kStageBytes, wring + st1 * kStageBytes};
           const int nvs[2] = {nv0, nv1};
-          if ((nv0 & nv1) == kPage)
-            process_pages<2, true, F>(stg, nvs, s, g, t);
-          else if (nv0 | nv1)
-            process_pages<2, false, F>(stg, nvs, s, g, t);
+          int dist[2] = {0, 0};
+          float* keep[2] = {nullptr, nullptr};
+          if constexpr ((M & kBiased) != 0) {
+            dist[0] = tab[j & 63].dist;
+            dist[1] = tab[(j + 1) & 63].dist;
+          }
+          if constexpr ((M & kStored) != 0) {
+            keep[0] = score_row(j);
+            keep[1] = score_row(j + 1);
+          }
+          if (M != 0 ? nv0 == kPage && nv1 == kPage : (nv0 & nv1) == kPage)
+            process_pages<2, true, F, M>(p, stg, nvs, dist, keep, s, g, t);
+          else if ((nv0 | nv1) || (M & kStored) != 0)  // scores are kept of pages with a bad id, too (-inf)
+            process_pages<2, false, F, M>(p, stg, nvs, dist, keep, s, g, t);
           __syncwarp();
           // refill the freed stages with items j + kStages and j + 1 + kStages
           const int ja = j + kStages, jb = ja + 1;
@@ -1078,7 +1291,11 @@ __global__ void __launch_bounds__(kNW * 32, kCtasPerSm) decode_kernel(const Deco
           const int nv0 = tab[j & 63].nv;
           const uint8_t* const stg[2] = {wring + st * kStageBytes, wring + st * kStageBytes};
           const int nvs[2] = {nv0, 0};
-          if (nv0) process_pages<2, false, F>(stg, nvs, s, g, t);
+          int dist[2] = {0, 0};
+          float* keep[2] = {nullptr, nullptr};
+          if constexpr ((M & kBiased) != 0) dist[0] = tab[j & 63].dist;
+          if constexpr ((M & kStored) != 0) keep[0] = score_row(j);
+          if (nv0 || (M & kStored) != 0) process_pages<2, false, F, M>(p, stg, nvs, dist, keep, s, g, t);
           __syncwarp();
           const int ja = j + kStages;
           if (ja < n) {
@@ -1100,7 +1317,7 @@ __global__ void __launch_bounds__(kNW * 32, kCtasPerSm) decode_kernel(const Deco
       const int last_page = page0 + (iend - i) - 1;
       const bool complete = page0 == 0 && last_page == np - 1;
       const int slot = (iend == n && nseg > 1) ? 1 : 0;
-      finish_piece<F>(p, s, pair, complete, p.part + (2 * gwarp + slot) * kRecFloats, g, t);
+      finish_piece<F, M>(p, s, pair, complete, p.part + (2 * gwarp + slot) * kRecFloats, g, t);
       i = iend;
     }
     return;
@@ -1159,7 +1376,7 @@ __device__ __forceinline__ int clamped_len(const DecodeParams& p, int b) {
 constexpr int kCombineMaxWarps = 32;
 constexpr int kCombineScanMax = 1024;  // batches up to this size: the combine sums the lengths itself
 
-template <int F>
+template <int F, int M>
 __global__ void __launch_bounds__(kCombineMaxWarps * 32) combine_kernel(const DecodeParams p) {
   __shared__ float s_m[kCombineMaxWarps][32], s_l[kCombineMaxWarps][32];
   __shared__ float4 s_o[kCombineMaxWarps][32];
@@ -1183,7 +1400,7 @@ __global__ void __launch_bounds__(kCombineMaxWarps * 32) combine_kernel(const De
     int before = 0, total = 0;
     if (scan) {
       for (int i = col; i < p.batch; i += 32) {
-        const int npi = (clamped_len(p, i) + kPage - 1) / kPage;
+        const int npi = visible_pages<M>(p, clamped_len(p, i)).count;
         total += npi;
         before += i < b ? npi : 0;
       }
@@ -1194,7 +1411,7 @@ __global__ void __launch_bounds__(kCombineMaxWarps * 32) combine_kernel(const De
       }
     }
     if (col == 0) {
-      const int np = (clamped_len(p, b) + kPage - 1) / kPage;
+      const int np = visible_pages<M>(p, clamped_len(p, b)).count;
       int rec0 = 0, wf = 0, cnt = 0;
       if (np > 0) {
         if (!scan) {
@@ -1223,12 +1440,15 @@ __global__ void __launch_bounds__(kCombineMaxWarps * 32) combine_kernel(const De
   }
   __syncthreads();
   const int rec0 = s_info[0], wf = s_info[1], cnt = s_info[2];
+  // (what is launched behind a scored decode's combine waits for the combine
+  // alone, so every block of that one waits for the decode)
+  if constexpr (M != 0) asm volatile("griddepcontrol.wait;" ::: "memory");
   if (cnt == 0) return;  // an empty sequence (the decode wrote its zeros) or one warp held the whole pair
   asm volatile("griddepcontrol.wait;" ::: "memory");
   // warp (head, grp) merges the head's records grp, grp + groups, ...: four at
   // a time, all loads issued before any is used (a warp of the decode with no
   // items marked its record m = -inf)
-  float M = -INFINITY, L = 0.0f;
+  float mrun = -INFINITY, L = 0.0f;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
   if (head < p.group) {
     for (int c0 = grp; c0 < cnt; c0 += 4 * groups) {
@@ -1248,17 +1468,17 @@ __global__ void __launch_bounds__(kCombineMaxWarps * 32) combine_kernel(const De
         }
       }
 #pragma unroll
-      for (int i = 0; i < 4; ++i) online_merge(M, L, acc, m[i], l[i], v[i]);
+      for (int i = 0; i < 4; ++i) online_merge(mrun, L, acc, m[i], l[i], v[i]);
     }
   }
-  s_m[warp][col] = M;
+  s_m[warp][col] = mrun;
   s_l[warp][col] = L;
   s_o[warp][col] = acc;
   __syncthreads();
   if (grp != 0 || head >= p.group) return;
   for (int k = 1; k < groups; ++k) {
     const int w2 = k * hb + hl;
-    online_merge(M, L, acc, s_m[w2][col], s_l[w2][col], s_o[w2][col]);
+    online_merge(mrun, L, acc, s_m[w2][col], s_l[w2][col], s_o[w2][col]);
   }
   const float sc = L > 0.0f ? p.v_gscale / L : 0.0f;
   float v[4] = {acc.x * sc, acc.y * sc, acc.z * sc, acc.w * sc};
@@ -1267,8 +1487,138 @@ __global__ void __launch_bounds__(kCombineMaxWarps * 32) combine_kernel(const De
     const int xs[5] = {1, 2, 4, 8, 16};
     hadamard_lanes<4, 5>(v, xs, col);
   }
-  reinterpret_cast<float4*>(p.out + ((long long)pair * p.group + head) * kHeadDim)[col] =
-      make_float4(v[0], v[1], v[2], v[3]);
+  const long long row = (long long)pair * p.group + head;
+  if constexpr (M != 0) {
+    reinterpret_cast<uint2*>(p.out16 + row * kHeadDim)[col] =
+        make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
+    if (col == 0) store_lse<M>(p, row, mrun, L);
+  } else {
+    reinterpret_cast<float4*>(p.out + row * kHeadDim)[col] = make_float4(v[0], v[1], v[2], v[3]);
+  }
+}
+
+// Accumulated attention weights: w[b][h][t] <- decay * w + sum over the KV
+// head's query heads of 2^(score - lse), from the scores the decode kept and
+// the pairs' log-sum-exps (base 2).  Memory-bound: per page-head 512 bytes of
+// scores (G = 8; written just before, so in part still in L2) and 64 bytes of
+// sums in and out.  A warp takes a contiguous range of the decode's page-heads,
+// as the scores lie, four at a time so that their loads overlap; lane = (token,
+// half of the heads).  Launched behind the combine as its programmatic
+// dependent.
+constexpr int kWeightWarps = 8;      // per block
+constexpr int kWeightBlocksPerSm = 6;
+constexpr int kWeightUnroll = 4;
+
+// The pair a walk over page-heads stands in.
+struct PairCursor {
+  int b, h, local;   // sequence, KV head, index among the pair's visited pages
+  int L;
+  VisiblePages v;
+};
+
+template <int kHalf>  // query heads per lane
+__global__ void __launch_bounds__(kWeightWarps * 32) weights_kernel(const DecodeParams p) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int token = lane >> 1, half = lane & 1;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const long long W = (long long)__ldcg(p.cu_pages + p.batch) * p.hkv;
+  if (W > p.score_items) {
+    if (blockIdx.x == 0 && threadIdx.x == 0) flag_error(p.status, NVFP4KV_DEVERR_LENGTH);
+    return;
+  }
+  const long long nwarps = (long long)gridDim.x * kWeightWarps, w = (long long)blockIdx.x * kWeightWarps + warp;
+  const long long r0 = W * w / nwarps, r1 = W * (w + 1) / nwarps;
+  if (r0 >= r1) return;
+  // the sequence of page-head r0: the last one whose first page-head is <= r0
+  // (a 32-way search of the page prefix)
+  PairCursor c;
+  {
+    int lo = 0, hi = p.batch;  // the answer lies in [lo, hi)
+    while (hi - lo > 1) {
+      const int step = (hi - lo + 31) / 32, at = lo + lane * step;
+      const bool before = at < hi && (long long)__ldcg(p.cu_pages + at) * p.hkv <= r0;
+      const int k = __popc(__ballot_sync(0xFFFFFFFFu, before)) - 1;  // lane 0's always is
+      lo += k * step;
+      hi = min(hi, lo + step);
+    }
+    c.b = lo;
+    c.L = clamped_len(p, lo);
+    c.v = visible_pages<kScored>(p, c.L);
+    const int in = (int)(r0 - (long long)__ldcg(p.cu_pages + lo) * p.hkv);
+    c.h = in / c.v.count;
+    c.local = in - c.h * c.v.count;
+  }
+  float lse[kHalf];  // of the lane's heads; +inf where nothing was visible or there is no such head
+  auto fetch_lse = [&]() {
+#pragma unroll
+    for (int k = 0; k < kHalf; ++k) {
+      const int head = half * kHalf + k;
+      float v = -INFINITY;
+      if (head < p.group) v = __ldcg(p.lse2 + ((long long)c.b * p.hkv + c.h) * p.group + head);
+      lse[k] = v == -INFINITY ? INFINITY : v;
+    }
+  };
+  fetch_lse();
+  const float* src = p.scores + (token * 2 + half) * kHalf;
+  for (long long r = r0; r < r1; r += kWeightUnroll) {
+    float x[kWeightUnroll][kHalf], ls[kWeightUnroll][kHalf], old[kWeightUnroll];
+    float* dst[kWeightUnroll];
+#pragma unroll
+    for (int k = 0; k < kWeightUnroll; ++k) {
+      dst[k] = nullptr;
+      old[k] = 0.0f;
+#pragma unroll
+      for (int i = 0; i < kHalf; ++i) x[k][i] = ls[k][i] = 0.0f;
+      if (r + k >= r1) continue;
+      const float* row = src + (r + k) * (long long)(2 * kPage * kHalf);
+      if constexpr (kHalf == 4) {
+        const float4 v = __ldcs(reinterpret_cast<const float4*>(row));
+        x[k][0] = v.x, x[k][1] = v.y, x[k][2] = v.z, x[k][3] = v.w;
+      } else if constexpr (kHalf == 2) {
+        const float2 v = __ldcs(reinterpret_cast<const float2*>(row));
+        x[k][0] = v.x, x[k][1] = v.y;
+      } else {
+        x[k][0] = __ldcs(row);
+      }
+      if (c.local == c.v.count) {  // the next pair
+        c.local = 0;
+        if (++c.h == p.hkv) {
+          c.h = 0;
+          do {
+            ++c.b;
+            c.L = clamped_len(p, c.b);
+          } while (c.L == 0);
+          c.v = visible_pages<kScored>(p, c.L);
+        }
+        fetch_lse();
+      }
+#pragma unroll
+      for (int i = 0; i < kHalf; ++i) ls[k][i] = lse[i];
+      float* base = p.weights + ((long long)c.b * p.hkv + c.h) * p.weight_stride;
+      const int t = (c.local < c.v.lead ? c.local : c.local + c.v.skip) * kPage + token;
+      if (t >= p.weight_stride && t < c.L) flag_error(p.status, NVFP4KV_DEVERR_LENGTH);
+      if (half == 0 && t < c.L && t < p.weight_stride) {
+        dst[k] = base + t;
+        if (p.decay != 0.0f) old[k] = *dst[k];
+      }
+      if (c.v.skip > 0 && p.decay != 1.0f) {
+        // the pages out of sight decay as well: an equal share of them for each page seen
+        const long long f0 = (c.v.lead + (long long)c.v.skip * c.local / c.v.count) * kPage;
+        const long long f1 =
+            min((c.v.lead + (long long)c.v.skip * (c.local + 1) / c.v.count) * kPage, p.weight_stride);
+        for (long long f = f0 + lane; f < f1; f += 32) base[f] = p.decay == 0.0f ? 0.0f : p.decay * base[f];
+      }
+      ++c.local;
+    }
+#pragma unroll
+    for (int k = 0; k < kWeightUnroll; ++k) {
+      float sum = 0.0f;
+#pragma unroll
+      for (int i = 0; i < kHalf; ++i) sum += ex2(x[k][i] - ls[k][i]);
+      sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 1);
+      if (dst[k] != nullptr) *dst[k] = fmaf(p.decay, old[k], sum);
+    }
+  }
 }
 
 }  // namespace
@@ -1288,24 +1638,32 @@ size_t decode_workspace_bound(int num_sms, int32_t batch, int32_t num_q_heads) {
 
 namespace {
 
+size_t up256(size_t n) { return (n + 255) / 256 * 256; }
+
+// Query heads of a group as the kept scores are laid out.
+int score_heads_of(int group) { return group <= 2 ? 2 : group <= 4 ? 4 : 8; }
+
+}  // namespace
+
+size_t decode_weights_workspace_bytes(int num_sms, int32_t batch, int32_t num_q_heads, int32_t num_kv_heads,
+                                      int64_t max_total_pages) {
+  const size_t lse = up256((size_t)batch * num_q_heads * sizeof(float));
+  const size_t row = (size_t)kPage * score_heads_of(num_q_heads / num_kv_heads) * sizeof(float);
+  return up256(decode_workspace_bytes(num_sms, batch, num_kv_heads)) + lse +
+         (size_t)max_total_pages * num_kv_heads * row;
+}
+
+namespace {
+
 template <int F>
-cudaError_t launch_decode_fmt(const nvfp4kv_cache& c, const uint16_t* q, float* out, const int32_t* page_table,
-                              int32_t max_pages, const int32_t* seq_lens, int32_t batch, int32_t num_q_heads,
-                              float softmax_scale, void* workspace, int32_t* device_status, int num_sms,
-                              cudaStream_t stream, bool after_kernel) {
-  // the shared-memory limit is an attribute of the function on each device
-  static PerDeviceOnce attr_once;
-  const cudaError_t ae = attr_once.run([] {
-    return cudaFuncSetAttribute(decode_kernel<F>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
-  });
-  if (ae != cudaSuccess) return ae;
-  const int num_ctas = decode_num_ctas(num_sms);
-  DecodeParams p;
+DecodeParams decode_params(const nvfp4kv_cache& c, const uint16_t* q, const int32_t* page_table, int32_t max_pages,
+                           const int32_t* seq_lens, int32_t batch, int32_t num_q_heads, float softmax_scale,
+                           void* workspace, int32_t* device_status, int num_sms) {
+  DecodeParams p = {};
   p.pages = c.pages;
   p.num_pages = (int32_t)c.num_pages;
   p.hkv = c.num_kv_heads;
   p.q = q;
-  p.out = out;
   p.page_table = page_table;
   p.max_pages = max_pages;
   p.seq_lens = seq_lens;
@@ -1316,35 +1674,53 @@ cudaError_t launch_decode_fmt(const nvfp4kv_cache& c, const uint16_t* q, float* 
   const float gk = F == kFmtMxfp4 ? 1.0f : c.k_global_scale, gv = F == kFmtMxfp4 ? 1.0f : c.v_global_scale;
   p.score_scale = softmax_scale * 1.4426950408889634f * gk;
   p.v_gscale = gv;
-  const size_t pairs = (size_t)batch * (size_t)c.num_kv_heads;
-  size_t rec = 2 * (size_t)num_ctas * kNW * kRecFloats * sizeof(float);
-  rec = (rec + 255) / 256 * 256;
+  p.ncta = decode_num_ctas(num_sms);
   p.part = static_cast<float*>(workspace);
-  p.cu_pages = reinterpret_cast<int32_t*>(static_cast<uint8_t*>(workspace) + rec);
+  p.cu_pages = reinterpret_cast<int32_t*>(static_cast<uint8_t*>(workspace) +
+                                          up256(2 * (size_t)p.ncta * kNW * kRecFloats * sizeof(float)));
   p.status = device_status;
-  p.ncta = num_ctas;
+  return p;
+}
+
+// A launch that may start before the kernel ahead of it on the stream has
+// finished (a programmatic dependent).
+template <class K>
+cudaError_t launch_dependent(K kernel, dim3 grid, int threads, size_t smem, cudaStream_t stream,
+                             const DecodeParams& p) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, p);
+}
+
+// The decode and its combine.
+template <int F, int M>
+cudaError_t enqueue_decode(DecodeParams p, cudaStream_t stream, bool after_kernel) {
+  // the shared-memory limit is an attribute of the function on each device
+  static PerDeviceOnce attr_once;
+  const cudaError_t ae = attr_once.run([] {
+    return cudaFuncSetAttribute(decode_kernel<F, M>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+  });
+  if (ae != cudaSuccess) return ae;
+  const int num_ctas = p.ncta;
   cudaError_t e;
   if (after_kernel) {
     // a programmatic dependent of the kernel before it on the stream
-    cudaLaunchConfig_t dc = {};
-    dc.gridDim = dim3((unsigned)num_ctas);
-    dc.blockDim = dim3(kNW * 32);
-    dc.dynamicSmemBytes = kSmemBytes;
-    dc.stream = stream;
-    cudaLaunchAttribute da[1];
-    da[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    da[0].val.programmaticStreamSerializationAllowed = 1;
-    dc.attrs = da;
-    dc.numAttrs = 1;
-    e = cudaLaunchKernelEx(&dc, decode_kernel<F>, p);
+    e = launch_dependent(decode_kernel<F, M>, dim3((unsigned)num_ctas), kNW * 32, kSmemBytes, stream, p);
   } else {
-    decode_kernel<F><<<num_ctas, kNW * 32, kSmemBytes, stream>>>(p);
+    decode_kernel<F, M><<<num_ctas, kNW * 32, kSmemBytes, stream>>>(p);
     e = cudaGetLastError();
   }
+  const size_t pairs = (size_t)p.batch * (size_t)p.hkv;
   if (e != cudaSuccess || pairs == 0) return e;
   // the combine, as a programmatic dependent of the decode on the same stream
-  // records per cut pair are about (warps / pairs) when the sequences are
-  // alike: give each thread a handful of them
   // records per cut pair are about (warps / pairs) when the sequences are
   // alike: a record group per four to eight of them, up to 16 groups per head,
   // and as many of the pair's query heads per block as fit 32 warps
@@ -1353,21 +1729,75 @@ cudaError_t launch_decode_fmt(const nvfp4kv_cache& c, const uint16_t* q, float* 
   while (groups < kCombineMaxGroups && groups * 8 < per_pair) groups *= 2;
   const int hb = p.group < kCombineMaxWarps / groups ? p.group : kCombineMaxWarps / groups;
   p.comb_heads = hb;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)pairs, (unsigned)((p.group + hb - 1) / hb));
-  cfg.blockDim = dim3(32 * hb * groups);
-  cfg.dynamicSmemBytes = 0;
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, combine_kernel<F>, p);
-  return e;
+  return launch_dependent(combine_kernel<F, M>, dim3((unsigned)pairs, (unsigned)((p.group + hb - 1) / hb)),
+                          32 * hb * groups, 0, stream, p);
+}
+
+template <int F>
+cudaError_t launch_decode_fmt(const nvfp4kv_cache& c, const uint16_t* q, float* out, const int32_t* page_table,
+                              int32_t max_pages, const int32_t* seq_lens, int32_t batch, int32_t num_q_heads,
+                              float softmax_scale, void* workspace, int32_t* device_status, int num_sms,
+                              cudaStream_t stream, bool after_kernel) {
+  DecodeParams p = decode_params<F>(c, q, page_table, max_pages, seq_lens, batch, num_q_heads, softmax_scale,
+                                    workspace, device_status, num_sms);
+  p.out = out;
+  return enqueue_decode<F, 0>(p, stream, after_kernel);
+}
+
+template <int M>
+cudaError_t enqueue_scored(const DecodeParams& p, cudaStream_t stream) {
+  return enqueue_decode<kFmtNvfp4, M>(p, stream, false);
 }
 
 }  // namespace
+
+cudaError_t launch_decode_scored(const nvfp4kv_cache& c, const uint16_t* q, uint16_t* out, float* lse,
+                                 const int32_t* page_table, int32_t max_pages, const int32_t* seq_lens,
+                                 int32_t batch, int32_t num_q_heads, float softmax_scale,
+                                 const nvfp4kv_scoring& sc, const DecodeWeights* weights, void* workspace,
+                                 int32_t* device_status, int num_sms, cudaStream_t stream) {
+  DecodeParams p = decode_params<kFmtNvfp4>(c, q, page_table, max_pages, seq_lens, batch, num_q_heads,
+                                            softmax_scale, workspace, device_status, num_sms);
+  p.out16 = out;
+  p.lse = lse;
+  p.window = sc.window;
+  p.sinks = sc.sinks;
+  p.slopes = sc.slopes;
+  int m = kScored;
+  if (sc.softcap > 0.0f) {
+    m |= kCapped;
+    p.cap_scale = (float)((double)softmax_scale * (double)c.k_global_scale / (double)sc.softcap);
+    p.score_scale = (float)((double)sc.softcap * 1.4426950408889634);
+  }
+  if (sc.slopes != nullptr) m |= kBiased;
+  if (weights == nullptr) {
+    switch (m) {
+      case kScored: return enqueue_scored<kScored>(p, stream);
+      case kScored | kCapped: return enqueue_scored<kScored | kCapped>(p, stream);
+      case kScored | kBiased: return enqueue_scored<kScored | kBiased>(p, stream);
+      default: return enqueue_scored<kScored | kCapped | kBiased>(p, stream);
+    }
+  }
+  uint8_t* at = static_cast<uint8_t*>(workspace) + up256(decode_workspace_bytes(num_sms, batch, p.hkv));
+  p.lse2 = reinterpret_cast<float*>(at);
+  p.scores = reinterpret_cast<float*>(at + up256((size_t)batch * num_q_heads * sizeof(float)));
+  p.score_heads = score_heads_of(p.group);
+  p.score_items = weights->max_total_pages * p.hkv;
+  p.weights = weights->sums;
+  p.weight_stride = weights->stride;
+  p.decay = weights->decay;
+  cudaError_t e;
+  switch (m) {
+    case kScored: e = enqueue_scored<kScored | kStored>(p, stream); break;
+    case kScored | kCapped: e = enqueue_scored<kScored | kStored | kCapped>(p, stream); break;
+    case kScored | kBiased: e = enqueue_scored<kScored | kStored | kBiased>(p, stream); break;
+    default: e = enqueue_scored<kScored | kStored | kCapped | kBiased>(p, stream); break;
+  }
+  if (e != cudaSuccess) return e;
+  const dim3 grid((unsigned)(num_sms * kWeightBlocksPerSm));
+  auto kernel = p.score_heads == 8 ? weights_kernel<4> : p.score_heads == 4 ? weights_kernel<2> : weights_kernel<1>;
+  return launch_dependent(kernel, grid, kWeightWarps * 32, 0, stream, p);
+}
 
 cudaError_t launch_decode(const nvfp4kv_cache& c, const uint16_t* q, float* out, const int32_t* page_table,
                           int32_t max_pages, const int32_t* seq_lens, int32_t batch, int32_t num_q_heads,

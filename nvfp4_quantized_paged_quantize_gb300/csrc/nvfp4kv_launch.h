@@ -74,6 +74,14 @@ cudaError_t launch_extend_attention(const uint16_t* q, const int64_t* cu_q, int3
                                     float k_ws_scale, float v_ws_scale, float softmax_scale, float* out,
                                     int32_t* device_status, cudaStream_t stream);
 
+// The same with scored attention and further masks (bf16 out).
+cudaError_t launch_extend_scored(const uint16_t* q, const int64_t* cu_q, int32_t max_q_len, const uint8_t* ws_k,
+                                 const uint8_t* ws_v, const int64_t* cu_prefix, const int32_t* prefix_lens,
+                                 int32_t batch, int64_t total_rows, int32_t num_q_heads, int32_t num_kv_heads,
+                                 float k_ws_scale, float v_ws_scale, float softmax_scale, const nvfp4kv_scoring& sc,
+                                 const int32_t* full_lens, const int32_t* doc_starts, uint16_t* out, float* lse,
+                                 int32_t* device_status, cudaStream_t stream);
+
 // Largest |x| of n bf16 values into the device float *amax (zeroed first
 // unless accumulate, which folds into the value already there).
 cudaError_t launch_tensor_amax(const uint16_t* x, int64_t n, float* amax, bool accumulate, int num_sms,
@@ -99,6 +107,30 @@ cudaError_t launch_decode_variant(int variant, const nvfp4kv_cache& c, const uin
                                   const int32_t* page_table, int32_t max_pages, const int32_t* seq_lens,
                                   int32_t batch, int32_t num_q_heads, float softmax_scale, void* workspace,
                                   int32_t* device_status, int num_sms, cudaStream_t stream);
+
+// The decode with scored attention (bf16 out); with `weights`, each cached
+// token's attention weight is added to its running sum afterwards.
+struct DecodeWeights {
+  float* sums;              // [batch][num_kv_heads][stride]
+  int64_t stride;
+  float decay;
+  int64_t max_total_pages;  // pages of the batch that the workspace holds scores of
+};
+cudaError_t launch_decode_scored(const nvfp4kv_cache& c, const uint16_t* q, uint16_t* out, float* lse,
+                                 const int32_t* page_table, int32_t max_pages, const int32_t* seq_lens,
+                                 int32_t batch, int32_t num_q_heads, float softmax_scale,
+                                 const nvfp4kv_scoring& sc, const DecodeWeights* weights, void* workspace,
+                                 int32_t* device_status, int num_sms, cudaStream_t stream);
+// Workspace of the decode with weights: the decode's, the log-sum-exps, the kept scores.
+size_t decode_weights_workspace_bytes(int num_sms, int32_t batch, int32_t num_q_heads, int32_t num_kv_heads,
+                                      int64_t max_total_pages);
+
+// Keep `budget` tokens per pair by their weights and pack them into other pages.
+cudaError_t launch_evict(const nvfp4kv_cache& c, const int32_t* page_table, int32_t max_pages,
+                         const int32_t* seq_lens, int32_t batch, const float* weights, int64_t weight_stride,
+                         int32_t budget, int32_t first, int32_t recent, const int32_t* dst_table,
+                         int32_t dst_max_pages, int32_t* kept, float* kept_weights, int64_t kept_stride,
+                         int32_t* new_lens, int32_t* device_status, int num_sms, cudaStream_t stream);
 
 cudaError_t launch_decode(const nvfp4kv_cache& c, const uint16_t* q, float* out,
                           const int32_t* page_table, int32_t max_pages, const int32_t* seq_lens,

@@ -1,0 +1,83 @@
+// scoring.cuh -- what the scored attention calls do to a score before the
+// softmax: a cap through tanh, computed on the FMA pipe two scores at a time.
+#pragma once
+
+#include <cstdint>
+
+namespace nvfp4kv {
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+// Two fp32 -> two bf16 (round to nearest even), `lo` in the low half.
+__device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+// Two fp32 products / fused multiply-adds per instruction.
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;"
+      : "=l"(r)
+      : "l"(*reinterpret_cast<uint64_t*>(&a)), "l"(*reinterpret_cast<uint64_t*>(&b)));
+  return *reinterpret_cast<float2*>(&r);
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;"
+      : "=l"(r)
+      : "l"(*reinterpret_cast<uint64_t*>(&a)), "l"(*reinterpret_cast<uint64_t*>(&b)),
+        "l"(*reinterpret_cast<uint64_t*>(&c)));
+  return *reinterpret_cast<float2*>(&r);
+}
+__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
+
+// tanh on |x| <= 1: x + x^3 P(x^2), P of degree 5, fitted here to tanh in the
+// relative maximum norm (5.5e-8 before rounding; with fp32 steps within 1.5e-7
+// of tanh over the whole interval).
+__device__ __forceinline__ float2 tanh_unit(float2 x) {
+  const float2 u = mul2(x, x);
+  float2 p = both(0x1.156afp-10f);
+  p = fma2(p, u, both(-0x1.9a364ap-8f));
+  p = fma2(p, u, both(0x1.4d9306p-6f));
+  p = fma2(p, u, both(-0x1.b642ecp-5f));
+  p = fma2(p, u, both(0x1.10ecc4p-3f));
+  p = fma2(p, u, both(-0x1.55546cp-2f));
+  return fma2(mul2(x, u), p, x);
+}
+
+// tanh for |x| > 1: 1 - 2 / (e^{2|x|} + 1) with the sign of x; the value is
+// above 0.76 there, so the error of the exponential and the quotient (a few
+// 1e-7 of 2 / (e^2 + 1)) stays below fp32's last place of it.
+__device__ __forceinline__ float tanh_outer(float x) {
+  float e, r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(fabsf(x) * (2.0f * kLog2e)));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(e + 1.0f));
+  return copysignf(fmaf(-2.0f, r, 1.0f), x);
+}
+
+// x <- tanh(x) for N pairs per lane.  Scores beyond their cap (|x| > 1) are
+// rare in practice, so the outer form (two special-function operations a
+// score, against nine packed FMA-pipe ones a pair) runs only when some lane of
+// the warp holds one.
+template <int N>
+__device__ __forceinline__ void tanh_warp(float2 (&x)[N]) {
+  float top = 0.0f;
+#pragma unroll
+  for (int i = 0; i < N; ++i) top = fmaxf(top, fmaxf(fabsf(x[i].x), fabsf(x[i].y)));
+  if (__any_sync(0xFFFFFFFFu, top > 1.0f)) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const float2 t = tanh_unit(x[i]);
+      x[i].x = fabsf(x[i].x) > 1.0f ? tanh_outer(x[i].x) : t.x;
+      x[i].y = fabsf(x[i].y) > 1.0f ? tanh_outer(x[i].y) : t.y;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i) x[i] = tanh_unit(x[i]);
+  }
+}
+
+}  // namespace nvfp4kv

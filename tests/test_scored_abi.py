@@ -1,0 +1,145 @@
+"""Host-side refusals of the scored attention calls and the eviction (no GPU:
+every check here returns before anything touches CUDA), and the references the
+GPU tests use, pinned to torch's own attention."""
+import ctypes
+
+import numpy as np
+import pytest
+import torch
+
+import nvfp4_quantized_paged_quantize_gb300 as kv
+
+INVALID, UNSUPPORTED, OK = kv.NVFP4KV_ERR_INVALID_ARGUMENT, kv.NVFP4KV_ERR_UNSUPPORTED, kv.NVFP4KV_OK
+
+
+@pytest.fixture(scope="module")
+def lib():
+    return kv.load()
+
+
+def _cache(**kw):
+    c = kv.Cache(0x10000, 4, 2)
+    for k, v in kw.items():
+        setattr(c, k, v)
+    return c.c_struct()
+
+
+def _call(fn, good):
+    def call(**kw):
+        a = list(good)
+        for k, v in kw.items():
+            a[int(k[1:])] = v
+        return fn(*a)
+    return call
+
+
+BAD_SCORINGS = [dict(softcap=-1.0), dict(softcap=float("nan")), dict(softcap=float("inf")), dict(softcap=1e-9),
+                dict(softcap=2e6), dict(window=-1), dict(sinks=-1, window=5), dict(slopes=0x1001)]
+
+
+def test_scored_decode_refusals(lib):
+    cs = ctypes.byref(_cache())
+    sc = kv.Scoring(softcap=1.0).c_struct()
+    # (cache, q, out, lse, page_table, max_pages, seq_lens, batch, hq, scale, scoring, ws, ws_bytes, status, stream)
+    call = _call(lib.nvfp4kv_decode_attention_scored,
+                 [cs, 16, 16, 4, 4, 1, 4, 0, 8, 0.1, ctypes.byref(sc), 256, 1 << 20, None, None])
+    assert call() == OK                                                        # an empty batch
+    for bad in BAD_SCORINGS:
+        assert call(a10=ctypes.byref(kv.Scoring(**bad).c_struct())) == INVALID, bad
+    assert call(a0=None) == INVALID and call(a3=6) == INVALID and call(a8=7) == INVALID
+    assert call(a8=18) == UNSUPPORTED                                          # nine query heads per KV head
+    assert call(a9=float("nan")) == INVALID and call(a7=-1) == INVALID
+    assert call(a7=1, a1=None) == INVALID and call(a7=1, a2=24) == INVALID     # null q, misaligned out
+    assert call(a0=ctypes.byref(_cache(head_dim=64))) == UNSUPPORTED
+    assert call(a10=None) == OK                                                # no scoring
+
+
+def test_weights_refusals(lib):
+    cs = ctypes.byref(_cache())
+    # (..., scale, scoring, weights, stride, decay, max_total_pages, ws, ws_bytes, status, stream)
+    call = _call(lib.nvfp4kv_decode_attention_weights,
+                 [cs, 16, 16, None, 4, 1, 4, 0, 8, 0.1, None, 4, 16, 1.0, 4, 256, 1 << 20, None, None])
+    assert call() == OK
+    assert call(a12=0) == INVALID and call(a13=-0.5) == INVALID and call(a13=float("nan")) == INVALID
+    assert call(a13=float("inf")) == INVALID and call(a14=-1) == INVALID
+    n = ctypes.c_size_t()
+    size = lib.nvfp4kv_decode_weights_workspace_size
+    assert size(cs, 1, 8, 4, None) == INVALID and size(None, 1, 8, 4, ctypes.byref(n)) == INVALID
+    assert size(cs, -1, 8, 4, ctypes.byref(n)) == INVALID and size(cs, 1, 7, 4, ctypes.byref(n)) == INVALID
+    assert size(cs, 1, 8, -1, ctypes.byref(n)) == INVALID and size(cs, 1, 18, 4, ctypes.byref(n)) == UNSUPPORTED
+    assert size(cs, 1, 8, 1 << 40, ctypes.byref(n)) == UNSUPPORTED
+
+
+def test_scored_extend_refusals(lib):
+    good = [16, 8, 4, 16, 16, 8, 4, 2, 100, 8, 2, 128, 1.0, 1.0, 0.1, None, None, None, 16, None, None, None]
+    call = _call(lib.nvfp4kv_extend_attention_scored, good)
+    for bad in BAD_SCORINGS:
+        assert call(a15=ctypes.byref(kv.Scoring(**bad).c_struct())) == INVALID, bad
+    assert call(a9=6) == UNSUPPORTED and call(a9=7) == INVALID and call(a11=64) == UNSUPPORTED
+    assert call(a16=6) == INVALID and call(a17=2) == INVALID and call(a19=1) == INVALID   # misaligned masks, lse
+    assert call(a18=None) == INVALID and call(a18=24) == INVALID
+    assert call(a7=0) == OK and call(a2=0) == OK
+
+
+def test_eviction_refusals(lib):
+    cs = ctypes.byref(_cache())
+    # (cache, pt, max_pages, lens, batch, weights, stride, budget, first, recent, dst_pt, dst_max, kept, kw, kw_stride,
+    #  new_lens, status, stream)
+    call = _call(lib.nvfp4kv_evict, [cs, 4, 8, 4, 0, 4, 128, 64, 4, 16, 4, 4, 4, 4, 64, 4, None, None])
+    assert call() == OK
+    assert call(a7=0) == INVALID and call(a8=-1) == INVALID and call(a9=-1) == INVALID
+    assert call(a8=49) == INVALID                                              # first + recent > budget
+    assert call(a8=2 ** 31 - 1, a9=2 ** 31 - 1) == INVALID                     # whose sum passes 32 bits
+    assert call(a11=3) == INVALID                                              # too few destination pages
+    assert call(a14=63) == INVALID and call(a13=None, a14=0) == OK
+    assert call(a2=0) == INVALID and call(a6=0) == INVALID and call(a4=-1) == INVALID
+    assert call(a4=1, a12=None) == INVALID and call(a4=1, a10=None) == INVALID and call(a4=1, a5=6) == INVALID
+    assert call(a4=1, a2=1 << 27) == UNSUPPORTED                               # tokens past 32 bits
+    assert call(a0=ctypes.byref(_cache(page_size=32))) == UNSUPPORTED
+
+
+def test_bindings_refuse_wrong_tensors():
+    # tensors that are not on the GPU, or of another type or shape, never reach the library
+    c = kv.Cache(torch.zeros((4, 2, 2304), dtype=torch.uint8), 4, 2)
+    q = torch.zeros((1, 8, 128), dtype=torch.bfloat16)
+    table, lens = torch.zeros((1, 4), dtype=torch.int32), torch.zeros(1, dtype=torch.int32)
+    out, ws = torch.zeros_like(q), torch.zeros(1 << 10, dtype=torch.uint8)
+    for args in ((q, out, table, lens), (q.float(), out, table, lens), (q, out.float(), table, lens),
+                 (q, out, table.long(), lens), (q[:, ::2], out[:, ::2], table, lens)):
+        with pytest.raises(ValueError):
+            kv.nvfp4kv_decode_attention_scored(c, *args, 0.1, ws)
+        with pytest.raises(ValueError):
+            kv.nvfp4kv_decode_attention_weights(c, *args, 0.1, torch.zeros((1, 2, 64)), ws)
+    with pytest.raises(ValueError):
+        kv.nvfp4kv_evict(c, table, lens, torch.zeros((1, 2, 64)), 16, 0, 0, table, torch.zeros((1, 2, 16), dtype=torch.int32))
+    with pytest.raises(ValueError):
+        mx = kv.Cache(torch.zeros((4, 2, 2176), dtype=torch.uint8), 4, 2, mxfp4=True)
+        kv.nvfp4kv_decode_attention_scored(mx, q, out, table, lens, 0.1, ws)
+
+
+def test_reference_attention_matches_torch():
+    from scored_util import attend, extend_seen
+
+    rng = np.random.default_rng(1)
+    K, V, q = rng.standard_normal((50, 128)), rng.standard_normal((50, 128)), rng.standard_normal(128)
+    for scoring, kw in ((kv.Scoring(), {}), (kv.Scoring(window=7, sinks=3), {}), (kv.Scoring(), dict(full=45)),
+                        (kv.Scoring(window=9, sinks=2), dict(doc=20))):
+        seen = extend_seen(30, 20, 5, scoring, **kw)
+        p = 35
+        want = [j for j in range(50) if j <= max(p, kw.get("full", 0) - 1) and j >= kw.get("doc", 0) and
+                (not scoring.window or p - j < scoring.window or j < kw.get("doc", 0) + scoring.sinks)]
+        assert np.flatnonzero(seen).tolist() == want
+        bias = -0.25 * np.abs(p - np.arange(50.0))
+        got = attend(q, K, V, seen, np.abs(p - np.arange(50.0)), 0.1, slope=0.25)
+        mask = torch.from_numpy(np.where(seen, bias, -np.inf))[None]
+        ref = torch.nn.functional.scaled_dot_product_attention(
+            torch.from_numpy(q)[None, None], torch.from_numpy(K)[None], torch.from_numpy(V)[None], attn_mask=mask, scale=0.1)
+        np.testing.assert_allclose(got["out"], ref[0, 0].numpy(), rtol=1e-10, atol=1e-12)
+        x = np.where(seen, 0.1 * (K @ q) + bias, -np.inf)
+        np.testing.assert_allclose(got["lse"], torch.logsumexp(torch.from_numpy(x), 0).item(), rtol=1e-12)
+    # the cap, and a row that sees nothing
+    got = attend(q, K, V, np.ones(50, bool), np.zeros(50), 0.1, softcap=2.0)
+    x = 2.0 * np.tanh(0.1 * (K @ q) / 2.0)
+    np.testing.assert_allclose(got["out"], torch.softmax(torch.from_numpy(x), 0).numpy() @ V, rtol=1e-10, atol=1e-12)
+    empty = attend(q, K, V, np.zeros(50, bool), np.zeros(50), 0.1)
+    assert not empty["out"].any() and empty["lse"] == -np.inf
