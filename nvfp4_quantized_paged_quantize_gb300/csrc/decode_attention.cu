@@ -1343,6 +1343,10 @@ __global__ void __launch_bounds__(kNW * 32, kCtasPerSm) decode_kernel(const Deco
 constexpr int kCombineMaxGroups = 16;
 
 __device__ __forceinline__ void online_merge(float& M, float& L, float4& acc, float m, float l, float4 v) {
+  if (m == -INFINITY) {  // an empty record: only its m was written, the rest is whatever the scratch held
+    l = 0.0f;
+    v = make_float4(0.f, 0.f, 0.f, 0.f);
+  }
   const float Mn = fmaxf(M, m);
   const float a = M == -INFINITY ? 0.0f : ex2(M - Mn);
   const float b = m == -INFINITY ? 0.0f : ex2(m - Mn);

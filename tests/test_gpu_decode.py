@@ -166,3 +166,18 @@ def test_workspace_bytes_from_the_batch_shape_covers_the_call(cuda_lib):
         cache = kv.Cache.empty(4, hkv)
         need = kv.nvfp4kv_decode_workspace_size(cache, B, hq)
         assert kv.nvfp4kv_decode_workspace_bytes(B, hq, 8193, nsm) >= need
+
+
+@pytest.mark.parametrize("fill", [0xFF, 0x7F])
+def test_scratch_needs_no_initialisation(cuda_lib, fill):
+    # fewer page-heads than warps: warps with nothing to do lie between a pair's
+    # records, and what the scratch held there (0xFF: NaN) must not come through
+    wl = inputs.decode_config(1)
+    prompts = wl.all_prompt_kv()
+    cache = fill_workload_gpu(wl, prompts)
+    q = wl.q()
+    want, _ = decode_gpu(wl, cache, q)
+    n = kv.nvfp4kv_decode_workspace_size(cache, wl.batch, wl.num_q_heads)
+    got, _ = decode_gpu(wl, cache, q, workspace=torch.full((n,), fill, dtype=torch.uint8, device="cuda"))
+    torch.cuda.synchronize()
+    assert torch.equal(got, want)
