@@ -97,6 +97,8 @@ def random_cache(num_pages, hkv, seed, gk=1.0, gv=1.0):
 
 def sequence_rows(o, table_row, h, L):
     """Dequantised K, V [L, 128] of a sequence's KV head from the oracle's cache."""
+    if L == 0:
+        return np.zeros((0, 128)), np.zeros((0, 128))
     t = np.arange(L)
     rows = (table_row[t // 16].astype(np.int64) * o.num_kv_heads + h) * 16 + t % 16
     return oracle.dequantize_rows(o, "k", rows), oracle.dequantize_rows(o, "v", rows)
