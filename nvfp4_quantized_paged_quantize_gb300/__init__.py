@@ -148,9 +148,9 @@ def _ptr(x) -> int | None:
 
 def _stream(stream) -> int | None:
     if stream is None:
-        import torch
-
-        return torch.cuda.current_stream().cuda_stream
+        # torch.cuda.current_stream().cuda_stream without building a Stream object (3 us a call)
+        t = _types()
+        return t._C._cuda_getCurrentRawStream(t.cuda.current_device())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -267,35 +267,54 @@ def _scoring(scoring, hq: int):
     if scoring is None:
         return None
     if scoring.slopes is not None:
-        _check_tensor("slopes", scoring.slopes, "float32", (hq,))
+        _check_tensor("slopes", scoring.slopes, _types().float32, (hq,))
     return ctypes.byref(scoring.c_struct())
 
 
-def _check_tensor(name: str, x, dtype: str, shape, optional: bool = False) -> None:
-    """x is a contiguous GPU tensor of this dtype and shape (None in `shape`: any size); raises ValueError."""
-    import torch
+_torch = None
 
-    if x is None and optional:
+
+def _types():
+    """torch, imported on first use."""
+    global _torch
+    if _torch is None:
+        import torch
+
+        _torch = torch
+    return _torch
+
+
+def _check_tensor(name: str, x, dtype, shape) -> None:
+    """x is a contiguous GPU tensor of this dtype and shape (a tuple); raises ValueError."""
+    if x is not None and x.dtype is dtype and x.is_cuda and x.shape == shape and x.is_contiguous():
         return
-    if (x is None or x.dtype is not getattr(torch, dtype) or not x.is_cuda or x.dim() != len(shape)
-            or not x.is_contiguous() or any(want is not None and got != want for got, want in zip(x.shape, shape))):
-        what = "None" if x is None else (f"{x.dtype} {tuple(x.shape)} on {x.device}"
-                                         f"{'' if x.is_contiguous() else ' (not contiguous)'}")
-        raise ValueError(f"{name}: expected a contiguous {dtype} GPU tensor of shape "
-                         f"{tuple('*' if d is None else d for d in shape)}, got {what}")
+    what = "None" if x is None else (f"{x.dtype} {tuple(x.shape)} on {x.device}"
+                                     f"{'' if x.is_contiguous() else ' (not contiguous)'}")
+    raise ValueError(f"{name}: expected a contiguous {dtype} GPU tensor of shape {shape}, got {what}")
+
+
+def _shape(name: str, x, dims: int):
+    """x's sizes; raises ValueError if it has not `dims` of them."""
+    if x is None or x.dim() != dims:
+        raise ValueError(f"{name}: expected a tensor of {dims} dimensions, got "
+                         f"{'None' if x is None else tuple(x.shape)}")
+    return x.shape
 
 
 def _check_decode(cache: "Cache", q, out, page_table, seq_lens, lse):
     """Shapes and types of a scored decode's tensors; returns (batch, query heads, page-table columns)."""
     if cache.mxfp4:
         raise ValueError("the cache holds MXFP4 page-heads; the scored decodes read NVFP4 ones")
-    _check_tensor("q", q, "bfloat16", (None, None, HEAD_DIM))
-    B, Hq = int(q.shape[0]), int(q.shape[1])
-    _check_tensor("out", out, "bfloat16", (B, Hq, HEAD_DIM))
-    _check_tensor("page_table", page_table, "int32", (B, None))
-    _check_tensor("seq_lens", seq_lens, "int32", (B,))
-    _check_tensor("lse", lse, "float32", (B, Hq), optional=True)
-    return B, Hq, int(page_table.shape[1])
+    t = _types()
+    B, Hq, _ = _shape("q", q, 3)
+    maxp = _shape("page_table", page_table, 2)[1]
+    _check_tensor("q", q, t.bfloat16, (B, Hq, HEAD_DIM))
+    _check_tensor("out", out, t.bfloat16, (B, Hq, HEAD_DIM))
+    _check_tensor("page_table", page_table, t.int32, (B, maxp))
+    _check_tensor("seq_lens", seq_lens, t.int32, (B,))
+    if lse is not None:
+        _check_tensor("lse", lse, t.float32, (B, Hq))
+    return B, Hq, maxp
 
 
 def nvfp4kv_decode_attention_scored(cache: "Cache", q, out, page_table, seq_lens, softmax_scale: float, workspace,
@@ -332,7 +351,8 @@ def nvfp4kv_decode_attention_weights(cache: "Cache", q, out, page_table, seq_len
     sum becomes decay * sum + the softmax weight it got from the KV head's query heads.  max_total_pages bounds
     the batch's cached pages (default: the cache's num_pages, right where sequences share no page)."""
     B, Hq, maxp = _check_decode(cache, q, out, page_table, seq_lens, lse)
-    _check_tensor("weights", weights, "float32", (B, cache.num_kv_heads, None))
+    stride = _shape("weights", weights, 3)[2]
+    _check_tensor("weights", weights, _types().float32, (B, cache.num_kv_heads, stride))
     if workspace_bytes is None:
         workspace_bytes = workspace.numel() * workspace.element_size()
     if max_total_pages is None:
@@ -341,7 +361,7 @@ def nvfp4kv_decode_attention_weights(cache: "Cache", q, out, page_table, seq_len
     _check("nvfp4kv_decode_attention_weights",
            _L().nvfp4kv_decode_attention_weights(ctypes.byref(c), _ptr(q), _ptr(out), _ptr(lse), _ptr(page_table),
                                                  maxp, _ptr(seq_lens), B, Hq, float(softmax_scale),
-                                                 _scoring(scoring, Hq), _ptr(weights), int(weights.shape[2]),
+                                                 _scoring(scoring, Hq), _ptr(weights), stride,
                                                  float(decay), int(max_total_pages), _ptr(workspace), workspace_bytes,
                                                  _ptr(device_status), _stream(stream)))
 
@@ -353,25 +373,30 @@ def nvfp4kv_extend_attention_scored(q, cu_q, max_q_len: int, ws_k, ws_v, cu_pref
     """nvfp4kv_extend_attention with a scoring, a prefix mask (full_lens, int32 [B]: leading positions that every
     query sees) and a document mask (doc_starts, int32 [total_q]: where each query's document starts); out bf16
     [total_q, Hq, 128], lse fp32 [total_q, Hq] or None."""
-    _check_tensor("q", q, "bfloat16", (None, None, HEAD_DIM))
-    n, hq = int(q.shape[0]), int(q.shape[1])
-    _check_tensor("prefix_lens", prefix_lens, "int32", (None,))
-    B = int(prefix_lens.shape[0])
-    _check_tensor("cu_q", cu_q, "int64", (B + 1,))
-    _check_tensor("cu_prefix", cu_prefix, "int64", (None,))
-    if int(cu_prefix.shape[0]) < B:
-        raise ValueError(f"cu_prefix: {int(cu_prefix.shape[0])} entries for {B} sequences")
-    _check_tensor("ws_k", ws_k, "uint8", (None, None, HEAD_DIM))
-    _check_tensor("ws_v", ws_v, "uint8", tuple(ws_k.shape))
-    _check_tensor("out", out, "bfloat16", (n, hq, HEAD_DIM))
-    _check_tensor("full_lens", full_lens, "int32", (B,), optional=True)
-    _check_tensor("doc_starts", doc_starts, "int32", (n,), optional=True)
-    _check_tensor("lse", lse, "float32", (n, hq), optional=True)
+    t = _types()
+    n, hq, _ = _shape("q", q, 3)
+    B = _shape("prefix_lens", prefix_lens, 1)[0]
+    rows, hkv, _ = _shape("ws_k", ws_k, 3)
+    sequences = _shape("cu_prefix", cu_prefix, 1)[0]
+    if sequences < B:
+        raise ValueError(f"cu_prefix: {sequences} entries for {B} sequences")
+    _check_tensor("q", q, t.bfloat16, (n, hq, HEAD_DIM))
+    _check_tensor("out", out, t.bfloat16, (n, hq, HEAD_DIM))
+    _check_tensor("prefix_lens", prefix_lens, t.int32, (B,))
+    _check_tensor("cu_q", cu_q, t.int64, (B + 1,))
+    _check_tensor("cu_prefix", cu_prefix, t.int64, (sequences,))
+    _check_tensor("ws_k", ws_k, t.uint8, (rows, hkv, HEAD_DIM))
+    _check_tensor("ws_v", ws_v, t.uint8, (rows, hkv, HEAD_DIM))
+    if full_lens is not None:
+        _check_tensor("full_lens", full_lens, t.int32, (B,))
+    if doc_starts is not None:
+        _check_tensor("doc_starts", doc_starts, t.int32, (n,))
+    if lse is not None:
+        _check_tensor("lse", lse, t.float32, (n, hq))
     _check("nvfp4kv_extend_attention_scored",
            _L().nvfp4kv_extend_attention_scored(_ptr(q), _ptr(cu_q), int(max_q_len), _ptr(ws_k), _ptr(ws_v),
-                                                _ptr(cu_prefix), _ptr(prefix_lens), B, int(ws_k.shape[0]), hq,
-                                                int(ws_k.shape[1]), HEAD_DIM, float(k_ws_scale), float(v_ws_scale),
-                                                float(softmax_scale), _scoring(scoring, hq), _ptr(full_lens),
+                                                _ptr(cu_prefix), _ptr(prefix_lens), B, rows, hq, hkv, HEAD_DIM,
+                                                float(k_ws_scale), float(v_ws_scale), float(softmax_scale), _scoring(scoring, hq), _ptr(full_lens),
                                                 _ptr(doc_starts), _ptr(out), _ptr(lse), _ptr(device_status),
                                                 _stream(stream)))
 
@@ -384,21 +409,26 @@ def nvfp4kv_evict(cache: "Cache", page_table, seq_lens, weights, budget: int, fi
     [B, Hkv, >= budget] or None; new_lens: int32 [B] or None."""
     if cache.mxfp4:
         raise ValueError("the cache holds MXFP4 page-heads; eviction moves NVFP4 ones")
-    _check_tensor("seq_lens", seq_lens, "int32", (None,))
-    B, hkv = int(seq_lens.shape[0]), int(cache.num_kv_heads)
-    _check_tensor("page_table", page_table, "int32", (B, None))
-    _check_tensor("weights", weights, "float32", (B, hkv, None))
-    _check_tensor("dst_page_table", dst_page_table, "int32", (B, None))
-    _check_tensor("kept", kept, "int32", (B, hkv, int(budget)))
-    _check_tensor("kept_weights", kept_weights, "float32", (B, hkv, None), optional=True)
-    _check_tensor("new_lens", new_lens, "int32", (B,), optional=True)
+    t = _types()
+    B, hkv = _shape("seq_lens", seq_lens, 1)[0], cache.num_kv_heads
+    maxp, dst_maxp = _shape("page_table", page_table, 2)[1], _shape("dst_page_table", dst_page_table, 2)[1]
+    stride = _shape("weights", weights, 3)[2]
+    _check_tensor("seq_lens", seq_lens, t.int32, (B,))
+    _check_tensor("page_table", page_table, t.int32, (B, maxp))
+    _check_tensor("weights", weights, t.float32, (B, hkv, stride))
+    _check_tensor("dst_page_table", dst_page_table, t.int32, (B, dst_maxp))
+    _check_tensor("kept", kept, t.int32, (B, hkv, budget))
+    kept_stride = 0
+    if kept_weights is not None:
+        kept_stride = _shape("kept_weights", kept_weights, 3)[2]
+        _check_tensor("kept_weights", kept_weights, t.float32, (B, hkv, kept_stride))
+    if new_lens is not None:
+        _check_tensor("new_lens", new_lens, t.int32, (B,))
     c = cache.c_struct()
     _check("nvfp4kv_evict",
-           _L().nvfp4kv_evict(ctypes.byref(c), _ptr(page_table), int(page_table.shape[1]), _ptr(seq_lens), B,
-                              _ptr(weights), int(weights.shape[2]), int(budget), int(first), int(recent),
-                              _ptr(dst_page_table), int(dst_page_table.shape[1]), _ptr(kept), _ptr(kept_weights),
-                              0 if kept_weights is None else int(kept_weights.shape[2]), _ptr(new_lens),
-                              _ptr(device_status), _stream(stream)))
+           _L().nvfp4kv_evict(ctypes.byref(c), _ptr(page_table), maxp, _ptr(seq_lens), B, _ptr(weights), stride,
+                              budget, first, recent, _ptr(dst_page_table), dst_maxp, _ptr(kept), _ptr(kept_weights),
+                              kept_stride, _ptr(new_lens), _ptr(device_status), _stream(stream)))
 
 
 def nvfp4kv_status_string(status: int) -> str:

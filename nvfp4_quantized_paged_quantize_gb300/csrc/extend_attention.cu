@@ -35,8 +35,8 @@
 // their TMEM.
 #include "nvfp4kv_device.cuh"
 #include "nvfp4kv_launch.h"
+#include "extend_tiles.cuh"
 #include "fp8_quotient.cuh"
-#include "scoring.cuh"
 #include "tcgen05.cuh"
 
 namespace nvfp4kv {
@@ -105,8 +105,6 @@ constexpr int kSoftmaxWarps = 4;
 constexpr int kLoadWarps = 4;
 constexpr int kThreads = (kSoftmaxWarps + kLoadWarps + 1) * 32;  // + the MMA warp
 constexpr int kMmaWarp = kSoftmaxWarps + kLoadWarps;
-constexpr uint32_t kLBO = 128;   // next core matrix along K
-constexpr uint32_t kSBO = 2048;  // next 8-row (N) group: 16 core matrices of 128 B
 constexpr uint32_t kHalfBytes = kHalfN * kHeadDim * 2;  // a CTA's half of one f16 B tile, 16 KB
 #ifndef NVFP4KV_EXTEND_STAGES
 #define NVFP4KV_EXTEND_STAGES 6
@@ -120,14 +118,6 @@ constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kTmemO = 256, kTmemQ = 384, kTmemP = 448;
 constexpr float kLazy = 8.0f;  // the running max moves only when a row max exceeds it by this (base 2)
 constexpr uint64_t kWaitNs = 1000000000ull;
-
-// Scored extend (nvfp4kv_extend_attention_scored): bit flags of the kernel's
-// template argument; 0 is the plain causal extend.
-enum : int {
-  kScored = 1,  // bf16 output, log-sum-exp, window with sinks, prefix and document masks
-  kCapped = 2,  // scores through cap * tanh(s / cap)
-  kBiased = 4   // minus slope * distance
-};
 
 struct ExtendParams {
   const uint16_t* q;
@@ -143,28 +133,7 @@ struct ExtendParams {
   float out_scale;    // v_ws_scale
   float* out;
   int32_t* status;
-  // scored extend only
-  float cap_scale;           // kCapped: softmax_scale * k_ws_scale / cap (score_scale is then cap * log2(e))
-  int32_t window, sinks;     // 0: no window
-  const float* slopes;       // [hq], kBiased
-  const int32_t* full_lens;  // [batch] or null
-  const int32_t* doc_starts; // [total_q] or null
-  uint16_t* out16;
-  float* lse;                // or null
 };
-
-// byte offset of element (row, k) in a K-major f16 tile / (mn, k) in an MN-major one
-__device__ __forceinline__ uint32_t kmajor_off(int row, int k) {
-  return (uint32_t)(row >> 3) * kSBO + (uint32_t)(k >> 3) * kLBO + (uint32_t)(row & 7) * 16 + (uint32_t)(k & 7) * 2;
-}
-__device__ __forceinline__ uint32_t mnmajor_off(int mn, int k) {
-  return (uint32_t)(mn >> 3) * kSBO + (uint32_t)(k >> 3) * kLBO + (uint32_t)(k & 7) * 16 + (uint32_t)(mn & 7) * 2;
-}
-
-__device__ __forceinline__ void st_shared_v4(uint32_t addr, const uint4& v) {
-  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
-               : "memory");
-}
 
 // One arrival, released at cluster scope, on the mbarrier of cluster rank 0
 // that sits at this shared-memory offset.
@@ -206,31 +175,6 @@ __device__ __forceinline__ bool warp_wait_cluster(uint32_t bar, uint32_t parity,
   }
 }
 
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
-__device__ __forceinline__ uint32_t f16x2_bits(float lo, float hi) {
-  const __half2 h = __floats2half2_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&h);
-}
-
-// 8 bf16 -> 8 f16 (round to nearest; exact for 2^-14 <= |x| <= 65504)
-__device__ __forceinline__ uint4 bf16x8_to_f16x8(const uint4& x) {
-  return make_uint4(f16x2_bits(bf16_to_f32(x.x & 0xFFFFu), bf16_to_f32(x.x >> 16)),
-                    f16x2_bits(bf16_to_f32(x.y & 0xFFFFu), bf16_to_f32(x.y >> 16)),
-                    f16x2_bits(bf16_to_f32(x.z & 0xFFFFu), bf16_to_f32(x.z >> 16)),
-                    f16x2_bits(bf16_to_f32(x.w & 0xFFFFu), bf16_to_f32(x.w >> 16)));
-}
-
-// 8 E4M3 bytes (a uint2) -> 8 f16 (exact)
-__device__ __forceinline__ uint4 e4m3x8_to_f16x8(uint32_t lo, uint32_t hi) {
-  return make_uint4(e4m3x2_to_f16x2(lo & 0xFFFFu), e4m3x2_to_f16x2(lo >> 16), e4m3x2_to_f16x2(hi & 0xFFFFu),
-                    e4m3x2_to_f16x2(hi >> 16));
-}
-
 struct Barriers {
   uint64_t q_full;
   uint64_t kv_full[kStages];
@@ -241,31 +185,6 @@ struct Barriers {
   uint64_t drain;
 };
 
-// The keys one query sees: low <= j <= high, and (with a window) j >= near or
-// j < sink_end.
-struct KeyRange {
-  int64_t low, high, near, sink_end;
-};
-
-// The query at position pos of a sequence of P prefix and C chunk tokens, whose
-// first `full` positions every query sees and whose document starts at doc.
-__device__ __forceinline__ KeyRange key_range(const ExtendParams& p, int64_t P, int64_t C, int64_t pos, int64_t full,
-                                              int64_t doc) {
-  KeyRange r;
-  const int64_t end = full < P + C ? full : P + C;
-  r.low = doc > 0 ? doc : 0;
-  r.high = pos > end - 1 ? pos : end - 1;
-  r.near = r.low;
-  r.sink_end = r.low;
-  if (p.window > 0) {
-    const int64_t first = pos - p.window + 1;
-    if (first > r.near) r.near = first;
-    r.sink_end = r.low + p.sinks;
-  }
-  return r;
-}
-
-template <int M>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) extend_attention_kernel(ExtendParams p) {
   extern __shared__ __align__(1024) uint8_t smem[];
   __shared__ Barriers bars;
@@ -293,53 +212,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) extend_
   // no query in the pair: both CTAs leave before any set-up (the test is the same in both)
   if (tp >= C) return;
   const int64_t t_hi = (tp + 2 * tokens_per_tile < C ? tp + 2 * tokens_per_tile : C) - 1;
-  int64_t nkeys = P + t_hi + 1;  // keys 0 .. P + t_hi: the pair's last query sees them all
-  int ntiles = (int)((nkeys + kTileN - 1) / kTileN);
-  // Scored: the pair visits the tiles that some of its queries see: those of
-  // the sinks (lead of them, from tile first on), then those from the nearest
-  // key of any query's window or document on (tile i >= lead is i + skip).
-  int first = 0, lead = 0, skip = 0;
-  int64_t full = 0;
-  if constexpr (M != 0) {
-    if (p.full_lens != nullptr) full = __ldg(p.full_lens + b);
-    int64_t low0 = 0, low1 = 0;  // the queries' lowest and highest document start
-    int64_t near0 = p.window > 0 && P + tp - p.window + 1 > 0 ? P + tp - p.window + 1 : 0;
-    if (p.doc_starts != nullptr) {
-      // every warp looks at all of the pair's tokens (256 / G), so both CTAs agree
-      int64_t l0 = INT64_MAX, l1 = 0, n0 = INT64_MAX;
-      for (int64_t t = tp + lane; t <= t_hi; t += 32) {
-        const KeyRange r = key_range(p, P, C, P + t, full, __ldg(p.doc_starts + q0 + t));
-        l0 = r.low < l0 ? r.low : l0;
-        l1 = r.low > l1 ? r.low : l1;
-        n0 = r.near < n0 ? r.near : n0;
-      }
-#pragma unroll
-      for (int off = 16; off > 0; off >>= 1) {
-        const int64_t a = __shfl_xor_sync(0xFFFFFFFFu, l0, off), c = __shfl_xor_sync(0xFFFFFFFFu, l1, off);
-        const int64_t d = __shfl_xor_sync(0xFFFFFFFFu, n0, off);
-        l0 = a < l0 ? a : l0;
-        l1 = c > l1 ? c : l1;
-        n0 = d < n0 ? d : n0;
-      }
-      low0 = l0;
-      low1 = l1;
-      near0 = n0;
-    }
-    nkeys = key_range(p, P, C, P + t_hi, full, 0).high + 1;
-    const int last = (int)((nkeys - 1) / kTileN);
-    const int near_tile = near0 / kTileN < last ? (int)(near0 / kTileN) : last;  // one tile at least
-    first = near_tile;
-    if (p.window > 0 && p.sinks > 0) {
-      const int s0 = low0 / kTileN < near_tile ? (int)(low0 / kTileN) : near_tile;
-      const int64_t s1 = (low1 + p.sinks - 1) / kTileN + 1;  // past the last sink tile
-      first = s0;
-      lead = (s1 < near_tile ? (int)s1 : near_tile) - s0;
-    }
-    skip = near_tile - lead;
-    ntiles = lead + last - near_tile + 1;
-  }
-  // the key tile of step i
-  auto tile_of = [&](int i) { return M == 0 ? i : (i < lead ? first + i : i + skip); };
+  const int64_t nkeys = P + t_hi + 1;  // keys 0 .. P + t_hi: the pair's last query sees them all
+  const int ntiles = (int)((nkeys + kTileN - 1) / kTileN);
 
   const uint32_t sbase = smem_u32(smem);
   const uint32_t sK0 = sbase + kOffK, sV0 = sbase + kOffV;
@@ -385,7 +259,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) extend_
     const int part = lane >> 3;
     uint4 xk[2][2], xv[4];
     auto load_tile = [&](int i) {
-      const int64_t base = (int64_t)tile_of(i) * kTileN;
+      const int64_t base = (int64_t)i * kTileN;
 #pragma unroll
       for (int g = 0; g < 2; ++g) {
         const int64_t j = base + kHalfN * (int)rank + lw * 16 + g * 8 + (lane & 7);
@@ -522,14 +396,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) extend_
     const uint32_t lane_base = (uint32_t)(warp * 32) << 16;
     float m = -INFINITY, l = 0.0f;
     bool ok = true;
-    KeyRange kr = {0, 0, 0, 0};
-    float slope = 0.0f;
-    if constexpr (M != 0) {
-      kr = key_range(p, P, C, kmax, full, p.doc_starts != nullptr && live ? __ldg(p.doc_starts + q0 + t) : 0);
-      if constexpr ((M & kBiased) != 0) slope = __ldg(p.slopes + hk * G + (r & (G - 1))) * kLog2e;
-    }
-    // what a unit of x is in base 2 (a biased score is in base 2 already)
-    const float unit = (M & kBiased) != 0 ? 1.0f : p.score_scale;
     for (int i = 0; i < ntiles; ++i) {
       if (!warp_wait_cluster(b_s[i & 1], (i >> 1) & 1, kWaitNs)) {
         ok = false;
@@ -544,36 +410,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) extend_
 #pragma unroll
         for (int j = 0; j < 32; ++j) x[c4 * 32 + j] = __uint_as_float(v[j]);
       }
-      const int64_t kbase = (int64_t)tile_of(i) * kTileN;
-      if constexpr ((M & kCapped) != 0) {
-        float2(&x2)[kTileN / 2] = *reinterpret_cast<float2(*)[kTileN / 2]>(&x[0]);
-#pragma unroll
-        for (int c = 0; c < kTileN / 2; ++c) x2[c] = mul2(x2[c], both(p.cap_scale));
-        tanh_warp(x2);
-      }
-      if constexpr ((M & kBiased) != 0) {
-        const float d0 = (float)(kmax - kbase);
-#pragma unroll
-        for (int c = 0; c < kTileN; ++c) x[c] = fmaf(-slope, fabsf(d0 - (float)c), x[c] * p.score_scale);
-      }
       // keys c <= lim of this tile are visible to the row (all of them away from
       // the causal edge, none for a row past the chunk)
-      const int64_t lim64 = live ? (M == 0 ? kmax : kr.high) - kbase : -1;
+      const int64_t lim64 = live ? kmax - (int64_t)i * kTileN : -1;
       const int lim = lim64 >= kTileN - 1 ? kTileN - 1 : (int)(lim64 < -1 ? -1 : lim64);
       float mr[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-      bool whole = lim == kTileN - 1;
-      if constexpr (M != 0) {
-        // keys c of [low, sink) and [near, lim] are visible
-        auto in_tile = [&](int64_t j) { return (int)(j - kbase < 0 ? 0 : (j - kbase > kTileN ? kTileN : j - kbase)); };
-        const int low = in_tile(kr.low), sink = in_tile(kr.sink_end), near = in_tile(kr.near);
-        whole = whole && (near == 0 || (low == 0 && sink == kTileN));
-        if (!whole) {
-#pragma unroll
-          for (int c = 0; c < kTileN; ++c)
-            if (c < near && (c < low || c >= sink)) x[c] = -INFINITY;
-        }
-      }
-      if (whole) {
+      if (lim == kTileN - 1) {
 #pragma unroll
         for (int c = 0; c < kTileN; ++c) mr[c & 3] = fmaxf(mr[c & 3], x[c]);
       } else {
@@ -584,7 +426,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) extend_
         }
       }
       // the row max in base-2 units (the scale is positive, so it commutes with max)
-      const float mx = fmaxf(fmaxf(mr[0], mr[1]), fmaxf(mr[2], mr[3])) * unit;
+      const float mx = fmaxf(fmaxf(mr[0], mr[1]), fmaxf(mr[2], mr[3])) * p.score_scale;
       float alpha = 1.0f;
       const bool grow = mx > m + kLazy;  // false for rows with nothing visible (mx = -inf)
       if (grow) {
@@ -593,13 +435,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) extend_
       }
       // p = 2^(s * scale - m); masked scores are -inf and give 0, and so does
       // every score of a row past the chunk (offset -inf)
-      // (scored: a row that has seen nothing yet has m = -inf and gives 0, too)
-      const float off = live && (M == 0 || m > -INFINITY) ? -m : -INFINITY;
+      const float off = live ? -m : -INFINITY;
       uint32_t ph[kTileN / 2];
       float ls[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
       for (int c = 0; c < kTileN; c += 2) {
-        const float p0 = ex2(fmaf(x[c], unit, off)), p1 = ex2(fmaf(x[c + 1], unit, off));
+        const float p0 = ex2(fmaf(x[c], p.score_scale, off)), p1 = ex2(fmaf(x[c + 1], p.score_scale, off));
         ph[c / 2] = f16x2_bits(p0, p1);
         ls[(c >> 1) & 3] += p0 + p1;
       }
@@ -635,24 +476,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) extend_
     if (ok && warp_wait_cluster(b_o, (ntiles - 1) & 1, kWaitNs)) {
       tc::fence_after_sync();
       const float inv = live && l > 0.0f ? p.out_scale / l : 0.0f;
-      const int64_t row = (q0 + (live ? t : 0)) * p.hq + hk * G + (r & (G - 1));
-      float4* dst = reinterpret_cast<float4*>(p.out + row * kHeadDim);
-      uint4* dst16 = reinterpret_cast<uint4*>(p.out16 + row * kHeadDim);
-      if (M != 0 && live && p.lse != nullptr) p.lse[row] = l > 0.0f ? (m + log2f(l)) * kLn2 : -INFINITY;
+      float4* dst = reinterpret_cast<float4*>(
+          p.out + ((q0 + (live ? t : 0)) * p.hq + hk * G + (r & (G - 1))) * kHeadDim);
 #pragma unroll
       for (int c4 = 0; c4 < kHeadDim / 32; ++c4) {
         uint32_t v[32];
         tc::tmem_ld32(tmem + lane_base + kTmemO + c4 * 32, v);
-        if (live && M != 0) {
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            uint32_t w[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              w[k] = pack_bf16x2(__uint_as_float(v[8 * j + 2 * k]) * inv, __uint_as_float(v[8 * j + 2 * k + 1]) * inv);
-            dst16[c4 * 4 + j] = make_uint4(w[0], w[1], w[2], w[3]);
-          }
-        } else if (live) {
+        if (live) {
 #pragma unroll
           for (int j = 0; j < 8; ++j)
             dst[c4 * 8 + j] = make_float4(__uint_as_float(v[4 * j]) * inv, __uint_as_float(v[4 * j + 1]) * inv,
@@ -704,13 +534,12 @@ cudaError_t launch_chunk_to_ws(const uint16_t* k, const uint16_t* v, const int64
   return cudaGetLastError();
 }
 
-namespace {
-
-ExtendParams extend_params(const uint16_t* q, const int64_t* cu_q, int32_t max_q_len, const uint8_t* ws_k,
-                           const uint8_t* ws_v, const int64_t* cu_prefix, const int32_t* prefix_lens,
-                           int64_t total_rows, int32_t num_q_heads, int32_t num_kv_heads, float k_ws_scale,
-                           float v_ws_scale, float softmax_scale, int32_t* device_status) {
-  ExtendParams p = {};
+cudaError_t launch_extend_attention(const uint16_t* q, const int64_t* cu_q, int32_t max_q_len, const uint8_t* ws_k,
+                                    const uint8_t* ws_v, const int64_t* cu_prefix, const int32_t* prefix_lens,
+                                    int32_t batch, int64_t total_rows, int32_t num_q_heads, int32_t num_kv_heads,
+                                    float k_ws_scale, float v_ws_scale, float softmax_scale, float* out,
+                                    int32_t* device_status, cudaStream_t stream) {
+  ExtendParams p;
   p.q = q;
   p.cu_q = cu_q;
   p.ws_k = ws_k;
@@ -726,60 +555,19 @@ ExtendParams extend_params(const uint16_t* q, const int64_t* cu_q, int32_t max_q
   p.total_rows = total_rows;
   p.score_scale = (float)((double)softmax_scale * (double)k_ws_scale * 1.4426950408889634);
   p.out_scale = v_ws_scale;
+  p.out = out;
   p.status = device_status;
-  return p;
-}
-
-template <int M>
-cudaError_t enqueue_extend(const ExtendParams& p, int32_t batch, cudaStream_t stream) {
   // the shared-memory limit is an attribute of the function on each device
   static PerDeviceOnce attr_once;
   const cudaError_t attr = attr_once.run([] {
-    return cudaFuncSetAttribute(extend_attention_kernel<M>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+    return cudaFuncSetAttribute(extend_attention_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
   });
   if (attr != cudaSuccess) return attr;
   // CTA pairs (clusters of two along x): an even number of m-tiles
-  const int64_t tiles = ((int64_t)p.max_q_len * p.group + kTileM - 1) / kTileM;
-  const dim3 grid((unsigned)((tiles + 1) / 2 * 2), (unsigned)batch, (unsigned)p.hkv);
-  extend_attention_kernel<M><<<grid, kThreads, kSmemBytes, stream>>>(p);
+  const int64_t tiles = ((int64_t)max_q_len * p.group + kTileM - 1) / kTileM;
+  const dim3 grid((unsigned)((tiles + 1) / 2 * 2), (unsigned)batch, (unsigned)num_kv_heads);
+  extend_attention_kernel<<<grid, kThreads, kSmemBytes, stream>>>(p);
   return cudaGetLastError();
-}
-
-}  // namespace
-
-cudaError_t launch_extend_attention(const uint16_t* q, const int64_t* cu_q, int32_t max_q_len, const uint8_t* ws_k,
-                                    const uint8_t* ws_v, const int64_t* cu_prefix, const int32_t* prefix_lens,
-                                    int32_t batch, int64_t total_rows, int32_t num_q_heads, int32_t num_kv_heads,
-                                    float k_ws_scale, float v_ws_scale, float softmax_scale, float* out,
-                                    int32_t* device_status, cudaStream_t stream) {
-  ExtendParams p = extend_params(q, cu_q, max_q_len, ws_k, ws_v, cu_prefix, prefix_lens, total_rows, num_q_heads,
-                                 num_kv_heads, k_ws_scale, v_ws_scale, softmax_scale, device_status);
-  p.out = out;
-  return enqueue_extend<0>(p, batch, stream);
-}
-
-cudaError_t launch_extend_scored(const uint16_t* q, const int64_t* cu_q, int32_t max_q_len, const uint8_t* ws_k,
-                                 const uint8_t* ws_v, const int64_t* cu_prefix, const int32_t* prefix_lens,
-                                 int32_t batch, int64_t total_rows, int32_t num_q_heads, int32_t num_kv_heads,
-                                 float k_ws_scale, float v_ws_scale, float softmax_scale, const nvfp4kv_scoring& sc,
-                                 const int32_t* full_lens, const int32_t* doc_starts, uint16_t* out, float* lse,
-                                 int32_t* device_status, cudaStream_t stream) {
-  ExtendParams p = extend_params(q, cu_q, max_q_len, ws_k, ws_v, cu_prefix, prefix_lens, total_rows, num_q_heads,
-                                 num_kv_heads, k_ws_scale, v_ws_scale, softmax_scale, device_status);
-  p.window = sc.window;
-  p.sinks = sc.sinks;
-  p.slopes = sc.slopes;
-  p.full_lens = full_lens;
-  p.doc_starts = doc_starts;
-  p.out16 = out;
-  p.lse = lse;
-  if (sc.softcap > 0.0f) {
-    p.cap_scale = (float)((double)softmax_scale * (double)k_ws_scale / (double)sc.softcap);
-    p.score_scale = (float)((double)sc.softcap * 1.4426950408889634);
-    return sc.slopes ? enqueue_extend<kScored | kCapped | kBiased>(p, batch, stream)
-                     : enqueue_extend<kScored | kCapped>(p, batch, stream);
-  }
-  return sc.slopes ? enqueue_extend<kScored | kBiased>(p, batch, stream) : enqueue_extend<kScored>(p, batch, stream);
 }
 
 }  // namespace nvfp4kv

@@ -1,0 +1,590 @@
+// extend_scored.cu -- extend attention over the FP8 workspace with scored
+// attention: a tanh cap, a distance bias, a window with sinks, prefix and
+// document masks, bf16 output and the log-sum-exp
+// (nvfp4kv_extend_attention_scored).
+//
+// A CTA owns 256 query rows of one (sequence, KV head): two tiles of 128 rows
+// (128 / G tokens x the G query heads of the KV head), so each K/V tile feeds
+// 256 rows.  13 warps:
+//   - Warps 0-3 and 4-7, a softmax group per row tile: one query row per
+//     thread (TMEM lane = row).  They write the row of Q (f16) into shared
+//     memory, then per key tile pass over the S row twice, 32 columns at a time
+//     with the next 32 on their way: the first pass caps, biases and masks the
+//     scores (and puts them back where that changed them) and finds their
+//     maximum, the second takes the exponentials and writes P (f16) over S
+//     columns already read.  The softmax is a lazy base-2 online one (the running
+//     max moves only when it grows by 2^8, and O is then rescaled in TMEM).  At
+//     the end: O * s_ws(V) / l -> bf16.  (Holding the whole row of 128 scores in
+//     registers spilled; with 224 KB of shared memory in use there is next to no
+//     L1 left, and a spilled word came back from L2 after some 400 cycles.)
+//   - Warps 8-11 load the key tiles of the workspace (K and V alternately, one
+//     of each in flight in registers), convert E4M3 -> f16 (exact) and store
+//     them as B operands (K K-major, V MN-major) in a ring of five 32 KB slots.
+//   - Warp 12 issues, from one thread, S_t = Q_t K^T (both operands in shared
+//     memory) and O_t += P_t V (P in TMEM), t = 0, 1, f32 accumulators.  The
+//     order PV_0, S_0, PV_1, S_1 lets one group's softmax run while the tensor
+//     core works for the other; MMAs execute in issue order, so S_t(i + 1) may
+//     overwrite the columns that P_t(i) was read from, and the completion of
+//     S_t(i + 1) implies that of PV_t(i).
+// TMEM (512 columns): S_0 0-127, S_1 128-255 (P_t in the first 64 of S_t),
+// O_0 256-383, O_1 384-511.
+// Key tiles that no query of the CTA sees are skipped, and workspace rows that
+// none sees read as zero.  Every wait is bounded: a stalled pipeline flags
+// NVFP4KV_DEVERR_TIMEOUT and drains its MMAs before the TMEM is freed.
+#include "extend_tiles.cuh"
+#include "nvfp4kv_device.cuh"
+#include "nvfp4kv_launch.h"
+#include "scoring.cuh"
+#include "tcgen05.cuh"
+
+namespace nvfp4kv {
+namespace {
+
+// the kernel's template argument
+enum : int {
+  kCapped = 1,  // scores through cap * tanh(s / cap)
+  kBiased = 2   // minus slope * distance
+};
+
+constexpr int kTileM = 128;    // query rows per tile (TMEM lanes); a CTA takes two
+constexpr int kTileN = 128;    // keys per K/V tile
+constexpr int kRows = 2 * kTileM;
+constexpr int kSoftmaxWarps = 8, kLoadWarps = 4;
+constexpr int kMmaWarp = kSoftmaxWarps + kLoadWarps;
+constexpr int kThreads = (kMmaWarp + 1) * 32;  // 416
+constexpr uint32_t kTileBytes = kTileN * kHeadDim * 2;  // one f16 tile (of Q, K or V), 32 KB
+constexpr uint32_t kSlotBytes = kTileBytes;
+constexpr int kSlots = 5;                               // K/V ring
+constexpr uint32_t kSmemBytes = 2 * kTileBytes + kSlots * kSlotBytes;  // 224 KB: one CTA per SM
+constexpr uint32_t kTmemCols = 512, kTmemO = 256;
+constexpr float kLazy = 8.0f;
+constexpr uint64_t kWaitNs = 1000000000ull;
+
+struct ScoredParams {
+  const uint16_t* q;
+  const int64_t* cu_q;
+  const uint8_t* ws_k;
+  const uint8_t* ws_v;
+  const int64_t* cu_prefix;
+  const int32_t* prefix_lens;
+  int32_t hq, hkv, group, log2_group;
+  int32_t max_q_len;
+  int64_t total_rows;
+  float unit;                // base-2 score per unit of q . k (of the tanh, capped)
+  float out_scale;           // v_ws_scale
+  CapPoly cap;               // capped: q . k -> tanh(x / softcap)
+  int32_t window, sinks;     // 0: no window
+  const float* slopes;       // [hq], biased
+  const int32_t* full_lens;  // [batch] or null
+  const int32_t* doc_starts; // [total_q] or null
+  uint16_t* out;
+  float* lse;                // or null
+  int32_t* status;
+};
+
+struct Barriers {
+  uint64_t q_full;         // 8: the softmax warps
+  uint64_t full[kSlots];   // 4: the load warps
+  uint64_t empty[kSlots];  // 1: an MMA commit
+  uint64_t s_full[2];      // 1: an MMA commit
+  uint64_t p_full[2];      // 4: the group's softmax warps
+  uint64_t drain;
+};
+
+// Q in shared memory (the A operand): K-major core matrices with the row groups
+// of one 16-byte K chunk next to each other.
+constexpr uint32_t kQLBO = kTileM * 16, kQSBO = 128;
+__device__ __forceinline__ uint32_t q_off(int row, int k) { return (uint32_t)(k >> 3) * kQLBO + (uint32_t)row * 16; }
+// V (MN-major: a key's head dims are contiguous) in the 128-byte swizzle: atoms
+// of 8 keys x 64 head dims, the 16-byte chunk c of key r stored at c ^ r; the
+// key groups of one half of the head dims follow one another.
+constexpr uint32_t kVLBO = kTileBytes / 2, kVSBO = 1024;  // next 64 head dims, next 8 keys
+__device__ __forceinline__ uint32_t v_off(int d, int key) {
+  return (uint32_t)(d >> 6) * kVLBO + (uint32_t)(key >> 3) * kVSBO + (uint32_t)(key & 7) * 128 +
+         ((((uint32_t)d >> 3) ^ (uint32_t)key) & 7) * 16;
+}
+
+// Positions within a sequence are 32-bit: prefix and chunk together stay below
+// 2^31 - 2^8 (a longer sequence is cut, and flagged).
+constexpr int kMaxKeys = INT32_MAX - 255;
+
+// The keys one query sees: low <= j < end, and (with a window) j >= near or
+// j < sink_end.
+struct KeyRange {
+  int low, end, near, sink_end;
+};
+
+// The query at position pos of a sequence of `keys` tokens, whose first `full`
+// positions every query sees and whose document starts at doc.
+__device__ __forceinline__ KeyRange key_range(const ScoredParams& p, int keys, int pos, int full, int doc) {
+  KeyRange r;
+  r.low = min(max(doc, 0), keys);
+  r.end = max(pos + 1, min(full, keys));
+  r.near = r.low;
+  r.sink_end = r.low;
+  if (p.window > 0) {
+    r.near = max(r.low, pos - p.window + 1);
+    r.sink_end = r.low + min(p.sinks, keys - r.low);
+  }
+  return r;
+}
+
+// The key tiles that some query of the CTA sees: those of the sinks (`lead` of
+// them, from tile `first` on), then those from the nearest key of any query's
+// window or document on (step i >= lead is tile i + skip).
+struct Visit {
+  int steps, first, lead, skip;
+  int low, sink_end, near, end;  // rows outside [low, sink_end) and [near, end) are seen by no query
+  __device__ __forceinline__ int tile(int i) const { return i < lead ? first + i : i + skip; }
+};
+
+// For the queries of tokens [t0, t1] of a chunk behind a prefix of P tokens.
+__device__ __forceinline__ Visit plan_visit(const ScoredParams& p, int64_t q0, int P, int keys, int t0, int t1,
+                                            int full, int lane) {
+  Visit v;
+  v.low = 0;
+  int low1 = 0;
+  v.near = p.window > 0 ? max(0, P + t0 - p.window + 1) : 0;
+  if (p.doc_starts != nullptr) {
+    // the queries' lowest and highest document start and nearest key (every warp for itself)
+    int l0 = INT32_MAX, l1 = 0, n0 = INT32_MAX;
+    for (int t = t0 + lane; t <= t1; t += 32) {
+      const KeyRange r = key_range(p, keys, P + t, full, __ldg(p.doc_starts + q0 + t));
+      l0 = min(l0, r.low);
+      l1 = max(l1, r.low);
+      n0 = min(n0, r.near);
+    }
+    v.low = __reduce_min_sync(0xFFFFFFFFu, l0);
+    low1 = __reduce_max_sync(0xFFFFFFFFu, l1);
+    v.near = __reduce_min_sync(0xFFFFFFFFu, n0);
+  }
+  v.end = key_range(p, keys, P + t1, full, 0).end;
+  v.sink_end = v.low;
+  const int last = (v.end - 1) / kTileN;
+  const int near_tile = min(v.near / kTileN, last);  // one tile at least
+  v.first = near_tile;
+  v.lead = 0;
+  if (p.window > 0 && p.sinks > 0) {
+    v.sink_end = low1 + min(p.sinks, keys - low1);
+    v.first = min(v.low / kTileN, near_tile);
+    v.lead = min((v.sink_end - 1) / kTileN + 1, near_tile) - v.first;
+    if (v.lead < 0) v.lead = 0;
+  }
+  v.skip = near_tile - v.lead;
+  v.steps = v.lead + last - near_tile + 1;
+  return v;
+}
+
+__device__ __forceinline__ uint32_t try_wait(uint32_t bar, uint32_t parity) {
+  uint32_t done;
+  asm volatile(
+      "{ .reg .pred p; mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3; selp.u32 %0, 1, 0, p; }"
+      : "=r"(done) : "r"(bar), "r"(parity), "r"(1000000u) : "memory");
+  return done;
+}
+
+// Wait for a phase with one outcome for the whole warp; false after about kWaitNs.
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity) {
+  if (__all_sync(0xFFFFFFFFu, try_wait(bar, parity))) return true;
+  const uint64_t t0 = global_timer_ns();
+  while (true) {
+    if (__all_sync(0xFFFFFFFFu, try_wait(bar, parity))) return true;
+    if (__shfl_sync(0xFFFFFFFFu, global_timer_ns() - t0 > kWaitNs ? 1 : 0, 0)) return false;
+  }
+}
+
+__device__ __forceinline__ void arrive(uint32_t bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
+template <int M>
+__global__ void __launch_bounds__(kThreads, 1) extend_scored_kernel(const ScoredParams p) {
+  extern __shared__ __align__(1024) uint8_t smem[];
+  __shared__ Barriers bars;
+  __shared__ uint32_t s_tmem;
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int b = blockIdx.y, hk = blockIdx.z;
+  const int tile_tokens = kTileM >> p.log2_group;
+
+  // the sequence: chunk length C, prefix P, first workspace row
+  const int64_t q0 = __ldg(p.cu_q + b);
+  const int64_t chunk = __ldg(p.cu_q + b + 1) - q0;
+  const int C = (int)(chunk < 0 ? 0 : (chunk > p.max_q_len ? p.max_q_len : chunk));
+  const int prefix = __ldg(p.prefix_lens + b);
+  const int P = min(max(prefix, 0), kMaxKeys - min(C, kMaxKeys));
+  if ((C != chunk || P != prefix) && threadIdx.x == 0 && blockIdx.x == 0) flag_error(p.status, NVFP4KV_DEVERR_LENGTH);
+  // the latest (longest) row blocks first
+  const int64_t first_token = (int64_t)(gridDim.x - 1 - blockIdx.x) * 2 * tile_tokens;
+  if (first_token >= min(C, kMaxKeys)) return;  // no query
+  const int t0 = (int)first_token, t1 = min(t0 + 2 * tile_tokens, min(C, kMaxKeys)) - 1;
+  const int keys = P + min(C, kMaxKeys);
+  const int full = p.full_lens != nullptr ? __ldg(p.full_lens + b) : 0;
+
+  const uint32_t sQ = smem_u32(smem), sRing = sQ + 2 * kTileBytes;
+  const uint32_t b_q = smem_u32(&bars.q_full), b_full = smem_u32(&bars.full[0]), b_empty = smem_u32(&bars.empty[0]);
+  const uint32_t b_s = smem_u32(&bars.s_full[0]), b_p = smem_u32(&bars.p_full[0]);  // [2], 8 bytes apart
+  const uint32_t b_drain = smem_u32(&bars.drain);
+  if (threadIdx.x == 0) {
+    mbar_init(b_q, kSoftmaxWarps);
+    for (int s = 0; s < kSlots; ++s) {
+      mbar_init(b_full + 8 * s, kLoadWarps);
+      mbar_init(b_empty + 8 * s, 1);
+    }
+    for (int t = 0; t < 2; ++t) {
+      mbar_init(b_s + 8 * t, 1);
+      mbar_init(b_p + 8 * t, kSoftmaxWarps / 2);
+    }
+    mbar_init(b_drain, 1);
+    fence_mbar_init();
+  }
+  if (warp == kMmaWarp) tc1::tmem_alloc(smem_u32(&s_tmem), kTmemCols);
+  const Visit v = plan_visit(p, q0, P, keys, t0, t1, full, lane);
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  const uint32_t tmem = s_tmem;
+  const int G = p.group;
+
+  if (warp == kMmaWarp) {
+    {
+      // ------------------------------------------------------------ MMA issue
+      if (lane == 0) {
+        constexpr uint32_t id_qk = tc::idesc_f16_f32(kTileM, kTileN, false, false);
+        constexpr uint32_t id_pv = tc::idesc_f16_f32(kTileM, kHeadDim, false, true);
+        // the ring's items are K of step 0, V of step 0, K of step 1, ...: `at` is
+        // the slot of the item in use, `round` the parity of its phase
+        const int items = 2 * v.steps;
+        int item = 0, at = 0;
+        uint32_t round = 0;
+        auto ready = [&]() { return mbar_wait(b_full + 8 * at, round, kWaitNs); };
+        auto done = [&]() {  // free the slot for a later item, if there is one, and step on
+          if (item + kSlots < items) tc1::commit(b_empty + 8 * at);
+          ++item;
+          if (++at == kSlots) {
+            at = 0;
+            round ^= 1;
+          }
+        };
+        auto scores = [&](int t, uint32_t sK) {
+#pragma unroll
+          for (int kk = 0; kk < kHeadDim / 16; ++kk)
+            tc1::mma_f16(tmem + t * kTileN, tc::smem_desc(sQ + t * kTileBytes + kk * 2 * kQLBO, kQLBO, kQSBO),
+                         tc::smem_desc(sK + kk * 256, kLBO, kSBO), id_qk, kk > 0);
+          tc1::commit(b_s + 8 * t);
+        };
+        bool ok = mbar_wait(b_q, 0, kWaitNs) && ready();
+        if (ok) {
+          tc::fence_after_sync();
+          scores(0, sRing);
+          scores(1, sRing);
+          done();
+        }
+        for (int i = 0; i < v.steps && ok; ++i) {
+          const bool more = i + 1 < v.steps;
+          const uint32_t sV = sRing + at * kSlotBytes;
+          if (!(ok = ready())) break;
+          // PV_0, S_0 of the next step, PV_1, S_1 of the next step
+          uint32_t sK = 0;
+          for (int t = 0; t < 2; ++t) {
+            if (!(ok = mbar_wait(b_p + 8 * t, i & 1, kWaitNs))) break;
+            tc::fence_after_sync();
+#pragma unroll
+            for (int kk = 0; kk < kTileN / 16; ++kk)
+              tc1::mma_f16_tmem_a(tmem + kTmemO + t * kHeadDim, tmem + t * kTileN + kk * 8,
+                                  tc::smem_desc_swizzle128(sV + kk * 2 * kVSBO, kVLBO, kVSBO), id_pv,
+                                  (i > 0 || kk > 0) ? 1u : 0u);
+            if (!more) {
+              tc1::commit(b_s + 8 * t);  // O_t is complete
+              continue;
+            }
+            if (t == 0) {
+              // K of the next step is the item after V
+              const int k_at = at + 1 == kSlots ? 0 : at + 1;
+              if (!(ok = mbar_wait(b_full + 8 * k_at, at + 1 == kSlots ? round ^ 1 : round, kWaitNs))) break;
+              tc::fence_after_sync();
+              sK = sRing + k_at * kSlotBytes;
+            } else {
+              done();  // V
+            }
+            scores(t, sK);
+            if (t == 1) done();  // K
+          }
+        }
+        if (!ok) flag_error(p.status, NVFP4KV_DEVERR_TIMEOUT);
+        // nothing this thread issued may still be running when the TMEM is freed
+        tc1::commit(b_drain);
+        mbar_wait(b_drain, 0, kWaitNs);
+      }
+      __syncwarp();
+    }
+  } else if (warp >= kSoftmaxWarps) {
+    // ------------------------------------------------------------ loaders
+    // lane parts of a tile: key 32 lw + 8 g + (lane & 7) (g < 4), bytes 16 part + 64 h (h < 2)
+    const int lw = warp - kSoftmaxWarps, part = lane >> 3;
+    uint4 xk[4][2], xv[4][2];
+    // this thread's bytes of key 0, the bytes from key to key, and the keys whose rows the workspace has
+    const int64_t row0 = __ldg(p.cu_prefix + b), key_bytes = (int64_t)p.hkv * kHeadDim;
+    const uint8_t* const k0 = p.ws_k + (row0 * p.hkv + hk) * kHeadDim + part * 16;
+    const uint8_t* const v0 = p.ws_v + (row0 * p.hkv + hk) * kHeadDim + part * 16;
+    auto clamp_key = [](int64_t j) { return (int)(j < 0 ? 0 : (j > INT32_MAX ? INT32_MAX : j)); };
+    const int row_low = clamp_key(-row0), row_high = clamp_key(p.total_rows - row0);
+    auto load = [&](const uint8_t* ws, int i, uint4 (&x)[4][2]) {
+      const int j0 = v.tile(i) * kTileN + lw * 32 + (lane & 7);
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        const int j = j0 + 8 * g;
+        bool live = j < v.end && (j >= v.near || (j >= v.low && j < v.sink_end));
+        if (live && (j < row_low || j >= row_high)) {
+          flag_error(p.status, NVFP4KV_DEVERR_ROW);
+          live = false;
+        }
+        const uint4* src = reinterpret_cast<const uint4*>(ws + j * key_bytes);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) x[g][h] = live ? __ldg(src + 4 * h) : make_uint4(0, 0, 0, 0);
+      }
+    };
+    load(k0, 0, xk);
+    load(v0, 0, xv);
+    bool ok = true;
+    int s = 0;            // the ring slot
+    uint32_t round = 1;   // the parity of its last release; its first use waits for none
+    bool reuse = false;
+    for (int i = 0; i < v.steps && ok; ++i) {
+#pragma unroll
+      for (int w = 0; w < 2; ++w) {  // K, then V
+        if (reuse && !warp_wait(b_empty + 8 * s, round)) {
+          ok = false;
+          break;
+        }
+        const uint32_t at = sRing + s * kSlotBytes;
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+          const int key = lw * 32 + g * 8 + (lane & 7);
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const uint4 x = w == 0 ? xk[g][h] : xv[g][h];
+            const int d = h * 64 + part * 16;
+            const uint32_t a0 = w == 0 ? kmajor_off(key, d) : v_off(d, key);
+            const uint32_t a1 = w == 0 ? kmajor_off(key, d + 8) : v_off(d + 8, key);
+            st_shared_v4(at + a0, e4m3x8_to_f16x8(x.x, x.y));
+            st_shared_v4(at + a1, e4m3x8_to_f16x8(x.z, x.w));
+          }
+        }
+        tc::fence_smem_to_async();
+        __syncwarp();
+        if (lane == 0) arrive(b_full + 8 * s);
+        if (++s == kSlots) {
+          s = 0;
+          round ^= 1;
+          reuse = true;
+        }
+        if (i + 1 < v.steps) {
+          if (w == 0) load(k0, i + 1, xk);
+          else load(v0, i + 1, xv);
+        }
+      }
+    }
+    if (!ok) flag_error(p.status, NVFP4KV_DEVERR_TIMEOUT);
+  } else {
+    // ------------------------------------------------------------ softmax rows
+    const int tile = warp >> 2, r = threadIdx.x & (kTileM - 1);  // the row tile, the row (TMEM lane)
+    const int t = t0 + tile * tile_tokens + (r >> p.log2_group);
+    const bool live = t <= t1;
+    const int pos = P + t;
+    const int head = hk * G + (r & (G - 1));
+    const int64_t row = (q0 + (live ? t : 0)) * p.hq + head;
+    {
+      const uint4* src = reinterpret_cast<const uint4*>(p.q + row * kHeadDim);
+      const uint32_t dst = sQ + tile * kTileBytes;
+#pragma unroll
+      for (int c = 0; c < kHeadDim / 8; ++c)
+        st_shared_v4(dst + q_off(r, 8 * c), bf16x8_to_f16x8(live ? __ldg(src + c) : make_uint4(0, 0, 0, 0)));
+      tc::fence_smem_to_async();
+      __syncwarp();
+      if (lane == 0) arrive(b_q);
+    }
+    KeyRange kr = key_range(p, keys, pos, full, p.doc_starts != nullptr && live ? __ldg(p.doc_starts + q0 + t) : 0);
+    if (!live) kr.end = 0;  // a row past the chunk sees nothing
+    const float slope = (M & kBiased) != 0 ? __ldg(p.slopes + head) * kLog2e : 0.0f;
+    const float unit = p.unit;
+    const uint32_t t_lane = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
+    const uint32_t t_s = t_lane + tile * kTileN, t_o = t_lane + kTmemO + tile * kHeadDim;
+    const uint32_t bar_s = b_s + 8 * tile, bar_p = b_p + 8 * tile;
+    float m = -INFINITY;
+    float2 l = make_float2(0.0f, 0.0f);
+    bool ok = true;
+    for (int i = 0; i < v.steps; ++i) {
+      if (!warp_wait(bar_s, i & 1)) {
+        ok = false;
+        break;
+      }
+      tc::fence_after_sync();
+      const int kbase = v.tile(i) * kTileN;
+      // keys c of [low, sink) and [near, end) of this tile are visible to the row
+      const int end = kr.end - kbase, low = kr.low - kbase, sink = kr.sink_end - kbase, near = kr.near - kbase;
+      const bool masked = end < kTileN || (near > 0 && (low > 0 || sink < kTileN));
+      const bool any_masked = __any_sync(0xFFFFFFFFu, masked);
+      uint32_t w[2][32];
+      float mr[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+      tc::tmem_ld32_async(t_s, w[0]);
+#pragma unroll
+      for (int c4 = 0; c4 < kTileN / 32; ++c4) {
+        tc::tmem_wait_ld(w[c4 & 1]);
+        if (c4 + 1 < kTileN / 32) tc::tmem_ld32_async(t_s + 32 * (c4 + 1), w[(c4 + 1) & 1]);
+        float2(&x)[16] = *reinterpret_cast<float2(*)[16]>(&w[c4 & 1][0]);
+        if constexpr ((M & kCapped) != 0) cap_scores(x, p.cap);
+        if constexpr ((M & kBiased) != 0) {
+          // base-2 scores from here on: x * unit - slope * |pos - j|
+          const float d0 = (float)(pos - kbase - 32 * c4);
+#pragma unroll
+          for (int c = 0; c < 16; ++c) {
+            x[c].x = fmaf(-slope, fabsf(d0 - (float)(2 * c)), x[c].x * unit);
+            x[c].y = fmaf(-slope, fabsf(d0 - (float)(2 * c + 1)), x[c].y * unit);
+          }
+        }
+        if (any_masked) {
+#pragma unroll
+          for (int c = 0; c < 16; ++c) {
+            const int c0 = 32 * c4 + 2 * c, c1 = c0 + 1;
+            if (c0 >= end || (c0 < near && (c0 < low || c0 >= sink))) x[c].x = -INFINITY;
+            if (c1 >= end || (c1 < near && (c1 < low || c1 >= sink))) x[c].y = -INFINITY;
+          }
+        }
+        if (M != 0 || any_masked) tc::tmem_st32_async(t_s + 32 * c4, w[c4 & 1]);
+#pragma unroll
+        for (int c = 0; c < 16; ++c) mr[c & 3] = fmaxf(mr[c & 3], fmaxf(x[c].x, x[c].y));
+      }
+      // the row max in base-2 units (the unit is positive, so it commutes with max)
+      const float u = (M & kBiased) != 0 ? 1.0f : unit;
+      const float mx = fmaxf(fmaxf(mr[0], mr[1]), fmaxf(mr[2], mr[3])) * u;
+      const bool grow = mx > m + kLazy;  // false while nothing is visible (mx = -inf)
+      if (__any_sync(0xFFFFFFFFu, grow)) {
+        const float alpha = grow ? ex2(m - mx) : 1.0f;  // 0 on the first visible tile (m = -inf)
+        if (grow) m = mx;
+        l = mul2(l, both(alpha));
+        if (i > 0) {
+          // S of this step is complete, so P V of the last one is: O may be rescaled
+#pragma unroll
+          for (int c4 = 0; c4 < kHeadDim / 32; ++c4) {
+            uint32_t o[32];
+            tc::tmem_ld32(t_o + c4 * 32, o);
+#pragma unroll
+            for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * alpha);
+            tc::tmem_st32_async(t_o + c4 * 32, o);
+          }
+        }
+      }
+      // p = 2^(x u - m); masked scores are -inf and give 0, and so does every
+      // score of a row that has seen nothing yet (m = -inf)
+      const float off = m > -INFINITY ? -m : -INFINITY;
+      float2 ls[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
+      if (M != 0 || any_masked) tc::tmem_wait_st();  // the scores put back
+      tc::tmem_ld32_async(t_s, w[0]);
+#pragma unroll
+      for (int c4 = 0; c4 < kTileN / 32; ++c4) {
+        tc::tmem_wait_ld(w[c4 & 1]);
+        if (c4 + 1 < kTileN / 32) tc::tmem_ld32_async(t_s + 32 * (c4 + 1), w[(c4 + 1) & 1]);
+        const float2(&x)[16] = *reinterpret_cast<const float2(*)[16]>(&w[c4 & 1][0]);
+        uint32_t ph[16];
+#pragma unroll
+        for (int c = 0; c < 16; ++c) {
+          float2 e = fma2(x[c], both(u), both(off));
+          e.x = ex2(e.x);
+          e.y = ex2(e.y);
+          ph[c] = f16x2_bits(e.x, e.y);
+          ls[c & 1] = add2(ls[c & 1], e);
+        }
+        // P (two keys per column) over S columns already read: the A operand of P V
+        tc::tmem_st16_async(t_s + 16 * c4, ph);
+      }
+      l = add2(l, add2(ls[0], ls[1]));
+      tc::tmem_wait_st();
+      tc::fence_before_sync();
+      __syncwarp();
+      if (lane == 0) arrive(bar_p);
+    }
+    if (ok && warp_wait(bar_s, v.steps & 1)) {
+      tc::fence_after_sync();
+      const float sum = l.x + l.y;
+      const float inv = sum > 0.0f ? p.out_scale / sum : 0.0f;
+      uint4* dst = reinterpret_cast<uint4*>(p.out + row * kHeadDim);
+      if (live && p.lse != nullptr) p.lse[row] = sum > 0.0f ? (m + log2f(sum)) * kLn2 : -INFINITY;
+#pragma unroll
+      for (int c4 = 0; c4 < kHeadDim / 32; ++c4) {
+        uint32_t w[32];
+        tc::tmem_ld32(t_o + c4 * 32, w);
+        if (live) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            uint32_t o[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              o[k] = pack_bf16x2(__uint_as_float(w[8 * j + 2 * k]) * inv, __uint_as_float(w[8 * j + 2 * k + 1]) * inv);
+            dst[c4 * 4 + j] = make_uint4(o[0], o[1], o[2], o[3]);
+          }
+        }
+      }
+    } else {
+      flag_error(p.status, NVFP4KV_DEVERR_TIMEOUT);
+    }
+  }
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  if (warp == kMmaWarp) tc1::tmem_dealloc(tmem, kTmemCols);
+}
+
+template <int M>
+cudaError_t enqueue(const ScoredParams& p, int32_t batch, cudaStream_t stream) {
+  // the shared-memory limit is an attribute of the function on each device
+  static PerDeviceOnce attr_once;
+  const cudaError_t attr = attr_once.run([] {
+    return cudaFuncSetAttribute(extend_scored_kernel<M>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+  });
+  if (attr != cudaSuccess) return attr;
+  const int64_t blocks = ((int64_t)p.max_q_len * p.group + kRows - 1) / kRows;
+  const dim3 grid((unsigned)blocks, (unsigned)batch, (unsigned)p.hkv);
+  extend_scored_kernel<M><<<grid, kThreads, kSmemBytes, stream>>>(p);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_extend_scored(const uint16_t* q, const int64_t* cu_q, int32_t max_q_len, const uint8_t* ws_k,
+                                 const uint8_t* ws_v, const int64_t* cu_prefix, const int32_t* prefix_lens,
+                                 int32_t batch, int64_t total_rows, int32_t num_q_heads, int32_t num_kv_heads,
+                                 float k_ws_scale, float v_ws_scale, float softmax_scale, const nvfp4kv_scoring& sc,
+                                 const int32_t* full_lens, const int32_t* doc_starts, uint16_t* out, float* lse,
+                                 int32_t* device_status, cudaStream_t stream) {
+  ScoredParams p = {};
+  p.q = q;
+  p.cu_q = cu_q;
+  p.ws_k = ws_k;
+  p.ws_v = ws_v;
+  p.cu_prefix = cu_prefix;
+  p.prefix_lens = prefix_lens;
+  p.hq = num_q_heads;
+  p.hkv = num_kv_heads;
+  p.group = num_q_heads / num_kv_heads;
+  while ((1 << p.log2_group) < p.group) ++p.log2_group;
+  p.max_q_len = max_q_len;
+  p.total_rows = total_rows;
+  const double scale = (double)softmax_scale * (double)k_ws_scale;
+  p.unit = (float)((sc.softcap > 0.0f ? (double)sc.softcap : scale) * 1.4426950408889634);
+  p.out_scale = v_ws_scale;
+  if (sc.softcap > 0.0f) p.cap = cap_poly(scale / (double)sc.softcap);
+  p.window = sc.window;
+  p.sinks = sc.sinks;
+  p.slopes = sc.slopes;
+  p.full_lens = full_lens;
+  p.doc_starts = doc_starts;
+  p.out = out;
+  p.lse = lse;
+  p.status = device_status;
+  if (sc.softcap > 0.0f)
+    return sc.slopes ? enqueue<kCapped | kBiased>(p, batch, stream) : enqueue<kCapped>(p, batch, stream);
+  return sc.slopes ? enqueue<kBiased>(p, batch, stream) : enqueue<0>(p, batch, stream);
+}
+
+}  // namespace nvfp4kv
