@@ -5,18 +5,13 @@
 //
 // A CTA owns 256 query rows of one (sequence, KV head): two tiles of 128 rows
 // (128 / G tokens x the G query heads of the KV head), so each K/V tile feeds
-// 256 rows.  13 warps:
+// 256 rows.  16 warps:
 //   - Warps 0-3 and 4-7, a softmax group per row tile: one query row per
 //     thread (TMEM lane = row).  They write the row of Q (f16) into shared
-//     memory, then per key tile pass over the S row twice, 32 columns at a time
-//     with the next 32 on their way: the first pass caps, biases and masks the
-//     scores (and puts them back where that changed them) and finds their
-//     maximum, the second takes the exponentials and writes P (f16) over S
-//     columns already read.  The softmax is a lazy base-2 online one (the running
-//     max moves only when it grows by 2^8, and O is then rescaled in TMEM).  At
-//     the end: O * s_ws(V) / l -> bf16.  (Holding the whole row of 128 scores in
-//     registers spilled; with 224 KB of shared memory in use there is next to no
-//     L1 left, and a spilled word came back from L2 after some 400 cycles.)
+//     memory, then per key tile read the S row (128 registers), cap, bias and
+//     mask it, run the lazy base-2 online softmax (the running max moves only
+//     when it grows by 2^8, and O is then rescaled in TMEM), and write P (f16)
+//     over the S columns just read.  At the end: O * s_ws(V) / l -> bf16.
 //   - Warps 8-11 load the key tiles of the workspace (K and V alternately, one
 //     of each in flight in registers), convert E4M3 -> f16 (exact) and store
 //     them as B operands (K K-major, V MN-major) in a ring of five 32 KB slots.
@@ -26,6 +21,10 @@
 //     core works for the other; MMAs execute in issue order, so S_t(i + 1) may
 //     overwrite the columns that P_t(i) was read from, and the completion of
 //     S_t(i + 1) implies that of PV_t(i).
+// Registers: the softmax groups take what the loaders and the MMA group give
+// back (setmaxnreg).  Nothing may spill: with 224 KB of shared memory in use there
+// is next to no L1 left, and a spilled word comes back from L2 after some 400
+// cycles.
 // TMEM (512 columns): S_0 0-127, S_1 128-255 (P_t in the first 64 of S_t),
 // O_0 256-383, O_1 384-511.
 // Key tiles that no query of the CTA sees are skipped, and workspace rows that
@@ -51,7 +50,7 @@ constexpr int kTileN = 128;    // keys per K/V tile
 constexpr int kRows = 2 * kTileM;
 constexpr int kSoftmaxWarps = 8, kLoadWarps = 4;
 constexpr int kMmaWarp = kSoftmaxWarps + kLoadWarps;
-constexpr int kThreads = (kMmaWarp + 1) * 32;  // 416
+constexpr int kThreads = (kMmaWarp + 4) * 32;  // 512: the MMA warp's group is whole for setmaxnreg
 constexpr uint32_t kTileBytes = kTileN * kHeadDim * 2;  // one f16 tile (of Q, K or V), 32 KB
 constexpr uint32_t kSlotBytes = kTileBytes;
 constexpr int kSlots = 5;                               // K/V ring
@@ -59,6 +58,9 @@ constexpr uint32_t kSmemBytes = 2 * kTileBytes + kSlots * kSlotBytes;  // 224 KB
 constexpr uint32_t kTmemCols = 512, kTmemO = 256;
 constexpr float kLazy = 8.0f;
 constexpr uint64_t kWaitNs = 1000000000ull;
+// registers: 512 threads are launched with 128 each, 65536 in all
+constexpr int kSoftmaxRegs = 184, kLoadRegs = 104, kMmaRegs = 40;
+static_assert(256 * kSoftmaxRegs + 128 * kLoadRegs + 128 * kMmaRegs <= 512 * 128, "register split");
 
 struct ScoredParams {
   const uint16_t* q;
@@ -175,6 +177,15 @@ __device__ __forceinline__ Visit plan_visit(const ScoredParams& p, int64_t q0, i
   return v;
 }
 
+template <int kRegs>
+__device__ __forceinline__ void more_registers() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegs));
+}
+template <int kRegs>
+__device__ __forceinline__ void fewer_registers() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs));
+}
+
 __device__ __forceinline__ uint32_t try_wait(uint32_t bar, uint32_t parity) {
   uint32_t done;
   asm volatile(
@@ -192,6 +203,9 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity) {
     if (__shfl_sync(0xFFFFFFFFu, global_timer_ns() - t0 > kWaitNs ? 1 : 0, 0)) return false;
   }
 }
+
+// The first n of 32 bits.
+__device__ __forceinline__ uint32_t first_bits(int n) { return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1u; }
 
 __device__ __forceinline__ void arrive(uint32_t bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
@@ -239,6 +253,16 @@ __global__ void __launch_bounds__(kThreads, 1) extend_scored_kernel(const Scored
     fence_mbar_init();
   }
   if (warp == kMmaWarp) tc1::tmem_alloc(smem_u32(&s_tmem), kTmemCols);
+  // bring the CTA's query rows (one 256-byte row per softmax thread) closer
+  // while the rest is set up
+  if (threadIdx.x < kRows) {
+    const int64_t t = t0 + (threadIdx.x >> p.log2_group);
+    if (t <= t1) {
+      const uint16_t* q = p.q + ((q0 + t) * p.hq + hk * p.group + (threadIdx.x & (p.group - 1))) * kHeadDim;
+      asm volatile("prefetch.global.L2 [%0];" ::"l"(q));
+      asm volatile("prefetch.global.L2 [%0];" ::"l"(q + 64));
+    }
+  }
   const Visit v = plan_visit(p, q0, P, keys, t0, t1, full, lane);
   tc::fence_before_sync();
   __syncthreads();
@@ -246,106 +270,106 @@ __global__ void __launch_bounds__(kThreads, 1) extend_scored_kernel(const Scored
   const uint32_t tmem = s_tmem;
   const int G = p.group;
 
-  if (warp == kMmaWarp) {
-    {
+  if (warp >= kMmaWarp) {
+    fewer_registers<kMmaRegs>();
+    if (warp == kMmaWarp) {
       // ------------------------------------------------------------ MMA issue
-      if (lane == 0) {
-        constexpr uint32_t id_qk = tc::idesc_f16_f32(kTileM, kTileN, false, false);
-        constexpr uint32_t id_pv = tc::idesc_f16_f32(kTileM, kHeadDim, false, true);
-        // the ring's items are K of step 0, V of step 0, K of step 1, ...: `at` is
-        // the slot of the item in use, `round` the parity of its phase
-        const int items = 2 * v.steps;
-        int item = 0, at = 0;
-        uint32_t round = 0;
-        auto ready = [&]() { return mbar_wait(b_full + 8 * at, round, kWaitNs); };
-        auto done = [&]() {  // free the slot for a later item, if there is one, and step on
-          if (item + kSlots < items) tc1::commit(b_empty + 8 * at);
-          ++item;
-          if (++at == kSlots) {
-            at = 0;
-            round ^= 1;
-          }
-        };
-        auto scores = [&](int t, uint32_t sK) {
-#pragma unroll
-          for (int kk = 0; kk < kHeadDim / 16; ++kk)
-            tc1::mma_f16(tmem + t * kTileN, tc::smem_desc(sQ + t * kTileBytes + kk * 2 * kQLBO, kQLBO, kQSBO),
-                         tc::smem_desc(sK + kk * 256, kLBO, kSBO), id_qk, kk > 0);
-          tc1::commit(b_s + 8 * t);
-        };
-        bool ok = mbar_wait(b_q, 0, kWaitNs) && ready();
-        if (ok) {
-          tc::fence_after_sync();
-          scores(0, sRing);
-          scores(1, sRing);
-          done();
+      // The whole warp runs this loop (so that addresses and descriptors live in
+      // uniform registers) and one lane's instructions take effect.
+      constexpr uint32_t id_qk = tc::idesc_f16_f32(kTileM, kTileN, false, false);
+      constexpr uint32_t id_pv = tc::idesc_f16_f32(kTileM, kHeadDim, false, true);
+      const uint32_t lead = lane == 0;
+      // shared-memory descriptors are a constant plus the address in their low word
+      const uint64_t dq = tc::smem_desc(0, kQLBO, kQSBO), dk = tc::smem_desc(0, kLBO, kSBO),
+                     dv = tc::smem_desc_swizzle128(0, kVLBO, kVSBO);
+      // the ring's items are K of step 0, V of step 0, K of step 1, ...: `at` is
+      // the slot of the item in use, `round` the parity of its phase
+      const int items = 2 * v.steps;
+      int item = 0, at = 0;
+      uint32_t round = 0;
+      auto ready = [&]() { return warp_wait(b_full + 8 * at, round); };
+      auto done = [&]() {  // free the slot for a later item, if there is one, and step on
+        if (item + kSlots < items) tc1::commit(b_empty + 8 * at, lead);
+        ++item;
+        if (++at == kSlots) {
+          at = 0;
+          round ^= 1;
         }
-        for (int i = 0; i < v.steps && ok; ++i) {
-          const bool more = i + 1 < v.steps;
-          const uint32_t sV = sRing + at * kSlotBytes;
-          if (!(ok = ready())) break;
-          // PV_0, S_0 of the next step, PV_1, S_1 of the next step
-          uint32_t sK = 0;
-          for (int t = 0; t < 2; ++t) {
-            if (!(ok = mbar_wait(b_p + 8 * t, i & 1, kWaitNs))) break;
-            tc::fence_after_sync();
+      };
+      auto scores = [&](int t, int slot) {  // S_t = Q_t K^T
+        uint32_t q = (sQ + t * kTileBytes) >> 4, k = (sRing + slot * kSlotBytes) >> 4;
+        asm volatile("" : "+r"(q));  // not worth 16 registers across the loop
 #pragma unroll
-            for (int kk = 0; kk < kTileN / 16; ++kk)
-              tc1::mma_f16_tmem_a(tmem + kTmemO + t * kHeadDim, tmem + t * kTileN + kk * 8,
-                                  tc::smem_desc_swizzle128(sV + kk * 2 * kVSBO, kVLBO, kVSBO), id_pv,
-                                  (i > 0 || kk > 0) ? 1u : 0u);
-            if (!more) {
-              tc1::commit(b_s + 8 * t);  // O_t is complete
-              continue;
-            }
-            if (t == 0) {
-              // K of the next step is the item after V
-              const int k_at = at + 1 == kSlots ? 0 : at + 1;
-              if (!(ok = mbar_wait(b_full + 8 * k_at, at + 1 == kSlots ? round ^ 1 : round, kWaitNs))) break;
-              tc::fence_after_sync();
-              sK = sRing + k_at * kSlotBytes;
-            } else {
-              done();  // V
-            }
-            scores(t, sK);
-            if (t == 1) done();  // K
-          }
-        }
-        if (!ok) flag_error(p.status, NVFP4KV_DEVERR_TIMEOUT);
-        // nothing this thread issued may still be running when the TMEM is freed
-        tc1::commit(b_drain);
-        mbar_wait(b_drain, 0, kWaitNs);
+        for (int kk = 0; kk < kHeadDim / 16; ++kk)
+          tc1::mma_f16(tmem + t * kTileN, dq | (q + kk * (2 * kQLBO >> 4)), dk | (k + kk * (256 >> 4)), id_qk, kk > 0,
+                       lead);
+        tc1::commit(b_s + 8 * t, lead);
+      };
+      bool ok = warp_wait(b_q, 0) && ready();
+      if (ok) {
+        tc::fence_after_sync();
+        scores(0, 0);
+        scores(1, 0);
+        done();
       }
-      __syncwarp();
+      for (int i = 0; i < v.steps && ok; ++i) {
+        const bool more = i + 1 < v.steps;
+        const int v_at = at, k_at = at + 1 == kSlots ? 0 : at + 1;  // V of this step, K of the next
+        if (!(ok = ready())) break;
+        if (more && !(ok = warp_wait(b_full + 8 * k_at, k_at == 0 ? round ^ 1 : round))) break;
+        // PV_0, S_0 of the next step, PV_1, S_1 of the next step
+#pragma unroll 1
+        for (int t = 0; t < 2; ++t) {
+          if (!(ok = warp_wait(b_p + 8 * t, i & 1))) break;
+          tc::fence_after_sync();
+          const uint32_t vv = (sRing + v_at * kSlotBytes) >> 4;
+#pragma unroll
+          for (int kk = 0; kk < kTileN / 16; ++kk)
+            tc1::mma_f16_tmem_a(tmem + kTmemO + t * kHeadDim, tmem + t * kTileN + kk * 8,
+                                dv | (vv + kk * (2 * kVSBO >> 4)), id_pv, (i > 0 || kk > 0) ? 1u : 0u, lead);
+          if (t == 1) done();  // V
+          if (more)
+            scores(t, k_at);
+          else
+            tc1::commit(b_s + 8 * t, lead);  // O_t is complete
+          if (t == 1 && more) done();  // K
+        }
+      }
+      if (!ok && lane == 0) flag_error(p.status, NVFP4KV_DEVERR_TIMEOUT);
+      // nothing this warp issued may still be running when the TMEM is freed
+      tc1::commit(b_drain, lead);
+      warp_wait(b_drain, 0);
     }
   } else if (warp >= kSoftmaxWarps) {
     // ------------------------------------------------------------ loaders
+    fewer_registers<kLoadRegs>();
     // lane parts of a tile: key 32 lw + 8 g + (lane & 7) (g < 4), bytes 16 part + 64 h (h < 2)
     const int lw = warp - kSoftmaxWarps, part = lane >> 3;
     uint4 xk[4][2], xv[4][2];
-    // this thread's bytes of key 0, the bytes from key to key, and the keys whose rows the workspace has
+    // this thread's first byte of key 0 in a workspace, and the bytes from key to key
     const int64_t row0 = __ldg(p.cu_prefix + b), key_bytes = (int64_t)p.hkv * kHeadDim;
-    const uint8_t* const k0 = p.ws_k + (row0 * p.hkv + hk) * kHeadDim + part * 16;
-    const uint8_t* const v0 = p.ws_v + (row0 * p.hkv + hk) * kHeadDim + part * 16;
+    const int64_t key0 = (row0 * p.hkv + hk) * kHeadDim + part * 16;
+    // the keys to load: those some query sees and whose rows the workspace has
     auto clamp_key = [](int64_t j) { return (int)(j < 0 ? 0 : (j > INT32_MAX ? INT32_MAX : j)); };
     const int row_low = clamp_key(-row0), row_high = clamp_key(p.total_rows - row0);
+    if (min(v.near, v.sink_end > v.low ? v.low : v.near) < row_low || v.end > row_high)
+      flag_error(p.status, NVFP4KV_DEVERR_ROW);
+    const int near = max(v.near, row_low), low = max(v.low, row_low);
+    const int end = min(v.end, row_high), sink_end = min(v.sink_end, row_high);
     auto load = [&](const uint8_t* ws, int i, uint4 (&x)[4][2]) {
       const int j0 = v.tile(i) * kTileN + lw * 32 + (lane & 7);
+      const uint8_t* src = ws + (key0 + j0 * key_bytes);
 #pragma unroll
       for (int g = 0; g < 4; ++g) {
         const int j = j0 + 8 * g;
-        bool live = j < v.end && (j >= v.near || (j >= v.low && j < v.sink_end));
-        if (live && (j < row_low || j >= row_high)) {
-          flag_error(p.status, NVFP4KV_DEVERR_ROW);
-          live = false;
-        }
-        const uint4* src = reinterpret_cast<const uint4*>(ws + j * key_bytes);
+        const bool live = j < end && (j >= near || (j >= low && j < sink_end));
 #pragma unroll
-        for (int h = 0; h < 2; ++h) x[g][h] = live ? __ldg(src + 4 * h) : make_uint4(0, 0, 0, 0);
+        for (int h = 0; h < 2; ++h)
+          x[g][h] = live ? __ldg(reinterpret_cast<const uint4*>(src + 8 * g * key_bytes) + 4 * h) : make_uint4(0, 0, 0, 0);
       }
     };
-    load(k0, 0, xk);
-    load(v0, 0, xv);
+    load(p.ws_k, 0, xk);
+    load(p.ws_v, 0, xv);
     bool ok = true;
     int s = 0;            // the ring slot
     uint32_t round = 1;   // the parity of its last release; its first use waits for none
@@ -380,14 +404,15 @@ __global__ void __launch_bounds__(kThreads, 1) extend_scored_kernel(const Scored
           reuse = true;
         }
         if (i + 1 < v.steps) {
-          if (w == 0) load(k0, i + 1, xk);
-          else load(v0, i + 1, xv);
+          if (w == 0) load(p.ws_k, i + 1, xk);
+          else load(p.ws_v, i + 1, xv);
         }
       }
     }
     if (!ok) flag_error(p.status, NVFP4KV_DEVERR_TIMEOUT);
   } else {
     // ------------------------------------------------------------ softmax rows
+    more_registers<kSoftmaxRegs>();
     const int tile = warp >> 2, r = threadIdx.x & (kTileM - 1);  // the row tile, the row (TMEM lane)
     const int t = t0 + tile * tile_tokens + (r >> p.log2_group);
     const bool live = t <= t1;
@@ -412,7 +437,8 @@ __global__ void __launch_bounds__(kThreads, 1) extend_scored_kernel(const Scored
     const uint32_t t_s = t_lane + tile * kTileN, t_o = t_lane + kTmemO + tile * kHeadDim;
     const uint32_t bar_s = b_s + 8 * tile, bar_p = b_p + 8 * tile;
     float m = -INFINITY;
-    float2 l = make_float2(0.0f, 0.0f);
+    float2 l[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
+    const float u = (M & kBiased) != 0 ? 1.0f : unit;  // base-2 score per unit of what is exponentiated
     bool ok = true;
     for (int i = 0; i < v.steps; ++i) {
       if (!warp_wait(bar_s, i & 1)) {
@@ -425,80 +451,70 @@ __global__ void __launch_bounds__(kThreads, 1) extend_scored_kernel(const Scored
       const int end = kr.end - kbase, low = kr.low - kbase, sink = kr.sink_end - kbase, near = kr.near - kbase;
       const bool masked = end < kTileN || (near > 0 && (low > 0 || sink < kTileN));
       const bool any_masked = __any_sync(0xFFFFFFFFu, masked);
-      uint32_t w[2][32];
-      float mr[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-      tc::tmem_ld32_async(t_s, w[0]);
+      uint32_t w[kTileN];
+      tc::tmem_ld128(t_s, w);
+      float2(&x)[kTileN / 2] = *reinterpret_cast<float2(*)[kTileN / 2]>(&w[0]);
+      if constexpr ((M & kCapped) != 0) cap_scores(x, p.cap);
+      if constexpr ((M & kBiased) != 0) {
+        // base-2 scores from here on: x * unit - slope * |pos - j|
+        const float d0 = (float)(pos - kbase);
 #pragma unroll
-      for (int c4 = 0; c4 < kTileN / 32; ++c4) {
-        tc::tmem_wait_ld(w[c4 & 1]);
-        if (c4 + 1 < kTileN / 32) tc::tmem_ld32_async(t_s + 32 * (c4 + 1), w[(c4 + 1) & 1]);
-        float2(&x)[16] = *reinterpret_cast<float2(*)[16]>(&w[c4 & 1][0]);
-        if constexpr ((M & kCapped) != 0) cap_scores(x, p.cap);
-        if constexpr ((M & kBiased) != 0) {
-          // base-2 scores from here on: x * unit - slope * |pos - j|
-          const float d0 = (float)(pos - kbase - 32 * c4);
-#pragma unroll
-          for (int c = 0; c < 16; ++c) {
-            x[c].x = fmaf(-slope, fabsf(d0 - (float)(2 * c)), x[c].x * unit);
-            x[c].y = fmaf(-slope, fabsf(d0 - (float)(2 * c + 1)), x[c].y * unit);
-          }
+        for (int c = 0; c < kTileN / 2; ++c) {
+          x[c].x = fmaf(-slope, fabsf(d0 - (float)(2 * c)), x[c].x * unit);
+          x[c].y = fmaf(-slope, fabsf(d0 - (float)(2 * c + 1)), x[c].y * unit);
         }
-        if (any_masked) {
-#pragma unroll
-          for (int c = 0; c < 16; ++c) {
-            const int c0 = 32 * c4 + 2 * c, c1 = c0 + 1;
-            if (c0 >= end || (c0 < near && (c0 < low || c0 >= sink))) x[c].x = -INFINITY;
-            if (c1 >= end || (c1 < near && (c1 < low || c1 >= sink))) x[c].y = -INFINITY;
-          }
-        }
-        if (M != 0 || any_masked) tc::tmem_st32_async(t_s + 32 * c4, w[c4 & 1]);
-#pragma unroll
-        for (int c = 0; c < 16; ++c) mr[c & 3] = fmaxf(mr[c & 3], fmaxf(x[c].x, x[c].y));
       }
+      if (any_masked) {
+#pragma unroll
+        for (int c4 = 0; c4 < kTileN / 32; ++c4) {
+          const int at = 32 * c4;
+          const uint32_t hidden = ~first_bits(end - at) |
+                                  (first_bits(near - at) & ~(first_bits(sink - at) & ~first_bits(low - at)));
+#pragma unroll
+          for (int c = 0; c < 32; ++c)
+            if (hidden >> c & 1) w[at + c] = 0xFF800000u;  // -inf
+        }
+      }
+      float mr[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+      for (int c = 0; c < kTileN / 2; ++c) mr[c & 3] = fmaxf(mr[c & 3], fmaxf(x[c].x, x[c].y));
       // the row max in base-2 units (the unit is positive, so it commutes with max)
-      const float u = (M & kBiased) != 0 ? 1.0f : unit;
       const float mx = fmaxf(fmaxf(mr[0], mr[1]), fmaxf(mr[2], mr[3])) * u;
       const bool grow = mx > m + kLazy;  // false while nothing is visible (mx = -inf)
       if (__any_sync(0xFFFFFFFFu, grow)) {
         const float alpha = grow ? ex2(m - mx) : 1.0f;  // 0 on the first visible tile (m = -inf)
         if (grow) m = mx;
-        l = mul2(l, both(alpha));
+        l[0] = mul2(l[0], both(alpha));
+        l[1] = mul2(l[1], both(alpha));
         if (i > 0) {
-          // S of this step is complete, so P V of the last one is: O may be rescaled
+          // S of this step is complete, so P V of the last one is: O is at rest
+#pragma unroll 1
+          for (int k = 0; k < kHeadDim / 16; ++k) {
+            uint32_t o[16];
+            tc::tmem_ld16(t_o + 16 * k, o);
 #pragma unroll
-          for (int c4 = 0; c4 < kHeadDim / 32; ++c4) {
-            uint32_t o[32];
-            tc::tmem_ld32(t_o + c4 * 32, o);
-#pragma unroll
-            for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * alpha);
-            tc::tmem_st32_async(t_o + c4 * 32, o);
+            for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * alpha);
+            tc::tmem_st16_async(t_o + 16 * k, o);
           }
         }
       }
       // p = 2^(x u - m); masked scores are -inf and give 0, and so does every
       // score of a row that has seen nothing yet (m = -inf)
       const float off = m > -INFINITY ? -m : -INFINITY;
-      float2 ls[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
-      if (M != 0 || any_masked) tc::tmem_wait_st();  // the scores put back
-      tc::tmem_ld32_async(t_s, w[0]);
 #pragma unroll
       for (int c4 = 0; c4 < kTileN / 32; ++c4) {
-        tc::tmem_wait_ld(w[c4 & 1]);
-        if (c4 + 1 < kTileN / 32) tc::tmem_ld32_async(t_s + 32 * (c4 + 1), w[(c4 + 1) & 1]);
-        const float2(&x)[16] = *reinterpret_cast<const float2(*)[16]>(&w[c4 & 1][0]);
         uint32_t ph[16];
 #pragma unroll
         for (int c = 0; c < 16; ++c) {
-          float2 e = fma2(x[c], both(u), both(off));
+          float2 e = fma2(x[16 * c4 + c], both(u), both(off));
           e.x = ex2(e.x);
           e.y = ex2(e.y);
           ph[c] = f16x2_bits(e.x, e.y);
-          ls[c & 1] = add2(ls[c & 1], e);
+          l[c & 1] = add2(l[c & 1], e);
         }
-        // P (two keys per column) over S columns already read: the A operand of P V
+        // P (two keys per column) over the S columns: the A operand of P V
         tc::tmem_st16_async(t_s + 16 * c4, ph);
       }
-      l = add2(l, add2(ls[0], ls[1]));
       tc::tmem_wait_st();
       tc::fence_before_sync();
       __syncwarp();
@@ -506,7 +522,7 @@ __global__ void __launch_bounds__(kThreads, 1) extend_scored_kernel(const Scored
     }
     if (ok && warp_wait(bar_s, v.steps & 1)) {
       tc::fence_after_sync();
-      const float sum = l.x + l.y;
+      const float sum = (l[0].x + l[1].x) + (l[0].y + l[1].y);
       const float inv = sum > 0.0f ? p.out_scale / sum : 0.0f;
       uint4* dst = reinterpret_cast<uint4*>(p.out + row * kHeadDim);
       if (live && p.lse != nullptr) p.lse[row] = sum > 0.0f ? (m + log2f(sum)) * kLn2 : -INFINITY;
