@@ -8,10 +8,12 @@
 // 256 rows.  16 warps:
 //   - Warps 0-3 and 4-7, a softmax group per row tile: one query row per
 //     thread (TMEM lane = row).  They write the row of Q (f16) into shared
-//     memory, then per key tile read the S row (128 registers), cap, bias and
-//     mask it, run the lazy base-2 online softmax (the running max moves only
-//     when it grows by 2^8, and O is then rescaled in TMEM), and write P (f16)
-//     over the S columns just read.  At the end: O * s_ws(V) / l -> bf16.
+//     memory, then per key tile read the S row, cap, bias and mask it (putting
+//     it back where that changes it) and find its maximum, run the lazy base-2
+//     online softmax (the running max moves only when it grows by 2^8, and O is
+//     then rescaled in TMEM), read the row once more for the exponentials, and
+//     write P (f16) over the S columns just read.  At the end: O * s_ws(V) / l ->
+//     bf16.
 //   - Warps 8-11 load the key tiles of the workspace (K and V alternately, one
 //     of each in flight in registers), convert E4M3 -> f16 (exact) and store
 //     them as B operands (K K-major, V MN-major) in a ring of five 32 KB slots.
@@ -59,7 +61,7 @@ constexpr uint32_t kTmemCols = 512, kTmemO = 256;
 constexpr float kLazy = 8.0f;
 constexpr uint64_t kWaitNs = 1000000000ull;
 // registers: 512 threads are launched with 128 each, 65536 in all
-constexpr int kSoftmaxRegs = 184, kLoadRegs = 104, kMmaRegs = 40;
+constexpr int kSoftmaxRegs = 192, kLoadRegs = 104, kMmaRegs = 24;
 static_assert(256 * kSoftmaxRegs + 128 * kLoadRegs + 128 * kMmaRegs <= 512 * 128, "register split");
 
 struct ScoredParams {
@@ -72,9 +74,9 @@ struct ScoredParams {
   int32_t hq, hkv, group, log2_group;
   int32_t max_q_len;
   int64_t total_rows;
-  float unit;                // base-2 score per unit of q . k (of the tanh, capped)
+  float unit;                // base-2 score per unit of q . k (not capped)
   float out_scale;           // v_ws_scale
-  CapPoly cap;               // capped: q . k -> tanh(x / softcap)
+  CapPoly cap;               // capped: q . k -> base-2 score
   int32_t window, sinks;     // 0: no window
   const float* slopes;       // [hq], biased
   const int32_t* full_lens;  // [batch] or null
@@ -97,13 +99,13 @@ struct Barriers {
 // of one 16-byte K chunk next to each other.
 constexpr uint32_t kQLBO = kTileM * 16, kQSBO = 128;
 __device__ __forceinline__ uint32_t q_off(int row, int k) { return (uint32_t)(k >> 3) * kQLBO + (uint32_t)row * 16; }
-// V (MN-major: a key's head dims are contiguous) in the 128-byte swizzle: atoms
-// of 8 keys x 64 head dims, the 16-byte chunk c of key r stored at c ^ r; the
-// key groups of one half of the head dims follow one another.
-constexpr uint32_t kVLBO = kTileBytes / 2, kVSBO = 1024;  // next 64 head dims, next 8 keys
-__device__ __forceinline__ uint32_t v_off(int d, int key) {
-  return (uint32_t)(d >> 6) * kVLBO + (uint32_t)(key >> 3) * kVSBO + (uint32_t)(key & 7) * 128 +
-         ((((uint32_t)d >> 3) ^ (uint32_t)key) & 7) * 16;
+// K and V in shared memory, in the 128-byte swizzle: atoms of 8 keys x 64 head
+// dims, the 16-byte chunk c (8 head dims) of key r stored at c ^ r; the key
+// groups of one half of the head dims follow one another.  For K (contracted
+// over head dims) this is the K-major form, for V (over keys) the MN-major one.
+constexpr uint32_t kHalfD = kTileBytes / 2, kSBO8 = 1024;  // next 64 head dims, next 8 keys
+__device__ __forceinline__ uint32_t kv_off(int key, int chunk) {  // chunk 0 .. 15
+  return (uint32_t)(chunk >> 3) * kHalfD + (uint32_t)key * 128 + (((uint32_t)chunk ^ (uint32_t)key) & 7) * 16;
 }
 
 // Positions within a sequence are 32-bit: prefix and chunk together stay below
@@ -217,7 +219,8 @@ __global__ void __launch_bounds__(kThreads, 1) extend_scored_kernel(const Scored
   __shared__ Barriers bars;
   __shared__ uint32_t s_tmem;
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // the broadcast tells the compiler that a warp's lanes take the same role
+  const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const int b = blockIdx.y, hk = blockIdx.z;
   const int tile_tokens = kTileM >> p.log2_group;
 
@@ -267,7 +270,7 @@ __global__ void __launch_bounds__(kThreads, 1) extend_scored_kernel(const Scored
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
-  const uint32_t tmem = s_tmem;
+  const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, s_tmem, 0);
   const int G = p.group;
 
   if (warp >= kMmaWarp) {
@@ -280,8 +283,7 @@ __global__ void __launch_bounds__(kThreads, 1) extend_scored_kernel(const Scored
       constexpr uint32_t id_pv = tc::idesc_f16_f32(kTileM, kHeadDim, false, true);
       const uint32_t lead = lane == 0;
       // shared-memory descriptors are a constant plus the address in their low word
-      const uint64_t dq = tc::smem_desc(0, kQLBO, kQSBO), dk = tc::smem_desc(0, kLBO, kSBO),
-                     dv = tc::smem_desc_swizzle128(0, kVLBO, kVSBO);
+      const uint64_t dq = tc::smem_desc(0, kQLBO, kQSBO), dkv = tc::smem_desc_swizzle128(0, kHalfD, kSBO8);
       // the ring's items are K of step 0, V of step 0, K of step 1, ...: `at` is
       // the slot of the item in use, `round` the parity of its phase
       const int items = 2 * v.steps;
@@ -301,7 +303,7 @@ __global__ void __launch_bounds__(kThreads, 1) extend_scored_kernel(const Scored
         asm volatile("" : "+r"(q));  // not worth 16 registers across the loop
 #pragma unroll
         for (int kk = 0; kk < kHeadDim / 16; ++kk)
-          tc1::mma_f16(tmem + t * kTileN, dq | (q + kk * (2 * kQLBO >> 4)), dk | (k + kk * (256 >> 4)), id_qk, kk > 0,
+          tc1::mma_f16(tmem + t * kTileN, dq | (q + kk * (2 * kQLBO >> 4)), dkv | (k + (kk >> 2) * (kHalfD >> 4) + (kk & 3) * 2), id_qk, kk > 0,
                        lead);
         tc1::commit(b_s + 8 * t, lead);
       };
@@ -326,7 +328,7 @@ __global__ void __launch_bounds__(kThreads, 1) extend_scored_kernel(const Scored
 #pragma unroll
           for (int kk = 0; kk < kTileN / 16; ++kk)
             tc1::mma_f16_tmem_a(tmem + kTmemO + t * kHeadDim, tmem + t * kTileN + kk * 8,
-                                dv | (vv + kk * (2 * kVSBO >> 4)), id_pv, (i > 0 || kk > 0) ? 1u : 0u, lead);
+                                dkv | (vv + kk * (2 * kSBO8 >> 4)), id_pv, (i > 0 || kk > 0) ? 1u : 0u, lead);
           if (t == 1) done();  // V
           if (more)
             scores(t, k_at);
@@ -343,9 +345,10 @@ __global__ void __launch_bounds__(kThreads, 1) extend_scored_kernel(const Scored
   } else if (warp >= kSoftmaxWarps) {
     // ------------------------------------------------------------ loaders
     fewer_registers<kLoadRegs>();
-    // lane parts of a tile: key 32 lw + 8 g + (lane & 7) (g < 4), bytes 16 part + 64 h (h < 2)
-    const int lw = warp - kSoftmaxWarps, part = lane >> 3;
-    uint4 xk[4][2], xv[4][2];
+    // lane parts of a tile: key 32 lw + 4 g + lane / 8 (g < 8), its 16 bytes (head
+    // dims) 16 (lane % 8): whole 128-byte rows per load
+    const int lw = warp - kSoftmaxWarps, part = lane & 7;
+    uint4 xk[8], xv[8];
     // this thread's first byte of key 0 in a workspace, and the bytes from key to key
     const int64_t row0 = __ldg(p.cu_prefix + b), key_bytes = (int64_t)p.hkv * kHeadDim;
     const int64_t key0 = (row0 * p.hkv + hk) * kHeadDim + part * 16;
@@ -356,16 +359,23 @@ __global__ void __launch_bounds__(kThreads, 1) extend_scored_kernel(const Scored
       flag_error(p.status, NVFP4KV_DEVERR_ROW);
     const int near = max(v.near, row_low), low = max(v.low, row_low);
     const int end = min(v.end, row_high), sink_end = min(v.sink_end, row_high);
-    auto load = [&](const uint8_t* ws, int i, uint4 (&x)[4][2]) {
-      const int j0 = v.tile(i) * kTileN + lw * 32 + (lane & 7);
+    auto load = [&](const uint8_t* ws, int i, uint4 (&x)[8]) {
+      const int jt = v.tile(i) * kTileN, j0 = jt + lw * 32 + (lane >> 3);
       const uint8_t* src = ws + (key0 + j0 * key_bytes);
+      if (jt >= near && jt + kTileN <= end) {  // the whole tile
 #pragma unroll
-      for (int g = 0; g < 4; ++g) {
-        const int j = j0 + 8 * g;
-        const bool live = j < end && (j >= near || (j >= low && j < sink_end));
+        for (int g = 0; g < 8; ++g) {
+          x[g] = __ldg(reinterpret_cast<const uint4*>(src));
+          src += 4 * key_bytes;
+        }
+      } else {
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
-          x[g][h] = live ? __ldg(reinterpret_cast<const uint4*>(src + 8 * g * key_bytes) + 4 * h) : make_uint4(0, 0, 0, 0);
+        for (int g = 0; g < 8; ++g) {
+          const int j = j0 + 4 * g;
+          const bool live = j < end && (j >= near || (j >= low && j < sink_end));
+          x[g] = live ? __ldg(reinterpret_cast<const uint4*>(src)) : make_uint4(0, 0, 0, 0);
+          src += 4 * key_bytes;
+        }
       }
     };
     load(p.ws_k, 0, xk);
@@ -382,18 +392,17 @@ __global__ void __launch_bounds__(kThreads, 1) extend_scored_kernel(const Scored
           break;
         }
         const uint32_t at = sRing + s * kSlotBytes;
+        // a lane's 16 values are chunks 2 part and 2 part + 1; the upper four lanes
+        // of a row store theirs the other way round, so that a row's eight lanes
+        // hit eight banks
+        const int first = part >> 2;
 #pragma unroll
-        for (int g = 0; g < 4; ++g) {
-          const int key = lw * 32 + g * 8 + (lane & 7);
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const uint4 x = w == 0 ? xk[g][h] : xv[g][h];
-            const int d = h * 64 + part * 16;
-            const uint32_t a0 = w == 0 ? kmajor_off(key, d) : v_off(d, key);
-            const uint32_t a1 = w == 0 ? kmajor_off(key, d + 8) : v_off(d + 8, key);
-            st_shared_v4(at + a0, e4m3x8_to_f16x8(x.x, x.y));
-            st_shared_v4(at + a1, e4m3x8_to_f16x8(x.z, x.w));
-          }
+        for (int g = 0; g < 8; ++g) {
+          const int key = lw * 32 + 4 * g + (lane >> 3);
+          const uint4 x = w == 0 ? xk[g] : xv[g];
+          const uint4 lo = e4m3x8_to_f16x8(x.x, x.y), hi = e4m3x8_to_f16x8(x.z, x.w);
+          st_shared_v4(at + kv_off(key, 2 * part + first), first ? hi : lo);
+          st_shared_v4(at + kv_off(key, 2 * part + 1 - first), first ? lo : hi);
         }
         tc::fence_smem_to_async();
         __syncwarp();
@@ -418,9 +427,8 @@ __global__ void __launch_bounds__(kThreads, 1) extend_scored_kernel(const Scored
     const bool live = t <= t1;
     const int pos = P + t;
     const int head = hk * G + (r & (G - 1));
-    const int64_t row = (q0 + (live ? t : 0)) * p.hq + head;
     {
-      const uint4* src = reinterpret_cast<const uint4*>(p.q + row * kHeadDim);
+      const uint4* src = reinterpret_cast<const uint4*>(p.q + ((q0 + (live ? t : 0)) * p.hq + head) * kHeadDim);
       const uint32_t dst = sQ + tile * kTileBytes;
 #pragma unroll
       for (int c = 0; c < kHeadDim / 8; ++c)
@@ -432,13 +440,11 @@ __global__ void __launch_bounds__(kThreads, 1) extend_scored_kernel(const Scored
     KeyRange kr = key_range(p, keys, pos, full, p.doc_starts != nullptr && live ? __ldg(p.doc_starts + q0 + t) : 0);
     if (!live) kr.end = 0;  // a row past the chunk sees nothing
     const float slope = (M & kBiased) != 0 ? __ldg(p.slopes + head) * kLog2e : 0.0f;
-    const float unit = p.unit;
     const uint32_t t_lane = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
     const uint32_t t_s = t_lane + tile * kTileN, t_o = t_lane + kTmemO + tile * kHeadDim;
     const uint32_t bar_s = b_s + 8 * tile, bar_p = b_p + 8 * tile;
     float m = -INFINITY;
     float2 l[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
-    const float u = (M & kBiased) != 0 ? 1.0f : unit;  // base-2 score per unit of what is exponentiated
     bool ok = true;
     for (int i = 0; i < v.steps; ++i) {
       if (!warp_wait(bar_s, i & 1)) {
@@ -451,39 +457,76 @@ __global__ void __launch_bounds__(kThreads, 1) extend_scored_kernel(const Scored
       const int end = kr.end - kbase, low = kr.low - kbase, sink = kr.sink_end - kbase, near = kr.near - kbase;
       const bool masked = end < kTileN || (near > 0 && (low > 0 || sink < kTileN));
       const bool any_masked = __any_sync(0xFFFFFFFFu, masked);
-      uint32_t w[kTileN];
-      tc::tmem_ld128(t_s, w);
-      float2(&x)[kTileN / 2] = *reinterpret_cast<float2(*)[kTileN / 2]>(&w[0]);
-      if constexpr ((M & kCapped) != 0) cap_scores(x, p.cap);
-      if constexpr ((M & kBiased) != 0) {
-        // base-2 scores from here on: x * unit - slope * |pos - j|
-        const float d0 = (float)(pos - kbase);
+      // All visible, and plain or capped within the polynomial's range: the row's
+      // maximum is that of the products (the cap keeps the order), and the cap is
+      // left to the second pass, where the FMA pipe works beside the
+      // special-function unit.
+      bool direct = false;
+      float top = -INFINITY;  // the row's maximum in base 2
+      if constexpr ((M & kBiased) == 0) {
+        if (!any_masked) {
+          uint32_t w[kTileN];
+          tc::tmem_ld128(t_s, w);
+          float hi[4], lo[4];
 #pragma unroll
-        for (int c = 0; c < kTileN / 2; ++c) {
-          x[c].x = fmaf(-slope, fabsf(d0 - (float)(2 * c)), x[c].x * unit);
-          x[c].y = fmaf(-slope, fabsf(d0 - (float)(2 * c + 1)), x[c].y * unit);
+          for (int c = 0; c < 4; ++c) hi[c] = lo[c] = __uint_as_float(w[c]);
+#pragma unroll
+          for (int c = 4; c < kTileN; c += 2) {
+            const float a = __uint_as_float(w[c]), b = __uint_as_float(w[c + 1]);
+            hi[c >> 1 & 3] = max3(hi[c >> 1 & 3], a, b);
+            if constexpr (M == kCapped) lo[c >> 1 & 3] = min3(lo[c >> 1 & 3], a, b);
+          }
+          const float h = fmaxf(max3(hi[0], hi[1], hi[2]), hi[3]);
+          if constexpr (M == kCapped) {
+            const float l0 = fminf(min3(lo[0], lo[1], lo[2]), lo[3]);
+            direct = __all_sync(0xFFFFFFFFu, h <= p.cap.limit && l0 >= -p.cap.limit);
+            top = cap_short(both(h), p.cap, both(0.0f)).x;
+          } else {
+            direct = true;
+            top = h * p.unit;  // (the unit is positive)
+          }
         }
       }
-      if (any_masked) {
+      if (!direct) {
+        // cap, bias and mask the scores where they lie, 32 at a time
+        float mr[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+        uint32_t y[2][32];
+        tc::tmem_ld32_async(t_s, y[0]);
 #pragma unroll
         for (int c4 = 0; c4 < kTileN / 32; ++c4) {
           const int at = 32 * c4;
-          const uint32_t hidden = ~first_bits(end - at) |
-                                  (first_bits(near - at) & ~(first_bits(sink - at) & ~first_bits(low - at)));
+          uint32_t(&w)[32] = y[c4 & 1];
+          tc::tmem_wait_ld(w);
+          if (c4 + 1 < kTileN / 32) tc::tmem_ld32_async(t_s + at + 32, y[(c4 + 1) & 1]);
+          float2(&x)[16] = *reinterpret_cast<float2(*)[16]>(&w[0]);
+          if constexpr ((M & kCapped) != 0) cap_scores(x, p.cap);
+          if constexpr ((M & kBiased) != 0) {
+            const float d0 = (float)(pos - kbase - at);
+            const float unit = (M & kCapped) != 0 ? 1.0f : p.unit;
 #pragma unroll
-          for (int c = 0; c < 32; ++c)
-            if (hidden >> c & 1) w[at + c] = 0xFF800000u;  // -inf
+            for (int c = 0; c < 16; ++c) {
+              x[c].x = fmaf(-slope, fabsf(d0 - (float)(2 * c)), x[c].x * unit);
+              x[c].y = fmaf(-slope, fabsf(d0 - (float)(2 * c + 1)), x[c].y * unit);
+            }
+          }
+          if (any_masked) {
+            const uint32_t hidden = ~first_bits(end - at) |
+                                    (first_bits(near - at) & ~(first_bits(sink - at) & ~first_bits(low - at)));
+#pragma unroll
+            for (int c = 0; c < 32; ++c)
+              if (hidden >> c & 1) w[c] = 0xFF800000u;  // -inf
+          }
+          tc::tmem_st32_async(t_s + at, w);
+#pragma unroll
+          for (int c = 0; c < 16; ++c) mr[c & 3] = max3(mr[c & 3], x[c].x, x[c].y);
         }
+        tc::tmem_wait_st();  // they are read again below
+        top = fmaxf(fmaxf(mr[0], mr[1]), fmaxf(mr[2], mr[3])) * (M == 0 ? p.unit : 1.0f);
       }
-      float mr[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-      for (int c = 0; c < kTileN / 2; ++c) mr[c & 3] = fmaxf(mr[c & 3], fmaxf(x[c].x, x[c].y));
-      // the row max in base-2 units (the unit is positive, so it commutes with max)
-      const float mx = fmaxf(fmaxf(mr[0], mr[1]), fmaxf(mr[2], mr[3])) * u;
-      const bool grow = mx > m + kLazy;  // false while nothing is visible (mx = -inf)
+      const bool grow = top > m + kLazy;  // false while nothing is visible (top = -inf)
       if (__any_sync(0xFFFFFFFFu, grow)) {
-        const float alpha = grow ? ex2(m - mx) : 1.0f;  // 0 on the first visible tile (m = -inf)
-        if (grow) m = mx;
+        const float alpha = grow ? ex2(m - top) : 1.0f;  // 0 on the first visible tile (m = -inf)
+        if (grow) m = top;
         l[0] = mul2(l[0], both(alpha));
         l[1] = mul2(l[1], both(alpha));
         if (i > 0) {
@@ -498,23 +541,39 @@ __global__ void __launch_bounds__(kThreads, 1) extend_scored_kernel(const Scored
           }
         }
       }
-      // p = 2^(x u - m); masked scores are -inf and give 0, and so does every
-      // score of a row that has seen nothing yet (m = -inf)
+      // p = 2^(x - m); masked scores are -inf and give 0, and so does every
+      // score of a row that has seen nothing yet (m = -inf).  The scores are read
+      // again, 32 at a time with the next 32 on their way: without a whole row in
+      // registers the compiler keeps 16 pairs in flight instead of two or three.
       const float off = m > -INFINITY ? -m : -INFINITY;
+      auto weights = [&](auto exponent) {
+        uint32_t y[2][32], ph[2][16];
+        tc::tmem_ld32_async(t_s, y[0]);
 #pragma unroll
-      for (int c4 = 0; c4 < kTileN / 32; ++c4) {
-        uint32_t ph[16];
+        for (int c4 = 0; c4 < kTileN / 32; ++c4) {
+          tc::tmem_wait_ld(y[c4 & 1]);
+          if (c4 + 1 < kTileN / 32) tc::tmem_ld32_async(t_s + 32 * (c4 + 1), y[(c4 + 1) & 1]);
 #pragma unroll
-        for (int c = 0; c < 16; ++c) {
-          float2 e = fma2(x[16 * c4 + c], both(u), both(off));
-          e.x = ex2(e.x);
-          e.y = ex2(e.y);
-          ph[c] = f16x2_bits(e.x, e.y);
-          l[c & 1] = add2(l[c & 1], e);
+          for (int c = 0; c < 16; ++c) {
+            float2 e = exponent(make_float2(__uint_as_float(y[c4 & 1][2 * c]), __uint_as_float(y[c4 & 1][2 * c + 1])));
+            e.x = ex2(e.x);
+            e.y = ex2(e.y);
+            ph[c4 & 1][c] = f16x2_bits(e.x, e.y);
+            l[c & 1] = add2(l[c & 1], e);
+          }
+          // P (two keys per column) over S columns already read: the A operand of
+          // P V.  Stored one round late, so that the next round's arithmetic can
+          // start under the end of this one's.
+          if (c4 > 0) tc::tmem_st16_async(t_s + 16 * (c4 - 1), ph[(c4 - 1) & 1]);
         }
-        // P (two keys per column) over the S columns: the A operand of P V
-        tc::tmem_st16_async(t_s + 16 * c4, ph);
-      }
+        tc::tmem_st16_async(t_s + kTileN / 2 - 16, ph[1]);
+      };
+      if constexpr (M == 0)
+        weights([&](float2 s) { return fma2(s, both(p.unit), both(off)); });
+      else if (M == kCapped && direct)
+        weights([&](float2 s) { return cap_short(s, p.cap, both(off)); });
+      else
+        weights([&](float2 s) { return add2(s, both(off)); });
       tc::tmem_wait_st();
       tc::fence_before_sync();
       __syncwarp();
@@ -524,6 +583,8 @@ __global__ void __launch_bounds__(kThreads, 1) extend_scored_kernel(const Scored
       tc::fence_after_sync();
       const float sum = (l[0].x + l[1].x) + (l[0].y + l[1].y);
       const float inv = sum > 0.0f ? p.out_scale / sum : 0.0f;
+      // (worked out again rather than kept over the loop)
+      const int64_t row = (__ldg(p.cu_q + b) + (live ? pos - P : 0)) * p.hq + hk * G + (r & (G - 1));
       uint4* dst = reinterpret_cast<uint4*>(p.out + row * kHeadDim);
       if (live && p.lse != nullptr) p.lse[row] = sum > 0.0f ? (m + log2f(sum)) * kLn2 : -INFINITY;
 #pragma unroll
@@ -587,9 +648,9 @@ cudaError_t launch_extend_scored(const uint16_t* q, const int64_t* cu_q, int32_t
   p.max_q_len = max_q_len;
   p.total_rows = total_rows;
   const double scale = (double)softmax_scale * (double)k_ws_scale;
-  p.unit = (float)((sc.softcap > 0.0f ? (double)sc.softcap : scale) * 1.4426950408889634);
+  p.unit = (float)(scale * 1.4426950408889634);
   p.out_scale = v_ws_scale;
-  if (sc.softcap > 0.0f) p.cap = cap_poly(scale / (double)sc.softcap);
+  if (sc.softcap > 0.0f) p.cap = cap_poly(scale / (double)sc.softcap, (double)sc.softcap * 1.4426950408889634);
   p.window = sc.window;
   p.sinks = sc.sinks;
   p.slopes = sc.slopes;

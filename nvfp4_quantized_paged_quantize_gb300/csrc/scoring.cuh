@@ -39,6 +39,17 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
       : "l"(*reinterpret_cast<uint64_t*>(&a)), "l"(*reinterpret_cast<uint64_t*>(&b)));
   return *reinterpret_cast<float2*>(&r);
 }
+// The largest and the smallest of three.
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+__device__ __forceinline__ float min3(float a, float b, float c) {
+  float r;
+  asm("min.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
 __device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
 
 // tanh on |x| <= 1: x + x^3 P(x^2), P of degree 5, fitted here to tanh in the
@@ -87,48 +98,61 @@ __device__ __forceinline__ void tanh_warp(float2 (&x)[N]) {
   }
 }
 
-// S -> tanh(c S) for many scores with one factor c.  While |c S| <= 0.6 (the
-// usual case: scores well inside their cap) the factor is part of the
+// a * tanh(c S) for many scores with the same factors.  While |c S| <= 0.6 (the
+// usual case: scores well inside their cap) both factors are part of a
 // polynomial's coefficients, S Q(S^2) with Q of degree 4, fitted here in the
-// relative maximum norm (7.3e-8 before rounding): six packed operations a pair
-// against ten with the separate product and the wider interval.
+// relative maximum norm (7.3e-8 before rounding): six packed operations a pair,
+// of which the last takes an addend with it.
 struct CapPoly {
-  float scale;  // c
-  float limit;  // the short form holds for |S| <= limit (-1: never)
-  float k[5];
+  float inner, outer;  // c, a
+  float limit;         // the short form holds for |S| <= limit (-1: never)
+  float2 k[5];         // each coefficient twice, as the packed operations take it
 };
 
-inline CapPoly cap_poly(double c) {
-  constexpr double a[5] = {0x1.fffffep-1, -0x1.5552a6p-2, 0x1.1097a4p-3, -0x1.aad0b8p-5, 0x1.fb1946p-7};
+inline CapPoly cap_poly(double c, double a) {
+  constexpr double fit[5] = {0x1.fffffep-1, -0x1.5552a6p-2, 0x1.1097a4p-3, -0x1.aad0b8p-5, 0x1.fb1946p-7};
   CapPoly p;
-  p.scale = (float)c;
-  // the coefficients' range: c^9 a_4 stays a normal number
-  p.limit = c >= 0x1p-12 && c <= 0x1p+12 ? (float)(0.6 / c) : -1.0f;
-  double f = c;
-  for (int i = 0; i < 5; ++i, f *= c * c) p.k[i] = p.limit > 0.0f ? (float)(a[i] * f) : 0.0f;
+  p.inner = (float)c;
+  p.outer = (float)a;
+  // the coefficients' range: a c^9 fit[4] stays a normal number
+  p.limit = c >= 0x1p-10 && c <= 0x1p+10 ? (float)(0.6 / c) : -1.0f;
+  double f = c * a;
+  for (int i = 0; i < 5; ++i, f *= c * c) {
+    const float k = p.limit > 0.0f ? (float)(fit[i] * f) : 0.0f;
+    p.k[i] = make_float2(k, k);
+  }
   return p;
 }
 
+// a * tanh(c S) + add, |S| <= limit.
+__device__ __forceinline__ float2 cap_short(float2 S, const CapPoly& p, float2 add) {
+  const float2 w = mul2(S, S);
+  float2 q = fma2(p.k[4], w, p.k[3]);
+  q = fma2(q, w, p.k[2]);
+  q = fma2(q, w, p.k[1]);
+  q = fma2(q, w, p.k[0]);
+  return fma2(S, q, add);
+}
+
+// S -> a * tanh(c S) for any S.
 template <int N>
 __device__ __forceinline__ void cap_scores(float2 (&x)[N], const CapPoly& p) {
-  float top[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+  float hi = x[0].x, lo = x[0].x;
 #pragma unroll
-  for (int i = 0; i < N; ++i) top[i & 3] = fmaxf(top[i & 3], fmaxf(fabsf(x[i].x), fabsf(x[i].y)));
-  if (__all_sync(0xFFFFFFFFu, fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) <= p.limit)) {
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const float2 w = mul2(x[i], x[i]);
-      float2 q = fma2(both(p.k[4]), w, both(p.k[3]));
-      q = fma2(q, w, both(p.k[2]));
-      q = fma2(q, w, both(p.k[1]));
-      q = fma2(q, w, both(p.k[0]));
-      x[i] = mul2(x[i], q);
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < N; ++i) x[i] = mul2(x[i], both(p.scale));
-    tanh_warp(x);
+  for (int i = 0; i < N; ++i) {
+    hi = max3(hi, x[i].x, x[i].y);
+    lo = min3(lo, x[i].x, x[i].y);
   }
+  if (__all_sync(0xFFFFFFFFu, hi <= p.limit && lo >= -p.limit)) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) x[i] = cap_short(x[i], p, both(0.0f));
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < N; ++i) x[i] = mul2(x[i], both(p.inner));
+  tanh_warp(x);
+#pragma unroll
+  for (int i = 0; i < N; ++i) x[i] = mul2(x[i], both(p.outer));
 }
 
 }  // namespace nvfp4kv
