@@ -6,8 +6,9 @@
 //   reads its share of the middle tokens' sums once into shared memory, as
 //   integers that order like the floats.  A radix selection finds the smallest
 //   kept key: three passes over shared memory (11, 11 and 10 bits), each a
-//   histogram whose bins are summed over the cluster through distributed
-//   shared memory.  Equal keys go to the lower index: with g tokens above and
+//   histogram of its own tokens whose bins that are not empty every CTA adds to
+//   the first CTA's totals (distributed shared memory; few bins hold anything),
+//   which finds the threshold's bin and tells the others.  Equal keys go to the lower index: with g tokens above and
 //   e tokens equal to the threshold before it, a kept token lands at place
 //   g + min(e, equal ones still wanted), so one ordered count over the cluster
 //   gives every destination and the list comes out in token order.
@@ -29,7 +30,9 @@ constexpr int kSelectThreads = 512;
 constexpr int kSelectWarps = kSelectThreads / 32;
 constexpr int kBins = 2048;           // 11 bits
 constexpr int kPasses = 3;            // of 11, 11 and 10 bits
+constexpr int kSpan = 128;            // tokens a warp takes at a time, four per lane
 constexpr int kKeyCap = 20 * 1024;    // keys a CTA holds: with the histograms two CTAs fit an SM
+static_assert(kKeyCap % (kSpan * kSelectWarps) == 0, "the keys are padded to whole spans of every warp");
 constexpr int kMaxCluster = 8;        // the portable limit
 constexpr int kPackWarps = 8;
 
@@ -74,7 +77,9 @@ __device__ __forceinline__ uint32_t order_key(float x) {
   return (u & 0x80000000u) ? ~u : u | 0x80000000u;
 }
 
-// The word at this address of the same shared-memory variable in another CTA of the cluster.
+constexpr uint32_t kKeyNone = 0;  // no float's key: below that of -inf
+
+// The words at this address of the same shared-memory variable in another CTA of the cluster.
 __device__ __forceinline__ uint32_t ld_cluster(const uint32_t* local, uint32_t rank) {
   uint32_t at, v;
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_u32(local)), "r"(rank));
@@ -82,14 +87,30 @@ __device__ __forceinline__ uint32_t ld_cluster(const uint32_t* local, uint32_t r
   return v;
 }
 
+// Store to, add to, the same shared-memory word in another CTA of the cluster.
+__device__ __forceinline__ void st_cluster(uint32_t* local, uint32_t rank, uint32_t n) {
+  uint32_t at;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_u32(local)), "r"(rank));
+  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(at), "r"(n) : "memory");
+}
+__device__ __forceinline__ void add_cluster(uint32_t* local, uint32_t rank, uint32_t n) {
+  uint32_t at;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_u32(local)), "r"(rank));
+  asm volatile("red.shared::cluster.add.u32 [%0], %1;" ::"r"(at), "r"(n) : "memory");
+}
+
 struct SelectShared {
-  uint32_t hist[kPasses][kBins];
+  alignas(16) uint32_t total[kPasses][kBins];  // over the cluster
+  alignas(16) uint32_t own[kBins];             // this CTA's, where the cluster has others
   uint32_t warp_sum[kSelectWarps];
-  uint32_t found_bin, found_above;       // the threshold's bin, and how many keys lie in bins above it
-  uint32_t warp_gt[kSelectWarps], warp_eq[kSelectWarps];
+  uint32_t found_bin[kPasses], found_above[kPasses];  // the threshold's bin, and how many keys lie in bins above it
+  uint32_t warp_count[kSelectWarps][2];  // tokens above / equal to the threshold
   uint32_t cta_gt, cta_eq;
 };
 
+// kFits: every CTA's share of the tokens fits its shared memory (else what does
+// not is read again in each pass).
+template <bool kFits>
 __global__ void __launch_bounds__(kSelectThreads, 2) select_kernel(const EvictParams p, int cluster) {
   extern __shared__ __align__(16) uint32_t keys[];  // kKeyCap
   __shared__ SelectShared s;
@@ -102,36 +123,83 @@ __global__ void __launch_bounds__(kSelectThreads, 2) select_kernel(const EvictPa
   const float* w = p.weights + (long long)pair * p.weight_stride;
   int32_t* kept = p.kept + (long long)pair * p.budget;
   float* kw = p.kept_weights ? p.kept_weights + (long long)pair * p.kept_stride : nullptr;
-  auto keep = [&](int place, int token) {
-    kept[place] = token;
-    if (kw) kw[place] = __ldg(w + token);
-  };
   const int part = rank * kSelectThreads + tid, parts = cluster * kSelectThreads;
   for (int i = n + part; i < p.budget; i += parts) {
     kept[i] = -1;
     if (kw) kw[i] = 0.0f;
   }
   if (L <= p.budget) {
-    for (int i = part; i < L; i += parts) keep(i, i);
+    for (int i = part; i < L; i += parts) {
+      kept[i] = i;
+      if (kw) kw[i] = __ldg(w + i);
+    }
     return;
   }
-  for (int i = part; i < p.first; i += parts) keep(i, i);
-  for (int i = part; i < p.recent; i += parts) keep(n - p.recent + i, L - p.recent + i);
   const int middle = L - p.first - p.recent, want = n - p.first - p.recent;  // 0 <= want < middle
-  if (want == 0) return;
+  // the tokens that stay in any case
+  auto keep_ends = [&]() {
+    for (int i = part; i < p.first + p.recent; i += parts) {
+      const int place = i < p.first ? i : n - p.first - p.recent + i;
+      const int token = i < p.first ? i : L - p.first - p.recent + i;
+      kept[place] = token;
+      if (kw) kw[place] = __ldg(w + token);
+    }
+  };
+  if (want == 0) {
+    keep_ends();
+    return;
+  }
 
   // this CTA's share of the middle tokens, as keys
   const int t0 = p.first + (int)((long long)middle * rank / cluster);
   const int count = p.first + (int)((long long)middle * (rank + 1) / cluster) - t0;
   const float* mine = w + t0;
-  for (int i = tid; i < kPasses * kBins; i += kSelectThreads) (&s.hist[0][0])[i] = 0;
+  constexpr int kBatch = 16;  // loads in flight per thread
+  float x[kBatch];
+  auto fetch = [&](int b0) {
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j) {
+      const int i = b0 + j * kSelectThreads;
+      x[j] = i < count ? __ldg(mine + i) : 0.0f;
+    }
+  };
+  fetch(tid);
+  constexpr int kPer = kBins / kSelectThreads;
+  static_assert(kPer == 4, "a thread's bins are one 16-byte word");
+#pragma unroll
+  for (int pass = 0; pass < kPasses; ++pass)
+    *reinterpret_cast<uint4*>(&s.total[pass][kPer * tid]) = make_uint4(0u, 0u, 0u, 0u);
+  *reinterpret_cast<uint4*>(&s.own[kPer * tid]) = make_uint4(0u, 0u, 0u, 0u);
+  // spans of the CTA's tokens; a warp's are contiguous: [i0, i1)
+  const int spans = (count + kSpan - 1) / kSpan, warp_spans = (spans + kSelectWarps - 1) / kSelectWarps;
+  const int i0 = warp * warp_spans * kSpan, i1 = i0 + warp_spans * kSpan;
+  // the keys of the CTA's tokens i .. i + 3 (i a multiple of 4)
+  auto keys_at = [&](int i) {
+    if (kFits || i < kKeyCap) return *reinterpret_cast<const uint4*>(keys + i);
+    uint4 k;
+    k.x = i < count ? order_key(__ldg(mine + i)) : kKeyNone;
+    k.y = i + 1 < count ? order_key(__ldg(mine + i + 1)) : kKeyNone;
+    k.z = i + 2 < count ? order_key(__ldg(mine + i + 2)) : kKeyNone;
+    k.w = i + 3 < count ? order_key(__ldg(mine + i + 3)) : kKeyNone;
+    return k;
+  };
+  const int padded = min(warp_spans * kSelectWarps * kSpan, kKeyCap);
+  for (int i = count + tid; i < padded; i += kSelectThreads) keys[i] = kKeyNone;
+  keep_ends();
+  // every CTA's totals are zero before any CTA adds to them
   __syncthreads();
-  // the key of the CTA's token i (those past the shared memory's room are read again in each pass)
-  auto key_at = [&](int i) { return i < kKeyCap ? keys[i] : order_key(__ldg(mine + i)); };
-  for (int i = tid; i < count; i += kSelectThreads) {
-    const uint32_t k = order_key(__ldg(mine + i));
-    if (i < kKeyCap) keys[i] = k;
-    atomicAdd(&s.hist[0][k >> 21], 1u);
+  if (cluster > 1) cluster_sync();
+  for (int b0 = tid; b0 < count; b0 += kBatch * kSelectThreads) {
+    if (b0 != tid) fetch(b0);
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j) {
+      const int i = b0 + j * kSelectThreads;
+      if (i < count) {
+        const uint32_t k = order_key(x[j]);
+        if (kFits || i < kKeyCap) keys[i] = k;
+        atomicAdd(&(cluster > 1 ? s.own : s.total[0])[k >> 21], 1u);
+      }
+    }
   }
 
   uint32_t prefix = 0, left = (uint32_t)want;  // the threshold's bits so far; keys still to be found among those that share them
@@ -139,74 +207,86 @@ __global__ void __launch_bounds__(kSelectThreads, 2) select_kernel(const EvictPa
   for (int pass = 0; pass < kPasses; ++pass) {
     constexpr int kShift[kPasses] = {21, 10, 0};
     const int shift = kShift[pass], bits = pass == kPasses - 1 ? 10 : 11;
+    uint32_t* const hist = cluster > 1 ? s.own : s.total[pass];
     if (pass > 0) {
       const int above = kShift[pass > 0 ? pass - 1 : 0];
-      for (int i = tid; i < count; i += kSelectThreads) {
-        const uint32_t k = key_at(i);
-        if ((k >> above) == prefix) atomicAdd(&s.hist[pass][(k >> shift) & ((1u << bits) - 1)], 1u);
+      for (int i = i0 + 4 * lane; i < i1; i += kSpan) {
+        const uint4 k4 = keys_at(i);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const uint32_t k = j == 0 ? k4.x : j == 1 ? k4.y : j == 2 ? k4.z : k4.w;
+          if ((k >> above) == prefix) atomicAdd(&hist[(k >> shift) & ((1u << bits) - 1)], 1u);
+        }
+      }
+    }
+    __syncthreads();
+    if (cluster > 1) {
+      uint4* const at = reinterpret_cast<uint4*>(&s.own[kPer * tid]);
+      const uint4 mine4 = *at;
+      *at = make_uint4(0u, 0u, 0u, 0u);
+      const uint32_t n[kPer] = {mine4.x, mine4.y, mine4.z, mine4.w};
+#pragma unroll
+      for (int j = 0; j < kPer; ++j)
+        if (n[j] != 0)
+          add_cluster(&s.total[pass][kPer * tid + j], 0, n[j]);
+      __syncwarp();
+      cluster_sync();
+    }
+    if (rank == 0) {
+      // this thread's four bins, from the top down
+      const uint4 c = *reinterpret_cast<const uint4*>(&s.total[pass][kBins - kPer * (tid + 1)]);
+      const uint32_t bin[kPer] = {c.w, c.z, c.y, c.x};
+      const uint32_t sum = (c.x + c.y) + (c.z + c.w);
+      uint32_t incl = sum;
+#pragma unroll
+      for (int off = 1; off < 32; off <<= 1) {
+        const uint32_t v = __shfl_up_sync(0xFFFFFFFFu, incl, off);
+        if (lane >= off) incl += v;
+      }
+      if (lane == 31) s.warp_sum[warp] = incl;
+      __syncthreads();
+      uint32_t before = incl - sum;
+      for (int k = 0; k < warp; ++k) before += s.warp_sum[k];
+#pragma unroll
+      for (int j = 0; j < kPer; ++j) {
+        if (before < left && before + bin[j] >= left) {  // exactly one bin of the whole histogram
+          const uint32_t found = kBins - 1 - (tid * kPer + j);
+          s.found_bin[pass] = found;
+          s.found_above[pass] = before;
+          for (int r = 1; r < cluster; ++r) {
+            st_cluster(&s.found_bin[pass], r, found);
+            st_cluster(&s.found_above[pass], r, before);
+          }
+        }
+        before += bin[j];
       }
     }
     __syncthreads();
     if (cluster > 1) cluster_sync();
-    // this thread's four bins, from the top down, over the cluster
-    constexpr int kPer = kBins / kSelectThreads;
-    uint32_t bin[kPer], sum = 0;
-#pragma unroll
-    for (int j = 0; j < kPer; ++j) {
-      const uint32_t* at = &s.hist[pass][kBins - 1 - (tid * kPer + j)];
-      uint32_t c = 0;
-      if (cluster > 1) {
-        for (int r = 0; r < cluster; ++r) c += ld_cluster(at, r);
-      } else {
-        c = *at;
-      }
-      bin[j] = c;
-      sum += c;
-    }
-    uint32_t incl = sum;
-#pragma unroll
-    for (int off = 1; off < 32; off <<= 1) {
-      const uint32_t v = __shfl_up_sync(0xFFFFFFFFu, incl, off);
-      if (lane >= off) incl += v;
-    }
-    if (lane == 31) s.warp_sum[warp] = incl;
-    __syncthreads();
-    uint32_t before = incl - sum;
-    for (int k = 0; k < warp; ++k) before += s.warp_sum[k];
-#pragma unroll
-    for (int j = 0; j < kPer; ++j) {
-      if (before < left && before + bin[j] >= left) {  // exactly one bin of the whole histogram
-        s.found_bin = kBins - 1 - (tid * kPer + j);
-        s.found_above = before;
-      }
-      before += bin[j];
-    }
-    __syncthreads();
-    prefix = (prefix << bits) | s.found_bin;
-    left -= s.found_above;
-    __syncthreads();
+    prefix = (prefix << bits) | s.found_bin[pass];
+    left -= s.found_above[pass];
   }
   // prefix is the smallest kept key; `left` of the tokens equal to it stay
 
   // ordered counts: a warp's contiguous tokens, then the warps, then the CTAs
-  const int span = ((count + kSelectWarps - 1) / kSelectWarps + 31) & ~31;
-  const int i0 = min(warp * span, count), i1 = min(i0 + span, count);
+  auto count4 = [&](const uint4& k, uint32_t& gt, uint32_t& eq) {
+    gt += (uint32_t)(k.x > prefix) + (uint32_t)(k.y > prefix) + (uint32_t)(k.z > prefix) + (uint32_t)(k.w > prefix);
+    eq += (uint32_t)(k.x == prefix) + (uint32_t)(k.y == prefix) + (uint32_t)(k.z == prefix) + (uint32_t)(k.w == prefix);
+  };
   uint32_t gt = 0, eq = 0;
-  for (int i = i0; i < i1; i += 32) {
-    const uint32_t k = i + lane < i1 ? key_at(i + lane) : 0;
-    gt += __popc(__ballot_sync(0xFFFFFFFFu, i + lane < i1 && k > prefix));
-    eq += __popc(__ballot_sync(0xFFFFFFFFu, i + lane < i1 && k == prefix));
-  }
+  for (int i = i0 + 4 * lane; i < i1; i += kSpan) count4(keys_at(i), gt, eq);
+  gt = __reduce_add_sync(0xFFFFFFFFu, gt);
+  eq = __reduce_add_sync(0xFFFFFFFFu, eq);
   if (lane == 0) {
-    s.warp_gt[warp] = gt;
-    s.warp_eq[warp] = eq;
+    s.warp_count[warp][0] = gt;
+    s.warp_count[warp][1] = eq;
   }
   __syncthreads();
-  uint32_t g0 = 0, e0 = 0, gall = 0, eall = 0;
+  uint32_t g0 = 0, e0 = 0, gall = 0, eall = 0, gcta = 0, ecta = 0;  // before: the warp (in its CTA), all of the CTA, the CTA
   for (int k = 0; k < kSelectWarps; ++k) {
     if (k == warp) g0 = gall, e0 = eall;
-    gall += s.warp_gt[k];
-    eall += s.warp_eq[k];
+    gall += s.warp_count[k][0];
+    eall += s.warp_count[k][1];
   }
   if (cluster > 1) {
     if (tid == 0) {
@@ -216,20 +296,45 @@ __global__ void __launch_bounds__(kSelectThreads, 2) select_kernel(const EvictPa
     __syncwarp();
     cluster_sync();
     for (int r = 0; r < rank; ++r) {
-      g0 += ld_cluster(&s.cta_gt, r);
-      e0 += ld_cluster(&s.cta_eq, r);
+      gcta += ld_cluster(&s.cta_gt, r);
+      ecta += ld_cluster(&s.cta_eq, r);
     }
+    g0 += gcta;
+    e0 += ecta;
   }
   const uint32_t below = (1u << lane) - 1;
-  for (int i = i0; i < i1; i += 32) {
-    const bool in = i + lane < i1;
-    const uint32_t k = in ? key_at(i + lane) : 0;
-    const uint32_t bg = __ballot_sync(0xFFFFFFFFu, in && k > prefix);
-    const uint32_t be = __ballot_sync(0xFFFFFFFFu, in && k == prefix);
-    const uint32_t e = e0 + __popc(be & below), g = g0 + __popc(bg & below);
-    if (in && (k > prefix || (k == prefix && e < left))) keep(p.first + (int)(g + min(e, left)), t0 + i + lane);
-    g0 += __popc(bg);
-    e0 += __popc(be);
+  for (int i = i0 + 4 * lane; i < i1; i += kSpan) {
+    const uint4 k4 = keys_at(i);
+    const uint32_t k[4] = {k4.x, k4.y, k4.z, k4.w};
+    uint32_t bg[4], be[4];  // token j of each lane: above, equal
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      bg[j] = __ballot_sync(0xFFFFFFFFu, k[j] > prefix);
+      be[j] = __ballot_sync(0xFFFFFFFFu, k[j] == prefix);
+    }
+    // what lies before the lane's first token: tokens run over j, then over lanes
+    uint32_t g = g0 + __popc(bg[0] & below) + __popc(bg[1] & below) + __popc(bg[2] & below) + __popc(bg[3] & below);
+    uint32_t e = e0;
+    const bool ties = (be[0] | be[1] | be[2] | be[3]) != 0;
+    if (ties) e += __popc(be[0] & below) + __popc(be[1] & below) + __popc(be[2] & below) + __popc(be[3] & below);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const bool up = k[j] > prefix, tie = ties && k[j] == prefix;
+      if (up || (tie && e < left)) {
+        kept[p.first + (int)(g + min(e, left))] = t0 + i + j;
+      }
+      g += up;
+      e += tie;
+    }
+    g0 += __popc(bg[0]) + __popc(bg[1]) + __popc(bg[2]) + __popc(bg[3]);
+    if (ties) e0 += __popc(be[0]) + __popc(be[1]) + __popc(be[2]) + __popc(be[3]);
+  }
+  if (kw) {
+    // the sums of what this CTA kept: [first_place, last_place) of the list
+    __syncthreads();
+    const int first_place = p.first + (int)(gcta + min(ecta, left));
+    const int last_place = p.first + (int)(gcta + gall + min(ecta + eall, left));
+    for (int i = first_place + tid; i < last_place; i += kSelectThreads) kw[i] = __ldg(w + kept[i]);
   }
   __syncwarp();
   if (cluster > 1) cluster_sync();  // no CTA leaves while another may still read its counts
@@ -352,7 +457,10 @@ cudaError_t launch_evict(const nvfp4kv_cache& c, const int32_t* page_table, int3
   p.status = device_status;
   static PerDeviceOnce attr_once;
   cudaError_t e = attr_once.run([] {
-    return cudaFuncSetAttribute(select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kKeyCap * 4);
+    const cudaError_t a =
+        cudaFuncSetAttribute(select_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kKeyCap * 4);
+    if (a != cudaSuccess) return a;
+    return cudaFuncSetAttribute(select_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, kKeyCap * 4);
   });
   if (e != cudaSuccess) return e;
   // as many CTAs per pair as its keys need to fit shared memory, and more while
@@ -373,7 +481,8 @@ cudaError_t launch_evict(const nvfp4kv_cache& c, const int32_t* page_table, int3
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, select_kernel, p, cluster);
+  e = cudaLaunchKernelEx(&cfg, most <= (int64_t)cluster * kKeyCap ? select_kernel<true> : select_kernel<false>, p,
+                         cluster);
   if (e != cudaSuccess) return e;
   cfg.gridDim = dim3((unsigned)((p.page_heads + kPackWarps - 1) / kPackWarps));
   cfg.blockDim = dim3(kPackWarps * 32);
