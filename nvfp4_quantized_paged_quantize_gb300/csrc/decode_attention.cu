@@ -1504,21 +1504,27 @@ __global__ void __launch_bounds__(kCombineMaxWarps * 32) combine_kernel(const De
 // Accumulated attention weights: w[b][h][t] <- decay * w + sum over the KV
 // head's query heads of 2^(score - lse), from the scores the decode kept and
 // the pairs' log-sum-exps (base 2).  Memory-bound: per page-head 512 bytes of
-// scores (G = 8; written just before, so in part still in L2) and 64 bytes of
-// sums in and out.  A warp takes a contiguous range of the decode's page-heads,
-// as the scores lie, four at a time so that their loads overlap; lane = (token,
-// half of the heads).  Launched behind the combine as its programmatic
-// dependent.
+// scores (G = 8) and 64 bytes of sums in and out.  A warp takes a contiguous
+// range of the decode's page-heads, as the scores lie, in runs of one pair's
+// consecutive pages; lane = (token, half of the heads), several pages' loads in
+// flight.  Launched behind the combine as its programmatic dependent.
 constexpr int kWeightWarps = 8;      // per block
 constexpr int kWeightBlocksPerSm = 6;
 constexpr int kWeightUnroll = 4;
 
-// The pair a walk over page-heads stands in.
-struct PairCursor {
-  int b, h, local;   // sequence, KV head, index among the pair's visited pages
-  int L;
-  VisiblePages v;
-};
+// kHalf query heads' scores of one token.
+template <int kHalf>
+__device__ __forceinline__ void load_scores(const float* src, float (&x)[kHalf]) {
+  if constexpr (kHalf == 4) {
+    const float4 v = __ldcs(reinterpret_cast<const float4*>(src));
+    x[0] = v.x, x[1] = v.y, x[2] = v.z, x[3] = v.w;
+  } else if constexpr (kHalf == 2) {
+    const float2 v = __ldcs(reinterpret_cast<const float2*>(src));
+    x[0] = v.x, x[1] = v.y;
+  } else {
+    x[0] = __ldcs(src);
+  }
+}
 
 template <int kHalf>  // query heads per lane
 __global__ void __launch_bounds__(kWeightWarps * 32) weights_kernel(const DecodeParams p) {
@@ -1531,96 +1537,80 @@ __global__ void __launch_bounds__(kWeightWarps * 32) weights_kernel(const Decode
     return;
   }
   const long long nwarps = (long long)gridDim.x * kWeightWarps, w = (long long)blockIdx.x * kWeightWarps + warp;
-  const long long r0 = W * w / nwarps, r1 = W * (w + 1) / nwarps;
-  if (r0 >= r1) return;
-  // the sequence of page-head r0: the last one whose first page-head is <= r0
-  // (a 32-way search of the page prefix)
-  PairCursor c;
-  {
-    int lo = 0, hi = p.batch;  // the answer lies in [lo, hi)
-    while (hi - lo > 1) {
-      const int step = (hi - lo + 31) / 32, at = lo + lane * step;
-      const bool before = at < hi && (long long)__ldcg(p.cu_pages + at) * p.hkv <= r0;
-      const int k = __popc(__ballot_sync(0xFFFFFFFFu, before)) - 1;  // lane 0's always is
-      lo += k * step;
-      hi = min(hi, lo + step);
-    }
-    c.b = lo;
-    c.L = clamped_len(p, lo);
-    c.v = visible_pages<kScored>(p, c.L);
-    const int in = (int)(r0 - (long long)__ldcg(p.cu_pages + lo) * p.hkv);
-    c.h = in / c.v.count;
-    c.local = in - c.h * c.v.count;
+  const long long r1 = W * (w + 1) / nwarps;
+  long long r = W * w / nwarps;
+  if (r >= r1) return;
+  // the sequence of page-head r: the last one whose first page-head is <= r (a
+  // 32-way search of the page prefix)
+  int b = 0;
+  for (int hi = p.batch; hi - b > 1;) {
+    const int step = (hi - b + 31) / 32, at = b + lane * step;
+    const bool before = at < hi && (long long)__ldcg(p.cu_pages + at) * p.hkv <= r;
+    b += (__popc(__ballot_sync(0xFFFFFFFFu, before)) - 1) * step;  // lane 0's always is
+    hi = min(hi, b + step);
   }
-  float lse[kHalf];  // of the lane's heads; +inf where nothing was visible or there is no such head
-  auto fetch_lse = [&]() {
+  int L = clamped_len(p, b);
+  VisiblePages v = visible_pages<kScored>(p, L);
+  const int in = (int)(r - (long long)__ldcg(p.cu_pages + b) * p.hkv);
+  int h = in / v.count, local = in - h * v.count;  // KV head, index among the pair's visited pages
+  while (true) {
+    // one run: pages [local, local + run) of the pair, consecutive in the sequence
+    const long long pair = (long long)b * p.hkv + h;
+    const int stop = (int)min((long long)(local < v.lead ? v.lead : v.count), local + (r1 - r));
+    float lse[kHalf];  // +inf where nothing was visible or there is no such head
 #pragma unroll
     for (int k = 0; k < kHalf; ++k) {
       const int head = half * kHalf + k;
-      float v = -INFINITY;
-      if (head < p.group) v = __ldcg(p.lse2 + ((long long)c.b * p.hkv + c.h) * p.group + head);
-      lse[k] = v == -INFINITY ? INFINITY : v;
+      const float x = head < p.group ? __ldcg(p.lse2 + pair * p.group + head) : -INFINITY;
+      lse[k] = x == -INFINITY ? INFINITY : x;
     }
-  };
-  fetch_lse();
-  const float* src = p.scores + (token * 2 + half) * kHalf;
-  for (long long r = r0; r < r1; r += kWeightUnroll) {
-    float x[kWeightUnroll][kHalf], ls[kWeightUnroll][kHalf], old[kWeightUnroll];
-    float* dst[kWeightUnroll];
+    float* const sums = p.weights + pair * p.weight_stride;
+    const int page = local < v.lead ? local : local + v.skip;  // the run's first page in the sequence
+    const int limit = (int)min((long long)L, p.weight_stride);
+    if (limit < L && (page + stop - local) * kPage > limit) flag_error(p.status, NVFP4KV_DEVERR_LENGTH);
+    const float* src = p.scores + (r * (2 * kPage) + lane) * kHalf;
+    int t = page * kPage + token;  // the lane's token
+    for (int k = local; k < stop; k += kWeightUnroll) {
+      float x[kWeightUnroll][kHalf], old[kWeightUnroll];
 #pragma unroll
-    for (int k = 0; k < kWeightUnroll; ++k) {
-      dst[k] = nullptr;
-      old[k] = 0.0f;
+      for (int j = 0; j < kWeightUnroll; ++j) {
+        old[j] = 0.0f;
+        if (k + j < stop) {
+          load_scores<kHalf>(src + j * (2 * kPage * kHalf), x[j]);
+          if (half == 0 && t + j * kPage < limit && p.decay != 0.0f) old[j] = sums[t + j * kPage];
+        } else {
 #pragma unroll
-      for (int i = 0; i < kHalf; ++i) x[k][i] = ls[k][i] = 0.0f;
-      if (r + k >= r1) continue;
-      const float* row = src + (r + k) * (long long)(2 * kPage * kHalf);
-      if constexpr (kHalf == 4) {
-        const float4 v = __ldcs(reinterpret_cast<const float4*>(row));
-        x[k][0] = v.x, x[k][1] = v.y, x[k][2] = v.z, x[k][3] = v.w;
-      } else if constexpr (kHalf == 2) {
-        const float2 v = __ldcs(reinterpret_cast<const float2*>(row));
-        x[k][0] = v.x, x[k][1] = v.y;
-      } else {
-        x[k][0] = __ldcs(row);
-      }
-      if (c.local == c.v.count) {  // the next pair
-        c.local = 0;
-        if (++c.h == p.hkv) {
-          c.h = 0;
-          do {
-            ++c.b;
-            c.L = clamped_len(p, c.b);
-          } while (c.L == 0);
-          c.v = visible_pages<kScored>(p, c.L);
+          for (int i = 0; i < kHalf; ++i) x[j][i] = -INFINITY;
         }
-        fetch_lse();
       }
 #pragma unroll
-      for (int i = 0; i < kHalf; ++i) ls[k][i] = lse[i];
-      float* base = p.weights + ((long long)c.b * p.hkv + c.h) * p.weight_stride;
-      const int t = (c.local < c.v.lead ? c.local : c.local + c.v.skip) * kPage + token;
-      if (t >= p.weight_stride && t < c.L) flag_error(p.status, NVFP4KV_DEVERR_LENGTH);
-      if (half == 0 && t < c.L && t < p.weight_stride) {
-        dst[k] = base + t;
-        if (p.decay != 0.0f) old[k] = *dst[k];
+      for (int j = 0; j < kWeightUnroll; ++j) {
+        float sum = 0.0f;
+#pragma unroll
+        for (int i = 0; i < kHalf; ++i) sum += ex2(x[j][i] - lse[i]);
+        sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 1);
+        if (half == 0 && k + j < stop && t + j * kPage < limit) sums[t + j * kPage] = fmaf(p.decay, old[j], sum);
       }
-      if (c.v.skip > 0 && p.decay != 1.0f) {
-        // the pages out of sight decay as well: an equal share of them for each page seen
-        const long long f0 = (c.v.lead + (long long)c.v.skip * c.local / c.v.count) * kPage;
-        const long long f1 =
-            min((c.v.lead + (long long)c.v.skip * (c.local + 1) / c.v.count) * kPage, p.weight_stride);
-        for (long long f = f0 + lane; f < f1; f += 32) base[f] = p.decay == 0.0f ? 0.0f : p.decay * base[f];
-      }
-      ++c.local;
+      src += kWeightUnroll * 2 * kPage * kHalf;
+      t += kWeightUnroll * kPage;
     }
-#pragma unroll
-    for (int k = 0; k < kWeightUnroll; ++k) {
-      float sum = 0.0f;
-#pragma unroll
-      for (int i = 0; i < kHalf; ++i) sum += ex2(x[k][i] - ls[k][i]);
-      sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 1);
-      if (dst[k] != nullptr) *dst[k] = fmaf(p.decay, old[k], sum);
+    if (v.skip > 0 && p.decay != 1.0f) {
+      // the pages out of sight decay as well: to each page seen an equal share of them
+      const long long f0 = (v.lead + (long long)v.skip * local / v.count) * kPage;
+      const long long f1 = min((v.lead + (long long)v.skip * stop / v.count) * kPage, (long long)limit);
+      for (long long f = f0 + lane; f < f1; f += 32) sums[f] = p.decay == 0.0f ? 0.0f : p.decay * sums[f];
+    }
+    r += stop - local;
+    if (r >= r1) return;
+    local = stop;
+    if (local == v.count) {  // the next pair
+      local = 0;
+      if (++h == p.hkv) {
+        h = 0;
+        do L = clamped_len(p, ++b);
+        while (L == 0);
+        v = visible_pages<kScored>(p, L);
+      }
     }
   }
 }
