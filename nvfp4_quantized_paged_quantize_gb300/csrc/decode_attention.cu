@@ -346,6 +346,7 @@ struct LaneCopy {
   const uint8_t* src;  // pages + 16 * lane
   uint32_t off;        // 16 * lane
   bool fifth;          // a fifth piece at 16 * (lane + 128)
+  uint64_t policy;     // kStored: the L2 policy of the copies (first to go)
 };
 
 template <int F>
@@ -354,6 +355,7 @@ __device__ __forceinline__ LaneCopy lane_copy(const DecodeParams& p, int lane) {
   c.src = p.pages + 16 * lane;
   c.off = 16u * lane;
   c.fifth = lane + 128 < ph_bytes(F) / 16;
+  c.policy = 0;
   return c;
 }
 
@@ -392,23 +394,38 @@ struct alignas(16) ItemEntry {
 // is 0, then arrives (no-increment) on the stage's mbarrier, which expects 32
 // arrivals; it fires once all of the lane's earlier copies have landed, so a
 // stage's barrier covers every stage issued before it as well.
-template <int F>
+template <int F, int M>
 __device__ __forceinline__ void issue_page_off(const LaneCopy& c, long long off, int nv, uint32_t st, uint32_t bar) {
   const uint8_t* src = c.src + off;
   const uint32_t dst = st + c.off;
   const uint32_t v5 = (nv > 0 && c.fifth) ? 1u : 0u;
-  asm volatile(
-      "{\n .reg .pred p, q;\n"
-      " setp.gt.s32 p, %2, 0;\n"
-      " setp.ne.u32 q, %3, 0;\n"
-      " @p cp.async.cg.shared.global [%0], [%1], 16;\n"
-      " @p cp.async.cg.shared.global [%0+512], [%1+512], 16;\n"
-      " @p cp.async.cg.shared.global [%0+1024], [%1+1024], 16;\n"
-      " @p cp.async.cg.shared.global [%0+1536], [%1+1536], 16;\n"
-      " @q cp.async.cg.shared.global [%0+2048], [%1+2048], 16;\n"
-      " cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%4];\n"
-      "}\n" ::"r"(dst), "l"(src), "r"(nv), "r"(v5), "r"(bar)
-      : "memory");
+  if constexpr ((M & kStored) != 0) {
+    asm volatile(
+        "{\n .reg .pred p, q;\n"
+        " setp.gt.s32 p, %2, 0;\n"
+        " setp.ne.u32 q, %3, 0;\n"
+        " @p cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %5;\n"
+        " @p cp.async.cg.shared.global.L2::cache_hint [%0+512], [%1+512], 16, %5;\n"
+        " @p cp.async.cg.shared.global.L2::cache_hint [%0+1024], [%1+1024], 16, %5;\n"
+        " @p cp.async.cg.shared.global.L2::cache_hint [%0+1536], [%1+1536], 16, %5;\n"
+        " @q cp.async.cg.shared.global.L2::cache_hint [%0+2048], [%1+2048], 16, %5;\n"
+        " cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%4];\n"
+        "}\n" ::"r"(dst), "l"(src), "r"(nv), "r"(v5), "r"(bar), "l"(c.policy)
+        : "memory");
+  } else {
+    asm volatile(
+        "{\n .reg .pred p, q;\n"
+        " setp.gt.s32 p, %2, 0;\n"
+        " setp.ne.u32 q, %3, 0;\n"
+        " @p cp.async.cg.shared.global [%0], [%1], 16;\n"
+        " @p cp.async.cg.shared.global [%0+512], [%1+512], 16;\n"
+        " @p cp.async.cg.shared.global [%0+1024], [%1+1024], 16;\n"
+        " @p cp.async.cg.shared.global [%0+1536], [%1+1536], 16;\n"
+        " @q cp.async.cg.shared.global [%0+2048], [%1+2048], 16;\n"
+        " cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%4];\n"
+        "}\n" ::"r"(dst), "l"(src), "r"(nv), "r"(v5), "r"(bar)
+        : "memory");
+  }
 }
 
 // Two NVFP4 page-heads (288 pieces of 16 bytes: 9 per lane), into stages a and
@@ -416,6 +433,7 @@ __device__ __forceinline__ void issue_page_off(const LaneCopy& c, long long off,
 // l, l + 32, l + 64, l + 96, then a's l + 128 (l < 16) or b's l - 16 (l >= 16),
 // then b's l + 16, l + 48, l + 80, l + 112; then arrives on both barriers.
 // Nothing is copied for an entry with no valid tokens (a bad page id).
+template <int M>
 __device__ __forceinline__ void issue_two_off(const LaneCopy& c, const ItemEntry& a, const ItemEntry& b,
                                               uint32_t sta, uint32_t stb, uint32_t bara, uint32_t barb,
                                               bool lo) {
@@ -425,25 +443,47 @@ __device__ __forceinline__ void issue_two_off(const LaneCopy& c, const ItemEntry
   const uint32_t dst4 = lo ? dsta + 2048 : dstb - 256;
   const uint8_t* src4 = lo ? srca + 2048 : srcb - 256;
   const int n4 = lo ? a.nv : b.nv;
-  asm volatile(
-      "{\n .reg .pred pa, pb, p4;\n"
-      " setp.gt.s32 pa, %4, 0;\n"
-      " setp.gt.s32 pb, %5, 0;\n"
-      " setp.gt.s32 p4, %6, 0;\n"
-      " @pa cp.async.cg.shared.global [%0], [%2], 16;\n"
-      " @pa cp.async.cg.shared.global [%0+512], [%2+512], 16;\n"
-      " @pa cp.async.cg.shared.global [%0+1024], [%2+1024], 16;\n"
-      " @pa cp.async.cg.shared.global [%0+1536], [%2+1536], 16;\n"
-      " @p4 cp.async.cg.shared.global [%7], [%8], 16;\n"
-      " @pb cp.async.cg.shared.global [%1+256], [%3+256], 16;\n"
-      " @pb cp.async.cg.shared.global [%1+768], [%3+768], 16;\n"
-      " @pb cp.async.cg.shared.global [%1+1280], [%3+1280], 16;\n"
-      " @pb cp.async.cg.shared.global [%1+1792], [%3+1792], 16;\n"
-      " cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%9];\n"
-      " cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%10];\n"
-      "}\n" ::"r"(dsta), "r"(dstb), "l"(srca), "l"(srcb), "r"(a.nv), "r"(b.nv), "r"(n4), "r"(dst4), "l"(src4),
-      "r"(bara), "r"(barb)
-      : "memory");
+  if constexpr ((M & kStored) != 0) {
+    asm volatile(
+        "{\n .reg .pred pa, pb, p4;\n"
+        " setp.gt.s32 pa, %4, 0;\n"
+        " setp.gt.s32 pb, %5, 0;\n"
+        " setp.gt.s32 p4, %6, 0;\n"
+        " @pa cp.async.cg.shared.global.L2::cache_hint [%0], [%2], 16, %11;\n"
+        " @pa cp.async.cg.shared.global.L2::cache_hint [%0+512], [%2+512], 16, %11;\n"
+        " @pa cp.async.cg.shared.global.L2::cache_hint [%0+1024], [%2+1024], 16, %11;\n"
+        " @pa cp.async.cg.shared.global.L2::cache_hint [%0+1536], [%2+1536], 16, %11;\n"
+        " @p4 cp.async.cg.shared.global.L2::cache_hint [%7], [%8], 16, %11;\n"
+        " @pb cp.async.cg.shared.global.L2::cache_hint [%1+256], [%3+256], 16, %11;\n"
+        " @pb cp.async.cg.shared.global.L2::cache_hint [%1+768], [%3+768], 16, %11;\n"
+        " @pb cp.async.cg.shared.global.L2::cache_hint [%1+1280], [%3+1280], 16, %11;\n"
+        " @pb cp.async.cg.shared.global.L2::cache_hint [%1+1792], [%3+1792], 16, %11;\n"
+        " cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%9];\n"
+        " cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%10];\n"
+        "}\n" ::"r"(dsta), "r"(dstb), "l"(srca), "l"(srcb), "r"(a.nv), "r"(b.nv), "r"(n4), "r"(dst4), "l"(src4),
+        "r"(bara), "r"(barb), "l"(c.policy)
+        : "memory");
+  } else {
+    asm volatile(
+        "{\n .reg .pred pa, pb, p4;\n"
+        " setp.gt.s32 pa, %4, 0;\n"
+        " setp.gt.s32 pb, %5, 0;\n"
+        " setp.gt.s32 p4, %6, 0;\n"
+        " @pa cp.async.cg.shared.global [%0], [%2], 16;\n"
+        " @pa cp.async.cg.shared.global [%0+512], [%2+512], 16;\n"
+        " @pa cp.async.cg.shared.global [%0+1024], [%2+1024], 16;\n"
+        " @pa cp.async.cg.shared.global [%0+1536], [%2+1536], 16;\n"
+        " @p4 cp.async.cg.shared.global [%7], [%8], 16;\n"
+        " @pb cp.async.cg.shared.global [%1+256], [%3+256], 16;\n"
+        " @pb cp.async.cg.shared.global [%1+768], [%3+768], 16;\n"
+        " @pb cp.async.cg.shared.global [%1+1280], [%3+1280], 16;\n"
+        " @pb cp.async.cg.shared.global [%1+1792], [%3+1792], 16;\n"
+        " cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%9];\n"
+        " cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%10];\n"
+        "}\n" ::"r"(dsta), "r"(dstb), "l"(srca), "l"(srcb), "r"(a.nv), "r"(b.nv), "r"(n4), "r"(dst4), "l"(src4),
+        "r"(bara), "r"(barb)
+        : "memory");
+  }
 }
 
 // Per-warp attention state of the current pair.
@@ -1172,10 +1212,12 @@ __global__ void __launch_bounds__(kNW * 32, kCtasPerSm) decode_kernel(const Deco
     asm volatile("griddepcontrol.wait;" ::: "memory");
     // producer: prefill the ring (all within the first chunk: kStages < 32)
     const int pre = n < kStages ? n : kStages;
-    const LaneCopy lc = lane_copy<F>(p, lane);
+    LaneCopy lc = lane_copy<F>(p, lane);
+    if constexpr ((M & kStored) != 0)
+      asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(lc.policy));
     const uint32_t wring_u32 = smem_u32(wring);
     for (int j = 0; j < pre; ++j) {
-      issue_page_off<F>(lc, tab[j].off, tab[j].nv, wring_u32 + j * kStageBytes, wbar + 8 * j);
+      issue_page_off<F, M>(lc, tab[j].off, tab[j].nv, wring_u32 + j * kStageBytes, wbar + 8 * j);
     }
     int issued = pre;
     int chunk = 0;   // the chunk `cur` maps
@@ -1264,15 +1306,15 @@ __global__ void __launch_bounds__(kNW * 32, kCtasPerSm) decode_kernel(const Deco
           if (jb < n) {
             const ItemEntry ea = tab[ja & 63], eb = tab[jb & 63];
             if constexpr (F == kFmtMxfp4) {
-              issue_page_off<F>(lc, ea.off, ea.nv, wring_u32 + st * kStageBytes, wbar + 8 * st);
-              issue_page_off<F>(lc, eb.off, eb.nv, wring_u32 + st1 * kStageBytes, wbar + 8 * st1);
+              issue_page_off<F, M>(lc, ea.off, ea.nv, wring_u32 + st * kStageBytes, wbar + 8 * st);
+              issue_page_off<F, M>(lc, eb.off, eb.nv, wring_u32 + st1 * kStageBytes, wbar + 8 * st1);
             } else {
-              issue_two_off(lc, ea, eb, wring_u32 + st * kStageBytes, wring_u32 + st1 * kStageBytes,
+              issue_two_off<M>(lc, ea, eb, wring_u32 + st * kStageBytes, wring_u32 + st1 * kStageBytes,
                             wbar + 8 * st, wbar + 8 * st1, lane < 16);
             }
             issued = jb + 1;
           } else if (ja < n) {
-            issue_page_off<F>(lc, tab[ja & 63].off, tab[ja & 63].nv, wring_u32 + st * kStageBytes, wbar + 8 * st);
+            issue_page_off<F, M>(lc, tab[ja & 63].off, tab[ja & 63].nv, wring_u32 + st * kStageBytes, wbar + 8 * st);
             issued = ja + 1;
           }
         }
@@ -1299,7 +1341,7 @@ __global__ void __launch_bounds__(kNW * 32, kCtasPerSm) decode_kernel(const Deco
           __syncwarp();
           const int ja = j + kStages;
           if (ja < n) {
-            issue_page_off<F>(lc, tab[ja & 63].off, tab[ja & 63].nv, wring_u32 + st * kStageBytes, wbar + 8 * st);
+            issue_page_off<F, M>(lc, tab[ja & 63].off, tab[ja & 63].nv, wring_u32 + st * kStageBytes, wbar + 8 * st);
             issued = ja + 1;
           }
         }
