@@ -95,17 +95,14 @@ struct Barriers {
   uint64_t drain;
 };
 
-// Q in shared memory (the A operand): K-major core matrices with the row groups
-// of one 16-byte K chunk next to each other.
-constexpr uint32_t kQLBO = kTileM * 16, kQSBO = 128;
-__device__ __forceinline__ uint32_t q_off(int row, int k) { return (uint32_t)(k >> 3) * kQLBO + (uint32_t)row * 16; }
-// K and V in shared memory, in the 128-byte swizzle: atoms of 8 keys x 64 head
-// dims, the 16-byte chunk c (8 head dims) of key r stored at c ^ r; the key
-// groups of one half of the head dims follow one another.  For K (contracted
-// over head dims) this is the K-major form, for V (over keys) the MN-major one.
+// Tiles of Q, K and V in shared memory, in the 128-byte swizzle: atoms of 8 rows
+// (queries or keys) x 64 head dims, the 16-byte chunk c (8 head dims) of row r
+// stored at c ^ r; the row groups of one half of the head dims follow one another.
+// For Q and K (contracted over head dims) this is the K-major form, for V (over
+// keys) the MN-major one.
 constexpr uint32_t kHalfD = kTileBytes / 2, kSBO8 = 1024;  // next 64 head dims, next 8 keys
-__device__ __forceinline__ uint32_t kv_off(int key, int chunk) {  // chunk 0 .. 15
-  return (uint32_t)(chunk >> 3) * kHalfD + (uint32_t)key * 128 + (((uint32_t)chunk ^ (uint32_t)key) & 7) * 16;
+__device__ __forceinline__ uint32_t tile_off(int row, int chunk) {  // chunk 0 .. 15
+  return (uint32_t)(chunk >> 3) * kHalfD + (uint32_t)row * 128 + (((uint32_t)chunk ^ (uint32_t)row) & 7) * 16;
 }
 
 // Positions within a sequence are 32-bit: prefix and chunk together stay below
@@ -283,7 +280,7 @@ __global__ void __launch_bounds__(kThreads, 1) extend_scored_kernel(const Scored
       constexpr uint32_t id_pv = tc::idesc_f16_f32(kTileM, kHeadDim, false, true);
       const uint32_t lead = lane == 0;
       // shared-memory descriptors are a constant plus the address in their low word
-      const uint64_t dq = tc::smem_desc(0, kQLBO, kQSBO), dkv = tc::smem_desc_swizzle128(0, kHalfD, kSBO8);
+      const uint64_t desc = tc::smem_desc_swizzle128(0, kHalfD, kSBO8);
       // the ring's items are K of step 0, V of step 0, K of step 1, ...: `at` is
       // the slot of the item in use, `round` the parity of its phase
       const int items = 2 * v.steps;
@@ -303,8 +300,9 @@ __global__ void __launch_bounds__(kThreads, 1) extend_scored_kernel(const Scored
         asm volatile("" : "+r"(q));  // not worth 16 registers across the loop
 #pragma unroll
         for (int kk = 0; kk < kHeadDim / 16; ++kk)
-          tc1::mma_f16(tmem + t * kTileN, dq | (q + kk * (2 * kQLBO >> 4)), dkv | (k + (kk >> 2) * (kHalfD >> 4) + (kk & 3) * 2), id_qk, kk > 0,
-                       lead);
+          // 16 head dims are 32 bytes of a row
+          tc1::mma_f16(tmem + t * kTileN, desc | (q + (kk >> 2) * (kHalfD >> 4) + (kk & 3) * 2),
+                       desc | (k + (kk >> 2) * (kHalfD >> 4) + (kk & 3) * 2), id_qk, kk > 0, lead);
         tc1::commit(b_s + 8 * t, lead);
       };
       bool ok = warp_wait(b_q, 0) && ready();
@@ -328,7 +326,7 @@ __global__ void __launch_bounds__(kThreads, 1) extend_scored_kernel(const Scored
 #pragma unroll
           for (int kk = 0; kk < kTileN / 16; ++kk)
             tc1::mma_f16_tmem_a(tmem + kTmemO + t * kHeadDim, tmem + t * kTileN + kk * 8,
-                                dkv | (vv + kk * (2 * kSBO8 >> 4)), id_pv, (i > 0 || kk > 0) ? 1u : 0u, lead);
+                                desc | (vv + kk * (2 * kSBO8 >> 4)), id_pv, (i > 0 || kk > 0) ? 1u : 0u, lead);
           if (t == 1) done();  // V
           if (more)
             scores(t, k_at);
@@ -401,8 +399,8 @@ __global__ void __launch_bounds__(kThreads, 1) extend_scored_kernel(const Scored
           const int key = lw * 32 + 4 * g + (lane >> 3);
           const uint4 x = w == 0 ? xk[g] : xv[g];
           const uint4 lo = e4m3x8_to_f16x8(x.x, x.y), hi = e4m3x8_to_f16x8(x.z, x.w);
-          st_shared_v4(at + kv_off(key, 2 * part + first), first ? hi : lo);
-          st_shared_v4(at + kv_off(key, 2 * part + 1 - first), first ? lo : hi);
+          st_shared_v4(at + tile_off(key, 2 * part + first), first ? hi : lo);
+          st_shared_v4(at + tile_off(key, 2 * part + 1 - first), first ? lo : hi);
         }
         tc::fence_smem_to_async();
         __syncwarp();
@@ -428,11 +426,18 @@ __global__ void __launch_bounds__(kThreads, 1) extend_scored_kernel(const Scored
     const int pos = P + t;
     const int head = hk * G + (r & (G - 1));
     {
-      const uint4* src = reinterpret_cast<const uint4*>(p.q + ((q0 + (live ? t : 0)) * p.hq + head) * kHeadDim);
+      // the warp's 32 rows of Q, two whole rows per load
       const uint32_t dst = sQ + tile * kTileBytes;
-#pragma unroll
-      for (int c = 0; c < kHeadDim / 8; ++c)
-        st_shared_v4(dst + q_off(r, 8 * c), bf16x8_to_f16x8(live ? __ldg(src + c) : make_uint4(0, 0, 0, 0)));
+#pragma unroll 8
+      for (int i = 0; i < 16; ++i) {
+        const int r2 = 32 * (warp & 3) + 2 * i + (lane >> 4);
+        const int t2 = t0 + tile * tile_tokens + (r2 >> p.log2_group);
+        uint4 x = make_uint4(0, 0, 0, 0);
+        if (t2 <= t1)
+          x = __ldg(reinterpret_cast<const uint4*>(p.q + ((q0 + t2) * p.hq + hk * G + (r2 & (G - 1))) * kHeadDim) +
+                    (lane & 15));
+        st_shared_v4(dst + tile_off(r2, lane & 15), bf16x8_to_f16x8(x));
+      }
       tc::fence_smem_to_async();
       __syncwarp();
       if (lane == 0) arrive(b_q);
@@ -461,7 +466,7 @@ __global__ void __launch_bounds__(kThreads, 1) extend_scored_kernel(const Scored
       // maximum is that of the products (the cap keeps the order), and the cap is
       // left to the second pass, where the FMA pipe works beside the
       // special-function unit.
-      bool direct = false;
+      bool direct = false, near_zero = false;  // (near_zero: in the shorter polynomial's range)
       float top = -INFINITY;  // the row's maximum in base 2
       if constexpr ((M & kBiased) == 0) {
         if (!any_masked) {
@@ -479,8 +484,9 @@ __global__ void __launch_bounds__(kThreads, 1) extend_scored_kernel(const Scored
           const float h = fmaxf(max3(hi[0], hi[1], hi[2]), hi[3]);
           if constexpr (M == kCapped) {
             const float l0 = fminf(min3(lo[0], lo[1], lo[2]), lo[3]);
-            direct = __all_sync(0xFFFFFFFFu, h <= p.cap.limit && l0 >= -p.cap.limit);
-            top = cap_short(both(h), p.cap, both(0.0f)).x;
+            direct = __all_sync(0xFFFFFFFFu, h <= p.cap.limit4 && l0 >= -p.cap.limit4);
+            near_zero = __all_sync(0xFFFFFFFFu, h <= p.cap.limit3 && l0 >= -p.cap.limit3);
+            top = (near_zero ? cap_short3(both(h), p.cap, both(0.0f)) : cap_short4(both(h), p.cap, both(0.0f))).x;
           } else {
             direct = true;
             top = h * p.unit;  // (the unit is positive)
@@ -570,8 +576,10 @@ __global__ void __launch_bounds__(kThreads, 1) extend_scored_kernel(const Scored
       };
       if constexpr (M == 0)
         weights([&](float2 s) { return fma2(s, both(p.unit), both(off)); });
+      else if (M == kCapped && near_zero)
+        weights([&](float2 s) { return cap_short3(s, p.cap, both(off)); });
       else if (M == kCapped && direct)
-        weights([&](float2 s) { return cap_short(s, p.cap, both(off)); });
+        weights([&](float2 s) { return cap_short4(s, p.cap, both(off)); });
       else
         weights([&](float2 s) { return add2(s, both(off)); });
       tc::tmem_wait_st();

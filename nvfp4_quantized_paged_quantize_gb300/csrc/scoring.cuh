@@ -100,37 +100,50 @@ __device__ __forceinline__ void tanh_warp(float2 (&x)[N]) {
 
 // a * tanh(c S) for many scores with the same factors.  While |c S| <= 0.6 (the
 // usual case: scores well inside their cap) both factors are part of a
-// polynomial's coefficients, S Q(S^2) with Q of degree 4, fitted here in the
-// relative maximum norm (7.3e-8 before rounding): six packed operations a pair,
-// of which the last takes an addend with it.
+// polynomial's coefficients, S Q(S^2) with Q of degree 4, or 3 up to 0.4, fitted
+// here in the relative maximum norm (7.3e-8 and 9.8e-8 before rounding).  Six
+// packed operations a pair, or five, of which the last takes an addend with it.
+// (Each step reads three register pairs and takes 2.6 cycles of a scheduler, so a
+// degree is worth a branch per tile.)
 struct CapPoly {
-  float inner, outer;  // c, a
-  float limit;         // the short form holds for |S| <= limit (-1: never)
-  float2 k[5];         // each coefficient twice, as the packed operations take it
+  float inner, outer;     // c, a
+  float limit3, limit4;   // the forms hold for |S| <= limit (-1: never)
+  float2 k3[4], k4[5];    // each coefficient twice, as the packed operations take it
 };
 
 inline CapPoly cap_poly(double c, double a) {
-  constexpr double fit[5] = {0x1.fffffep-1, -0x1.5552a6p-2, 0x1.1097a4p-3, -0x1.aad0b8p-5, 0x1.fb1946p-7};
+  constexpr double fit3[4] = {0x1.fffffcp-1, -0x1.55502ap-2, 0x1.0fca24p-3, -0x1.858f2p-5};
+  constexpr double fit4[5] = {0x1.fffffep-1, -0x1.5552a6p-2, 0x1.1097a4p-3, -0x1.aad0b8p-5, 0x1.fb1946p-7};
   CapPoly p;
   p.inner = (float)c;
   p.outer = (float)a;
-  // the coefficients' range: a c^9 fit[4] stays a normal number
-  p.limit = c >= 0x1p-10 && c <= 0x1p+10 ? (float)(0.6 / c) : -1.0f;
-  double f = c * a;
+  // the coefficients' range: a c^9 fit4[4] stays a normal number
+  const bool fits = c >= 0x1p-10 && c <= 0x1p+10;
+  p.limit3 = fits ? (float)(0.4 / c) : -1.0f;
+  p.limit4 = fits ? (float)(0.6 / c) : -1.0f;
+  double f = fits ? c * a : 0.0;
   for (int i = 0; i < 5; ++i, f *= c * c) {
-    const float k = p.limit > 0.0f ? (float)(fit[i] * f) : 0.0f;
-    p.k[i] = make_float2(k, k);
+    const float k3 = i < 4 ? (float)(fit3[i] * f) : 0.0f, k4 = (float)(fit4[i] * f);
+    if (i < 4) p.k3[i] = make_float2(k3, k3);
+    p.k4[i] = make_float2(k4, k4);
   }
   return p;
 }
 
-// a * tanh(c S) + add, |S| <= limit.
-__device__ __forceinline__ float2 cap_short(float2 S, const CapPoly& p, float2 add) {
+// a * tanh(c S) + add, |S| <= limit3 or limit4.
+__device__ __forceinline__ float2 cap_short3(float2 S, const CapPoly& p, float2 add) {
   const float2 w = mul2(S, S);
-  float2 q = fma2(p.k[4], w, p.k[3]);
-  q = fma2(q, w, p.k[2]);
-  q = fma2(q, w, p.k[1]);
-  q = fma2(q, w, p.k[0]);
+  float2 q = fma2(p.k3[3], w, p.k3[2]);
+  q = fma2(q, w, p.k3[1]);
+  q = fma2(q, w, p.k3[0]);
+  return fma2(S, q, add);
+}
+__device__ __forceinline__ float2 cap_short4(float2 S, const CapPoly& p, float2 add) {
+  const float2 w = mul2(S, S);
+  float2 q = fma2(p.k4[4], w, p.k4[3]);
+  q = fma2(q, w, p.k4[2]);
+  q = fma2(q, w, p.k4[1]);
+  q = fma2(q, w, p.k4[0]);
   return fma2(S, q, add);
 }
 
@@ -143,9 +156,9 @@ __device__ __forceinline__ void cap_scores(float2 (&x)[N], const CapPoly& p) {
     hi = max3(hi, x[i].x, x[i].y);
     lo = min3(lo, x[i].x, x[i].y);
   }
-  if (__all_sync(0xFFFFFFFFu, hi <= p.limit && lo >= -p.limit)) {
+  if (__all_sync(0xFFFFFFFFu, hi <= p.limit4 && lo >= -p.limit4)) {
 #pragma unroll
-    for (int i = 0; i < N; ++i) x[i] = cap_short(x[i], p, both(0.0f));
+    for (int i = 0; i < N; ++i) x[i] = cap_short4(x[i], p, both(0.0f));
     return;
   }
 #pragma unroll
