@@ -462,11 +462,11 @@ __global__ void __launch_bounds__(kThreads, 1) extend_scored_kernel(const Scored
       const int end = kr.end - kbase, low = kr.low - kbase, sink = kr.sink_end - kbase, near = kr.near - kbase;
       const bool masked = end < kTileN || (near > 0 && (low > 0 || sink < kTileN));
       const bool any_masked = __any_sync(0xFFFFFFFFu, masked);
-      // All visible, and plain or capped within the polynomial's range: the row's
-      // maximum is that of the products (the cap keeps the order), and the cap is
-      // left to the second pass, where the FMA pipe works beside the
-      // special-function unit.
-      bool direct = false, near_zero = false;  // (near_zero: in the shorter polynomial's range)
+      // All visible, and no bias: the row's maximum is that of the products (the
+      // cap keeps the order), and the cap is left to the second pass, where the FMA
+      // pipe works beside the special-function unit.
+      bool direct = false;
+      int form = 0;           // the cap's: the polynomial of degree 3, of 4, or any
       float top = -INFINITY;  // the row's maximum in base 2
       if constexpr ((M & kBiased) == 0) {
         if (!any_masked) {
@@ -484,13 +484,18 @@ __global__ void __launch_bounds__(kThreads, 1) extend_scored_kernel(const Scored
           const float h = fmaxf(max3(hi[0], hi[1], hi[2]), hi[3]);
           if constexpr (M == kCapped) {
             const float l0 = fminf(min3(lo[0], lo[1], lo[2]), lo[3]);
-            direct = __all_sync(0xFFFFFFFFu, h <= p.cap.limit4 && l0 >= -p.cap.limit4);
-            near_zero = __all_sync(0xFFFFFFFFu, h <= p.cap.limit3 && l0 >= -p.cap.limit3);
-            top = (near_zero ? cap_short3(both(h), p.cap, both(0.0f)) : cap_short4(both(h), p.cap, both(0.0f))).x;
+            form = __all_sync(0xFFFFFFFFu, h <= p.cap.limit3 && l0 >= -p.cap.limit3)   ? 3
+                   : __all_sync(0xFFFFFFFFu, h <= p.cap.limit4 && l0 >= -p.cap.limit4) ? 4
+                                                                                        : 0;
+            const float2 zero = both(0.0f);
+            top = (form == 3   ? cap_short3(both(h), p.cap, zero)
+                   : form == 4 ? cap_short4(both(h), p.cap, zero)
+                               : cap_any(both(h), p.cap, zero))
+                      .x;
           } else {
-            direct = true;
             top = h * p.unit;  // (the unit is positive)
           }
+          direct = true;
         }
       }
       if (!direct) {
@@ -576,10 +581,12 @@ __global__ void __launch_bounds__(kThreads, 1) extend_scored_kernel(const Scored
       };
       if constexpr (M == 0)
         weights([&](float2 s) { return fma2(s, both(p.unit), both(off)); });
-      else if (M == kCapped && near_zero)
+      else if (M == kCapped && direct && form == 3)
         weights([&](float2 s) { return cap_short3(s, p.cap, both(off)); });
-      else if (M == kCapped && direct)
+      else if (M == kCapped && direct && form == 4)
         weights([&](float2 s) { return cap_short4(s, p.cap, both(off)); });
+      else if (M == kCapped && direct)
+        weights([&](float2 s) { return cap_any(s, p.cap, both(off)); });
       else
         weights([&](float2 s) { return add2(s, both(off)); });
       tc::tmem_wait_st();

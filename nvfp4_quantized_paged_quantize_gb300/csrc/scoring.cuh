@@ -104,9 +104,11 @@ __device__ __forceinline__ void tanh_warp(float2 (&x)[N]) {
 // here in the relative maximum norm (7.3e-8 and 9.8e-8 before rounding).  Six
 // packed operations a pair, or five, of which the last takes an addend with it.
 // (Each step reads three register pairs and takes 2.6 cycles of a scheduler, so a
-// degree is worth a branch per tile.)
+// degree is worth a branch per tile.)  Beyond: a - 2 a / (e^{2 c S} + 1) by two
+// special-function operations a score, whose error is absolute, some 2^-23 a (in
+// base 2, 1e-5 for a cap of 50).
 struct CapPoly {
-  float inner, outer;     // c, a
+  float inner, outer;     // 2 c log2(e), a
   float limit3, limit4;   // the forms hold for |S| <= limit (-1: never)
   float2 k3[4], k4[5];    // each coefficient twice, as the packed operations take it
 };
@@ -115,7 +117,7 @@ inline CapPoly cap_poly(double c, double a) {
   constexpr double fit3[4] = {0x1.fffffcp-1, -0x1.55502ap-2, 0x1.0fca24p-3, -0x1.858f2p-5};
   constexpr double fit4[5] = {0x1.fffffep-1, -0x1.5552a6p-2, 0x1.1097a4p-3, -0x1.aad0b8p-5, 0x1.fb1946p-7};
   CapPoly p;
-  p.inner = (float)c;
+  p.inner = (float)(2.0 * c * 1.4426950408889634);
   p.outer = (float)a;
   // the coefficients' range: a c^9 fit4[4] stays a normal number
   const bool fits = c >= 0x1p-10 && c <= 0x1p+10;
@@ -147,7 +149,19 @@ __device__ __forceinline__ float2 cap_short4(float2 S, const CapPoly& p, float2 
   return fma2(S, q, add);
 }
 
-// S -> a * tanh(c S) for any S.
+// The same for any S.
+__device__ __forceinline__ float2 cap_any(float2 S, const CapPoly& p, float2 add) {
+  const float2 z = mul2(S, both(p.inner));
+  float2 e, r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.x) : "f"(z.x));
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.y) : "f"(z.y));
+  e = add2(e, both(1.0f));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.x) : "f"(e.x));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.y) : "f"(e.y));
+  return fma2(r, both(-2.0f * p.outer), add2(add, both(p.outer)));
+}
+
+// S -> a * tanh(c S) in place.
 template <int N>
 __device__ __forceinline__ void cap_scores(float2 (&x)[N], const CapPoly& p) {
   float hi = x[0].x, lo = x[0].x;
@@ -159,13 +173,10 @@ __device__ __forceinline__ void cap_scores(float2 (&x)[N], const CapPoly& p) {
   if (__all_sync(0xFFFFFFFFu, hi <= p.limit4 && lo >= -p.limit4)) {
 #pragma unroll
     for (int i = 0; i < N; ++i) x[i] = cap_short4(x[i], p, both(0.0f));
-    return;
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i) x[i] = cap_any(x[i], p, both(0.0f));
   }
-#pragma unroll
-  for (int i = 0; i < N; ++i) x[i] = mul2(x[i], both(p.inner));
-  tanh_warp(x);
-#pragma unroll
-  for (int i = 0; i < N; ++i) x[i] = mul2(x[i], both(p.outer));
 }
 
 }  // namespace nvfp4kv
