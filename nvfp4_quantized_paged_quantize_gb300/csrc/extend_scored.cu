@@ -467,6 +467,7 @@ __global__ void __launch_bounds__(kThreads, 1) extend_scored_kernel(const Scored
       // pipe works beside the special-function unit.
       bool direct = false;
       int form = 0;           // the cap's: the polynomial of degree 3, of 4, or any
+      uint32_t gone = 0;      // bit k: none of the warp's rows sees keys 32 k .. 32 k + 31
       float top = -INFINITY;  // the row's maximum in base 2
       if constexpr ((M & kBiased) == 0) {
         if (!any_masked) {
@@ -499,16 +500,22 @@ __global__ void __launch_bounds__(kThreads, 1) extend_scored_kernel(const Scored
         }
       }
       if (!direct) {
-        // cap, bias and mask the scores where they lie, 32 at a time
+        // cap, bias and mask the scores where they lie, 32 at a time, leaving out
+        // the chunks that none of the warp's rows sees
         float mr[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-        uint32_t y[2][32];
-        tc::tmem_ld32_async(t_s, y[0]);
-#pragma unroll
-        for (int c4 = 0; c4 < kTileN / 32; ++c4) {
-          const int at = 32 * c4;
-          uint32_t(&w)[32] = y[c4 & 1];
-          tc::tmem_wait_ld(w);
-          if (c4 + 1 < kTileN / 32) tc::tmem_ld32_async(t_s + at + 32, y[(c4 + 1) & 1]);
+#pragma unroll 1
+        for (int at = 0; at < kTileN; at += 32) {
+          uint32_t hidden = 0;  // bit c: key at + c
+          if (any_masked) {
+            hidden = ~first_bits(end - at) |
+                     (first_bits(near - at) & ~(first_bits(sink - at) & ~first_bits(low - at)));
+            if (__all_sync(0xFFFFFFFFu, hidden == ~0u)) {
+              gone |= 1u << (at / 32);
+              continue;
+            }
+          }
+          uint32_t w[32];
+          tc::tmem_ld32(t_s + at, w);
           float2(&x)[16] = *reinterpret_cast<float2(*)[16]>(&w[0]);
           if constexpr ((M & kCapped) != 0) cap_scores(x, p.cap);
           if constexpr ((M & kBiased) != 0) {
@@ -520,9 +527,7 @@ __global__ void __launch_bounds__(kThreads, 1) extend_scored_kernel(const Scored
               x[c].y = fmaf(-slope, fabsf(d0 - (float)(2 * c + 1)), x[c].y * unit);
             }
           }
-          if (any_masked) {
-            const uint32_t hidden = ~first_bits(end - at) |
-                                    (first_bits(near - at) & ~(first_bits(sink - at) & ~first_bits(low - at)));
+          if (__any_sync(0xFFFFFFFFu, hidden != 0)) {
 #pragma unroll
             for (int c = 0; c < 32; ++c)
               if (hidden >> c & 1) w[c] = 0xFF800000u;  // -inf
@@ -559,25 +564,42 @@ __global__ void __launch_bounds__(kThreads, 1) extend_scored_kernel(const Scored
       const float off = m > -INFINITY ? -m : -INFINITY;
       auto weights = [&](auto exponent) {
         uint32_t y[2][32], ph[2][16];
-        tc::tmem_ld32_async(t_s, y[0]);
-#pragma unroll
-        for (int c4 = 0; c4 < kTileN / 32; ++c4) {
-          tc::tmem_wait_ld(y[c4 & 1]);
-          if (c4 + 1 < kTileN / 32) tc::tmem_ld32_async(t_s + 32 * (c4 + 1), y[(c4 + 1) & 1]);
+        auto chunk = [&](const uint32_t (&x)[32], uint32_t (&out)[16]) {
 #pragma unroll
           for (int c = 0; c < 16; ++c) {
-            float2 e = exponent(make_float2(__uint_as_float(y[c4 & 1][2 * c]), __uint_as_float(y[c4 & 1][2 * c + 1])));
+            float2 e = exponent(make_float2(__uint_as_float(x[2 * c]), __uint_as_float(x[2 * c + 1])));
             e.x = ex2(e.x);
             e.y = ex2(e.y);
-            ph[c4 & 1][c] = f16x2_bits(e.x, e.y);
+            out[c] = f16x2_bits(e.x, e.y);
             l[c & 1] = add2(l[c & 1], e);
           }
-          // P (two keys per column) over S columns already read: the A operand of
-          // P V.  Stored one round late, so that the next round's arithmetic can
-          // start under the end of this one's.
-          if (c4 > 0) tc::tmem_st16_async(t_s + 16 * (c4 - 1), ph[(c4 - 1) & 1]);
+        };
+        // P (two keys per column) goes over S columns already read: the A operand
+        // of P V
+        if (!any_masked) {
+          // a chunk is stored one round late, under the next one's arithmetic
+          tc::tmem_ld32_async(t_s, y[0]);
+#pragma unroll
+          for (int c4 = 0; c4 < kTileN / 32; ++c4) {
+            tc::tmem_wait_ld(y[c4 & 1]);
+            if (c4 + 1 < kTileN / 32) tc::tmem_ld32_async(t_s + 32 * (c4 + 1), y[(c4 + 1) & 1]);
+            chunk(y[c4 & 1], ph[c4 & 1]);
+            if (c4 > 0) tc::tmem_st16_async(t_s + 16 * (c4 - 1), ph[(c4 - 1) & 1]);
+          }
+          tc::tmem_st16_async(t_s + kTileN / 2 - 16, ph[1]);
+        } else {  // (an edge tile: in a loop, which costs less to fetch than it loses)
+#pragma unroll 1
+          for (int at = 0; at < kTileN; at += 32) {
+            if (gone >> (at / 32) & 1) {
+#pragma unroll
+              for (int c = 0; c < 16; ++c) ph[0][c] = 0;
+            } else {
+              tc::tmem_ld32(t_s + at, y[0]);
+              chunk(y[0], ph[0]);
+            }
+            tc::tmem_st16_async(t_s + at / 2, ph[0]);
+          }
         }
-        tc::tmem_st16_async(t_s + kTileN / 2 - 16, ph[1]);
       };
       if constexpr (M == 0)
         weights([&](float2 s) { return fma2(s, both(p.unit), both(off)); });
