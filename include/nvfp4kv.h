@@ -502,8 +502,10 @@ int nvfp4kv_decode_weights_workspace_size(const nvfp4kv_cache* cache, int32_t ba
  *   out          device bf16 [total_q][num_q_heads][head_dim]; a row with no
  *                visible key is zeros
  *   lse          device fp32 [total_q][num_q_heads], or NULL; -inf for such a row
- * Key tiles that no query of a block of rows sees are not read.  Other
- * arguments, limits and errors as in nvfp4kv_extend_attention. */
+ * Workspace rows that no query of a block of rows sees are not read, so they
+ * may hold anything.  A prefix of more than 2^31 - 256 keys with its chunk is cut
+ * with NVFP4KV_DEVERR_LENGTH.  Other arguments, limits and errors as in
+ * nvfp4kv_extend_attention. */
 int nvfp4kv_extend_attention_scored(const void* q_bf16, const int64_t* cu_q, int32_t max_q_len,
                                     const uint8_t* ws_k, const uint8_t* ws_v, const int64_t* cu_prefix,
                                     const int32_t* prefix_lens, int32_t batch, int64_t total_rows,
@@ -532,7 +534,7 @@ int nvfp4kv_extend_attention_scored(const void* q_bf16, const int64_t* cu_q, int
  *                   >= ceil(budget / page_size); its first ceil(n / page_size)
  *                   pages are written whole (rows past n as zeros).  They must
  *                   differ from each other and from every page that page_table
- *                   lists for the call
+ *                   lists for the call (the two tables may not be one)
  *   kept            device int32 [batch][num_kv_heads][budget]; -1 from n on
  *   kept_weights    device fp32 [batch][num_kv_heads][kept_stride], or NULL:
  *                   weights[kept], zeros from n to budget; kept_stride >= budget.

@@ -293,6 +293,12 @@ def _check_tensor(name: str, x, dtype, shape) -> None:
     raise ValueError(f"{name}: expected a contiguous {dtype} GPU tensor of shape {shape}, got {what}")
 
 
+def _check_device(name: str, x) -> None:
+    """x lives on the current device, where the call's kernels run; raises ValueError."""
+    if x.get_device() != _types().cuda.current_device():
+        raise ValueError(f"{name}: on {x.device}, but the current device is {_types().cuda.current_device()}")
+
+
 def _shape(name: str, x, dims: int):
     """x's sizes; raises ValueError if it has not `dims` of them."""
     if x is None or x.dim() != dims:
@@ -314,6 +320,7 @@ def _check_decode(cache: "Cache", q, out, page_table, seq_lens, lse):
     _check_tensor("seq_lens", seq_lens, t.int32, (B,))
     if lse is not None:
         _check_tensor("lse", lse, t.float32, (B, Hq))
+    _check_device("q", q)
     return B, Hq, maxp
 
 
@@ -393,6 +400,7 @@ def nvfp4kv_extend_attention_scored(q, cu_q, max_q_len: int, ws_k, ws_v, cu_pref
         _check_tensor("doc_starts", doc_starts, t.int32, (n,))
     if lse is not None:
         _check_tensor("lse", lse, t.float32, (n, hq))
+    _check_device("q", q)
     _check("nvfp4kv_extend_attention_scored",
            _L().nvfp4kv_extend_attention_scored(_ptr(q), _ptr(cu_q), int(max_q_len), _ptr(ws_k), _ptr(ws_v),
                                                 _ptr(cu_prefix), _ptr(prefix_lens), B, rows, hq, hkv, HEAD_DIM,
@@ -424,6 +432,7 @@ def nvfp4kv_evict(cache: "Cache", page_table, seq_lens, weights, budget: int, fi
         _check_tensor("kept_weights", kept_weights, t.float32, (B, hkv, kept_stride))
     if new_lens is not None:
         _check_tensor("new_lens", new_lens, t.int32, (B,))
+    _check_device("weights", weights)
     c = cache.c_struct()
     _check("nvfp4kv_evict",
            _L().nvfp4kv_evict(ctypes.byref(c), _ptr(page_table), maxp, _ptr(seq_lens), B, _ptr(weights), stride,

@@ -432,6 +432,11 @@ int nvfp4kv_evict(const nvfp4kv_cache* cache, const int32_t* page_table, int32_t
                           (const void*)dst_page_table, (const void*)kept, (const void*)kept_weights,
                           (const void*)new_lens, (const void*)device_status})
     if (!aligned(ptr, 4)) return NVFP4KV_ERR_INVALID_ARGUMENT;
+  // packing in place, or sums on top of those still being read, would go wrong silently
+  const float* const weights_end = weights + pairs * weight_stride;
+  const float* const kept_end = kept_weights ? kept_weights + pairs * kept_stride : kept_weights;
+  if (dst_page_table == page_table || (kept_weights && kept_weights < weights_end && weights < kept_end))
+    return NVFP4KV_ERR_INVALID_ARGUMENT;
   int nsm = 0;
   if ((st = current_num_sms(&nsm)) != NVFP4KV_OK) return st;
   return cuda_status(nvfp4kv::launch_evict(*cache, page_table, max_pages_per_seq, seq_lens, batch, weights,

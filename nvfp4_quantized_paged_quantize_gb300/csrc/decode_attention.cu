@@ -1802,7 +1802,8 @@ cudaError_t launch_decode_scored(const nvfp4kv_cache& c, const uint16_t* q, uint
   int m = kScored;
   if (sc.softcap > 0.0f) {
     m |= kCapped;
-    p.cap_scale = (float)((double)softmax_scale * (double)c.k_global_scale / (double)sc.softcap);
+    const double inner = (double)softmax_scale * (double)c.k_global_scale / (double)sc.softcap;
+    p.cap_scale = (float)(inner < 0x1p+20 ? inner : 0x1p+20);  // stays finite under q's prescale (up to 2^100)
     p.score_scale = (float)((double)sc.softcap * 1.4426950408889634);
   }
   if (sc.slopes != nullptr) m |= kBiased;

@@ -47,6 +47,8 @@ enum : int {
   kBiased = 2   // minus slope * distance
 };
 
+enum : int { kFar, kNear, kAny };  // the cap's forms
+
 constexpr int kTileM = 128;    // query rows per tile (TMEM lanes); a CTA takes two
 constexpr int kTileN = 128;    // keys per K/V tile
 constexpr int kRows = 2 * kTileM;
@@ -224,15 +226,15 @@ __global__ void __launch_bounds__(kThreads, 1) extend_scored_kernel(const Scored
   // the sequence: chunk length C, prefix P, first workspace row
   const int64_t q0 = __ldg(p.cu_q + b);
   const int64_t chunk = __ldg(p.cu_q + b + 1) - q0;
-  const int C = (int)(chunk < 0 ? 0 : (chunk > p.max_q_len ? p.max_q_len : chunk));
+  const int C = (int)min(max(chunk, (int64_t)0), (int64_t)min(p.max_q_len, kMaxKeys));
   const int prefix = __ldg(p.prefix_lens + b);
-  const int P = min(max(prefix, 0), kMaxKeys - min(C, kMaxKeys));
+  const int P = min(max(prefix, 0), kMaxKeys - C);
   if ((C != chunk || P != prefix) && threadIdx.x == 0 && blockIdx.x == 0) flag_error(p.status, NVFP4KV_DEVERR_LENGTH);
   // the latest (longest) row blocks first
   const int64_t first_token = (int64_t)(gridDim.x - 1 - blockIdx.x) * 2 * tile_tokens;
-  if (first_token >= min(C, kMaxKeys)) return;  // no query
-  const int t0 = (int)first_token, t1 = min(t0 + 2 * tile_tokens, min(C, kMaxKeys)) - 1;
-  const int keys = P + min(C, kMaxKeys);
+  if (first_token >= C) return;  // no query
+  const int t0 = (int)first_token, t1 = min(t0 + 2 * tile_tokens, C) - 1;
+  const int keys = P + C;
   const int full = p.full_lens != nullptr ? __ldg(p.full_lens + b) : 0;
 
   const uint32_t sQ = smem_u32(smem), sRing = sQ + 2 * kTileBytes;
@@ -466,7 +468,7 @@ __global__ void __launch_bounds__(kThreads, 1) extend_scored_kernel(const Scored
       // cap keeps the order), and the cap is left to the second pass, where the FMA
       // pipe works beside the special-function unit.
       bool direct = false;
-      int form = 0;           // the cap's: the polynomial of degree 3, of 4, or any
+      int form = kAny;        // the cap's
       uint32_t gone = 0;      // bit k: none of the warp's rows sees keys 32 k .. 32 k + 31
       float top = -INFINITY;  // the row's maximum in base 2
       if constexpr ((M & kBiased) == 0) {
@@ -485,13 +487,13 @@ __global__ void __launch_bounds__(kThreads, 1) extend_scored_kernel(const Scored
           const float h = fmaxf(max3(hi[0], hi[1], hi[2]), hi[3]);
           if constexpr (M == kCapped) {
             const float l0 = fminf(min3(lo[0], lo[1], lo[2]), lo[3]);
-            form = __all_sync(0xFFFFFFFFu, h <= p.cap.limit3 && l0 >= -p.cap.limit3)   ? 3
-                   : __all_sync(0xFFFFFFFFu, h <= p.cap.limit4 && l0 >= -p.cap.limit4) ? 4
-                                                                                        : 0;
+            form = __all_sync(0xFFFFFFFFu, h <= p.cap.far && l0 >= -p.cap.far)     ? kFar
+                   : __all_sync(0xFFFFFFFFu, h <= p.cap.near && l0 >= -p.cap.near) ? kNear
+                                                                                    : kAny;
             const float2 zero = both(0.0f);
-            top = (form == 3   ? cap_short3(both(h), p.cap, zero)
-                   : form == 4 ? cap_short4(both(h), p.cap, zero)
-                               : cap_any(both(h), p.cap, zero))
+            top = (form == kFar    ? cap_far(both(h), p.cap, zero)
+                   : form == kNear ? cap_near(both(h), p.cap, zero)
+                                   : cap_any(both(h), p.cap, zero))
                       .x;
           } else {
             top = h * p.unit;  // (the unit is positive)
@@ -603,10 +605,10 @@ __global__ void __launch_bounds__(kThreads, 1) extend_scored_kernel(const Scored
       };
       if constexpr (M == 0)
         weights([&](float2 s) { return fma2(s, both(p.unit), both(off)); });
-      else if (M == kCapped && direct && form == 3)
-        weights([&](float2 s) { return cap_short3(s, p.cap, both(off)); });
-      else if (M == kCapped && direct && form == 4)
-        weights([&](float2 s) { return cap_short4(s, p.cap, both(off)); });
+      else if (M == kCapped && direct && form == kFar)
+        weights([&](float2 s) { return cap_far(s, p.cap, both(off)); });
+      else if (M == kCapped && direct && form == kNear)
+        weights([&](float2 s) { return cap_near(s, p.cap, both(off)); });
       else if (M == kCapped && direct)
         weights([&](float2 s) { return cap_any(s, p.cap, both(off)); });
       else

@@ -98,67 +98,66 @@ __device__ __forceinline__ void tanh_warp(float2 (&x)[N]) {
   }
 }
 
-// a * tanh(c S) for many scores with the same factors.  While |c S| <= 0.6 (the
-// usual case: scores well inside their cap) both factors are part of a
-// polynomial's coefficients, S Q(S^2) with Q of degree 4, or 3 up to 0.4, fitted
-// here in the relative maximum norm (7.3e-8 and 9.8e-8 before rounding).  Six
-// packed operations a pair, or five, of which the last takes an addend with it.
-// (Each step reads three register pairs and takes 2.6 cycles of a scheduler, so a
-// degree is worth a branch per tile.)  Beyond: a - 2 a / (e^{2 c S} + 1) by two
-// special-function operations a score, whose error is absolute, some 2^-23 a (in
-// base 2, 1e-5 for a cap of 50).
+// a * tanh(c S) + add for many scores S with the same factors, in three forms.
+//   far from the cap (|c S| <= 0.4, the usual case): a polynomial whose
+//     coefficients hold both factors, S Q(S^2) with Q of degree 3: five packed
+//     operations a pair, the last of which adds;
+//   |c S| <= 0.6: x Q(x^2), x = c S, Q of degree 4: eight;
+//   any: a - 2 a / (e^{2 c S} + 1) by two special-function operations a score.
+// Both Q were fitted here in the relative maximum norm (9.8e-8 and 7.3e-8 before
+// rounding).  The last form's error is absolute, some 2^-23 a (in base 2, 1e-5
+// for a cap of 50), which is little beside a score of half the cap.  (A packed
+// multiply-add reads three register pairs and takes 2.6 cycles of a scheduler, so
+// a shorter form is worth a branch per tile.)
 struct CapPoly {
-  float inner, outer;     // 2 c log2(e), a
-  float limit3, limit4;   // the forms hold for |S| <= limit (-1: never)
-  float2 k3[4], k4[5];    // each coefficient twice, as the packed operations take it
+  float c, a;
+  float far, near;  // the first form holds for |S| <= far (-1: never), the second up to near
+  float2 k[4];      // the first form's coefficients, each twice, as the packed operations take them
 };
 
 inline CapPoly cap_poly(double c, double a) {
-  constexpr double fit3[4] = {0x1.fffffcp-1, -0x1.55502ap-2, 0x1.0fca24p-3, -0x1.858f2p-5};
-  constexpr double fit4[5] = {0x1.fffffep-1, -0x1.5552a6p-2, 0x1.1097a4p-3, -0x1.aad0b8p-5, 0x1.fb1946p-7};
+  constexpr double fit[4] = {0x1.fffffcp-1, -0x1.55502ap-2, 0x1.0fca24p-3, -0x1.858f2p-5};
+  if (c > 0x1p+100) c = 0x1p+100;  // finite: it may meet a zero
   CapPoly p;
-  p.inner = (float)(2.0 * c * 1.4426950408889634);
-  p.outer = (float)a;
-  // the coefficients' range: a c^9 fit4[4] stays a normal number
-  const bool fits = c >= 0x1p-10 && c <= 0x1p+10;
-  p.limit3 = fits ? (float)(0.4 / c) : -1.0f;
-  p.limit4 = fits ? (float)(0.6 / c) : -1.0f;
-  double f = fits ? c * a : 0.0;
-  for (int i = 0; i < 5; ++i, f *= c * c) {
-    const float k3 = i < 4 ? (float)(fit3[i] * f) : 0.0f, k4 = (float)(fit4[i] * f);
-    if (i < 4) p.k3[i] = make_float2(k3, k3);
-    p.k4[i] = make_float2(k4, k4);
+  p.c = (float)c;
+  p.a = (float)a;
+  p.near = (float)(0.6 / c);
+  // the last coefficient is the one that leaves fp32's range first
+  const double c6 = c * c * c * c * c * c, last = a * c * c6;
+  const bool fits = last > 0x1p-110 && last < 0x1p+110 && a * c > 0x1p-110 && a * c < 0x1p+110;
+  p.far = fits ? (float)(0.4 / c) : -1.0f;
+  double f = fits ? a * c : 0.0;
+  for (int i = 0; i < 4; ++i, f *= c * c) {
+    const float k = (float)(fit[i] * f);
+    p.k[i] = make_float2(k, k);
   }
   return p;
 }
 
-// a * tanh(c S) + add, |S| <= limit3 or limit4.
-__device__ __forceinline__ float2 cap_short3(float2 S, const CapPoly& p, float2 add) {
+__device__ __forceinline__ float2 cap_far(float2 S, const CapPoly& p, float2 add) {
   const float2 w = mul2(S, S);
-  float2 q = fma2(p.k3[3], w, p.k3[2]);
-  q = fma2(q, w, p.k3[1]);
-  q = fma2(q, w, p.k3[0]);
+  float2 q = fma2(p.k[3], w, p.k[2]);
+  q = fma2(q, w, p.k[1]);
+  q = fma2(q, w, p.k[0]);
   return fma2(S, q, add);
 }
-__device__ __forceinline__ float2 cap_short4(float2 S, const CapPoly& p, float2 add) {
-  const float2 w = mul2(S, S);
-  float2 q = fma2(p.k4[4], w, p.k4[3]);
-  q = fma2(q, w, p.k4[2]);
-  q = fma2(q, w, p.k4[1]);
-  q = fma2(q, w, p.k4[0]);
-  return fma2(S, q, add);
+__device__ __forceinline__ float2 cap_near(float2 S, const CapPoly& p, float2 add) {
+  const float2 x = mul2(S, both(p.c)), w = mul2(x, x);
+  float2 q = fma2(both(0x1.fb1946p-7f), w, both(-0x1.aad0b8p-5f));
+  q = fma2(q, w, both(0x1.1097a4p-3f));
+  q = fma2(q, w, both(-0x1.5552a6p-2f));
+  q = fma2(q, w, both(0x1.fffffep-1f));
+  return fma2(mul2(x, both(p.a)), q, add);
 }
-
-// The same for any S.
 __device__ __forceinline__ float2 cap_any(float2 S, const CapPoly& p, float2 add) {
-  const float2 z = mul2(S, both(p.inner));
+  const float2 z = mul2(S, both(p.c * (2.0f * kLog2e)));
   float2 e, r;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.x) : "f"(z.x));
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.y) : "f"(z.y));
   e = add2(e, both(1.0f));
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.x) : "f"(e.x));
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.y) : "f"(e.y));
-  return fma2(r, both(-2.0f * p.outer), add2(add, both(p.outer)));
+  return fma2(r, both(-2.0f * p.a), add2(add, both(p.a)));
 }
 
 // S -> a * tanh(c S) in place.
@@ -170,9 +169,9 @@ __device__ __forceinline__ void cap_scores(float2 (&x)[N], const CapPoly& p) {
     hi = max3(hi, x[i].x, x[i].y);
     lo = min3(lo, x[i].x, x[i].y);
   }
-  if (__all_sync(0xFFFFFFFFu, hi <= p.limit4 && lo >= -p.limit4)) {
+  if (__all_sync(0xFFFFFFFFu, hi <= p.near && lo >= -p.near)) {
 #pragma unroll
-    for (int i = 0; i < N; ++i) x[i] = cap_short4(x[i], p, both(0.0f));
+    for (int i = 0; i < N; ++i) x[i] = cap_near(x[i], p, both(0.0f));
   } else {
 #pragma unroll
     for (int i = 0; i < N; ++i) x[i] = cap_any(x[i], p, both(0.0f));

@@ -269,3 +269,28 @@ def test_capture_and_another_stream(cuda_lib):
     weights.zero_()
     graph.replay()
     batch.check(scoring, weights, np.zeros((2, 2, 304), np.float32))
+
+
+@pytest.mark.parametrize("softcap", [2.0 ** -20, 2.0 ** -6, 1.0, 6.0, 2.0 ** 20])
+def test_caps_of_every_size(cuda_lib, softcap):
+    batch = Batch([40, 300], 8, 2, seed=17, q_size=2.0)
+    batch.decode(kv.Scoring(softcap=softcap))
+    batch.check(kv.Scoring(softcap=softcap))
+
+
+def test_outputs_stay_inside_their_buffers(cuda_lib):
+    from test_gpu_canary import Guarded
+
+    batch = Batch([0, 33, 400, 17], 10, 2, seed=18)
+    out, lse = Guarded((4, 10, 128), torch.bfloat16), Guarded((4, 10), torch.float32)
+    weights = Guarded((4, 2, 401), torch.float32)
+    weights.t.zero_()
+    n = kv.nvfp4kv_decode_weights_workspace_size(batch.cache, 4, 10, batch.cache.num_pages)
+    ws = Guarded((n,), torch.uint8)
+    scoring = kv.Scoring(softcap=10.0, window=40, sinks=3)
+    kv.nvfp4kv_decode_attention_weights(batch.cache, batch.q, out.t, batch.pt, batch.sl, SCALE, weights.t, ws.t,
+                                        scoring=scoring, decay=0.5, lse=lse.t, device_status=batch.status)
+    batch.out, batch.lse = out.t, lse.t
+    batch.check(scoring, weights.t, np.zeros((4, 2, 401), np.float32), 0.5)
+    for g in (out, lse, weights, ws):
+        assert g.intact()

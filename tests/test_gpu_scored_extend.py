@@ -226,3 +226,27 @@ def test_capture_and_another_stream(cuda_lib):
     graph.replay()
     torch.cuda.synchronize()
     assert torch.equal(case.out, want)
+
+
+def test_rows_out_of_sight_may_hold_anything(cuda_lib):
+    # rows that no query sees (between the sinks and the window, before the
+    # documents) are NaN bytes, in tiles that others make visible
+    case = Case([600, 300], [9, 40], 4, 1, seed=30)
+    scoring = kv.Scoring(window=50, sinks=4)
+    docs = [0] * 9 + [170] * 40
+    r0, r1 = int(case.first[0]), int(case.first[1])
+    hidden = np.r_[r0 + 4:r0 + 600 - 49, r1:r1 + 170, r1 + 174:r1 + 300 - 49]
+    case.gpu[1][dev(hidden)] = 0x7F
+    case.gpu[2][dev(hidden)] = 0x7F
+    for sc in (scoring, kv.Scoring(window=50, sinks=4, softcap=20.0), kv.Scoring(window=50, sinks=4, slopes=SLOPES(4))):
+        case.out.fill_(float("nan"))
+        case.run(sc, docs=docs)
+        case.check(sc, docs=docs)
+
+
+@pytest.mark.parametrize("softcap", [2.0 ** -20, 2.0 ** -6, 1.0, 6.0, 2.0 ** 20])
+def test_caps_of_every_size(cuda_lib, softcap):
+    # all scores far beyond the cap, around it (each form of the cap), far inside it
+    case = Case([200], [70], 4, 2, seed=31, q_size=2.0)
+    case.run(kv.Scoring(softcap=softcap))
+    case.check(kv.Scoring(softcap=softcap))

@@ -95,6 +95,10 @@ def test_eviction_refusals(lib):
     assert call(a2=0) == INVALID and call(a6=0) == INVALID and call(a4=-1) == INVALID
     assert call(a4=1, a12=None) == INVALID and call(a4=1, a10=None) == INVALID and call(a4=1, a5=6) == INVALID
     assert call(a4=1, a2=1 << 27) == UNSUPPORTED                               # tokens past 32 bits
+    assert call(a4=1, a1=64, a10=64) == INVALID                                # packed into the old pages
+    assert call(a4=1, a5=4096, a13=4096, a10=64) == INVALID                    # kept sums over the old ones
+    assert call(a4=1, a5=4096, a13=4096 + 4 * (2 * 128 - 1), a10=64) == INVALID
+    assert call(a4=1, a5=4096, a13=4096 - 4 * (2 * 64 - 1), a10=64) == INVALID
     assert call(a0=ctypes.byref(_cache(page_size=32))) == UNSUPPORTED
 
 
