@@ -295,8 +295,8 @@ def _check_tensor(name: str, x, dtype, shape) -> None:
 
 def _check_device(name: str, x) -> None:
     """x lives on the current device, where the call's kernels run; raises ValueError."""
-    if x.get_device() != _types().cuda.current_device():
-        raise ValueError(f"{name}: on {x.device}, but the current device is {_types().cuda.current_device()}")
+    if x.get_device() != _torch._C._cuda_getDevice():  # (current_device() without its lazy set-up: x is on a GPU)
+        raise ValueError(f"{name}: on {x.device}, but the current device is {_torch._C._cuda_getDevice()}")
 
 
 def _shape(name: str, x, dims: int):
