@@ -503,7 +503,8 @@ int nvfp4kv_decode_weights_workspace_size(const nvfp4kv_cache* cache, int32_t ba
  *                visible key is zeros
  *   lse          device fp32 [total_q][num_q_heads], or NULL; -inf for such a row
  * Workspace rows that no query of a block of rows sees are not read, so they
- * may hold anything.  A prefix of more than 2^31 - 256 keys with its chunk is cut
+ * may hold anything; rows that some query of it sees must be finite, for the
+ * other queries of the block, too (a NaN times a weight of 0).  A prefix of more than 2^31 - 256 keys with its chunk is cut
  * with NVFP4KV_DEVERR_LENGTH.  Other arguments, limits and errors as in
  * nvfp4kv_extend_attention. */
 int nvfp4kv_extend_attention_scored(const void* q_bf16, const int64_t* cu_q, int32_t max_q_len,
@@ -539,7 +540,8 @@ int nvfp4kv_extend_attention_scored(const void* q_bf16, const int64_t* cu_q, int
  *   kept_weights    device fp32 [batch][num_kv_heads][kept_stride], or NULL:
  *                   weights[kept], zeros from n to budget; kept_stride >= budget.
  *                   Must not overlap weights
- *   new_lens        device int32 [batch], or NULL: n.  May be seq_lens itself
+ *   new_lens        device int32 [batch], or NULL: n.  May be seq_lens itself, not
+ *                   overlap it otherwise
  * A source page id out of range reads as zeros, a destination page id out of
  * range is not written, both with NVFP4KV_DEVERR_PAGE.  Enqueues two kernels;
  * needs no workspace. */

@@ -437,6 +437,10 @@ int nvfp4kv_evict(const nvfp4kv_cache* cache, const int32_t* page_table, int32_t
   const float* const kept_end = kept_weights ? kept_weights + pairs * kept_stride : kept_weights;
   if (dst_page_table == page_table || (kept_weights && kept_weights < weights_end && weights < kept_end))
     return NVFP4KV_ERR_INVALID_ARGUMENT;
+  // new_lens may be seq_lens (min(min(L, budget), budget) = min(L, budget)), but at an offset one
+  // sequence's new length would be another's old one
+  if (new_lens && new_lens != seq_lens && new_lens < seq_lens + batch && seq_lens < new_lens + batch)
+    return NVFP4KV_ERR_INVALID_ARGUMENT;
   int nsm = 0;
   if ((st = current_num_sms(&nsm)) != NVFP4KV_OK) return st;
   return cuda_status(nvfp4kv::launch_evict(*cache, page_table, max_pages_per_seq, seq_lens, batch, weights,

@@ -147,3 +147,10 @@ def test_reference_attention_matches_torch():
     np.testing.assert_allclose(got["out"], torch.softmax(torch.from_numpy(x), 0).numpy() @ V, rtol=1e-10, atol=1e-12)
     empty = attend(q, K, V, np.zeros(50, bool), np.zeros(50), 0.1)
     assert not empty["out"].any() and empty["lse"] == -np.inf
+
+
+def test_eviction_refuses_lengths_at_an_offset(lib):
+    cs = ctypes.byref(_cache())
+    call = _call(lib.nvfp4kv_evict,
+                 [cs, 64, 8, 4096, 3, 1 << 20, 128, 64, 4, 16, 128, 4, 4, None, 0, 4, None, None])
+    assert call(a15=4100) == INVALID and call(a15=4096 - 8) == INVALID
