@@ -285,8 +285,9 @@ def _types():
 
 
 def _check_tensor(name: str, x, dtype, shape) -> None:
-    """x is a contiguous GPU tensor of this dtype and shape (a tuple); raises ValueError."""
+    """x is a contiguous tensor of this dtype and shape (a tuple) on the current GPU; raises ValueError."""
     if x is not None and x.dtype is dtype and x.is_cuda and x.shape == shape and x.is_contiguous():
+        _check_device(name, x)
         return
     what = "None" if x is None else (f"{x.dtype} {tuple(x.shape)} on {x.device}"
                                      f"{'' if x.is_contiguous() else ' (not contiguous)'}")
@@ -295,8 +296,9 @@ def _check_tensor(name: str, x, dtype, shape) -> None:
 
 def _check_device(name: str, x) -> None:
     """x lives on the current device, where the call's kernels run; raises ValueError."""
-    if x.get_device() != _torch._C._cuda_getDevice():  # (current_device() without its lazy set-up: x is on a GPU)
-        raise ValueError(f"{name}: on {x.device}, but the current device is {_torch._C._cuda_getDevice()}")
+    current = _types()._C._cuda_getDevice()  # (current_device() without its lazy set-up: x is on a GPU)
+    if x.get_device() != current:
+        raise ValueError(f"{name}: on {x.device}, but the current device is {current}")
 
 
 def _shape(name: str, x, dims: int):
@@ -320,7 +322,6 @@ def _check_decode(cache: "Cache", q, out, page_table, seq_lens, lse):
     _check_tensor("seq_lens", seq_lens, t.int32, (B,))
     if lse is not None:
         _check_tensor("lse", lse, t.float32, (B, Hq))
-    _check_device("q", q)
     return B, Hq, maxp
 
 
@@ -400,13 +401,12 @@ def nvfp4kv_extend_attention_scored(q, cu_q, max_q_len: int, ws_k, ws_v, cu_pref
         _check_tensor("doc_starts", doc_starts, t.int32, (n,))
     if lse is not None:
         _check_tensor("lse", lse, t.float32, (n, hq))
-    _check_device("q", q)
     _check("nvfp4kv_extend_attention_scored",
            _L().nvfp4kv_extend_attention_scored(_ptr(q), _ptr(cu_q), int(max_q_len), _ptr(ws_k), _ptr(ws_v),
                                                 _ptr(cu_prefix), _ptr(prefix_lens), B, rows, hq, hkv, HEAD_DIM,
-                                                float(k_ws_scale), float(v_ws_scale), float(softmax_scale), _scoring(scoring, hq), _ptr(full_lens),
-                                                _ptr(doc_starts), _ptr(out), _ptr(lse), _ptr(device_status),
-                                                _stream(stream)))
+                                                float(k_ws_scale), float(v_ws_scale), float(softmax_scale),
+                                                _scoring(scoring, hq), _ptr(full_lens), _ptr(doc_starts), _ptr(out), _ptr(lse),
+                                                _ptr(device_status), _stream(stream)))
 
 
 def nvfp4kv_evict(cache: "Cache", page_table, seq_lens, weights, budget: int, first: int, recent: int,
@@ -432,7 +432,6 @@ def nvfp4kv_evict(cache: "Cache", page_table, seq_lens, weights, budget: int, fi
         _check_tensor("kept_weights", kept_weights, t.float32, (B, hkv, kept_stride))
     if new_lens is not None:
         _check_tensor("new_lens", new_lens, t.int32, (B,))
-    _check_device("weights", weights)
     c = cache.c_struct()
     _check("nvfp4kv_evict",
            _L().nvfp4kv_evict(ctypes.byref(c), _ptr(page_table), maxp, _ptr(seq_lens), B, _ptr(weights), stride,

@@ -154,3 +154,35 @@ def test_eviction_refuses_lengths_at_an_offset(lib):
     call = _call(lib.nvfp4kv_evict,
                  [cs, 64, 8, 4096, 3, 1 << 20, 128, 64, 4, 16, 128, 4, 4, None, 0, 4, None, None])
     assert call(a15=4100) == INVALID and call(a15=4096 - 8) == INVALID
+
+
+def test_bindings_refuse_tensors_of_another_gpu(monkeypatch):
+    class OnGpu:
+        """What the checks look at of a tensor, on GPU `gpu`."""
+        is_cuda = True
+
+        def __init__(self, dtype, shape, gpu):
+            self.dtype, self.shape, self.gpu, self.device = dtype, shape, gpu, f"cuda:{gpu}"
+
+        def dim(self):
+            return len(self.shape)
+
+        def is_contiguous(self):
+            return True
+
+        def get_device(self):
+            return self.gpu
+
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0, raising=False)
+    c = kv.Cache(0x10000, 4, 2)
+    i32, bf16, f32 = torch.int32, torch.bfloat16, torch.float32
+    decode = [(bf16, (1, 8, 128)), (bf16, (1, 8, 128)), (i32, (1, 4)), (i32, (1,))]
+    evict = [(i32, (1, 4)), (i32, (1,)), (f32, (1, 2, 64)), (i32, (1, 4)), (i32, (1, 2, 16))]
+    for k in range(4):
+        t = [OnGpu(*a, gpu=int(i == k)) for i, a in enumerate(decode)]
+        with pytest.raises(ValueError, match="on cuda:1"):
+            kv.nvfp4kv_decode_attention_scored(c, *t, 0.1, None, workspace_bytes=0)
+    for k in range(5):
+        t = [OnGpu(*a, gpu=int(i == k)) for i, a in enumerate(evict)]
+        with pytest.raises(ValueError, match="on cuda:1"):
+            kv.nvfp4kv_evict(c, t[0], t[1], t[2], 16, 0, 0, t[3], t[4])
