@@ -8,18 +8,23 @@
 //   kept key: three passes over shared memory (11, 11 and 10 bits), each a
 //   histogram of its own tokens whose bins that are not empty every CTA adds to
 //   the first CTA's totals (distributed shared memory; few bins hold anything),
-//   which finds the threshold's bin and tells the others.  Equal keys go to the lower index: with g tokens above and
-//   e tokens equal to the threshold before it, a kept token lands at place
-//   g + min(e, equal ones still wanted), so one ordered count over the cluster
-//   gives every destination and the list comes out in token order.
-//   Bytes: 4 read per token, 8 written per kept token; a few microseconds of
-//   latency per pass otherwise.
+//   which finds the threshold's bin and tells the others.  Equal keys go to the
+//   lower index: with g tokens above and e tokens equal to the threshold before
+//   it, a kept token lands at place g + min(e, equal ones still wanted), so one
+//   ordered count over the cluster gives every destination and the list comes out
+//   in token order.
+//   Bytes: 4 read per token, 8 written per kept token.  Bound by the latency of
+//   its passes: 18 us for 256 pairs of 8193 tokens (8.4 MB read), 31 us for 32
+//   pairs of 100K to 131K (14.8 MB), cold.
 // pack_kernel: one warp per destination page-head, launched as the programmatic
 //   dependent of the first.  It gathers 16 tokens' K rows and scales, their
 //   nibbles of V's token-pair bytes and their V scale bytes, all loads in
 //   flight together, and writes the page-head whole.  HBM-bound: 144 bytes in
 //   and out per kept token, plus what the 32-byte sectors drag along (a V byte
-//   holds two tokens, a V scale sector the scales of two blocks).
+//   holds two tokens, a V scale sector the scales of two blocks).  2048 of 8193
+//   tokens kept, 256 pairs: 45 us, 147.8 MB read and 39.4 MB written back to DRAM.
+//   With the packing in the selection's launch (a cluster packs its own pair) the
+//   whole eviction took 73 us instead of 69: fewer warps gather at a time.
 #include "nvfp4kv_device.cuh"
 #include "nvfp4kv_launch.h"
 
@@ -464,7 +469,10 @@ cudaError_t launch_evict(const nvfp4kv_cache& c, const int32_t* page_table, int3
   });
   if (e != cudaSuccess) return e;
   // as many CTAs per pair as its keys need to fit shared memory, and more while
-  // SMs would stay empty and a CTA keeps 2048 tokens or more
+  // SMs would stay empty and a CTA keeps 2048 tokens or more.  Selection with 1,
+  // 2, 4, 8 CTAs a pair: 32 pairs of 16384 tokens 14.9, 12.9, 11.5 (taken), 13.2
+  // us; 256 pairs of 8193 16.0 (taken), 27.6, 47.7, 93.7; 32 pairs of 131072 163,
+  // 102, 57 (keys read again in each pass), 26.0 (taken)
   const int64_t most = weight_stride < (int64_t)max_pages * kPage ? weight_stride : (int64_t)max_pages * kPage;
   int cluster = 1;
   while (cluster < kMaxCluster && (most > (int64_t)cluster * kKeyCap ||

@@ -29,6 +29,10 @@
 // cycles.
 // TMEM (512 columns): S_0 0-127, S_1 128-255 (P_t in the first 64 of S_t),
 // O_0 256-383, O_1 384-511.
+// What bounds it: the chain softmax -> P V -> S of a tile, which the other tile's
+// hides in part, then the FMA pipe where scores are capped.  16384 + 2048 tokens,
+// 64 / 8 heads: 1.23 ms capped, 0.98 ms plain (0.49 and 0.61 of the measured bf16
+// rate; nvfp4kv_extend_attention, without any scoring, 1.49 ms).
 // Key tiles that no query of the CTA sees are skipped, and workspace rows that
 // none sees read as zero.  Every wait is bounded: a stalled pipeline flags
 // NVFP4KV_DEVERR_TIMEOUT and drains its MMAs before the TMEM is freed.
