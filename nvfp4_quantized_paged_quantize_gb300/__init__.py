@@ -262,12 +262,12 @@ class Scoring:
         return _CScoring(float(self.softcap), int(self.window), int(self.sinks), _ptr(self.slopes))
 
 
-def _scoring(scoring, hq: int):
+def _scoring(scoring, hq: int, gpu: int):
     """The C struct of a Scoring (None stays NULL); its slopes are checked against the query heads."""
     if scoring is None:
         return None
     if scoring.slopes is not None:
-        _check_tensor("slopes", scoring.slopes, _types().float32, (hq,))
+        _check_tensor("slopes", scoring.slopes, _types().float32, (hq,), gpu)
     return ctypes.byref(scoring.c_struct())
 
 
@@ -284,21 +284,26 @@ def _types():
     return _torch
 
 
-def _check_tensor(name: str, x, dtype, shape) -> None:
-    """x is a contiguous tensor of this dtype and shape (a tuple) on the current GPU; raises ValueError."""
-    if x is not None and x.dtype is dtype and x.is_cuda and x.shape == shape and x.is_contiguous():
-        _check_device(name, x)
+def _current_gpu(x) -> int:
+    """The current device, where a call's kernels run; one that no tensor is on if x is not on a GPU."""
+    # (current_device() without its lazy set-up: x is on a GPU)
+    return _types()._C._cuda_getDevice() if x.is_cuda else -2
+
+
+def _check_tensor(name: str, x, dtype, shape, gpu: int) -> None:
+    """x is a contiguous tensor of this dtype and shape (a tuple) on this GPU; raises ValueError."""
+    if x is not None and x.dtype is dtype and x.get_device() == gpu and x.shape == shape and x.is_contiguous():
         return
     what = "None" if x is None else (f"{x.dtype} {tuple(x.shape)} on {x.device}"
                                      f"{'' if x.is_contiguous() else ' (not contiguous)'}")
-    raise ValueError(f"{name}: expected a contiguous {dtype} GPU tensor of shape {shape}, got {what}")
+    where = f" on the current device, cuda:{gpu}" if gpu >= 0 else ""
+    raise ValueError(f"{name}: expected a contiguous {dtype} GPU tensor of shape {shape}{where}, got {what}")
 
 
-def _check_device(name: str, x) -> None:
-    """x lives on the current device, where the call's kernels run; raises ValueError."""
-    current = _types()._C._cuda_getDevice()  # (current_device() without its lazy set-up: x is on a GPU)
-    if x.get_device() != current:
-        raise ValueError(f"{name}: on {x.device}, but the current device is {current}")
+def _check_memory(name: str, x, gpu: int) -> None:
+    """x, where it is a tensor and not an address, lies on this GPU; raises ValueError."""
+    if hasattr(x, "get_device") and x.get_device() != gpu:
+        raise ValueError(f"{name}: expected memory of the current device, cuda:{gpu}, got {x.device}")
 
 
 def _shape(name: str, x, dims: int):
@@ -309,20 +314,22 @@ def _shape(name: str, x, dims: int):
     return x.shape
 
 
-def _check_decode(cache: "Cache", q, out, page_table, seq_lens, lse):
-    """Shapes and types of a scored decode's tensors; returns (batch, query heads, page-table columns)."""
+def _check_decode(cache: "Cache", q, out, page_table, seq_lens, lse, workspace):
+    """Checks a scored decode's tensors; returns (batch, query heads, page-table columns, the current device)."""
     if cache.mxfp4:
         raise ValueError("the cache holds MXFP4 page-heads; the scored decodes read NVFP4 ones")
     t = _types()
     B, Hq, _ = _shape("q", q, 3)
-    maxp = _shape("page_table", page_table, 2)[1]
-    _check_tensor("q", q, t.bfloat16, (B, Hq, HEAD_DIM))
-    _check_tensor("out", out, t.bfloat16, (B, Hq, HEAD_DIM))
-    _check_tensor("page_table", page_table, t.int32, (B, maxp))
-    _check_tensor("seq_lens", seq_lens, t.int32, (B,))
+    maxp, gpu = _shape("page_table", page_table, 2)[1], _current_gpu(q)
+    _check_tensor("q", q, t.bfloat16, (B, Hq, HEAD_DIM), gpu)
+    _check_tensor("out", out, t.bfloat16, (B, Hq, HEAD_DIM), gpu)
+    _check_tensor("page_table", page_table, t.int32, (B, maxp), gpu)
+    _check_tensor("seq_lens", seq_lens, t.int32, (B,), gpu)
     if lse is not None:
-        _check_tensor("lse", lse, t.float32, (B, Hq))
-    return B, Hq, maxp
+        _check_tensor("lse", lse, t.float32, (B, Hq), gpu)
+    _check_memory("cache.pages", cache.pages, gpu)
+    _check_memory("workspace", workspace, gpu)
+    return B, Hq, maxp, gpu
 
 
 def nvfp4kv_decode_attention_scored(cache: "Cache", q, out, page_table, seq_lens, softmax_scale: float, workspace,
@@ -330,13 +337,13 @@ def nvfp4kv_decode_attention_scored(cache: "Cache", q, out, page_table, seq_lens
                                     workspace_bytes: int | None = None) -> None:
     """Paged decode attention with a scoring (cap, distance bias, window with sinks): q bf16 [B, Hq, 128], out
     bf16 [B, Hq, 128], lse fp32 [B, Hq] or None; the rest as nvfp4kv_decode_attention."""
-    B, Hq, maxp = _check_decode(cache, q, out, page_table, seq_lens, lse)
+    B, Hq, maxp, gpu = _check_decode(cache, q, out, page_table, seq_lens, lse, workspace)
     if workspace_bytes is None:
         workspace_bytes = workspace.numel() * workspace.element_size()
     c = cache.c_struct()
     _check("nvfp4kv_decode_attention_scored",
            _L().nvfp4kv_decode_attention_scored(ctypes.byref(c), _ptr(q), _ptr(out), _ptr(lse), _ptr(page_table), maxp,
-                                                _ptr(seq_lens), B, Hq, float(softmax_scale), _scoring(scoring, Hq),
+                                                _ptr(seq_lens), B, Hq, float(softmax_scale), _scoring(scoring, Hq, gpu),
                                                 _ptr(workspace), workspace_bytes, _ptr(device_status),
                                                 _stream(stream)))
 
@@ -358,9 +365,9 @@ def nvfp4kv_decode_attention_weights(cache: "Cache", q, out, page_table, seq_len
     """nvfp4kv_decode_attention_scored that also updates weights (fp32 [B, Hkv, tokens]): each cached token's
     sum becomes decay * sum + the softmax weight it got from the KV head's query heads.  max_total_pages bounds
     the batch's cached pages (default: the cache's num_pages, right where sequences share no page)."""
-    B, Hq, maxp = _check_decode(cache, q, out, page_table, seq_lens, lse)
+    B, Hq, maxp, gpu = _check_decode(cache, q, out, page_table, seq_lens, lse, workspace)
     stride = _shape("weights", weights, 3)[2]
-    _check_tensor("weights", weights, _types().float32, (B, cache.num_kv_heads, stride))
+    _check_tensor("weights", weights, _types().float32, (B, cache.num_kv_heads, stride), gpu)
     if workspace_bytes is None:
         workspace_bytes = workspace.numel() * workspace.element_size()
     if max_total_pages is None:
@@ -369,7 +376,7 @@ def nvfp4kv_decode_attention_weights(cache: "Cache", q, out, page_table, seq_len
     _check("nvfp4kv_decode_attention_weights",
            _L().nvfp4kv_decode_attention_weights(ctypes.byref(c), _ptr(q), _ptr(out), _ptr(lse), _ptr(page_table),
                                                  maxp, _ptr(seq_lens), B, Hq, float(softmax_scale),
-                                                 _scoring(scoring, Hq), _ptr(weights), stride,
+                                                 _scoring(scoring, Hq, gpu), _ptr(weights), stride,
                                                  float(decay), int(max_total_pages), _ptr(workspace), workspace_bytes,
                                                  _ptr(device_status), _stream(stream)))
 
@@ -385,28 +392,28 @@ def nvfp4kv_extend_attention_scored(q, cu_q, max_q_len: int, ws_k, ws_v, cu_pref
     n, hq, _ = _shape("q", q, 3)
     B = _shape("prefix_lens", prefix_lens, 1)[0]
     rows, hkv, _ = _shape("ws_k", ws_k, 3)
-    sequences = _shape("cu_prefix", cu_prefix, 1)[0]
+    sequences, gpu = _shape("cu_prefix", cu_prefix, 1)[0], _current_gpu(q)
     if sequences < B:
         raise ValueError(f"cu_prefix: {sequences} entries for {B} sequences")
-    _check_tensor("q", q, t.bfloat16, (n, hq, HEAD_DIM))
-    _check_tensor("out", out, t.bfloat16, (n, hq, HEAD_DIM))
-    _check_tensor("prefix_lens", prefix_lens, t.int32, (B,))
-    _check_tensor("cu_q", cu_q, t.int64, (B + 1,))
-    _check_tensor("cu_prefix", cu_prefix, t.int64, (sequences,))
-    _check_tensor("ws_k", ws_k, t.uint8, (rows, hkv, HEAD_DIM))
-    _check_tensor("ws_v", ws_v, t.uint8, (rows, hkv, HEAD_DIM))
+    _check_tensor("q", q, t.bfloat16, (n, hq, HEAD_DIM), gpu)
+    _check_tensor("out", out, t.bfloat16, (n, hq, HEAD_DIM), gpu)
+    _check_tensor("prefix_lens", prefix_lens, t.int32, (B,), gpu)
+    _check_tensor("cu_q", cu_q, t.int64, (B + 1,), gpu)
+    _check_tensor("cu_prefix", cu_prefix, t.int64, (sequences,), gpu)
+    _check_tensor("ws_k", ws_k, t.uint8, (rows, hkv, HEAD_DIM), gpu)
+    _check_tensor("ws_v", ws_v, t.uint8, (rows, hkv, HEAD_DIM), gpu)
     if full_lens is not None:
-        _check_tensor("full_lens", full_lens, t.int32, (B,))
+        _check_tensor("full_lens", full_lens, t.int32, (B,), gpu)
     if doc_starts is not None:
-        _check_tensor("doc_starts", doc_starts, t.int32, (n,))
+        _check_tensor("doc_starts", doc_starts, t.int32, (n,), gpu)
     if lse is not None:
-        _check_tensor("lse", lse, t.float32, (n, hq))
+        _check_tensor("lse", lse, t.float32, (n, hq), gpu)
     _check("nvfp4kv_extend_attention_scored",
            _L().nvfp4kv_extend_attention_scored(_ptr(q), _ptr(cu_q), int(max_q_len), _ptr(ws_k), _ptr(ws_v),
                                                 _ptr(cu_prefix), _ptr(prefix_lens), B, rows, hq, hkv, HEAD_DIM,
                                                 float(k_ws_scale), float(v_ws_scale), float(softmax_scale),
-                                                _scoring(scoring, hq), _ptr(full_lens), _ptr(doc_starts), _ptr(out), _ptr(lse),
-                                                _ptr(device_status), _stream(stream)))
+                                                _scoring(scoring, hq, gpu), _ptr(full_lens), _ptr(doc_starts),
+                                                _ptr(out), _ptr(lse), _ptr(device_status), _stream(stream)))
 
 
 def nvfp4kv_evict(cache: "Cache", page_table, seq_lens, weights, budget: int, first: int, recent: int,
@@ -420,18 +427,19 @@ def nvfp4kv_evict(cache: "Cache", page_table, seq_lens, weights, budget: int, fi
     t = _types()
     B, hkv = _shape("seq_lens", seq_lens, 1)[0], cache.num_kv_heads
     maxp, dst_maxp = _shape("page_table", page_table, 2)[1], _shape("dst_page_table", dst_page_table, 2)[1]
-    stride = _shape("weights", weights, 3)[2]
-    _check_tensor("seq_lens", seq_lens, t.int32, (B,))
-    _check_tensor("page_table", page_table, t.int32, (B, maxp))
-    _check_tensor("weights", weights, t.float32, (B, hkv, stride))
-    _check_tensor("dst_page_table", dst_page_table, t.int32, (B, dst_maxp))
-    _check_tensor("kept", kept, t.int32, (B, hkv, budget))
+    stride, gpu = _shape("weights", weights, 3)[2], _current_gpu(weights)
+    _check_tensor("seq_lens", seq_lens, t.int32, (B,), gpu)
+    _check_tensor("page_table", page_table, t.int32, (B, maxp), gpu)
+    _check_tensor("weights", weights, t.float32, (B, hkv, stride), gpu)
+    _check_tensor("dst_page_table", dst_page_table, t.int32, (B, dst_maxp), gpu)
+    _check_tensor("kept", kept, t.int32, (B, hkv, budget), gpu)
     kept_stride = 0
     if kept_weights is not None:
         kept_stride = _shape("kept_weights", kept_weights, 3)[2]
-        _check_tensor("kept_weights", kept_weights, t.float32, (B, hkv, kept_stride))
+        _check_tensor("kept_weights", kept_weights, t.float32, (B, hkv, kept_stride), gpu)
     if new_lens is not None:
-        _check_tensor("new_lens", new_lens, t.int32, (B,))
+        _check_tensor("new_lens", new_lens, t.int32, (B,), gpu)
+    _check_memory("cache.pages", cache.pages, gpu)
     c = cache.c_struct()
     _check("nvfp4kv_evict",
            _L().nvfp4kv_evict(ctypes.byref(c), _ptr(page_table), maxp, _ptr(seq_lens), B, _ptr(weights), stride,

@@ -180,9 +180,15 @@ def test_bindings_refuse_tensors_of_another_gpu(monkeypatch):
     evict = [(i32, (1, 4)), (i32, (1,)), (f32, (1, 2, 64)), (i32, (1, 4)), (i32, (1, 2, 16))]
     for k in range(4):
         t = [OnGpu(*a, gpu=int(i == k)) for i, a in enumerate(decode)]
-        with pytest.raises(ValueError, match="on cuda:1"):
+        with pytest.raises(ValueError, match="got .* on cuda:1"):
             kv.nvfp4kv_decode_attention_scored(c, *t, 0.1, None, workspace_bytes=0)
     for k in range(5):
         t = [OnGpu(*a, gpu=int(i == k)) for i, a in enumerate(evict)]
-        with pytest.raises(ValueError, match="on cuda:1"):
+        with pytest.raises(ValueError, match="got .* on cuda:1"):
             kv.nvfp4kv_evict(c, t[0], t[1], t[2], 16, 0, 0, t[3], t[4])
+    # the pool and the workspace
+    other, t = OnGpu(torch.uint8, (4, 2, 2304), 1), [OnGpu(*a, gpu=0) for a in decode]
+    with pytest.raises(ValueError, match="cache.pages: .* got cuda:1"):
+        kv.nvfp4kv_decode_attention_scored(kv.Cache(other, 4, 2), *t, 0.1, None, workspace_bytes=0)
+    with pytest.raises(ValueError, match="workspace: .* got cuda:1"):
+        kv.nvfp4kv_decode_attention_scored(c, *t, 0.1, other, workspace_bytes=0)
