@@ -136,50 +136,122 @@ __device__ __forceinline__ KeyRange key_range(const ScoredParams& p, int keys, i
   return r;
 }
 
-// The key tiles that some query of the CTA sees: those of the sinks (`lead` of
-// them, from tile `first` on), then those from the nearest key of any query's
-// window or document on (step i >= lead is tile i + skip).
-struct Visit {
-  int steps, first, lead, skip;
-  int low, sink_end, near, end;  // rows outside [low, sink_end) and [near, end) are seen by no query
-  __device__ __forceinline__ int tile(int i) const { return i < lead ? first + i : i + skip; }
+// The first n of 32 bits.
+__device__ __forceinline__ uint32_t first_bits(int n) { return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1u; }
+
+// Of keys at .. at + 31, those outside the range (bit c: key at + c).
+__device__ __forceinline__ uint32_t hidden_bits(const KeyRange& r, int at) {
+  return ~first_bits(r.end - at) |
+         (first_bits(r.near - at) & ~(first_bits(r.sink_end - at) & ~first_bits(r.low - at)));
+}
+
+// What the CTA's queries see, as the warps share it.  Without documents one
+// range holds what any of them sees (their windows follow one another); with
+// documents each query has its own, as the sinks of two documents may lie far
+// apart and no query sees what is between them.
+struct Sight {
+  KeyRange all;             // without documents
+  int ranges;               // 1, or one per query
+  int keys, full;           // the sequence's tokens, the positions that every query sees
+  int first_pos;            // of the queries
+  int row_low, row_high;    // keys outside have no row in the workspace
+  int steps;                // documents with sinks: the tiles to visit
+  int32_t doc[kRows];       // document starts of the queries
 };
 
-// For the queries of tokens [t0, t1] of a chunk behind a prefix of P tokens.
+__device__ __forceinline__ KeyRange sight_range(const ScoredParams& p, const Sight& s, int k) {
+  return p.doc_starts != nullptr ? key_range(p, s.keys, s.first_pos + k, s.full, s.doc[k]) : s.all;
+}
+
+// The tiles [first, last] that hold a range's sinks (none: last is -1).
+struct Tiles {
+  int first, last;
+};
+__device__ __forceinline__ Tiles sink_tiles(const KeyRange& r) {
+  const int stop = min(r.sink_end, r.end);
+  Tiles t;
+  t.first = r.low / kTileN;
+  t.last = stop > r.low ? (stop - 1) / kTileN : -1;
+  return t;
+}
+
+// The key tiles to visit: all from near_tile on (where the nearest key of any
+// query's window or document lies), and before it those that hold a sink.
+struct Visit {
+  int steps;      // one at least
+  int near_tile;
+  int lead;       // without documents: tiles [0, lead) hold the sinks
+};
+
+__device__ __forceinline__ bool document_sinks(const ScoredParams& p) {
+  return p.doc_starts != nullptr && p.window > 0 && p.sinks > 0;
+}
+
+// The first tile to visit from `from` on; warp-uniform.
+__device__ __forceinline__ int next_tile(const ScoredParams& p, const Visit& v, const Sight& s, int from, int lane) {
+  if (from >= v.near_tile) return from;
+  if (!document_sinks(p)) return from < v.lead ? from : v.near_tile;
+  int t = v.near_tile;
+  for (int k = lane; k < s.ranges; k += 32) {
+    const Tiles sinks = sink_tiles(sight_range(p, s, k));
+    if (sinks.last >= from) t = min(t, max(from, sinks.first));
+  }
+  return __reduce_min_sync(0xFFFFFFFFu, t);
+}
+
+// For the queries of tokens [t0, t1] of a chunk behind a prefix of P tokens
+// (every warp for itself; v.steps without the tiles of documents' sinks).  One
+// warp keeps the document starts.
 __device__ __forceinline__ Visit plan_visit(const ScoredParams& p, int64_t q0, int P, int keys, int t0, int t1,
-                                            int full, int lane) {
+                                            int full, KeyRange& all, int32_t* keep, int lane) {
   Visit v;
-  v.low = 0;
-  int low1 = 0;
-  v.near = p.window > 0 ? max(0, P + t0 - p.window + 1) : 0;
-  if (p.doc_starts != nullptr) {
-    // the queries' lowest and highest document start and nearest key (every warp for itself)
-    int l0 = INT32_MAX, l1 = 0, n0 = INT32_MAX;
-    for (int t = t0 + lane; t <= t1; t += 32) {
-      const KeyRange r = key_range(p, keys, P + t, full, __ldg(p.doc_starts + q0 + t));
-      l0 = min(l0, r.low);
-      l1 = max(l1, r.low);
-      n0 = min(n0, r.near);
-    }
-    v.low = __reduce_min_sync(0xFFFFFFFFu, l0);
-    low1 = __reduce_max_sync(0xFFFFFFFFu, l1);
-    v.near = __reduce_min_sync(0xFFFFFFFFu, n0);
-  }
-  v.end = key_range(p, keys, P + t1, full, 0).end;
-  v.sink_end = v.low;
-  const int last = (v.end - 1) / kTileN;
-  const int near_tile = min(v.near / kTileN, last);  // one tile at least
-  v.first = near_tile;
   v.lead = 0;
-  if (p.window > 0 && p.sinks > 0) {
-    v.sink_end = low1 + min(p.sinks, keys - low1);
-    v.first = min(v.low / kTileN, near_tile);
-    v.lead = min((v.sink_end - 1) / kTileN + 1, near_tile) - v.first;
-    if (v.lead < 0) v.lead = 0;
+  int last;
+  if (p.doc_starts == nullptr) {
+    all = key_range(p, keys, P + t1, full, 0);
+    all.near = key_range(p, keys, P + t0, full, 0).near;
+    last = (all.end - 1) / kTileN;
+    v.near_tile = all.near / kTileN;
+    v.lead = min(sink_tiles(all).last + 1, v.near_tile);
+  } else {
+    int first = INT32_MAX;
+    last = 0;
+    for (int t = t0 + lane; t <= t1; t += 32) {
+      const int doc = __ldg(p.doc_starts + q0 + t);
+      if (keep != nullptr) keep[t - t0] = doc;
+      const KeyRange r = key_range(p, keys, P + t, full, doc);
+      if (r.low < r.end) {  // (else the query sees nothing)
+        first = min(first, r.near);
+        last = max(last, r.end - 1);
+      }
+    }
+    last = __reduce_max_sync(0xFFFFFFFFu, last) / kTileN;
+    v.near_tile = min(__reduce_min_sync(0xFFFFFFFFu, first) / kTileN, last);
   }
-  v.skip = near_tile - v.lead;
-  v.steps = v.lead + last - near_tile + 1;
+  v.steps = v.lead + last - v.near_tile + 1;
   return v;
+}
+
+// How many tiles before near_tile hold a document's sinks (one warp's work):
+// run after run of tiles [t, stop] that sinks cover without a gap.
+__device__ __forceinline__ int count_sink_tiles(const ScoredParams& p, const Visit& v, const Sight& s, int lane) {
+  int count = 0;
+  for (int t = next_tile(p, v, s, 0, lane); t < v.near_tile;) {
+    int stop = t;
+    while (true) {
+      int reach = stop;
+      for (int k = lane; k < s.ranges; k += 32) {
+        const Tiles sinks = sink_tiles(sight_range(p, s, k));
+        if (sinks.first <= stop + 1) reach = max(reach, sinks.last);
+      }
+      reach = min(__reduce_max_sync(0xFFFFFFFFu, reach), v.near_tile - 1);
+      if (reach == stop) break;
+      stop = reach;
+    }
+    count += stop - t + 1;
+    t = next_tile(p, v, s, stop + 1, lane);
+  }
+  return count;
 }
 
 template <int kRegs>
@@ -209,9 +281,6 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity) {
   }
 }
 
-// The first n of 32 bits.
-__device__ __forceinline__ uint32_t first_bits(int n) { return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1u; }
-
 __device__ __forceinline__ void arrive(uint32_t bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
@@ -221,6 +290,7 @@ __global__ void __launch_bounds__(kThreads, 1) extend_scored_kernel(const Scored
   extern __shared__ __align__(1024) uint8_t smem[];
   __shared__ Barriers bars;
   __shared__ uint32_t s_tmem;
+  __shared__ Sight sight;
 
   // the broadcast tells the compiler that a warp's lanes take the same role
   const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
@@ -269,11 +339,32 @@ __global__ void __launch_bounds__(kThreads, 1) extend_scored_kernel(const Scored
       asm volatile("prefetch.global.L2 [%0];" ::"l"(q + 64));
     }
   }
-  const Visit v = plan_visit(p, q0, P, keys, t0, t1, full, lane);
+  KeyRange all = {};
+  const bool keeps = warp == kMmaWarp + 1;
+  const int64_t row0 = __ldg(p.cu_prefix + b);
+  Visit v = plan_visit(p, q0, P, keys, t0, t1, full, all, keeps ? sight.doc : nullptr, lane);
+  if (keeps) {
+    if (lane == 0) {
+      auto clamp_key = [](int64_t j) { return (int)(j < 0 ? 0 : (j > INT32_MAX ? INT32_MAX : j)); };
+      sight.all = all;
+      sight.ranges = p.doc_starts != nullptr ? t1 - t0 + 1 : 1;
+      sight.keys = keys;
+      sight.full = full;
+      sight.first_pos = P + t0;
+      sight.row_low = clamp_key(-row0);
+      sight.row_high = clamp_key(p.total_rows - row0);
+    }
+    __syncwarp();
+    if (document_sinks(p)) {
+      const int sinks = count_sink_tiles(p, v, sight, lane);
+      if (lane == 0) sight.steps = v.steps + sinks;
+    }
+  }
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
   const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, s_tmem, 0);
+  if (document_sinks(p)) v.steps = __shfl_sync(0xFFFFFFFFu, sight.steps, 0);
   const int G = p.group;
 
   if (warp >= kMmaWarp) {
@@ -354,36 +445,59 @@ __global__ void __launch_bounds__(kThreads, 1) extend_scored_kernel(const Scored
     const int lw = warp - kSoftmaxWarps, part = lane & 7;
     uint4 xk[8], xv[8];
     // this thread's first byte of key 0 in a workspace, and the bytes from key to key
-    const int64_t row0 = __ldg(p.cu_prefix + b), key_bytes = (int64_t)p.hkv * kHeadDim;
+    const int64_t key_bytes = (int64_t)p.hkv * kHeadDim;
     const int64_t key0 = (row0 * p.hkv + hk) * kHeadDim + part * 16;
-    // the keys to load: those some query sees and whose rows the workspace has
-    auto clamp_key = [](int64_t j) { return (int)(j < 0 ? 0 : (j > INT32_MAX ? INT32_MAX : j)); };
-    const int row_low = clamp_key(-row0), row_high = clamp_key(p.total_rows - row0);
-    if (min(v.near, v.sink_end > v.low ? v.low : v.near) < row_low || v.end > row_high)
-      flag_error(p.status, NVFP4KV_DEVERR_ROW);
-    const int near = max(v.near, row_low), low = max(v.low, row_low);
-    const int end = min(v.end, row_high), sink_end = min(v.sink_end, row_high);
-    auto load = [&](const uint8_t* ws, int i, uint4 (&x)[8]) {
-      const int jt = v.tile(i) * kTileN, j0 = jt + lw * 32 + (lane >> 3);
-      const uint8_t* src = ws + (key0 + j0 * key_bytes);
-      if (jt >= near && jt + kTileN <= end) {  // the whole tile
+    // Keys [whole_low, whole_high) are seen and have their rows, so that few tiles
+    // take the long way.  With documents: what the query with the most near keys
+    // sees, found while the first tile is on its way.
+    int whole_low = max(all.near, sight.row_low), whole_high = min(all.end, sight.row_high);
+    // of the warp's keys of a tile, those that some query sees and whose rows the workspace has
+    auto rows_to_load = [&](int tile) {
+      if (tile * kTileN >= whole_low && (tile + 1) * kTileN <= whole_high) return ~0u;
+      const int at = tile * kTileN + 32 * lw;
+      uint32_t seen = 0;
+      for (int k = lane; k < sight.ranges; k += 32) seen |= ~hidden_bits(sight_range(p, sight, k), at);
+      return __reduce_or_sync(0xFFFFFFFFu, seen) & first_bits(sight.row_high - at) & ~first_bits(sight.row_low - at);
+    };
+    int tile = next_tile(p, v, sight, 0, lane);
+    uint32_t rows = rows_to_load(tile);
+    auto load = [&](const uint8_t* ws, uint4 (&x)[8]) {
+      const uint8_t* src = ws + (key0 + (tile * kTileN + lw * 32 + (lane >> 3)) * key_bytes);
+      if (rows == ~0u) {
 #pragma unroll
         for (int g = 0; g < 8; ++g) {
           x[g] = __ldg(reinterpret_cast<const uint4*>(src));
           src += 4 * key_bytes;
         }
       } else {
+        const uint32_t mine = rows >> (lane >> 3);
 #pragma unroll
         for (int g = 0; g < 8; ++g) {
-          const int j = j0 + 4 * g;
-          const bool live = j < end && (j >= near || (j >= low && j < sink_end));
-          x[g] = live ? __ldg(reinterpret_cast<const uint4*>(src)) : make_uint4(0, 0, 0, 0);
+          x[g] = (mine >> (4 * g) & 1) ? __ldg(reinterpret_cast<const uint4*>(src)) : make_uint4(0, 0, 0, 0);
           src += 4 * key_bytes;
         }
       }
     };
-    load(p.ws_k, 0, xk);
-    load(p.ws_v, 0, xv);
+    load(p.ws_k, xk);
+    load(p.ws_v, xv);
+    {
+      KeyRange most = {0, 0, 0, 0};
+      bool missing = false;
+      for (int k = lane; k < sight.ranges; k += 32) {
+        const KeyRange r = sight_range(p, sight, k);
+        if (r.low >= r.end) continue;
+        if (r.end - r.near > most.end - most.near) most = r;
+        missing |= (r.sink_end > r.low ? r.low : r.near) < sight.row_low || r.end > sight.row_high;
+      }
+      if (missing) flag_error(p.status, NVFP4KV_DEVERR_ROW);
+      if (p.doc_starts != nullptr) {
+        const int keys_of = most.end - most.near, top = __reduce_max_sync(0xFFFFFFFFu, keys_of);
+        const int of = __ffs(__ballot_sync(0xFFFFFFFFu, keys_of == top)) - 1;
+        whole_low = __shfl_sync(0xFFFFFFFFu, most.near, of);
+        whole_high = min(whole_low + top, sight.row_high);
+        whole_low = max(whole_low, sight.row_low);
+      }
+    }
     bool ok = true;
     int s = 0;            // the ring slot
     uint32_t round = 1;   // the parity of its last release; its first use waits for none
@@ -417,8 +531,13 @@ __global__ void __launch_bounds__(kThreads, 1) extend_scored_kernel(const Scored
           reuse = true;
         }
         if (i + 1 < v.steps) {
-          if (w == 0) load(p.ws_k, i + 1, xk);
-          else load(p.ws_v, i + 1, xv);
+          if (w == 0) {
+            tile = next_tile(p, v, sight, tile + 1, lane);
+            rows = rows_to_load(tile);
+            load(p.ws_k, xk);
+          } else {
+            load(p.ws_v, xv);
+          }
         }
       }
     }
@@ -457,13 +576,15 @@ __global__ void __launch_bounds__(kThreads, 1) extend_scored_kernel(const Scored
     float m = -INFINITY;
     float2 l[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
     bool ok = true;
+    int key_tile = -1;
     for (int i = 0; i < v.steps; ++i) {
+      key_tile = next_tile(p, v, sight, key_tile + 1, lane);
       if (!warp_wait(bar_s, i & 1)) {
         ok = false;
         break;
       }
       tc::fence_after_sync();
-      const int kbase = v.tile(i) * kTileN;
+      const int kbase = key_tile * kTileN;
       // keys c of [low, sink) and [near, end) of this tile are visible to the row
       const int end = kr.end - kbase, low = kr.low - kbase, sink = kr.sink_end - kbase, near = kr.near - kbase;
       const bool masked = end < kTileN || (near > 0 && (low > 0 || sink < kTileN));
@@ -513,8 +634,7 @@ __global__ void __launch_bounds__(kThreads, 1) extend_scored_kernel(const Scored
         for (int at = 0; at < kTileN; at += 32) {
           uint32_t hidden = 0;  // bit c: key at + c
           if (any_masked) {
-            hidden = ~first_bits(end - at) |
-                     (first_bits(near - at) & ~(first_bits(sink - at) & ~first_bits(low - at)));
+            hidden = hidden_bits(kr, kbase + at);
             if (__all_sync(0xFFFFFFFFu, hidden == ~0u)) {
               gone |= 1u << (at / 32);
               continue;

@@ -250,3 +250,40 @@ def test_caps_of_every_size(cuda_lib, softcap):
     case = Case([200], [70], 4, 2, seed=31, q_size=2.0)
     case.run(kv.Scoring(softcap=softcap))
     case.check(kv.Scoring(softcap=softcap))
+
+
+UNSEEN = {
+    # two documents in a block of rows: the first one's middle is behind its window
+    "two_documents": ([600], [40], [[0] * 20 + [620] * 20], dict(window=50, sinks=4)),
+    # padding between documents, hidden from itself too by a start behind every token
+    "padding": ([30], [90], [[0] * 25 + [2 ** 31 - 1] * 15 + [70] * 50], {}),
+    "padding_window": ([300], [90], [[0] * 25 + [5000] * 15 + [340] * 50], dict(window=20, sinks=3)),
+    # starts in no order, sinks that cross a tile's edge, documents that see ahead
+    "any_order": ([2000, 700], [37, 50], [([1800] * 9 + [3] * 9 + [900] * 9 + [120] * 10), [640, 10, 250, 9000, 380] * 10],
+                  dict(window=8, sinks=20)),
+    "many_documents": ([500], [250], [[max(0, 3 * (t // 3) - 200) * (t % 2) + 500 * (t % 7 == 0) for t in range(250)]],
+                       dict(window=5, sinks=2)),
+}
+
+
+@pytest.mark.parametrize("name", list(UNSEEN))
+@pytest.mark.parametrize("kind", ["plain", "cap", "bias"])
+@pytest.mark.parametrize("hq,hkv,full", [(4, 1, False), (2, 2, False), (8, 1, True)])
+def test_rows_that_no_document_shows_may_hold_anything(cuda_lib, name, kind, hq, hkv, full):
+    prefix, chunk, docs, mask = UNSEEN[name]
+    case = Case(prefix, chunk, hq, hkv, seed=40 + len(name))
+    scoring = kv.Scoring(softcap=20.0 if kind == "cap" else 0.0, slopes=SLOPES(hq) if kind == "bias" else None, **mask)
+    full = [P // 3 for P in prefix] if full else None
+    hidden = []
+    for b, (P, C) in enumerate(zip(prefix, chunk)):
+        seen = np.zeros(P + C, bool)
+        for t in range(C):
+            seen |= extend_seen(P, C, t, scoring, None if full is None else full[b], docs[b][t])
+        assert not seen.all()
+        hidden.append(int(case.first[b]) + np.flatnonzero(~seen))
+    hidden = dev(np.concatenate(hidden))
+    case.gpu[1][hidden] = 0x7F
+    case.gpu[2][hidden] = 0x7F
+    flat = np.concatenate(docs)
+    case.run(scoring, full=full, docs=flat)
+    case.check(scoring, full=full, docs=flat)
