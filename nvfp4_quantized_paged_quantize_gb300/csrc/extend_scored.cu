@@ -589,9 +589,9 @@ __global__ void __launch_bounds__(kThreads, 1) extend_scored_kernel(const Scored
       const int end = kr.end - kbase, low = kr.low - kbase, sink = kr.sink_end - kbase, near = kr.near - kbase;
       const bool masked = end < kTileN || (near > 0 && (low > 0 || sink < kTileN));
       const bool any_masked = __any_sync(0xFFFFFFFFu, masked);
-      // All visible, and no bias: the row's maximum is that of the products (the
-      // cap keeps the order), and the cap is left to the second pass, where the FMA
-      // pipe works beside the special-function unit.
+      // All visible, no bias, and no score beyond 0.6 of its cap: the row's maximum is
+      // that of the products (the cap keeps the order), and the cap is left to the
+      // second pass, where the FMA pipe works beside the special-function unit.
       bool direct = false;
       int form = kAny;        // the cap's
       uint32_t gone = 0;      // bit k: none of the warp's rows sees keys 32 k .. 32 k + 31
@@ -616,14 +616,11 @@ __global__ void __launch_bounds__(kThreads, 1) extend_scored_kernel(const Scored
                    : __all_sync(0xFFFFFFFFu, h <= p.cap.near && l0 >= -p.cap.near) ? kNear
                                                                                     : kAny;
             const float2 zero = both(0.0f);
-            top = (form == kFar    ? cap_far(both(h), p.cap, zero)
-                   : form == kNear ? cap_near(both(h), p.cap, zero)
-                                   : cap_any(both(h), p.cap, zero))
-                      .x;
+            top = (form == kFar ? cap_far(both(h), p.cap, zero) : cap_near(both(h), p.cap, zero)).x;
           } else {
             top = h * p.unit;  // (the unit is positive)
           }
-          direct = true;
+          direct = M == 0 || form != kAny;
         }
       }
       if (!direct) {
@@ -729,14 +726,12 @@ __global__ void __launch_bounds__(kThreads, 1) extend_scored_kernel(const Scored
       };
       if constexpr (M == 0)
         weights([&](float2 s) { return fma2(s, both(p.unit), both(off)); });
-      else if (M == kCapped && direct && form == kFar)
-        weights([&](float2 s) { return cap_far(s, p.cap, both(off)); });
-      else if (M == kCapped && direct && form == kNear)
-        weights([&](float2 s) { return cap_near(s, p.cap, both(off)); });
-      else if (M == kCapped && direct)
-        weights([&](float2 s) { return cap_any(s, p.cap, both(off)); });
-      else
+      else if (M != kCapped || !direct)
         weights([&](float2 s) { return add2(s, both(off)); });
+      else if (form == kFar)
+        weights([&](float2 s) { return cap_far(s, p.cap, both(off)); });
+      else
+        weights([&](float2 s) { return cap_near(s, p.cap, both(off)); });
       tc::tmem_wait_st();
       tc::fence_before_sync();
       __syncwarp();

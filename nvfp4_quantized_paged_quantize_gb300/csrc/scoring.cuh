@@ -66,9 +66,10 @@ __device__ __forceinline__ float2 tanh_unit(float2 x) {
   return fma2(mul2(x, u), p, x);
 }
 
-// tanh for |x| > 1: 1 - 2 / (e^{2|x|} + 1) with the sign of x; the value is
-// above 0.76 there, so the error of the exponential and the quotient (a few
-// 1e-7 of 2 / (e^2 + 1)) stays below fp32's last place of it.
+// tanh away from 0: 1 - 2 / (e^{2|x|} + 1) with the sign of x.  For |x| > 1 the
+// value is above 0.76, so the error of the exponential and the quotient (a few
+// 1e-7 of 2 / (e^2 + 1)) stays below fp32's last place of it; for |x| > 0.6 it is
+// above 0.53 and off by 2e-7 of it at most.
 __device__ __forceinline__ float tanh_outer(float x) {
   float e, r;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(fabsf(x) * (2.0f * kLog2e)));
@@ -103,10 +104,12 @@ __device__ __forceinline__ void tanh_warp(float2 (&x)[N]) {
 //     coefficients hold both factors, S Q(S^2) with Q of degree 3: five packed
 //     operations a pair, the last of which adds;
 //   |c S| <= 0.6: x Q(x^2), x = c S, Q of degree 4: eight;
-//   any: a - 2 a / (e^{2 c S} + 1) by two special-function operations a score.
+//   any: the second form where |c S| <= 0.6, elsewhere a (1 - 2 / (e^{2 |c S|} + 1))
+//     with the sign of S, two special-function operations a score.
 // Both Q were fitted here in the relative maximum norm (9.8e-8 and 7.3e-8 before
-// rounding).  The last form's error is absolute, some 2^-23 a (in base 2, 1e-5
-// for a cap of 50), which is little beside a score of half the cap.  (A packed
+// rounding).  The exponential alone would do for the last form, but its error is
+// one of a (2^-23 a): scores far from the cap, which take this form when another
+// row of the warp needs it, would lose what a large cap leaves of them.  (A packed
 // multiply-add reads three register pairs and takes 2.6 cycles of a scheduler, so
 // a shorter form is worth a branch per tile.)
 struct CapPoly {
@@ -150,14 +153,9 @@ __device__ __forceinline__ float2 cap_near(float2 S, const CapPoly& p, float2 ad
   return fma2(mul2(x, both(p.a)), q, add);
 }
 __device__ __forceinline__ float2 cap_any(float2 S, const CapPoly& p, float2 add) {
-  const float2 z = mul2(S, both(p.c * (2.0f * kLog2e)));
-  float2 e, r;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.x) : "f"(z.x));
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.y) : "f"(z.y));
-  e = add2(e, both(1.0f));
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.x) : "f"(e.x));
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.y) : "f"(e.y));
-  return fma2(r, both(-2.0f * p.a), add2(add, both(p.a)));
+  const float2 near = cap_near(S, p, add);
+  const float2 far = fma2(make_float2(tanh_outer(S.x * p.c), tanh_outer(S.y * p.c)), both(p.a), add);
+  return make_float2(fabsf(S.x) <= p.near ? near.x : far.x, fabsf(S.y) <= p.near ? near.y : far.y);
 }
 
 // S -> a * tanh(c S) in place.

@@ -287,3 +287,19 @@ def test_rows_that_no_document_shows_may_hold_anything(cuda_lib, name, kind, hq,
     flat = np.concatenate(docs)
     case.run(scoring, full=full, docs=flat)
     case.check(scoring, full=full, docs=flat)
+
+
+@pytest.mark.parametrize("mask", ["none", "window", "bias"])
+@pytest.mark.parametrize("softcap", [500.0, 2.0 ** 14, 2.0 ** 20])
+def test_small_scores_beside_one_at_its_cap(cuda_lib, softcap, mask):
+    # one query whose scores pass its cap among queries with scores of a few units:
+    # theirs stay as accurate.  (The keys' scale keeps every query inside f16's range.)
+    case = Case([120], [40], 4, 1, seed=33, k_exp=(9, 12), sk=32.0)
+    size = torch.full((40, 1, 1), 2.0 ** -10)
+    size[11] = 2.0 ** -10 * softcap                              # in the same warp as queries 8 .. 15
+    q = (torch.from_numpy(case.q64).float() * size).to(torch.bfloat16)
+    case.q, case.q64 = q.cuda(), q.double().numpy()
+    scoring = kv.Scoring(softcap=softcap, window=100 if mask == "window" else 0, sinks=2,
+                         slopes=SLOPES(4) if mask == "bias" else None)
+    case.run(scoring)
+    case.check(scoring)
