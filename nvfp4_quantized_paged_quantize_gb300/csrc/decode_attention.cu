@@ -820,7 +820,12 @@ __device__ __forceinline__ void softmax_phase(const DecodeParams& p, const float
       mx1 = fmaxf(mx1, __shfl_xor_sync(0xFFFFFFFFu, mx1, off));
     }
     const float n0 = fmaxf(s.m0, mx0), n1 = fmaxf(s.m1, mx1);
-    const float f0 = ex2(s.m0 - n0), f1 = ex2(s.m1 - n1);
+    float f0 = ex2(s.m0 - n0), f1 = ex2(s.m1 - n1);
+    if constexpr ((M & kBiased) != 0) {
+      // a head that has seen nothing yet (a bias of -inf) while another's maximum moves
+      f0 = n0 == -INFINITY ? 1.0f : f0;
+      f1 = n1 == -INFINITY ? 1.0f : f1;
+    }
     s.l0 *= f0;
     s.l1 *= f1;
 #pragma unroll

@@ -294,3 +294,20 @@ def test_outputs_stay_inside_their_buffers(cuda_lib):
     batch.check(scoring, weights.t, np.zeros((4, 2, 401), np.float32), 0.5)
     for g in (out, lse, weights, ws):
         assert g.intact()
+
+
+@pytest.mark.parametrize("kept", [False, True])
+def test_a_bias_that_leaves_fp32_hides_its_head_alone(cuda_lib, kept):
+    # a head whose bias is -inf in fp32 on all but its nearest keys, beside heads
+    # whose maximum moves; several pages of a pair to a warp
+    lens = [300] * 500 + [17, 1, 0]
+    batch = Batch(lens, 4, 1, seed=19, q_size=2.0)
+    scoring = kv.Scoring(slopes=np.array([1e37, 0.01, 1e35, 0.0]))
+    if kept:
+        before = np.ones((len(lens), 1, 304), np.float32)
+        weights = dev(before)
+        batch.weighted(scoring, weights, 0.5)
+        batch.check(scoring, weights, before, 0.5)
+    else:
+        batch.decode(scoring)
+        batch.check(scoring)
