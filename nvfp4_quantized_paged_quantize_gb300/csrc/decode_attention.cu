@@ -625,8 +625,8 @@ __device__ __forceinline__ void load_q(const DecodeParams& p, const QRaw& raw, W
   }
   if constexpr ((M & kBiased) != 0) {
     const float* sl = p.slopes + (long long)(pair % p.hkv) * p.group;
-    s.b0 = 2 * t < p.group ? __ldg(sl + 2 * t) * kLog2e : 0.0f;
-    s.b1 = 2 * t + 1 < p.group ? __ldg(sl + 2 * t + 1) * kLog2e : 0.0f;
+    s.b0 = 2 * t < p.group ? base2_slope(__ldg(sl + 2 * t)) : 0.0f;
+    s.b1 = 2 * t + 1 < p.group ? base2_slope(__ldg(sl + 2 * t + 1)) : 0.0f;
   }
 #pragma unroll
   for (int i = 0; i < 8; ++i)

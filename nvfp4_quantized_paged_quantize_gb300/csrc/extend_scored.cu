@@ -569,7 +569,7 @@ __global__ void __launch_bounds__(kThreads, 1) extend_scored_kernel(const Scored
     }
     KeyRange kr = key_range(p, keys, pos, full, p.doc_starts != nullptr && live ? __ldg(p.doc_starts + q0 + t) : 0);
     if (!live) kr.end = 0;  // a row past the chunk sees nothing
-    const float slope = (M & kBiased) != 0 ? __ldg(p.slopes + head) * kLog2e : 0.0f;
+    const float slope = (M & kBiased) != 0 ? base2_slope(__ldg(p.slopes + head)) : 0.0f;
     const uint32_t t_lane = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
     const uint32_t t_s = t_lane + tile * kTileN, t_o = t_lane + kTmemO + tile * kHeadDim;
     const uint32_t bar_s = b_s + 8 * tile, bar_p = b_p + 8 * tile;

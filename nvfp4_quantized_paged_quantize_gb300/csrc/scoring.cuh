@@ -39,6 +39,13 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
       : "l"(*reinterpret_cast<uint64_t*>(&a)), "l"(*reinterpret_cast<uint64_t*>(&b)));
   return *reinterpret_cast<float2*>(&r);
 }
+// A slope in base-2 units per token, kept finite: the query's own key lies at
+// distance 0, and infinity times 0 would be NaN.
+__device__ __forceinline__ float base2_slope(float slope) {
+  constexpr float kMax = 0x1.fffffep+127f;
+  return fminf(fmaxf(slope * kLog2e, -kMax), kMax);
+}
+
 // The largest and the smallest of three.
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float r;

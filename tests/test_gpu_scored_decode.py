@@ -311,3 +311,11 @@ def test_a_bias_that_leaves_fp32_hides_its_head_alone(cuda_lib, kept):
     else:
         batch.decode(scoring)
         batch.check(scoring)
+
+
+def test_the_steepest_slopes(cuda_lib):
+    # log2(e) times the slope is past fp32's range: the nearest key alone is left
+    batch = Batch([300, 17, 1], 4, 1, seed=21, q_size=2.0)
+    scoring = kv.Scoring(slopes=np.array([float(np.finfo(np.float32).max), 0.5, 2.5e38, 3e38]))
+    batch.decode(scoring)
+    batch.check(scoring)

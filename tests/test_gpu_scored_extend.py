@@ -303,3 +303,12 @@ def test_small_scores_beside_one_at_its_cap(cuda_lib, softcap, mask):
                          slopes=SLOPES(4) if mask == "bias" else None)
     case.run(scoring)
     case.check(scoring)
+
+
+@pytest.mark.parametrize("softcap", [0.0, 20.0])
+def test_the_steepest_slopes(cuda_lib, softcap):
+    # log2(e) times the slope is past fp32's range: the nearest key alone is left
+    case = Case([70, 0], [40, 9], 4, 1, seed=34)
+    scoring = kv.Scoring(softcap=softcap, slopes=np.array([float(np.finfo(np.float32).max), 0.5, 2.5e38, 3e38]))
+    case.run(scoring)
+    case.check(scoring)
