@@ -530,7 +530,8 @@ int nvfp4kv_extend_attention_scored(const void* q_bf16, const int64_t* cu_q, int
  *   weights         device fp32 [batch][num_kv_heads][weight_stride], weight_stride
  *                   >= max_pages_per_seq * page_size or >= every seq_lens[b]
  *                   (longer ones are cut there, NVFP4KV_DEVERR_LENGTH)
- *   budget, first, recent   budget > 0, first >= 0, recent >= 0, first + recent <= budget
+ *   budget, first, recent   0 < budget <= 2^31 - 4096, first >= 0, recent >= 0,
+ *                   first + recent <= budget
  *   dst_page_table  device int32 [batch][dst_max_pages_per_seq], dst_max_pages_per_seq
  *                   >= ceil(budget / page_size); its first ceil(n / page_size)
  *                   pages are written whole (rows past n as zeros).  They must

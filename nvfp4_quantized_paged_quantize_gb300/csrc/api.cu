@@ -427,6 +427,8 @@ int nvfp4kv_evict(const nvfp4kv_cache* cache, const int32_t* page_table, int32_t
   if ((int64_t)max_pages_per_seq * kPageSize >= (int64_t(1) << 31) || weight_stride > (int64_t(1) << 40) ||
       kept_stride > (int64_t(1) << 40) || pairs >= (int64_t(1) << 27) || pairs * dst_pages >= (int64_t(1) << 31))
     return NVFP4KV_ERR_UNSUPPORTED;
+  // the selection's loops over a list of `budget` step by up to 4096 (8 CTAs of 512 threads) in 32 bits
+  if (budget > INT32_MAX - 4095) return NVFP4KV_ERR_UNSUPPORTED;
   if (!page_table || !seq_lens || !weights || !dst_page_table || !kept) return NVFP4KV_ERR_INVALID_ARGUMENT;
   for (const void* ptr : {(const void*)page_table, (const void*)seq_lens, (const void*)weights,
                           (const void*)dst_page_table, (const void*)kept, (const void*)kept_weights,

@@ -39,6 +39,7 @@ constexpr int kSpan = 128;            // tokens a warp takes at a time, four per
 constexpr int kKeyCap = 20 * 1024;    // keys a CTA holds: with the histograms two CTAs fit an SM
 static_assert(kKeyCap % (kSpan * kSelectWarps) == 0, "the keys are padded to whole spans of every warp");
 constexpr int kMaxCluster = 8;        // the portable limit
+static_assert(kMaxCluster * kSelectThreads == 4096, "the largest budget of nvfp4kv_evict allows for this stride");
 constexpr int kPackWarps = 8;
 
 struct EvictParams {

@@ -192,3 +192,14 @@ def test_bindings_refuse_tensors_of_another_gpu(monkeypatch):
         kv.nvfp4kv_decode_attention_scored(kv.Cache(other, 4, 2), *t, 0.1, None, workspace_bytes=0)
     with pytest.raises(ValueError, match="workspace: .* got cuda:1"):
         kv.nvfp4kv_decode_attention_scored(c, *t, 0.1, other, workspace_bytes=0)
+
+
+def test_eviction_refuses_budgets_that_its_loops_cannot_count(lib):
+    # a cluster's loops over a budget step by up to 4096 in 32 bits
+    cs = ctypes.byref(_cache())
+    pages = 1 << 27
+    call = _call(lib.nvfp4kv_evict,
+                 [cs, 64, 8, 4096, 1, 1 << 20, 128, 2 ** 31 - 1, 4, 16, 128, pages, 4, None, 0, None, None, None])
+    for over in (2 ** 31 - 1, 2 ** 31 - 4095):
+        assert call(a7=over, a12=None) == UNSUPPORTED, over
+    assert call(a7=2 ** 31 - 4096, a12=None) == INVALID        # only the missing list is refused
