@@ -50,6 +50,7 @@
 // Khat and Vhat are exact in f16.  q is bf16; it is multiplied by a power of
 // two per head so its largest element sits in [2^14, 2^15) before rounding to
 // f16, and the factor is folded back into the score scale.
+#include <cfloat>
 #include <cstdint>
 
 #include "nvfp4kv_device.cuh"
@@ -615,7 +616,8 @@ __device__ __forceinline__ void load_q(const DecodeParams& p, const QRaw& raw, W
   }
   const float c = p.score_scale * inv;  // score multiplier of head g
   if constexpr ((M & kCapped) != 0) {
-    const float x = p.cap_scale * inv;
+    // finite: it may meet a zero (and anything else it makes far larger than 1 either way)
+    const float x = fminf(p.cap_scale * inv, FLT_MAX);
     s.x0 = __shfl_sync(0xFFFFFFFFu, x, (2 * t) * 4);
     s.x1 = __shfl_sync(0xFFFFFFFFu, x, (2 * t + 1) * 4);
     s.c0 = s.c1 = p.score_scale;
@@ -1822,7 +1824,7 @@ cudaError_t launch_decode_scored(const nvfp4kv_cache& c, const uint16_t* q, uint
   if (sc.softcap > 0.0f) {
     m |= kCapped;
     const double inner = (double)softmax_scale * (double)c.k_global_scale / (double)sc.softcap;
-    p.cap_scale = (float)(inner < 0x1p+20 ? inner : 0x1p+20);  // stays finite under q's prescale (up to 2^100)
+    p.cap_scale = (float)(inner < FLT_MAX ? inner : FLT_MAX);
     p.score_scale = (float)((double)sc.softcap * 1.4426950408889634);
   }
   if (sc.slopes != nullptr) m |= kBiased;

@@ -319,3 +319,12 @@ def test_the_steepest_slopes(cuda_lib):
     scoring = kv.Scoring(slopes=np.array([float(np.finfo(np.float32).max), 0.5, 2.5e38, 3e38]))
     batch.decode(scoring)
     batch.check(scoring)
+
+
+@pytest.mark.parametrize("exponent", [24, 40, 90])
+def test_caps_with_large_global_scales(cuda_lib, exponent):
+    # scores of a few units from keys of 2^exponent and queries as small: the factor inside the tanh is large
+    batch = Batch([40, 300], 8, 2, seed=20, gk=2.0 ** exponent, q_size=2.0 ** (1 - exponent))
+    for softcap in (1.0, 2.0 ** -20):
+        batch.decode(kv.Scoring(softcap=softcap))
+        batch.check(kv.Scoring(softcap=softcap))
