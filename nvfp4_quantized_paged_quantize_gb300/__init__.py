@@ -314,7 +314,7 @@ def _shape(name: str, x, dims: int):
     return x.shape
 
 
-def _check_decode(cache: "Cache", q, out, page_table, seq_lens, lse, workspace):
+def _check_decode(cache: "Cache", q, out, page_table, seq_lens, lse, workspace, device_status):
     """Checks a scored decode's tensors; returns (batch, query heads, page-table columns, the current device)."""
     if cache.mxfp4:
         raise ValueError("the cache holds MXFP4 page-heads; the scored decodes read NVFP4 ones")
@@ -329,6 +329,7 @@ def _check_decode(cache: "Cache", q, out, page_table, seq_lens, lse, workspace):
         _check_tensor("lse", lse, t.float32, (B, Hq), gpu)
     _check_memory("cache.pages", cache.pages, gpu)
     _check_memory("workspace", workspace, gpu)
+    _check_memory("device_status", device_status, gpu)
     return B, Hq, maxp, gpu
 
 
@@ -337,7 +338,7 @@ def nvfp4kv_decode_attention_scored(cache: "Cache", q, out, page_table, seq_lens
                                     workspace_bytes: int | None = None) -> None:
     """Paged decode attention with a scoring (cap, distance bias, window with sinks): q bf16 [B, Hq, 128], out
     bf16 [B, Hq, 128], lse fp32 [B, Hq] or None; the rest as nvfp4kv_decode_attention."""
-    B, Hq, maxp, gpu = _check_decode(cache, q, out, page_table, seq_lens, lse, workspace)
+    B, Hq, maxp, gpu = _check_decode(cache, q, out, page_table, seq_lens, lse, workspace, device_status)
     if workspace_bytes is None:
         workspace_bytes = workspace.numel() * workspace.element_size()
     c = cache.c_struct()
@@ -365,7 +366,7 @@ def nvfp4kv_decode_attention_weights(cache: "Cache", q, out, page_table, seq_len
     """nvfp4kv_decode_attention_scored that also updates weights (fp32 [B, Hkv, tokens]): each cached token's
     sum becomes decay * sum + the softmax weight it got from the KV head's query heads.  max_total_pages bounds
     the batch's cached pages (default: the cache's num_pages, right where sequences share no page)."""
-    B, Hq, maxp, gpu = _check_decode(cache, q, out, page_table, seq_lens, lse, workspace)
+    B, Hq, maxp, gpu = _check_decode(cache, q, out, page_table, seq_lens, lse, workspace, device_status)
     stride = _shape("weights", weights, 3)[2]
     _check_tensor("weights", weights, _types().float32, (B, cache.num_kv_heads, stride), gpu)
     if workspace_bytes is None:
@@ -408,6 +409,7 @@ def nvfp4kv_extend_attention_scored(q, cu_q, max_q_len: int, ws_k, ws_v, cu_pref
         _check_tensor("doc_starts", doc_starts, t.int32, (n,), gpu)
     if lse is not None:
         _check_tensor("lse", lse, t.float32, (n, hq), gpu)
+    _check_memory("device_status", device_status, gpu)
     _check("nvfp4kv_extend_attention_scored",
            _L().nvfp4kv_extend_attention_scored(_ptr(q), _ptr(cu_q), int(max_q_len), _ptr(ws_k), _ptr(ws_v),
                                                 _ptr(cu_prefix), _ptr(prefix_lens), B, rows, hq, hkv, HEAD_DIM,
@@ -440,6 +442,7 @@ def nvfp4kv_evict(cache: "Cache", page_table, seq_lens, weights, budget: int, fi
     if new_lens is not None:
         _check_tensor("new_lens", new_lens, t.int32, (B,), gpu)
     _check_memory("cache.pages", cache.pages, gpu)
+    _check_memory("device_status", device_status, gpu)
     c = cache.c_struct()
     _check("nvfp4kv_evict",
            _L().nvfp4kv_evict(ctypes.byref(c), _ptr(page_table), maxp, _ptr(seq_lens), B, _ptr(weights), stride,

@@ -203,3 +203,44 @@ def test_eviction_refuses_budgets_that_its_loops_cannot_count(lib):
     for over in (2 ** 31 - 1, 2 ** 31 - 4095):
         assert call(a7=over, a12=None) == UNSUPPORTED, over
     assert call(a7=2 ** 31 - 4096, a12=None) == INVALID        # only the missing list is refused
+
+
+class OnGpu:
+    """What the bindings' checks look at of a tensor, on GPU `gpu` (-1: on the CPU)."""
+
+    def __init__(self, dtype, shape, gpu=0):
+        self.dtype, self.shape, self.gpu = dtype, shape, gpu
+        self.device, self.is_cuda = f"cuda:{gpu}" if gpu >= 0 else "cpu", gpu >= 0
+
+    def dim(self):
+        return len(self.shape)
+
+    def is_contiguous(self):
+        return True
+
+    def get_device(self):
+        return self.gpu
+
+
+@pytest.mark.parametrize("gpu", [1, -1])
+def test_bindings_refuse_a_status_word_elsewhere(monkeypatch, gpu):
+    # the kernels write it, so it has to be memory of the current GPU too
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0, raising=False)
+    c, status = kv.Cache(0x10000, 4, 2), OnGpu(torch.int32, (1,), gpu)
+    i32, i64, bf16, f32, u8 = torch.int32, torch.int64, torch.bfloat16, torch.float32, torch.uint8
+    q, out, table, lens, sums = (OnGpu(*a) for a in ((bf16, (1, 8, 128)), (bf16, (1, 8, 128)), (i32, (1, 4)), (i32, (1,)),
+                                                     (f32, (1, 2, 64))))
+    ws = OnGpu(u8, (5, 2, 128))
+    calls = [
+        lambda: kv.nvfp4kv_decode_attention_scored(c, q, out, table, lens, 0.1, None, workspace_bytes=0,
+                                                   device_status=status),
+        lambda: kv.nvfp4kv_decode_attention_weights(c, q, out, table, lens, 0.1, sums, None, workspace_bytes=0,
+                                                    device_status=status),
+        lambda: kv.nvfp4kv_extend_attention_scored(q, OnGpu(i64, (2,)), 1, ws, ws, OnGpu(i64, (2,)), lens, out, 0.1,
+                                                   device_status=status),
+        lambda: kv.nvfp4kv_evict(c, table, lens, sums, 16, 0, 0, OnGpu(i32, (1, 4)), OnGpu(i32, (1, 2, 16)),
+                                 device_status=status),
+    ]
+    for call in calls:
+        with pytest.raises(ValueError, match="device_status: "):
+            call()
