@@ -148,9 +148,10 @@ def _ptr(x) -> int | None:
 
 def _stream(stream) -> int | None:
     if stream is None:
-        # torch.cuda.current_stream().cuda_stream without building a Stream object (3 us a call)
+        # torch.cuda.current_stream().cuda_stream; without building a Stream object (3 us a call) where torch can
         t = _types()
-        return t._C._cuda_getCurrentRawStream(t.cuda.current_device())
+        raw = getattr(t._C, "_cuda_getCurrentRawStream", None)
+        return raw(t.cuda.current_device()) if raw is not None else t.cuda.current_stream().cuda_stream
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -286,8 +287,11 @@ def _types():
 
 def _current_gpu(x) -> int:
     """The current device, where a call's kernels run; one that no tensor is on if x is not on a GPU."""
-    # (current_device() without its lazy set-up: x is on a GPU)
-    return _types()._C._cuda_getDevice() if x.is_cuda else -2
+    if not x.is_cuda:
+        return -2
+    # current_device() without its lazy set-up, where torch has that: x is on a GPU
+    t = _types()
+    return getattr(t._C, "_cuda_getDevice", t.cuda.current_device)()
 
 
 def _check_tensor(name: str, x, dtype, shape, gpu: int) -> None:

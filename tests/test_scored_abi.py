@@ -244,3 +244,16 @@ def test_bindings_refuse_a_status_word_elsewhere(monkeypatch, gpu):
     for call in calls:
         with pytest.raises(ValueError, match="device_status: "):
             call()
+
+
+def test_streams_and_devices_without_torchs_private_calls(monkeypatch):
+    # the bindings take a shortcut where torch has it; the public calls do without
+    class Stream:
+        cuda_stream = 0x1234
+
+    monkeypatch.delattr(torch._C, "_cuda_getCurrentRawStream", raising=False)
+    monkeypatch.delattr(torch._C, "_cuda_getDevice", raising=False)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 3)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda: Stream)
+    assert kv._stream(None) == 0x1234 and kv._stream(Stream) == 0x1234 and kv._stream(7) == 7
+    assert kv._current_gpu(OnGpu(torch.int32, (1,))) == 3
