@@ -328,3 +328,28 @@ def test_caps_with_large_global_scales(cuda_lib, exponent):
     for softcap in (1.0, 2.0 ** -20):
         batch.decode(kv.Scoring(softcap=softcap))
         batch.check(kv.Scoring(softcap=softcap))
+
+
+@pytest.mark.parametrize("window", [0, 50])
+@pytest.mark.parametrize("stride", [1, 60, 64, 399])
+def test_sums_shorter_than_a_sequence(cuda_lib, window, stride):
+    # tokens below the stride get their sums, the others none, and nothing past them is touched
+    from test_gpu_canary import Guarded
+
+    lens = [64, 400, 33]
+    batch = Batch(lens, 8, 2, seed=22)
+    scoring = kv.Scoring(window=window, sinks=4)
+    weights = Guarded((3, 2, stride), torch.float32)
+    before = np.random.default_rng(6).random((3, 2, stride), dtype=np.float32)
+    weights.t.copy_(dev(before))
+    batch.weighted(scoring, weights.t, 0.5)
+    torch.cuda.synchronize()
+    assert batch.status.item() == kv.NVFP4KV_DEVERR_LENGTH and weights.intact()
+    w = weights.t.double().cpu().numpy()
+    for b, h, refs in batch.refs(scoring):
+        n = min(stride, lens[b])
+        old = before[b, h].astype(np.float64)
+        want, tol = sum(r["p"] for r in refs)[:n], sum(r["tol_p"] for r in refs)[:n]
+        want = 0.5 * old[:n] + want
+        check(w[b, h, :n], want, tol + 2.0 ** -22 * want, f"weights {b} {h}")
+        assert np.array_equal(w[b, h, n:], old[n:])
