@@ -415,7 +415,9 @@ int nvfp4kv_decode_attention_variant(int variant, const nvfp4kv_cache* cache, co
  *     x <- x - slopes[h] * |p - j|              if slopes is not NULL
  * and with window > 0 only keys with p - j < window, and the first `sinks`
  * ones, are visible.  The struct itself is read on the host only; a NULL
- * nvfp4kv_scoring pointer means none of the three. */
+ * nvfp4kv_scoring pointer means none of the three.
+ * x stays below fp32's largest value (with slopes below 0, too); a bias that
+ * leaves fp32's range downwards hides its key. */
 typedef struct nvfp4kv_scoring {
   float softcap;       /* 0 (no cap), or in [2^-20, 2^20] */
   int32_t window;      /* 0 (no window), or > 0 */
@@ -463,7 +465,9 @@ int nvfp4kv_decode_attention_scored(const nvfp4kv_cache* cache, const void* q, v
  *                    (and does not read weights)
  *   max_total_pages  a bound of the batch's cached pages, sum over b of
  *                    ceil(seq_lens[b] / page_size); num_pages of the cache
- *                    serves where no page is shared.  If the batch has more,
+ *                    serves where no page is shared, at the price of scratch
+ *                    for the whole pool (22 % of its bytes for G > 4).  If the
+ *                    batch has more,
  *                    weights are left alone with NVFP4KV_DEVERR_LENGTH (out
  *                    and lse are valid)
  *   workspace        >= nvfp4kv_decode_weights_workspace_size() bytes,
@@ -487,7 +491,10 @@ int nvfp4kv_decode_weights_workspace_size(const nvfp4kv_cache* cache, int32_t ba
                                           int64_t max_total_pages, size_t* bytes);
 
 /* nvfp4kv_extend_attention with a scoring, further masks, a bf16 output and
- * the log-sum-exp.  Chunk token t of sequence b has position
+ * the log-sum-exp.  (The cap is worked out in one of three forms, chosen for 32
+ * rows and 32 or 128 keys at a time; each holds fp32's accuracy, but the last
+ * places of a row can depend on the rows beside it.)  Chunk token t of sequence b
+ * has position
  * p = prefix_lens[b] + t; its keys are low <= j <= high with
  *     high = p, or max(p, full_lens[b] - 1) with full_lens: the sequence's
  *            first full_lens[b] positions are seen by every query (a prefix
@@ -545,7 +552,9 @@ int nvfp4kv_extend_attention_scored(const void* q_bf16, const int64_t* cu_q, int
  *                   overlap it otherwise
  * A source page id out of range reads as zeros, a destination page id out of
  * range is not written, both with NVFP4KV_DEVERR_PAGE.  Enqueues two kernels;
- * needs no workspace. */
+ * needs no workspace.  The launch is sized by what the page table and the sums
+ * have room for, not by seq_lens: the call takes longer where both are much
+ * wider than the sequences (twice as long at 16 times the width). */
 int nvfp4kv_evict(const nvfp4kv_cache* cache, const int32_t* page_table, int32_t max_pages_per_seq,
                   const int32_t* seq_lens, int32_t batch, const float* weights, int64_t weight_stride,
                   int32_t budget, int32_t first, int32_t recent, const int32_t* dst_page_table,

@@ -369,7 +369,9 @@ def nvfp4kv_decode_attention_weights(cache: "Cache", q, out, page_table, seq_len
                                      workspace_bytes: int | None = None) -> None:
     """nvfp4kv_decode_attention_scored that also updates weights (fp32 [B, Hkv, tokens]): each cached token's
     sum becomes decay * sum + the softmax weight it got from the KV head's query heads.  max_total_pages bounds
-    the batch's cached pages (default: the cache's num_pages, right where sequences share no page)."""
+    the batch's cached pages (default: the cache's num_pages, right where sequences share no page); the workspace
+    holds 512 bytes for each of them and KV head with more than four query heads (a page-head is 2304), so a bound
+    of the batch's own is smaller."""
     B, Hq, maxp, gpu = _check_decode(cache, q, out, page_table, seq_lens, lse, workspace, device_status)
     stride = _shape("weights", weights, 3)[2]
     _check_tensor("weights", weights, _types().float32, (B, cache.num_kv_heads, stride), gpu)

@@ -470,7 +470,11 @@ cudaError_t launch_evict(const nvfp4kv_cache& c, const int32_t* page_table, int3
   });
   if (e != cudaSuccess) return e;
   // as many CTAs per pair as its keys need to fit shared memory, and more while
-  // SMs would stay empty and a CTA keeps 2048 tokens or more.  Selection with 1,
+  // SMs would stay empty and a CTA keeps 2048 tokens or more.  The lengths are on
+  // the device, so the rule goes by what the page table and the sums have room
+  // for, and room to spare costs time: the whole call for 256 pairs of 8193 tokens
+  // takes 73 us with room for 8208 tokens, 86, 104 and 148 with room for 32768,
+  // 65536 and 131072.  Selection, with just the room it needs, with 1,
   // 2, 4, 8 CTAs a pair: 32 pairs of 16384 tokens 14.9, 12.9, 11.5 (taken), 13.2
   // us; 256 pairs of 8193 16.0 (taken), 27.6, 47.7, 93.7; 32 pairs of 131072 163,
   // 102, 57 (keys read again in each pass), 26.0 (taken)

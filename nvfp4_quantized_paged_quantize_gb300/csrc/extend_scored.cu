@@ -8,18 +8,19 @@
 // 256 rows.  16 warps:
 //   - Warps 0-3 and 4-7, a softmax group per row tile: one query row per
 //     thread (TMEM lane = row).  They write the row of Q (f16) into shared
-//     memory, then per key tile read the S row, cap, bias and mask it (putting
-//     it back where that changes it) and find its maximum, run the lazy base-2
-//     online softmax (the running max moves only when it grows by 2^8, and O is
-//     then rescaled in TMEM), read the row once more for the exponentials, and
-//     write P (f16) over the S columns just read.  At the end: O * s_ws(V) / l ->
-//     bf16.
+//     memory, then per key tile read the S row for its maximum.  A tile with
+//     nothing masked, no bias and no score near its cap is left as it is; any
+//     other is capped, biased and masked in the same pass and put back.  They run
+//     the lazy base-2 online softmax (the running max moves only when it grows by
+//     2^8, and O is then rescaled in TMEM), read the row once more for the
+//     exponentials (and the cap, where the first pass left it), and write P (f16)
+//     over the S columns just read.  At the end: O * s_ws(V) / l -> bf16.
 //   - Warps 8-11 load the key tiles of the workspace (K and V alternately, one
 //     of each in flight in registers), convert E4M3 -> f16 (exact) and store
 //     them as B operands (K K-major, V MN-major) in a ring of five 32 KB slots.
-//   - Warp 12 issues, from one thread, S_t = Q_t K^T (both operands in shared
-//     memory) and O_t += P_t V (P in TMEM), t = 0, 1, f32 accumulators.  The
-//     order PV_0, S_0, PV_1, S_1 lets one group's softmax run while the tensor
+//   - Warp 12 issues S_t = Q_t K^T (both operands in shared memory) and O_t +=
+//     P_t V (P in TMEM), t = 0, 1, f32 accumulators; the whole warp runs the loop
+//     and one lane's instructions take effect.  The order PV_0, S_0, PV_1, S_1 lets one group's softmax run while the tensor
 //     core works for the other; MMAs execute in issue order, so S_t(i + 1) may
 //     overwrite the columns that P_t(i) was read from, and the completion of
 //     S_t(i + 1) implies that of PV_t(i).
@@ -31,10 +32,11 @@
 // O_0 256-383, O_1 384-511.
 // What bounds it: the chain softmax -> P V -> S of a tile, which the other tile's
 // hides in part, then the FMA pipe where scores are capped.  16384 + 2048 tokens,
-// 64 / 8 heads: 1.23 ms capped, 0.98 ms plain (0.49 and 0.61 of the measured bf16
-// rate; nvfp4kv_extend_attention, without any scoring, 1.49 ms).
+// 64 / 8 heads: 1.27 ms capped, 0.99 ms plain (0.48 and 0.61 of the measured bf16
+// rate; nvfp4kv_extend_attention, without any scoring, 1.49 ms), 1.43 ms biased
+// (every tile is put back), 0.11 ms under a window of 1024.
 // Key tiles that no query of the CTA sees are skipped, and workspace rows that
-// none sees read as zero.  Every wait is bounded: a stalled pipeline flags
+// none sees are zeros in shared memory, not read.  Every wait is bounded: a stalled pipeline flags
 // NVFP4KV_DEVERR_TIMEOUT and drains its MMAs before the TMEM is freed.
 #include "extend_tiles.cuh"
 #include "nvfp4kv_device.cuh"
