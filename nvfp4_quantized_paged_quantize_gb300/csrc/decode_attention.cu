@@ -37,8 +37,8 @@
 // The scored decode (template argument M, 0 for the plain one) is the same two
 // kernels with the scores of step 2 capped (tanh on the FMA pipe, two scores per
 // instruction) and biased before the maximum, bf16 outputs and the log-sum-exp.
-// Decode kernel of 32 x 8193 tokens, 64 / 8 heads: 56.1 us, biased 58.0, capped
-// 60.5.  A window changes only which pages are items: those of the sinks and of
+// Decode kernel of 32 x 8193 tokens, 64 / 8 heads: 56.1 us, biased 60.1, capped
+// 60.3.  A window changes only which pages are items: those of the sinks and of
 // the window, so it costs what it reads (14.7 us under one of 1024).
 // With accumulated weights the scores are also written out (fp32, 512 bytes per
 // 2304-byte page-head) for weights_kernel, which adds every token's weight to
