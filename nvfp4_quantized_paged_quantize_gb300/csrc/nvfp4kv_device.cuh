@@ -128,6 +128,13 @@ __device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
 
 __device__ __forceinline__ float bf16_to_f32(uint32_t bits16) { return __uint_as_float(bits16 << 16); }
 
+// Two fp32 -> two bf16 (round to nearest even), `lo` in the low half.
+__device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
 // Correctly rounded a / b from r = RN(1 / b): q0 = RN(a r), then Markstein's
 // correction RN(q0 + r RN(a - b q0)) (two FMAs).  Valid while b, 1 / b and
 // the quotient stay well inside the normal range; the caller checks.

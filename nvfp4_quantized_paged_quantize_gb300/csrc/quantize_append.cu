@@ -6,20 +6,16 @@
 // takes two (token, KV head) rows of K (lanes 0-7 and 8-15) and the two
 // tokens of a token pair of one KV head of V (lanes 16-23: token 2q, lanes
 // 24-31: token 2q + 1), so the per-block work (amax, the scale's division,
-// the reciprocal) is done once per block.  Per block:
-//   amax = max |x|                       (exact; inputs are bf16)
-//   sb   = E4M3(amax / (6 g))            (correctly rounded quotient, RNE, saturating)
-//   den  = E4M3val(sb) * g
-//   code = E2M1(x / den)                 (correctly rounded quotient, RNE, saturating)
-// A block with den == 0 stores signed zeros.  A token's codes and scales go
-// to slot slot_mapping[token]: row slot % 16 of the page-head (slot / 16,
-// head).  V data is stored by token pair (byte d of pair row p: dimension d of
-// tokens 2p and 2p + 1): when the two tokens of a step land in the two rows
-// of one pair row (the usual case: consecutive slots from an even one), one
-// lane writes both tokens' bytes; otherwise each token's nibbles are merged
-// into their bytes with atomic XORs.  HBM-bound: 2 B read and 9/16 B
+// the reciprocal; nvfp4_block.cuh) is done once per block.  A token's codes
+// and scales go to slot slot_mapping[token]: row slot % 16 of the page-head
+// (slot / 16, head).  V data is stored by token pair (byte d of pair row p:
+// dimension d of tokens 2p and 2p + 1): when the two tokens of a step land in
+// the two rows of one pair row (the usual case: consecutive slots from an even
+// one), one lane writes both tokens' bytes; otherwise each token's nibbles are
+// merged into their bytes with atomic XORs.  HBM-bound: 2 B read and 9/16 B
 // written per value.
 #include "fp8_quotient.cuh"
+#include "nvfp4_block.cuh"
 #include "nvfp4kv_device.cuh"
 #include "nvfp4kv_launch.h"
 
@@ -42,8 +38,7 @@ struct QuantParams {
   int64_t ws_total_rows;
   uint8_t* ws_k;
   uint8_t* ws_v;
-  float sk, sv, rsk, rsv;
-  bool sk_fast, sv_fast, ws_unit;
+  WsScales ws;
 };
 
 constexpr int kThreads = 256;
@@ -75,13 +70,6 @@ struct RowWalk {
   }
 };
 
-__device__ __forceinline__ void unpack_bf16x8(const uint4& x, float* f) {
-  f[0] = bf16_to_f32(x.x & 0xFFFFu); f[1] = bf16_to_f32(x.x >> 16);
-  f[2] = bf16_to_f32(x.y & 0xFFFFu); f[3] = bf16_to_f32(x.y >> 16);
-  f[4] = bf16_to_f32(x.z & 0xFFFFu); f[5] = bf16_to_f32(x.z >> 16);
-  f[6] = bf16_to_f32(x.w & 0xFFFFu); f[7] = bf16_to_f32(x.w >> 16);
-}
-
 // kWs: also write each row's FP8 workspace row, E4M3(fp32(x) / s_ws), at
 // ws_rows[token] (< 0: none) from the same registers.
 template <bool kWs>
@@ -95,9 +83,7 @@ __global__ void __launch_bounds__(kThreads) quantize_append_kernel(QuantParams p
   const int which = (lane >> 3) & 1;  // first or second row of the step
   const uint16_t* src = tensor ? p.v : p.k;
   const float g = tensor ? p.gv : p.gk;
-  const float t6 = __fmul_rn(6.0f, g);  // the block amax maps onto E2M1's 6
-  const float r6 = __frcp_rn(t6);
-  const bool t6_ok = t6 >= 0x1p-100f && t6 <= 0x1p+100f;  // t6 and 1/t6 well inside the normal range
+  const GlobalScale gs = global_scale(g);
   const int warp = (int)((blockIdx.x * (unsigned)blockDim.x + threadIdx.x) >> 5);
   const int nwarps = (int)((gridDim.x * (unsigned)blockDim.x) >> 5);
   // steps cover the K rows and the V token pairs: (ntok rounded up to even) * hkv,
@@ -158,12 +144,12 @@ __global__ void __launch_bounds__(kThreads) quantize_append_kernel(QuantParams p
       } else if (cw >= 0) {
         // this lane's 16 values -> 16 E4M3 bytes of the workspace row
         const uint32_t w[8] = {ca.x, ca.y, ca.z, ca.w, cb.x, cb.y, cb.z, cb.w};
-        const float s = tensor ? p.sv : p.sk, rs = tensor ? p.rsv : p.rsk;
-        const bool fast = tensor ? p.sv_fast : p.sk_fast;
+        const float s = tensor ? p.ws.sv : p.ws.sk, rs = tensor ? p.ws.rsv : p.ws.rsk;
+        const bool fast = tensor ? p.ws.sv_fast : p.ws.sk_fast;
         uint32_t e[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-          e[i] = e4m3x2_from_quotients(bf16_to_f32(w[i] & 0xFFFFu), bf16_to_f32(w[i] >> 16), s, rs, fast, p.ws_unit);
+          e[i] = e4m3x2_from_quotients(bf16_to_f32(w[i] & 0xFFFFu), bf16_to_f32(w[i] >> 16), s, rs, fast, p.ws.unit);
         uint8_t* ws = tensor ? p.ws_v : p.ws_k;
         reinterpret_cast<uint4*>(ws + (cw * p.hkv + h) * kHeadDim)[sub] =
             make_uint4(e[0] | (e[1] << 16), e[2] | (e[3] << 16), e[4] | (e[5] << 16), e[6] | (e[7] << 16));
@@ -172,38 +158,8 @@ __global__ void __launch_bounds__(kThreads) quantize_append_kernel(QuantParams p
     float f[16];
     unpack_bf16x8(ca, f);
     unpack_bf16x8(cb, f + 8);
-    float amax = 0.0f;
-#pragma unroll
-    for (int i = 0; i < 16; ++i) amax = fmaxf(amax, fabsf(f[i]));
-    // the block scale's quotient: Markstein while the first product stays far
-    // from overflow (a quotient below 2^-11 encodes as 0 either way)
-    const float sq = (t6_ok && __fmul_rn(amax, r6) < 0x1p+64f) ? div_markstein(amax, t6, r6) : __fdiv_rn(amax, t6);
-    const uint32_t sb = e4m3_from_f32(sq);
-    const float den = __fmul_rn(e4m3_to_f32(sb), g);
-    uint32_t lo = 0, hi = 0;
-    if (den == 0.0f) {
-      // signed zeros: code 8 for negative inputs
-#pragma unroll
-      for (int i = 0; i < 8; ++i) lo |= (__float_as_uint(f[i]) >> 31) << (4 * i + 3);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) hi |= (__float_as_uint(f[8 + i]) >> 31) << (4 * i + 3);
-    } else {
-      const float rcp = __frcp_rn(den);
-      float y[16];
-      if (den >= 0x1p-100f && den <= 0x1p+100f && __fmul_rn(amax, rcp) < 0x1p+64f) {
-        // a quotient that rounds to zero can come out as +0 for negative x;
-        // the sign of x / den is the sign of x (den > 0)
-#pragma unroll
-        for (int i = 0; i < 16; ++i) y[i] = copysignf(div_markstein(f[i], den, rcp), f[i]);
-      } else {
-#pragma unroll
-        for (int i = 0; i < 16; ++i) y[i] = __fdiv_rn(f[i], den);
-      }
-#pragma unroll
-      for (int k = 0; k < 4; ++k) lo |= e2m1x2_from_f32(y[2 * k], y[2 * k + 1]) << (8 * k);
-#pragma unroll
-      for (int k = 0; k < 4; ++k) hi |= e2m1x2_from_f32(y[8 + 2 * k], y[8 + 2 * k + 1]) << (8 * k);
-    }
+    const BlockCodes codes = quantize_block(f, gs);
+    const uint32_t lo = codes.lo, hi = codes.hi, sb = codes.sb;
     // V: the other token of the pair (lane ^ 8 holds the same block of it);
     // every lane takes part in the exchange
     const uint32_t plo = __shfl_xor_sync(0xFFFFFFFFu, lo, 8);
@@ -292,13 +248,7 @@ cudaError_t launch_quantize_append_fp8(const nvfp4kv_cache& c, const uint16_t* k
   p.ws_total_rows = total_rows;
   p.ws_k = ws_k;
   p.ws_v = ws_v;
-  p.sk = k_ws_scale;
-  p.sv = v_ws_scale;
-  p.rsk = 1.0f / k_ws_scale;  // host IEEE division: RN(1 / s_ws)
-  p.rsv = 1.0f / v_ws_scale;
-  p.sk_fast = k_ws_scale >= 0x1p-100f && k_ws_scale <= 0x1p+100f;
-  p.sv_fast = v_ws_scale >= 0x1p-100f && v_ws_scale <= 0x1p+100f;
-  p.ws_unit = k_ws_scale == 1.0f && v_ws_scale == 1.0f;
+  p.ws = ws_scales(k_ws_scale, v_ws_scale);
   return launch_quantize<true>(p, num_sms, stream);
 }
 

@@ -4,17 +4,12 @@
 
 #include <cstdint>
 
+#include "nvfp4kv_device.cuh"
+
 namespace nvfp4kv {
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
-
-// Two fp32 -> two bf16 (round to nearest even), `lo` in the low half.
-__device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
-}
 
 // Two fp32 products / fused multiply-adds per instruction.
 __device__ __forceinline__ float2 mul2(float2 a, float2 b) {
