@@ -90,13 +90,19 @@ enum {
   NVFP4KV_DEVERR_LENGTH = 4, /* a length < 0 or > max_pages_per_seq * page_size: clamped */
   NVFP4KV_DEVERR_TIMEOUT = 8, /* a copy into shared memory (or a tensor-core step) did not
                                  complete within ~1 s: the call's outputs are not valid */
-  NVFP4KV_DEVERR_ROW = 16     /* a workspace row outside [0, total_rows): that row was skipped
+  NVFP4KV_DEVERR_ROW = 16,    /* a workspace row outside [0, total_rows): that row was skipped
                                  (an attention key reads as zero) */
+  NVFP4KV_DEVERR_POOL = 32,   /* too few free pages, or places for tokens, for every request of a
+                                 plan: that one and those behind it got none */
+  NVFP4KV_DEVERR_POSITION = 64 /* a position outside [0, max_position): that token was not rotated */
 };
 
 /* Bytes of one page-head: 16 rows of K data and scales, then of V (9/16 byte
  * per value). */
 #define NVFP4KV_PAGE_HEAD_BYTES 2304
+/* Bytes of one page-head's digest: 128 upper and 128 lower bounds, a scale, 12
+ * zero bytes (nvfp4kv_page_digest). */
+#define NVFP4KV_DIGEST_BYTES 272
 /* Bytes of one page-head of the MXFP4 variant's pool (4 E8M0 scale bytes per
  * row): K data [0, 1024), K scales [1024, 1088) token-major, V data
  * [1088, 2112) by token pair as in the NVFP4 page-head, V scales
@@ -560,6 +566,159 @@ int nvfp4kv_evict(const nvfp4kv_cache* cache, const int32_t* page_table, int32_t
                   int32_t budget, int32_t first, int32_t recent, const int32_t* dst_page_table,
                   int32_t dst_max_pages_per_seq, int32_t* kept, float* kept_weights, int64_t kept_stride,
                   int32_t* new_lens, int32_t* device_status, nvfp4kv_stream_t stream);
+
+/* Where a step's new tokens go, worked out on the GPU, so that a captured step
+ * needs nothing from the host but the requests' lengths.  Request b of `batch`
+ * has cached_lens[b] tokens in the cache and new_lens[b] more to come; it needs
+ * ceil((cached + new) / page_size) - ceil(cached / page_size) more pages.  Requests
+ * are served in order, until one needs more pages than are left or more tokens
+ * than there is room for: that one and all behind it get nothing (as if their
+ * new_lens were 0), with NVFP4KV_DEVERR_POOL if they had new tokens.
+ *   page_table    device int32 [batch][max_pages_per_seq], in and out: the cached
+ *                 tokens' pages stay, entries behind them get the new ones, others
+ *                 are left alone
+ *   cached_lens   device int32 [batch], >= 0 and <= max_pages_per_seq * page_size
+ *   new_lens      device int32 [batch], >= 0, likewise with the cached ones (cut to
+ *                 that with NVFP4KV_DEVERR_LENGTH)
+ *   free_pages    device int32 [free_capacity]: a stack of page ids, the top at
+ *                 *free_count - 1; the n-th page needed is the n-th from the top.
+ *                 Not written: pages are given back by storing them from
+ *                 *free_count on and raising the count
+ *   free_count    device int32 (outside [0, free_capacity]: cut to it with
+ *                 NVFP4KV_DEVERR_LENGTH)
+ *   num_pages     of the cache; a page id outside [0, num_pages) gives its tokens
+ *                 the slot -1 with NVFP4KV_DEVERR_PAGE
+ *   max_tokens    room for new tokens in the arrays below
+ * Outputs, device; the optional ones may be NULL:
+ *   seq_lens      int32 [batch]: cached + new.  May be cached_lens itself
+ *   slot_mapping  int64 [max_tokens]: the slot of each new token, request by
+ *                 request; -1 (which an append skips) behind the last one
+ *   positions     int32 [max_tokens], optional: its position; 0 behind the last
+ *   cu_q          int64 [batch + 1], optional: the requests' first new tokens
+ *   ws_rows       int64 [max_tokens], optional: its row of an FP8 workspace that holds
+ *                 every request's tokens one request after the other; -1 behind the last
+ *   cu_prefix     int64 [batch + 1], optional: the requests' first workspace rows
+ *   free_left     int32: the count without the pages taken.  May be free_count itself
+ * Enqueues one kernel, which reads and writes its few pages' worth of data from
+ * one cluster of CTAs. */
+int nvfp4kv_plan_append(int32_t* page_table, int32_t max_pages_per_seq, const int32_t* cached_lens,
+                        const int32_t* new_lens, int32_t batch, const int32_t* free_pages, int32_t free_capacity,
+                        const int32_t* free_count, int64_t num_pages, int64_t max_tokens, int32_t* seq_lens,
+                        int64_t* slot_mapping, int32_t* positions, int64_t* cu_q, int64_t* ws_rows,
+                        int64_t* cu_prefix, int32_t* free_left, int32_t* device_status, nvfp4kv_stream_t stream);
+
+/* What nvfp4kv_norm_rope_append does to queries and keys. */
+typedef struct nvfp4kv_norm_rope {
+  const void* q_weight; /* device bf16 [head_dim], 16-byte aligned, or NULL: no norm of the queries */
+  const void* k_weight; /* the same of the keys */
+  float eps;            /* finite, > 0 (with a weight) */
+  int32_t rotary_dim;   /* the first rotary_dim values turn: 0 (none), 32, 64, 96 or 128 */
+  int32_t interleaved;  /* pairs (2i, 2i + 1) if not 0, else (i, i + rotary_dim / 2) */
+} nvfp4kv_norm_rope;
+
+/* Root-mean-square norms of queries and keys for each head, the rotation by their
+ * positions, and the append of keys and values to the cache (and to the FP8
+ * workspace), in one pass over the projection's output.  For each row x of 128
+ * values of a token's query or key head, every step one IEEE binary32 operation
+ * rounded to nearest:
+ *     r = 1 / sqrt(sum * (1 / 128) + eps),  sum = the tree of neighbours' sums
+ *         ((x_0^2 + x_1^2) + (x_2^2 + x_3^2)) + ... (seven levels)
+ *     y = (x * r) * weight
+ *     y_a <- y_a * cos - y_b * sin,  y_b <- y_b * cos + y_a * sin   for each pair (a, b)
+ * then rounded to bf16.  Queries are stored; keys, and values as they are, are
+ * quantised exactly as nvfp4kv_quantize_append (and, with ws_rows,
+ * nvfp4kv_bf16_to_fp8_workspace) would quantise those bf16 rows.
+ *   q, k, v       device bf16 [num_tokens][heads][head_dim], 16-byte aligned; from one
+ *                 token to the next q_stride, k_stride, v_stride elements (multiples of 8,
+ *                 at least a token's heads * head_dim): parts of one projection's rows are
+ *                 taken as they lie
+ *   slot_mapping  device int64 [num_tokens], as in nvfp4kv_quantize_append (a
+ *                 skipped token's queries are made all the same)
+ *   positions     device int32 [num_tokens] (NULL with rotary_dim 0); outside
+ *                 [0, max_position): not rotated, NVFP4KV_DEVERR_POSITION
+ *   cos_sin       device fp32 [max_position][rotary_dim], 16-byte aligned: the cosines of the
+ *                 rotary_dim / 2 pairs' angles, then their sines
+ *   how           host struct
+ *   q_out         device bf16 [num_tokens][num_q_heads][head_dim] with q_out_stride; may
+ *                 be q itself (with q_stride), and must not overlap q otherwise, nor k or v
+ *   ws_rows       device int64 [num_tokens], or NULL: no workspace (total_rows, the scales,
+ *                 ws_k and ws_v are then not looked at)
+ * num_tokens * heads < 2^31.  Values up to 2^60 in size have exact norms.  Enqueues
+ * one kernel. */
+int nvfp4kv_norm_rope_append(const nvfp4kv_cache* cache, const void* q, int64_t q_stride, const void* k,
+                             int64_t k_stride, const void* v, int64_t v_stride, int32_t num_q_heads,
+                             int64_t num_tokens, const int64_t* slot_mapping, const int32_t* positions,
+                             const float* cos_sin, int32_t max_position, const nvfp4kv_norm_rope* how, void* q_out,
+                             int64_t q_out_stride, const int64_t* ws_rows, int64_t total_rows, float k_ws_scale,
+                             float v_ws_scale, uint8_t* ws_k, uint8_t* ws_v, int32_t* device_status,
+                             nvfp4kv_stream_t stream);
+
+/* Reading a part of a long cache: each page's keys are bounded once
+ * (nvfp4kv_page_digest), a decode step bounds each page's scores from that
+ * (nvfp4kv_page_scores, an eighth of the page's bytes), picks pages for every KV head
+ * (nvfp4kv_select_pages) and attends to those alone
+ * (nvfp4kv_decode_attention_selected).
+ *
+ * nvfp4kv_page_digest: for the pages of sequence b from token first_tokens[b] on, and
+ * each KV head, with k the page's cached keys e2m1 * e4m3 (without the global scale):
+ *     hi_d = max k_d,  lo_d = min k_d           over the page's tokens < seq_lens[b]
+ *     scale = 2^(floor(log2 max(|hi|, |lo|)) - 7)      (1 where all are 0)
+ *     bytes [0, 128): E4M3 of hi / scale rounded up; [128, 256): of lo / scale rounded
+ *     down; [256, 260): scale (fp32); [260, 272): zeros
+ *   digest        device uint8 [num_pages][num_kv_heads][NVFP4KV_DIGEST_BYTES], 16-byte
+ *                 aligned, by page id as the cache is; other pages' are left alone
+ *   first_tokens  device int32 [batch], or NULL: from the start.  After an append, the
+ *                 sequence's length before it: the page that it falls into is made anew
+ * Two sequences that share pages write the same bytes, if both see them whole.
+ * A page id outside the pool is skipped with NVFP4KV_DEVERR_PAGE; a length outside the
+ * page table is clamped with NVFP4KV_DEVERR_LENGTH. */
+int nvfp4kv_page_digest(const nvfp4kv_cache* cache, const int32_t* page_table, int32_t max_pages_per_seq,
+                        const int32_t* seq_lens, const int32_t* first_tokens, int32_t batch, uint8_t* digest,
+                        int32_t* device_status, nvfp4kv_stream_t stream);
+
+/* nvfp4kv_page_scores: for every page p of sequence b and each KV head,
+ *     scores[b][hk][p] = softmax_scale * g_K * scale * max over the head's G query heads
+ *                        of sum_d max(q_d hi_d, q_d lo_d)
+ * which no token's softmax_scale * q . khat in the page exceeds (but for fp32's
+ * rounding).  cache gives the pool's size and g_K; its pages are not read.
+ *   q             device bf16 [batch][num_q_heads][head_dim], 16-byte aligned; G <= 8
+ *   scores        device fp32 [batch][num_kv_heads][score_stride]; entries behind a
+ *                 sequence's last page are left alone.  A longer sequence's pages from
+ *                 score_stride on get none, with NVFP4KV_DEVERR_LENGTH
+ * A page id outside the pool scores -inf with NVFP4KV_DEVERR_PAGE. */
+int nvfp4kv_page_scores(const nvfp4kv_cache* cache, const uint8_t* digest, const void* q, const int32_t* page_table,
+                        int32_t max_pages_per_seq, const int32_t* seq_lens, int32_t batch, int32_t num_q_heads,
+                        float softmax_scale, float* scores, int64_t score_stride, int32_t* device_status,
+                        nvfp4kv_stream_t stream);
+
+/* nvfp4kv_select_pages: of the n = ceil(seq_lens[b] / page_size) pages of a sequence,
+ * all if there are no more than budget; else the first `first`, the last `recent`, and of
+ * those between the budget - first - recent with the largest scores (equal scores: the
+ * lower page; a NaN counts as larger than any number).
+ *   scores        device fp32 [batch][num_kv_heads][score_stride], score_stride >= every n
+ *                 (longer sequences are cut there with NVFP4KV_DEVERR_LENGTH)
+ *   budget, first, recent   0 < budget <= 2^27, first >= 0, recent >= 0, first + recent <= budget
+ *   selected      device int32 [batch][num_kv_heads][budget]: the pages' indices in the
+ *                 sequence, ascending; -1 from min(n, budget) on */
+int nvfp4kv_select_pages(const float* scores, int64_t score_stride, const int32_t* seq_lens, int32_t batch,
+                         int32_t num_kv_heads, int32_t budget, int32_t first, int32_t recent, int32_t* selected,
+                         int32_t* device_status, nvfp4kv_stream_t stream);
+
+/* nvfp4kv_decode_attention_scored (without a scoring) over the selected pages alone: the
+ * softmax runs over the tokens < seq_lens[b] of the pages that the KV head's list names.
+ *   selected      device int32 [batch][num_kv_heads][budget]: page indices in the sequence,
+ *                 in any order, each at most once (one named twice counts twice); an
+ *                 entry below 0 names none.  Only the first min(budget, n) entries of a
+ *                 list are looked at, n = ceil(seq_lens[b] / page_size).  An index >= n is
+ *                 skipped with NVFP4KV_DEVERR_PAGE
+ * A list that names no page gives zeros, and a log-sum-exp of -inf.  Page-table entries of
+ * other pages are not looked at.  Other arguments, the workspace
+ * (nvfp4kv_decode_workspace_size) and errors as in nvfp4kv_decode_attention_scored. */
+int nvfp4kv_decode_attention_selected(const nvfp4kv_cache* cache, const void* q, void* out, float* lse,
+                                      const int32_t* page_table, int32_t max_pages_per_seq, const int32_t* seq_lens,
+                                      int32_t batch, int32_t num_q_heads, float softmax_scale,
+                                      const int32_t* selected, int32_t budget, void* workspace,
+                                      size_t workspace_bytes, int32_t* device_status, nvfp4kv_stream_t stream);
 
 /* Global-scale calibration ("nvfp4-kv-cache-memory-wall", section 2: the
  * FP32 per-tensor scale is 1 in the uncalibrated public setting; a calibrated

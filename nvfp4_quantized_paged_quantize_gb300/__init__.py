@@ -28,6 +28,8 @@ NVFP4KV_DEVERR_PAGE = 2
 NVFP4KV_DEVERR_LENGTH = 4
 NVFP4KV_DEVERR_TIMEOUT = 8
 NVFP4KV_DEVERR_ROW = 16
+NVFP4KV_DEVERR_POOL = 32
+NVFP4KV_DEVERR_POSITION = 64
 NVFP4KV_PROBE_DECODE_PATTERN = 0
 NVFP4KV_PROBE_WHOLE_PAGES = 1
 NVFP4KV_VARIANT_SR = 1
@@ -39,6 +41,8 @@ PAGE_SIZE = 16
 # bytes of one page-head (16 tokens of one KV head): K data, K scales, V data, V scales
 NVFP4KV_PAGE_HEAD_BYTES = 2304
 NVFP4KV_MXFP4_PAGE_HEAD_BYTES = 2176
+# bytes of one page-head's digest: 128 upper and 128 lower bounds, the scale, padding
+NVFP4KV_DIGEST_BYTES = 272
 
 _lib = None
 
@@ -67,6 +71,11 @@ class _CCache(ctypes.Structure):
 class _CScoring(ctypes.Structure):
     _fields_ = [("softcap", ctypes.c_float), ("window", ctypes.c_int32), ("sinks", ctypes.c_int32),
                 ("slopes", ctypes.c_void_p)]
+
+
+class _CNormRope(ctypes.Structure):
+    _fields_ = [("q_weight", ctypes.c_void_p), ("k_weight", ctypes.c_void_p), ("eps", ctypes.c_float),
+                ("rotary_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32)]
 
 
 def load(path: str | None = None, build_if_missing: bool = True):
@@ -116,6 +125,13 @@ def load(path: str | None = None, build_if_missing: bool = True):
     L.nvfp4kv_extend_attention_scored.argtypes = [vp, vp, i32, vp, vp, vp, vp, i32, i64, i32, i32, i32, f32, f32, f32,
                                                   ps, vp, vp, vp, vp, vp, vp]
     L.nvfp4kv_evict.argtypes = [pc, vp, i32, vp, i32, vp, i64, i32, i32, i32, vp, i32, vp, vp, i64, vp, vp, vp]
+    L.nvfp4kv_plan_append.argtypes = [vp, i32, vp, vp, i32, vp, i32, vp, i64, i64, vp, vp, vp, vp, vp, vp, vp, vp, vp]
+    L.nvfp4kv_norm_rope_append.argtypes = [pc, vp, i64, vp, i64, vp, i64, i32, i64, vp, vp, vp, i32,
+                                           ctypes.POINTER(_CNormRope), vp, i64, vp, i64, f32, f32, vp, vp, vp, vp]
+    L.nvfp4kv_page_digest.argtypes = [pc, vp, i32, vp, vp, i32, vp, vp, vp]
+    L.nvfp4kv_page_scores.argtypes = [pc, vp, vp, vp, i32, vp, i32, i32, f32, vp, i64, vp, vp]
+    L.nvfp4kv_select_pages.argtypes = [vp, i64, vp, i32, i32, i32, i32, i32, vp, vp, vp]
+    L.nvfp4kv_decode_attention_selected.argtypes = [pc, vp, vp, vp, vp, i32, vp, i32, i32, f32, vp, i32, vp, sz, vp, vp]
     L.nvfp4kv_last_cuda_error.argtypes = []
     L.nvfp4kv_last_cuda_error.restype = ctypes.c_char_p
     L.nvfp4kv_status_string.argtypes = [ctypes.c_int]
@@ -127,7 +143,9 @@ def load(path: str | None = None, build_if_missing: bool = True):
                  "nvfp4kv_extend_attention", "nvfp4kv_quantize_append_fp8", "nvfp4kv_quantize_append_variant",
                  "nvfp4kv_stream_probe", "nvfp4kv_decode_attention_variant", "nvfp4kv_decode_attention_scored",
                  "nvfp4kv_decode_weights_workspace_size", "nvfp4kv_decode_attention_weights",
-                 "nvfp4kv_extend_attention_scored", "nvfp4kv_evict"):
+                 "nvfp4kv_extend_attention_scored", "nvfp4kv_evict", "nvfp4kv_plan_append", "nvfp4kv_norm_rope_append",
+                 "nvfp4kv_page_digest", "nvfp4kv_page_scores", "nvfp4kv_select_pages",
+                 "nvfp4kv_decode_attention_selected"):
         getattr(L, name).restype = ctypes.c_int
     _lib = L
     return L
@@ -456,6 +474,178 @@ def nvfp4kv_evict(cache: "Cache", page_table, seq_lens, weights, budget: int, fi
                               kept_stride, _ptr(new_lens), _ptr(device_status), _stream(stream)))
 
 
+def nvfp4kv_plan_append(page_table, cached_lens, new_lens, free_pages, free_count, num_pages: int, seq_lens,
+                        slot_mapping, free_left, positions=None, cu_q=None, ws_rows=None, cu_prefix=None,
+                        device_status=None, stream=None) -> None:
+    """Where a step's new tokens go: new page-table entries (page_table int32 [B, max_pages], in place) off the stack
+    free_pages (int32 [n], its top at free_count - 1), seq_lens = cached_lens + new_lens (int32 [B]; seq_lens may be
+    cached_lens), slot_mapping (int64 [tokens], -1 behind the last new token) and, where given, positions (int32
+    [tokens]), ws_rows (int64 [tokens]), cu_q and cu_prefix (int64 [B + 1]).  free_count and free_left: int32 [1],
+    may be one tensor."""
+    t = _types()
+    B, maxp = _shape("page_table", page_table, 2)
+    tokens, capacity = _shape("slot_mapping", slot_mapping, 1)[0], _shape("free_pages", free_pages, 1)[0]
+    gpu = _current_gpu(page_table)
+    _check_tensor("page_table", page_table, t.int32, (B, maxp), gpu)
+    _check_tensor("cached_lens", cached_lens, t.int32, (B,), gpu)
+    _check_tensor("new_lens", new_lens, t.int32, (B,), gpu)
+    _check_tensor("free_pages", free_pages, t.int32, (capacity,), gpu)
+    _check_tensor("free_count", free_count, t.int32, (1,), gpu)
+    _check_tensor("seq_lens", seq_lens, t.int32, (B,), gpu)
+    _check_tensor("slot_mapping", slot_mapping, t.int64, (tokens,), gpu)
+    _check_tensor("free_left", free_left, t.int32, (1,), gpu)
+    if positions is not None:
+        _check_tensor("positions", positions, t.int32, (tokens,), gpu)
+    if cu_q is not None:
+        _check_tensor("cu_q", cu_q, t.int64, (B + 1,), gpu)
+    if ws_rows is not None:
+        _check_tensor("ws_rows", ws_rows, t.int64, (tokens,), gpu)
+    if cu_prefix is not None:
+        _check_tensor("cu_prefix", cu_prefix, t.int64, (B + 1,), gpu)
+    _check_memory("device_status", device_status, gpu)
+    _check("nvfp4kv_plan_append",
+           _L().nvfp4kv_plan_append(_ptr(page_table), maxp, _ptr(cached_lens), _ptr(new_lens), B, _ptr(free_pages),
+                                    capacity, _ptr(free_count), int(num_pages), tokens, _ptr(seq_lens),
+                                    _ptr(slot_mapping), _ptr(positions), _ptr(cu_q), _ptr(ws_rows), _ptr(cu_prefix),
+                                    _ptr(free_left), _ptr(device_status), _stream(stream)))
+
+
+def _token_stride(name: str, x, gpu: int) -> int:
+    """Elements from one token of x (bf16 [tokens, heads, 128], a token's heads contiguous) to the next; raises
+    ValueError."""
+    _shape(name, x, 3)
+    if x.dtype is not _types().bfloat16 or x.get_device() != gpu or x.shape[2] != HEAD_DIM:
+        raise ValueError(f"{name}: expected bfloat16 [tokens, heads, {HEAD_DIM}] on the current device, got {x.dtype} "
+                         f"{tuple(x.shape)} on {x.device}")
+    token, head, value = x.stride()
+    if value != 1 or (x.shape[1] > 1 and head != HEAD_DIM):
+        raise ValueError(f"{name}: a token's heads are contiguous rows, got strides {x.stride()}")
+    return token if x.shape[0] > 1 else x.shape[1] * HEAD_DIM
+
+
+def nvfp4kv_norm_rope_append(cache: "Cache", q, k, v, slot_mapping, positions, cos_sin, q_out, q_weight=None,
+                             k_weight=None, eps: float = 1e-6, interleaved: bool = False, ws_rows=None, ws_k=None,
+                             ws_v=None, k_ws_scale: float = 1.0, v_ws_scale: float = 1.0, device_status=None,
+                             stream=None) -> None:
+    """Norms of queries and keys for each head (bf16 weights [128], or None), rotation by the positions' cosines and
+    sines (cos_sin fp32 [max_position, rotary_dim]; None: no rotation), then q_out (bf16 [n, Hq, 128], may be q) and
+    the quantised append of k and v at slot_mapping (and workspace rows ws_rows).  q: bf16 [n, Hq, 128], k and v:
+    bf16 [n, Hkv, 128], with any distance between tokens (parts of one projection's output)."""
+    if cache.mxfp4:
+        raise ValueError("the cache holds MXFP4 page-heads; this append writes NVFP4 ones")
+    t = _types()
+    n, hq, _ = _shape("q", q, 3)
+    gpu, hkv = _current_gpu(q), cache.num_kv_heads
+    strides = [_token_stride(name, x, gpu) for name, x in (("q", q), ("k", k), ("v", v), ("q_out", q_out))]
+    for name, x, heads in (("k", k, hkv), ("v", v, hkv), ("q_out", q_out, hq)):
+        if x.shape[0] != n or x.shape[1] != heads:
+            raise ValueError(f"{name}: expected {n} tokens of {heads} heads, got {tuple(x.shape)}")
+    _check_tensor("slot_mapping", slot_mapping, t.int64, (n,), gpu)
+    max_position, rot = (0, 0) if cos_sin is None else _shape("cos_sin", cos_sin, 2)
+    if cos_sin is not None:
+        _check_tensor("cos_sin", cos_sin, t.float32, (max_position, rot), gpu)
+        _check_tensor("positions", positions, t.int32, (n,), gpu)
+    for name, x in (("q_weight", q_weight), ("k_weight", k_weight)):
+        if x is not None:
+            _check_tensor(name, x, t.bfloat16, (HEAD_DIM,), gpu)
+    rows = 0
+    if ws_rows is not None:
+        rows = _shape("ws_k", ws_k, 3)[0]
+        _check_tensor("ws_rows", ws_rows, t.int64, (n,), gpu)
+        _check_tensor("ws_k", ws_k, t.uint8, (rows, hkv, HEAD_DIM), gpu)
+        _check_tensor("ws_v", ws_v, t.uint8, (rows, hkv, HEAD_DIM), gpu)
+    _check_memory("cache.pages", cache.pages, gpu)
+    _check_memory("device_status", device_status, gpu)
+    c = cache.c_struct()
+    how = _CNormRope(_ptr(q_weight), _ptr(k_weight), float(eps), rot, int(bool(interleaved)))
+    _check("nvfp4kv_norm_rope_append",
+           _L().nvfp4kv_norm_rope_append(ctypes.byref(c), _ptr(q), strides[0], _ptr(k), strides[1], _ptr(v),
+                                         strides[2], hq, n, _ptr(slot_mapping),
+                                         None if cos_sin is None else _ptr(positions), _ptr(cos_sin), max_position,
+                                         ctypes.byref(how), _ptr(q_out), strides[3], _ptr(ws_rows), rows,
+                                         float(k_ws_scale), float(v_ws_scale), _ptr(ws_k), _ptr(ws_v),
+                                         _ptr(device_status), _stream(stream)))
+
+
+def _check_digest(cache: "Cache", digest, page_table, seq_lens, device_status):
+    """Checks a digest's tensors; returns (batch, page-table columns, the current device)."""
+    if cache.mxfp4:
+        raise ValueError("the cache holds MXFP4 page-heads; a digest is made of NVFP4 ones")
+    t = _types()
+    B, maxp = _shape("page_table", page_table, 2)
+    gpu = _current_gpu(page_table)
+    _check_tensor("page_table", page_table, t.int32, (B, maxp), gpu)
+    _check_tensor("seq_lens", seq_lens, t.int32, (B,), gpu)
+    _check_tensor("digest", digest, t.uint8, (cache.num_pages, cache.num_kv_heads, NVFP4KV_DIGEST_BYTES), gpu)
+    _check_memory("cache.pages", cache.pages, gpu)
+    _check_memory("device_status", device_status, gpu)
+    return B, maxp, gpu
+
+
+def nvfp4kv_page_digest(cache: "Cache", page_table, seq_lens, digest, first_tokens=None, device_status=None,
+                        stream=None) -> None:
+    """Bounds of the pages' keys (digest: uint8 [num_pages, Hkv, 272], by page id): of each sequence's pages from
+    token first_tokens[b] on (int32 [B]; None: all of them)."""
+    B, maxp, gpu = _check_digest(cache, digest, page_table, seq_lens, device_status)
+    if first_tokens is not None:
+        _check_tensor("first_tokens", first_tokens, _types().int32, (B,), gpu)
+    c = cache.c_struct()
+    _check("nvfp4kv_page_digest",
+           _L().nvfp4kv_page_digest(ctypes.byref(c), _ptr(page_table), maxp, _ptr(seq_lens), _ptr(first_tokens), B,
+                                    _ptr(digest), _ptr(device_status), _stream(stream)))
+
+
+def nvfp4kv_page_scores(cache: "Cache", digest, q, page_table, seq_lens, softmax_scale: float, scores,
+                        device_status=None, stream=None) -> None:
+    """An upper bound of every page's scores (scores: fp32 [B, Hkv, >= pages]) for the queries q (bf16 [B, Hq, 128]),
+    from the pages' digests."""
+    t = _types()
+    B, maxp, gpu = _check_digest(cache, digest, page_table, seq_lens, device_status)
+    hq, stride = _shape("q", q, 3)[1], _shape("scores", scores, 3)[2]
+    _check_tensor("q", q, t.bfloat16, (B, hq, HEAD_DIM), gpu)
+    _check_tensor("scores", scores, t.float32, (B, cache.num_kv_heads, stride), gpu)
+    c = cache.c_struct()
+    _check("nvfp4kv_page_scores",
+           _L().nvfp4kv_page_scores(ctypes.byref(c), _ptr(digest), _ptr(q), _ptr(page_table), maxp, _ptr(seq_lens), B,
+                                    hq, float(softmax_scale), _ptr(scores), stride, _ptr(device_status),
+                                    _stream(stream)))
+
+
+def nvfp4kv_select_pages(scores, seq_lens, budget: int, first: int, recent: int, selected, device_status=None,
+                         stream=None) -> None:
+    """`budget` pages of every (sequence, KV head) -- the first `first`, the last `recent` and those of largest scores
+    (fp32 [B, Hkv, >= pages]) -- as ascending page indices, -1 past the end (selected: int32 [B, Hkv, budget])."""
+    t = _types()
+    B, hkv, stride = _shape("scores", scores, 3)
+    gpu = _current_gpu(scores)
+    _check_tensor("scores", scores, t.float32, (B, hkv, stride), gpu)
+    _check_tensor("seq_lens", seq_lens, t.int32, (B,), gpu)
+    _check_tensor("selected", selected, t.int32, (B, hkv, budget), gpu)
+    _check_memory("device_status", device_status, gpu)
+    _check("nvfp4kv_select_pages",
+           _L().nvfp4kv_select_pages(_ptr(scores), stride, _ptr(seq_lens), B, hkv, budget, first, recent,
+                                     _ptr(selected), _ptr(device_status), _stream(stream)))
+
+
+def nvfp4kv_decode_attention_selected(cache: "Cache", q, out, page_table, seq_lens, softmax_scale: float, selected,
+                                      workspace, lse=None, device_status=None, stream=None,
+                                      workspace_bytes: int | None = None) -> None:
+    """Paged decode attention over listed pages alone (selected: int32 [B, Hkv, budget] page indices in the sequence,
+    below 0 for none): q bf16 [B, Hq, 128], out bf16 [B, Hq, 128], lse fp32 [B, Hq] or None; the rest as
+    nvfp4kv_decode_attention."""
+    B, Hq, maxp, gpu = _check_decode(cache, q, out, page_table, seq_lens, lse, workspace, device_status)
+    budget = _shape("selected", selected, 3)[2]
+    _check_tensor("selected", selected, _types().int32, (B, cache.num_kv_heads, budget), gpu)
+    if workspace_bytes is None:
+        workspace_bytes = workspace.numel() * workspace.element_size()
+    c = cache.c_struct()
+    _check("nvfp4kv_decode_attention_selected",
+           _L().nvfp4kv_decode_attention_selected(ctypes.byref(c), _ptr(q), _ptr(out), _ptr(lse), _ptr(page_table),
+                                                  maxp, _ptr(seq_lens), B, Hq, float(softmax_scale), _ptr(selected),
+                                                  budget, _ptr(workspace), workspace_bytes, _ptr(device_status),
+                                                  _stream(stream)))
+
+
 def nvfp4kv_status_string(status: int) -> str:
     return _L().nvfp4kv_status_string(int(status)).decode()
 
@@ -658,4 +848,6 @@ __all__ = ["Cache", "Nvfp4kvError", "load", "NVFP4KV_PAGE_HEAD_BYTES", "NVFP4KV_
            "nvfp4kv_stream_probe", "NVFP4KV_PROBE_DECODE_PATTERN", "NVFP4KV_PROBE_WHOLE_PAGES",
            "nvfp4kv_decode_attention_variant", "Scoring", "nvfp4kv_decode_attention_scored",
            "nvfp4kv_decode_weights_workspace_size", "nvfp4kv_decode_attention_weights",
-           "nvfp4kv_extend_attention_scored", "nvfp4kv_evict"]
+           "nvfp4kv_extend_attention_scored", "nvfp4kv_evict", "NVFP4KV_DIGEST_BYTES", "nvfp4kv_plan_append",
+           "nvfp4kv_norm_rope_append", "nvfp4kv_page_digest", "nvfp4kv_page_scores", "nvfp4kv_select_pages",
+           "nvfp4kv_decode_attention_selected"]

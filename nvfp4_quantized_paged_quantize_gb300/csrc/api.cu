@@ -451,6 +451,214 @@ int nvfp4kv_evict(const nvfp4kv_cache* cache, const int32_t* page_table, int32_t
                                            device_status, nsm, reinterpret_cast<cudaStream_t>(stream)));
 }
 
+// ---------------------------------------------------------------------------
+// a step's plan, its normed and rotated append, and the pages that its decode reads
+// ---------------------------------------------------------------------------
+
+// Whether the n elements of two arrays share memory other than by being the same array.
+static bool overlap_at_offset(const int32_t* a, const int32_t* b, int64_t n) {
+  return a != b && a < b + n && b < a + n;
+}
+
+int nvfp4kv_plan_append(int32_t* page_table, int32_t max_pages_per_seq, const int32_t* cached_lens,
+                        const int32_t* new_lens, int32_t batch, const int32_t* free_pages, int32_t free_capacity,
+                        const int32_t* free_count, int64_t num_pages, int64_t max_tokens, int32_t* seq_lens,
+                        int64_t* slot_mapping, int32_t* positions, int64_t* cu_q, int64_t* ws_rows,
+                        int64_t* cu_prefix, int32_t* free_left, int32_t* device_status, nvfp4kv_stream_t stream) {
+  if (batch < 0 || max_pages_per_seq <= 0 || free_capacity < 0 || num_pages <= 0 || max_tokens < 0)
+    return NVFP4KV_ERR_INVALID_ARGUMENT;
+  if ((int64_t)max_pages_per_seq * kPageSize >= (int64_t(1) << 31) || max_tokens >= (int64_t(1) << 31) - (1 << 14) ||
+      num_pages * kPageSize >= (int64_t(1) << 31) || batch >= (1 << 30))
+    return NVFP4KV_ERR_UNSUPPORTED;
+  if (!free_count || !free_left || (free_capacity > 0 && !free_pages) || (max_tokens > 0 && !slot_mapping))
+    return NVFP4KV_ERR_INVALID_ARGUMENT;
+  if (batch > 0 && (!page_table || !cached_lens || !new_lens || !seq_lens)) return NVFP4KV_ERR_INVALID_ARGUMENT;
+  for (const void* ptr : {(const void*)page_table, (const void*)cached_lens, (const void*)new_lens,
+                          (const void*)free_pages, (const void*)free_count, (const void*)seq_lens,
+                          (const void*)positions, (const void*)free_left, (const void*)device_status})
+    if (!aligned(ptr, 4)) return NVFP4KV_ERR_INVALID_ARGUMENT;
+  for (const void* ptr : {(const void*)slot_mapping, (const void*)cu_q, (const void*)ws_rows, (const void*)cu_prefix})
+    if (!aligned(ptr, 8)) return NVFP4KV_ERR_INVALID_ARGUMENT;
+  // the lengths may be updated in place, but not at an offset
+  if (overlap_at_offset(seq_lens, cached_lens, batch) || (batch > 0 && seq_lens == new_lens) ||
+      overlap_at_offset(seq_lens, new_lens, batch))
+    return NVFP4KV_ERR_INVALID_ARGUMENT;
+  const nvfp4kv::PlanArgs a = {page_table, max_pages_per_seq, cached_lens, new_lens,  batch,  free_pages,
+                               free_capacity, free_count,     num_pages,   max_tokens, seq_lens, slot_mapping,
+                               positions,  cu_q,              ws_rows,     cu_prefix, free_left, device_status};
+  return cuda_status(nvfp4kv::launch_plan_append(a, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int nvfp4kv_norm_rope_append(const nvfp4kv_cache* cache, const void* q, int64_t q_stride, const void* k,
+                             int64_t k_stride, const void* v, int64_t v_stride, int32_t num_q_heads,
+                             int64_t num_tokens, const int64_t* slot_mapping, const int32_t* positions,
+                             const float* cos_sin, int32_t max_position, const nvfp4kv_norm_rope* how, void* q_out,
+                             int64_t q_out_stride, const int64_t* ws_rows, int64_t total_rows, float k_ws_scale,
+                             float v_ws_scale, uint8_t* ws_k, uint8_t* ws_v, int32_t* device_status,
+                             nvfp4kv_stream_t stream) {
+  int st = check_cache(cache);
+  if (st != NVFP4KV_OK) return st;
+  if (how == nullptr || num_tokens < 0 || num_q_heads <= 0) return NVFP4KV_ERR_INVALID_ARGUMENT;
+  if (how->rotary_dim < 0 || how->rotary_dim > kHeadDim || how->rotary_dim % 32 != 0) return NVFP4KV_ERR_UNSUPPORTED;
+  if (!aligned(how->q_weight, 16) || !aligned(how->k_weight, 16)) return NVFP4KV_ERR_INVALID_ARGUMENT;
+  if ((how->q_weight || how->k_weight) && !positive_finite(how->eps)) return NVFP4KV_ERR_INVALID_ARGUMENT;
+  if (how->rotary_dim > 0 && max_position <= 0) return NVFP4KV_ERR_INVALID_ARGUMENT;
+  // rows of one token do not run into the next token's, and start on 16 bytes
+  const int64_t q_row = (int64_t)num_q_heads * kHeadDim, kv_row = (int64_t)cache->num_kv_heads * kHeadDim;
+  if (q_stride < q_row || q_out_stride < q_row || k_stride < kv_row || v_stride < kv_row || q_stride % 8 != 0 ||
+      q_out_stride % 8 != 0 || k_stride % 8 != 0 || v_stride % 8 != 0)
+    return NVFP4KV_ERR_INVALID_ARGUMENT;
+  if (ws_rows &&
+      (total_rows < 0 || !positive_finite(k_ws_scale) || !positive_finite(v_ws_scale)))
+    return NVFP4KV_ERR_INVALID_ARGUMENT;
+  if (device_status && !aligned(device_status, 4)) return NVFP4KV_ERR_INVALID_ARGUMENT;
+  if (num_tokens == 0) return NVFP4KV_OK;
+  const int64_t most = int64_t(1) << 40;
+  if (num_tokens >= (int64_t(1) << 31) / (num_q_heads > cache->num_kv_heads ? num_q_heads : cache->num_kv_heads) ||
+      q_stride > most || q_out_stride > most || k_stride > most || v_stride > most || total_rows > most)
+    return NVFP4KV_ERR_UNSUPPORTED;
+  if (!q || !k || !v || !slot_mapping || !q_out || (how->rotary_dim > 0 && (!positions || !cos_sin)))
+    return NVFP4KV_ERR_INVALID_ARGUMENT;
+  if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(q_out, 16) || !aligned(cos_sin, 16) ||
+      !aligned(slot_mapping, 8) || !aligned(positions, 4))
+    return NVFP4KV_ERR_INVALID_ARGUMENT;
+  if (ws_rows && (!ws_k || !ws_v || !aligned(ws_rows, 8) || !aligned(ws_k, 16) || !aligned(ws_v, 16)))
+    return NVFP4KV_ERR_INVALID_ARGUMENT;
+  // normed queries may replace their inputs, not lie across them
+  const uint16_t *q0 = static_cast<const uint16_t*>(q), *o0 = static_cast<const uint16_t*>(q_out);
+  if (q_out == q ? q_out_stride != q_stride
+                 : o0 < q0 + (num_tokens - 1) * q_stride + q_row && q0 < o0 + (num_tokens - 1) * q_out_stride + q_row)
+    return NVFP4KV_ERR_INVALID_ARGUMENT;
+  int nsm = 0;
+  if ((st = current_num_sms(&nsm)) != NVFP4KV_OK) return st;
+  nvfp4kv::NormRopeArgs a = {};
+  a.q = static_cast<const uint16_t*>(q);
+  a.k = static_cast<const uint16_t*>(k);
+  a.v = static_cast<const uint16_t*>(v);
+  a.q_stride = q_stride;
+  a.k_stride = k_stride;
+  a.v_stride = v_stride;
+  a.q_out = static_cast<uint16_t*>(q_out);
+  a.q_out_stride = q_out_stride;
+  a.q_weight = static_cast<const uint16_t*>(how->q_weight);
+  a.k_weight = static_cast<const uint16_t*>(how->k_weight);
+  a.eps = how->eps;
+  a.cos_sin = cos_sin;
+  a.rot = how->rotary_dim;
+  a.max_position = max_position;
+  a.interleaved = how->interleaved != 0;
+  a.positions = positions;
+  a.slots = slot_mapping;
+  a.ntok = (int32_t)num_tokens;
+  a.hq = num_q_heads;
+  a.hkv = cache->num_kv_heads;
+  a.capacity = cache->num_pages * (int64_t)kPageSize;
+  a.pages = cache->pages;
+  a.gk = cache->k_global_scale;
+  a.gv = cache->v_global_scale;
+  a.ws_rows = ws_rows;
+  a.ws_total_rows = total_rows;
+  a.ws_k = ws_k;
+  a.ws_v = ws_v;
+  a.status = device_status;
+  return cuda_status(nvfp4kv::launch_norm_rope_append(a, ws_rows ? k_ws_scale : 1.0f, ws_rows ? v_ws_scale : 1.0f, nsm,
+                                                      reinterpret_cast<cudaStream_t>(stream)));
+}
+
+// Host checks of what the digest and the page scores share (nothing is enqueued).
+static int check_digest(const nvfp4kv_cache* cache, const int32_t* page_table, int32_t max_pages_per_seq,
+                        const int32_t* seq_lens, int32_t batch, const uint8_t* digest, const int32_t* device_status) {
+  const int st = check_cache(cache);
+  if (st != NVFP4KV_OK) return st;
+  if (batch < 0 || max_pages_per_seq <= 0 || !aligned(device_status, 4)) return NVFP4KV_ERR_INVALID_ARGUMENT;
+  if (batch == 0) return NVFP4KV_OK;
+  if ((int64_t)batch * max_pages_per_seq * cache->num_kv_heads >= (int64_t(1) << 31) ||
+      (int64_t)max_pages_per_seq * kPageSize >= (int64_t(1) << 31))
+    return NVFP4KV_ERR_UNSUPPORTED;
+  if (!page_table || !seq_lens || !digest) return NVFP4KV_ERR_INVALID_ARGUMENT;
+  if (!aligned(page_table, 4) || !aligned(seq_lens, 4) || !aligned(digest, 16)) return NVFP4KV_ERR_INVALID_ARGUMENT;
+  return NVFP4KV_OK;
+}
+
+static nvfp4kv::DigestArgs digest_args(const nvfp4kv_cache& c, const int32_t* page_table, int32_t max_pages_per_seq,
+                                       const int32_t* seq_lens, const int32_t* first_tokens, int32_t batch,
+                                       uint8_t* digest, int32_t* device_status) {
+  return nvfp4kv::DigestArgs{c.pages,  (int32_t)c.num_pages, c.num_kv_heads, page_table, max_pages_per_seq,
+                             seq_lens, first_tokens,         batch,          digest,     device_status};
+}
+
+int nvfp4kv_page_digest(const nvfp4kv_cache* cache, const int32_t* page_table, int32_t max_pages_per_seq,
+                        const int32_t* seq_lens, const int32_t* first_tokens, int32_t batch, uint8_t* digest,
+                        int32_t* device_status, nvfp4kv_stream_t stream) {
+  int st = check_digest(cache, page_table, max_pages_per_seq, seq_lens, batch, digest, device_status);
+  if (st != NVFP4KV_OK) return st;
+  if (!aligned(first_tokens, 4)) return NVFP4KV_ERR_INVALID_ARGUMENT;
+  if (batch == 0) return NVFP4KV_OK;
+  int nsm = 0;
+  if ((st = current_num_sms(&nsm)) != NVFP4KV_OK) return st;
+  return cuda_status(nvfp4kv::launch_page_digest(
+      digest_args(*cache, page_table, max_pages_per_seq, seq_lens, first_tokens, batch, digest, device_status), nsm,
+      reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int nvfp4kv_page_scores(const nvfp4kv_cache* cache, const uint8_t* digest, const void* q, const int32_t* page_table,
+                        int32_t max_pages_per_seq, const int32_t* seq_lens, int32_t batch, int32_t num_q_heads,
+                        float softmax_scale, float* scores, int64_t score_stride, int32_t* device_status,
+                        nvfp4kv_stream_t stream) {
+  int st = check_digest(cache, page_table, max_pages_per_seq, seq_lens, batch, digest, device_status);
+  if (st != NVFP4KV_OK) return st;
+  if (num_q_heads <= 0 || num_q_heads % cache->num_kv_heads != 0 || score_stride <= 0)
+    return NVFP4KV_ERR_INVALID_ARGUMENT;
+  if (num_q_heads / cache->num_kv_heads > 8) return NVFP4KV_ERR_UNSUPPORTED;
+  if (!positive_finite(softmax_scale)) return NVFP4KV_ERR_INVALID_ARGUMENT;
+  if (batch == 0) return NVFP4KV_OK;
+  if (score_stride > (int64_t(1) << 40)) return NVFP4KV_ERR_UNSUPPORTED;
+  if (!q || !scores || !aligned(q, 16) || !aligned(scores, 4)) return NVFP4KV_ERR_INVALID_ARGUMENT;
+  int nsm = 0;
+  if ((st = current_num_sms(&nsm)) != NVFP4KV_OK) return st;
+  const nvfp4kv::ScoreArgs a = {
+      digest_args(*cache, page_table, max_pages_per_seq, seq_lens, nullptr, batch, const_cast<uint8_t*>(digest),
+                  device_status),
+      static_cast<const uint16_t*>(q), num_q_heads / cache->num_kv_heads, softmax_scale * cache->k_global_scale, scores,
+      score_stride};
+  return cuda_status(nvfp4kv::launch_page_scores(a, nsm, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int nvfp4kv_select_pages(const float* scores, int64_t score_stride, const int32_t* seq_lens, int32_t batch,
+                         int32_t num_kv_heads, int32_t budget, int32_t first, int32_t recent, int32_t* selected,
+                         int32_t* device_status, nvfp4kv_stream_t stream) {
+  if (batch < 0 || num_kv_heads <= 0 || score_stride <= 0) return NVFP4KV_ERR_INVALID_ARGUMENT;
+  if (budget <= 0 || first < 0 || recent < 0 || (int64_t)first + recent > budget) return NVFP4KV_ERR_INVALID_ARGUMENT;
+  // pages of a sequence fit 27 bits, as its tokens fit 31
+  if (budget > (1 << 27) || (int64_t)batch * num_kv_heads >= (int64_t(1) << 27) || score_stride > (int64_t(1) << 40))
+    return NVFP4KV_ERR_UNSUPPORTED;
+  if (!aligned(device_status, 4)) return NVFP4KV_ERR_INVALID_ARGUMENT;
+  if (batch == 0) return NVFP4KV_OK;
+  if (!scores || !seq_lens || !selected || !aligned(scores, 4) || !aligned(seq_lens, 4) || !aligned(selected, 4))
+    return NVFP4KV_ERR_INVALID_ARGUMENT;
+  const nvfp4kv::SelectArgs a = {scores, score_stride, seq_lens, batch, num_kv_heads, budget, first, recent, selected,
+                                 device_status};
+  return cuda_status(nvfp4kv::launch_select_pages(a, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int nvfp4kv_decode_attention_selected(const nvfp4kv_cache* cache, const void* q, void* out, float* lse,
+                                      const int32_t* page_table, int32_t max_pages_per_seq, const int32_t* seq_lens,
+                                      int32_t batch, int32_t num_q_heads, float softmax_scale,
+                                      const int32_t* selected, int32_t budget, void* workspace,
+                                      size_t workspace_bytes, int32_t* device_status, nvfp4kv_stream_t stream) {
+  int nsm = 0;
+  int st = check_decode(cache, q, static_cast<float*>(out), page_table, max_pages_per_seq, seq_lens, batch,
+                        num_q_heads, softmax_scale, workspace, workspace_bytes, device_status, &nsm);
+  if (st != NVFP4KV_OK) return st;
+  if (budget <= 0 || !aligned(lse, 4) || !aligned(selected, 4)) return NVFP4KV_ERR_INVALID_ARGUMENT;
+  if (batch == 0) return NVFP4KV_OK;
+  if (!selected) return NVFP4KV_ERR_INVALID_ARGUMENT;
+  return cuda_status(nvfp4kv::launch_decode_selected(
+      *cache, static_cast<const uint16_t*>(q), static_cast<uint16_t*>(out), lse, page_table, max_pages_per_seq,
+      seq_lens, batch, num_q_heads, softmax_scale, selected, budget, workspace, device_status, nsm,
+      reinterpret_cast<cudaStream_t>(stream)));
+}
+
 int nvfp4kv_tensor_amax(const void* x_bf16, int64_t n, float* amax, int accumulate,
                         nvfp4kv_stream_t stream) {
   if (n < 0 || amax == nullptr || !aligned(amax, 4)) return NVFP4KV_ERR_INVALID_ARGUMENT;

@@ -89,7 +89,8 @@ enum : int {
   kScored = 1,   // bf16 output, log-sum-exp, a window with sinks (both run-time: they touch no inner loop)
   kCapped = 2,   // scores through cap * tanh(s / cap)
   kBiased = 4,   // minus slope * distance
-  kStored = 8    // the scores of every visited token are kept for weights_kernel
+  kStored = 8,   // the scores of every visited token are kept for weights_kernel
+  kSelected = 16 // only the pages that a list names are items (nvfp4kv_decode_attention_selected)
 };
 
 // stage layout: the page-head as stored (K data | K scales | V data | V scales)
@@ -142,6 +143,8 @@ struct DecodeParams {
   float* weights;        // [batch][hkv][weight_stride]
   long long weight_stride;
   float decay;
+  const int32_t* selected;  // kSelected: [batch][hkv][budget] pages of the sequence, below 0 for none
+  int32_t budget;
 };
 
 // ---------------------------------------------------------------------------
@@ -174,7 +177,10 @@ __device__ __forceinline__ VisiblePages visible_pages(const DecodeParams& p, int
   v.count = (L + kPage - 1) / kPage;
   v.lead = v.count;
   v.skip = 0;
-  if constexpr (M != 0) {
+  if constexpr ((M & kSelected) != 0) {
+    // as many items as the list has places for the sequence's pages
+    v.lead = v.count = min(v.count, p.budget);
+  } else if constexpr (M != 0) {
     if (p.window > 0 && L > p.window) {
       const int first = (L - p.window) / kPage;  // page of the window's first token
       v.lead = min(first, p.sinks / kPage + (p.sinks % kPage != 0));
@@ -269,7 +275,7 @@ struct ItemMap {
   int pair;    // b * hkv + h, -1 past the warp's range
   int page;    // page index within the sequence
   int np;      // pages of the pair
-  int lastnv;  // valid tokens in the pair's last page (1..16)
+  int lastnv;  // valid tokens in the pair's last page (1..16); kSelected: in this page (0: the list names none)
   int nv;      // after resolve_chunk: valid tokens of the item's page (0 for an invalid id or past the range)
   int hole;    // scored: rows [hole & 255, hole >> 8) of the page are out of sight (0: none)
   int dist;    // scored: the position of the page's first token minus the query's
@@ -321,8 +327,14 @@ __device__ __forceinline__ ItemMap map_chunk(const DecodeParams& p, long long wr
     m.page = page;
     m.np = np;
     m.lastnv = L - (np + v.skip - 1) * kPage;
-    const int at = page < v.lead ? page : page + v.skip;  // the page within the sequence
-    if constexpr (M != 0) {
+    int at = page < v.lead ? page : page + v.skip;  // the page within the sequence
+    if constexpr ((M & kSelected) != 0) {
+      at = __ldg(p.selected + (long long)m.pair * p.budget + page);
+      const bool named = at >= 0 && at < (L + kPage - 1) / kPage;
+      if (at >= 0 && !named) flag_error(p.status, NVFP4KV_DEVERR_PAGE);
+      at = named ? at : 0;
+      m.lastnv = named ? min(L - at * kPage, kPage) : 0;
+    } else if constexpr (M != 0) {
       const int t0 = at * kPage;
       m.dist = t0 - (L - 1);
       if (p.window > 0 && L > p.window) {
@@ -341,12 +353,13 @@ __device__ __forceinline__ ItemMap map_chunk(const DecodeParams& p, long long wr
 
 // Turn the loaded page ids of a chunk map into physical rows (-1 for an id out
 // of range, which is flagged); returns the valid-page bits (bit l: lane l).
+template <int M>
 __device__ __forceinline__ uint32_t resolve_chunk(const DecodeParams& p, ItemMap& m) {
-  const bool real = m.pair >= 0;
+  const bool real = m.pair >= 0 && ((M & kSelected) == 0 || m.lastnv > 0);
   const bool valid = real && m.row >= 0 && m.row < p.num_pages;
   if (real && !valid) flag_error(p.status, NVFP4KV_DEVERR_PAGE);
   m.row = valid ? m.row * p.hkv + m.h : -1;
-  m.nv = valid ? (m.page == m.np - 1 ? m.lastnv : kPage) : 0;
+  m.nv = valid ? ((M & kSelected) != 0 || m.page == m.np - 1 ? m.lastnv : kPage) : 0;
   return __ballot_sync(0xFFFFFFFFu, valid);
 }
 
@@ -1221,7 +1234,7 @@ __global__ void __launch_bounds__(kNW * 32, kCtasPerSm) decode_kernel(const Deco
       e.dist = M != 0 ? m.dist : 0;
       return e;
     };
-    resolve_chunk(p, cur);
+    resolve_chunk<M>(p, cur);
     tab[lane] = entry_of(cur);
     __syncwarp();
 
@@ -1254,7 +1267,7 @@ __global__ void __launch_bounds__(kNW * 32, kCtasPerSm) decode_kernel(const Deco
     // resolve the next chunk's map into the item table
 #define NVFP4KV_RESOLVE_NXT()                                          \
   {                                                                     \
-    resolve_chunk(p, nxt);                                              \
+    resolve_chunk<M>(p, nxt);                                           \
     tab[(32 * (chunk + 1) + lane) & 63] = entry_of(nxt);                \
     __syncwarp();                                                       \
   }
@@ -1855,6 +1868,20 @@ cudaError_t launch_decode_scored(const nvfp4kv_cache& c, const uint16_t* q, uint
   const dim3 grid((unsigned)(num_sms * kWeightBlocksPerSm));
   auto kernel = p.score_heads == 8 ? weights_kernel<4> : p.score_heads == 4 ? weights_kernel<2> : weights_kernel<1>;
   return launch_dependent(kernel, grid, kWeightWarps * 32, 0, stream, p);
+}
+
+cudaError_t launch_decode_selected(const nvfp4kv_cache& c, const uint16_t* q, uint16_t* out, float* lse,
+                                   const int32_t* page_table, int32_t max_pages, const int32_t* seq_lens,
+                                   int32_t batch, int32_t num_q_heads, float softmax_scale, const int32_t* selected,
+                                   int32_t budget, void* workspace, int32_t* device_status, int num_sms,
+                                   cudaStream_t stream) {
+  DecodeParams p = decode_params<kFmtNvfp4>(c, q, page_table, max_pages, seq_lens, batch, num_q_heads,
+                                            softmax_scale, workspace, device_status, num_sms);
+  p.out16 = out;
+  p.lse = lse;
+  p.selected = selected;
+  p.budget = budget;
+  return enqueue_scored<kScored | kSelected>(p, stream);
 }
 
 cudaError_t launch_decode(const nvfp4kv_cache& c, const uint16_t* q, float* out, const int32_t* page_table,

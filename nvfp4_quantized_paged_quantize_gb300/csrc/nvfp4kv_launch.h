@@ -132,6 +132,96 @@ cudaError_t launch_evict(const nvfp4kv_cache& c, const int32_t* page_table, int3
                          int32_t dst_max_pages, int32_t* kept, float* kept_weights, int64_t kept_stride,
                          int32_t* new_lens, int32_t* device_status, int num_sms, cudaStream_t stream);
 
+// Page tables, slots, positions and workspace rows of a step's new tokens.
+struct PlanArgs {
+  int32_t* page_table;  // [batch][max_pages], in and out
+  int32_t max_pages;
+  const int32_t* cached_lens;
+  const int32_t* new_lens;
+  int32_t batch;
+  const int32_t* free_pages;  // a stack, its top at free_count - 1
+  int32_t free_capacity;
+  const int32_t* free_count;
+  int64_t num_pages;
+  int64_t max_tokens;  // < 2^31
+  int32_t* seq_lens;      // may be cached_lens
+  int64_t* slot_mapping;  // [max_tokens]
+  int32_t* positions;     // [max_tokens], or null
+  int64_t* cu_q;          // [batch + 1], or null
+  int64_t* ws_rows;       // [max_tokens], or null
+  int64_t* cu_prefix;     // [batch + 1], or null
+  int32_t* free_left;     // may be free_count
+  int32_t* status;
+};
+cudaError_t launch_plan_append(const PlanArgs& args, cudaStream_t stream);
+
+// Norms and rotation of queries and keys, queries stored, keys and values appended.
+struct NormRopeArgs {
+  const uint16_t *q, *k, *v;
+  int64_t q_stride, k_stride, v_stride, q_out_stride;  // elements from one token to the next
+  uint16_t* q_out;
+  const uint16_t *q_weight, *k_weight;  // [128], or null: no norm
+  float eps;
+  const float* cos_sin;  // [max_position][rot]: cosines, then sines
+  int32_t rot;           // 0, or a multiple of 32 up to 128
+  int32_t max_position;
+  bool interleaved;
+  const int32_t* positions;
+  const int64_t* slots;
+  int32_t ntok, hq, hkv;
+  int64_t capacity;  // slots of the pool
+  uint8_t* pages;
+  float gk, gv;
+  const int64_t* ws_rows;  // or null: no workspace rows
+  int64_t ws_total_rows;
+  uint8_t *ws_k, *ws_v;
+  int32_t* status;
+};
+cudaError_t launch_norm_rope_append(const NormRopeArgs& args, float k_ws_scale, float v_ws_scale, int num_sms,
+                                    cudaStream_t stream);
+
+// Bounds of the pages' keys, and upper bounds of the pages' scores from them.
+struct DigestArgs {
+  const uint8_t* pages;
+  int32_t num_pages, hkv;
+  const int32_t* page_table;
+  int32_t max_pages;
+  const int32_t* seq_lens;
+  const int32_t* first_tokens;  // or null: from the start (digests only)
+  int32_t batch;
+  uint8_t* digest;  // [num_pages][hkv][NVFP4KV_DIGEST_BYTES]
+  int32_t* status;
+};
+cudaError_t launch_page_digest(const DigestArgs& args, int num_sms, cudaStream_t stream);
+struct ScoreArgs {
+  DigestArgs d;
+  const uint16_t* q;
+  int32_t group;
+  float score_scale;  // softmax_scale * g_K
+  float* scores;      // [batch][hkv][score_stride]
+  int64_t score_stride;
+};
+cudaError_t launch_page_scores(const ScoreArgs& args, int num_sms, cudaStream_t stream);
+
+// The first, the latest and the best scored pages of each (sequence, KV head).
+struct SelectArgs {
+  const float* scores;
+  int64_t score_stride;
+  const int32_t* seq_lens;
+  int32_t batch, hkv;
+  int32_t budget, first, recent;
+  int32_t* selected;  // [batch][hkv][budget]
+  int32_t* status;
+};
+cudaError_t launch_select_pages(const SelectArgs& args, cudaStream_t stream);
+
+// The decode over listed pages alone (bf16 out).
+cudaError_t launch_decode_selected(const nvfp4kv_cache& c, const uint16_t* q, uint16_t* out, float* lse,
+                                   const int32_t* page_table, int32_t max_pages, const int32_t* seq_lens,
+                                   int32_t batch, int32_t num_q_heads, float softmax_scale, const int32_t* selected,
+                                   int32_t budget, void* workspace, int32_t* device_status, int num_sms,
+                                   cudaStream_t stream);
+
 cudaError_t launch_decode(const nvfp4kv_cache& c, const uint16_t* q, float* out,
                           const int32_t* page_table, int32_t max_pages, const int32_t* seq_lens,
                           int32_t batch, int32_t num_q_heads, float softmax_scale, void* workspace,

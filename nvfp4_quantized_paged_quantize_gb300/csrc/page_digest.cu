@@ -1,0 +1,404 @@
+// page_digest.cu -- bounds of every page's keys (nvfp4kv_page_digest), and from
+// them an upper bound of every page's scores (nvfp4kv_page_scores), so that a
+// decode can leave out the pages that cannot matter much to it.
+//
+// With hi_d and lo_d the largest and smallest of the keys' dimension d in a page,
+// each token's score obeys
+//   q . k = sum_d q_d k_d <= sum_d max(q_d hi_d, q_d lo_d) = q+ . hi + q- . lo
+// (q+ = max(q, 0), q- = min(q, 0)): one product of twice the length.  A digest
+// keeps hi and lo in E4M3, rounded outwards so that the bound holds, times one
+// power of two per page-head that puts the largest into [128, 256).
+//
+// Both kernels cut the flattened list of their items evenly over all warps.
+#include "nvfp4kv_device.cuh"
+#include "nvfp4kv_launch.h"
+
+namespace nvfp4kv {
+namespace {
+
+constexpr int kDgThreads = 256;
+constexpr int kDgWarps = kDgThreads / 32;
+constexpr uint32_t kAll = 0xFFFFFFFFu;
+
+constexpr int kOffScale = 2 * kHeadDim;  // behind hi and lo
+constexpr int kDigestBytes = NVFP4KV_DIGEST_BYTES;
+static_assert(kDigestBytes == kOffScale + 16, "a digest's tail keeps the next one 16-byte aligned");
+
+// A sequence's tokens, cut to what the page table covers (flagged on request).
+__device__ __forceinline__ int seq_tokens(const DigestArgs& p, int b, bool flag) {
+  int L = __ldg(p.seq_lens + b);
+  const int lmax = p.max_pages * kPage;
+  if (L < 0 || L > lmax) {
+    if (flag) flag_error(p.status, NVFP4KV_DEVERR_LENGTH);
+    L = L < 0 ? 0 : lmax;
+  }
+  return L;
+}
+
+// Where a warp's share [begin, end) of the flattened items starts: in sequence b,
+// whose first item is `first`.
+struct Share {
+  int begin, end;
+  int b, first;
+};
+
+struct ShareShared {
+  int sums[kDgWarps];
+  int b[kDgWarps], first[kDgWarps];
+};
+
+// Items of sequence b: count(b).  Every thread of the block calls this.
+template <class Count>
+__device__ __forceinline__ Share split(ShareShared& s, int batch, Count count) {
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const long long warps = (long long)gridDim.x * kDgWarps, w0 = (long long)blockIdx.x * kDgWarps;
+  // one pass over the sequences for the total, and (again, unless they were few
+  // enough to stay in a register) one to find the warps' starts
+  int mine = 0, local = 0;
+  for (int b = tid; b < batch; b += kDgThreads) local += mine = count(b);
+  int sum = __reduce_add_sync(kAll, local);
+  if (lane == 0) s.sums[warp] = sum;
+  __syncthreads();
+  int total = 0;
+#pragma unroll
+  for (int w = 0; w < kDgWarps; ++w) total += s.sums[w];
+  __syncthreads();
+  int carry = 0;
+  for (int base = 0; base < batch; base += kDgThreads) {
+    const int b = base + tid;
+    const int n = batch <= kDgThreads ? mine : b < batch ? count(b) : 0;
+    int incl = n;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const int v = __shfl_up_sync(kAll, incl, off);
+      if (lane >= off) incl += v;
+    }
+    if (lane == 31) s.sums[warp] = incl;
+    __syncthreads();
+    int first = carry + incl - n, all = carry;
+#pragma unroll
+    for (int w = 0; w < kDgWarps; ++w) {
+      if (w < warp) first += s.sums[w];
+      all += s.sums[w];
+    }
+    if (n > 0) {
+      for (int w = 0; w < kDgWarps; ++w) {
+        const int at = (int)(total * (w0 + w) / warps);
+        if (at >= first && at - first < n) {
+          s.b[w] = b;
+          s.first[w] = first;
+        }
+      }
+    }
+    carry = all;
+    __syncthreads();
+  }
+  Share r;
+  r.begin = (int)(total * (w0 + warp) / warps);
+  r.end = (int)(total * (w0 + warp + 1) / warps);
+  r.b = s.b[warp];
+  r.first = s.first[warp];
+  return r;
+}
+
+// ---------------------------------------------------------------------------
+// digests
+// ---------------------------------------------------------------------------
+
+union H2 {
+  uint32_t u;
+  __half2 h;
+};
+__device__ __forceinline__ uint32_t hmax2(uint32_t a, uint32_t b) {
+  H2 x, y, r;
+  x.u = a, y.u = b;
+  r.h = __hmax2(x.h, y.h);
+  return r.u;
+}
+__device__ __forceinline__ uint32_t hmin2(uint32_t a, uint32_t b) {
+  H2 x, y, r;
+  x.u = a, y.u = b;
+  r.h = __hmin2(x.h, y.h);
+  return r.u;
+}
+
+// A warp takes one page-head at a time: lane = (8 dimensions, every other row).
+// A row past the sequence's end reads row 0 instead, which changes no bound.
+// 1152 bytes in (whole lines) and 272 out per page-head.
+__global__ void __launch_bounds__(kDgThreads) digest_kernel(const DigestArgs p) {
+  __shared__ ShareShared s;
+  const int lane = threadIdx.x & 31;
+  auto from_page = [&](int b) { return p.first_tokens ? max(__ldg(p.first_tokens + b), 0) / kPage : 0; };
+  Share w = split(s, p.batch, [&](int b) {
+    const int L = seq_tokens(p, b, blockIdx.x == 0);
+    return max((L + kPage - 1) / kPage - from_page(b), 0) * p.hkv;
+  });
+  if (w.begin >= w.end) return;
+  int b = w.b, i = w.begin - w.first;
+  int L = seq_tokens(p, b, false), page0 = from_page(b), n = ((L + kPage - 1) / kPage - page0) * p.hkv;
+  int page = i / p.hkv, h = i - page * p.hkv;  // page counts from page0
+  const int dg = lane & 15, rh = lane >> 4;    // dimensions 8 dg .. 8 dg + 7 of rows 2 i + rh
+  for (int at = w.begin; at < w.end; ++at) {
+    while (i >= n) {  // the next sequence that has any
+      i -= n;
+      ++b;
+      L = seq_tokens(p, b, false);
+      page0 = from_page(b);
+      n = max((L + kPage - 1) / kPage - page0, 0) * p.hkv;
+      page = 0;
+      h = 0;
+    }
+    const int id = __ldg(p.page_table + (long long)b * p.max_pages + page0 + page);
+    if (id < 0 || id >= p.num_pages) {
+      if (lane == 0) flag_error(p.status, NVFP4KV_DEVERR_PAGE);
+    } else {
+      const long long row = (long long)id * p.hkv + h;
+      const uint8_t* ph = p.pages + row * kPageHeadBytes;
+      const int valid = L - (page0 + page) * kPage;
+      uint32_t k[8];
+#pragma unroll
+      for (int r = 0; r < 8; ++r) {
+        const int src = 2 * r + rh < valid ? 2 * r + rh : 0;
+        k[r] = __ldg(reinterpret_cast<const uint32_t*>(ph + kOffKData + src * kRowBytes) + dg);
+      }
+      const uint32_t scales = __ldg(reinterpret_cast<const uint32_t*>(ph + kOffKScale) + lane);
+      uint32_t hi[4], lo[4];
+#pragma unroll
+      for (int r = 0; r < 8; ++r) {
+        // block dg / 2 of the row: byte dg / 2 of its eight scales, two lanes' words
+        const int src = 2 * r + rh < valid ? 2 * r + rh : 0;
+        const uint32_t word = __shfl_sync(kAll, scales, 2 * src + (dg >> 3));
+        const uint32_t byte = (word >> (8 * ((dg >> 1) & 3))) & 0xFFu;
+        const uint32_t sc = e4m3x2_to_f16x2(byte | byte << 8);
+        const uint32_t v[4] = {hmul2(e2m1x2_to_f16x2<0>(k[r]), sc), hmul2(e2m1x2_to_f16x2<1>(k[r]), sc),
+                               hmul2(e2m1x2_to_f16x2<2>(k[r]), sc), hmul2(e2m1x2_to_f16x2<3>(k[r]), sc)};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          hi[j] = r == 0 ? v[j] : hmax2(hi[j], v[j]);
+          lo[j] = r == 0 ? v[j] : hmin2(lo[j], v[j]);
+        }
+      }
+      // the other rows; then lanes 0-15 go on with hi, lanes 16-31 with -lo
+      uint32_t top = 0;
+      float x[8];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        hi[j] = hmax2(hi[j], __shfl_xor_sync(kAll, hi[j], 16));
+        lo[j] = hmin2(lo[j], __shfl_xor_sync(kAll, lo[j], 16));
+        const uint32_t bound = rh ? lo[j] ^ 0x80008000u : hi[j];
+        top = hmax2(top, hmax2(hi[j] & 0x7FFF7FFFu, lo[j] & 0x7FFF7FFFu));
+        H2 u;
+        u.u = bound;
+        x[2 * j] = __low2float(u.h);
+        x[2 * j + 1] = __high2float(u.h);
+      }
+#pragma unroll
+      for (int off = 1; off < 16; off <<= 1) top = hmax2(top, __shfl_xor_sync(kAll, top, off));
+      H2 t;
+      t.u = top;
+      const float most = fmaxf(__low2float(t.h), __high2float(t.h));
+      // 2^e with most / 2^e in [128, 256): most is 0 or at least 2^-10, so both are normal
+      const int e = most > 0.0f ? (int)(__float_as_uint(most) >> 23) - 127 - 7 : 0;
+      const float unit = __uint_as_float((uint32_t)(127 + e) << 23), per_unit = __uint_as_float((uint32_t)(127 - e) << 23);
+      uint32_t code[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        float y[2];
+#pragma unroll
+        for (int i2 = 0; i2 < 2; ++i2) {
+          // up to a whole number of the binade's steps (2^-9 below 2^-6): exact
+          const float v = x[2 * j + i2] * per_unit;
+          const uint32_t ex = max(__float_as_uint(v) >> 23 & 0xFFu, 127u - 6u);
+          const float step = __uint_as_float((ex - 3u) << 23), steps = __uint_as_float((254u + 3u - ex) << 23);
+          y[i2] = ceilf(v * steps) * step;
+          y[i2] = (rh ? -y[i2] : y[i2]) + 0.0f;  // no negative zero
+        }
+        code[j] = e4m3x2_from_f32(y[0], y[1]);
+      }
+      uint8_t* d = p.digest + row * kDigestBytes;
+      reinterpret_cast<uint2*>(d)[lane] = make_uint2(code[0] | code[1] << 16, code[2] | code[3] << 16);
+      if (lane == 0) *reinterpret_cast<uint4*>(d + kOffScale) = make_uint4(__float_as_uint(unit), 0u, 0u, 0u);
+    }
+    ++i;
+    if (++h == p.hkv) {
+      h = 0;
+      ++page;
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// scores
+// ---------------------------------------------------------------------------
+
+constexpr int kTile = 16;  // pages of one KV head per step: the rows of an MMA
+
+__device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                         uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+// The queries of a pair as B fragments, and what their heads' products are
+// multiplied with.  Lane (g, t) holds head g's dimensions 16 t .. 16 t + 15 and
+// 64 + 16 t ..: the order in which a digest's 16-byte pieces bring them.
+struct Queries {
+  uint32_t pos[8][2], neg[8][2];
+  float c0, c1;  // heads 2 t, 2 t + 1
+};
+
+__device__ __forceinline__ void load_queries(const ScoreArgs& p, int pair, int lane, Queries& q) {
+  const int g = lane >> 2, t = lane & 3;
+  float v[32];
+  if (g < p.group) {
+    const uint4* src = reinterpret_cast<const uint4*>(p.q + ((long long)pair * p.group + g) * kHeadDim);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const uint4 w = __ldg(src + 8 * (j >> 1) + 2 * t + (j & 1));
+      v[8 * j + 0] = bf16_to_f32(w.x & 0xFFFFu); v[8 * j + 1] = bf16_to_f32(w.x >> 16);
+      v[8 * j + 2] = bf16_to_f32(w.y & 0xFFFFu); v[8 * j + 3] = bf16_to_f32(w.y >> 16);
+      v[8 * j + 4] = bf16_to_f32(w.z & 0xFFFFu); v[8 * j + 5] = bf16_to_f32(w.z >> 16);
+      v[8 * j + 6] = bf16_to_f32(w.w & 0xFFFFu); v[8 * j + 7] = bf16_to_f32(w.w >> 16);
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 32; ++j) v[j] = 0.0f;
+  }
+  // times a power of two that puts the head's largest into [2^14, 2^15), so that
+  // f16 holds them (as in the decode); the products stay below 2^31
+  float amax = 0.0f;
+#pragma unroll
+  for (int j = 0; j < 32; ++j) amax = fmaxf(amax, fabsf(v[j]));
+  amax = fmaxf(amax, __shfl_xor_sync(kAll, amax, 1));
+  amax = fmaxf(amax, __shfl_xor_sync(kAll, amax, 2));
+  int e = 0;
+  if (amax > 0.0f) e = min(max(14 - ((int)((__float_as_uint(amax) >> 23) & 0xFF) - 127), -100), 100);
+  const float pre = __uint_as_float((uint32_t)(e + 127) << 23), inv = __uint_as_float((uint32_t)(127 - e) << 23);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float a = v[4 * i] * pre, b = v[4 * i + 1] * pre, c = v[4 * i + 2] * pre, d = v[4 * i + 3] * pre;
+    q.pos[i][0] = pack_f16x2(fmaxf(a, 0.0f), fmaxf(b, 0.0f));
+    q.pos[i][1] = pack_f16x2(fmaxf(c, 0.0f), fmaxf(d, 0.0f));
+    q.neg[i][0] = pack_f16x2(fminf(a, 0.0f), fminf(b, 0.0f));
+    q.neg[i][1] = pack_f16x2(fminf(c, 0.0f), fminf(d, 0.0f));
+  }
+  const float c = p.score_scale * inv;
+  q.c0 = __shfl_sync(kAll, c, 8 * t);
+  q.c1 = __shfl_sync(kAll, c, 8 * t + 4);
+}
+
+// A warp takes tiles of 16 consecutive pages of one (sequence, KV head) pair; the
+// heads are an MMA's eight columns.  Lane (g, t) reads 16-byte pieces t and 4 + t
+// of hi and of lo of pages g and g + 8: whole sectors, each byte once.
+__global__ void __launch_bounds__(kDgThreads) scores_kernel(const ScoreArgs p) {
+  __shared__ ShareShared s;
+  const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  const DigestArgs& d = p.d;
+  auto pages_of = [&](int b, bool flag) {
+    int n = (seq_tokens(d, b, flag) + kPage - 1) / kPage;
+    if (n > p.score_stride) {
+      if (flag) flag_error(d.status, NVFP4KV_DEVERR_LENGTH);
+      n = (int)p.score_stride;
+    }
+    return n;
+  };
+  Share w = split(s, d.batch, [&](int b) { return (pages_of(b, blockIdx.x == 0) + kTile - 1) / kTile * d.hkv; });
+  if (w.begin >= w.end) return;
+  int b = w.b, i = w.begin - w.first;
+  int pages = pages_of(b, false), tiles = (pages + kTile - 1) / kTile;
+  int h = i / tiles, tile = i - h * tiles;
+  Queries q;
+  int loaded = -1;
+  for (int at = w.begin; at < w.end; ++at) {
+    while (h >= d.hkv) {  // the next sequence that has any
+      ++b;
+      pages = pages_of(b, false);
+      tiles = (pages + kTile - 1) / kTile;
+      h = tiles > 0 ? 0 : d.hkv;
+    }
+    const int pair = b * d.hkv + h;
+    // lanes 0-15: the tile's page ids
+    const int page = tile * kTile + (lane & 15);
+    int id = -1;
+    if (page < pages) {
+      id = __ldg(d.page_table + (long long)b * d.max_pages + page);
+      if (id < 0 || id >= d.num_pages) {
+        flag_error(d.status, NVFP4KV_DEVERR_PAGE);
+        id = -1;
+      }
+    }
+    const int id0 = __shfl_sync(kAll, id, g), id1 = __shfl_sync(kAll, id, g + 8);
+    const uint8_t* r0 = d.digest + ((long long)max(id0, 0) * d.hkv + h) * kDigestBytes;
+    const uint8_t* r1 = d.digest + ((long long)max(id1, 0) * d.hkv + h) * kDigestBytes;
+    uint4 x[2][4];  // pages g, g + 8: hi pieces t, 4 + t, lo pieces t, 4 + t
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      x[0][j] = __ldg(reinterpret_cast<const uint4*>(r0) + 4 * j + t);
+      x[1][j] = __ldg(reinterpret_cast<const uint4*>(r1) + 4 * j + t);
+    }
+    const float u0 = __ldg(reinterpret_cast<const float*>(r0 + kOffScale)), u1 = __ldg(reinterpret_cast<const float*>(r1 + kOffScale));
+    if (pair != loaded) {
+      load_queries(p, pair, lane, q);
+      loaded = pair;
+    }
+    float c[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const uint32_t a[4] = {x[0][j].x, x[0][j].y, x[0][j].z, x[0][j].w};
+      const uint32_t e[4] = {x[1][j].x, x[1][j].y, x[1][j].z, x[1][j].w};
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const uint32_t* f = (j & 2) ? q.neg[4 * (j & 1) + k] : q.pos[4 * (j & 1) + k];
+        mma16816(c, e4m3x2_to_f16x2(a[k] & 0xFFFFu), e4m3x2_to_f16x2(e[k] & 0xFFFFu), e4m3x2_to_f16x2(a[k] >> 16),
+                 e4m3x2_to_f16x2(e[k] >> 16), f[0], f[1]);
+      }
+    }
+    // the largest over the group's heads, 2 t and 2 t + 1 in this lane
+    const float c00 = 2 * t < p.group ? c[0] * q.c0 : -INFINITY, c01 = 2 * t + 1 < p.group ? c[1] * q.c1 : -INFINITY;
+    const float c10 = 2 * t < p.group ? c[2] * q.c0 : -INFINITY, c11 = 2 * t + 1 < p.group ? c[3] * q.c1 : -INFINITY;
+    float m0 = fmaxf(c00, c01), m1 = fmaxf(c10, c11);
+#pragma unroll
+    for (int off = 1; off < 4; off <<= 1) {
+      m0 = fmaxf(m0, __shfl_xor_sync(kAll, m0, off));
+      m1 = fmaxf(m1, __shfl_xor_sync(kAll, m1, off));
+    }
+    float* out = p.scores + (long long)pair * p.score_stride + tile * kTile;
+    if (t == 0 && tile * kTile + g < pages) out[g] = id0 < 0 ? -INFINITY : m0 * u0;
+    if (t == 1 && tile * kTile + g + 8 < pages) out[g + 8] = id1 < 0 ? -INFINITY : m1 * u1;
+    if (++tile == tiles) {
+      tile = 0;
+      ++h;
+    }
+  }
+}
+
+unsigned blocks_for(int64_t items_most, int num_sms, int per_sm) {
+  const int64_t need = (items_most + kDgWarps - 1) / kDgWarps, fit = (int64_t)num_sms * per_sm;
+  return (unsigned)(need < 1 ? 1 : need < fit ? need : fit);
+}
+
+}  // namespace
+
+cudaError_t launch_page_digest(const DigestArgs& args, int num_sms, cudaStream_t stream) {
+  const unsigned blocks = blocks_for((int64_t)args.batch * args.max_pages * args.hkv, num_sms, 6);
+  digest_kernel<<<blocks, kDgThreads, 0, stream>>>(args);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_page_scores(const ScoreArgs& args, int num_sms, cudaStream_t stream) {
+  const int64_t tiles = ((int64_t)args.d.max_pages + kTile - 1) / kTile;
+  const unsigned blocks = blocks_for(args.d.batch * tiles * args.d.hkv, num_sms, 2);
+  scores_kernel<<<blocks, kDgThreads, 0, stream>>>(args);
+  return cudaGetLastError();
+}
+
+}  // namespace nvfp4kv
