@@ -121,10 +121,107 @@ __device__ __forceinline__ uint32_t hmin2(uint32_t a, uint32_t b) {
   r.h = __hmin2(x.h, y.h);
   return r.u;
 }
+__device__ __forceinline__ uint32_t hneg2(uint32_t a) { return a ^ 0x80008000u; }
+__device__ __forceinline__ uint32_t hfma2(uint32_t a, uint32_t b, uint32_t c) {
+  uint32_t r;
+  asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
+  return r;
+}
 
-// A warp takes one page-head at a time: lane = (8 dimensions, every other row).
-// A row past the sequence's end reads row 0 instead, which changes no bound.
-// 1152 bytes in (whole lines) and 272 out per page-head.
+// A lane's share of a page-head's keys: dimensions 8 dg .. 8 dg + 7 of every other
+// row, and those rows' scale bytes.
+struct KeyRows {
+  uint32_t k[8];
+  uint32_t scale[8];
+};
+
+// Rows past the sequence's end read row 0 instead, which changes no bound.
+__device__ __forceinline__ void load_keys(const uint8_t* ph, int valid, int dg, int rh, KeyRows& x) {
+  if (valid >= kPage) {
+    const uint8_t* const k = ph + kOffKData + rh * kRowBytes + 4 * dg;
+    const uint8_t* const s = ph + kOffKScale + rh * kRowScales + (dg >> 1);
+#pragma unroll
+    for (int r = 0; r < 8; ++r) {
+      x.k[r] = __ldg(reinterpret_cast<const uint32_t*>(k + 2 * r * kRowBytes));
+      x.scale[r] = __ldg(s + 2 * r * kRowScales);
+    }
+  } else {
+#pragma unroll
+    for (int r = 0; r < 8; ++r) {
+      const int row = 2 * r + rh < valid ? 2 * r + rh : 0;
+      x.k[r] = __ldg(reinterpret_cast<const uint32_t*>(ph + kOffKData + row * kRowBytes + 4 * dg));
+      x.scale[r] = __ldg(ph + k_scale_offset(row, dg >> 1));
+    }
+  }
+}
+
+// v (below 256 in size) rounded up to an E4M3 value: to a whole number of its
+// binade's steps, 2^-9 below 2^-6.
+__device__ __forceinline__ float up_to_step(float v) {
+  const uint32_t ex = max(__float_as_uint(v) >> 23 & 0xFFu, 127u - 6u);
+  const float step = __uint_as_float((ex - 3u) << 23), steps = __uint_as_float((254u + 3u - ex) << 23);
+  return ceilf(v * steps) * step;
+}
+
+// A page-head's digest from a warp's keys.  Every value e2m1 * e4m3 has at most six
+// significant bits and is 0 or at least 2^-10 in size: exact in f16.  The lanes of
+// the odd rows hold all values negated (their scales' signs are flipped), so that
+// after one exchange the even ones hold hi, the odd ones -lo, and both round up.
+__device__ __forceinline__ void write_digest(const KeyRows& in, uint8_t* d, int lane) {
+  const int rh = lane >> 4;
+  uint32_t hi[4], lo[4];
+#pragma unroll
+  for (int r = 0; r < 8; ++r) {
+    const uint32_t sc = e4m3x2_to_f16x2(in.scale[r] * 0x0101u + (rh ? 0x8080u : 0u));
+    const uint32_t v[4] = {hmul2(e2m1x2_to_f16x2<0>(in.k[r]), sc), hmul2(e2m1x2_to_f16x2<1>(in.k[r]), sc),
+                           hmul2(e2m1x2_to_f16x2<2>(in.k[r]), sc), hmul2(e2m1x2_to_f16x2<3>(in.k[r]), sc)};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      hi[j] = r == 0 ? v[j] : hmax2(hi[j], v[j]);
+      lo[j] = r == 0 ? v[j] : hmin2(lo[j], v[j]);
+    }
+  }
+  uint32_t x[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) x[j] = hmax2(hi[j], hneg2(__shfl_xor_sync(kAll, lo[j], 16)));
+  // the largest of them all is max(|hi|, |lo|) >= 0 (negative zeros count as below 0)
+  const uint32_t t2 = hmax2(hmax2(x[0], x[1]), hmax2(x[2], x[3]));
+  const int most = __reduce_max_sync(kAll, max((int)(int16_t)(t2 & 0xFFFFu), (int)t2 >> 16));
+  // 2^e with most / 2^e in [128, 256), from f16's exponent field (a normal number)
+  const int field = most > 0 ? most >> 10 : 15 + 7;
+  const int down = 15 + 7 - field;  // -e, in [-4, 17]: one or two factors that f16 holds
+  const int first = min(down, 15), second = down - first;
+  const uint32_t f1 = (uint32_t)(15 + first) << 10, f2 = (uint32_t)(15 + second) << 10;
+  uint32_t code[4];
+  bool small = false;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const uint32_t t = hfma2(hmul2(x[j], f1 | f1 << 16), f2 | f2 << 16, 0u);  // + 0: no negative zeros
+    H2 u, lim;
+    u.u = t & 0x7FFF7FFFu;
+    lim.u = 0x24002400u;  // 2^-6
+    small |= (__hlt2_mask(u.h, lim.h) & u.u) != 0;  // 0 < |t| < 2^-6: steps that are coarser than the binade's
+    // E4M3 drops seven of f16's ten mantissa bits; a negative value's magnitude is cut off
+    const uint32_t up = (t + 0x007F007Fu - (t >> 15 & 0x00010001u) * 0x7Fu) & 0xFF80FF80u;
+    code[j] = e4m3x2_from_f16x2(hfma2(up, rh ? 0xBC00BC00u : 0x3C003C00u, 0u));  // times the lane's sign
+    x[j] = t;
+  }
+  if (__any_sync(kAll, small)) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      H2 u;
+      u.u = x[j];
+      const float a = up_to_step(__low2float(u.h)), b = up_to_step(__high2float(u.h));
+      code[j] = e4m3x2_from_f32((rh ? -a : a) + 0.0f, (rh ? -b : b) + 0.0f);
+    }
+  }
+  reinterpret_cast<uint2*>(d)[lane] = make_uint2(code[0] | code[1] << 16, code[2] | code[3] << 16);
+  if (lane == 0)
+    *reinterpret_cast<uint4*>(d + kOffScale) = make_uint4((uint32_t)(127 - down) << 23, 0u, 0u, 0u);  // 2^e; 1 without any
+}
+
+// A warp takes one page-head at a time, its keys loaded while the one before is
+// bounded.  1152 bytes in (whole lines) and 272 out per page-head.
 __global__ void __launch_bounds__(kDgThreads) digest_kernel(const DigestArgs p) {
   __shared__ ShareShared s;
   const int lane = threadIdx.x & 31;
@@ -134,96 +231,40 @@ __global__ void __launch_bounds__(kDgThreads) digest_kernel(const DigestArgs p) 
     return max((L + kPage - 1) / kPage - from_page(b), 0) * p.hkv;
   });
   if (w.begin >= w.end) return;
-  int b = w.b, i = w.begin - w.first;
-  int L = seq_tokens(p, b, false), page0 = from_page(b), n = ((L + kPage - 1) / kPage - page0) * p.hkv;
-  int page = i / p.hkv, h = i - page * p.hkv;  // page counts from page0
-  const int dg = lane & 15, rh = lane >> 4;    // dimensions 8 dg .. 8 dg + 7 of rows 2 i + rh
-  for (int at = w.begin; at < w.end; ++at) {
-    while (i >= n) {  // the next sequence that has any
-      i -= n;
+  // the next item to load: head h of page `page` of sequence b, of `end` pages
+  int b = w.b, L = seq_tokens(p, b, false), page = from_page(b), end = (L + kPage - 1) / kPage;
+  const int i = w.begin - w.first;
+  page += i / p.hkv;
+  int h = i % p.hkv;
+  const int dg = lane & 15, rh = lane >> 4;  // dimensions 8 dg .. 8 dg + 7 of rows 2 r + rh
+  // loads the next item's keys; returns its row of the pool, or -1
+  auto load = [&](KeyRows& x) -> int {
+    while (page >= end) {  // the next sequence that has any
       ++b;
       L = seq_tokens(p, b, false);
-      page0 = from_page(b);
-      n = max((L + kPage - 1) / kPage - page0, 0) * p.hkv;
-      page = 0;
-      h = 0;
+      page = from_page(b);
+      end = (L + kPage - 1) / kPage;
     }
-    const int id = __ldg(p.page_table + (long long)b * p.max_pages + page0 + page);
-    if (id < 0 || id >= p.num_pages) {
-      if (lane == 0) flag_error(p.status, NVFP4KV_DEVERR_PAGE);
-    } else {
-      const long long row = (long long)id * p.hkv + h;
-      const uint8_t* ph = p.pages + row * kPageHeadBytes;
-      const int valid = L - (page0 + page) * kPage;
-      uint32_t k[8];
-#pragma unroll
-      for (int r = 0; r < 8; ++r) {
-        const int src = 2 * r + rh < valid ? 2 * r + rh : 0;
-        k[r] = __ldg(reinterpret_cast<const uint32_t*>(ph + kOffKData + src * kRowBytes) + dg);
-      }
-      const uint32_t scales = __ldg(reinterpret_cast<const uint32_t*>(ph + kOffKScale) + lane);
-      uint32_t hi[4], lo[4];
-#pragma unroll
-      for (int r = 0; r < 8; ++r) {
-        // block dg / 2 of the row: byte dg / 2 of its eight scales, two lanes' words
-        const int src = 2 * r + rh < valid ? 2 * r + rh : 0;
-        const uint32_t word = __shfl_sync(kAll, scales, 2 * src + (dg >> 3));
-        const uint32_t byte = (word >> (8 * ((dg >> 1) & 3))) & 0xFFu;
-        const uint32_t sc = e4m3x2_to_f16x2(byte | byte << 8);
-        const uint32_t v[4] = {hmul2(e2m1x2_to_f16x2<0>(k[r]), sc), hmul2(e2m1x2_to_f16x2<1>(k[r]), sc),
-                               hmul2(e2m1x2_to_f16x2<2>(k[r]), sc), hmul2(e2m1x2_to_f16x2<3>(k[r]), sc)};
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          hi[j] = r == 0 ? v[j] : hmax2(hi[j], v[j]);
-          lo[j] = r == 0 ? v[j] : hmin2(lo[j], v[j]);
-        }
-      }
-      // the other rows; then lanes 0-15 go on with hi, lanes 16-31 with -lo
-      uint32_t top = 0;
-      float x[8];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        hi[j] = hmax2(hi[j], __shfl_xor_sync(kAll, hi[j], 16));
-        lo[j] = hmin2(lo[j], __shfl_xor_sync(kAll, lo[j], 16));
-        const uint32_t bound = rh ? lo[j] ^ 0x80008000u : hi[j];
-        top = hmax2(top, hmax2(hi[j] & 0x7FFF7FFFu, lo[j] & 0x7FFF7FFFu));
-        H2 u;
-        u.u = bound;
-        x[2 * j] = __low2float(u.h);
-        x[2 * j + 1] = __high2float(u.h);
-      }
-#pragma unroll
-      for (int off = 1; off < 16; off <<= 1) top = hmax2(top, __shfl_xor_sync(kAll, top, off));
-      H2 t;
-      t.u = top;
-      const float most = fmaxf(__low2float(t.h), __high2float(t.h));
-      // 2^e with most / 2^e in [128, 256): most is 0 or at least 2^-10, so both are normal
-      const int e = most > 0.0f ? (int)(__float_as_uint(most) >> 23) - 127 - 7 : 0;
-      const float unit = __uint_as_float((uint32_t)(127 + e) << 23), per_unit = __uint_as_float((uint32_t)(127 - e) << 23);
-      uint32_t code[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        float y[2];
-#pragma unroll
-        for (int i2 = 0; i2 < 2; ++i2) {
-          // up to a whole number of the binade's steps (2^-9 below 2^-6): exact
-          const float v = x[2 * j + i2] * per_unit;
-          const uint32_t ex = max(__float_as_uint(v) >> 23 & 0xFFu, 127u - 6u);
-          const float step = __uint_as_float((ex - 3u) << 23), steps = __uint_as_float((254u + 3u - ex) << 23);
-          y[i2] = ceilf(v * steps) * step;
-          y[i2] = (rh ? -y[i2] : y[i2]) + 0.0f;  // no negative zero
-        }
-        code[j] = e4m3x2_from_f32(y[0], y[1]);
-      }
-      uint8_t* d = p.digest + row * kDigestBytes;
-      reinterpret_cast<uint2*>(d)[lane] = make_uint2(code[0] | code[1] << 16, code[2] | code[3] << 16);
-      if (lane == 0) *reinterpret_cast<uint4*>(d + kOffScale) = make_uint4(__float_as_uint(unit), 0u, 0u, 0u);
-    }
-    ++i;
+    int id = __ldg(p.page_table + (long long)b * p.max_pages + page);
+    const bool valid = id >= 0 && id < p.num_pages;
+    if (!valid && lane == 0) flag_error(p.status, NVFP4KV_DEVERR_PAGE);
+    const int row = (valid ? id : 0) * p.hkv + h;
+    load_keys(p.pages + (long long)row * kPageHeadBytes, L - page * kPage, dg, rh, x);
     if (++h == p.hkv) {
       h = 0;
       ++page;
     }
+    return valid ? row : -1;
+  };
+  KeyRows now;
+  int row = load(now);
+  for (int at = w.begin; at < w.end; ++at) {
+    KeyRows next = now;
+    int next_row = -1;
+    if (at + 1 < w.end) next_row = load(next);
+    if (row >= 0) write_digest(now, p.digest + (long long)row * kDigestBytes, lane);
+    now = next;
+    row = next_row;
   }
 }
 

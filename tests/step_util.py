@@ -30,6 +30,15 @@ def bits(x):
     return (np.ascontiguousarray(x, np.float32).view(np.uint32) >> 16).astype(np.uint16)
 
 
+def same(got, want, what):
+    """The two arrays hold the same bits."""
+    got, want = np.asarray(got), np.asarray(want)
+    assert got.shape == want.shape and got.dtype == want.dtype, f"{what}: {got.dtype} {got.shape}, {want.dtype} {want.shape}"
+    off = int(np.count_nonzero(got != want))
+    first = np.argwhere(got != want)[0].tolist() if off else None
+    assert off == 0, f"{what}: {off} of {got.size} differ, the first at {first}: {got[tuple(first)]}, not {want[tuple(first)]}"
+
+
 def plan_ref(table, cached, new, free, count, num_pages, tokens):
     """The plan's outputs, request by request."""
     table = table.copy()

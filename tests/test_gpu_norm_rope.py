@@ -7,13 +7,14 @@ import torch
 import oracle
 import nvfp4_quantized_paged_quantize_gb300 as kv
 from gpu_util import dev, pool_host, status_word
-from step_util import bf16_round, bits, norm_rope_exact, norm_rope_steps
+from step_util import bf16_round, bits, norm_rope_exact, norm_rope_steps, same
 from test_gpu_canary import Guarded
 
 pytestmark = pytest.mark.gpu
 
 BF16 = torch.bfloat16
 EPS = 1e-5
+PARTS = ("k_data", "v_data", "k_scale", "v_scale")
 
 
 def table_of(max_position, rot):
@@ -76,19 +77,20 @@ class Append:
         qx, kx, vx = self.x[:, :hq], self.x[:, hq:hq + hkv], self.x[:, hq + hkv:]
         made = [bf16_round(norm_rope_steps(a, w, EPS, self.cs, self.pos, self.inter)) for a, w in zip((qx, kx), self.weights)]
         got = (self.q_out.t if q_out is None else q_out).float().cpu().numpy()
-        assert np.array_equal(bits(got), bits(made[0]))
+        same(bits(got), bits(made[0]), "queries")
         ok = (self.pos >= 0) & (self.pos < self.max_position)
         want, tol = norm_rope_exact(qx[ok], self.weights[0], EPS, self.cs, self.pos[ok], self.inter)
         assert (np.abs(got[ok] - want) <= tol).all()
         # the cache, as quantising those rows would leave it
         ref = oracle.Cache(self.pages, hkv, 128, 16, *self.g, arrays=[a.copy() for a in self.before])
         oracle.quantize_append(ref, bits(made[1]), bits(vx), self.slots)
-        for a, b in zip(pool_host(self.cache), (ref.k_data, ref.v_data, ref.k_scale, ref.v_scale)):
-            assert np.array_equal(a, b)
+        for name, a, b in zip(PARTS, pool_host(self.cache), (ref.k_data, ref.v_data, ref.k_scale, ref.v_scale)):
+            same(a, b, name)
         wk, wv = (np.full((self.total, hkv, 128), 0x55, np.uint8) for _ in range(2))
         if self.fp8:
             oracle.bf16_to_fp8_workspace(bits(made[1]), bits(vx), self.ws_rows, wk, wv, *self.ws)
-        assert np.array_equal(self.wk.t.cpu().numpy(), wk) and np.array_equal(self.wv.t.cpu().numpy(), wv)
+        same(self.wk.t.cpu().numpy(), wk, "workspace keys")
+        same(self.wv.t.cpu().numpy(), wv, "workspace values")
 
 
 @pytest.mark.parametrize("n,hq,hkv", [(1, 8, 1), (1, 1, 1), (2, 8, 2), (3, 5, 5), (17, 6, 3), (33, 64, 8), (130, 10, 2)])
@@ -151,8 +153,8 @@ def test_nothing_to_do(cuda_lib):
                                 q_weight=a.dw[0], k_weight=a.dw[1], device_status=a.status)
     torch.cuda.synchronize()
     assert a.status.item() == 0
-    for x, y in zip(pool_host(a.cache), a.before):
-        assert np.array_equal(x, y)
+    for name, x, y in zip(PARTS, pool_host(a.cache), a.before):
+        same(x, y, name)
 
 
 def test_the_parts_are_those_of_the_other_calls(cuda_lib):

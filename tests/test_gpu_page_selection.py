@@ -9,9 +9,9 @@ import nvfp4_quantized_paged_quantize_gb300 as kv
 from gpu_util import bf16_dev, dev, pool_host, status_word
 from nvfp4_quantized_paged_quantize_gb300 import inputs
 from scored_util import SCALE, attend, check, evict_ref, page_tables, random_cache, random_q, sequence_rows
-from step_util import bf16_round, bits, digest_ref, e4m3_values, norm_rope_steps, score_ref
+from step_util import bf16_round, bits, digest_ref, e4m3_values, norm_rope_steps, same, score_ref
 from test_gpu_canary import Guarded
-from test_gpu_norm_rope import EPS, table_of
+from test_gpu_norm_rope import EPS, PARTS, table_of
 
 pytestmark = pytest.mark.gpu
 
@@ -194,7 +194,7 @@ def check_selection(w, lens, budget, first, recent):
     for b, n in enumerate(pages_of(lens)):
         for h in range(w.shape[1]):
             want = evict_ref(w[b, h, :n], n, budget, first, recent)
-            assert np.array_equal(got[b, h, :len(want)], want), (b, h)
+            same(got[b, h, :len(want)].astype(int), want, f"{b} {h}")
             assert (got[b, h, len(want):] == -1).all()
 
 
@@ -408,14 +408,15 @@ def test_captured_decode_steps_over_selected_pages(cuda_lib):
             if lens[b] % 16 == 0:
                 left -= 1
                 table[b, lens[b] // 16] = ids[at + left]
-        assert np.array_equal(pt.cpu().numpy(), table) and count.item() == left
+        same(pt.cpu().numpy(), table, "page table")
+        assert count.item() == left
         p = np.asarray(lens, np.int32)
         made = [bf16_round(norm_rope_steps(a, w, EPS, cs, p, False)) for a, w in zip((x[:, :hq], x[:, hq:hq + hkv]), weights)]
         at_slot = np.array([int(table[b, n // 16]) * 16 + n % 16 for b, n in enumerate(lens)], np.int64)
         oracle.quantize_append(o, bits(made[1]), bits(x[:, hq + hkv:]), at_slot)
-        for got, want in zip(pool_host(cache), (o.k_data, o.v_data, o.k_scale, o.v_scale)):
-            assert np.array_equal(got, want)
-        assert np.array_equal(bits(qr.float().cpu().numpy()), bits(made[0]))
+        for name, got, want in zip(PARTS, pool_host(cache), (o.k_data, o.v_data, o.k_scale, o.v_scale)):
+            same(got, want, name)
+        same(bits(qr.float().cpu().numpy()), bits(made[0]), "queries")
         lens = [n + 1 for n in lens]
         assert sl.tolist() == lens
         raw, sc, se = digest.cpu().numpy(), scores.cpu().numpy(), sel.cpu().numpy()
