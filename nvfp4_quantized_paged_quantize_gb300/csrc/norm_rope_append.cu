@@ -12,14 +12,16 @@
 // cache are determined.  Queries are stored; keys, and values as they come, go
 // through the blocks of quantize_append.cu to their slot.
 //
-// Eight lanes hold a row, 16 consecutive values each: a quantisation block, and
-// with half-split pairs the partner's values lie one to four lanes away.  A warp
-// takes four rows at a time and walks the flattened (token, head) list of its share,
-// so that a token's cosines and sines, 128 bytes a lane, stay in registers over its
-// heads.  Values go by token pairs, two groups of lanes to a unit, because a byte of
-// V data holds two tokens.  Rows come through a ring of kStages stages of shared
-// memory per warp (cp.async, no barrier but the warp's own), which keeps 64 KB in
-// flight on an SM at two CTAs; products two to an instruction.
+// Eight lanes hold a row: lane s has values 8 s .. 8 s + 7 and 64 + 8 s .., so that
+// its loads and stores are whole sectors, the partners of a rotation of all 128
+// values (in either order of pairs) are in one lane, and a quantisation block in
+// two neighbours.  A warp takes four rows at a time and walks the flattened (token,
+// head) list of its share, so that a token's cosines and sines stay in registers
+// over its heads.  Values go by token pairs, two groups of lanes to a unit, because a
+// byte of V data holds two tokens.  Rows come through a ring of kStages stages of
+// shared memory per warp (cp.async; a lane reads what it copied itself, so without
+// any barrier), which keeps 64 KB in flight on an SM at two CTAs; products two to an
+// instruction.
 // HBM-bound on long inputs: 512 bytes per query row, 256 + 72 (+ 128 with the
 // workspace) per key or value row, and the cosines once per token.
 #include "fp8_quotient.cuh"
@@ -60,60 +62,53 @@ __device__ __forceinline__ Steps share(const NormRopeParams& p, int steps, int b
 }
 
 // Where an 8-lane group is in a flattened list of `heads` per major index (a token,
-// or a pair of tokens).
+// or a pair of tokens), and that row's address.
 struct Walk {
   int major, head;
-  __device__ __forceinline__ void start(long long at, int heads) {
+  const uint16_t* row;
+  long long gap;  // from one token's last head to the next one's first
+  __device__ __forceinline__ void start(const uint16_t* base, long long at, int heads, long long stride) {
     major = (int)(at / heads);
     head = (int)(at - (long long)major * heads);
+    row = base + major * stride + head * kHeadDim;
+    gap = stride - (long long)heads * kHeadDim;
   }
   __device__ __forceinline__ void skip(int by, int heads) {
     head += by;
+    row += by * kHeadDim;
     while (head >= heads) {
       head -= heads;
       ++major;
+      row += gap;
     }
   }
 };
 
-// One row's 16 values of a lane, as stored.
-struct Row {
-  uint4 a, b;
-};
-
-// A row's 16-byte piece q lies at piece_at(q) of its 256 bytes of a stage: the
-// lanes of a group write pieces s and 8 + s (whole sectors of the row) and read 2 s
-// and 2 s + 1, both without bank conflicts.
-__device__ __forceinline__ int piece_at(int q) { return 16 * ((q & 1) ? 8 + ((q >> 1) ^ 4) : q >> 1); }
-
-// Starts the copy of the group's row (nothing for a null one) into a stage.
-__device__ __forceinline__ void fetch_row(uint32_t stage, const uint16_t* row, int lane) {
-  const int sub = lane & 7;
-  if (row != nullptr) {
-    const uint32_t dst = stage + (lane >> 3) * 256;
-    const uint8_t* src = reinterpret_cast<const uint8_t*>(row) + 16 * sub;
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst + piece_at(sub)), "l"(src) : "memory");
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst + piece_at(8 + sub)), "l"(src + 128) : "memory");
-  }
-  asm volatile("cp.async.commit_group;" ::: "memory");
+// Starts the copy of the lane's two pieces of a row (none if it is not live) into a
+// stage: [half][lane][16 bytes].
+__device__ __forceinline__ void fetch_row(uint32_t stage, const uint16_t* row, bool live) {
+  asm volatile(
+      "{\n .reg .pred p;\n"
+      " setp.ne.u32 p, %2, 0;\n"
+      " @p cp.async.cg.shared.global [%0], [%1], 16;\n"
+      " @p cp.async.cg.shared.global [%0+512], [%1+128], 16;\n"
+      " cp.async.commit_group;\n"
+      "}\n" ::"r"(stage), "l"(row), "r"((uint32_t)live)
+      : "memory");
 }
 
-// The oldest stage's row, once its copy (kStages - 1 later ones may be under way) has landed.
-__device__ __forceinline__ Row take_row(const uint8_t* stage, int lane) {
+// The lane's values of the oldest stage's row, as stored, once its copy (kStages - 1
+// later ones may be under way) has landed: words 0-3 values 8 s .., 4-7 64 + 8 s ...
+__device__ __forceinline__ void take_row(const uint8_t* stage, uint32_t (&w)[8]) {
   asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
-  __syncwarp();
-  const uint8_t* r = stage + (lane >> 3) * 256;
-  const int sub = lane & 7;
-  Row x;
-  x.a = *reinterpret_cast<const uint4*>(r + piece_at(2 * sub));
-  x.b = *reinterpret_cast<const uint4*>(r + piece_at(2 * sub + 1));
-  __syncwarp();  // the stage may be filled again
-  return x;
+  const uint4 a = *reinterpret_cast<const uint4*>(stage), b = *reinterpret_cast<const uint4*>(stage + 512);
+  w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w;
+  w[4] = b.x, w[5] = b.y, w[6] = b.z, w[7] = b.w;
 }
 
 // Two products per instruction.  Sums of products stay scalar: __fadd_rn is never
-// merged with the products before it, where add.rn.f32x2 was (one query value in 50000 a
-// bit off).
+// merged with the products before it, where add.rn.f32x2 was (one query value in
+// 50000 a bit off).
 __device__ __forceinline__ float2 mul2(float2 a, float2 b) {
   uint64_t r;
   asm("mul.rn.f32x2 %0, %1, %2;"
@@ -122,99 +117,138 @@ __device__ __forceinline__ float2 mul2(float2 a, float2 b) {
   return *reinterpret_cast<float2*>(&r);
 }
 __device__ __forceinline__ float2 add2(float2 a, float2 b) { return make_float2(__fadd_rn(a.x, b.x), __fadd_rn(a.y, b.y)); }
-
-__device__ __forceinline__ void unpack(const uint4& x, float2* f) {
-  const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) f[i] = make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u));
+__device__ __forceinline__ float2 neg2(float2 a) { return make_float2(-a.x, -a.y); }
+__device__ __forceinline__ float2 shfl2(float2 a, int from) {
+  return make_float2(__shfl_sync(kAll, a.x, from), __shfl_sync(kAll, a.y, from));
 }
 
-// The lane's cosines and signed sines of one token: value i of the lane turns as
-// y_i cos_i + partner_i sin_i.
-struct Turn {
-  float2 cos[8], sin[8];
-  bool on;  // the lane's values take part in the rotation
+__device__ __forceinline__ float2 unpack2(uint32_t w) {
+  return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+}
+
+// How the pairs of a rotation lie over the lanes.
+enum Rotation : int {
+  kNone,         // no rotation
+  kWhole,        // halves, all 128 values: (8 s + i, 64 + 8 s + i), one lane's two pieces
+  kFirst,        // halves of the first 32 or 64 values: the first pieces of lanes s and s ^ (rotary_dim / 16)
+  kThreeQuarters,// halves of the first 96: pieces of different lanes and places
+  kInterleaved   // (2 i, 2 i + 1)
 };
 
-template <bool kInterleaved>
+// The lane's cosines and sines of one token: value i of piece h turns as
+// y_i cos[h]_i + partner_i sin[h]_i, the sine's sign taken in.  kWhole: both pieces
+// have the angles of cos[0], sin[0].
+struct Turn {
+  float2 cos[2][4], sin[2][4];
+  bool on[2];  // the piece takes part
+};
+
+__device__ __forceinline__ void load4x2(const float* src, float2 (&d)[4]) {
+  const float4 a = __ldg(reinterpret_cast<const float4*>(src)), b = __ldg(reinterpret_cast<const float4*>(src) + 1);
+  d[0] = make_float2(a.x, a.y), d[1] = make_float2(a.z, a.w), d[2] = make_float2(b.x, b.y), d[3] = make_float2(b.z, b.w);
+}
+
+template <int R>
 __device__ __forceinline__ void load_turn(const NormRopeArgs& p, int token, int sub, Turn& t) {
   const int pos = __ldg(p.positions + token);
-  t.on = 16 * sub < p.rot;
-  if (pos < 0 || pos >= p.max_position) {
-    flag_error(p.status, NVFP4KV_DEVERR_POSITION);
-    t.on = false;
-  }
-  if (!t.on) return;
+  const bool good = pos >= 0 && pos < p.max_position;
+  if (!good) flag_error(p.status, NVFP4KV_DEVERR_POSITION);
   const int half = p.rot >> 1;
-  const float* row = p.cos_sin + (long long)pos * p.rot;
-  if constexpr (kInterleaved) {
-    // pairs (2 i, 2 i + 1): angles 8 sub .. 8 sub + 7
+  const float* row = p.cos_sin + (long long)(good ? pos : 0) * p.rot;
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const float4 c = __ldg(reinterpret_cast<const float4*>(row + 8 * sub) + j);
-      const float4 s = __ldg(reinterpret_cast<const float4*>(row + half + 8 * sub) + j);
+  for (int h = 0; h < 2; ++h) {
+    const int d = 64 * h + 8 * sub;  // the piece's first value
+    t.on[h] = good && d < p.rot;
+    if (!t.on[h]) continue;
+    if constexpr (R == kInterleaved) {
+      const float4 c = __ldg(reinterpret_cast<const float4*>(row + d / 2));
+      const float4 s = __ldg(reinterpret_cast<const float4*>(row + half + d / 2));
       const float cs[4] = {c.x, c.y, c.z, c.w}, sn[4] = {s.x, s.y, s.z, s.w};
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        t.cos[4 * j + i] = make_float2(cs[i], cs[i]);
-        t.sin[4 * j + i] = make_float2(-sn[i], sn[i]);
+        t.cos[h][i] = make_float2(cs[i], cs[i]);
+        t.sin[h][i] = make_float2(-sn[i], sn[i]);
       }
-    }
-  } else {
-    // pairs (i, i + half): the first half's lanes hold a, the second's b
-    const bool second = 16 * sub >= half;
-    const int at = 16 * sub - (second ? half : 0);
+    } else if (R != kWhole || h == 0) {
+      const bool second = d >= half;
+      const int at = d - (second ? half : 0);
+      load4x2(row + at, t.cos[h]);
+      load4x2(row + half + at, t.sin[h]);
+      if (R != kWhole && !second) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const float4 c = __ldg(reinterpret_cast<const float4*>(row + at) + j);
-      const float4 s = __ldg(reinterpret_cast<const float4*>(row + half + at) + j);
-      t.cos[2 * j] = make_float2(c.x, c.y);
-      t.cos[2 * j + 1] = make_float2(c.z, c.w);
-      t.sin[2 * j] = second ? make_float2(s.x, s.y) : make_float2(-s.x, -s.y);
-      t.sin[2 * j + 1] = second ? make_float2(s.z, s.w) : make_float2(-s.z, -s.w);
+        for (int i = 0; i < 4; ++i) t.sin[h][i] = neg2(t.sin[h][i]);
+      }
     }
   }
 }
 
 // y = (x r) w over the eight lanes of a row.
 __device__ __forceinline__ void normalise(float2 (&f)[8], const float2 (&w)[8], float eps) {
-  float s[8];
+  float sum[2];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const float2 sq = mul2(f[i], f[i]);
-    s[i] = __fadd_rn(sq.x, sq.y);
+  for (int h = 0; h < 2; ++h) {
+    float s[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 sq = mul2(f[4 * h + i], f[4 * h + i]);
+      s[i] = __fadd_rn(sq.x, sq.y);
+    }
+    sum[h] = __fadd_rn(__fadd_rn(s[0], s[1]), __fadd_rn(s[2], s[3]));
+#pragma unroll
+    for (int x = 1; x < 8; x <<= 1) sum[h] = __fadd_rn(sum[h], __shfl_xor_sync(kAll, sum[h], x));
   }
-#pragma unroll
-  for (int n = 4; n > 0; n >>= 1)
-#pragma unroll
-    for (int i = 0; i < n; ++i) s[i] = __fadd_rn(s[2 * i], s[2 * i + 1]);
-  float sum = s[0];
-#pragma unroll
-  for (int x = 1; x < 8; x <<= 1) sum = __fadd_rn(sum, __shfl_xor_sync(kAll, sum, x));
-  const float r = __frcp_rn(__fsqrt_rn(__fadd_rn(__fmul_rn(sum, 1.0f / kHeadDim), eps)));
+  const float r = __frcp_rn(__fsqrt_rn(__fadd_rn(__fmul_rn(__fadd_rn(sum[0], sum[1]), 1.0f / kHeadDim), eps)));
 #pragma unroll
   for (int i = 0; i < 8; ++i) f[i] = mul2(mul2(f[i], make_float2(r, r)), w[i]);
 }
 
-template <bool kInterleaved>
+__device__ __forceinline__ void turn4(float2* f, const float2 (&o)[4], const float2 (&cos)[4], const float2 (&sin)[4]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) f[i] = add2(mul2(f[i], cos[i]), mul2(o[i], sin[i]));
+}
+
+template <int R>
 __device__ __forceinline__ void rotate(float2 (&f)[8], const Turn& t, int lane, int rot) {
-  if constexpr (kInterleaved) {
-    if (t.on) {
+  const int sub = lane & 7;
+  if constexpr (R == kWhole) {
+    if (t.on[0]) {  // (on[1] is the same)
 #pragma unroll
-      for (int i = 0; i < 8; ++i) f[i] = add2(mul2(f[i], t.cos[i]), mul2(make_float2(f[i].y, f[i].x), t.sin[i]));
+      for (int i = 0; i < 4; ++i) {
+        const float2 a = f[i], b = f[4 + i];
+        f[i] = add2(mul2(a, t.cos[0][i]), neg2(mul2(b, t.sin[0][i])));
+        f[4 + i] = add2(mul2(b, t.cos[0][i]), mul2(a, t.sin[0][i]));
+      }
     }
-  } else {
-    const int sub = lane & 7, by = rot >> 5;  // lanes of half the rotated values
-    const int from = sub < by ? lane + by : sub < 2 * by ? lane - by : lane;
+  } else if constexpr (R == kFirst) {
+    float2 o[4];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float2 o = make_float2(__shfl_sync(kAll, f[i].x, from), __shfl_sync(kAll, f[i].y, from));
-      if (t.on) f[i] = add2(mul2(f[i], t.cos[i]), mul2(o, t.sin[i]));
+    for (int i = 0; i < 4; ++i) o[i] = shfl2(f[i], lane ^ (rot >> 4));
+    if (t.on[0]) turn4(f, o, t.cos[0], t.sin[0]);
+  } else if constexpr (R == kThreeQuarters) {
+    // 48 apart: first pieces of lanes 0, 1 and 6, 7; first pieces of lanes 2 .. 5 and second ones of 0 .. 3
+    float2 far[4], low[4], high[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      far[i] = shfl2(f[i], sub < 2 ? lane + 6 : sub > 5 ? lane - 6 : lane);
+      low[i] = shfl2(f[i], sub < 4 ? lane + 2 : lane);       // for the second pieces of lanes 0 .. 3
+      high[i] = shfl2(f[4 + i], sub >= 2 ? lane - 2 : lane);  // for the first pieces of lanes 2 .. 5
+      if (sub >= 2 && sub <= 5) far[i] = high[i];
+    }
+    if (t.on[0]) turn4(f, far, t.cos[0], t.sin[0]);
+    if (t.on[1]) turn4(f + 4, low, t.cos[1], t.sin[1]);
+  } else if constexpr (R == kInterleaved) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      if (!t.on[h]) continue;
+      float2 o[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) o[i] = make_float2(f[4 * h + i].y, f[4 * h + i].x);
+      turn4(f + 4 * h, o, t.cos[h], t.sin[h]);
     }
   }
 }
 
-// The lane's 16 bf16 values as 16 E4M3 bytes of workspace row `row`.
+// The lane's 16 bf16 values as E4M3 bytes of workspace row `row`.
 __device__ __forceinline__ void store_ws(const NormRopeParams& p, bool v, long long row, int head, int sub,
                                          const uint32_t (&w)[8]) {
   if (row < 0) return;
@@ -228,9 +262,9 @@ __device__ __forceinline__ void store_ws(const NormRopeParams& p, bool v, long l
 #pragma unroll
   for (int i = 0; i < 8; ++i)
     e[i] = e4m3x2_from_quotients(bf16_to_f32(w[i] & 0xFFFFu), bf16_to_f32(w[i] >> 16), s, rs, fast, p.ws.unit);
-  uint8_t* ws = v ? p.a.ws_v : p.a.ws_k;
-  reinterpret_cast<uint4*>(ws + (row * p.a.hkv + head) * kHeadDim)[sub] =
-      make_uint4(e[0] | (e[1] << 16), e[2] | (e[3] << 16), e[4] | (e[5] << 16), e[6] | (e[7] << 16));
+  uint2* dst = reinterpret_cast<uint2*>((v ? p.a.ws_v : p.a.ws_k) + (row * p.a.hkv + head) * kHeadDim) + sub;
+  dst[0] = make_uint2(e[0] | (e[1] << 16), e[2] | (e[3] << 16));
+  dst[8] = make_uint2(e[4] | (e[5] << 16), e[6] | (e[7] << 16));
 }
 
 // The slot's page-head, null for padding and for a slot past the pool (flagged).
@@ -243,87 +277,104 @@ __device__ __forceinline__ uint8_t* page_head(const NormRopeArgs& p, long long s
   return p.pages + ((slot >> 4) * p.hkv + head) * kPageHeadBytes;
 }
 
-__device__ __forceinline__ void unpack_words(const uint32_t (&w)[8], float (&f)[16]) {
+// The codes and scales of the lane's two half blocks: piece h is half of block
+// sub / 2 + 4 h, whose other half the neighbour lane has.  Every lane calls this.
+struct HalfBlocks {
+  uint32_t codes[2], sb[2];
+};
+__device__ __forceinline__ HalfBlocks quantize_halves(const uint32_t (&w)[8], const GlobalScale& gs) {
+  HalfBlocks q;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    f[2 * i] = bf16_to_f32(w[i] & 0xFFFFu);
-    f[2 * i + 1] = bf16_to_f32(w[i] >> 16);
+  for (int h = 0; h < 2; ++h) {
+    float f[8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 x = unpack2(w[4 * h + i]);
+      f[2 * i] = x.x, f[2 * i + 1] = x.y;
+    }
+    float amax = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fabsf(f[i]));
+    amax = fmaxf(amax, __shfl_xor_sync(kAll, amax, 1));
+    const BlockScale b = block_scale(amax, gs);
+    q.codes[h] = block_codes8(f, b);
+    q.sb[h] = b.sb;
   }
+  return q;
 }
 
 // The warp's steps of the queries or of the keys.
-template <bool kInterleaved, bool kKeys>
+template <int R, bool kKeys>
 __device__ __forceinline__ void turn_rows(const NormRopeParams& p, Steps st, uint8_t* ring, int lane) {
   if (st.begin >= st.end) return;
   const NormRopeArgs& a = p.a;
   const int sub = lane & 7, heads = kKeys ? a.hkv : a.hq;
-  const uint16_t* src = kKeys ? a.k : a.q;
-  const long long stride = kKeys ? a.k_stride : a.q_stride;
   const uint16_t* weight = kKeys ? a.k_weight : a.q_weight;
   float2 w[8];
   if (weight) {
-    unpack(__ldg(reinterpret_cast<const uint4*>(weight) + 2 * sub), w);
-    unpack(__ldg(reinterpret_cast<const uint4*>(weight) + 2 * sub + 1), w + 4);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const uint4 x = __ldg(reinterpret_cast<const uint4*>(weight) + 8 * h + sub);
+      w[4 * h] = unpack2(x.x), w[4 * h + 1] = unpack2(x.y), w[4 * h + 2] = unpack2(x.z), w[4 * h + 3] = unpack2(x.w);
+    }
   }
-  Walk at, ahead;
-  at.start(4LL * st.begin + (lane >> 3), heads);
-  ahead = at;
-  int fetched = st.begin;  // the step that the next fetch is of
-  const uint32_t ring_u32 = smem_u32(ring);
+  Walk ahead;
+  ahead.start((kKeys ? a.k : a.q) + 8 * sub, 4LL * st.begin + (lane >> 3), heads, kKeys ? a.k_stride : a.q_stride);
+  Walk at;
+  at.start(kKeys ? nullptr : a.q_out + 8 * sub, 4LL * st.begin + (lane >> 3), heads, kKeys ? 0 : a.q_out_stride);
+  int left = st.end - st.begin;  // fetches to come
+  const uint32_t ring_u32 = smem_u32(ring) + 16 * lane;
   auto fetch = [&](int stage) {
-    const bool live = fetched < st.end && ahead.major < a.ntok;
-    fetch_row(ring_u32 + stage * kStageBytes, live ? src + ahead.major * stride + ahead.head * kHeadDim : nullptr, lane);
+    fetch_row(ring_u32 + stage * kStageBytes, ahead.row, left > 0 && ahead.major < a.ntok);
     ahead.skip(4, heads);
-    ++fetched;
+    --left;
   };
 #pragma unroll
   for (int j = 0; j < kStages - 1; ++j) fetch(j);
   GlobalScale gs;
   if constexpr (kKeys) gs = global_scale(a.gk);
   Turn turn;
-  turn.on = false;
+  turn.on[0] = turn.on[1] = false;
   int turned = -1;  // the token that `turn` is of
   int stage = 0;
   for (int step = st.begin; step < st.end; ++step) {
     fetch(stage == 0 ? kStages - 1 : stage - 1);
     const int tok = at.major, h = at.head;
+    uint16_t* const dst = const_cast<uint16_t*>(at.row);
     const bool live = tok < a.ntok;
     at.skip(4, heads);
-    if (live && a.rot > 0 && tok != turned) {
-      load_turn<kInterleaved>(a, tok, sub, turn);
+    if (R != kNone && live && tok != turned) {
+      load_turn<R>(a, tok, sub, turn);
       turned = tok;
     }
-    const Row row = take_row(ring + stage * kStageBytes, lane);
+    uint32_t y[8];
+    take_row(ring + stage * kStageBytes + 16 * lane, y);
     stage = stage + 1 == kStages ? 0 : stage + 1;
     float2 f[8];
-    unpack(row.a, f);
-    unpack(row.b, f + 4);
-    if (weight) normalise(f, w, a.eps);
-    if (a.rot > 0) rotate<kInterleaved>(f, turn, lane, a.rot);
-    uint32_t y[8];
 #pragma unroll
-    for (int k = 0; k < 8; ++k) y[k] = pack_bf16x2(f[k].x, f[k].y);
-    if (!live) continue;
+    for (int i = 0; i < 8; ++i) f[i] = unpack2(y[i]);
+    if (weight) normalise(f, w, a.eps);
+    rotate<R>(f, turn, lane, a.rot);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) y[i] = pack_bf16x2(f[i].x, f[i].y);
     if constexpr (kKeys) {
+      const HalfBlocks q = quantize_halves(y, gs);
+      if (!live) continue;
       if (a.ws_rows) store_ws(p, false, __ldg(a.ws_rows + tok), h, sub, y);
       const long long slot = __ldg(a.slots + tok);
       uint8_t* ph = page_head(a, slot, h);
-      if (ph) {
-        float x[16];
-        unpack_words(y, x);
-        const BlockCodes c = quantize_block(x, gs);
-        const int rin = (int)(slot & (kPage - 1));
-        reinterpret_cast<uint2*>(ph + kOffKData + rin * kRowBytes)[sub] = make_uint2(c.lo, c.hi);
-        ph[k_scale_offset(rin, sub)] = (uint8_t)c.sb;
-      }
-    } else {
-      uint4* dst = reinterpret_cast<uint4*>(a.q_out + tok * a.q_out_stride + h * kHeadDim) + 2 * sub;
-      dst[0] = make_uint4(y[0], y[1], y[2], y[3]);
-      dst[1] = make_uint4(y[4], y[5], y[6], y[7]);
+      if (!ph) continue;
+      const int rin = (int)(slot & (kPage - 1));
+      uint32_t* d = reinterpret_cast<uint32_t*>(ph + kOffKData + rin * kRowBytes) + sub;
+      d[0] = q.codes[0];
+      d[8] = q.codes[1];
+      ph[k_scale_offset(rin, (sub >> 1) + 4 * (sub & 1))] = (uint8_t)((sub & 1) ? q.sb[1] : q.sb[0]);  // lane 2 j: block j, 2 j + 1: block 4 + j
+    } else if (live) {
+      *reinterpret_cast<uint4*>(dst) = make_uint4(y[0], y[1], y[2], y[3]);
+      *reinterpret_cast<uint4*>(dst + 64) = make_uint4(y[4], y[5], y[6], y[7]);
     }
   }
   asm volatile("cp.async.wait_all;" ::: "memory");
-  __syncwarp();
 }
 
 // The warp's steps of the values: two units of a token pair and a head each, two
@@ -333,61 +384,63 @@ __device__ __forceinline__ void value_rows(const NormRopeParams& p, Steps st, ui
   const NormRopeArgs& a = p.a;
   const int sub = lane & 7, which = (lane >> 3) & 1;
   const GlobalScale gs = global_scale(a.gv);
-  Walk at, ahead;
-  at.start(2LL * st.begin + (lane >> 4), a.hkv);
-  ahead = at;
-  int fetched = st.begin;
-  const uint32_t ring_u32 = smem_u32(ring);
+  Walk ahead;
+  ahead.start(a.v + which * a.v_stride + 8 * sub, 2LL * st.begin + (lane >> 4), a.hkv, 2 * a.v_stride);
+  int pair = ahead.major, head = ahead.head;
+  int left = st.end - st.begin;
+  const uint32_t ring_u32 = smem_u32(ring) + 16 * lane;
   auto fetch = [&](int stage) {
-    const int tok = 2 * ahead.major + which;
-    const bool live = fetched < st.end && ahead.major < (a.ntok + 1) >> 1 && tok < a.ntok;
-    fetch_row(ring_u32 + stage * kStageBytes, live ? a.v + tok * a.v_stride + ahead.head * kHeadDim : nullptr, lane);
+    fetch_row(ring_u32 + stage * kStageBytes, ahead.row, left > 0 && 2LL * ahead.major + which < a.ntok);
     ahead.skip(2, a.hkv);
-    ++fetched;
+    --left;
   };
 #pragma unroll
   for (int j = 0; j < kStages - 1; ++j) fetch(j);
   int stage = 0;
   for (int step = st.begin; step < st.end; ++step) {
     fetch(stage == 0 ? kStages - 1 : stage - 1);
-    const int tok = 2 * at.major + which, h = at.head;
-    const bool live = at.major < (a.ntok + 1) >> 1 && tok < a.ntok;
-    at.skip(2, a.hkv);
+    const int tok = 2 * pair + which, h = head;
+    const bool live = tok < a.ntok;
+    head += 2;
+    while (head >= a.hkv) {
+      head -= a.hkv;
+      ++pair;
+    }
     const long long slot = live ? __ldg(a.slots + tok) : -1;
     const long long mate = live && (tok ^ 1) < a.ntok ? __ldg(a.slots + (tok ^ 1)) : -1;
-    const Row row = take_row(ring + stage * kStageBytes, lane);
+    uint32_t y[8];
+    take_row(ring + stage * kStageBytes + 16 * lane, y);
     stage = stage + 1 == kStages ? 0 : stage + 1;
-    const uint32_t y[8] = {row.a.x, row.a.y, row.a.z, row.a.w, row.b.x, row.b.y, row.b.z, row.b.w};
-    float f[16];
-    unpack_words(y, f);
-    const BlockCodes c = quantize_block(f, gs);
-    // the pair's other token (lane ^ 8 holds the same block of it)
-    const uint32_t plo = __shfl_xor_sync(kAll, c.lo, 8), phi = __shfl_xor_sync(kAll, c.hi, 8);
+    const HalfBlocks q = quantize_halves(y, gs);
+    // the pair's other token (lane ^ 8 holds the same values of it)
+    const uint32_t o0 = __shfl_xor_sync(kAll, q.codes[0], 8), o1 = __shfl_xor_sync(kAll, q.codes[1], 8);
     if (!live) continue;
     if (a.ws_rows) store_ws(p, true, __ldg(a.ws_rows + tok), h, sub, y);
     uint8_t* ph = page_head(a, slot, h);
     if (!ph) continue;
     const int rin = (int)(slot & (kPage - 1));
     const long long even = which ? mate : slot, odd = which ? slot : mate;
+    uint8_t* const d = ph + kOffVData + (rin >> 1) * kVPairBytes + 8 * sub;
     if ((even & 1) == 0 && odd == even + 1) {
-      if (which == 0) v_store_block_pair(ph + kOffVData, rin >> 1, sub, c.lo, c.hi, plo, phi);
+      // a lane of either token writes one of the two pieces of both
+      *reinterpret_cast<uint2*>(d + 64 * which) = which ? v_pair_bytes(o1, q.codes[1]) : v_pair_bytes(q.codes[0], o0);
     } else {
-      v_store_block_one(ph + kOffVData, rin, sub, c.lo, c.hi);
+      v_store_half_one(d, rin & 1, q.codes[0]);
+      v_store_half_one(d + 64, rin & 1, q.codes[1]);
     }
-    ph[v_scale_offset(rin, sub)] = (uint8_t)c.sb;
+    ph[v_scale_offset(rin, (sub >> 1) + 4 * (sub & 1))] = (uint8_t)((sub & 1) ? q.sb[1] : q.sb[0]);
   }
   asm volatile("cp.async.wait_all;" ::: "memory");
-  __syncwarp();
 }
 
-template <bool kInterleaved>
+template <int R>
 __global__ void __launch_bounds__(kNrThreads, kNrCtasPerSm) norm_rope_kernel(const NormRopeParams p) {
   __shared__ __align__(128) uint8_t rings[kNrWarps][kStages * kStageBytes];
   const int lane = threadIdx.x & 31;
   uint8_t* ring = rings[threadIdx.x >> 5];
-  turn_rows<kInterleaved, true>(p, share(p, p.k_steps, 0), ring, lane);
+  turn_rows<R, true>(p, share(p, p.k_steps, 0), ring, lane);
   value_rows(p, share(p, p.v_steps, p.k_steps), ring, lane);
-  turn_rows<kInterleaved, false>(p, share(p, p.q_steps, p.k_steps + p.v_steps), ring, lane);
+  turn_rows<R, false>(p, share(p, p.q_steps, p.k_steps + p.v_steps), ring, lane);
 }
 
 }  // namespace
@@ -404,10 +457,12 @@ cudaError_t launch_norm_rope_append(const NormRopeArgs& args, float k_ws_scale, 
   const int64_t all = (int64_t)p.q_steps + p.k_steps + p.v_steps, fit = (int64_t)num_sms * kNrCtasPerSm;
   const int64_t need = (all + kNrWarps - 1) / kNrWarps;
   const unsigned blocks = (unsigned)(need < fit ? need : fit);
-  if (args.interleaved)
-    norm_rope_kernel<true><<<blocks, kNrThreads, 0, stream>>>(p);
-  else
-    norm_rope_kernel<false><<<blocks, kNrThreads, 0, stream>>>(p);
+  auto kernel = args.rot == 0         ? norm_rope_kernel<kNone>
+                : args.interleaved    ? norm_rope_kernel<kInterleaved>
+                : args.rot == kHeadDim ? norm_rope_kernel<kWhole>
+                : args.rot == 96      ? norm_rope_kernel<kThreeQuarters>
+                                      : norm_rope_kernel<kFirst>;
+  kernel<<<blocks, kNrThreads, 0, stream>>>(p);
   return cudaGetLastError();
 }
 

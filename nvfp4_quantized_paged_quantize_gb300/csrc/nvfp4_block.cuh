@@ -24,53 +24,65 @@ __device__ __forceinline__ GlobalScale global_scale(float g) {
   return s;
 }
 
-struct BlockCodes {
-  uint32_t lo, hi;  // codes of values 0-7 and 8-15, value i in nibble i % 8
-  uint32_t sb;      // E4M3 block scale
-};
-
 //   amax = max |x|                       (exact; inputs are bf16)
 //   sb   = E4M3(amax / (6 g))            (correctly rounded quotient, RNE, saturating)
 //   den  = E4M3val(sb) * g
 //   code = E2M1(x / den)                 (correctly rounded quotient, RNE, saturating)
 // A block with den == 0 stores signed zeros.
-__device__ __forceinline__ BlockCodes quantize_block(const float (&f)[16], const GlobalScale& s) {
-  float amax = 0.0f;
-#pragma unroll
-  for (int i = 0; i < 16; ++i) amax = fmaxf(amax, fabsf(f[i]));
+struct BlockScale {
+  uint32_t sb;  // E4M3 block scale
+  float den, rcp;
+  bool fast;    // den, 1 / den and every quotient well inside the normal range
+};
+
+__device__ __forceinline__ BlockScale block_scale(float amax, const GlobalScale& s) {
   // the block scale's quotient: Markstein while the first product stays far
   // from overflow (a quotient below 2^-11 encodes as 0 either way)
   const float sq =
       (s.t6_ok && __fmul_rn(amax, s.r6) < 0x1p+64f) ? div_markstein(amax, s.t6, s.r6) : __fdiv_rn(amax, s.t6);
-  BlockCodes c;
-  c.sb = e4m3_from_f32(sq);
-  const float den = __fmul_rn(e4m3_to_f32(c.sb), s.g);
-  c.lo = 0;
-  c.hi = 0;
-  if (den == 0.0f) {
+  BlockScale b;
+  b.sb = e4m3_from_f32(sq);
+  b.den = __fmul_rn(e4m3_to_f32(b.sb), s.g);
+  b.rcp = __frcp_rn(b.den);
+  b.fast = b.den >= 0x1p-100f && b.den <= 0x1p+100f && __fmul_rn(amax, b.rcp) < 0x1p+64f;
+  return b;
+}
+
+// The codes of eight of the block's values, value i in nibble i.
+__device__ __forceinline__ uint32_t block_codes8(const float* f, const BlockScale& b) {
+  uint32_t c = 0;
+  if (b.den == 0.0f) {
     // signed zeros: code 8 for negative inputs
 #pragma unroll
-    for (int i = 0; i < 8; ++i) c.lo |= (__float_as_uint(f[i]) >> 31) << (4 * i + 3);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) c.hi |= (__float_as_uint(f[8 + i]) >> 31) << (4 * i + 3);
-  } else {
-    const float rcp = __frcp_rn(den);
-    float y[16];
-    if (den >= 0x1p-100f && den <= 0x1p+100f && __fmul_rn(amax, rcp) < 0x1p+64f) {
-      // a quotient that rounds to zero can come out as +0 for negative x;
-      // the sign of x / den is the sign of x (den > 0)
-#pragma unroll
-      for (int i = 0; i < 16; ++i) y[i] = copysignf(div_markstein(f[i], den, rcp), f[i]);
-    } else {
-#pragma unroll
-      for (int i = 0; i < 16; ++i) y[i] = __fdiv_rn(f[i], den);
-    }
-#pragma unroll
-    for (int k = 0; k < 4; ++k) c.lo |= e2m1x2_from_f32(y[2 * k], y[2 * k + 1]) << (8 * k);
-#pragma unroll
-    for (int k = 0; k < 4; ++k) c.hi |= e2m1x2_from_f32(y[8 + 2 * k], y[8 + 2 * k + 1]) << (8 * k);
+    for (int i = 0; i < 8; ++i) c |= (__float_as_uint(f[i]) >> 31) << (4 * i + 3);
+    return c;
   }
+  float y[8];
+  if (b.fast) {
+    // a quotient that rounds to zero can come out as +0 for negative x;
+    // the sign of x / den is the sign of x (den > 0)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) y[i] = copysignf(div_markstein(f[i], b.den, b.rcp), f[i]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) y[i] = __fdiv_rn(f[i], b.den);
+  }
+#pragma unroll
+  for (int k = 0; k < 4; ++k) c |= e2m1x2_from_f32(y[2 * k], y[2 * k + 1]) << (8 * k);
   return c;
+}
+
+struct BlockCodes {
+  uint32_t lo, hi;  // codes of values 0-7 and 8-15, value i in nibble i % 8
+  uint32_t sb;      // E4M3 block scale
+};
+
+__device__ __forceinline__ BlockCodes quantize_block(const float (&f)[16], const GlobalScale& s) {
+  float amax = 0.0f;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) amax = fmaxf(amax, fabsf(f[i]));
+  const BlockScale b = block_scale(amax, s);
+  return BlockCodes{block_codes8(f, b), block_codes8(f + 8, b), b.sb};
 }
 
 // Eight packed bf16 (16 bytes) -> fp32.

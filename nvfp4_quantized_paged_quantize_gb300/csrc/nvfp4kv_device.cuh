@@ -185,6 +185,18 @@ __device__ __forceinline__ void v_store_block_one(uint8_t* vdata, int r, int j, 
   }
 }
 
+// The same for half a block: eight codes of a token (odd: the pair's second) into
+// the eight bytes at w.
+__device__ __forceinline__ void v_store_half_one(uint8_t* w, bool odd, uint32_t codes) {
+  const uint2 a = odd ? v_pair_bytes(0u, codes) : v_pair_bytes(codes, 0u);
+  const uint32_t mask = odd ? 0xF0F0F0F0u : 0x0F0F0F0Fu;
+  uint32_t* const at = reinterpret_cast<uint32_t*>(w);
+  const uint2 old = __ldcg(reinterpret_cast<const uint2*>(w));
+  const uint32_t d0 = (a.x ^ old.x) & mask, d1 = (a.y ^ old.y) & mask;
+  if (d0) atomicXor(at, d0);
+  if (d1) atomicXor(at + 1, d1);
+}
+
 // ---------------------------------------------------------------------------
 // shared memory and mbarriers
 // ---------------------------------------------------------------------------
