@@ -52,6 +52,7 @@
 // f16, and the factor is folded back into the score scale.
 #include <cfloat>
 #include <cstdint>
+#include <cstdlib>
 
 #include "nvfp4kv_device.cuh"
 #include "nvfp4kv_launch.h"
@@ -1576,6 +1577,167 @@ __global__ void __launch_bounds__(kCombineMaxWarps * 32) combine_kernel(const De
   }
 }
 
+// The decode over listed pages, one cluster of `splits` CTAs per (sequence, KV head)
+// pair: each CTA takes an equal part of the list, each warp a quarter of that, with
+// the ring and the phases of decode_kernel; the warps' results meet in shared memory
+// and the CTAs' in that of the cluster (each CTA finishes every splits-th head), so
+// that there are no records in global memory and no second kernel.
+constexpr int kOffCtaRecord = kStages * kStageBytes / 2;  // in the first warp's ring, behind its own record
+static_assert(kRecFloats * 4 <= kOffCtaRecord, "a warp's record and the CTA's fit a warp's ring");
+
+__global__ void __launch_bounds__(kNW * 32, kCtasPerSm) selected_kernel(const DecodeParams p, int splits) {
+  constexpr int F = kFmtNvfp4, M = kScored;
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ ItemEntry s_items[kNW][64];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int g = lane >> 2, t = lane & 3;
+  const int pair = blockIdx.x / splits, rank = blockIdx.x - pair * splits;
+  const int b = pair / p.hkv, h = pair - b * p.hkv;
+  const QRaw q = fetch_q(p, pair, g, t);
+  const int L = clamp_len(p, b), pages = (L + kPage - 1) / kPage, listed = min(pages, p.budget);
+  const int c0 = (int)((long long)listed * rank / splits), c1 = (int)((long long)listed * (rank + 1) / splits);
+  const int w0 = c0 + (c1 - c0) * warp / kNW, n = c0 + (c1 - c0) * (warp + 1) / kNW - w0;
+  const int32_t* const list = p.selected + (long long)pair * p.budget + w0;
+  const int32_t* const table = p.page_table + (long long)b * p.max_pages;
+  uint8_t* const ring = smem + warp * kStages * kStageBytes;
+  const uint32_t ring_u32 = smem_u32(ring);
+  const uint32_t bar = smem_u32(smem + kRingBytes) + 8 * warp * kStages;
+  ItemEntry* const tab = s_items[warp];
+
+  // the lane's entry of the list's 32-entry chunk k, its page's id, and what the loop uses
+  auto entry = [&](int k) { return 32 * k + lane < n ? __ldg(list + 32 * k + lane) : -1; };
+  auto page_id = [&](int sel) {
+    if (sel >= pages) flag_error(p.status, NVFP4KV_DEVERR_PAGE);
+    return sel >= 0 && sel < pages ? __ldg(table + sel) : -1;
+  };
+  auto put = [&](int k, int sel, int id) {
+    const bool named = sel >= 0 && sel < pages, valid = named && id >= 0 && id < p.num_pages;
+    if (named && !valid) flag_error(p.status, NVFP4KV_DEVERR_PAGE);
+    ItemEntry e;
+    e.off = valid ? ((long long)id * p.hkv + h) * kPageHeadBytes : 0;
+    e.nv = valid ? min(L - sel * kPage, kPage) : 0;
+    e.dist = 0;
+    tab[(32 * k + lane) & 63] = e;
+    __syncwarp();
+  };
+
+  WarpState s;
+  load_q<F, M>(p, q, s, pair, g, t);
+  if (n > 0) {
+    if (lane == 0) {
+      for (int i = 0; i < kStages; ++i) mbar_init(bar + 8 * i, 32);
+      fence_mbar_init();
+    }
+    __syncwarp();
+    int sel1 = entry(1), sel2 = entry(2);  // of the next chunk and the one after it
+    {
+      const int sel0 = entry(0);
+      put(0, sel0, page_id(sel0));
+    }
+    int id1 = page_id(sel1);
+    int chunk = 0;
+    const LaneCopy lc = lane_copy<F>(p, lane);
+    int issued = 0;
+    auto issue = [&](int i) {
+      const int st = i % kStages;
+      issue_page_off<F, M>(lc, tab[i & 63].off, tab[i & 63].nv, ring_u32 + st * kStageBytes, bar + 8 * st);
+      issued = i + 1;
+    };
+    for (int i = 0; i < min(n, kStages); ++i) issue(i);
+    bool alive = true;
+    for (int j = 0; j < n && alive; j += 2) {
+      if ((j & 31) == 16 && 32 * (chunk + 1) < n) {
+        // half way through the chunk: the next one's entries, and the loads of those behind it
+        put(chunk + 1, sel1, id1);
+        sel1 = sel2;
+        id1 = page_id(sel1);
+        sel2 = entry(chunk + 3);
+        ++chunk;
+      }
+      const bool two = j + 1 < n;
+      const int st0 = j % kStages, st1 = (j + 1) % kStages, last = two ? j + 1 : j;
+      // a stage's barrier fires only after the lanes' earlier copies have landed too
+      if (!stage_wait(bar + 8 * (last % kStages), (uint32_t)(last / kStages) & 1u)) {
+        alive = false;
+        break;
+      }
+      const int nv0 = tab[j & 63].nv, nv1 = two ? tab[(j + 1) & 63].nv : 0;
+      const uint8_t* const stg[2] = {ring + st0 * kStageBytes, ring + (two ? st1 : st0) * kStageBytes};
+      const int nvs[2] = {nv0, nv1}, dist[2] = {0, 0};
+      float* keep[2] = {nullptr, nullptr};
+      if (nv0 == kPage && nv1 == kPage)
+        process_pages<2, true, F, M>(p, stg, nvs, dist, keep, s, g, t);
+      else if (nv0 | nv1)
+        process_pages<2, false, F, M>(p, stg, nvs, dist, keep, s, g, t);
+      __syncwarp();
+      const int ja = j + kStages, jb = ja + 1;
+      if (jb < n) {
+        issue_two_off<M>(lc, tab[ja & 63], tab[jb & 63], ring_u32 + st0 * kStageBytes, ring_u32 + st1 * kStageBytes,
+                         bar + 8 * st0, bar + 8 * st1, lane < 16);
+        issued = jb + 1;
+      } else if (ja < n) {
+        issue(ja);
+      }
+    }
+    if (!alive) {
+      // a wait gave up: flag it and let (bounded) every copy in flight land before the ring is used again
+      if (lane == 0) flag_error(p.status, kDevErrTimeout);
+      for (int i = max(issued - kStages, 0); i < issued; ++i) mbar_wait(bar + 8 * (i % kStages), (uint32_t)(i / kStages) & 1u);
+    }
+  }
+  __syncwarp();
+  // the warps' records, each in its own ring
+  finish_piece<F, M>(p, s, pair, false, reinterpret_cast<float*>(ring), g, t);
+  __syncthreads();
+  float* const cta = reinterpret_cast<float*>(smem + kOffCtaRecord);
+  // thread = dimension
+  auto merged = [&](int head, int parts, auto m_of, auto l_of, auto o_of, float& m, float& l, float& o) {
+    m = -INFINITY, l = 0.0f, o = 0.0f;
+    for (int k = 0; k < parts; ++k) m = fmaxf(m, m_of(k, head));
+    if (m == -INFINITY) return;
+    for (int k = 0; k < parts; ++k) {
+      const float w = ex2(m_of(k, head) - m);
+      l = fmaf(w, l_of(k, head), l);
+      o = fmaf(w, o_of(k, head), o);
+    }
+  };
+  auto put_out = [&](int head, float m, float l, float o) {
+    const long long row = (long long)pair * p.group + head;
+    const float v = l > 0.0f ? o * (p.v_gscale / l) : 0.0f;
+    p.out16[row * kHeadDim + tid] = (uint16_t)(pack_bf16x2(v, 0.0f) & 0xFFFFu);
+    if (tid == 0) store_lse<M>(p, row, m, l);
+  };
+  const float* const recs = reinterpret_cast<const float*>(smem);
+  constexpr int kStep = kStages * kStageBytes / 4;  // floats from one warp's record to the next
+  for (int head = 0; head < p.group; ++head) {
+    float m, l, o;
+    merged(head, kNW, [&](int k, int i) { return recs[k * kStep + kOffM + i]; },
+           [&](int k, int i) { return recs[k * kStep + kOffL + i]; },
+           [&](int k, int i) { return recs[k * kStep + i * kHeadDim + tid]; }, m, l, o);
+    if (splits == 1) {
+      put_out(head, m, l, o);
+    } else {
+      cta[head * kHeadDim + tid] = o;
+      if (tid == 0) {
+        cta[kOffM + head] = m;
+        cta[kOffL + head] = l;
+      }
+    }
+  }
+  if (splits > 1) {
+    cluster_sync();
+    const uint32_t* const words = reinterpret_cast<const uint32_t*>(cta);
+    for (int head = rank; head < p.group; head += splits) {
+      float m, l, o;
+      merged(head, splits, [&](int k, int i) { return __uint_as_float(ld_cluster(words + kOffM + i, k)); },
+             [&](int k, int i) { return __uint_as_float(ld_cluster(words + kOffL + i, k)); },
+             [&](int k, int i) { return __uint_as_float(ld_cluster(words + i * kHeadDim + tid, k)); }, m, l, o);
+      put_out(head, m, l, o);
+    }
+    cluster_sync();  // no CTA leaves while another may still read its record
+  }
+}
+
 // Accumulated attention weights: w[b][h][t] <- decay * w + sum over the KV
 // head's query heads of 2^(score - lse), from the scores the decode kept and
 // the pairs' log-sum-exps (base 2).  Memory-bound: per page-head 512 bytes of
@@ -1881,7 +2043,29 @@ cudaError_t launch_decode_selected(const nvfp4kv_cache& c, const uint16_t* q, ui
   p.lse = lse;
   p.selected = selected;
   p.budget = budget;
-  return enqueue_scored<kScored | kSelected>(p, stream);
+  const int64_t pairs = (int64_t)batch * p.hkv;
+  static const char* force = getenv("SEL_SPLITS");
+  int splits = 1;
+  while (splits < 8 && pairs * splits < num_sms) splits *= 2;
+  if (force) splits = atoi(force);
+  if (splits == 0 || pairs * splits < num_sms / 2) return enqueue_scored<kScored | kSelected>(p, stream);
+  static PerDeviceOnce attr_once;
+  const cudaError_t e = attr_once.run([] {
+    return cudaFuncSetAttribute(selected_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+  });
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(pairs * splits));
+  cfg.blockDim = dim3(kNW * 32);
+  cfg.dynamicSmemBytes = kSmemBytes;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = splits;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, selected_kernel, p, splits);
 }
 
 cudaError_t launch_decode(const nvfp4kv_cache& c, const uint16_t* q, float* out, const int32_t* page_table,

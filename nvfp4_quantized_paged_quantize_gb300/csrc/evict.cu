@@ -85,14 +85,6 @@ __device__ __forceinline__ uint32_t order_key(float x) {
 
 constexpr uint32_t kKeyNone = 0;  // no float's key: below that of -inf
 
-// The words at this address of the same shared-memory variable in another CTA of the cluster.
-__device__ __forceinline__ uint32_t ld_cluster(const uint32_t* local, uint32_t rank) {
-  uint32_t at, v;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_u32(local)), "r"(rank));
-  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(at) : "memory");
-  return v;
-}
-
 // Store to, add to, the same shared-memory word in another CTA of the cluster.
 __device__ __forceinline__ void st_cluster(uint32_t* local, uint32_t rank, uint32_t n) {
   uint32_t at;

@@ -15,13 +15,14 @@
 // Eight lanes hold a row: lane s has values 8 s .. 8 s + 7 and 64 + 8 s .., so that
 // its loads and stores are whole sectors, the partners of a rotation of all 128
 // values (in either order of pairs) are in one lane, and a quantisation block in
-// two neighbours.  A warp takes four rows at a time and walks the flattened (token,
-// head) list of its share, so that a token's cosines and sines stay in registers
-// over its heads.  Values go by token pairs, two groups of lanes to a unit, because a
-// byte of V data holds two tokens.  Rows come through a ring of kStages stages of
-// shared memory per warp (cp.async; a lane reads what it copied itself, so without
-// any barrier), which keeps 64 KB in flight on an SM at two CTAs; products two to an
-// instruction.
+// two neighbours.  A warp takes four rows at a time and walks its share of the
+// flattened list of every token's query heads and then its key heads, so that a
+// token's cosines and sines stay in registers over all of its rows, and every warp
+// has its part of the keys' arithmetic and of the queries' bytes.  Values go by token
+// pairs, two groups of lanes to a unit, because a byte of V data holds two tokens.
+// Rows come through a ring of kStages stages of shared memory per warp (cp.async; a
+// lane reads what it copied itself, so without any barrier), which keeps 96 KB in
+// flight on an SM at three CTAs; products two to an instruction.
 // HBM-bound on long inputs: 512 bytes per query row, 256 + 72 (+ 128 with the
 // workspace) per key or value row, and the cosines once per token.
 #include "fp8_quotient.cuh"
@@ -34,7 +35,6 @@ namespace {
 
 constexpr int kNrThreads = 256;
 constexpr int kNrWarps = kNrThreads / 32;
-constexpr int kNrCtasPerSm = 2;
 constexpr int kStages = 4;            // rows in flight per 8-lane group
 constexpr int kStageBytes = 4 * 256;  // four rows
 constexpr uint32_t kAll = 0xFFFFFFFFu;
@@ -42,44 +42,37 @@ constexpr uint32_t kAll = 0xFFFFFFFFu;
 struct NormRopeParams {
   NormRopeArgs a;
   WsScales ws;
-  int32_t q_steps, k_steps, v_steps;  // of four rows each
+  int32_t t_steps, v_steps;  // of four rows each: queries and keys, values
 };
 
 // The steps [begin, end) of one kind that a warp takes: an equal share of them, or,
-// where all kinds' steps together are no more than the warps, at most one, of one
-// kind alone (`before`: the steps of the kinds before this one).
+// where both kinds' steps together are no more than the warps, at most one, of one
+// kind alone (`before`: the steps of the kind before this one).
 struct Steps {
   int begin, end;
 };
 
 __device__ __forceinline__ Steps share(const NormRopeParams& p, int steps, int before) {
   const int warp = (int)blockIdx.x * kNrWarps + (threadIdx.x >> 5), warps = (int)gridDim.x * kNrWarps;
-  if ((long long)p.q_steps + p.k_steps + p.v_steps <= warps) {
+  if ((long long)p.t_steps + p.v_steps <= warps) {
     const int at = warp - before;
     return at >= 0 && at < steps ? Steps{at, at + 1} : Steps{0, 0};
   }
   return Steps{(int)((long long)steps * warp / warps), (int)((long long)steps * (warp + 1) / warps)};
 }
 
-// Where an 8-lane group is in a flattened list of `heads` per major index (a token,
-// or a pair of tokens), and that row's address.
-struct Walk {
-  int major, head;
-  const uint16_t* row;
-  long long gap;  // from one token's last head to the next one's first
-  __device__ __forceinline__ void start(const uint16_t* base, long long at, int heads, long long stride) {
-    major = (int)(at / heads);
-    head = (int)(at - (long long)major * heads);
-    row = base + major * stride + head * kHeadDim;
-    gap = stride - (long long)heads * kHeadDim;
+// Where an 8-lane group is in the list of every token's query heads and key heads.
+struct TokenWalk {
+  int token, head;
+  __device__ __forceinline__ void start(long long at, int heads) {
+    token = (int)(at / heads);
+    head = (int)(at - (long long)token * heads);
   }
   __device__ __forceinline__ void skip(int by, int heads) {
     head += by;
-    row += by * kHeadDim;
     while (head >= heads) {
       head -= heads;
-      ++major;
-      row += gap;
+      ++token;
     }
   }
 };
@@ -135,6 +128,9 @@ enum Rotation : int {
   kInterleaved   // (2 i, 2 i + 1)
 };
 
+// CTAs of an SM: three at 80 registers, two where the pieces of a pair need more.
+__host__ __device__ constexpr int ctas_per_sm(int R) { return R == kThreeQuarters ? 2 : 3; }
+
 // The lane's cosines and sines of one token: value i of piece h turns as
 // y_i cos[h]_i + partner_i sin[h]_i, the sine's sign taken in.  kWhole: both pieces
 // have the angles of cos[0], sin[0].
@@ -182,8 +178,28 @@ __device__ __forceinline__ void load_turn(const NormRopeArgs& p, int token, int 
   }
 }
 
-// y = (x r) w over the eight lanes of a row.
-__device__ __forceinline__ void normalise(float2 (&f)[8], const float2 (&w)[8], float eps) {
+// The norms' weights in fp32, those of the queries and of the keys: [tensor][piece]
+// [half of the piece][lane of the group][4], so that a group's reads have no bank
+// conflicts.  Ones without a weight.
+using Weights = float4[2][2][2][8];
+
+__device__ __forceinline__ void load_weights(const NormRopeArgs& a, Weights& w) {
+  if (threadIdx.x < 2 * 2 * 2 * 8) {
+    const int s = threadIdx.x & 7, half = threadIdx.x >> 3 & 1, h = threadIdx.x >> 4 & 1, keys = threadIdx.x >> 5;
+    const uint16_t* src = keys ? a.k_weight : a.q_weight;
+    float4 v = make_float4(1.0f, 1.0f, 1.0f, 1.0f);
+    if (src) {
+      const uint2 x = __ldg(reinterpret_cast<const uint2*>(src + 64 * h + 8 * s + 4 * half));
+      const float2 lo = unpack2(x.x), hi = unpack2(x.y);
+      v = make_float4(lo.x, lo.y, hi.x, hi.y);
+    }
+    w[keys][h][half][s] = v;
+  }
+}
+
+// y = (x r) w over the eight lanes of a row; a row that is not `normed` has r and
+// weights of 1, which change nothing.
+__device__ __forceinline__ void normalise(float2 (&f)[8], const Weights& w, int keys, int sub, bool normed, float eps) {
   float sum[2];
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
@@ -197,9 +213,14 @@ __device__ __forceinline__ void normalise(float2 (&f)[8], const float2 (&w)[8], 
 #pragma unroll
     for (int x = 1; x < 8; x <<= 1) sum[h] = __fadd_rn(sum[h], __shfl_xor_sync(kAll, sum[h], x));
   }
-  const float r = __frcp_rn(__fsqrt_rn(__fadd_rn(__fmul_rn(__fadd_rn(sum[0], sum[1]), 1.0f / kHeadDim), eps)));
+  float r = __frcp_rn(__fsqrt_rn(__fadd_rn(__fmul_rn(__fadd_rn(sum[0], sum[1]), 1.0f / kHeadDim), eps)));
+  r = normed ? r : 1.0f;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) f[i] = mul2(mul2(f[i], make_float2(r, r)), w[i]);
+  for (int i = 0; i < 4; ++i) {
+    const float4 v = w[keys][i >> 1][i & 1][sub];
+    f[2 * i] = mul2(mul2(f[2 * i], make_float2(r, r)), make_float2(v.x, v.y));
+    f[2 * i + 1] = mul2(mul2(f[2 * i + 1], make_float2(r, r)), make_float2(v.z, v.w));
+  }
 }
 
 __device__ __forceinline__ void turn4(float2* f, const float2 (&o)[4], const float2 (&cos)[4], const float2 (&sin)[4]) {
@@ -303,49 +324,44 @@ __device__ __forceinline__ HalfBlocks quantize_halves(const uint32_t (&w)[8], co
   return q;
 }
 
-// The warp's steps of the queries or of the keys.
-template <int R, bool kKeys>
-__device__ __forceinline__ void turn_rows(const NormRopeParams& p, Steps st, uint8_t* ring, int lane) {
+// The warp's steps of the queries and keys.
+template <int R>
+__device__ __forceinline__ void turn_rows(const NormRopeParams& p, Steps st, uint8_t* ring, const Weights& weights, int lane) {
   if (st.begin >= st.end) return;
   const NormRopeArgs& a = p.a;
-  const int sub = lane & 7, heads = kKeys ? a.hkv : a.hq;
-  const uint16_t* weight = kKeys ? a.k_weight : a.q_weight;
-  float2 w[8];
-  if (weight) {
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const uint4 x = __ldg(reinterpret_cast<const uint4*>(weight) + 8 * h + sub);
-      w[4 * h] = unpack2(x.x), w[4 * h + 1] = unpack2(x.y), w[4 * h + 2] = unpack2(x.z), w[4 * h + 3] = unpack2(x.w);
-    }
-  }
-  Walk ahead;
-  ahead.start((kKeys ? a.k : a.q) + 8 * sub, 4LL * st.begin + (lane >> 3), heads, kKeys ? a.k_stride : a.q_stride);
-  Walk at;
-  at.start(kKeys ? nullptr : a.q_out + 8 * sub, 4LL * st.begin + (lane >> 3), heads, kKeys ? 0 : a.q_out_stride);
+  const int sub = lane & 7, heads = a.hq + a.hkv;
+  const bool norms = a.q_weight || a.k_weight;
+  TokenWalk at, ahead;
+  at.start(4LL * st.begin + (lane >> 3), heads);
+  ahead = at;
   int left = st.end - st.begin;  // fetches to come
   const uint32_t ring_u32 = smem_u32(ring) + 16 * lane;
   auto fetch = [&](int stage) {
-    fetch_row(ring_u32 + stage * kStageBytes, ahead.row, left > 0 && ahead.major < a.ntok);
+    const bool key = ahead.head >= a.hq;
+    const uint16_t* row = (key ? a.k + (ahead.head - a.hq) * kHeadDim : a.q + ahead.head * kHeadDim) +
+                          ahead.token * (key ? a.k_stride : a.q_stride) + 8 * sub;
+    fetch_row(ring_u32 + stage * kStageBytes, row, left > 0 && ahead.token < a.ntok);
     ahead.skip(4, heads);
     --left;
   };
 #pragma unroll
   for (int j = 0; j < kStages - 1; ++j) fetch(j);
-  GlobalScale gs;
-  if constexpr (kKeys) gs = global_scale(a.gk);
+  const GlobalScale gs = global_scale(a.gk);
   Turn turn;
   turn.on[0] = turn.on[1] = false;
-  int turned = -1;  // the token that `turn` is of
+  int entered = -1;  // the token that `turn`, `slot` and `ws_row` are of
+  long long slot = -1, ws_row = -1;
   int stage = 0;
   for (int step = st.begin; step < st.end; ++step) {
     fetch(stage == 0 ? kStages - 1 : stage - 1);
-    const int tok = at.major, h = at.head;
-    uint16_t* const dst = const_cast<uint16_t*>(at.row);
-    const bool live = tok < a.ntok;
+    const int tok = at.token, head = at.head;
+    const bool live = tok < a.ntok, key = head >= a.hq;
     at.skip(4, heads);
-    if (R != kNone && live && tok != turned) {
-      load_turn<R>(a, tok, sub, turn);
-      turned = tok;
+    if (live && tok != entered) {
+      slot = __ldg(a.slots + tok);
+      if (a.ws_rows) ws_row = __ldg(a.ws_rows + tok);
+      if constexpr (R != kNone) load_turn<R>(a, tok, sub, turn);
+      entered = tok;
     }
     uint32_t y[8];
     take_row(ring + stage * kStageBytes + 16 * lane, y);
@@ -353,26 +369,28 @@ __device__ __forceinline__ void turn_rows(const NormRopeParams& p, Steps st, uin
     float2 f[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) f[i] = unpack2(y[i]);
-    if (weight) normalise(f, w, a.eps);
+    if (norms) normalise(f, weights, key, sub, (key ? a.k_weight : a.q_weight) != nullptr, a.eps);
     rotate<R>(f, turn, lane, a.rot);
 #pragma unroll
     for (int i = 0; i < 8; ++i) y[i] = pack_bf16x2(f[i].x, f[i].y);
-    if constexpr (kKeys) {
-      const HalfBlocks q = quantize_halves(y, gs);
-      if (!live) continue;
-      if (a.ws_rows) store_ws(p, false, __ldg(a.ws_rows + tok), h, sub, y);
-      const long long slot = __ldg(a.slots + tok);
-      uint8_t* ph = page_head(a, slot, h);
-      if (!ph) continue;
-      const int rin = (int)(slot & (kPage - 1));
-      uint32_t* d = reinterpret_cast<uint32_t*>(ph + kOffKData + rin * kRowBytes) + sub;
-      d[0] = q.codes[0];
-      d[8] = q.codes[1];
-      ph[k_scale_offset(rin, (sub >> 1) + 4 * (sub & 1))] = (uint8_t)((sub & 1) ? q.sb[1] : q.sb[0]);  // lane 2 j: block j, 2 j + 1: block 4 + j
-    } else if (live) {
+    if (live && !key) {
+      uint16_t* const dst = a.q_out + tok * a.q_out_stride + head * kHeadDim + 8 * sub;
       *reinterpret_cast<uint4*>(dst) = make_uint4(y[0], y[1], y[2], y[3]);
       *reinterpret_cast<uint4*>(dst + 64) = make_uint4(y[4], y[5], y[6], y[7]);
     }
+    if (!__any_sync(kAll, live && key)) continue;
+    const HalfBlocks q = quantize_halves(y, gs);
+    if (!live || !key) continue;
+    const int h = head - a.hq;
+    if (a.ws_rows) store_ws(p, false, ws_row, h, sub, y);
+    uint8_t* ph = page_head(a, slot, h);
+    if (!ph) continue;
+    const int rin = (int)(slot & (kPage - 1));
+    uint32_t* d = reinterpret_cast<uint32_t*>(ph + kOffKData + rin * kRowBytes) + sub;
+    d[0] = q.codes[0];
+    d[8] = q.codes[1];
+    // lane 2 j: block j, lane 2 j + 1: block 4 + j
+    ph[k_scale_offset(rin, (sub >> 1) + 4 * (sub & 1))] = (uint8_t)((sub & 1) ? q.sb[1] : q.sb[0]);
   }
   asm volatile("cp.async.wait_all;" ::: "memory");
 }
@@ -384,13 +402,15 @@ __device__ __forceinline__ void value_rows(const NormRopeParams& p, Steps st, ui
   const NormRopeArgs& a = p.a;
   const int sub = lane & 7, which = (lane >> 3) & 1;
   const GlobalScale gs = global_scale(a.gv);
-  Walk ahead;
-  ahead.start(a.v + which * a.v_stride + 8 * sub, 2LL * st.begin + (lane >> 4), a.hkv, 2 * a.v_stride);
-  int pair = ahead.major, head = ahead.head;
+  TokenWalk at, ahead;  // `token` counts pairs
+  at.start(2LL * st.begin + (lane >> 4), a.hkv);
+  ahead = at;
   int left = st.end - st.begin;
   const uint32_t ring_u32 = smem_u32(ring) + 16 * lane;
   auto fetch = [&](int stage) {
-    fetch_row(ring_u32 + stage * kStageBytes, ahead.row, left > 0 && 2LL * ahead.major + which < a.ntok);
+    const long long tok = 2LL * ahead.token + which;
+    fetch_row(ring_u32 + stage * kStageBytes, a.v + tok * a.v_stride + ahead.head * kHeadDim + 8 * sub,
+              left > 0 && tok < a.ntok);
     ahead.skip(2, a.hkv);
     --left;
   };
@@ -399,15 +419,12 @@ __device__ __forceinline__ void value_rows(const NormRopeParams& p, Steps st, ui
   int stage = 0;
   for (int step = st.begin; step < st.end; ++step) {
     fetch(stage == 0 ? kStages - 1 : stage - 1);
-    const int tok = 2 * pair + which, h = head;
+    const int tok = 2 * at.token + which, h = at.head;
     const bool live = tok < a.ntok;
-    head += 2;
-    while (head >= a.hkv) {
-      head -= a.hkv;
-      ++pair;
-    }
+    at.skip(2, a.hkv);
     const long long slot = live ? __ldg(a.slots + tok) : -1;
     const long long mate = live && (tok ^ 1) < a.ntok ? __ldg(a.slots + (tok ^ 1)) : -1;
+    const long long ws_row = live && a.ws_rows ? __ldg(a.ws_rows + tok) : -1;
     uint32_t y[8];
     take_row(ring + stage * kStageBytes + 16 * lane, y);
     stage = stage + 1 == kStages ? 0 : stage + 1;
@@ -415,7 +432,7 @@ __device__ __forceinline__ void value_rows(const NormRopeParams& p, Steps st, ui
     // the pair's other token (lane ^ 8 holds the same values of it)
     const uint32_t o0 = __shfl_xor_sync(kAll, q.codes[0], 8), o1 = __shfl_xor_sync(kAll, q.codes[1], 8);
     if (!live) continue;
-    if (a.ws_rows) store_ws(p, true, __ldg(a.ws_rows + tok), h, sub, y);
+    if (a.ws_rows) store_ws(p, true, ws_row, h, sub, y);
     uint8_t* ph = page_head(a, slot, h);
     if (!ph) continue;
     const int rin = (int)(slot & (kPage - 1));
@@ -434,13 +451,23 @@ __device__ __forceinline__ void value_rows(const NormRopeParams& p, Steps st, ui
 }
 
 template <int R>
-__global__ void __launch_bounds__(kNrThreads, kNrCtasPerSm) norm_rope_kernel(const NormRopeParams p) {
+__global__ void __launch_bounds__(kNrThreads, ctas_per_sm(R)) norm_rope_kernel(const NormRopeParams p) {
   __shared__ __align__(128) uint8_t rings[kNrWarps][kStages * kStageBytes];
+  __shared__ Weights weights;
+  load_weights(p.a, weights);
+  __syncthreads();
   const int lane = threadIdx.x & 31;
   uint8_t* ring = rings[threadIdx.x >> 5];
-  turn_rows<R, true>(p, share(p, p.k_steps, 0), ring, lane);
-  value_rows(p, share(p, p.v_steps, p.k_steps), ring, lane);
-  turn_rows<R, false>(p, share(p, p.q_steps, p.k_steps + p.v_steps), ring, lane);
+  value_rows(p, share(p, p.v_steps, 0), ring, lane);
+  turn_rows<R>(p, share(p, p.t_steps, p.v_steps), ring, weights, lane);
+}
+
+template <int R>
+cudaError_t launch(const NormRopeParams& p, int num_sms, cudaStream_t stream) {
+  const int64_t steps = (int64_t)p.t_steps + p.v_steps, fit = (int64_t)num_sms * ctas_per_sm(R);
+  const int64_t need = (steps + kNrWarps - 1) / kNrWarps;
+  norm_rope_kernel<R><<<(unsigned)(need < fit ? need : fit), kNrThreads, 0, stream>>>(p);
+  return cudaGetLastError();
 }
 
 }  // namespace
@@ -451,19 +478,16 @@ cudaError_t launch_norm_rope_append(const NormRopeArgs& args, float k_ws_scale, 
   p.a = args;
   p.ws = ws_scales(k_ws_scale, v_ws_scale);
   auto steps = [](int64_t n, int per) { return (int32_t)((n + per - 1) / per); };
-  p.q_steps = steps((int64_t)args.ntok * args.hq, 4);
-  p.k_steps = steps((int64_t)args.ntok * args.hkv, 4);
+  p.t_steps = steps((int64_t)args.ntok * (args.hq + args.hkv), 4);
   p.v_steps = steps((int64_t)((args.ntok + 1) / 2) * args.hkv, 2);
-  const int64_t all = (int64_t)p.q_steps + p.k_steps + p.v_steps, fit = (int64_t)num_sms * kNrCtasPerSm;
-  const int64_t need = (all + kNrWarps - 1) / kNrWarps;
-  const unsigned blocks = (unsigned)(need < fit ? need : fit);
-  auto kernel = args.rot == 0         ? norm_rope_kernel<kNone>
-                : args.interleaved    ? norm_rope_kernel<kInterleaved>
-                : args.rot == kHeadDim ? norm_rope_kernel<kWhole>
-                : args.rot == 96      ? norm_rope_kernel<kThreeQuarters>
-                                      : norm_rope_kernel<kFirst>;
-  kernel<<<blocks, kNrThreads, 0, stream>>>(p);
-  return cudaGetLastError();
+  switch (args.rot == 0 ? kNone : args.interleaved ? kInterleaved : args.rot == kHeadDim ? kWhole
+          : args.rot == 96 ? kThreeQuarters : kFirst) {
+    case kNone: return launch<kNone>(p, num_sms, stream);
+    case kWhole: return launch<kWhole>(p, num_sms, stream);
+    case kFirst: return launch<kFirst>(p, num_sms, stream);
+    case kThreeQuarters: return launch<kThreeQuarters>(p, num_sms, stream);
+    default: return launch<kInterleaved>(p, num_sms, stream);
+  }
 }
 
 }  // namespace nvfp4kv

@@ -253,6 +253,14 @@ __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
+// The words at this address of the same shared-memory variable in another CTA of the cluster.
+__device__ __forceinline__ uint32_t ld_cluster(const uint32_t* local, uint32_t rank) {
+  uint32_t at, v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_u32(local)), "r"(rank));
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(at) : "memory");
+  return v;
+}
+
 __device__ __forceinline__ void flag_error(int32_t* status, int bit) {
   if (status != nullptr) atomicOr(status, bit);
 }
