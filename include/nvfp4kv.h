@@ -643,7 +643,7 @@ typedef struct nvfp4kv_norm_rope {
  *                 be q itself (with q_stride), and must not overlap q otherwise, nor k or v
  *   ws_rows       device int64 [num_tokens], or NULL: no workspace (total_rows, the scales,
  *                 ws_k and ws_v are then not looked at)
- * num_tokens * heads < 2^31.  Values up to 2^60 in size have exact norms.  Enqueues
+ * num_tokens < 2^30, num_tokens * heads < 2^31.  Values up to 2^60 in size have exact norms.  Enqueues
  * one kernel. */
 int nvfp4kv_norm_rope_append(const nvfp4kv_cache* cache, const void* q, int64_t q_stride, const void* k,
                              int64_t k_stride, const void* v, int64_t v_stride, int32_t num_q_heads,

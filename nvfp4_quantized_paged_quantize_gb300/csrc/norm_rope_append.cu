@@ -15,11 +15,12 @@
 // Eight lanes hold a row: lane s has values 8 s .. 8 s + 7 and 64 + 8 s .., so that
 // its loads and stores are whole sectors, the partners of a rotation of all 128
 // values (in either order of pairs) are in one lane, and a quantisation block in
-// two neighbours.  A warp takes four rows at a time and walks its share of the
-// flattened list of every token's query heads and then its key heads, so that a
-// token's cosines and sines stay in registers over all of its rows, and every warp
-// has its part of the keys' arithmetic and of the queries' bytes.  Values go by token
-// pairs, two groups of lanes to a unit, because a byte of V data holds two tokens.
+// two neighbours.  A step is four heads of one token, all queries or all keys (the
+// last one of either may have fewer), and a warp walks its share of the list of every
+// token's steps: what a step does is the same over the warp, a token's cosines and
+// sines stay in registers over its steps, and every warp has its part of the keys'
+// arithmetic and of the queries' bytes.  Values go by two heads of a token pair,
+// because a byte of V data holds two tokens.
 // Rows come through a ring of kStages stages of shared memory per warp (cp.async; a
 // lane reads what it copied itself, so without any barrier), which keeps 96 KB in
 // flight on an SM at three CTAs; products two to an instruction.
@@ -42,7 +43,9 @@ constexpr uint32_t kAll = 0xFFFFFFFFu;
 struct NormRopeParams {
   NormRopeArgs a;
   WsScales ws;
-  int32_t t_steps, v_steps;  // of four rows each: queries and keys, values
+  int32_t q_steps, k_steps;  // of one token
+  int32_t v_steps;           // of one token pair
+  int32_t t_all, v_all;      // of all tokens, of all pairs
 };
 
 // The steps [begin, end) of one kind that a warp takes: an equal share of them, or,
@@ -52,30 +55,14 @@ struct Steps {
   int begin, end;
 };
 
-__device__ __forceinline__ Steps share(const NormRopeParams& p, int steps, int before) {
-  const int warp = (int)blockIdx.x * kNrWarps + (threadIdx.x >> 5), warps = (int)gridDim.x * kNrWarps;
-  if ((long long)p.t_steps + p.v_steps <= warps) {
+__device__ __forceinline__ Steps share(const NormRopeParams& p, int warp_in_block, int steps, int before) {
+  const int warp = (int)blockIdx.x * kNrWarps + warp_in_block, warps = (int)gridDim.x * kNrWarps;
+  if ((long long)p.t_all + p.v_all <= warps) {
     const int at = warp - before;
     return at >= 0 && at < steps ? Steps{at, at + 1} : Steps{0, 0};
   }
   return Steps{(int)((long long)steps * warp / warps), (int)((long long)steps * (warp + 1) / warps)};
 }
-
-// Where an 8-lane group is in the list of every token's query heads and key heads.
-struct TokenWalk {
-  int token, head;
-  __device__ __forceinline__ void start(long long at, int heads) {
-    token = (int)(at / heads);
-    head = (int)(at - (long long)token * heads);
-  }
-  __device__ __forceinline__ void skip(int by, int heads) {
-    head += by;
-    while (head >= heads) {
-      head -= heads;
-      ++token;
-    }
-  }
-};
 
 // Starts the copy of the lane's two pieces of a row (none if it is not live) into a
 // stage: [half][lane][16 bytes].
@@ -329,40 +316,52 @@ template <int R>
 __device__ __forceinline__ void turn_rows(const NormRopeParams& p, Steps st, uint8_t* ring, const Weights& weights, int lane) {
   if (st.begin >= st.end) return;
   const NormRopeArgs& a = p.a;
-  const int sub = lane & 7, heads = a.hq + a.hkv;
+  const int sub = lane & 7, group = lane >> 3, steps = p.q_steps + p.k_steps;
   const bool norms = a.q_weight || a.k_weight;
-  TokenWalk at, ahead;
-  at.start(4LL * st.begin + (lane >> 3), heads);
-  ahead = at;
-  int left = st.end - st.begin;  // fetches to come
+  // the lane's first value of head 4 j + group of a token, j counting its steps
+  auto row_of = [&](int token, int j) {
+    return (j < p.q_steps ? a.q + token * a.q_stride + 4 * j * kHeadDim
+                          : a.k + token * a.k_stride + 4 * (j - p.q_steps) * kHeadDim) + group * kHeadDim + 8 * sub;
+  };
+  auto live_at = [&](int j) { return j < p.q_steps ? 4 * j + group < a.hq : 4 * (j - p.q_steps) + group < a.hkv; };
+  int token = st.begin / steps, j = st.begin - token * steps;
+  // the fetches run kStages - 1 steps ahead
+  int left = st.end - st.begin, next_token = token, next_j = j;
+  const uint16_t* next = row_of(token, j);
   const uint32_t ring_u32 = smem_u32(ring) + 16 * lane;
   auto fetch = [&](int stage) {
-    const bool key = ahead.head >= a.hq;
-    const uint16_t* row = (key ? a.k + (ahead.head - a.hq) * kHeadDim : a.q + ahead.head * kHeadDim) +
-                          ahead.token * (key ? a.k_stride : a.q_stride) + 8 * sub;
-    fetch_row(ring_u32 + stage * kStageBytes, row, left > 0 && ahead.token < a.ntok);
-    ahead.skip(4, heads);
+    fetch_row(ring_u32 + stage * kStageBytes, next, left > 0 && live_at(next_j));
     --left;
+    next += 4 * kHeadDim;
+    ++next_j;
+    if (next_j == p.q_steps || next_j == steps) {
+      if (next_j == steps) {
+        next_j = 0;
+        ++next_token;
+      }
+      next = row_of(next_token, next_j);
+    }
   };
 #pragma unroll
-  for (int j = 0; j < kStages - 1; ++j) fetch(j);
+  for (int i = 0; i < kStages - 1; ++i) fetch(i);
   const GlobalScale gs = global_scale(a.gk);
   Turn turn;
   turn.on[0] = turn.on[1] = false;
-  int entered = -1;  // the token that `turn`, `slot` and `ws_row` are of
+  bool entered = false;  // `turn`, `slot`, `ws_row` and `dst` are of this token
   long long slot = -1, ws_row = -1;
+  uint16_t* dst = nullptr;  // where the queries' next step goes
   int stage = 0;
   for (int step = st.begin; step < st.end; ++step) {
     fetch(stage == 0 ? kStages - 1 : stage - 1);
-    const int tok = at.token, head = at.head;
-    const bool live = tok < a.ntok, key = head >= a.hq;
-    at.skip(4, heads);
-    if (live && tok != entered) {
-      slot = __ldg(a.slots + tok);
-      if (a.ws_rows) ws_row = __ldg(a.ws_rows + tok);
-      if constexpr (R != kNone) load_turn<R>(a, tok, sub, turn);
-      entered = tok;
+    if (!entered) {
+      slot = __ldg(a.slots + token);
+      if (a.ws_rows) ws_row = __ldg(a.ws_rows + token);
+      if constexpr (R != kNone) load_turn<R>(a, token, sub, turn);
+      dst = a.q_out + token * a.q_out_stride + (4 * j + group) * kHeadDim + 8 * sub;
+      entered = true;
     }
+    const bool key = j >= p.q_steps, live = live_at(j);
+    const int h = 4 * (j - p.q_steps) + group;
     uint32_t y[8];
     take_row(ring + stage * kStageBytes + 16 * lane, y);
     stage = stage + 1 == kStages ? 0 : stage + 1;
@@ -373,55 +372,67 @@ __device__ __forceinline__ void turn_rows(const NormRopeParams& p, Steps st, uin
     rotate<R>(f, turn, lane, a.rot);
 #pragma unroll
     for (int i = 0; i < 8; ++i) y[i] = pack_bf16x2(f[i].x, f[i].y);
-    if (live && !key) {
-      uint16_t* const dst = a.q_out + tok * a.q_out_stride + head * kHeadDim + 8 * sub;
-      *reinterpret_cast<uint4*>(dst) = make_uint4(y[0], y[1], y[2], y[3]);
-      *reinterpret_cast<uint4*>(dst + 64) = make_uint4(y[4], y[5], y[6], y[7]);
+    const long long s = slot, ws = ws_row;
+    if (++j == steps) {
+      j = 0;
+      ++token;
+      entered = false;
     }
-    if (!__any_sync(kAll, live && key)) continue;
+    if (!key) {
+      if (live) {
+        *reinterpret_cast<uint4*>(dst) = make_uint4(y[0], y[1], y[2], y[3]);
+        *reinterpret_cast<uint4*>(dst + 64) = make_uint4(y[4], y[5], y[6], y[7]);
+      }
+      dst += 4 * kHeadDim;
+      continue;
+    }
     const HalfBlocks q = quantize_halves(y, gs);
-    if (!live || !key) continue;
-    const int h = head - a.hq;
-    if (a.ws_rows) store_ws(p, false, ws_row, h, sub, y);
-    uint8_t* ph = page_head(a, slot, h);
+    if (!live) continue;
+    if (a.ws_rows) store_ws(p, false, ws, h, sub, y);
+    uint8_t* ph = page_head(a, s, h);
     if (!ph) continue;
-    const int rin = (int)(slot & (kPage - 1));
+    const int rin = (int)(s & (kPage - 1));
     uint32_t* d = reinterpret_cast<uint32_t*>(ph + kOffKData + rin * kRowBytes) + sub;
     d[0] = q.codes[0];
     d[8] = q.codes[1];
-    // lane 2 j: block j, lane 2 j + 1: block 4 + j
+    // lane 2 i: block i, lane 2 i + 1: block 4 + i
     ph[k_scale_offset(rin, (sub >> 1) + 4 * (sub & 1))] = (uint8_t)((sub & 1) ? q.sb[1] : q.sb[0]);
   }
   asm volatile("cp.async.wait_all;" ::: "memory");
 }
 
-// The warp's steps of the values: two units of a token pair and a head each, two
-// 8-lane groups to a unit.
+// The warp's steps of the values: two heads of a token pair, two 8-lane groups to
+// each.
 __device__ __forceinline__ void value_rows(const NormRopeParams& p, Steps st, uint8_t* ring, int lane) {
   if (st.begin >= st.end) return;
   const NormRopeArgs& a = p.a;
-  const int sub = lane & 7, which = (lane >> 3) & 1;
+  const int sub = lane & 7, which = (lane >> 3) & 1, group = lane >> 4;
   const GlobalScale gs = global_scale(a.gv);
-  TokenWalk at, ahead;  // `token` counts pairs
-  at.start(2LL * st.begin + (lane >> 4), a.hkv);
-  ahead = at;
-  int left = st.end - st.begin;
+  int pair = st.begin / p.v_steps, j = st.begin - pair * p.v_steps;
+  int left = st.end - st.begin, next_pair = pair, next_j = j;
   const uint32_t ring_u32 = smem_u32(ring) + 16 * lane;
   auto fetch = [&](int stage) {
-    const long long tok = 2LL * ahead.token + which;
-    fetch_row(ring_u32 + stage * kStageBytes, a.v + tok * a.v_stride + ahead.head * kHeadDim + 8 * sub,
-              left > 0 && tok < a.ntok);
-    ahead.skip(2, a.hkv);
+    const long long tok = 2LL * next_pair + which;
+    const int h = 2 * next_j + group;
+    fetch_row(ring_u32 + stage * kStageBytes, a.v + tok * a.v_stride + h * kHeadDim + 8 * sub,
+              left > 0 && tok < a.ntok && h < a.hkv);
     --left;
+    if (++next_j == p.v_steps) {
+      next_j = 0;
+      ++next_pair;
+    }
   };
 #pragma unroll
-  for (int j = 0; j < kStages - 1; ++j) fetch(j);
+  for (int i = 0; i < kStages - 1; ++i) fetch(i);
   int stage = 0;
   for (int step = st.begin; step < st.end; ++step) {
     fetch(stage == 0 ? kStages - 1 : stage - 1);
-    const int tok = 2 * at.token + which, h = at.head;
-    const bool live = tok < a.ntok;
-    at.skip(2, a.hkv);
+    const int tok = 2 * pair + which, h = 2 * j + group;
+    const bool live = tok < a.ntok && h < a.hkv;
+    if (++j == p.v_steps) {
+      j = 0;
+      ++pair;
+    }
     const long long slot = live ? __ldg(a.slots + tok) : -1;
     const long long mate = live && (tok ^ 1) < a.ntok ? __ldg(a.slots + (tok ^ 1)) : -1;
     const long long ws_row = live && a.ws_rows ? __ldg(a.ws_rows + tok) : -1;
@@ -456,15 +467,16 @@ __global__ void __launch_bounds__(kNrThreads, ctas_per_sm(R)) norm_rope_kernel(c
   __shared__ Weights weights;
   load_weights(p.a, weights);
   __syncthreads();
-  const int lane = threadIdx.x & 31;
-  uint8_t* ring = rings[threadIdx.x >> 5];
-  value_rows(p, share(p, p.v_steps, 0), ring, lane);
-  turn_rows<R>(p, share(p, p.t_steps, p.v_steps), ring, weights, lane);
+  // (broadcast: the compiler then keeps what follows from it in uniform registers)
+  const int lane = threadIdx.x & 31, warp = __shfl_sync(kAll, (int)(threadIdx.x >> 5), 0);
+  uint8_t* ring = rings[warp];
+  value_rows(p, share(p, warp, p.v_all, 0), ring, lane);
+  turn_rows<R>(p, share(p, warp, p.t_all, p.v_all), ring, weights, lane);
 }
 
 template <int R>
 cudaError_t launch(const NormRopeParams& p, int num_sms, cudaStream_t stream) {
-  const int64_t steps = (int64_t)p.t_steps + p.v_steps, fit = (int64_t)num_sms * ctas_per_sm(R);
+  const int64_t steps = (int64_t)p.t_all + p.v_all, fit = (int64_t)num_sms * ctas_per_sm(R);
   const int64_t need = (steps + kNrWarps - 1) / kNrWarps;
   norm_rope_kernel<R><<<(unsigned)(need < fit ? need : fit), kNrThreads, 0, stream>>>(p);
   return cudaGetLastError();
@@ -477,9 +489,11 @@ cudaError_t launch_norm_rope_append(const NormRopeArgs& args, float k_ws_scale, 
   NormRopeParams p;
   p.a = args;
   p.ws = ws_scales(k_ws_scale, v_ws_scale);
-  auto steps = [](int64_t n, int per) { return (int32_t)((n + per - 1) / per); };
-  p.t_steps = steps((int64_t)args.ntok * (args.hq + args.hkv), 4);
-  p.v_steps = steps((int64_t)((args.ntok + 1) / 2) * args.hkv, 2);
+  p.q_steps = (args.hq + 3) / 4;
+  p.k_steps = (args.hkv + 3) / 4;
+  p.v_steps = (args.hkv + 1) / 2;
+  p.t_all = args.ntok * (p.q_steps + p.k_steps);  // (below 2^31: ntok times the more of hq and hkv is)
+  p.v_all = (args.ntok + 1) / 2 * p.v_steps;
   switch (args.rot == 0 ? kNone : args.interleaved ? kInterleaved : args.rot == kHeadDim ? kWhole
           : args.rot == 96 ? kThreeQuarters : kFirst) {
     case kNone: return launch<kNone>(p, num_sms, stream);
