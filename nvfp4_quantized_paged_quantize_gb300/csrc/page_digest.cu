@@ -18,6 +18,7 @@ namespace {
 
 constexpr int kDgThreads = 256;
 constexpr int kDgWarps = kDgThreads / 32;
+constexpr int kDigestCtasPerSm = 4, kScoreCtasPerSm = 2;  // the grids are what fits at once
 constexpr uint32_t kAll = 0xFFFFFFFFu;
 
 constexpr int kOffScale = 2 * kHeadDim;  // behind hi and lo
@@ -121,6 +122,15 @@ __device__ __forceinline__ uint32_t hmin2(uint32_t a, uint32_t b) {
   r.h = __hmin2(x.h, y.h);
   return r.u;
 }
+// a * (the low or the high half of s, in both halves): the broadcast is left to the
+// multiply's operand selection
+template <bool kHi>
+__device__ __forceinline__ uint32_t hmul2_bcast(uint32_t a, uint32_t s) {
+  H2 x, y, r;
+  x.u = a, y.u = s;
+  r.h = __hmul2(x.h, kHi ? __high2half2(y.h) : __low2half2(y.h));
+  return r.u;
+}
 __device__ __forceinline__ uint32_t hneg2(uint32_t a) { return a ^ 0x80008000u; }
 __device__ __forceinline__ uint32_t hfma2(uint32_t a, uint32_t b, uint32_t c) {
   uint32_t r;
@@ -128,31 +138,24 @@ __device__ __forceinline__ uint32_t hfma2(uint32_t a, uint32_t b, uint32_t c) {
   return r;
 }
 
-// A lane's share of a page-head's keys: dimensions 8 dg .. 8 dg + 7 of every other
-// row, and those rows' scale bytes.
-struct KeyRows {
-  uint32_t k[8];
-  uint32_t scale[8];
-};
+// A warp's ring: page-heads' keys and scales as stored, 1152 bytes a stage.
+constexpr int kDgStages = 3;
+constexpr int kDgStageBytes = kPageDataBytes + kPageScaleBytes;
+static_assert(kOffKScale == kPageDataBytes, "the keys' scales follow the keys");
 
-// Rows past the sequence's end read row 0 instead, which changes no bound.
-__device__ __forceinline__ void load_keys(const uint8_t* ph, int valid, int dg, int rh, KeyRows& x) {
-  if (valid >= kPage) {
-    const uint8_t* const k = ph + kOffKData + rh * kRowBytes + 4 * dg;
-    const uint8_t* const s = ph + kOffKScale + rh * kRowScales + (dg >> 1);
-#pragma unroll
-    for (int r = 0; r < 8; ++r) {
-      x.k[r] = __ldg(reinterpret_cast<const uint32_t*>(k + 2 * r * kRowBytes));
-      x.scale[r] = __ldg(s + 2 * r * kRowScales);
-    }
-  } else {
-#pragma unroll
-    for (int r = 0; r < 8; ++r) {
-      const int row = 2 * r + rh < valid ? 2 * r + rh : 0;
-      x.k[r] = __ldg(reinterpret_cast<const uint32_t*>(ph + kOffKData + row * kRowBytes + 4 * dg));
-      x.scale[r] = __ldg(ph + k_scale_offset(row, dg >> 1));
-    }
+// Starts the copy of a page-head's keys and scales (nothing for a null one) into a stage.
+__device__ __forceinline__ void fetch_keys(uint32_t stage, const uint8_t* ph, int lane) {
+  if (ph != nullptr) {
+    asm volatile(
+        "{\n .reg .pred p;\n"
+        " setp.lt.u32 p, %2, 8;\n"
+        " cp.async.cg.shared.global [%0], [%1], 16;\n"
+        " cp.async.cg.shared.global [%0+512], [%1+512], 16;\n"
+        " @p cp.async.cg.shared.global [%0+1024], [%1+1024], 16;\n"
+        "}\n" ::"r"(stage + 16 * lane), "l"(ph + 16 * lane), "r"((uint32_t)lane)
+        : "memory");
   }
+  asm volatile("cp.async.commit_group;" ::: "memory");
 }
 
 // v (below 256 in size) rounded up to an E4M3 value: to a whole number of its
@@ -167,14 +170,24 @@ __device__ __forceinline__ float up_to_step(float v) {
 // significant bits and is 0 or at least 2^-10 in size: exact in f16.  The lanes of
 // the odd rows hold all values negated (their scales' signs are flipped), so that
 // after one exchange the even ones hold hi, the odd ones -lo, and both round up.
-__device__ __forceinline__ void write_digest(const KeyRows& in, uint8_t* d, int lane) {
-  const int rh = lane >> 4;
+// A lane has dimensions 8 dg .. 8 dg + 7 of every other row; kFull: the page is (else
+// rows past its `valid` ones read row 0 instead, which changes no bound).
+template <bool kFull>
+__device__ __forceinline__ void write_digest(const uint8_t* keys, int valid, uint8_t* d, int lane) {
+  const int dg = lane & 15, rh = lane >> 4;
+  const uint8_t* const data = keys + 4 * dg;
+  const uint8_t* const scales = keys + kOffKScale + (dg >> 1);
+  auto row_at = [&](int r) { return kFull || 2 * r + rh < valid ? 2 * r + rh : 0; };
   uint32_t hi[4], lo[4];
 #pragma unroll
   for (int r = 0; r < 8; ++r) {
-    const uint32_t sc = e4m3x2_to_f16x2(in.scale[r] * 0x0101u + (rh ? 0x8080u : 0u));
-    const uint32_t v[4] = {hmul2(e2m1x2_to_f16x2<0>(in.k[r]), sc), hmul2(e2m1x2_to_f16x2<1>(in.k[r]), sc),
-                           hmul2(e2m1x2_to_f16x2<2>(in.k[r]), sc), hmul2(e2m1x2_to_f16x2<3>(in.k[r]), sc)};
+    // the scales of rows r and r + 1 together
+    const uint32_t sc = e4m3x2_to_f16x2(scales[row_at(r & 6) * kRowScales] +
+                                        scales[row_at((r & 6) + 1) * kRowScales] * 0x100u + (rh ? 0x8080u : 0u));
+    const uint32_t k = *reinterpret_cast<const uint32_t*>(data + row_at(r) * kRowBytes);
+    auto scaled = [&](uint32_t v) { return (r & 1) ? hmul2_bcast<true>(v, sc) : hmul2_bcast<false>(v, sc); };
+    const uint32_t v[4] = {scaled(e2m1x2_to_f16x2<0>(k)), scaled(e2m1x2_to_f16x2<1>(k)),
+                           scaled(e2m1x2_to_f16x2<2>(k)), scaled(e2m1x2_to_f16x2<3>(k))};
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       hi[j] = r == 0 ? v[j] : hmax2(hi[j], v[j]);
@@ -193,20 +206,22 @@ __device__ __forceinline__ void write_digest(const KeyRows& in, uint8_t* d, int 
   const int first = min(down, 15), second = down - first;
   const uint32_t f1 = (uint32_t)(15 + first) << 10, f2 = (uint32_t)(15 + second) << 10;
   uint32_t code[4];
-  bool small = false;
+  uint32_t small = 0;
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     const uint32_t t = hfma2(hmul2(x[j], f1 | f1 << 16), f2 | f2 << 16, 0u);  // + 0: no negative zeros
     H2 u, lim;
-    u.u = t & 0x7FFF7FFFu;
+    u.u = t;
     lim.u = 0x24002400u;  // 2^-6
-    small |= (__hlt2_mask(u.h, lim.h) & u.u) != 0;  // 0 < |t| < 2^-6: steps that are coarser than the binade's
+    small |= __hlt2_mask(__habs2(u.h), lim.h) & t;  // 0 < |t| < 2^-6: steps that are coarser than the binade's
     // E4M3 drops seven of f16's ten mantissa bits; a negative value's magnitude is cut off
-    const uint32_t up = (t + 0x007F007Fu - (t >> 15 & 0x00010001u) * 0x7Fu) & 0xFF80FF80u;
+    uint32_t negative;  // each half all ones where its sign is set (prmt copying bytes 1 and 3's signs)
+    asm("prmt.b32 %0, %1, 0, 0xBB99;" : "=r"(negative) : "r"(t));
+    const uint32_t up = (t + (0x007F007Fu & ~negative)) & 0xFF80FF80u;
     code[j] = e4m3x2_from_f16x2(hfma2(up, rh ? 0xBC00BC00u : 0x3C003C00u, 0u));  // times the lane's sign
     x[j] = t;
   }
-  if (__any_sync(kAll, small)) {
+  if (__any_sync(kAll, small != 0)) {
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       H2 u;
@@ -220,10 +235,11 @@ __device__ __forceinline__ void write_digest(const KeyRows& in, uint8_t* d, int 
     *reinterpret_cast<uint4*>(d + kOffScale) = make_uint4((uint32_t)(127 - down) << 23, 0u, 0u, 0u);  // 2^e; 1 without any
 }
 
-// A warp takes one page-head at a time, its keys loaded while the one before is
-// bounded.  1152 bytes in (whole lines) and 272 out per page-head.
-__global__ void __launch_bounds__(kDgThreads) digest_kernel(const DigestArgs p) {
+// A warp takes one page-head at a time; the keys of the next kDgStages - 1 are on
+// their way meanwhile.  1152 bytes in (whole lines) and 272 out per page-head.
+__global__ void __launch_bounds__(kDgThreads, kDigestCtasPerSm) digest_kernel(const DigestArgs p) {
   __shared__ ShareShared s;
+  __shared__ __align__(128) uint8_t rings[kDgWarps][kDgStages * kDgStageBytes];
   const int lane = threadIdx.x & 31;
   auto from_page = [&](int b) { return p.first_tokens ? max(__ldg(p.first_tokens + b), 0) / kPage : 0; };
   Share w = split(s, p.batch, [&](int b) {
@@ -231,41 +247,66 @@ __global__ void __launch_bounds__(kDgThreads) digest_kernel(const DigestArgs p) 
     return max((L + kPage - 1) / kPage - from_page(b), 0) * p.hkv;
   });
   if (w.begin >= w.end) return;
-  // the next item to load: head h of page `page` of sequence b, of `end` pages
+  // the next item to fetch: head h of page `page` of sequence b, which has `end` pages
   int b = w.b, L = seq_tokens(p, b, false), page = from_page(b), end = (L + kPage - 1) / kPage;
   const int i = w.begin - w.first;
   page += i / p.hkv;
-  int h = i % p.hkv;
-  const int dg = lane & 15, rh = lane >> 4;  // dimensions 8 dg .. 8 dg + 7 of rows 2 r + rh
-  // loads the next item's keys; returns its row of the pool, or -1
-  auto load = [&](KeyRows& x) -> int {
+  int h = i % p.hkv, id = -1;  // id: of `page`, read at its first head
+  bool known = false;
+  int fetched = w.begin;
+  const uint8_t* const ring = rings[threadIdx.x >> 5];
+  const uint32_t ring_u32 = smem_u32(ring);
+  // starts the next item's copy; returns its row of the pool (-1 for none) and its valid tokens
+  auto fetch = [&](int stage) -> int2 {
+    if (fetched == w.end) {
+      fetch_keys(0, nullptr, lane);
+      return make_int2(-1, 0);
+    }
+    ++fetched;
     while (page >= end) {  // the next sequence that has any
       ++b;
       L = seq_tokens(p, b, false);
       page = from_page(b);
       end = (L + kPage - 1) / kPage;
     }
-    int id = __ldg(p.page_table + (long long)b * p.max_pages + page);
-    const bool valid = id >= 0 && id < p.num_pages;
-    if (!valid && lane == 0) flag_error(p.status, NVFP4KV_DEVERR_PAGE);
-    const int row = (valid ? id : 0) * p.hkv + h;
-    load_keys(p.pages + (long long)row * kPageHeadBytes, L - page * kPage, dg, rh, x);
+    if (!known) {
+      id = __ldg(p.page_table + (long long)b * p.max_pages + page);
+      if (id < 0 || id >= p.num_pages) {
+        if (lane == 0) flag_error(p.status, NVFP4KV_DEVERR_PAGE);
+        id = -1;
+      }
+      known = true;
+    }
+    const int row = id < 0 ? -1 : id * p.hkv + h, valid = min(L - page * kPage, kPage);
+    fetch_keys(ring_u32 + stage * kDgStageBytes, row < 0 ? nullptr : p.pages + (long long)row * kPageHeadBytes, lane);
     if (++h == p.hkv) {
       h = 0;
       ++page;
+      known = false;
     }
-    return valid ? row : -1;
+    return make_int2(row, valid);
   };
-  KeyRows now;
-  int row = load(now);
+  static_assert(kDgStages == 3, "the items under way have names");
+  int2 now = fetch(0), next = fetch(1);
+  int stage = 0;
   for (int at = w.begin; at < w.end; ++at) {
-    KeyRows next = now;
-    int next_row = -1;
-    if (at + 1 < w.end) next_row = load(next);
-    if (row >= 0) write_digest(now, p.digest + (long long)row * kDigestBytes, lane);
+    const int2 later = fetch(stage == 0 ? 2 : stage - 1);
+    asm volatile("cp.async.wait_group 2;" ::: "memory");
+    __syncwarp();
+    if (now.x >= 0) {
+      uint8_t* const d = p.digest + (long long)now.x * kDigestBytes;
+      const uint8_t* const keys = ring + stage * kDgStageBytes;
+      if (now.y == kPage)
+        write_digest<true>(keys, kPage, d, lane);
+      else
+        write_digest<false>(keys, now.y, d, lane);
+    }
+    __syncwarp();  // the stage may be filled again
+    stage = stage == 2 ? 0 : stage + 1;
     now = next;
-    row = next_row;
+    next = later;
   }
+  asm volatile("cp.async.wait_all;" ::: "memory");
 }
 
 // ---------------------------------------------------------------------------
@@ -340,7 +381,7 @@ __device__ __forceinline__ void load_queries(const ScoreArgs& p, int pair, int l
 // A warp takes tiles of 16 consecutive pages of one (sequence, KV head) pair; the
 // heads are an MMA's eight columns.  Lane (g, t) reads 16-byte pieces t and 4 + t
 // of hi and of lo of pages g and g + 8: whole sectors, each byte once.
-__global__ void __launch_bounds__(kDgThreads) scores_kernel(const ScoreArgs p) {
+__global__ void __launch_bounds__(kDgThreads, kScoreCtasPerSm) scores_kernel(const ScoreArgs p) {
   __shared__ ShareShared s;
   const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const DigestArgs& d = p.d;
@@ -430,14 +471,14 @@ unsigned blocks_for(int64_t items_most, int num_sms, int per_sm) {
 }  // namespace
 
 cudaError_t launch_page_digest(const DigestArgs& args, int num_sms, cudaStream_t stream) {
-  const unsigned blocks = blocks_for((int64_t)args.batch * args.max_pages * args.hkv, num_sms, 6);
+  const unsigned blocks = blocks_for((int64_t)args.batch * args.max_pages * args.hkv, num_sms, kDigestCtasPerSm);
   digest_kernel<<<blocks, kDgThreads, 0, stream>>>(args);
   return cudaGetLastError();
 }
 
 cudaError_t launch_page_scores(const ScoreArgs& args, int num_sms, cudaStream_t stream) {
   const int64_t tiles = ((int64_t)args.d.max_pages + kTile - 1) / kTile;
-  const unsigned blocks = blocks_for(args.d.batch * tiles * args.d.hkv, num_sms, 2);
+  const unsigned blocks = blocks_for(args.d.batch * tiles * args.d.hkv, num_sms, kScoreCtasPerSm);
   scores_kernel<<<blocks, kDgThreads, 0, stream>>>(args);
   return cudaGetLastError();
 }
