@@ -9,7 +9,8 @@
 // keeps hi and lo in E4M3, rounded outwards so that the bound holds, times one
 // power of two per page-head that puts the largest into [128, 256).
 //
-// Both kernels cut the flattened list of their items evenly over all warps.
+// Both kernels cut the flattened list of their items evenly, over all warps (digests)
+// or blocks (scores).
 #include "nvfp4kv_device.cuh"
 #include "nvfp4kv_launch.h"
 
@@ -36,7 +37,7 @@ __device__ __forceinline__ int seq_tokens(const DigestArgs& p, int b, bool flag)
   return L;
 }
 
-// Where a warp's share [begin, end) of the flattened items starts: in sequence b,
+// Where a share [begin, end) of the flattened items starts: in sequence b,
 // whose first item is `first`.
 struct Share {
   int begin, end;
@@ -45,29 +46,32 @@ struct Share {
 
 struct ShareShared {
   int sums[kDgWarps];
+  int begin[kDgWarps + 1];  // the block's shares
   int b[kDgWarps], first[kDgWarps];
 };
 
-// Items of sequence b: count(b).  Every thread of the block calls this.
+// The block's share number `mine`, of `shares`; items of sequence b: count(b).  Every
+// thread of the block calls this.
 template <class Count>
-__device__ __forceinline__ Share split(ShareShared& s, int batch, Count count) {
+__device__ __forceinline__ Share split(ShareShared& s, int batch, int shares, int mine, Count count) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const long long warps = (long long)gridDim.x * kDgWarps, w0 = (long long)blockIdx.x * kDgWarps;
   // one pass over the sequences for the total, and (again, unless they were few
-  // enough to stay in a register) one to find the warps' starts
-  int mine = 0, local = 0;
-  for (int b = tid; b < batch; b += kDgThreads) local += mine = count(b);
+  // enough to stay in a register) one to find the shares' starts
+  int kept = 0, local = 0;
+  for (int b = tid; b < batch; b += kDgThreads) local += kept = count(b);
   int sum = __reduce_add_sync(kAll, local);
   if (lane == 0) s.sums[warp] = sum;
   __syncthreads();
   int total = 0;
 #pragma unroll
   for (int w = 0; w < kDgWarps; ++w) total += s.sums[w];
+  if (tid <= shares)
+    s.begin[tid] = (int)(total * ((long long)blockIdx.x * shares + tid) / ((long long)gridDim.x * shares));
   __syncthreads();
   int carry = 0;
   for (int base = 0; base < batch; base += kDgThreads) {
     const int b = base + tid;
-    const int n = batch <= kDgThreads ? mine : b < batch ? count(b) : 0;
+    const int n = batch <= kDgThreads ? kept : b < batch ? count(b) : 0;
     int incl = n;
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
@@ -83,8 +87,8 @@ __device__ __forceinline__ Share split(ShareShared& s, int batch, Count count) {
       all += s.sums[w];
     }
     if (n > 0) {
-      for (int w = 0; w < kDgWarps; ++w) {
-        const int at = (int)(total * (w0 + w) / warps);
+      for (int w = 0; w < shares; ++w) {
+        const int at = s.begin[w];
         if (at >= first && at - first < n) {
           s.b[w] = b;
           s.first[w] = first;
@@ -95,10 +99,10 @@ __device__ __forceinline__ Share split(ShareShared& s, int batch, Count count) {
     __syncthreads();
   }
   Share r;
-  r.begin = (int)(total * (w0 + warp) / warps);
-  r.end = (int)(total * (w0 + warp + 1) / warps);
-  r.b = s.b[warp];
-  r.first = s.first[warp];
+  r.begin = s.begin[mine];
+  r.end = s.begin[mine + 1];
+  r.b = s.b[mine];
+  r.first = s.first[mine];
   return r;
 }
 
@@ -242,7 +246,7 @@ __global__ void __launch_bounds__(kDgThreads, kDigestCtasPerSm) digest_kernel(co
   __shared__ __align__(128) uint8_t rings[kDgWarps][kDgStages * kDgStageBytes];
   const int lane = threadIdx.x & 31;
   auto from_page = [&](int b) { return p.first_tokens ? max(__ldg(p.first_tokens + b), 0) / kPage : 0; };
-  Share w = split(s, p.batch, [&](int b) {
+  const Share w = split(s, p.batch, kDgWarps, (int)(threadIdx.x >> 5), [&](int b) {
     const int L = seq_tokens(p, b, blockIdx.x == 0);
     return max((L + kPage - 1) / kPage - from_page(b), 0) * p.hkv;
   });
@@ -378,13 +382,49 @@ __device__ __forceinline__ void load_queries(const ScoreArgs& p, int pair, int l
   q.c1 = __shfl_sync(kAll, c, 8 * t + 4);
 }
 
-// A warp takes tiles of 16 consecutive pages of one (sequence, KV head) pair; the
-// heads are an MMA's eight columns.  Lane (g, t) reads 16-byte pieces t and 4 + t
-// of hi and of lo of pages g and g + 8: whole sectors, each byte once.
+// How a block goes through a sequence's pages: `together` KV heads at once, one per
+// warp, of `streams` tiles of 16 consecutive pages, in `rounds` over all heads.  A
+// page's digests of those heads are one run of memory, copied as such to every
+// `stride` bytes of a stage (64 more than a multiple of 128: the 16-byte reads of eight
+// lanes, two pages' 64 bytes each, then meet no bank twice).
+struct ScorePlan {
+  int together, streams, rounds, pages, stride;
+};
+
+__host__ __device__ inline ScorePlan score_plan(int hkv) {
+  ScorePlan k;
+  k.together = hkv < kDgWarps ? hkv : kDgWarps;
+  k.streams = kDgWarps / k.together;
+  k.rounds = (hkv + k.together - 1) / k.together;
+  k.pages = kTile * k.streams;
+  k.stride = (k.together * kDigestBytes + 63) / 128 * 128 + 64;
+  return k;
+}
+
+constexpr int kScStages = 2;
+// the most that score_plan asks for: one head, 128 pages of 320 bytes
+constexpr int kScStageBytes = 128 * 320;
+
+// A block takes items of 16 to 128 consecutive pages of one sequence and up to eight
+// KV heads; a warp one of the heads and 16 of the pages, the rows of an MMA whose
+// eight columns are the query heads.  Lane (g, t) reads 16-byte pieces t and 4 + t of
+// hi and of lo of pages g and g + 8.  One copy per page (2176 bytes with eight heads;
+// 272-byte rows fetched one by one were slower, however many at a time), two items
+// ahead, the page ids read one item before that.
 __global__ void __launch_bounds__(kDgThreads, kScoreCtasPerSm) scores_kernel(const ScoreArgs p) {
+  extern __shared__ __align__(128) uint8_t stages[];
   __shared__ ShareShared s;
-  const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  __shared__ __align__(8) uint64_t bars[kScStages];
+  __shared__ uint32_t s_there[kScStages][4];  // a stage's pages that are there, bit by bit
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
   const DigestArgs& d = p.d;
+  const ScorePlan k = score_plan(d.hkv);
+  const uint32_t bar = smem_u32(bars), st0 = smem_u32(stages);
+  const int copiers = (k.pages + 31) / 32;  // warps that start copies, one page per thread
+  if (tid == 0) {
+    for (int i = 0; i < kScStages; ++i) mbar_init(bar + 8 * i, copiers);
+    fence_mbar_init();
+  }
   auto pages_of = [&](int b, bool flag) {
     int n = (seq_tokens(d, b, flag) + kPage - 1) / kPage;
     if (n > p.score_stride) {
@@ -393,93 +433,147 @@ __global__ void __launch_bounds__(kDgThreads, kScoreCtasPerSm) scores_kernel(con
     }
     return n;
   };
-  Share w = split(s, d.batch, [&](int b) { return (pages_of(b, blockIdx.x == 0) + kTile - 1) / kTile * d.hkv; });
+  auto steps_of = [&](int pages) { return (pages + k.pages - 1) / k.pages; };
+  const Share w = split(s, d.batch, 1, 0, [&](int b) { return steps_of(pages_of(b, blockIdx.x == 0)) * k.rounds; });
   if (w.begin >= w.end) return;
-  int b = w.b, i = w.begin - w.first;
-  int pages = pages_of(b, false), tiles = (pages + kTile - 1) / kTile;
-  int h = i / tiles, tile = i - h * tiles;
+  // a walk over the share's items: step `step` of `steps` of sequence b, heads from together * round on
+  struct Walk {
+    int b, round, step, steps, pages;
+  };
+  auto advance = [&](Walk& x) {
+    if (++x.step < x.steps) return;
+    x.step = 0;
+    if (++x.round < k.rounds) return;
+    x.round = 0;
+    do {  // the next sequence that has any; behind the last one there is none to look at
+      if (++x.b >= d.batch) return;
+      x.pages = pages_of(x.b, false);
+    } while (x.pages == 0);
+    x.steps = steps_of(x.pages);
+  };
+  Walk at;
+  at.b = w.b;
+  at.pages = pages_of(w.b, false);
+  at.steps = steps_of(at.pages);
+  at.round = (w.begin - w.first) / at.steps;
+  at.step = w.begin - w.first - at.round * at.steps;
+  Walk ahead = at;
+  int to_read = w.end - w.begin;  // items whose ids have not been read yet
+  // thread = page of the item: its id (-1: none), and the first of its heads
+  struct Ids {
+    int id, head;
+    bool page, item;
+  };
+  auto read_ids = [&]() {
+    Ids x = {-1, 0, false, false};
+    if (to_read > 0) {
+      const int page = ahead.step * k.pages + tid;
+      x.item = true;
+      x.head = ahead.round * k.together;
+      x.page = tid < k.pages && page < ahead.pages;
+      if (x.page) x.id = __ldg(d.page_table + (long long)ahead.b * d.max_pages + page);
+      --to_read;
+      advance(ahead);
+    }
+    return x;
+  };
+  auto copy = [&](int stage, const Ids& x) {
+    if (warp >= copiers || !x.item) return;
+    const bool there = x.page && x.id >= 0 && x.id < d.num_pages;
+    if (x.page && !there) flag_error(d.status, NVFP4KV_DEVERR_PAGE);
+    const uint32_t bytes = (uint32_t)(min(k.together, d.hkv - x.head) * kDigestBytes);
+    const uint32_t mask = __ballot_sync(kAll, there);
+    if (lane == 0) {
+      s_there[stage][warp] = mask;
+      asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar + 8 * stage), "r"(bytes * __popc(mask))
+                   : "memory");
+    }
+    __syncwarp();
+    if (there) {
+      const uint8_t* src = d.digest + ((long long)x.id * d.hkv + x.head) * kDigestBytes;
+      asm volatile("cp.async.bulk.shared::cta.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                       st0 + stage * kScStageBytes + tid * k.stride),
+                   "l"(src), "r"(bytes), "r"(bar + 8 * stage)
+                   : "memory");
+    }
+  };
+  static_assert(kScStages == 2, "the items under way have names");
+  const int stream = warp / k.together, mine = warp - stream * k.together;
+  const Ids first = read_ids(), second = read_ids();
+  copy(0, first);
+  copy(1, second);
+  Ids third = read_ids();
   Queries q;
-  int loaded = -1;
-  for (int at = w.begin; at < w.end; ++at) {
-    while (h >= d.hkv) {  // the next sequence that has any
-      ++b;
-      pages = pages_of(b, false);
-      tiles = (pages + kTile - 1) / kTile;
-      h = tiles > 0 ? 0 : d.hkv;
-    }
-    const int pair = b * d.hkv + h;
-    // lanes 0-15: the tile's page ids
-    const int page = tile * kTile + (lane & 15);
-    int id = -1;
-    if (page < pages) {
-      id = __ldg(d.page_table + (long long)b * d.max_pages + page);
-      if (id < 0 || id >= d.num_pages) {
-        flag_error(d.status, NVFP4KV_DEVERR_PAGE);
-        id = -1;
-      }
-    }
-    const int id0 = __shfl_sync(kAll, id, g), id1 = __shfl_sync(kAll, id, g + 8);
-    const uint8_t* r0 = d.digest + ((long long)max(id0, 0) * d.hkv + h) * kDigestBytes;
-    const uint8_t* r1 = d.digest + ((long long)max(id1, 0) * d.hkv + h) * kDigestBytes;
-    uint4 x[2][4];  // pages g, g + 8: hi pieces t, 4 + t, lo pieces t, 4 + t
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      x[0][j] = __ldg(reinterpret_cast<const uint4*>(r0) + 4 * j + t);
-      x[1][j] = __ldg(reinterpret_cast<const uint4*>(r1) + 4 * j + t);
-    }
-    const float u0 = __ldg(reinterpret_cast<const float*>(r0 + kOffScale)), u1 = __ldg(reinterpret_cast<const float*>(r1 + kOffScale));
-    if (pair != loaded) {
+  int loaded = -1, n = 0;
+  for (int i = w.begin; i < w.end; ++i, ++n) {
+    const int stage = n & 1, head = at.round * k.together + mine, pair = at.b * d.hkv + head;
+    const int page0 = at.step * k.pages + stream * kTile;  // the warp's first page
+    const bool live = stream < k.streams && head < d.hkv && page0 < at.pages;
+    if (live && pair != loaded) {
       load_queries(p, pair, lane, q);
       loaded = pair;
     }
-    float c[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    // (a wait that gives up: the outputs are not valid, every access stays in bounds)
+    if (!mbar_wait(bar + 8 * stage, (uint32_t)(n >> 1) & 1u) && lane == 0) flag_error(d.status, kDevErrTimeout);
+    if (live) {
+      const uint32_t there = s_there[stage][stream >> 1] >> (kTile * (stream & 1));
+      const uint8_t* const rows = stages + stage * kScStageBytes + stream * kTile * k.stride + mine * kDigestBytes;
+      const uint8_t* const r0 = rows + g * k.stride + 16 * t;
+      const uint8_t* const r1 = r0 + 8 * k.stride;
+      float c[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const uint32_t a[4] = {x[0][j].x, x[0][j].y, x[0][j].z, x[0][j].w};
-      const uint32_t e[4] = {x[1][j].x, x[1][j].y, x[1][j].z, x[1][j].w};
+      for (int j = 0; j < 4; ++j) {
+        const uint4 x0 = *reinterpret_cast<const uint4*>(r0 + 64 * j), x1 = *reinterpret_cast<const uint4*>(r1 + 64 * j);
+        const uint32_t a[4] = {x0.x, x0.y, x0.z, x0.w}, e[4] = {x1.x, x1.y, x1.z, x1.w};
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const uint32_t* f = (j & 2) ? q.neg[4 * (j & 1) + k] : q.pos[4 * (j & 1) + k];
-        mma16816(c, e4m3x2_to_f16x2(a[k] & 0xFFFFu), e4m3x2_to_f16x2(e[k] & 0xFFFFu), e4m3x2_to_f16x2(a[k] >> 16),
-                 e4m3x2_to_f16x2(e[k] >> 16), f[0], f[1]);
+        for (int m = 0; m < 4; ++m) {
+          const uint32_t* f = (j & 2) ? q.neg[4 * (j & 1) + m] : q.pos[4 * (j & 1) + m];
+          mma16816(c, e4m3x2_to_f16x2(a[m] & 0xFFFFu), e4m3x2_to_f16x2(e[m] & 0xFFFFu), e4m3x2_to_f16x2(a[m] >> 16),
+                   e4m3x2_to_f16x2(e[m] >> 16), f[0], f[1]);
+        }
+      }
+      // the largest over the group's heads, 2 t and 2 t + 1 in this lane
+      const float c00 = 2 * t < p.group ? c[0] * q.c0 : -INFINITY, c01 = 2 * t + 1 < p.group ? c[1] * q.c1 : -INFINITY;
+      const float c10 = 2 * t < p.group ? c[2] * q.c0 : -INFINITY, c11 = 2 * t + 1 < p.group ? c[3] * q.c1 : -INFINITY;
+      float m0 = fmaxf(c00, c01), m1 = fmaxf(c10, c11);
+#pragma unroll
+      for (int off = 1; off < 4; off <<= 1) {
+        m0 = fmaxf(m0, __shfl_xor_sync(kAll, m0, off));
+        m1 = fmaxf(m1, __shfl_xor_sync(kAll, m1, off));
+      }
+      // lanes t = 0 and 1 write pages g and g + 8
+      const int r = g + 8 * t, page = page0 + r;
+      if (t < 2 && page < at.pages) {
+        const float unit = *reinterpret_cast<const float*>(rows + r * k.stride + kOffScale);
+        p.scores[(long long)pair * p.score_stride + page] = (there >> r & 1) ? (t ? m1 : m0) * unit : -INFINITY;
       }
     }
-    // the largest over the group's heads, 2 t and 2 t + 1 in this lane
-    const float c00 = 2 * t < p.group ? c[0] * q.c0 : -INFINITY, c01 = 2 * t + 1 < p.group ? c[1] * q.c1 : -INFINITY;
-    const float c10 = 2 * t < p.group ? c[2] * q.c0 : -INFINITY, c11 = 2 * t + 1 < p.group ? c[3] * q.c1 : -INFINITY;
-    float m0 = fmaxf(c00, c01), m1 = fmaxf(c10, c11);
-#pragma unroll
-    for (int off = 1; off < 4; off <<= 1) {
-      m0 = fmaxf(m0, __shfl_xor_sync(kAll, m0, off));
-      m1 = fmaxf(m1, __shfl_xor_sync(kAll, m1, off));
-    }
-    float* out = p.scores + (long long)pair * p.score_stride + tile * kTile;
-    if (t == 0 && tile * kTile + g < pages) out[g] = id0 < 0 ? -INFINITY : m0 * u0;
-    if (t == 1 && tile * kTile + g + 8 < pages) out[g + 8] = id1 < 0 ? -INFINITY : m1 * u1;
-    if (++tile == tiles) {
-      tile = 0;
-      ++h;
-    }
+    advance(at);
+    __syncthreads();  // the stage may be filled again
+    copy(stage, third);
+    third = read_ids();
   }
-}
-
-unsigned blocks_for(int64_t items_most, int num_sms, int per_sm) {
-  const int64_t need = (items_most + kDgWarps - 1) / kDgWarps, fit = (int64_t)num_sms * per_sm;
-  return (unsigned)(need < 1 ? 1 : need < fit ? need : fit);
 }
 
 }  // namespace
 
 cudaError_t launch_page_digest(const DigestArgs& args, int num_sms, cudaStream_t stream) {
-  const unsigned blocks = blocks_for((int64_t)args.batch * args.max_pages * args.hkv, num_sms, kDigestCtasPerSm);
-  digest_kernel<<<blocks, kDgThreads, 0, stream>>>(args);
+  const int64_t need = ((int64_t)args.batch * args.max_pages * args.hkv + kDgWarps - 1) / kDgWarps;
+  const int64_t fit = (int64_t)num_sms * kDigestCtasPerSm;
+  digest_kernel<<<(unsigned)(need < fit ? need : fit), kDgThreads, 0, stream>>>(args);
   return cudaGetLastError();
 }
 
 cudaError_t launch_page_scores(const ScoreArgs& args, int num_sms, cudaStream_t stream) {
-  const int64_t tiles = ((int64_t)args.d.max_pages + kTile - 1) / kTile;
-  const unsigned blocks = blocks_for(args.d.batch * tiles * args.d.hkv, num_sms, kScoreCtasPerSm);
-  scores_kernel<<<blocks, kDgThreads, 0, stream>>>(args);
+  static PerDeviceOnce attr_once;
+  const cudaError_t e = attr_once.run([] {
+    return cudaFuncSetAttribute(scores_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kScStages * kScStageBytes);
+  });
+  if (e != cudaSuccess) return e;
+  const ScorePlan k = score_plan(args.d.hkv);
+  const int64_t items = args.d.batch * (((int64_t)args.d.max_pages + k.pages - 1) / k.pages) * k.rounds;
+  const int64_t fit = (int64_t)num_sms * kScoreCtasPerSm;
+  scores_kernel<<<(unsigned)(items < fit ? items : fit), kDgThreads, kScStages * kScStageBytes, stream>>>(args);
   return cudaGetLastError();
 }
 
