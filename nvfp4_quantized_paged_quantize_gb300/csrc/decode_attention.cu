@@ -52,7 +52,6 @@
 // f16, and the factor is folded back into the score scale.
 #include <cfloat>
 #include <cstdint>
-#include <cstdlib>
 
 #include "nvfp4kv_device.cuh"
 #include "nvfp4kv_launch.h"
@@ -1577,18 +1576,29 @@ __global__ void __launch_bounds__(kCombineMaxWarps * 32) combine_kernel(const De
   }
 }
 
-// The decode over listed pages, one cluster of `splits` CTAs per (sequence, KV head)
-// pair: each CTA takes an equal part of the list, each warp a quarter of that, with
-// the ring and the phases of decode_kernel; the warps' results meet in shared memory
-// and the CTAs' in that of the cluster (each CTA finishes every splits-th head), so
-// that there are no records in global memory and no second kernel.
+// The decode over listed pages where one wave of CTAs holds it: a cluster of `splits`
+// CTAs per (sequence, KV head) pair, each CTA an equal part of the pair's list, each
+// warp an eighth of that, with the ring and the phases of decode_kernel.  The warps'
+// results meet in shared memory and the CTAs' in that of the cluster (each CTA
+// finishes every splits-th head), so there are no records in global memory, no second
+// kernel and no scan over the batch: what is left of them is 7 us, beside some 11 of
+// decode_kernel and its combine.  Captured, 64 / 8 heads, here and there: 32 x 8193
+// tokens, 8 pages a head 7.5 and 11.3 us, 64 13.9 and 17.0, 256 34.4 and 36.3;
+// 4 x 131073 tokens, 1024 pages 22.6 and 23.4, 4096 61 and 59.  Past one wave the
+// even cut wins: 96 sequences, 64 pages 37.8 and 32.9.
+// (Cutting several pairs of a cluster evenly over its warps: 23.3 us for the second
+// of these; the merge of cut pairs is what cost.  4 warps and three CTAs an SM: 14.8.)
+constexpr int kSW = 8, kSelCtas = 2;  // warps of a CTA, CTAs of an SM
+constexpr int kSelRingBytes = kSW * kStages * kStageBytes, kSelSmemBytes = kSelRingBytes + kSW * kStages * 8;
 constexpr int kOffCtaRecord = kStages * kStageBytes / 2;  // in the first warp's ring, behind its own record
+constexpr int kSelHeads = kSW * 32 / kHeadDim;            // heads that the CTA's threads finish at once
 static_assert(kRecFloats * 4 <= kOffCtaRecord, "a warp's record and the CTA's fit a warp's ring");
+static_assert(kSW * 32 % kHeadDim == 0, "every thread has a dimension of a head");
 
-__global__ void __launch_bounds__(kNW * 32, kCtasPerSm) selected_kernel(const DecodeParams p, int splits) {
+__global__ void __launch_bounds__(kSW * 32, kSelCtas) selected_kernel(const DecodeParams p, int splits) {
   constexpr int F = kFmtNvfp4, M = kScored;
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ ItemEntry s_items[kNW][64];
+  __shared__ ItemEntry s_items[kSW][64];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int g = lane >> 2, t = lane & 3;
   const int pair = blockIdx.x / splits, rank = blockIdx.x - pair * splits;
@@ -1596,12 +1606,12 @@ __global__ void __launch_bounds__(kNW * 32, kCtasPerSm) selected_kernel(const De
   const QRaw q = fetch_q(p, pair, g, t);
   const int L = clamp_len(p, b), pages = (L + kPage - 1) / kPage, listed = min(pages, p.budget);
   const int c0 = (int)((long long)listed * rank / splits), c1 = (int)((long long)listed * (rank + 1) / splits);
-  const int w0 = c0 + (c1 - c0) * warp / kNW, n = c0 + (c1 - c0) * (warp + 1) / kNW - w0;
+  const int w0 = c0 + (c1 - c0) * warp / kSW, n = c0 + (c1 - c0) * (warp + 1) / kSW - w0;
   const int32_t* const list = p.selected + (long long)pair * p.budget + w0;
   const int32_t* const table = p.page_table + (long long)b * p.max_pages;
   uint8_t* const ring = smem + warp * kStages * kStageBytes;
   const uint32_t ring_u32 = smem_u32(ring);
-  const uint32_t bar = smem_u32(smem + kRingBytes) + 8 * warp * kStages;
+  const uint32_t bar = smem_u32(smem + kSelRingBytes) + 8 * warp * kStages;
   ItemEntry* const tab = s_items[warp];
 
   // the lane's entry of the list's 32-entry chunk k, its page's id, and what the loop uses
@@ -1690,7 +1700,7 @@ __global__ void __launch_bounds__(kNW * 32, kCtasPerSm) selected_kernel(const De
   finish_piece<F, M>(p, s, pair, false, reinterpret_cast<float*>(ring), g, t);
   __syncthreads();
   float* const cta = reinterpret_cast<float*>(smem + kOffCtaRecord);
-  // thread = dimension
+  const int col = tid % kHeadDim;  // thread = dimension of a head
   auto merged = [&](int head, int parts, auto m_of, auto l_of, auto o_of, float& m, float& l, float& o) {
     m = -INFINITY, l = 0.0f, o = 0.0f;
     for (int k = 0; k < parts; ++k) m = fmaxf(m, m_of(k, head));
@@ -1704,21 +1714,21 @@ __global__ void __launch_bounds__(kNW * 32, kCtasPerSm) selected_kernel(const De
   auto put_out = [&](int head, float m, float l, float o) {
     const long long row = (long long)pair * p.group + head;
     const float v = l > 0.0f ? o * (p.v_gscale / l) : 0.0f;
-    p.out16[row * kHeadDim + tid] = (uint16_t)(pack_bf16x2(v, 0.0f) & 0xFFFFu);
-    if (tid == 0) store_lse<M>(p, row, m, l);
+    p.out16[row * kHeadDim + col] = (uint16_t)(pack_bf16x2(v, 0.0f) & 0xFFFFu);
+    if (col == 0) store_lse<M>(p, row, m, l);
   };
   const float* const recs = reinterpret_cast<const float*>(smem);
   constexpr int kStep = kStages * kStageBytes / 4;  // floats from one warp's record to the next
-  for (int head = 0; head < p.group; ++head) {
+  for (int head = tid / kHeadDim; head < p.group; head += kSelHeads) {
     float m, l, o;
-    merged(head, kNW, [&](int k, int i) { return recs[k * kStep + kOffM + i]; },
+    merged(head, kSW, [&](int k, int i) { return recs[k * kStep + kOffM + i]; },
            [&](int k, int i) { return recs[k * kStep + kOffL + i]; },
-           [&](int k, int i) { return recs[k * kStep + i * kHeadDim + tid]; }, m, l, o);
+           [&](int k, int i) { return recs[k * kStep + i * kHeadDim + col]; }, m, l, o);
     if (splits == 1) {
       put_out(head, m, l, o);
     } else {
-      cta[head * kHeadDim + tid] = o;
-      if (tid == 0) {
+      cta[head * kHeadDim + col] = o;
+      if (col == 0) {
         cta[kOffM + head] = m;
         cta[kOffL + head] = l;
       }
@@ -1727,11 +1737,11 @@ __global__ void __launch_bounds__(kNW * 32, kCtasPerSm) selected_kernel(const De
   if (splits > 1) {
     cluster_sync();
     const uint32_t* const words = reinterpret_cast<const uint32_t*>(cta);
-    for (int head = rank; head < p.group; head += splits) {
+    for (int head = rank + splits * (tid / kHeadDim); head < p.group; head += splits * kSelHeads) {
       float m, l, o;
       merged(head, splits, [&](int k, int i) { return __uint_as_float(ld_cluster(words + kOffM + i, k)); },
              [&](int k, int i) { return __uint_as_float(ld_cluster(words + kOffL + i, k)); },
-             [&](int k, int i) { return __uint_as_float(ld_cluster(words + i * kHeadDim + tid, k)); }, m, l, o);
+             [&](int k, int i) { return __uint_as_float(ld_cluster(words + i * kHeadDim + col, k)); }, m, l, o);
       put_out(head, m, l, o);
     }
     cluster_sync();  // no CTA leaves while another may still read its record
@@ -2043,21 +2053,24 @@ cudaError_t launch_decode_selected(const nvfp4kv_cache& c, const uint16_t* q, ui
   p.lse = lse;
   p.selected = selected;
   p.budget = budget;
-  const int64_t pairs = (int64_t)batch * p.hkv;
-  static const char* force = getenv("SEL_SPLITS");
+  // as many CTAs per pair (up to the portable cluster) as one wave holds
+  const int64_t pairs = (int64_t)batch * p.hkv, slots = (int64_t)num_sms * kSelCtas;
   int splits = 1;
-  while (splits < 8 && pairs * splits < num_sms) splits *= 2;
-  if (force) splits = atoi(force);
-  if (splits == 0 || pairs * splits < num_sms / 2) return enqueue_scored<kScored | kSelected>(p, stream);
+  while (splits < 8 && pairs * (splits + 1) <= slots) ++splits;
+  // past one wave, or with more than 256 pages to a CTA (in proportion fewer where
+  // SMs stay empty), the even cut over the whole device (both sides: selected_kernel)
+  const int64_t ctas = pairs * splits, listed = budget < max_pages ? budget : max_pages;
+  if (ctas > slots || listed * num_sms > 256 * splits * (ctas < num_sms ? ctas : num_sms))
+    return enqueue_scored<kScored | kSelected>(p, stream);
   static PerDeviceOnce attr_once;
   const cudaError_t e = attr_once.run([] {
-    return cudaFuncSetAttribute(selected_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+    return cudaFuncSetAttribute(selected_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSelSmemBytes);
   });
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(pairs * splits));
-  cfg.blockDim = dim3(kNW * 32);
-  cfg.dynamicSmemBytes = kSmemBytes;
+  cfg.gridDim = dim3((unsigned)ctas);
+  cfg.blockDim = dim3(kSW * 32);
+  cfg.dynamicSmemBytes = kSelSmemBytes;
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;

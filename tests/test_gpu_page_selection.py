@@ -290,16 +290,19 @@ def random_lists(lens, hkv, budget, seed, last=True):
 
 
 @pytest.mark.parametrize("lens,hkv,group,budget", [([1], 1, 1, 1), ([17, 300, 0, 5], 2, 4, 3), ([1000, 33, 257], 2, 8, 20),
-                                                   ([700], 3, 5, 1), ([512, 100], 1, 7, 200), ([5000, 40], 2, 8, 64)])
+                                                   ([700], 3, 5, 1), ([512, 100], 1, 7, 200), ([5000, 40], 2, 8, 64),
+                                                   ([8000, 100], 1, 8, 480)])
 def test_selected_decode(cuda_lib, lens, hkv, group, budget):
     table, used = page_tables(lens, 22, extra_cols=1)
     cache, o = random_cache(used, hkv, 23, gk=0.5, gv=0.25)
     run_attend(cache, o, table, lens, hkv * group, random_lists(lens, hkv, budget, 24), 25)
 
 
-def test_selected_decode_of_a_large_batch(cuda_lib):
+@pytest.mark.parametrize("batch", [20, 70, 150, 200])
+def test_selected_decode_of_a_large_batch(cuda_lib, batch):
+    # one wave of CTAs (several to a pair, one to a pair), and more pairs than that
     rng = np.random.default_rng(26)
-    lens = np.where(rng.random(150) < 0.2, 0, rng.integers(0, 700, 150)).tolist()
+    lens = np.where(rng.random(batch) < 0.2, 0, rng.integers(0, 700, batch)).tolist()
     table, used = page_tables(lens, 27)
     cache, o = random_cache(used, 2, 28)
     run_attend(cache, o, table, lens, 8, random_lists(lens, 2, 9, 29), 30)
@@ -333,7 +336,12 @@ def test_every_page_listed_is_the_plain_decode(cuda_lib):
     ws = torch.empty(kv.nvfp4kv_decode_workspace_size(cache, 3, 16), dtype=U8, device="cuda")
     o2, l2 = torch.empty_like(out), torch.empty_like(lse)
     kv.nvfp4kv_decode_attention_scored(cache, q, o2, dev(table), dev(np.asarray(lens, np.int32)), SCALE, ws, lse=l2)
-    assert torch.equal(out, o2) and torch.equal(lse, l2)                       # the same items in the same order
+    q64 = random_q((3, 16, 128), 36)[1]
+    for b, m in enumerate(lens):
+        for i in range(16):                                                    # both within the same bounds of the same values
+            r = attend_ref(o, table[b], i // 8, m, range(pages_of(lens)[b]), q64[b, i])
+            check(o2[b, i].double().cpu().numpy(), r["out"], r["tol_out"], f"{b} {i}")
+            check(l2[b, i].double().cpu().numpy(), r["lse"], r["tol_lse"], f"lse {b} {i}")
 
 
 def test_selected_decode_flags_bad_entries(cuda_lib):
