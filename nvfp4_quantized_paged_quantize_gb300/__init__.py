@@ -510,17 +510,17 @@ def nvfp4kv_plan_append(page_table, cached_lens, new_lens, free_pages, free_coun
                                     _ptr(free_left), _ptr(device_status), _stream(stream)))
 
 
-def _token_stride(name: str, x, gpu: int) -> int:
-    """Elements from one token of x (bf16 [tokens, heads, 128], a token's heads contiguous) to the next; raises
-    ValueError."""
-    _shape(name, x, 3)
-    if x.dtype is not _types().bfloat16 or x.get_device() != gpu or x.shape[2] != HEAD_DIM:
-        raise ValueError(f"{name}: expected bfloat16 [tokens, heads, {HEAD_DIM}] on the current device, got {x.dtype} "
-                         f"{tuple(x.shape)} on {x.device}")
+def _token_stride(name: str, x, tokens: int, heads: int, gpu: int) -> int:
+    """Elements from one token of x (bf16 [tokens, heads, 128] on this GPU, a token's heads contiguous) to the next;
+    raises ValueError."""
+    shape = (tokens, heads, HEAD_DIM)
+    if x is None or x.dtype is not _types().bfloat16 or x.get_device() != gpu or x.shape != shape:
+        what = "None" if x is None else f"{x.dtype} {tuple(x.shape)} on {x.device}"
+        raise ValueError(f"{name}: expected a bfloat16 tensor of shape {shape} on the current device, got {what}")
     token, head, value = x.stride()
-    if value != 1 or (x.shape[1] > 1 and head != HEAD_DIM):
+    if value != 1 or (head != HEAD_DIM and heads > 1):
         raise ValueError(f"{name}: a token's heads are contiguous rows, got strides {x.stride()}")
-    return token if x.shape[0] > 1 else x.shape[1] * HEAD_DIM
+    return token if tokens > 1 else heads * HEAD_DIM
 
 
 def nvfp4kv_norm_rope_append(cache: "Cache", q, k, v, slot_mapping, positions, cos_sin, q_out, q_weight=None,
@@ -536,18 +536,17 @@ def nvfp4kv_norm_rope_append(cache: "Cache", q, k, v, slot_mapping, positions, c
     t = _types()
     n, hq, _ = _shape("q", q, 3)
     gpu, hkv = _current_gpu(q), cache.num_kv_heads
-    strides = [_token_stride(name, x, gpu) for name, x in (("q", q), ("k", k), ("v", v), ("q_out", q_out))]
-    for name, x, heads in (("k", k, hkv), ("v", v, hkv), ("q_out", q_out, hq)):
-        if x.shape[0] != n or x.shape[1] != heads:
-            raise ValueError(f"{name}: expected {n} tokens of {heads} heads, got {tuple(x.shape)}")
+    q_stride, out_stride = _token_stride("q", q, n, hq, gpu), _token_stride("q_out", q_out, n, hq, gpu)
+    k_stride, v_stride = _token_stride("k", k, n, hkv, gpu), _token_stride("v", v, n, hkv, gpu)
     _check_tensor("slot_mapping", slot_mapping, t.int64, (n,), gpu)
     max_position, rot = (0, 0) if cos_sin is None else _shape("cos_sin", cos_sin, 2)
     if cos_sin is not None:
         _check_tensor("cos_sin", cos_sin, t.float32, (max_position, rot), gpu)
         _check_tensor("positions", positions, t.int32, (n,), gpu)
-    for name, x in (("q_weight", q_weight), ("k_weight", k_weight)):
-        if x is not None:
-            _check_tensor(name, x, t.bfloat16, (HEAD_DIM,), gpu)
+    if q_weight is not None:
+        _check_tensor("q_weight", q_weight, t.bfloat16, (HEAD_DIM,), gpu)
+    if k_weight is not None:
+        _check_tensor("k_weight", k_weight, t.bfloat16, (HEAD_DIM,), gpu)
     rows = 0
     if ws_rows is not None:
         rows = _shape("ws_k", ws_k, 3)[0]
@@ -559,10 +558,10 @@ def nvfp4kv_norm_rope_append(cache: "Cache", q, k, v, slot_mapping, positions, c
     c = cache.c_struct()
     how = _CNormRope(_ptr(q_weight), _ptr(k_weight), float(eps), rot, int(bool(interleaved)))
     _check("nvfp4kv_norm_rope_append",
-           _L().nvfp4kv_norm_rope_append(ctypes.byref(c), _ptr(q), strides[0], _ptr(k), strides[1], _ptr(v),
-                                         strides[2], hq, n, _ptr(slot_mapping),
+           _L().nvfp4kv_norm_rope_append(ctypes.byref(c), _ptr(q), q_stride, _ptr(k), k_stride, _ptr(v), v_stride,
+                                         hq, n, _ptr(slot_mapping),
                                          None if cos_sin is None else _ptr(positions), _ptr(cos_sin), max_position,
-                                         ctypes.byref(how), _ptr(q_out), strides[3], _ptr(ws_rows), rows,
+                                         ctypes.byref(how), _ptr(q_out), out_stride, _ptr(ws_rows), rows,
                                          float(k_ws_scale), float(v_ws_scale), _ptr(ws_k), _ptr(ws_v),
                                          _ptr(device_status), _stream(stream)))
 

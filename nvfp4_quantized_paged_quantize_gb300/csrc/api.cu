@@ -468,7 +468,7 @@ int nvfp4kv_plan_append(int32_t* page_table, int32_t max_pages_per_seq, const in
   if (batch < 0 || max_pages_per_seq <= 0 || free_capacity < 0 || num_pages <= 0 || max_tokens < 0)
     return NVFP4KV_ERR_INVALID_ARGUMENT;
   if ((int64_t)max_pages_per_seq * kPageSize >= (int64_t(1) << 31) || max_tokens >= (int64_t(1) << 31) - (1 << 14) ||
-      num_pages * kPageSize >= (int64_t(1) << 31) || batch >= (1 << 30))
+      num_pages * kPageSize >= (int64_t(1) << 31) || batch >= (1 << 30) || free_capacity > (1 << 30))
     return NVFP4KV_ERR_UNSUPPORTED;
   if (!free_count || !free_left || (free_capacity > 0 && !free_pages) || (max_tokens > 0 && !slot_mapping))
     return NVFP4KV_ERR_INVALID_ARGUMENT;

@@ -2,25 +2,28 @@
 // head) the first, the latest, and those between with the largest scores
 // (nvfp4kv_select_pages), in page order.
 //
-// One CTA per pair; each thread keeps its pages' scores in registers, as integers
-// that order like the floats.  The smallest kept key is found by a histogram of
-// 2048 equal parts of the keys' range (not of all keys: scores of one pair share
-// their upper bits), then of the part that holds it, until that part's keys all
-// stay, are all equal, or are few enough (32) for a warp to rank.  Equal keys go to
+// One CTA per pair; each thread keeps its pages' scores in registers.  The smallest
+// kept one is found by a histogram of equal parts of the scores' range (1024 or 2048),
+// whose part with the threshold mostly has few enough (32) for a warp to rank.  Else,
+// and where the range is not finite, by histograms of the scores as integers that
+// order like the floats (keys), of equal parts of what is left each time.
+// (Parts of the integers' range from the start are too wide wherever scores lie on both
+// sides of zero: half of the integers are smaller than 1 in size.)  Equal keys go to
 // the lower page: with n keys above the threshold and e equal to it before a page,
 // the page lands at place n + min(e, equal ones still wanted), so one ordered count
 // over the warps, which hold consecutive pages, gives every destination.
-// Bound by latency: the loads, then some seven block barriers.
+// Bound by the instructions of one SM and the latency of its steps: the loads, then
+// six block barriers.
 #include "nvfp4kv_device.cuh"
 #include "nvfp4kv_launch.h"
 
 namespace nvfp4kv {
 namespace {
 
-constexpr int kBins = 2048;
 constexpr int kFew = 32;
 constexpr uint32_t kAll = 0xFFFFFFFFu;
 constexpr uint32_t kKeyNone = 0;  // no float's key: below that of -inf
+constexpr float kLeastRange = 1e-30f;  // of the scores, for parts of it
 
 // An unsigned integer that orders like the float: +-0 equal, NaN on top.
 __device__ __forceinline__ uint32_t order_key(float x) {
@@ -29,7 +32,11 @@ __device__ __forceinline__ uint32_t order_key(float x) {
   return (u & 0x80000000u) ? ~u : u | 0x80000000u;
 }
 
-template <int kThreads>
+__device__ __forceinline__ float key_score(uint32_t k) {
+  return __uint_as_float((k & 0x80000000u) ? k ^ 0x80000000u : ~k);
+}
+
+template <int kThreads, int kBins>
 struct SelectShared {
   uint32_t hist[kBins];
   uint32_t warp_sum[kThreads / 32], warp_min[kThreads / 32], warp_max[kThreads / 32];
@@ -38,12 +45,12 @@ struct SelectShared {
   uint32_t few[kFew], few_count;
 };
 
-// kRows: keys of a thread in registers.  A warp holds consecutive pages, `rows` to a
+// kRows: scores of a thread in registers.  A warp holds consecutive pages, `rows` to a
 // lane; kMore: there may be more than kRows, read again at every use.
-template <int kThreads, int kRows, bool kMore>
-__global__ void __launch_bounds__(kThreads) select_kernel(const SelectArgs p) {
+template <int kThreads, int kBins, int kRows, bool kMore, int kCtas>
+__global__ void __launch_bounds__(kThreads, kCtas) select_kernel(const SelectArgs p) {
   constexpr int kWarps = kThreads / 32;
-  __shared__ SelectShared<kThreads> s;
+  __shared__ SelectShared<kThreads, kBins> s;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const long long pair = blockIdx.x;
   const int L = __ldg(p.seq_lens + (int)(pair / p.hkv));
@@ -63,53 +70,58 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const SelectArgs p) {
   const float* mine = p.scores + pair * p.score_stride + p.first;
   const int rows = (middle + kThreads - 1) / kThreads;  // warp w: pages [32 rows w, 32 rows (w + 1)) of the middle
   const int at0 = warp * rows * 32 + lane;
-  uint32_t key[kRows];
+  const int own = min(max((middle - at0 + 31) / 32, 0), rows);  // scores of this thread
+  float x[kRows];
 #pragma unroll
-  for (int j = 0; j < kRows; ++j) {
-    const int i = at0 + 32 * j;
-    key[j] = j < rows && i < middle ? order_key(__ldg(mine + i)) : kKeyNone;
-  }
-  auto key_at = [&](int j) {  // rows past the registers
-    const int i = at0 + 32 * j;
-    return i < middle ? order_key(__ldg(mine + i)) : kKeyNone;
-  };
-  auto each = [&](auto f) {  // every key of the thread, in page order over the warp
+  for (int j = 0; j < kRows; ++j) x[j] = j < own ? __ldg(mine + at0 + 32 * j) : 0.0f;
+  auto each = [&](auto f) {  // every score of the thread
 #pragma unroll
     for (int j = 0; j < kRows; ++j)
-      if (j < rows) f(j, key[j]);
+      if (j < own) f(x[j]);
     if constexpr (kMore)
-      for (int j = kRows; j < rows; ++j) f(j, key_at(j));
+      for (int j = kRows; j < own; ++j) f(__ldg(mine + at0 + 32 * j));
   };
   for (int i = tid; i < p.first; i += kThreads) selected[i] = i;
   for (int i = tid; i < p.recent; i += kThreads) selected[p.budget - p.recent + i] = n - p.recent + i;
   if (want == 0) return;
 
-  uint32_t lo = 0xFFFFFFFFu, hi = 0;
-  each([&](int, uint32_t k) {
-    if (k != kKeyNone) {
+  // the smallest and the largest key of the scores that `of` picks, over the block; every
+  // thread calls it, after the last use of the warps' words
+  uint32_t lo, hi;
+  auto bounds = [&](auto of) {
+    lo = 0xFFFFFFFFu;
+    hi = 0;
+    each([&](float v) {
+      if (!of(v)) return;
+      const uint32_t k = order_key(v);
       lo = min(lo, k);
       hi = max(hi, k);
+    });
+    lo = __reduce_min_sync(kAll, lo);
+    hi = __reduce_max_sync(kAll, hi);
+    if (lane == 0) {
+      s.warp_min[warp] = lo;
+      s.warp_max[warp] = hi;
     }
-  });
-  lo = __reduce_min_sync(kAll, lo);
-  hi = __reduce_max_sync(kAll, hi);
-  if (lane == 0) {
-    s.warp_min[warp] = lo;
-    s.warp_max[warp] = hi;
-  }
+    __syncthreads();
+    lo = __reduce_min_sync(kAll, s.warp_min[lane % kWarps]);
+    hi = __reduce_max_sync(kAll, s.warp_max[lane % kWarps]);
+  };
   if (tid == 0) s.few_count = 0;
 #pragma unroll
   for (int i = 0; i < kBins / kThreads; ++i) s.hist[tid + i * kThreads] = 0;
-  __syncthreads();
-  lo = __reduce_min_sync(kAll, s.warp_min[lane % kWarps]);
-  hi = __reduce_max_sync(kAll, s.warp_max[lane % kWarps]);
+  bounds([](float) { return true; });
 
   // the threshold lies among the keys lo + [0, width), of which the `left` largest stay
-  uint32_t left = (uint32_t)want, width = 0xFFFFFFFFu, cut;
-  int shift = max(0, 32 - __clz(hi - lo) - 11);  // (hi - lo) >> shift < 2048
-  while (true) {
-    each([&](int, uint32_t k) {
-      if (k != kKeyNone && k - lo < width) atomicAdd(&s.hist[(k - lo) >> shift], 1u);
+  uint32_t left = (uint32_t)want, width = 0xFFFFFFFFu, cut = 0;
+  int shift = 0;
+  // the largest part, and what a count found: the threshold's part, the keys in it
+  uint32_t bin = 0, count = 0;
+  // counts the scores by their parts `of` (kBins for none), finds the threshold's
+  auto find = [&](auto of) {
+    each([&](float v) {
+      const uint32_t at = of(v);
+      if (at < kBins) atomicAdd(&s.hist[at], 1u);
     });
     __syncthreads();
     constexpr int kPer = kBins / kThreads;
@@ -117,9 +129,9 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const SelectArgs p) {
     uint32_t c[kPer], sum = 0;
 #pragma unroll
     for (int j = 0; j < kPer; ++j) {
-      const int bin = kBins - 1 - (kPer * tid + j);
-      sum += c[j] = s.hist[bin];
-      s.hist[bin] = 0;
+      const int i = kBins - 1 - (kPer * tid + j);
+      sum += c[j] = s.hist[i];
+      s.hist[i] = 0;
     }
     uint32_t incl = sum;
 #pragma unroll
@@ -140,62 +152,113 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const SelectArgs p) {
       above += c[j];
     }
     __syncthreads();
-    lo += s.bin << shift;
+    bin = s.bin;
+    count = s.in_bin;
     left -= s.above;
-    const uint32_t count = s.in_bin;
+  };
+  // the cut among the `count` <= kFew scores that `of` picks, ranked by every warp: it has
+  // fewer than `left` keys above it, and with its equals at least that
+  auto rank = [&](auto of) {
+    each([&](float v) {
+      if (of(v)) s.few[atomicAdd(&s.few_count, 1u)] = order_key(v);
+    });
+    __syncthreads();
+    const uint32_t k = lane < count ? s.few[lane] : kKeyNone;
+    uint32_t greater = 0, equal = 0;
+    for (uint32_t r = 0; r < count; ++r) {
+      const uint32_t other = __shfl_sync(kAll, k, r);
+      greater += other > k;
+      equal += other == k;
+    }
+    const int who = __ffs(__ballot_sync(kAll, lane < count && greater < left && greater + equal >= left)) - 1;
+    cut = __shfl_sync(kAll, k, who);
+    left -= __shfl_sync(kAll, greater, who);
+  };
+  bool found = false;
+  const float low = key_score(lo), range = key_score(hi) - low;
+  if (range >= kLeastRange && range < INFINITY) {  // (not with an infinity or a NaN at either end)
+    const float scale = (float)(kBins - 1) / range;
+    // rounding keeps the order: a larger score is in no lower part
+    auto part = [&](float v) { return min((uint32_t)((v - low) * scale), (uint32_t)kBins - 1); };
+    find(part);
+    const uint32_t chosen = bin;
+    if (count <= kFew) {
+      rank([&](float v) { return part(v) == chosen; });
+      found = true;
+    } else {
+      bounds([&](float v) { return part(v) == chosen; });
+      width = hi - lo + 1;
+    }
+  }
+  constexpr int kBits = kBins == 2048 ? 11 : 10;
+  static_assert(kBins == 1 << kBits, "a part is a bit field of the keys");
+  if (!found) shift = max(0, 32 - __clz(hi - lo) - kBits);  // (hi - lo) >> shift < kBins
+  while (!found) {
+    find([&](float v) {
+      const uint32_t k = order_key(v);
+      return k - lo < width ? (k - lo) >> shift : (uint32_t)kBins;
+    });
+    lo += bin << shift;
+    found = true;
+    width = 1u << shift;
     if (shift == 0) {  // one key
       cut = lo;
-      break;
-    }
-    if (count == left) {  // the whole part stays
+    } else if (count == left) {  // the whole part stays
       cut = lo - 1;
       left = 0;
-      break;
+    } else if (count <= kFew) {
+      rank([&](float v) { return order_key(v) - lo < width; });
+    } else {
+      shift = max(0, shift - kBits);
+      found = false;
     }
-    width = 1u << shift;
-    if (count <= kFew) {
-      each([&](int, uint32_t k) {
-        if (k != kKeyNone && k - lo < width) s.few[atomicAdd(&s.few_count, 1u)] = k;
-      });
-      __syncthreads();
-      // every warp ranks them: the cut has fewer than `left` keys above it, and with its equals at least that
-      const uint32_t k = lane < count ? s.few[lane] : kKeyNone;
-      uint32_t greater = 0, equal = 0;
-      for (uint32_t r = 0; r < count; ++r) {
-        const uint32_t other = __shfl_sync(kAll, k, r);
-        greater += other > k;
-        equal += other == k;
-      }
-      const uint32_t is = __ballot_sync(kAll, lane < count && greater < left && greater + equal >= left);
-      const int who = __ffs(is) - 1;
-      cut = __shfl_sync(kAll, k, who);
-      left -= __shfl_sync(kAll, greater, who);
-      break;
-    }
-    shift = max(0, shift - 11);
   }
 
-  // keys above the cut stay, and the first `left` equal to it
-  uint32_t gt = 0, eq = 0;
-  each([&](int, uint32_t k) {
-    gt += k > cut;
-    eq += k == cut;
-  });
-  gt = __reduce_add_sync(kAll, gt);
-  eq = __reduce_add_sync(kAll, eq);
-  if (lane == 0) s.warp_count[warp] = make_uint2(gt, eq);
+  // keys above the cut stay, and the first `left` equal to it: by rows of the warp, then
+  // by warps
+  uint32_t above[kRows], equal[kRows], g = 0, e = 0;
+#pragma unroll
+  for (int j = 0; j < kRows; ++j) {
+    const uint32_t k = j < own ? order_key(x[j]) : kKeyNone;
+    above[j] = __ballot_sync(kAll, k > cut);
+    equal[j] = __ballot_sync(kAll, k == cut);
+    g += __popc(above[j]);
+    e += __popc(equal[j]);
+  }
+  auto more = [&](int j, uint32_t& a, uint32_t& q) {  // a row past the registers
+    const uint32_t k = j < own ? order_key(__ldg(mine + at0 + 32 * j)) : kKeyNone;
+    a = __ballot_sync(kAll, k > cut);
+    q = __ballot_sync(kAll, k == cut);
+  };
+  if constexpr (kMore)
+    for (int j = kRows; j < rows; ++j) {
+      uint32_t a, q;
+      more(j, a, q);
+      g += __popc(a);
+      e += __popc(q);
+    }
+  if (lane == 0) s.warp_count[warp] = make_uint2(g, e);
   __syncthreads();
   const uint2 counted = s.warp_count[lane % kWarps];
-  uint32_t g = __reduce_add_sync(kAll, lane < warp ? counted.x : 0u), e = __reduce_add_sync(kAll, lane < warp ? counted.y : 0u);
+  g = __reduce_add_sync(kAll, lane < warp ? counted.x : 0u);
+  e = __reduce_add_sync(kAll, lane < warp ? counted.y : 0u);
   const uint32_t below = (1u << lane) - 1;
-  each([&](int j, uint32_t k) {
-    const uint32_t bg = __ballot_sync(kAll, k > cut), be = __ballot_sync(kAll, k == cut);
-    const uint32_t before = e + __popc(be & below);
-    if (k > cut || (k == cut && before < left))
-      selected[p.first + (int)(g + __popc(bg & below) + min(before, left))] = p.first + at0 + 32 * j;
-    g += __popc(bg);
-    e += __popc(be);
-  });
+  auto put = [&](int j, uint32_t a, uint32_t q) {
+    const uint32_t before = e + __popc(q & below);
+    if ((a >> lane & 1) || ((q >> lane & 1) && before < left))
+      selected[p.first + (int)(g + __popc(a & below) + min(before, left))] = p.first + at0 + 32 * j;
+    g += __popc(a);
+    e += __popc(q);
+  };
+#pragma unroll
+  for (int j = 0; j < kRows; ++j)
+    if (j < rows) put(j, above[j], equal[j]);
+  if constexpr (kMore)
+    for (int j = kRows; j < rows; ++j) {
+      uint32_t a, q;
+      more(j, a, q);
+      put(j, a, q);
+    }
 }
 
 }  // namespace
@@ -205,11 +268,11 @@ cudaError_t launch_select_pages(const SelectArgs& args, cudaStream_t stream) {
   // the lengths are on the device, so the shape goes by the pages that the scores have room for
   const int64_t most = args.score_stride;
   if (most <= 256 * 8)
-    select_kernel<256, 8, false><<<pairs, 256, 0, stream>>>(args);
-  else if (most <= 1024 * 16)
-    select_kernel<1024, 16, false><<<pairs, 1024, 0, stream>>>(args);
+    select_kernel<256, 1024, 8, false, 6><<<pairs, 256, 0, stream>>>(args);
+  else if (most <= 1024 * 9)
+    select_kernel<1024, 2048, 9, false, 1><<<pairs, 1024, 0, stream>>>(args);
   else
-    select_kernel<1024, 16, true><<<pairs, 1024, 0, stream>>>(args);
+    select_kernel<1024, 2048, 16, true, 1><<<pairs, 1024, 0, stream>>>(args);
   return cudaGetLastError();
 }
 

@@ -123,6 +123,18 @@ def test_bad_inputs_are_flagged(cuda_lib):
         assert p.check()["flags"] & kv.NVFP4KV_DEVERR_LENGTH
 
 
+def test_sums_past_32_bits(cuda_lib):
+    # requests that want 2^20 tokens each (3000 of them: more than 2^31 together), in small and in large blocks; the
+    # first one fits
+    for batch in (200, 3000):
+        p = Plan(np.zeros(batch), np.zeros(batch), cols=1 << 16, tokens=50, spare=4)
+        p.new[0], p.new[1:] = 20, 1 << 20
+        p.nl = dev(p.new)
+        p.run()
+        want = p.check()
+        assert want["flags"] == kv.NVFP4KV_DEVERR_POOL and want["lens"][:2] == [20, 0]
+
+
 def test_in_place_and_without_the_optional_outputs(cuda_lib):
     rng = np.random.default_rng(3)
     for batch in (4, 1500):
