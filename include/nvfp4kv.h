@@ -580,15 +580,15 @@ int nvfp4kv_evict(const nvfp4kv_cache* cache, const int32_t* page_table, int32_t
  *   cached_lens   device int32 [batch], >= 0 and <= max_pages_per_seq * page_size
  *   new_lens      device int32 [batch], >= 0, likewise with the cached ones (cut to
  *                 that with NVFP4KV_DEVERR_LENGTH)
- *   free_pages    device int32 [free_capacity]: a stack of page ids, the top at
- *                 *free_count - 1; the n-th page needed is the n-th from the top.
+ *   free_pages    device int32 [free_capacity]: a stack of page ids (at most 2^30),
+ *                 the top at *free_count - 1; the n-th page needed is the n-th from the top.
  *                 Not written: pages are given back by storing them from
  *                 *free_count on and raising the count
  *   free_count    device int32 (outside [0, free_capacity]: cut to it with
  *                 NVFP4KV_DEVERR_LENGTH)
  *   num_pages     of the cache; a page id outside [0, num_pages) gives its tokens
  *                 the slot -1 with NVFP4KV_DEVERR_PAGE
- *   max_tokens    room for new tokens in the arrays below
+ *   max_tokens    room for new tokens in the arrays below, < 2^31 - 2^18
  * Outputs, device; the optional ones may be NULL:
  *   seq_lens      int32 [batch]: cached + new.  May be cached_lens itself
  *   slot_mapping  int64 [max_tokens]: the slot of each new token, request by
@@ -599,8 +599,7 @@ int nvfp4kv_evict(const nvfp4kv_cache* cache, const int32_t* page_table, int32_t
  *                 every request's tokens one request after the other; -1 behind the last
  *   cu_prefix     int64 [batch + 1], optional: the requests' first workspace rows
  *   free_left     int32: the count without the pages taken.  May be free_count itself
- * Enqueues one kernel, which reads and writes its few pages' worth of data from
- * one cluster of CTAs. */
+ * Enqueues one kernel. */
 int nvfp4kv_plan_append(int32_t* page_table, int32_t max_pages_per_seq, const int32_t* cached_lens,
                         const int32_t* new_lens, int32_t batch, const int32_t* free_pages, int32_t free_capacity,
                         const int32_t* free_count, int64_t num_pages, int64_t max_tokens, int32_t* seq_lens,

@@ -467,7 +467,7 @@ int nvfp4kv_plan_append(int32_t* page_table, int32_t max_pages_per_seq, const in
                         int64_t* cu_prefix, int32_t* free_left, int32_t* device_status, nvfp4kv_stream_t stream) {
   if (batch < 0 || max_pages_per_seq <= 0 || free_capacity < 0 || num_pages <= 0 || max_tokens < 0)
     return NVFP4KV_ERR_INVALID_ARGUMENT;
-  if ((int64_t)max_pages_per_seq * kPageSize >= (int64_t(1) << 31) || max_tokens >= (int64_t(1) << 31) - (1 << 14) ||
+  if ((int64_t)max_pages_per_seq * kPageSize >= (int64_t(1) << 31) || max_tokens >= (int64_t(1) << 31) - (1 << 18) ||
       num_pages * kPageSize >= (int64_t(1) << 31) || batch >= (1 << 30) || free_capacity > (1 << 30))
     return NVFP4KV_ERR_UNSUPPORTED;
   if (!free_count || !free_left || (free_capacity > 0 && !free_pages) || (max_tokens > 0 && !slot_mapping))

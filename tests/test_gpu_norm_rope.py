@@ -181,3 +181,16 @@ def test_capture_on_another_stream(cuda_lib):
     graph.replay()                                            # writing the same bytes again changes nothing
     torch.cuda.synchronize()
     a.check()
+
+
+def test_tokens_far_apart(cuda_lib):
+    # rows whose offsets pass 2^31 elements, of the queries, keys and values and of the result
+    a = Append(3, 2, 1, packed=False, seed=16)
+    far = (1 << 30) + 128
+    big = torch.empty(2 * far + 512, dtype=BF16, device="cuda")
+    rows = big.as_strided((3, 4, 128), (far, 128, 1))
+    for h, part in ((0, a.q), (2, a.k), (3, a.v)):
+        rows[:, h:h + part.shape[1]] = part
+    a.q, a.k, a.v = rows[:, :2], rows[:, 2:3], rows[:, 3:4]
+    a.run(q_out=a.q)
+    a.check(q_out=a.q)

@@ -125,7 +125,8 @@ def test_digest_and_scores_flag_bad_pages_and_lengths(cuda_lib):
 
 
 @pytest.mark.parametrize("lens,hkv,group,size", [([1], 1, 1, 1.0), ([16, 300, 0, 5], 2, 4, 1.0), ([257, 256, 255], 3, 8, 30.0),
-                                                 ([1000, 33], 2, 5, 2.0 ** -70), ([500], 8, 7, 2.0 ** 60)])
+                                                 ([1000, 33], 2, 5, 2.0 ** -70), ([500], 8, 7, 2.0 ** 60), ([300, 40], 5, 2, 1.0),
+                                                 ([90, 530], 12, 1, 1.0), ([2100], 1, 3, 1.0), ([700, 50], 4, 2, 1.0)])
 def test_scores(cuda_lib, lens, hkv, group, size):
     table, used = page_tables(lens, 14, extra_cols=1)
     cache, o = random_cache(used, hkv, 15, gk=0.37)
@@ -354,6 +355,68 @@ def test_selected_decode_flags_bad_entries(cuda_lib):
     table[0, sel[0, 1, 0]] = used                                              # a listed page outside the pool
     sel = random_lists(lens, 2, 4, 39)
     run_attend(cache, o, table, lens, 8, sel, 40, flags=kv.NVFP4KV_DEVERR_PAGE, skip={(0, int(sel[0, 1, 0]))})
+
+
+def test_pages_at_the_end_of_a_large_pool(cuda_lib):
+    # byte offsets past 2^32 in the pool and past 2^29 in the digests: the same results as from a small pool
+    lens, hkv = [200, 37], 8
+    table, used = page_tables(lens, 60)
+    small, _ = random_cache(used, hkv, 61)
+    many = 280000
+    big = kv.Cache.empty(many, hkv)
+    big.pages[many - used:] = small.pages
+    sl, sel = dev(np.asarray(lens, np.int32)), dev(random_lists(lens, hkv, 5, 62))
+    q, _ = random_q((2, 16, 128), 63)
+    got = []
+    for cache, shift in ((small, 0), (big, many - used)):
+        pt = dev(np.where(table >= 0, table + shift, table).astype(np.int32))
+        status = status_word()
+        d = torch.zeros((cache.num_pages, hkv, kv.NVFP4KV_DIGEST_BYTES), dtype=U8, device="cuda")
+        kv.nvfp4kv_page_digest(cache, pt, sl, d, device_status=status)
+        scores = torch.zeros((2, hkv, table.shape[1]), device="cuda")
+        kv.nvfp4kv_page_scores(cache, d, q, pt, sl, SCALE, scores, device_status=status)
+        out, lse = torch.empty_like(q), torch.empty((2, 16), device="cuda")
+        ws = torch.empty(kv.nvfp4kv_decode_workspace_size(cache, 2, 16), dtype=U8, device="cuda")
+        kv.nvfp4kv_decode_attention_selected(cache, q, out, pt, sl, SCALE, sel, ws, lse=lse, device_status=status)
+        torch.cuda.synchronize()
+        assert status.item() == 0
+        got.append((d[cache.num_pages - used:], scores, out, lse))
+    for name, a, b in zip(("digests", "scores", "out", "lse"), *got):
+        assert torch.equal(a, b), name
+
+
+def test_two_streams_at_once(cuda_lib):
+    # the calls keep no state: two batches in flight on two streams give what each gives alone
+    made = []
+    for k in range(2):
+        lens = [1500 + 700 * k, 333]
+        table, used = page_tables(lens, 64 + k)
+        cache, _ = random_cache(used, 2, 66 + k)
+        sl, pt = dev(np.asarray(lens, np.int32)), dev(table)
+        q, _ = random_q((2, 8, 128), 68 + k)
+        d = torch.zeros((used, 2, kv.NVFP4KV_DIGEST_BYTES), dtype=U8, device="cuda")
+        ws = torch.empty(kv.nvfp4kv_decode_workspace_size(cache, 2, 8), dtype=U8, device="cuda")
+        made.append((cache, pt, sl, q, d, ws, table.shape[1]))
+
+    def run(m, stream=None):
+        cache, pt, sl, q, d, ws, pages = m
+        scores, sel = torch.zeros((2, 2, pages), device="cuda"), torch.empty((2, 2, 20), dtype=torch.int32, device="cuda")
+        out = torch.empty_like(q)
+        if stream:
+            stream.wait_stream(torch.cuda.current_stream())
+        for _ in range(20):
+            kv.nvfp4kv_page_digest(cache, pt, sl, d, stream=stream)
+            kv.nvfp4kv_page_scores(cache, d, q, pt, sl, SCALE, scores, stream=stream)
+            kv.nvfp4kv_select_pages(scores, sl, 20, 1, 2, sel, stream=stream)
+            kv.nvfp4kv_decode_attention_selected(cache, q, out, pt, sl, SCALE, sel, ws, stream=stream)
+        return scores, sel, out
+
+    alone = [run(m) for m in made]
+    torch.cuda.synchronize()
+    together = [run(m, torch.cuda.Stream()) for m in made]
+    torch.cuda.synchronize()
+    for a, b in zip(alone, together):
+        assert all(torch.equal(x, y) for x, y in zip(a, b))
 
 
 # --- a whole step ----------------------------------------------------------

@@ -43,7 +43,7 @@ def test_plan_refusals(lib):
     assert call() == INVALID                                                   # no free count
     for bad in (dict(a1=0), dict(a4=-1), dict(a6=-1), dict(a8=0), dict(a9=-1)):
         assert call(a7=4, **bad) == INVALID, bad
-    for big in (dict(a1=1 << 27), dict(a9=(1 << 31) - 1), dict(a8=1 << 27), dict(a4=1 << 30),
+    for big in (dict(a1=1 << 27), dict(a9=(1 << 31) - 1), dict(a9=(1 << 31) - (1 << 18)), dict(a8=1 << 27), dict(a4=1 << 30),
                 dict(a6=(1 << 30) + 1)):
         assert call(a7=4, **big) == UNSUPPORTED, big
     for missing in (0, 2, 3, 5, 10, 11, 16):
