@@ -1604,18 +1604,32 @@ __global__ void __launch_bounds__(kSW * 32, kSelCtas) selected_kernel(const Deco
   const int pair = blockIdx.x / splits, rank = blockIdx.x - pair * splits;
   const int b = pair / p.hkv, h = pair - b * p.hkv;
   const QRaw q = fetch_q(p, pair, g, t);
+  // the warp's part [w0, w0 + n) of a list of `listed` entries
+  int w0, n;
+  auto part = [&](int listed) {
+    const int c0 = (int)((long long)listed * rank / splits), c1 = (int)((long long)listed * (rank + 1) / splits);
+    w0 = c0 + (c1 - c0) * warp / kSW;
+    n = c0 + (c1 - c0) * (warp + 1) / kSW - w0;
+  };
+  // the lane's entry of the part's 32-entry chunk k
+  const int32_t* const list = p.selected + (long long)pair * p.budget;
+  auto entry = [&](int k) { return 32 * k + lane < n ? __ldg(list + w0 + 32 * k + lane) : -1; };
+  // the first entries are read before the length is there, as if the list were full
+  const int full = min(p.max_pages, p.budget);
+  part(full);
+  int sel0 = entry(0);
   const int L = clamp_len(p, b), pages = (L + kPage - 1) / kPage, listed = min(pages, p.budget);
-  const int c0 = (int)((long long)listed * rank / splits), c1 = (int)((long long)listed * (rank + 1) / splits);
-  const int w0 = c0 + (c1 - c0) * warp / kSW, n = c0 + (c1 - c0) * (warp + 1) / kSW - w0;
-  const int32_t* const list = p.selected + (long long)pair * p.budget + w0;
+  if (listed != full) {
+    part(listed);
+    sel0 = entry(0);
+  }
   const int32_t* const table = p.page_table + (long long)b * p.max_pages;
   uint8_t* const ring = smem + warp * kStages * kStageBytes;
   const uint32_t ring_u32 = smem_u32(ring);
   const uint32_t bar = smem_u32(smem + kSelRingBytes) + 8 * warp * kStages;
   ItemEntry* const tab = s_items[warp];
 
-  // the lane's entry of the list's 32-entry chunk k, its page's id, and what the loop uses
-  auto entry = [&](int k) { return 32 * k + lane < n ? __ldg(list + 32 * k + lane) : -1; };
+  // an entry's page id, and what the loop uses of it
   auto page_id = [&](int sel) {
     if (sel >= pages) flag_error(p.status, NVFP4KV_DEVERR_PAGE);
     return sel >= 0 && sel < pages ? __ldg(table + sel) : -1;
@@ -1632,18 +1646,16 @@ __global__ void __launch_bounds__(kSW * 32, kSelCtas) selected_kernel(const Deco
   };
 
   WarpState s;
-  load_q<F, M>(p, q, s, pair, g, t);
+  if (n == 0) load_q<F, M>(p, q, s, pair, g, t);
   if (n > 0) {
+    int sel1 = entry(1), sel2 = entry(2);  // of the next chunk and the one after it
+    const int id0 = page_id(sel0);
     if (lane == 0) {
       for (int i = 0; i < kStages; ++i) mbar_init(bar + 8 * i, 32);
       fence_mbar_init();
     }
     __syncwarp();
-    int sel1 = entry(1), sel2 = entry(2);  // of the next chunk and the one after it
-    {
-      const int sel0 = entry(0);
-      put(0, sel0, page_id(sel0));
-    }
+    put(0, sel0, id0);
     int id1 = page_id(sel1);
     int chunk = 0;
     const LaneCopy lc = lane_copy<F>(p, lane);
@@ -1654,6 +1666,7 @@ __global__ void __launch_bounds__(kSW * 32, kSelCtas) selected_kernel(const Deco
       issued = i + 1;
     };
     for (int i = 0; i < min(n, kStages); ++i) issue(i);
+    load_q<F, M>(p, q, s, pair, g, t);
     bool alive = true;
     for (int j = 0; j < n && alive; j += 2) {
       if ((j & 31) == 16 && 32 * (chunk + 1) < n) {
