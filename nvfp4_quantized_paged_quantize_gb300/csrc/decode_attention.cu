@@ -1591,9 +1591,21 @@ __global__ void __launch_bounds__(kCombineMaxWarps * 32) combine_kernel(const De
 constexpr int kSW = 8, kSelCtas = 2;  // warps of a CTA, CTAs of an SM
 constexpr int kSelRingBytes = kSW * kStages * kStageBytes, kSelSmemBytes = kSelRingBytes + kSW * kStages * 8;
 constexpr int kOffCtaRecord = kStages * kStageBytes / 2;  // in the first warp's ring, behind its own record
-constexpr int kSelHeads = kSW * 32 / kHeadDim;            // heads that the CTA's threads finish at once
+constexpr int kMaxSplits = 8;  // the portable cluster
 static_assert(kRecFloats * 4 <= kOffCtaRecord, "a warp's record and the CTA's fit a warp's ring");
-static_assert(kSW * 32 % kHeadDim == 0, "every thread has a dimension of a head");
+static_assert(kSW >= kGMax && kSW <= 8 && kMaxSplits <= 8 && kHeadDim == 32 * 4, "a warp finishes a head of eight parts at most");
+
+// The word, the four words, at this address of the same shared memory in another CTA of the cluster.
+__device__ __forceinline__ float ld_cluster_f32(const float* local, uint32_t rank) {
+  return __uint_as_float(ld_cluster(reinterpret_cast<const uint32_t*>(local), rank));
+}
+__device__ __forceinline__ float4 ld_cluster_f32x4(const float* local, uint32_t rank) {
+  uint32_t at;
+  float4 v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_u32(local)), "r"(rank));
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(at) : "memory");
+  return v;
+}
 
 __global__ void __launch_bounds__(kSW * 32, kSelCtas) selected_kernel(const DecodeParams p, int splits) {
   constexpr int F = kFmtNvfp4, M = kScored;
@@ -1712,51 +1724,70 @@ __global__ void __launch_bounds__(kSW * 32, kSelCtas) selected_kernel(const Deco
   // the warps' records, each in its own ring
   finish_piece<F, M>(p, s, pair, false, reinterpret_cast<float*>(ring), g, t);
   __syncthreads();
-  float* const cta = reinterpret_cast<float*>(smem + kOffCtaRecord);
-  const int col = tid % kHeadDim;  // thread = dimension of a head
-  auto merged = [&](int head, int parts, auto m_of, auto l_of, auto o_of, float& m, float& l, float& o) {
-    m = -INFINITY, l = 0.0f, o = 0.0f;
-    for (int k = 0; k < parts; ++k) m = fmaxf(m, m_of(k, head));
-    if (m == -INFINITY) return;
-    for (int k = 0; k < parts; ++k) {
-      const float w = ex2(m_of(k, head) - m);
-      l = fmaf(w, l_of(k, head), l);
-      o = fmaf(w, o_of(k, head), o);
+  // warp = head, lane = four dimensions: the head's parts, lane k < parts holding part
+  // k's maximum and sum, o4(k) its four values
+  auto merge = [&](int parts, float m, float l, auto o4, float& top, float& sum, float4& o) {
+    top = lane < parts ? m : -INFINITY;
+#pragma unroll
+    for (int off = 1; off < 8; off <<= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, off));
+    const float w = lane < parts && m != -INFINITY ? ex2(m - top) : 0.0f;
+    sum = lane < parts ? w * l : 0.0f;
+#pragma unroll
+    for (int off = 1; off < 8; off <<= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, off);
+    top = __shfl_sync(0xFFFFFFFFu, top, 0);
+    sum = __shfl_sync(0xFFFFFFFFu, sum, 0);
+    o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      if (k >= parts) break;
+      const float4 v = o4(k);
+      const float wk = __shfl_sync(0xFFFFFFFFu, w, k);
+      o.x = fmaf(wk, v.x, o.x);
+      o.y = fmaf(wk, v.y, o.y);
+      o.z = fmaf(wk, v.z, o.z);
+      o.w = fmaf(wk, v.w, o.w);
     }
   };
-  auto put_out = [&](int head, float m, float l, float o) {
+  auto put_out = [&](int head, float m, float l, const float4& o) {
     const long long row = (long long)pair * p.group + head;
-    const float v = l > 0.0f ? o * (p.v_gscale / l) : 0.0f;
-    p.out16[row * kHeadDim + col] = (uint16_t)(pack_bf16x2(v, 0.0f) & 0xFFFFu);
-    if (col == 0) store_lse<M>(p, row, m, l);
+    const float r = l > 0.0f ? p.v_gscale / l : 0.0f;
+    reinterpret_cast<uint2*>(p.out16 + row * kHeadDim)[lane] =
+        make_uint2(pack_bf16x2(o.x * r, o.y * r), pack_bf16x2(o.z * r, o.w * r));
+    if (lane == 0) store_lse<M>(p, row, m, l);
   };
-  const float* const recs = reinterpret_cast<const float*>(smem);
-  constexpr int kStep = kStages * kStageBytes / 4;  // floats from one warp's record to the next
-  for (int head = tid / kHeadDim; head < p.group; head += kSelHeads) {
-    float m, l, o;
-    merged(head, kSW, [&](int k, int i) { return recs[k * kStep + kOffM + i]; },
-           [&](int k, int i) { return recs[k * kStep + kOffL + i]; },
-           [&](int k, int i) { return recs[k * kStep + i * kHeadDim + col]; }, m, l, o);
+  float* const cta = reinterpret_cast<float*>(smem + kOffCtaRecord);
+  if (warp < p.group) {
+    // part k: warp k's record
+    auto rec = [&](int k) { return reinterpret_cast<const float*>(smem + k * kStages * kStageBytes); };
+    const int k = lane < kSW ? lane : 0;
+    float m, l;
+    float4 o;
+    merge(kSW, rec(k)[kOffM + warp], rec(k)[kOffL + warp],
+          [&](int i) { return reinterpret_cast<const float4*>(rec(i) + warp * kHeadDim)[lane]; }, m, l, o);
     if (splits == 1) {
-      put_out(head, m, l, o);
+      put_out(warp, m, l, o);
     } else {
-      cta[head * kHeadDim + col] = o;
-      if (col == 0) {
-        cta[kOffM + head] = m;
-        cta[kOffL + head] = l;
+      reinterpret_cast<float4*>(cta + warp * kHeadDim)[lane] = o;
+      if (lane == 0) {
+        cta[kOffM + warp] = m;
+        cta[kOffL + warp] = l;
       }
     }
   }
   if (splits > 1) {
+    __syncwarp();
     cluster_sync();
-    const uint32_t* const words = reinterpret_cast<const uint32_t*>(cta);
-    for (int head = rank + splits * (tid / kHeadDim); head < p.group; head += splits * kSelHeads) {
-      float m, l, o;
-      merged(head, splits, [&](int k, int i) { return __uint_as_float(ld_cluster(words + kOffM + i, k)); },
-             [&](int k, int i) { return __uint_as_float(ld_cluster(words + kOffL + i, k)); },
-             [&](int k, int i) { return __uint_as_float(ld_cluster(words + i * kHeadDim + col, k)); }, m, l, o);
+    // part k: CTA k's record; every splits-th head to a CTA
+    const int head = rank + splits * warp;
+    if (head < p.group) {
+      const int k = lane < splits ? lane : 0;
+      float m, l;
+      float4 o;
+      merge(splits, ld_cluster_f32(cta + kOffM + head, k), ld_cluster_f32(cta + kOffL + head, k),
+            [&](int i) { return ld_cluster_f32x4(cta + head * kHeadDim + 4 * lane, i); }, m, l, o);
       put_out(head, m, l, o);
     }
+    __syncwarp();
     cluster_sync();  // no CTA leaves while another may still read its record
   }
 }
@@ -2066,10 +2097,10 @@ cudaError_t launch_decode_selected(const nvfp4kv_cache& c, const uint16_t* q, ui
   p.lse = lse;
   p.selected = selected;
   p.budget = budget;
-  // as many CTAs per pair (up to the portable cluster) as one wave holds
+  // as many CTAs per pair (up to the largest cluster) as one wave holds
   const int64_t pairs = (int64_t)batch * p.hkv, slots = (int64_t)num_sms * kSelCtas;
   int splits = 1;
-  while (splits < 8 && pairs * (splits + 1) <= slots) ++splits;
+  while (splits < kMaxSplits && pairs * (splits + 1) <= slots) ++splits;
   // past one wave, or with more than 256 pages to a CTA (in proportion fewer where
   // SMs stay empty), the even cut over the whole device (both sides: selected_kernel)
   const int64_t ctas = pairs * splits, listed = budget < max_pages ? budget : max_pages;
