@@ -639,10 +639,11 @@ typedef struct nvfp4kv_norm_rope {
  *                 rotary_dim / 2 pairs' angles, then their sines
  *   how           host struct
  *   q_out         device bf16 [num_tokens][num_q_heads][head_dim] with q_out_stride; may
- *                 be q itself (with q_stride), and must not overlap q otherwise, nor k or v
+ *                 be q itself (with q_stride); else the memory from its first to its last row
+ *                 must not reach into that of q, and its rows must not overlap those of k or v
  *   ws_rows       device int64 [num_tokens], or NULL: no workspace (total_rows, the scales,
  *                 ws_k and ws_v are then not looked at)
- * num_tokens < 2^30, num_tokens * heads < 2^31.  Values up to 2^60 in size have exact norms.  Enqueues
+ * num_tokens < 2^30, heads <= 2^20, num_tokens * heads < 2^31.  Values up to 2^60 in size have exact norms.  Enqueues
  * one kernel. */
 int nvfp4kv_norm_rope_append(const nvfp4kv_cache* cache, const void* q, int64_t q_stride, const void* k,
                              int64_t k_stride, const void* v, int64_t v_stride, int32_t num_q_heads,
@@ -680,7 +681,8 @@ int nvfp4kv_page_digest(const nvfp4kv_cache* cache, const int32_t* page_table, i
  *                        of sum_d max(q_d hi_d, q_d lo_d)
  * which no token's softmax_scale * q . khat in the page exceeds (but for fp32's
  * rounding).  cache gives the pool's size and g_K; its pages are not read.
- *   q             device bf16 [batch][num_q_heads][head_dim], 16-byte aligned; G <= 8
+ *   q             device bf16 [batch][num_q_heads][head_dim], 16-byte aligned; G <= 8 (a
+ *                 NaN or an infinity in it leaves its KV head's scores undefined)
  *   scores        device fp32 [batch][num_kv_heads][score_stride]; entries behind a
  *                 sequence's last page are left alone.  A longer sequence's pages from
  *                 score_stride on get none, with NVFP4KV_DEVERR_LENGTH

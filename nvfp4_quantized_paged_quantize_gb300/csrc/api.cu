@@ -514,7 +514,7 @@ int nvfp4kv_norm_rope_append(const nvfp4kv_cache* cache, const void* q, int64_t 
   if (device_status && !aligned(device_status, 4)) return NVFP4KV_ERR_INVALID_ARGUMENT;
   if (num_tokens == 0) return NVFP4KV_OK;
   const int64_t most = int64_t(1) << 40;
-  if (num_tokens >= (int64_t(1) << 30) ||
+  if (num_q_heads > (1 << 20) || cache->num_kv_heads > (1 << 20) || num_tokens >= (int64_t(1) << 30) ||
       num_tokens >= (int64_t(1) << 31) / (num_q_heads > cache->num_kv_heads ? num_q_heads : cache->num_kv_heads) ||
       q_stride > most || q_out_stride > most || k_stride > most || v_stride > most || total_rows > most)
     return NVFP4KV_ERR_UNSUPPORTED;

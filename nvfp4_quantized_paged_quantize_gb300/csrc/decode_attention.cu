@@ -1581,13 +1581,15 @@ __global__ void __launch_bounds__(kCombineMaxWarps * 32) combine_kernel(const De
 // warp an eighth of that, with the ring and the phases of decode_kernel.  The warps'
 // results meet in shared memory and the CTAs' in that of the cluster (each CTA
 // finishes every splits-th head), so there are no records in global memory, no second
-// kernel and no scan over the batch: what is left of them is 7 us, beside some 11 of
-// decode_kernel and its combine.  Captured, 64 / 8 heads, here and there: 32 x 8193
-// tokens, 8 pages a head 7.5 and 11.3 us, 64 13.9 and 17.0, 256 34.4 and 36.3;
-// 4 x 131073 tokens, 1024 pages 22.6 and 23.4, 4096 61 and 59.  Past one wave the
-// even cut wins: 96 sequences, 64 pages 37.8 and 32.9.
-// (Cutting several pairs of a cluster evenly over its warps: 23.3 us for the second
-// of these; the merge of cut pairs is what cost.  4 warps and three CTAs an SM: 14.8.)
+// kernel and no scan over the batch: what is left of them is some 6 us, beside 11 of
+// decode_kernel and its combine, and the pages come at 5.7 TB/s and more.  Captured,
+// 64 / 8 heads, here and there: 32 x 8193 tokens, 8 pages a head 6.5 and 11.3 us, 64
+// 12.3 and 17.1, 256 32.6 and 35.8, 512 58.4 and 59.9; 37 x 8193, 512 58.9 and 66.5;
+// 4 x 131073, 1024 21.5 and 23.2, 4096 60.3 and 59.0.  Past one wave the even cut
+// wins (96 sequences, 64 pages 37.8 and 32.9), and where the clusters leave SMs empty
+// and lists are long: 1 x 131073, 1024 pages 14.6 and 15.7, 2048 23.5 and 20.8.
+// (Cutting several pairs of a cluster evenly over its warps, and 4 warps with three
+// CTAs an SM, were both a tenth slower; the merge of cut pairs is what cost the first.)
 constexpr int kSW = 8, kSelCtas = 2;  // warps of a CTA, CTAs of an SM
 constexpr int kSelRingBytes = kSW * kStages * kStageBytes, kSelSmemBytes = kSelRingBytes + kSW * kStages * 8;
 constexpr int kOffCtaRecord = kStages * kStageBytes / 2;  // in the first warp's ring, behind its own record
@@ -2101,10 +2103,10 @@ cudaError_t launch_decode_selected(const nvfp4kv_cache& c, const uint16_t* q, ui
   const int64_t pairs = (int64_t)batch * p.hkv, slots = (int64_t)num_sms * kSelCtas;
   int splits = 1;
   while (splits < kMaxSplits && pairs * (splits + 1) <= slots) ++splits;
-  // past one wave, or with more than 256 pages to a CTA (in proportion fewer where
+  // past one wave, or with more than 512 pages to a CTA (in proportion fewer where
   // SMs stay empty), the even cut over the whole device (both sides: selected_kernel)
   const int64_t ctas = pairs * splits, listed = budget < max_pages ? budget : max_pages;
-  if (ctas > slots || listed * num_sms > 256 * splits * (ctas < num_sms ? ctas : num_sms))
+  if (ctas > slots || listed * num_sms > 512 * splits * (ctas < num_sms ? ctas : num_sms))
     return enqueue_scored<kScored | kSelected>(p, stream);
   static PerDeviceOnce attr_once;
   const cudaError_t e = attr_once.run([] {

@@ -96,6 +96,8 @@ def test_norm_rope_refusals(lib):
     assert some(a14=16) == INVALID                                             # in place, with another stride
     assert some(a14=16 + 2 * 1024) == INVALID                                  # across the next token's
     assert some(a1=1 << 20, a14=(1 << 20) - 16) == INVALID
+    wide = ((1 << 20) + 4) * 128
+    assert some(a7=(1 << 20) + 4, a8=1, a2=wide, a15=wide) == UNSUPPORTED      # more heads than offsets in a token count
 
 
 def test_digest_and_score_refusals(lib):
