@@ -48,28 +48,35 @@ __device__ __forceinline__ BlockScale block_scale(float amax, const GlobalScale&
   return b;
 }
 
-// The codes of eight of the block's values, value i in nibble i.
-__device__ __forceinline__ uint32_t block_codes8(const float* f, const BlockScale& b) {
-  uint32_t c = 0;
+// The codes of 8 kWords of the block's values, value i in nibble i % 8 of word i / 8.
+template <int kWords>
+__device__ __forceinline__ void block_codes(const float* f, const BlockScale& b, uint32_t (&c)[kWords]) {
   if (b.den == 0.0f) {
     // signed zeros: code 8 for negative inputs
 #pragma unroll
-    for (int i = 0; i < 8; ++i) c |= (__float_as_uint(f[i]) >> 31) << (4 * i + 3);
-    return c;
+    for (int w = 0; w < kWords; ++w) {
+      c[w] = 0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) c[w] |= (__float_as_uint(f[8 * w + i]) >> 31) << (4 * i + 3);
+    }
+    return;
   }
-  float y[8];
+  float y[8 * kWords];
   if (b.fast) {
     // a quotient that rounds to zero can come out as +0 for negative x;
     // the sign of x / den is the sign of x (den > 0)
 #pragma unroll
-    for (int i = 0; i < 8; ++i) y[i] = copysignf(div_markstein(f[i], b.den, b.rcp), f[i]);
+    for (int i = 0; i < 8 * kWords; ++i) y[i] = copysignf(div_markstein(f[i], b.den, b.rcp), f[i]);
   } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) y[i] = __fdiv_rn(f[i], b.den);
+    for (int i = 0; i < 8 * kWords; ++i) y[i] = __fdiv_rn(f[i], b.den);
   }
 #pragma unroll
-  for (int k = 0; k < 4; ++k) c |= e2m1x2_from_f32(y[2 * k], y[2 * k + 1]) << (8 * k);
-  return c;
+  for (int w = 0; w < kWords; ++w) {
+    c[w] = 0;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) c[w] |= e2m1x2_from_f32(y[8 * w + 2 * k], y[8 * w + 2 * k + 1]) << (8 * k);
+  }
 }
 
 struct BlockCodes {
@@ -82,7 +89,9 @@ __device__ __forceinline__ BlockCodes quantize_block(const float (&f)[16], const
 #pragma unroll
   for (int i = 0; i < 16; ++i) amax = fmaxf(amax, fabsf(f[i]));
   const BlockScale b = block_scale(amax, s);
-  return BlockCodes{block_codes8(f, b), block_codes8(f + 8, b), b.sb};
+  uint32_t c[2];
+  block_codes(f, b, c);
+  return BlockCodes{c[0], c[1], b.sb};
 }
 
 // Eight packed bf16 (16 bytes) -> fp32.
