@@ -322,6 +322,22 @@ def _check_tensor(name: str, x, dtype, shape, gpu: int) -> None:
     raise ValueError(f"{name}: expected a contiguous {dtype} GPU tensor of shape {shape}{where}, got {what}")
 
 
+def _checked(name: str, x, dtype, shape, gpu: int) -> int:
+    """The address of x, after _check_tensor."""
+    if x is not None and x.dtype is dtype and x.get_device() == gpu and x.shape == shape and x.is_contiguous():
+        return x.data_ptr()
+    _check_tensor(name, x, dtype, shape, gpu)
+    return x.data_ptr()
+
+
+def _checked_memory(name: str, x, gpu: int) -> int | None:
+    """The address of x, a tensor on this GPU, an address or None; raises ValueError."""
+    if x is None:
+        return None
+    _check_memory(name, x, gpu)
+    return _ptr(x)
+
+
 def _check_memory(name: str, x, gpu: int) -> None:
     """x, where it is a tensor and not an address, lies on this GPU; raises ValueError."""
     if hasattr(x, "get_device") and x.get_device() != gpu:
@@ -483,44 +499,38 @@ def nvfp4kv_plan_append(page_table, cached_lens, new_lens, free_pages, free_coun
     [tokens]), ws_rows (int64 [tokens]), cu_q and cu_prefix (int64 [B + 1]).  free_count and free_left: int32 [1],
     may be one tensor."""
     t = _types()
+    i32, i64 = t.int32, t.int64
     B, maxp = _shape("page_table", page_table, 2)
     tokens, capacity = _shape("slot_mapping", slot_mapping, 1)[0], _shape("free_pages", free_pages, 1)[0]
     gpu = _current_gpu(page_table)
-    _check_tensor("page_table", page_table, t.int32, (B, maxp), gpu)
-    _check_tensor("cached_lens", cached_lens, t.int32, (B,), gpu)
-    _check_tensor("new_lens", new_lens, t.int32, (B,), gpu)
-    _check_tensor("free_pages", free_pages, t.int32, (capacity,), gpu)
-    _check_tensor("free_count", free_count, t.int32, (1,), gpu)
-    _check_tensor("seq_lens", seq_lens, t.int32, (B,), gpu)
-    _check_tensor("slot_mapping", slot_mapping, t.int64, (tokens,), gpu)
-    _check_tensor("free_left", free_left, t.int32, (1,), gpu)
-    if positions is not None:
-        _check_tensor("positions", positions, t.int32, (tokens,), gpu)
-    if cu_q is not None:
-        _check_tensor("cu_q", cu_q, t.int64, (B + 1,), gpu)
-    if ws_rows is not None:
-        _check_tensor("ws_rows", ws_rows, t.int64, (tokens,), gpu)
-    if cu_prefix is not None:
-        _check_tensor("cu_prefix", cu_prefix, t.int64, (B + 1,), gpu)
-    _check_memory("device_status", device_status, gpu)
+    requests, words, sums = (B,), (1,), (B + 1,)
     _check("nvfp4kv_plan_append",
-           _L().nvfp4kv_plan_append(_ptr(page_table), maxp, _ptr(cached_lens), _ptr(new_lens), B, _ptr(free_pages),
-                                    capacity, _ptr(free_count), int(num_pages), tokens, _ptr(seq_lens),
-                                    _ptr(slot_mapping), _ptr(positions), _ptr(cu_q), _ptr(ws_rows), _ptr(cu_prefix),
-                                    _ptr(free_left), _ptr(device_status), _stream(stream)))
+           _L().nvfp4kv_plan_append(
+               _checked("page_table", page_table, i32, (B, maxp), gpu), maxp,
+               _checked("cached_lens", cached_lens, i32, requests, gpu),
+               _checked("new_lens", new_lens, i32, requests, gpu), B,
+               _checked("free_pages", free_pages, i32, (capacity,), gpu), capacity,
+               _checked("free_count", free_count, i32, words, gpu), int(num_pages), tokens,
+               _checked("seq_lens", seq_lens, i32, requests, gpu),
+               _checked("slot_mapping", slot_mapping, i64, (tokens,), gpu),
+               None if positions is None else _checked("positions", positions, i32, (tokens,), gpu),
+               None if cu_q is None else _checked("cu_q", cu_q, i64, sums, gpu),
+               None if ws_rows is None else _checked("ws_rows", ws_rows, i64, (tokens,), gpu),
+               None if cu_prefix is None else _checked("cu_prefix", cu_prefix, i64, sums, gpu),
+               _checked("free_left", free_left, i32, words, gpu),
+               _checked_memory("device_status", device_status, gpu), _stream(stream)))
 
 
-def _token_stride(name: str, x, tokens: int, heads: int, gpu: int) -> int:
-    """Elements from one token of x (bf16 [tokens, heads, 128] on this GPU, a token's heads contiguous) to the next;
-    raises ValueError."""
-    shape = (tokens, heads, HEAD_DIM)
-    if x is None or x.dtype is not _types().bfloat16 or x.get_device() != gpu or x.shape != shape:
+def _token_rows(name: str, x, dtype, shape, gpu: int):
+    """The address of x (tokens of heads of 128 values on this GPU, a token's heads contiguous) and the elements from
+    one token to the next; raises ValueError."""
+    if x is None or x.dtype is not dtype or x.get_device() != gpu or x.shape != shape:
         what = "None" if x is None else f"{x.dtype} {tuple(x.shape)} on {x.device}"
-        raise ValueError(f"{name}: expected a bfloat16 tensor of shape {shape} on the current device, got {what}")
+        raise ValueError(f"{name}: expected a {dtype} tensor of shape {shape} on the current device, got {what}")
     token, head, value = x.stride()
-    if value != 1 or (head != HEAD_DIM and heads > 1):
+    if value != 1 or (head != HEAD_DIM and shape[1] > 1):
         raise ValueError(f"{name}: a token's heads are contiguous rows, got strides {x.stride()}")
-    return token if tokens > 1 else heads * HEAD_DIM
+    return x.data_ptr(), token if shape[0] > 1 else shape[1] * HEAD_DIM
 
 
 def nvfp4kv_norm_rope_append(cache: "Cache", q, k, v, slot_mapping, positions, cos_sin, q_out, q_weight=None,
@@ -534,64 +544,63 @@ def nvfp4kv_norm_rope_append(cache: "Cache", q, k, v, slot_mapping, positions, c
     if cache.mxfp4:
         raise ValueError("the cache holds MXFP4 page-heads; this append writes NVFP4 ones")
     t = _types()
+    bf16 = t.bfloat16
     n, hq, _ = _shape("q", q, 3)
     gpu, hkv = _current_gpu(q), cache.num_kv_heads
-    q_stride, out_stride = _token_stride("q", q, n, hq, gpu), _token_stride("q_out", q_out, n, hq, gpu)
-    k_stride, v_stride = _token_stride("k", k, n, hkv, gpu), _token_stride("v", v, n, hkv, gpu)
-    _check_tensor("slot_mapping", slot_mapping, t.int64, (n,), gpu)
-    max_position, rot = (0, 0) if cos_sin is None else _shape("cos_sin", cos_sin, 2)
+    queries, keys = (n, hq, HEAD_DIM), (n, hkv, HEAD_DIM)
+    q_at, q_stride = _token_rows("q", q, bf16, queries, gpu)
+    k_at, k_stride = _token_rows("k", k, bf16, keys, gpu)
+    v_at, v_stride = _token_rows("v", v, bf16, keys, gpu)
+    out_at, out_stride = _token_rows("q_out", q_out, bf16, queries, gpu)
+    slots_at = _checked("slot_mapping", slot_mapping, t.int64, (n,), gpu)
+    max_position, rot, turns_at, positions_at = 0, 0, None, None
     if cos_sin is not None:
-        _check_tensor("cos_sin", cos_sin, t.float32, (max_position, rot), gpu)
-        _check_tensor("positions", positions, t.int32, (n,), gpu)
-    if q_weight is not None:
-        _check_tensor("q_weight", q_weight, t.bfloat16, (HEAD_DIM,), gpu)
-    if k_weight is not None:
-        _check_tensor("k_weight", k_weight, t.bfloat16, (HEAD_DIM,), gpu)
-    rows = 0
+        max_position, rot = _shape("cos_sin", cos_sin, 2)
+        turns_at = _checked("cos_sin", cos_sin, t.float32, (max_position, rot), gpu)
+        positions_at = _checked("positions", positions, t.int32, (n,), gpu)
+    weights = (HEAD_DIM,)
+    how = _CNormRope(None if q_weight is None else _checked("q_weight", q_weight, bf16, weights, gpu),
+                     None if k_weight is None else _checked("k_weight", k_weight, bf16, weights, gpu),
+                     eps, rot, 1 if interleaved else 0)
+    rows, rows_at, ws_k_at, ws_v_at = 0, None, None, None
     if ws_rows is not None:
         rows = _shape("ws_k", ws_k, 3)[0]
-        _check_tensor("ws_rows", ws_rows, t.int64, (n,), gpu)
-        _check_tensor("ws_k", ws_k, t.uint8, (rows, hkv, HEAD_DIM), gpu)
-        _check_tensor("ws_v", ws_v, t.uint8, (rows, hkv, HEAD_DIM), gpu)
+        rows_at = _checked("ws_rows", ws_rows, t.int64, (n,), gpu)
+        ws_k_at = _checked("ws_k", ws_k, t.uint8, (rows, hkv, HEAD_DIM), gpu)
+        ws_v_at = _checked("ws_v", ws_v, t.uint8, (rows, hkv, HEAD_DIM), gpu)
     _check_memory("cache.pages", cache.pages, gpu)
-    _check_memory("device_status", device_status, gpu)
-    c = cache.c_struct()
-    how = _CNormRope(_ptr(q_weight), _ptr(k_weight), float(eps), rot, int(bool(interleaved)))
     _check("nvfp4kv_norm_rope_append",
-           _L().nvfp4kv_norm_rope_append(ctypes.byref(c), _ptr(q), q_stride, _ptr(k), k_stride, _ptr(v), v_stride,
-                                         hq, n, _ptr(slot_mapping),
-                                         None if cos_sin is None else _ptr(positions), _ptr(cos_sin), max_position,
-                                         ctypes.byref(how), _ptr(q_out), out_stride, _ptr(ws_rows), rows,
-                                         float(k_ws_scale), float(v_ws_scale), _ptr(ws_k), _ptr(ws_v),
-                                         _ptr(device_status), _stream(stream)))
+           _L().nvfp4kv_norm_rope_append(cache.c_struct(), q_at, q_stride, k_at, k_stride, v_at, v_stride, hq, n,
+                                         slots_at, positions_at, turns_at, max_position, how, out_at, out_stride,
+                                         rows_at, rows, k_ws_scale, v_ws_scale, ws_k_at, ws_v_at,
+                                         _checked_memory("device_status", device_status, gpu), _stream(stream)))
 
 
 def _check_digest(cache: "Cache", digest, page_table, seq_lens, device_status):
-    """Checks a digest's tensors; returns (batch, page-table columns, the current device)."""
+    """Checks a digest's tensors; returns (batch, page-table columns, the current device, the addresses of digest, page
+    table, lengths and status)."""
     if cache.mxfp4:
         raise ValueError("the cache holds MXFP4 page-heads; a digest is made of NVFP4 ones")
     t = _types()
     B, maxp = _shape("page_table", page_table, 2)
     gpu = _current_gpu(page_table)
-    _check_tensor("page_table", page_table, t.int32, (B, maxp), gpu)
-    _check_tensor("seq_lens", seq_lens, t.int32, (B,), gpu)
-    _check_tensor("digest", digest, t.uint8, (cache.num_pages, cache.num_kv_heads, NVFP4KV_DIGEST_BYTES), gpu)
+    table_at = _checked("page_table", page_table, t.int32, (B, maxp), gpu)
+    lens_at = _checked("seq_lens", seq_lens, t.int32, (B,), gpu)
+    digest_at = _checked("digest", digest, t.uint8, (cache.num_pages, cache.num_kv_heads, NVFP4KV_DIGEST_BYTES), gpu)
     _check_memory("cache.pages", cache.pages, gpu)
-    _check_memory("device_status", device_status, gpu)
-    return B, maxp, gpu
+    return B, maxp, gpu, digest_at, table_at, lens_at, _checked_memory("device_status", device_status, gpu)
 
 
 def nvfp4kv_page_digest(cache: "Cache", page_table, seq_lens, digest, first_tokens=None, device_status=None,
                         stream=None) -> None:
     """Bounds of the pages' keys (digest: uint8 [num_pages, Hkv, 272], by page id): of each sequence's pages from
     token first_tokens[b] on (int32 [B]; None: all of them)."""
-    B, maxp, gpu = _check_digest(cache, digest, page_table, seq_lens, device_status)
-    if first_tokens is not None:
-        _check_tensor("first_tokens", first_tokens, _types().int32, (B,), gpu)
-    c = cache.c_struct()
+    B, maxp, gpu, digest_at, table_at, lens_at, status_at = _check_digest(cache, digest, page_table, seq_lens,
+                                                                          device_status)
+    first_at = None if first_tokens is None else _checked("first_tokens", first_tokens, _types().int32, (B,), gpu)
     _check("nvfp4kv_page_digest",
-           _L().nvfp4kv_page_digest(ctypes.byref(c), _ptr(page_table), maxp, _ptr(seq_lens), _ptr(first_tokens), B,
-                                    _ptr(digest), _ptr(device_status), _stream(stream)))
+           _L().nvfp4kv_page_digest(cache.c_struct(), table_at, maxp, lens_at, first_at, B, digest_at, status_at,
+                                    _stream(stream)))
 
 
 def nvfp4kv_page_scores(cache: "Cache", digest, q, page_table, seq_lens, softmax_scale: float, scores,
@@ -599,15 +608,14 @@ def nvfp4kv_page_scores(cache: "Cache", digest, q, page_table, seq_lens, softmax
     """An upper bound of every page's scores (scores: fp32 [B, Hkv, >= pages]) for the queries q (bf16 [B, Hq, 128]),
     from the pages' digests."""
     t = _types()
-    B, maxp, gpu = _check_digest(cache, digest, page_table, seq_lens, device_status)
+    B, maxp, gpu, digest_at, table_at, lens_at, status_at = _check_digest(cache, digest, page_table, seq_lens,
+                                                                          device_status)
     hq, stride = _shape("q", q, 3)[1], _shape("scores", scores, 3)[2]
-    _check_tensor("q", q, t.bfloat16, (B, hq, HEAD_DIM), gpu)
-    _check_tensor("scores", scores, t.float32, (B, cache.num_kv_heads, stride), gpu)
-    c = cache.c_struct()
+    q_at = _checked("q", q, t.bfloat16, (B, hq, HEAD_DIM), gpu)
+    scores_at = _checked("scores", scores, t.float32, (B, cache.num_kv_heads, stride), gpu)
     _check("nvfp4kv_page_scores",
-           _L().nvfp4kv_page_scores(ctypes.byref(c), _ptr(digest), _ptr(q), _ptr(page_table), maxp, _ptr(seq_lens), B,
-                                    hq, float(softmax_scale), _ptr(scores), stride, _ptr(device_status),
-                                    _stream(stream)))
+           _L().nvfp4kv_page_scores(cache.c_struct(), digest_at, q_at, table_at, maxp, lens_at, B, hq,
+                                    float(softmax_scale), scores_at, stride, status_at, _stream(stream)))
 
 
 def nvfp4kv_select_pages(scores, seq_lens, budget: int, first: int, recent: int, selected, device_status=None,
@@ -617,13 +625,11 @@ def nvfp4kv_select_pages(scores, seq_lens, budget: int, first: int, recent: int,
     t = _types()
     B, hkv, stride = _shape("scores", scores, 3)
     gpu = _current_gpu(scores)
-    _check_tensor("scores", scores, t.float32, (B, hkv, stride), gpu)
-    _check_tensor("seq_lens", seq_lens, t.int32, (B,), gpu)
-    _check_tensor("selected", selected, t.int32, (B, hkv, budget), gpu)
-    _check_memory("device_status", device_status, gpu)
     _check("nvfp4kv_select_pages",
-           _L().nvfp4kv_select_pages(_ptr(scores), stride, _ptr(seq_lens), B, hkv, budget, first, recent,
-                                     _ptr(selected), _ptr(device_status), _stream(stream)))
+           _L().nvfp4kv_select_pages(_checked("scores", scores, t.float32, (B, hkv, stride), gpu), stride,
+                                     _checked("seq_lens", seq_lens, t.int32, (B,), gpu), B, hkv, budget, first, recent,
+                                     _checked("selected", selected, t.int32, (B, hkv, budget), gpu),
+                                     _checked_memory("device_status", device_status, gpu), _stream(stream)))
 
 
 def nvfp4kv_decode_attention_selected(cache: "Cache", q, out, page_table, seq_lens, softmax_scale: float, selected,

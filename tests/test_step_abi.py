@@ -159,6 +159,9 @@ class OnGpu:
     def get_device(self):
         return self.gpu
 
+    def data_ptr(self):
+        return 0  # none: the library refuses it
+
 
 def _calls(cache, **kw):
     """Every binding of this kind as (function, tensors, the rest)."""
