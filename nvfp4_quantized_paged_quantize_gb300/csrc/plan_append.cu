@@ -187,10 +187,12 @@ __global__ void __launch_bounds__(kThreads) plan_kernel(const PlanArgs p, int ct
 }  // namespace
 
 cudaError_t launch_plan_append(const PlanArgs& args, cudaStream_t stream) {
-  // few requests: small blocks, whose barriers cost less
+  // few requests: small blocks, whose barriers cost less (256 requests of one token 3.3 us, with
+  // 1024 threads 3.9; 300 in two rounds 5.0 and 4.1)
   const bool small = args.batch <= 256;
   const int threads = small ? 256 : 1024;
   const bool in_place = args.seq_lens == args.cached_lens || args.free_left == args.free_count;
+  // (16 requests of up to 2048 tokens over 128 blocks 3.4 us, over 8 9.3)
   const int64_t want = (args.max_tokens + threads - 1) / threads, most = in_place ? kPlanMaxCluster : 128;
   const int ctas = (int)(want < 1 ? 1 : want < most ? want : most);
   cudaLaunchConfig_t cfg = {};
