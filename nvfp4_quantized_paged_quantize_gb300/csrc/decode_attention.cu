@@ -151,8 +151,10 @@ struct DecodeParams {
 // small helpers
 // ---------------------------------------------------------------------------
 
+// (kFresh: from a kernel that overlaps the one ahead of it; see after_earlier_kernels)
+template <bool kFresh = false>
 __device__ __forceinline__ int clamp_len(const DecodeParams& p, int b) {
-  int L = __ldg(p.seq_lens + b);
+  int L = kFresh ? p.seq_lens[b] : __ldg(p.seq_lens + b);
   const int lmax = p.max_pages * kPage;
   if (L < 0 || L > lmax) {
     flag_error(p.status, NVFP4KV_DEVERR_LENGTH);
@@ -575,12 +577,13 @@ struct QRaw {
   uint4 w[4];
 };
 
+template <bool kFresh = false>
 __device__ __forceinline__ QRaw fetch_q(const DecodeParams& p, int pair, int g, int t) {
   QRaw r;
   if (g < p.group) {
     const uint4* src = reinterpret_cast<const uint4*>(p.q + ((long long)pair * p.group + g) * kHeadDim + 32 * t);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) r.w[j] = __ldg(src + j);
+    for (int j = 0; j < 4; ++j) r.w[j] = kFresh ? src[j] : __ldg(src + j);
   } else {
 #pragma unroll
     for (int j = 0; j < 4; ++j) r.w[j] = make_uint4(0u, 0u, 0u, 0u);
@@ -1617,7 +1620,8 @@ __global__ void __launch_bounds__(kSW * 32, kSelCtas) selected_kernel(const Deco
   const int g = lane >> 2, t = lane & 3;
   const int pair = blockIdx.x / splits, rank = blockIdx.x - pair * splits;
   const int b = pair / p.hkv, h = pair - b * p.hkv;
-  const QRaw q = fetch_q(p, pair, g, t);
+  after_earlier_kernels();
+  const QRaw q = fetch_q<true>(p, pair, g, t);
   // the warp's part [w0, w0 + n) of a list of `listed` entries
   int w0, n;
   auto part = [&](int listed) {
@@ -1627,12 +1631,12 @@ __global__ void __launch_bounds__(kSW * 32, kSelCtas) selected_kernel(const Deco
   };
   // the lane's entry of the part's 32-entry chunk k
   const int32_t* const list = p.selected + (long long)pair * p.budget;
-  auto entry = [&](int k) { return 32 * k + lane < n ? __ldg(list + w0 + 32 * k + lane) : -1; };
+  auto entry = [&](int k) { return 32 * k + lane < n ? list[w0 + 32 * k + lane] : -1; };
   // the first entries are read before the length is there, as if the list were full
   const int full = min(p.max_pages, p.budget);
   part(full);
   int sel0 = entry(0);
-  const int L = clamp_len(p, b), pages = (L + kPage - 1) / kPage, listed = min(pages, p.budget);
+  const int L = clamp_len<true>(p, b), pages = (L + kPage - 1) / kPage, listed = min(pages, p.budget);
   if (listed != full) {
     part(listed);
     sel0 = entry(0);
@@ -1646,7 +1650,7 @@ __global__ void __launch_bounds__(kSW * 32, kSelCtas) selected_kernel(const Deco
   // an entry's page id, and what the loop uses of it
   auto page_id = [&](int sel) {
     if (sel >= pages) flag_error(p.status, NVFP4KV_DEVERR_PAGE);
-    return sel >= 0 && sel < pages ? __ldg(table + sel) : -1;
+    return sel >= 0 && sel < pages ? table[sel] : -1;
   };
   auto put = [&](int k, int sel, int id) {
     const bool named = sel >= 0 && sel < pages, valid = named && id >= 0 && id < p.num_pages;
@@ -2113,18 +2117,7 @@ cudaError_t launch_decode_selected(const nvfp4kv_cache& c, const uint16_t* q, ui
     return cudaFuncSetAttribute(selected_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSelSmemBytes);
   });
   if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)ctas);
-  cfg.blockDim = dim3(kSW * 32);
-  cfg.dynamicSmemBytes = kSelSmemBytes;
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = splits;
-  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, selected_kernel, p, splits);
+  return launch_overlapped(selected_kernel, ctas, kSW * 32, kSelSmemBytes, splits, stream, p, splits);
 }
 
 cudaError_t launch_decode(const nvfp4kv_cache& c, const uint16_t* q, float* out, const int32_t* page_table,

@@ -129,13 +129,13 @@ struct Turn {
 };
 
 __device__ __forceinline__ void load4x2(const float* src, float2 (&d)[4]) {
-  const float4 a = __ldg(reinterpret_cast<const float4*>(src)), b = __ldg(reinterpret_cast<const float4*>(src) + 1);
+  const float4 a = *reinterpret_cast<const float4*>(src), b = reinterpret_cast<const float4*>(src)[1];
   d[0] = make_float2(a.x, a.y), d[1] = make_float2(a.z, a.w), d[2] = make_float2(b.x, b.y), d[3] = make_float2(b.z, b.w);
 }
 
 template <int R>
 __device__ __forceinline__ void load_turn(const NormRopeArgs& p, int token, int sub, Turn& t) {
-  const int pos = __ldg(p.positions + token);
+  const int pos = p.positions[token];
   const bool good = pos >= 0 && pos < p.max_position;
   if (!good) flag_error(p.status, NVFP4KV_DEVERR_POSITION);
   const int half = p.rot >> 1;
@@ -146,8 +146,8 @@ __device__ __forceinline__ void load_turn(const NormRopeArgs& p, int token, int 
     t.on[h] = good && d < p.rot;
     if (!t.on[h]) continue;
     if constexpr (R == kInterleaved) {
-      const float4 c = __ldg(reinterpret_cast<const float4*>(row + d / 2));
-      const float4 s = __ldg(reinterpret_cast<const float4*>(row + half + d / 2));
+      const float4 c = *reinterpret_cast<const float4*>(row + d / 2);
+      const float4 s = *reinterpret_cast<const float4*>(row + half + d / 2);
       const float cs[4] = {c.x, c.y, c.z, c.w}, sn[4] = {s.x, s.y, s.z, s.w};
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -178,7 +178,7 @@ __device__ __forceinline__ void load_weights(const NormRopeArgs& a, Weights& w) 
     const uint16_t* src = keys ? a.k_weight : a.q_weight;
     float4 v = make_float4(1.0f, 1.0f, 1.0f, 1.0f);
     if (src) {
-      const uint2 x = __ldg(reinterpret_cast<const uint2*>(src + 64 * h + 8 * s + 4 * half));
+      const uint2 x = *reinterpret_cast<const uint2*>(src + 64 * h + 8 * s + 4 * half);
       const float2 lo = unpack2(x.x), hi = unpack2(x.y);
       v = make_float4(lo.x, lo.y, hi.x, hi.y);
     }
@@ -358,8 +358,8 @@ __device__ __forceinline__ void turn_rows(const NormRopeParams& p, Steps st, uin
   for (int step = st.begin; step < st.end; ++step) {
     fetch(stage == 0 ? kStages - 1 : stage - 1);
     if (!entered) {
-      slot = __ldg(a.slots + token);
-      if (a.ws_rows) ws_row = __ldg(a.ws_rows + token);
+      slot = a.slots[token];
+      if (a.ws_rows) ws_row = a.ws_rows[token];
       if constexpr (R != kNone) load_turn<R>(a, token, sub, turn);
       dst = a.q_out + token * a.q_out_stride + (4 * j + group) * kHeadDim + 8 * sub;
       entered = true;
@@ -437,9 +437,9 @@ __device__ __forceinline__ void value_rows(const NormRopeParams& p, Steps st, ui
       j = 0;
       ++pair;
     }
-    const long long slot = live ? __ldg(a.slots + tok) : -1;
-    const long long mate = live && (tok ^ 1) < a.ntok ? __ldg(a.slots + (tok ^ 1)) : -1;
-    const long long ws_row = live && a.ws_rows ? __ldg(a.ws_rows + tok) : -1;
+    const long long slot = live ? a.slots[tok] : -1;
+    const long long mate = live && (tok ^ 1) < a.ntok ? a.slots[tok ^ 1] : -1;
+    const long long ws_row = live && a.ws_rows ? a.ws_rows[tok] : -1;
     uint32_t y[8];
     take_row(ring + stage * kStageBytes + 16 * lane, y);
     stage = stage + 1 == kStages ? 0 : stage + 1;
@@ -469,6 +469,7 @@ template <int R>
 __global__ void __launch_bounds__(kNrThreads, ctas_per_sm(R)) norm_rope_kernel(const NormRopeParams p) {
   __shared__ __align__(128) uint8_t rings[kNrWarps][kStages * kStageBytes];
   __shared__ Weights weights;
+  after_earlier_kernels();
   load_weights(p.a, weights);
   __syncthreads();
   // (broadcast: the compiler then keeps what follows from it in uniform registers)
@@ -482,8 +483,7 @@ template <int R>
 cudaError_t launch(const NormRopeParams& p, int num_sms, cudaStream_t stream) {
   const int64_t steps = (int64_t)p.t_all + p.v_all, fit = (int64_t)num_sms * ctas_per_sm(R);
   const int64_t need = (steps + kNrWarps - 1) / kNrWarps;
-  norm_rope_kernel<R><<<(unsigned)(need < fit ? need : fit), kNrThreads, 0, stream>>>(p);
-  return cudaGetLastError();
+  return launch_overlapped(norm_rope_kernel<R>, need < fit ? need : fit, kNrThreads, 0, 1, stream, p);
 }
 
 }  // namespace

@@ -261,6 +261,11 @@ __device__ __forceinline__ uint32_t ld_cluster(const uint32_t* local, uint32_t r
   return v;
 }
 
+// First in a kernel of launch_overlapped: the kernels ahead on the stream have ended, and
+// what they wrote is visible to plain loads (not to __ldg, which takes its memory for
+// constant from the kernel's start).
+__device__ __forceinline__ void after_earlier_kernels() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 __device__ __forceinline__ void flag_error(int32_t* status, int bit) {
   if (status != nullptr) atomicOr(status, bit);
 }

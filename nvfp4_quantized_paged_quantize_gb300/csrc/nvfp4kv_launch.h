@@ -40,6 +40,31 @@ class PerDeviceOnce {
   std::mutex mu_;
 };
 
+// Launches a kernel, in clusters of `cluster` blocks, whose blocks may take the places of
+// those of the kernel ahead of it on the stream as these leave (a programmatic dependent; the
+// kernel itself waits for that one's end: after_earlier_kernels).  Calls in a row, with it
+// and without: page scores 10.6 and 12.3 us, selection 7.0 and 9.0, selected decode 12.2
+// and 14.3.  (With the next kernel's blocks let in from the start, they take the free
+// places of some SMs and then run there unevenly: 11.4, 7.4 and 12.6.)
+template <class... Params, class... Args>
+cudaError_t launch_overlapped(void (*kernel)(Params...), int64_t blocks, int threads, size_t smem, int cluster,
+                              cudaStream_t stream, const Args&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)blocks);
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cluster;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 cudaError_t launch_quantize_append(const nvfp4kv_cache& c, const uint16_t* k, const uint16_t* v,
                                    const int64_t* slot_mapping, int64_t num_tokens,
                                    int32_t* device_status, int num_sms, cudaStream_t stream);

@@ -28,7 +28,7 @@ static_assert(kDigestBytes == kOffScale + 16, "a digest's tail keeps the next on
 
 // A sequence's tokens, cut to what the page table covers (flagged on request).
 __device__ __forceinline__ int seq_tokens(const DigestArgs& p, int b, bool flag) {
-  int L = __ldg(p.seq_lens + b);
+  int L = p.seq_lens[b];
   const int lmax = p.max_pages * kPage;
   if (L < 0 || L > lmax) {
     if (flag) flag_error(p.status, NVFP4KV_DEVERR_LENGTH);
@@ -247,7 +247,8 @@ __global__ void __launch_bounds__(kDgThreads, kDigestCtasPerSm) digest_kernel(co
   __shared__ ShareShared s;
   __shared__ __align__(128) uint8_t rings[kDgWarps][kDgStages * kDgStageBytes];
   const int lane = threadIdx.x & 31;
-  auto from_page = [&](int b) { return p.first_tokens ? max(__ldg(p.first_tokens + b), 0) / kPage : 0; };
+  after_earlier_kernels();
+  auto from_page = [&](int b) { return p.first_tokens ? max(p.first_tokens[b], 0) / kPage : 0; };
   const Share w = split(s, p.batch, kDgWarps, (int)(threadIdx.x >> 5), [&](int b) {
     const int L = seq_tokens(p, b, blockIdx.x == 0);
     return max((L + kPage - 1) / kPage - from_page(b), 0) * p.hkv;
@@ -276,7 +277,7 @@ __global__ void __launch_bounds__(kDgThreads, kDigestCtasPerSm) digest_kernel(co
       end = (L + kPage - 1) / kPage;
     }
     if (!known) {
-      id = __ldg(p.page_table + (long long)b * p.max_pages + page);
+      id = p.page_table[(long long)b * p.max_pages + page];
       if (id < 0 || id >= p.num_pages) {
         if (lane == 0) flag_error(p.status, NVFP4KV_DEVERR_PAGE);
         id = -1;
@@ -351,7 +352,7 @@ __device__ __forceinline__ void load_queries(const ScoreArgs& p, int pair, int l
     const uint4* src = reinterpret_cast<const uint4*>(p.q + ((long long)pair * p.group + g) * kHeadDim);
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const uint4 w = __ldg(src + 8 * (j >> 1) + 2 * t + (j & 1));
+      const uint4 w = src[8 * (j >> 1) + 2 * t + (j & 1)];
       v[8 * j + 0] = bf16_to_f32(w.x & 0xFFFFu); v[8 * j + 1] = bf16_to_f32(w.x >> 16);
       v[8 * j + 2] = bf16_to_f32(w.y & 0xFFFFu); v[8 * j + 3] = bf16_to_f32(w.y >> 16);
       v[8 * j + 4] = bf16_to_f32(w.z & 0xFFFFu); v[8 * j + 5] = bf16_to_f32(w.z >> 16);
@@ -429,6 +430,7 @@ __global__ void __launch_bounds__(kDgThreads, kScoreCtasPerSm) scores_kernel(con
     for (int i = 0; i < kScStages; ++i) mbar_init(bar + 8 * i, copiers);
     fence_mbar_init();
   }
+  after_earlier_kernels();
   auto pages_of = [&](int b, bool flag) {
     int n = (seq_tokens(d, b, flag) + kPage - 1) / kPage;
     if (n > p.score_stride) {
@@ -475,7 +477,7 @@ __global__ void __launch_bounds__(kDgThreads, kScoreCtasPerSm) scores_kernel(con
       x.item = true;
       x.head = ahead.round * k.together;
       x.page = tid < k.pages && page < ahead.pages;
-      if (x.page) x.id = __ldg(d.page_table + (long long)ahead.b * d.max_pages + page);
+      if (x.page) x.id = d.page_table[(long long)ahead.b * d.max_pages + page];
       --to_read;
       advance(ahead);
     }
@@ -564,8 +566,7 @@ __global__ void __launch_bounds__(kDgThreads, kScoreCtasPerSm) scores_kernel(con
 cudaError_t launch_page_digest(const DigestArgs& args, int num_sms, cudaStream_t stream) {
   const int64_t need = ((int64_t)args.batch * args.max_pages * args.hkv + kDgWarps - 1) / kDgWarps;
   const int64_t fit = (int64_t)num_sms * kDigestCtasPerSm;
-  digest_kernel<<<(unsigned)(need < fit ? need : fit), kDgThreads, 0, stream>>>(args);
-  return cudaGetLastError();
+  return launch_overlapped(digest_kernel, need < fit ? need : fit, kDgThreads, 0, 1, stream, args);
 }
 
 cudaError_t launch_page_scores(const ScoreArgs& args, int num_sms, cudaStream_t stream) {
@@ -577,8 +578,8 @@ cudaError_t launch_page_scores(const ScoreArgs& args, int num_sms, cudaStream_t 
   const ScorePlan k = score_plan(args.d.hkv);
   const int64_t items = args.d.batch * (((int64_t)args.d.max_pages + k.pages - 1) / k.pages) * k.rounds;
   const int64_t fit = (int64_t)num_sms * kScoreCtasPerSm;
-  scores_kernel<<<(unsigned)(items < fit ? items : fit), kDgThreads, kScStages * kScStageBytes, stream>>>(args);
-  return cudaGetLastError();
+  return launch_overlapped(scores_kernel, items < fit ? items : fit, kDgThreads, kScStages * kScStageBytes, 1, stream,
+                           args);
 }
 
 }  // namespace nvfp4kv

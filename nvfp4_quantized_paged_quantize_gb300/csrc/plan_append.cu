@@ -48,6 +48,7 @@ __global__ void __launch_bounds__(kThreads) plan_kernel(const PlanArgs p, int ct
   constexpr int kWarps = kThreads / 32;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int rank = blockIdx.x;
+  after_earlier_kernels();
   int free_count = *p.free_count;
   if (free_count < 0 || free_count > p.free_capacity) {
     if (rank == 0 && tid == 0) flag_error(p.status, NVFP4KV_DEVERR_LENGTH);
@@ -195,18 +196,8 @@ cudaError_t launch_plan_append(const PlanArgs& args, cudaStream_t stream) {
   // (16 requests of up to 2048 tokens over 128 blocks 3.4 us, over 8 9.3)
   const int64_t want = (args.max_tokens + threads - 1) / threads, most = in_place ? kPlanMaxCluster : 128;
   const int ctas = (int)(want < 1 ? 1 : want < most ? want : most);
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)ctas);
-  cfg.blockDim = dim3((unsigned)threads);
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = in_place ? ctas : 1;
-  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return small ? cudaLaunchKernelEx(&cfg, plan_kernel<256>, args, ctas, in_place)
-               : cudaLaunchKernelEx(&cfg, plan_kernel<1024>, args, ctas, in_place);
+  return launch_overlapped(small ? plan_kernel<256> : plan_kernel<1024>, ctas, threads, 0, in_place ? ctas : 1, stream,
+                           args, ctas, in_place);
 }
 
 }  // namespace nvfp4kv

@@ -36,6 +36,13 @@ __device__ __forceinline__ float key_score(uint32_t k) {
   return __uint_as_float((k & 0x80000000u) ? k ^ 0x80000000u : ~k);
 }
 
+// (in order with its like; the compiler spread plain loads: 0.3 us)
+__device__ __forceinline__ float load_score(const float* p) {
+  float v;
+  asm volatile("ld.global.f32 %0, [%1];" : "=f"(v) : "l"(p) : "memory");
+  return v;
+}
+
 template <int kThreads, int kBins>
 struct SelectShared {
   uint32_t hist[kBins];
@@ -53,7 +60,8 @@ __global__ void __launch_bounds__(kThreads, kCtas) select_kernel(const SelectArg
   __shared__ SelectShared<kThreads, kBins> s;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const long long pair = blockIdx.x;
-  const int L = __ldg(p.seq_lens + (int)(pair / p.hkv));
+  after_earlier_kernels();
+  const int L = p.seq_lens[(int)(pair / p.hkv)];
   long long pages = ((long long)L + kPage - 1) / kPage;
   if (L < 0 || pages > p.score_stride) {
     if (tid == 0) flag_error(p.status, NVFP4KV_DEVERR_LENGTH);
@@ -73,13 +81,13 @@ __global__ void __launch_bounds__(kThreads, kCtas) select_kernel(const SelectArg
   const int own = min(max((middle - at0 + 31) / 32, 0), rows);  // scores of this thread
   float x[kRows];
 #pragma unroll
-  for (int j = 0; j < kRows; ++j) x[j] = j < own ? __ldg(mine + at0 + 32 * j) : 0.0f;
+  for (int j = 0; j < kRows; ++j) x[j] = j < own ? load_score(mine + at0 + 32 * j) : 0.0f;
   auto each = [&](auto f) {  // every score of the thread
 #pragma unroll
     for (int j = 0; j < kRows; ++j)
       if (j < own) f(x[j]);
     if constexpr (kMore)
-      for (int j = kRows; j < own; ++j) f(__ldg(mine + at0 + 32 * j));
+      for (int j = kRows; j < own; ++j) f(mine[at0 + 32 * j]);
   };
   for (int i = tid; i < p.first; i += kThreads) selected[i] = i;
   for (int i = tid; i < p.recent; i += kThreads) selected[p.budget - p.recent + i] = n - p.recent + i;
@@ -226,7 +234,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) select_kernel(const SelectArg
     e += __popc(equal[j]);
   }
   auto more = [&](int j, uint32_t& a, uint32_t& q) {  // a row past the registers
-    const uint32_t k = j < own ? order_key(__ldg(mine + at0 + 32 * j)) : kKeyNone;
+    const uint32_t k = j < own ? order_key(mine[at0 + 32 * j]) : kKeyNone;
     a = __ballot_sync(kAll, k > cut);
     q = __ballot_sync(kAll, k == cut);
   };
@@ -264,7 +272,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) select_kernel(const SelectArg
 }  // namespace
 
 cudaError_t launch_select_pages(const SelectArgs& args, cudaStream_t stream) {
-  const unsigned pairs = (unsigned)((int64_t)args.batch * args.hkv);
+  const int64_t pairs = (int64_t)args.batch * args.hkv;
   // The lengths are on the device, so the shape goes by the pages that the scores have room
   // for.  256 threads, 1024 with 9 scores each and 1024 with 16, in a captured graph: 768
   // pairs of 500 pages 6.8, 25 and 34 us, of 2000 8.9, 27 and 36, 32 pairs of 2000 4.5, 5.5
@@ -272,12 +280,10 @@ cudaError_t launch_select_pages(const SelectArgs& args, cudaStream_t stream) {
   // of 31250 pages 25 us.
   const int64_t most = args.score_stride;
   if (most <= 256 * 8)
-    select_kernel<256, 1024, 8, false, 6><<<pairs, 256, 0, stream>>>(args);
-  else if (most <= 1024 * 9)
-    select_kernel<1024, 2048, 9, false, 1><<<pairs, 1024, 0, stream>>>(args);
-  else
-    select_kernel<1024, 2048, 16, true, 1><<<pairs, 1024, 0, stream>>>(args);
-  return cudaGetLastError();
+    return launch_overlapped(select_kernel<256, 1024, 8, false, 6>, pairs, 256, 0, 1, stream, args);
+  if (most <= 1024 * 9)
+    return launch_overlapped(select_kernel<1024, 2048, 9, false, 1>, pairs, 1024, 0, 1, stream, args);
+  return launch_overlapped(select_kernel<1024, 2048, 16, true, 1>, pairs, 1024, 0, 1, stream, args);
 }
 
 }  // namespace nvfp4kv
