@@ -45,33 +45,33 @@ struct Share {
 };
 
 struct ShareShared {
-  int sums[kDgWarps];
+  int sums[kDgWarps + 1];
   int begin[kDgWarps + 1];  // the block's shares
   int b[kDgWarps], first[kDgWarps];
 };
 
 // The block's share number `mine`, of `shares`; items of sequence b: count(b).  Every
-// thread of the block calls this.
-template <class Count>
+// thread of the block's kThreads calls this.
+template <int kThreads, class Count>
 __device__ __forceinline__ Share split(ShareShared& s, int batch, int shares, int mine, Count count) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   // one pass over the sequences for the total, and (again, unless they were few
   // enough to stay in a register) one to find the shares' starts
   int kept = 0, local = 0;
-  for (int b = tid; b < batch; b += kDgThreads) local += kept = count(b);
+  for (int b = tid; b < batch; b += kThreads) local += kept = count(b);
   int sum = __reduce_add_sync(kAll, local);
   if (lane == 0) s.sums[warp] = sum;
   __syncthreads();
   int total = 0;
 #pragma unroll
-  for (int w = 0; w < kDgWarps; ++w) total += s.sums[w];
+  for (int w = 0; w < kThreads / 32; ++w) total += s.sums[w];
   if (tid <= shares)
     s.begin[tid] = (int)(total * ((long long)blockIdx.x * shares + tid) / ((long long)gridDim.x * shares));
   __syncthreads();
   int carry = 0;
-  for (int base = 0; base < batch; base += kDgThreads) {
+  for (int base = 0; base < batch; base += kThreads) {
     const int b = base + tid;
-    const int n = batch <= kDgThreads ? kept : b < batch ? count(b) : 0;
+    const int n = batch <= kThreads ? kept : b < batch ? count(b) : 0;
     int incl = n;
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
@@ -82,7 +82,7 @@ __device__ __forceinline__ Share split(ShareShared& s, int batch, int shares, in
     __syncthreads();
     int first = carry + incl - n, all = carry;
 #pragma unroll
-    for (int w = 0; w < kDgWarps; ++w) {
+    for (int w = 0; w < kThreads / 32; ++w) {
       if (w < warp) first += s.sums[w];
       all += s.sums[w];
     }
@@ -249,7 +249,7 @@ __global__ void __launch_bounds__(kDgThreads, kDigestCtasPerSm) digest_kernel(co
   const int lane = threadIdx.x & 31;
   after_earlier_kernels();
   auto from_page = [&](int b) { return p.first_tokens ? max(p.first_tokens[b], 0) / kPage : 0; };
-  const Share w = split(s, p.batch, kDgWarps, (int)(threadIdx.x >> 5), [&](int b) {
+  const Share w = split<kDgThreads>(s, p.batch, kDgWarps, (int)(threadIdx.x >> 5), [&](int b) {
     const int L = seq_tokens(p, b, blockIdx.x == 0);
     return max((L + kPage - 1) / kPage - from_page(b), 0) * p.hkv;
   });
@@ -409,25 +409,33 @@ constexpr int kScStages = 2;
 constexpr int kScStageBytes = 128 * 320;
 
 // A block takes items of 16 to 128 consecutive pages of one sequence and up to eight
-// KV heads; a warp one of the heads and 16 of the pages, the rows of an MMA whose
-// eight columns are the query heads.  Lane (g, t) reads 16-byte pieces t and 4 + t of
-// hi and of lo of pages g and g + 8.  One copy per page (2176 bytes with eight heads),
-// two items ahead, the page ids read one item before that.  28.8 thousand pages of 8 heads
-// 16.7 us (17.7 with each row fetched by itself, however many at a time), 16.4
-// thousand 11.5: some 5 us for the launch, the shares and the first page, then the
-// pages at 5.5 TB/s.
-__global__ void __launch_bounds__(kDgThreads, kScoreCtasPerSm) scores_kernel(const ScoreArgs p) {
+// KV heads; a warp (but the last) one of the heads and 16 of the pages, the rows of an MMA
+// whose eight columns are the query heads.  Lane (g, t) reads 16-byte pieces t and 4 + t of
+// hi and of lo of pages g and g + 8.  The last warp starts the copies, one per page (2176
+// bytes with eight heads), into a stage as soon as the others have left it.  28.8 thousand
+// pages of 8 heads 15.5 us (15.9 with a barrier of all warps per item, 19.8 so with items of
+// half the pages; some 18 with each row fetched by itself), 16.4 thousand 10.7: some 5 us for
+// the launch, the shares and the first page, then the pages at 6 TB/s.
+constexpr int kScThreads = kDgThreads + 32;
+
+__device__ __forceinline__ void arrive(uint32_t bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
+__global__ void __launch_bounds__(kScThreads, kScoreCtasPerSm) scores_kernel(const ScoreArgs p) {
   extern __shared__ __align__(128) uint8_t stages[];
   __shared__ ShareShared s;
-  __shared__ __align__(8) uint64_t bars[kScStages];
+  __shared__ __align__(8) uint64_t bars[2 * kScStages];
   __shared__ uint32_t s_there[kScStages][4];  // a stage's pages that are there, bit by bit
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
   const DigestArgs& d = p.d;
   const ScorePlan k = score_plan(d.hkv);
-  const uint32_t bar = smem_u32(bars), st0 = smem_u32(stages);
-  const int copiers = (k.pages + 31) / 32;  // warps that start copies, one page per thread
+  const uint32_t full = smem_u32(bars), empty = full + 8 * kScStages, st0 = smem_u32(stages);
   if (tid == 0) {
-    for (int i = 0; i < kScStages; ++i) mbar_init(bar + 8 * i, copiers);
+    for (int i = 0; i < kScStages; ++i) {
+      mbar_init(full + 8 * i, 1);
+      mbar_init(empty + 8 * i, kDgWarps);
+    }
     fence_mbar_init();
   }
   after_earlier_kernels();
@@ -440,7 +448,8 @@ __global__ void __launch_bounds__(kDgThreads, kScoreCtasPerSm) scores_kernel(con
     return n;
   };
   auto steps_of = [&](int pages) { return (pages + k.pages - 1) / k.pages; };
-  const Share w = split(s, d.batch, 1, 0, [&](int b) { return steps_of(pages_of(b, blockIdx.x == 0)) * k.rounds; });
+  const Share w =
+      split<kScThreads>(s, d.batch, 1, 0, [&](int b) { return steps_of(pages_of(b, blockIdx.x == 0)) * k.rounds; });
   if (w.begin >= w.end) return;
   // a walk over the share's items: step `step` of `steps` of sequence b, heads from together * round on
   struct Walk {
@@ -463,56 +472,66 @@ __global__ void __launch_bounds__(kDgThreads, kScoreCtasPerSm) scores_kernel(con
   at.steps = steps_of(at.pages);
   at.round = (w.begin - w.first) / at.steps;
   at.step = w.begin - w.first - at.round * at.steps;
-  Walk ahead = at;
-  int to_read = w.end - w.begin;  // items whose ids have not been read yet
-  // thread = page of the item: its id (-1: none), and the first of its heads
-  struct Ids {
-    int id, head;
-    bool page, item;
-  };
-  auto read_ids = [&]() {
-    Ids x = {-1, 0, false, false};
-    if (to_read > 0) {
-      const int page = ahead.step * k.pages + tid;
-      x.item = true;
-      x.head = ahead.round * k.together;
-      x.page = tid < k.pages && page < ahead.pages;
-      if (x.page) x.id = d.page_table[(long long)ahead.b * d.max_pages + page];
-      --to_read;
-      advance(ahead);
+
+  if (warp == kDgWarps) {
+    // the copies: lane = page of the item modulo 32; the ids of an item are read while the one before it is copied
+    constexpr int kMost = 128 / 32;
+    int ids[kMost];
+    auto read_ids = [&](const Walk& x, bool item) {
+#pragma unroll
+      for (int c = 0; c < kMost; ++c) {
+        const int in = 32 * c + lane, page = x.step * k.pages + in;
+        ids[c] = -1;
+        if (item && in < k.pages && page < x.pages) {
+          ids[c] = d.page_table[(long long)x.b * d.max_pages + page];
+          if (ids[c] < 0 || ids[c] >= d.num_pages) {
+            flag_error(d.status, NVFP4KV_DEVERR_PAGE);
+            ids[c] = -1;
+          }
+        }
+      }
+    };
+    read_ids(at, true);
+    for (int n = 0; n < w.end - w.begin; ++n) {
+      const int stage = n % kScStages, head = at.round * k.together;
+      const uint32_t bytes = (uint32_t)(min(k.together, d.hkv - head) * kDigestBytes);
+      int now[kMost];
+      uint32_t there[kMost], count = 0;
+#pragma unroll
+      for (int c = 0; c < kMost; ++c) {
+        now[c] = ids[c];
+        there[c] = __ballot_sync(kAll, ids[c] >= 0);
+        count += __popc(there[c]);
+      }
+      advance(at);
+      read_ids(at, n + 1 < w.end - w.begin);
+      if (n >= kScStages && !mbar_wait(empty + 8 * stage, (uint32_t)(n / kScStages - 1) & 1u) && lane == 0)
+        flag_error(d.status, kDevErrTimeout);
+      if (lane == 0) {
+#pragma unroll
+        for (int c = 0; c < kMost; ++c) s_there[stage][c] = there[c];
+        asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(full + 8 * stage), "r"(bytes * count)
+                     : "memory");
+      }
+      __syncwarp();
+#pragma unroll
+      for (int c = 0; c < kMost; ++c) {
+        if (now[c] < 0) continue;
+        const uint8_t* src = d.digest + ((long long)now[c] * d.hkv + head) * kDigestBytes;
+        asm volatile("cp.async.bulk.shared::cta.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                         st0 + stage * kScStageBytes + (32 * c + lane) * k.stride),
+                     "l"(src), "r"(bytes), "r"(full + 8 * stage)
+                     : "memory");
+      }
     }
-    return x;
-  };
-  auto copy = [&](int stage, const Ids& x) {
-    if (warp >= copiers || !x.item) return;
-    const bool there = x.page && x.id >= 0 && x.id < d.num_pages;
-    if (x.page && !there) flag_error(d.status, NVFP4KV_DEVERR_PAGE);
-    const uint32_t bytes = (uint32_t)(min(k.together, d.hkv - x.head) * kDigestBytes);
-    const uint32_t mask = __ballot_sync(kAll, there);
-    if (lane == 0) {
-      s_there[stage][warp] = mask;
-      asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar + 8 * stage), "r"(bytes * __popc(mask))
-                   : "memory");
-    }
-    __syncwarp();
-    if (there) {
-      const uint8_t* src = d.digest + ((long long)x.id * d.hkv + x.head) * kDigestBytes;
-      asm volatile("cp.async.bulk.shared::cta.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-                       st0 + stage * kScStageBytes + tid * k.stride),
-                   "l"(src), "r"(bytes), "r"(bar + 8 * stage)
-                   : "memory");
-    }
-  };
-  static_assert(kScStages == 2, "the items under way have names");
+    return;
+  }
+
   const int stream = warp / k.together, mine = warp - stream * k.together;
-  const Ids first = read_ids(), second = read_ids();
-  copy(0, first);
-  copy(1, second);
-  Ids third = read_ids();
   Queries q;
-  int loaded = -1, n = 0;
-  for (int i = w.begin; i < w.end; ++i, ++n) {
-    const int stage = n & 1, head = at.round * k.together + mine, pair = at.b * d.hkv + head;
+  int loaded = -1;
+  for (int n = 0; n < w.end - w.begin; ++n) {
+    const int stage = n % kScStages, head = at.round * k.together + mine, pair = at.b * d.hkv + head;
     const int page0 = at.step * k.pages + stream * kTile;  // the warp's first page
     const bool live = stream < k.streams && head < d.hkv && page0 < at.pages;
     if (live && pair != loaded) {
@@ -520,7 +539,7 @@ __global__ void __launch_bounds__(kDgThreads, kScoreCtasPerSm) scores_kernel(con
       loaded = pair;
     }
     // (a wait that gives up: the outputs are not valid, every access stays in bounds)
-    if (!mbar_wait(bar + 8 * stage, (uint32_t)(n >> 1) & 1u) && lane == 0) flag_error(d.status, kDevErrTimeout);
+    if (!mbar_wait(full + 8 * stage, (uint32_t)(n / kScStages) & 1u) && lane == 0) flag_error(d.status, kDevErrTimeout);
     if (live) {
       const uint32_t there = s_there[stage][stream >> 1] >> (kTile * (stream & 1));
       const uint8_t* const rows = stages + stage * kScStageBytes + stream * kTile * k.stride + mine * kDigestBytes;
@@ -538,6 +557,10 @@ __global__ void __launch_bounds__(kDgThreads, kScoreCtasPerSm) scores_kernel(con
                    e4m3x2_to_f16x2(e[m] >> 16), f[0], f[1]);
         }
       }
+      const int r = g + 8 * t;  // lanes t = 0 and 1 write pages g and g + 8
+      const float unit = t < 2 ? *reinterpret_cast<const float*>(rows + r * k.stride + kOffScale) : 0.0f;
+      __syncwarp();
+      if (lane == 0) arrive(empty + 8 * stage);
       // the largest over the group's heads, 2 t and 2 t + 1 in this lane
       const float c00 = 2 * t < p.group ? c[0] * q.c0 : -INFINITY, c01 = 2 * t + 1 < p.group ? c[1] * q.c1 : -INFINITY;
       const float c10 = 2 * t < p.group ? c[2] * q.c0 : -INFINITY, c11 = 2 * t + 1 < p.group ? c[3] * q.c1 : -INFINITY;
@@ -547,17 +570,13 @@ __global__ void __launch_bounds__(kDgThreads, kScoreCtasPerSm) scores_kernel(con
         m0 = fmaxf(m0, __shfl_xor_sync(kAll, m0, off));
         m1 = fmaxf(m1, __shfl_xor_sync(kAll, m1, off));
       }
-      // lanes t = 0 and 1 write pages g and g + 8
-      const int r = g + 8 * t, page = page0 + r;
-      if (t < 2 && page < at.pages) {
-        const float unit = *reinterpret_cast<const float*>(rows + r * k.stride + kOffScale);
+      const int page = page0 + r;
+      if (t < 2 && page < at.pages)
         p.scores[(long long)pair * p.score_stride + page] = (there >> r & 1) ? (t ? m1 : m0) * unit : -INFINITY;
-      }
+    } else if (lane == 0) {
+      arrive(empty + 8 * stage);
     }
     advance(at);
-    __syncthreads();  // the stage may be filled again
-    copy(stage, third);
-    third = read_ids();
   }
 }
 
@@ -578,7 +597,7 @@ cudaError_t launch_page_scores(const ScoreArgs& args, int num_sms, cudaStream_t 
   const ScorePlan k = score_plan(args.d.hkv);
   const int64_t items = args.d.batch * (((int64_t)args.d.max_pages + k.pages - 1) / k.pages) * k.rounds;
   const int64_t fit = (int64_t)num_sms * kScoreCtasPerSm;
-  return launch_overlapped(scores_kernel, items < fit ? items : fit, kDgThreads, kScStages * kScStageBytes, 1, stream,
+  return launch_overlapped(scores_kernel, items < fit ? items : fit, kScThreads, kScStages * kScStageBytes, 1, stream,
                            args);
 }
 
