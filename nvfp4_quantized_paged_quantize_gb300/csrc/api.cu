@@ -639,7 +639,10 @@ int nvfp4kv_select_pages(const float* scores, int64_t score_stride, const int32_
     return NVFP4KV_ERR_INVALID_ARGUMENT;
   const nvfp4kv::SelectArgs a = {scores, score_stride, seq_lens, batch, num_kv_heads, budget, first, recent, selected,
                                  device_status};
-  return cuda_status(nvfp4kv::launch_select_pages(a, reinterpret_cast<cudaStream_t>(stream)));
+  int nsm = 0;
+  const int st = current_num_sms(&nsm);
+  if (st != NVFP4KV_OK) return st;
+  return cuda_status(nvfp4kv::launch_select_pages(a, nsm, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 int nvfp4kv_decode_attention_selected(const nvfp4kv_cache* cache, const void* q, void* out, float* lse,

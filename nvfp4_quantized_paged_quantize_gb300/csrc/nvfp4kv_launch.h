@@ -238,7 +238,7 @@ struct SelectArgs {
   int32_t* selected;  // [batch][hkv][budget]
   int32_t* status;
 };
-cudaError_t launch_select_pages(const SelectArgs& args, cudaStream_t stream);
+cudaError_t launch_select_pages(const SelectArgs& args, int num_sms, cudaStream_t stream);
 
 // The decode over listed pages alone (bf16 out).
 cudaError_t launch_decode_selected(const nvfp4kv_cache& c, const uint16_t* q, uint16_t* out, float* lse,

@@ -2,9 +2,9 @@
 // head) the first, the latest, and those between with the largest scores
 // (nvfp4kv_select_pages), in page order.
 //
-// One CTA per pair; each thread keeps its pages' scores in registers.  The smallest
+// One CTA per pair, or a cluster where there are many pages; each thread keeps its pages' scores in registers.  The smallest
 // kept one is found by a histogram of equal parts of the scores' range (1024 or 2048),
-// whose part with the threshold mostly has few enough (32) for a warp to rank.  Else,
+// whose part with the threshold mostly has few enough to rank one by one.  Else,
 // and where the range is not finite, by histograms of the scores as integers that
 // order like the floats (keys), of equal parts of what is left each time.
 // (Parts of the integers' range from the start are too wide wherever scores lie on both
@@ -20,7 +20,8 @@
 namespace nvfp4kv {
 namespace {
 
-constexpr int kFew = 32;
+constexpr int kFew = 256;
+constexpr int kMaxCtas = 8;  // of a cluster, the portable limit
 constexpr uint32_t kAll = 0xFFFFFFFFu;
 constexpr uint32_t kKeyNone = 0;  // no float's key: below that of -inf
 constexpr float kLeastRange = 1e-30f;  // of the scores, for parts of it
@@ -50,34 +51,46 @@ struct SelectShared {
   uint2 warp_count[kThreads / 32];  // a warp's keys above and equal to the threshold
   uint32_t bin, above, in_bin;      // the threshold's part, the keys above it, the keys in it
   uint32_t few[kFew], few_count;
+  uint32_t all_few[kFew];  // of a cluster's CTAs
+  uint32_t cta_min, cta_max;  // of a cluster's CTA
+  uint2 cta_count;
 };
 
 // kRows: scores of a thread in registers.  A warp holds consecutive pages, `rows` to a
-// lane; kMore: there may be more than kRows, read again at every use.
-template <int kThreads, int kBins, int kRows, bool kMore, int kCtas>
-__global__ void __launch_bounds__(kThreads, kCtas) select_kernel(const SelectArgs p) {
+// lane; kMore: there may be more than kRows, read again at every use.  kCluster: a cluster
+// of `ctas` CTAs per pair, each with consecutive pages; every CTA adds up all parts of the
+// histograms and finds the same cut.
+template <int kThreads, int kBins, int kRows, bool kMore, bool kCluster, int kCtas>
+__global__ void __launch_bounds__(kThreads, kCtas) select_kernel(const SelectArgs p, int ctas) {
   constexpr int kWarps = kThreads / 32;
   __shared__ SelectShared<kThreads, kBins> s;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const long long pair = blockIdx.x;
+  const long long pair = kCluster ? blockIdx.x / ctas : blockIdx.x;
+  const int cta = kCluster ? blockIdx.x % ctas : 0;
   after_earlier_kernels();
   const int L = p.seq_lens[(int)(pair / p.hkv)];
   long long pages = ((long long)L + kPage - 1) / kPage;
   if (L < 0 || pages > p.score_stride) {
-    if (tid == 0) flag_error(p.status, NVFP4KV_DEVERR_LENGTH);
+    if (tid == 0 && cta == 0) flag_error(p.status, NVFP4KV_DEVERR_LENGTH);
     pages = L < 0 ? 0 : p.score_stride;
   }
   const int n = (int)pages;
   int32_t* selected = p.selected + pair * p.budget;
+  auto meet = [] {  // of the cluster's threads
+    __syncwarp();
+    cluster_sync();
+  };
+  const int all_threads = kCluster ? ctas * kThreads : kThreads, all_tid = cta * kThreads + tid;
   if (n <= p.budget) {
-    for (int i = tid; i < p.budget; i += kThreads) selected[i] = i < n ? i : -1;
+    for (int i = all_tid; i < p.budget; i += all_threads) selected[i] = i < n ? i : -1;
     return;
   }
   // n > budget >= first + recent: the middle is not empty
   const int middle = n - p.first - p.recent, want = p.budget - p.first - p.recent;
   const float* mine = p.scores + pair * p.score_stride + p.first;
-  const int rows = (middle + kThreads - 1) / kThreads;  // warp w: pages [32 rows w, 32 rows (w + 1)) of the middle
-  const int at0 = warp * rows * 32 + lane;
+  // warp w of all: pages [32 rows w, 32 rows (w + 1)) of the middle
+  const int rows = (middle + all_threads - 1) / all_threads;
+  const int at0 = (all_tid >> 5) * rows * 32 + lane;
   const int own = min(max((middle - at0 + 31) / 32, 0), rows);  // scores of this thread
   float x[kRows];
 #pragma unroll
@@ -89,8 +102,8 @@ __global__ void __launch_bounds__(kThreads, kCtas) select_kernel(const SelectArg
     if constexpr (kMore)
       for (int j = kRows; j < own; ++j) f(mine[at0 + 32 * j]);
   };
-  for (int i = tid; i < p.first; i += kThreads) selected[i] = i;
-  for (int i = tid; i < p.recent; i += kThreads) selected[p.budget - p.recent + i] = n - p.recent + i;
+  for (int i = all_tid; i < p.first; i += all_threads) selected[i] = i;
+  for (int i = all_tid; i < p.recent; i += all_threads) selected[p.budget - p.recent + i] = n - p.recent + i;
   if (want == 0) return;
 
   // the smallest and the largest key of the scores that `of` picks, over the block; every
@@ -114,6 +127,15 @@ __global__ void __launch_bounds__(kThreads, kCtas) select_kernel(const SelectArg
     __syncthreads();
     lo = __reduce_min_sync(kAll, s.warp_min[lane % kWarps]);
     hi = __reduce_max_sync(kAll, s.warp_max[lane % kWarps]);
+    if constexpr (kCluster) {
+      if (tid == 0) {
+        s.cta_min = lo;
+        s.cta_max = hi;
+      }
+      meet();
+      lo = __reduce_min_sync(kAll, ld_cluster(&s.cta_min, lane % ctas));
+      hi = __reduce_max_sync(kAll, ld_cluster(&s.cta_max, lane % ctas));
+    }
   };
   if (tid == 0) s.few_count = 0;
 #pragma unroll
@@ -131,15 +153,28 @@ __global__ void __launch_bounds__(kThreads, kCtas) select_kernel(const SelectArg
       const uint32_t at = of(v);
       if (at < kBins) atomicAdd(&s.hist[at], 1u);
     });
-    __syncthreads();
+    if constexpr (kCluster) meet(); else __syncthreads();
     constexpr int kPer = kBins / kThreads;
     // this thread's parts, from the top down
     uint32_t c[kPer], sum = 0;
 #pragma unroll
     for (int j = 0; j < kPer; ++j) {
       const int i = kBins - 1 - (kPer * tid + j);
-      sum += c[j] = s.hist[i];
-      s.hist[i] = 0;
+      if constexpr (kCluster) {
+        c[j] = 0;
+#pragma unroll
+        for (int r = 0; r < kMaxCtas; ++r)
+          if (r < ctas) c[j] += ld_cluster(&s.hist[i], r);
+      } else {
+        c[j] = s.hist[i];
+        s.hist[i] = 0;
+      }
+      sum += c[j];
+    }
+    if constexpr (kCluster) {
+      meet();  // every CTA has read them
+#pragma unroll
+      for (int j = 0; j < kPer; ++j) s.hist[kBins - 1 - (kPer * tid + j)] = 0;
     }
     uint32_t incl = sum;
 #pragma unroll
@@ -164,23 +199,55 @@ __global__ void __launch_bounds__(kThreads, kCtas) select_kernel(const SelectArg
     count = s.in_bin;
     left -= s.above;
   };
-  // the cut among the `count` <= kFew scores that `of` picks, ranked by every warp: it has
-  // fewer than `left` keys above it, and with its equals at least that
+  // the cut among the `count` <= kFew scores that `of` picks, ranked by every warp (up to 32)
+  // or by the block: it has fewer than `left` keys above it, and with its equals at least that
   auto rank = [&](auto of) {
     each([&](float v) {
       if (of(v)) s.few[atomicAdd(&s.few_count, 1u)] = order_key(v);
     });
-    __syncthreads();
-    const uint32_t k = lane < count ? s.few[lane] : kKeyNone;
-    uint32_t greater = 0, equal = 0;
-    for (uint32_t r = 0; r < count; ++r) {
-      const uint32_t other = __shfl_sync(kAll, k, r);
-      greater += other > k;
-      equal += other == k;
+    const uint32_t* few = s.few;
+    if constexpr (kCluster) {
+      meet();
+      // the CTAs' keys one after the other
+      uint32_t before = 0, here = 0;
+      int from = 0;
+      for (; from < ctas; before += here, ++from) {
+        here = ld_cluster(&s.few_count, from);
+        if (tid < before + here) break;
+      }
+      if (from < ctas) s.all_few[tid] = ld_cluster(&s.few[tid - before], from);
+      few = s.all_few;
     }
-    const int who = __ffs(__ballot_sync(kAll, lane < count && greater < left && greater + equal >= left)) - 1;
-    cut = __shfl_sync(kAll, k, who);
-    left -= __shfl_sync(kAll, greater, who);
+    __syncthreads();
+    if (count <= 32) {
+      const uint32_t k = lane < count ? few[lane] : kKeyNone;
+      uint32_t greater = 0, equal = 0;
+      for (uint32_t r = 0; r < count; ++r) {
+        const uint32_t other = __shfl_sync(kAll, k, r);
+        greater += other > k;
+        equal += other == k;
+      }
+      const int who = __ffs(__ballot_sync(kAll, lane < count && greater < left && greater + equal >= left)) - 1;
+      cut = __shfl_sync(kAll, k, who);
+      left -= __shfl_sync(kAll, greater, who);
+    } else {
+      if (tid < count) {
+        const uint32_t k = few[tid];
+        uint32_t greater = 0, equal = 0;
+        for (uint32_t r = 0; r < count; ++r) {
+          const uint32_t other = few[r];
+          greater += other > k;
+          equal += other == k;
+        }
+        if (greater < left && greater + equal >= left) {  // equal keys: the same words
+          s.bin = k;
+          s.above = greater;
+        }
+      }
+      __syncthreads();
+      cut = s.bin;
+      left -= s.above;
+    }
   };
   bool found = false;
   const float low = key_score(lo), range = key_score(hi) - low;
@@ -247,9 +314,16 @@ __global__ void __launch_bounds__(kThreads, kCtas) select_kernel(const SelectArg
     }
   if (lane == 0) s.warp_count[warp] = make_uint2(g, e);
   __syncthreads();
-  const uint2 counted = s.warp_count[lane % kWarps];
+  const uint2 counted = s.warp_count[lane % kWarps], counted_last = s.warp_count[kWarps - 1];
   g = __reduce_add_sync(kAll, lane < warp ? counted.x : 0u);
   e = __reduce_add_sync(kAll, lane < warp ? counted.y : 0u);
+  if constexpr (kCluster) {
+    if (warp == kWarps - 1 && lane == 0) s.cta_count = make_uint2(g + counted_last.x, e + counted_last.y);
+    meet();
+    const bool earlier = lane < cta;
+    g += __reduce_add_sync(kAll, earlier ? ld_cluster(&s.cta_count.x, lane) : 0u);
+    e += __reduce_add_sync(kAll, earlier ? ld_cluster(&s.cta_count.y, lane) : 0u);
+  }
   const uint32_t below = (1u << lane) - 1;
   auto put = [&](int j, uint32_t a, uint32_t q) {
     const uint32_t before = e + __popc(q & below);
@@ -267,23 +341,33 @@ __global__ void __launch_bounds__(kThreads, kCtas) select_kernel(const SelectArg
       more(j, a, q);
       put(j, a, q);
     }
+  if constexpr (kCluster) meet();  // no CTA leaves while another may still read its words
 }
 
 }  // namespace
 
-cudaError_t launch_select_pages(const SelectArgs& args, cudaStream_t stream) {
+cudaError_t launch_select_pages(const SelectArgs& args, int num_sms, cudaStream_t stream) {
   const int64_t pairs = (int64_t)args.batch * args.hkv;
   // The lengths are on the device, so the shape goes by the pages that the scores have room
   // for.  256 threads, 1024 with 9 scores each and 1024 with 16, in a captured graph: 768
   // pairs of 500 pages 6.8, 25 and 34 us, of 2000 8.9, 27 and 36, 32 pairs of 2000 4.5, 5.5
-  // and 7.1, of 8187 -, 7.4 and 9.4.  With more than 16, read again at every use: 32 pairs
-  // of 31250 pages 25 us.
+  // and 7.1, of 8187 -, 7.4 and 9.4.
   const int64_t most = args.score_stride;
   if (most <= 256 * 8)
-    return launch_overlapped(select_kernel<256, 1024, 8, false, 6>, pairs, 256, 0, 1, stream, args);
+    return launch_overlapped(select_kernel<256, 1024, 8, false, false, 6>, pairs, 256, 0, 1, stream, args, 1);
+  // More than a CTA keeps in registers, where SMs would stay empty: clusters with 4096 pages
+  // or more to a CTA.  With them and without (scores past the registers read again at every
+  // use): 8 pairs of 62500 pages 18 and 40 us, of 125000 20 and 88, 32 of 31250 14 and 20;
+  // but 32 of 15625 11.5 and 10.9, six barriers of a cluster.
+  int ctas = 1;
+  while (most > 1024 * 16 && ctas < kMaxCtas && pairs * 2 * ctas <= num_sms && most >= 2 * ctas * 4096) ctas *= 2;
+  if (ctas > 1 && most <= (int64_t)ctas * 1024 * 9)
+    return launch_overlapped(select_kernel<1024, 2048, 9, false, true, 1>, pairs * ctas, 1024, 0, ctas, stream, args, ctas);
+  if (ctas > 1)
+    return launch_overlapped(select_kernel<1024, 2048, 16, true, true, 1>, pairs * ctas, 1024, 0, ctas, stream, args, ctas);
   if (most <= 1024 * 9)
-    return launch_overlapped(select_kernel<1024, 2048, 9, false, 1>, pairs, 1024, 0, 1, stream, args);
-  return launch_overlapped(select_kernel<1024, 2048, 16, true, 1>, pairs, 1024, 0, 1, stream, args);
+    return launch_overlapped(select_kernel<1024, 2048, 9, false, false, 1>, pairs, 1024, 0, 1, stream, args, 1);
+  return launch_overlapped(select_kernel<1024, 2048, 16, true, false, 1>, pairs, 1024, 0, 1, stream, args, 1);
 }
 
 }  // namespace nvfp4kv

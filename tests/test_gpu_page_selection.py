@@ -228,6 +228,21 @@ def test_selection_of_long_sequences(cuda_lib, pages):
         check_selection(w, [16 * pages, 16 * (pages // 2) + 5], budget, 1, 4)
 
 
+@pytest.mark.parametrize("pages", [16385, 40000])
+def test_selection_of_long_sequences_with_special_values(cuda_lib, pages):
+    at = np.arange(pages)
+    rng = np.random.default_rng(5)
+    rows = [np.zeros(pages), np.where(at % 7 == 0, np.inf, 1.0), np.where(at % 5 == 0, np.nan, at), np.linspace(-3, 3, pages),
+            np.where(at % 3 == 0, -np.inf, at), 1.0 + (at % 1000) * 2.0 ** -23, np.where(at < 350, 1e30, -1e30),
+            rng.standard_normal(pages), np.where(at == pages - 9, 1e9, rng.random(pages))]
+    w = np.stack(rows).astype(np.float32)[:, None]
+    for budget in (1, 40, pages // 3, pages - 1):
+        check_selection(w, [16 * pages - 3] * len(rows), budget, min(3, budget), min(40, budget - min(3, budget)))
+    # lengths of which some parts, or all, have nothing to choose from
+    check_selection(w, [0, 1, 16 * 60, 16 * 61, 16 * 100, 16 * 5000, 16 * pages, 16 * 33, 16 * 9000], 60, 7, 21)
+    check_selection(np.repeat(w, 5, 1), [16 * pages - 3] * len(rows), 77, 2, 2)
+
+
 def test_selection_of_many_pairs_and_cut_lengths(cuda_lib):
     rng = np.random.default_rng(21)
     lens = rng.integers(0, 2000, 200)
