@@ -434,6 +434,60 @@ def test_two_streams_at_once(cuda_lib):
         assert all(torch.equal(x, y) for x, y in zip(a, b))
 
 
+@pytest.mark.parametrize("captured", [False, True])
+@pytest.mark.parametrize("ahead", ["kernel", "copy", "clear", "other stream", "own kernel on another stream"])
+def test_calls_wait_for_what_is_ahead(cuda_lib, ahead, captured):
+    # a call's blocks may be placed before the work ahead of it ends; what that writes is seen all the same
+    rng = np.random.default_rng(77)
+    n, lens = 500, dev(np.asarray([8000, 7777], np.int32))
+    news = [rng.standard_normal((2, 4, n)).astype(np.float32) for _ in range(3)]
+    scores, src = torch.zeros((2, 4, n), device="cuda"), torch.empty((2, 4, n), device="cuda")
+    sel, again = (torch.empty((2, 4, 60), dtype=torch.int32, device="cuda") for _ in range(2))
+    busy = torch.rand((3000, 3000), device="cuda")
+    side = torch.cuda.Stream()
+
+    def step():
+        for _ in range(4):
+            busy.mul_(1.0).add_(0.0)                                           # some time for the work ahead
+        if ahead == "kernel":
+            torch.mul(src, 1.0, out=scores)
+        elif ahead == "copy":
+            scores.copy_(src)
+        elif ahead == "clear":
+            torch.mul(src, 1.0, out=scores)
+            scores.zero_()
+        else:
+            side.wait_stream(torch.cuda.current_stream())
+            with torch.cuda.stream(side):
+                busy.mul_(1.0)
+                torch.mul(src, 1.0, out=scores)
+                if ahead.startswith("own"):
+                    kv.nvfp4kv_select_pages(scores, lens, 60, 1, 2, again)
+            kv.nvfp4kv_select_pages(src, lens, 60, 1, 2, sel)                  # something on this stream, too
+            torch.cuda.current_stream().wait_stream(side)
+        kv.nvfp4kv_select_pages(scores, lens, 60, 1, 2, sel)
+        scores.fill_(-1.0)                                                     # not before the selection has read them
+        kv.nvfp4kv_select_pages(scores, lens, 60, 1, 2, again)
+
+    if captured:
+        graph, stream = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+        src.copy_(dev(news[0]))
+        torch.cuda.synchronize()
+        with torch.cuda.graph(graph, stream=stream):
+            step()
+    flat = np.concatenate([[0], np.arange(1, 58), [0, 0]])
+    for new in news:
+        src.copy_(dev(new))
+        graph.replay() if captured else step()
+        torch.cuda.synchronize()
+        for b, pages in enumerate((500, 487)):
+            for h in range(4):
+                w = np.zeros(pages) if ahead == "clear" else new[b, h, :pages]
+                same(sel[b, h].cpu().numpy().astype(int), evict_ref(w, pages, 60, 1, 2), f"{b} {h}")
+                flat[-2:] = pages - 2, pages - 1
+                same(again[b, h].cpu().numpy().astype(int), flat, f"again {b} {h}")
+
+
 # --- a whole step ----------------------------------------------------------
 
 def test_captured_decode_steps_over_selected_pages(cuda_lib):
