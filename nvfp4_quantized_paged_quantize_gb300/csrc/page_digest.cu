@@ -404,18 +404,20 @@ __host__ __device__ inline ScorePlan score_plan(int hkv) {
   return k;
 }
 
+constexpr int kUnit = 8;  // shares are cut at multiples of so many pages: whole sectors of scores and ids
 constexpr int kScStages = 2;
 // the most that score_plan asks for: one head, 128 pages of 320 bytes
 constexpr int kScStageBytes = 128 * 320;
 
-// A block takes items of 16 to 128 consecutive pages of one sequence and up to eight
-// KV heads; a warp (but the last) one of the heads and 16 of the pages, the rows of an MMA
-// whose eight columns are the query heads.  Lane (g, t) reads 16-byte pieces t and 4 + t of
-// hi and of lo of pages g and g + 8.  The last warp starts the copies, one per page (2176
-// bytes with eight heads), into a stage as soon as the others have left it.  28.8 thousand
-// pages of 8 heads 15.5 us (15.9 with a barrier of all warps per item, 19.8 so with items of
-// half the pages; some 18 with each row fetched by itself), 16.4 thousand 10.7: some 5 us for
-// the launch, the shares and the first page, then the pages at 6 TB/s.
+// A block takes an equal share of all pages, in items of up to 16 to 128 consecutive ones
+// of one sequence and up to eight KV heads; a warp (but the last) one of the heads and 16
+// of the pages, the rows of an MMA whose eight columns are the query heads.  Lane (g, t)
+// reads 16-byte pieces t and 4 + t of hi and of lo of pages g and g + 8.  The last warp
+// starts the copies, one per page (2176 bytes with eight heads), into a stage as soon as the
+// others have left it.  28.8 thousand pages of 8 heads 15.3 us (15.9 with a barrier of all warps
+// per item, 19.8 so with items of half the pages; some 18 with each row fetched by
+// itself), 16.4 thousand 10.4 (10.7 with shares of whole items): some 5 us for the launch,
+// the shares and the first page, then the pages at 6 TB/s.
 constexpr int kScThreads = kDgThreads + 32;
 
 __device__ __forceinline__ void arrive(uint32_t bar) {
@@ -447,43 +449,51 @@ __global__ void __launch_bounds__(kScThreads, kScoreCtasPerSm) scores_kernel(con
     }
     return n;
   };
-  auto steps_of = [&](int pages) { return (pages + k.pages - 1) / k.pages; };
+  auto units_of = [&](int pages) { return (pages + kUnit - 1) / kUnit; };
   const Share w =
-      split<kScThreads>(s, d.batch, 1, 0, [&](int b) { return steps_of(pages_of(b, blockIdx.x == 0)) * k.rounds; });
+      split<kScThreads>(s, d.batch, 1, 0, [&](int b) { return units_of(pages_of(b, blockIdx.x == 0)) * k.rounds; });
   if (w.begin >= w.end) return;
-  // a walk over the share's items: step `step` of `steps` of sequence b, heads from together * round on
+  // a walk over the share: from page `page` of the `pages` of sequence b, heads from together *
+  // round on, `left` units to go
   struct Walk {
-    int b, round, step, steps, pages;
+    int b, round, page, pages, left;
   };
+  auto item_pages = [&](const Walk& x) { return min(min(k.pages, x.pages - x.page), x.left * kUnit); };
   auto advance = [&](Walk& x) {
-    if (++x.step < x.steps) return;
-    x.step = 0;
+    const int n = item_pages(x);
+    x.page += n;
+    x.left -= units_of(n);
+    if (x.left == 0 || x.page < x.pages) return;
+    x.page = 0;
     if (++x.round < k.rounds) return;
     x.round = 0;
-    do {  // the next sequence that has any; behind the last one there is none to look at
-      if (++x.b >= d.batch) return;
+    do {  // the next sequence that has any
+      if (++x.b >= d.batch) {
+        x.left = 0;
+        return;
+      }
       x.pages = pages_of(x.b, false);
     } while (x.pages == 0);
-    x.steps = steps_of(x.pages);
   };
   Walk at;
   at.b = w.b;
   at.pages = pages_of(w.b, false);
-  at.steps = steps_of(at.pages);
-  at.round = (w.begin - w.first) / at.steps;
-  at.step = w.begin - w.first - at.round * at.steps;
+  at.round = (w.begin - w.first) / units_of(at.pages);
+  at.page = (w.begin - w.first - at.round * units_of(at.pages)) * kUnit;
+  at.left = w.end - w.begin;
 
   if (warp == kDgWarps) {
     // the copies: lane = page of the item modulo 32; the ids of an item are read while the one before it is copied
     constexpr int kMost = 128 / 32;
     int ids[kMost];
-    auto read_ids = [&](const Walk& x, bool item) {
+    auto read_ids = [&](const Walk& x) {
+      const int item = item_pages(x);
 #pragma unroll
       for (int c = 0; c < kMost; ++c) {
-        const int in = 32 * c + lane, page = x.step * k.pages + in;
+        const int in = 32 * c + lane;
         ids[c] = -1;
-        if (item && in < k.pages && page < x.pages) {
-          ids[c] = d.page_table[(long long)x.b * d.max_pages + page];
+        if (in < item) {
+          ids[c] = d.page_table[(long long)x.b * d.max_pages + x.page + in];
           if (ids[c] < 0 || ids[c] >= d.num_pages) {
             flag_error(d.status, NVFP4KV_DEVERR_PAGE);
             ids[c] = -1;
@@ -491,8 +501,8 @@ __global__ void __launch_bounds__(kScThreads, kScoreCtasPerSm) scores_kernel(con
         }
       }
     };
-    read_ids(at, true);
-    for (int n = 0; n < w.end - w.begin; ++n) {
+    read_ids(at);
+    for (int n = 0; at.left > 0; ++n) {
       const int stage = n % kScStages, head = at.round * k.together;
       const uint32_t bytes = (uint32_t)(min(k.together, d.hkv - head) * kDigestBytes);
       int now[kMost];
@@ -504,7 +514,7 @@ __global__ void __launch_bounds__(kScThreads, kScoreCtasPerSm) scores_kernel(con
         count += __popc(there[c]);
       }
       advance(at);
-      read_ids(at, n + 1 < w.end - w.begin);
+      read_ids(at);
       if (n >= kScStages && !mbar_wait(empty + 8 * stage, (uint32_t)(n / kScStages - 1) & 1u) && lane == 0)
         flag_error(d.status, kDevErrTimeout);
       if (lane == 0) {
@@ -530,10 +540,10 @@ __global__ void __launch_bounds__(kScThreads, kScoreCtasPerSm) scores_kernel(con
   const int stream = warp / k.together, mine = warp - stream * k.together;
   Queries q;
   int loaded = -1;
-  for (int n = 0; n < w.end - w.begin; ++n) {
+  for (int n = 0; at.left > 0; ++n) {
     const int stage = n % kScStages, head = at.round * k.together + mine, pair = at.b * d.hkv + head;
-    const int page0 = at.step * k.pages + stream * kTile;  // the warp's first page
-    const bool live = stream < k.streams && head < d.hkv && page0 < at.pages;
+    const int mine_pages = item_pages(at) - stream * kTile;  // of the item, from the warp's first on
+    const bool live = stream < k.streams && head < d.hkv && mine_pages > 0;
     if (live && pair != loaded) {
       load_queries(p, pair, lane, q);
       loaded = pair;
@@ -570,9 +580,8 @@ __global__ void __launch_bounds__(kScThreads, kScoreCtasPerSm) scores_kernel(con
         m0 = fmaxf(m0, __shfl_xor_sync(kAll, m0, off));
         m1 = fmaxf(m1, __shfl_xor_sync(kAll, m1, off));
       }
-      const int page = page0 + r;
-      if (t < 2 && page < at.pages)
-        p.scores[(long long)pair * p.score_stride + page] = (there >> r & 1) ? (t ? m1 : m0) * unit : -INFINITY;
+      if (t < 2 && r < mine_pages)
+        p.scores[(long long)pair * p.score_stride + at.page + stream * kTile + r] = (there >> r & 1) ? (t ? m1 : m0) * unit : -INFINITY;
     } else if (lane == 0) {
       arrive(empty + 8 * stage);
     }
