@@ -26,8 +26,8 @@
 // flight on an SM at three CTAs; products two to an instruction.
 // HBM-bound on long inputs: 512 bytes per query row, 256 + 72 (+ 128 with the
 // workspace) per key or value row, and the cosines once per token.  12.7 thousand tokens
-// of 64 / 8 heads with workspace rows take 91 us, 5.7 TB/s (a warp per row with a piece
-// of four values to a lane: 154; lists of rows of mixed kinds: 107); 32 tokens 3.3.
+// of 64 / 8 heads with workspace rows take 91 us, 5.6 TB/s (a warp per row with a piece
+// of four values to a lane: 154; lists of rows of mixed kinds: 107); 32 tokens 3.1.
 #include "fp8_quotient.cuh"
 #include "nvfp4_block.cuh"
 #include "nvfp4kv_device.cuh"

@@ -242,7 +242,7 @@ __device__ __forceinline__ void write_digest(const uint8_t* keys, int valid, uin
 // A warp takes one page-head at a time; the keys of the next kDgStages - 1 are on
 // their way meanwhile.  1152 bytes in (whole lines) and 272 out per page-head.  Bound by
 // the integer pipe (75 % busy), which converts the codes and takes the bounds: 28.8
-// thousand pages of 8 heads 81 us, 4.0 TB/s (without the ring 99); 32 pages 3.3.
+// thousand pages of 8 heads 82 us, 4.0 TB/s (without the ring 99); 32 pages 3.1.
 __global__ void __launch_bounds__(kDgThreads, kDigestCtasPerSm) digest_kernel(const DigestArgs p) {
   __shared__ ShareShared s;
   __shared__ __align__(128) uint8_t rings[kDgWarps][kDgStages * kDgStageBytes];

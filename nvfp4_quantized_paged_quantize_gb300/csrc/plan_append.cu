@@ -14,8 +14,8 @@
 // lengths or the free count are updated in place, the CTAs are one cluster, with a
 // barrier between reading and writing them.
 // Bound by latency: a launch, the loads of the lengths, the sums, and for each token
-// two dependent loads and its stores.  256 requests of one token each 3.2 us, 16 of
-// 820 to 2048 3.1, in a captured graph (one block of 1024 threads with 64-bit sums:
+// two dependent loads and its stores.  256 requests of one token each 2.9 us, 16 of
+// 820 to 2048 2.9, in a captured graph (one block of 1024 threads with 64-bit sums:
 // 6.9 and, in a cluster of eight, 8.9: the instructions of its SM).
 #include "nvfp4kv_device.cuh"
 #include "nvfp4kv_launch.h"
