@@ -164,12 +164,15 @@ def _ptr(x) -> int | None:
     return x.data_ptr()
 
 
-def _stream(stream) -> int | None:
+def _stream(stream, gpu: int | None = None) -> int | None:
+    """The stream's address; of None, torch's current stream (on `gpu`, the current device, where that is known)."""
     if stream is None:
         # torch.cuda.current_stream().cuda_stream; without building a Stream object (3 us a call) where torch can
         t = _types()
         raw = getattr(t._C, "_cuda_getCurrentRawStream", None)
-        return raw(t.cuda.current_device()) if raw is not None else t.cuda.current_stream().cuda_stream
+        if raw is None:
+            return t.cuda.current_stream().cuda_stream
+        return raw(t.cuda.current_device() if gpu is None else gpu)
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -518,7 +521,7 @@ def nvfp4kv_plan_append(page_table, cached_lens, new_lens, free_pages, free_coun
                None if ws_rows is None else _checked("ws_rows", ws_rows, i64, (tokens,), gpu),
                None if cu_prefix is None else _checked("cu_prefix", cu_prefix, i64, sums, gpu),
                _checked("free_left", free_left, i32, words, gpu),
-               _checked_memory("device_status", device_status, gpu), _stream(stream)))
+               _checked_memory("device_status", device_status, gpu), _stream(stream, gpu)))
 
 
 def _token_rows(name: str, x, dtype, shape, gpu: int):
@@ -573,7 +576,7 @@ def nvfp4kv_norm_rope_append(cache: "Cache", q, k, v, slot_mapping, positions, c
            _L().nvfp4kv_norm_rope_append(cache.c_struct(), q_at, q_stride, k_at, k_stride, v_at, v_stride, hq, n,
                                          slots_at, positions_at, turns_at, max_position, how, out_at, out_stride,
                                          rows_at, rows, k_ws_scale, v_ws_scale, ws_k_at, ws_v_at,
-                                         _checked_memory("device_status", device_status, gpu), _stream(stream)))
+                                         _checked_memory("device_status", device_status, gpu), _stream(stream, gpu)))
 
 
 def _check_digest(cache: "Cache", digest, page_table, seq_lens, device_status):
@@ -600,7 +603,7 @@ def nvfp4kv_page_digest(cache: "Cache", page_table, seq_lens, digest, first_toke
     first_at = None if first_tokens is None else _checked("first_tokens", first_tokens, _types().int32, (B,), gpu)
     _check("nvfp4kv_page_digest",
            _L().nvfp4kv_page_digest(cache.c_struct(), table_at, maxp, lens_at, first_at, B, digest_at, status_at,
-                                    _stream(stream)))
+                                    _stream(stream, gpu)))
 
 
 def nvfp4kv_page_scores(cache: "Cache", digest, q, page_table, seq_lens, softmax_scale: float, scores,
@@ -615,7 +618,7 @@ def nvfp4kv_page_scores(cache: "Cache", digest, q, page_table, seq_lens, softmax
     scores_at = _checked("scores", scores, t.float32, (B, cache.num_kv_heads, stride), gpu)
     _check("nvfp4kv_page_scores",
            _L().nvfp4kv_page_scores(cache.c_struct(), digest_at, q_at, table_at, maxp, lens_at, B, hq,
-                                    float(softmax_scale), scores_at, stride, status_at, _stream(stream)))
+                                    float(softmax_scale), scores_at, stride, status_at, _stream(stream, gpu)))
 
 
 def nvfp4kv_select_pages(scores, seq_lens, budget: int, first: int, recent: int, selected, device_status=None,
@@ -629,7 +632,7 @@ def nvfp4kv_select_pages(scores, seq_lens, budget: int, first: int, recent: int,
            _L().nvfp4kv_select_pages(_checked("scores", scores, t.float32, (B, hkv, stride), gpu), stride,
                                      _checked("seq_lens", seq_lens, t.int32, (B,), gpu), B, hkv, budget, first, recent,
                                      _checked("selected", selected, t.int32, (B, hkv, budget), gpu),
-                                     _checked_memory("device_status", device_status, gpu), _stream(stream)))
+                                     _checked_memory("device_status", device_status, gpu), _stream(stream, gpu)))
 
 
 def nvfp4kv_decode_attention_selected(cache: "Cache", q, out, page_table, seq_lens, softmax_scale: float, selected,
@@ -640,15 +643,15 @@ def nvfp4kv_decode_attention_selected(cache: "Cache", q, out, page_table, seq_le
     nvfp4kv_decode_attention."""
     B, Hq, maxp, gpu = _check_decode(cache, q, out, page_table, seq_lens, lse, workspace, device_status)
     budget = _shape("selected", selected, 3)[2]
-    _check_tensor("selected", selected, _types().int32, (B, cache.num_kv_heads, budget), gpu)
+    selected_at = _checked("selected", selected, _types().int32, (B, cache.num_kv_heads, budget), gpu)
     if workspace_bytes is None:
         workspace_bytes = workspace.numel() * workspace.element_size()
-    c = cache.c_struct()
     _check("nvfp4kv_decode_attention_selected",
-           _L().nvfp4kv_decode_attention_selected(ctypes.byref(c), _ptr(q), _ptr(out), _ptr(lse), _ptr(page_table),
-                                                  maxp, _ptr(seq_lens), B, Hq, float(softmax_scale), _ptr(selected),
-                                                  budget, _ptr(workspace), workspace_bytes, _ptr(device_status),
-                                                  _stream(stream)))
+           _L().nvfp4kv_decode_attention_selected(cache.c_struct(), q.data_ptr(), out.data_ptr(),
+                                                  None if lse is None else lse.data_ptr(), page_table.data_ptr(), maxp,
+                                                  seq_lens.data_ptr(), B, Hq, float(softmax_scale), selected_at, budget,
+                                                  _ptr(workspace), workspace_bytes, _ptr(device_status),
+                                                  _stream(stream, gpu)))
 
 
 def nvfp4kv_status_string(status: int) -> str:
