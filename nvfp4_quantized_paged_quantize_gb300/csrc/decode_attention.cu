@@ -1583,34 +1583,39 @@ __global__ void __launch_bounds__(kCombineMaxWarps * 32) combine_kernel(const De
 // CTAs per (sequence, KV head) pair, each CTA an equal part of the pair's list, each
 // warp an eighth of that, with the ring and the phases of decode_kernel.  The warps'
 // results meet in shared memory and the CTAs' in that of the cluster (each CTA
-// finishes every splits-th head), so there are no records in global memory, no second
+// finishes every splits-th head, which the others store in its memory), so there are no records in global memory, no second
 // kernel and no scan over the batch: what is left of them is some 6 us, beside 11 of
 // decode_kernel and its combine, and the pages come at 5.7 TB/s and more.  Captured,
-// 64 / 8 heads, here and there: 32 x 8193 tokens, 8 pages a head 6.5 and 11.3 us, 64
-// 12.3 and 17.1, 256 32.6 and 35.8, 512 58.4 and 59.9; 37 x 8193, 512 58.9 and 66.5;
-// 4 x 131073, 1024 21.5 and 23.2, 4096 60.3 and 59.0.  Past one wave the even cut
+// 64 / 8 heads, here and there: 32 x 8193 tokens, 8 pages a head 6.3 and 11.3 us, 64
+// 12.2 and 17.1, 256 32.4 and 35.8, 512 58.4 and 59.9; 37 x 8193, 512 58.9 and 66.5;
+// 4 x 131073, 64 7.7, 1024 20.9 and 23.2, 4096 59.5 and 59.0.  Past one wave the even cut
 // wins (96 sequences, 64 pages 37.8 and 32.9), and where the clusters leave SMs empty
-// and lists are long: 1 x 131073, 1024 pages 14.6 and 15.7, 2048 23.5 and 20.8.
+// and lists are long: 1 x 131073, 256 pages 7.1 and 14.6, 1024 13.5 and 15.7, 2048 22.5 and 20.8.
 // (Cutting several pairs of a cluster evenly over its warps, and 4 warps with three
 // CTAs an SM, were both a tenth slower; the merge of cut pairs is what cost the first.)
 constexpr int kSW = 8, kSelCtas = 2;  // warps of a CTA, CTAs of an SM
-constexpr int kSelRingBytes = kSW * kStages * kStageBytes, kSelSmemBytes = kSelRingBytes + kSW * kStages * 8;
-constexpr int kOffCtaRecord = kStages * kStageBytes / 2;  // in the first warp's ring, behind its own record
 constexpr int kMaxSplits = 8;  // the portable cluster
-static_assert(kRecFloats * 4 <= kOffCtaRecord, "a warp's record and the CTA's fit a warp's ring");
+// in shared memory: the warps' rings (and records), their barriers, the parts of the heads
+// that this CTA finishes, from every CTA of the cluster
+constexpr int kSelRingBytes = kSW * kStages * kStageBytes;
+constexpr int kOffParts = kSelRingBytes + (kSW * kStages * 8 + 127) / 128 * 128;
+constexpr int kPartFloats = kHeadDim + 4;
+constexpr int kSelSmemBytes = kOffParts + (kGMax + kMaxSplits - 1) * kPartFloats * 4;
+static_assert(kRecFloats * 4 <= kStages * kStageBytes, "a warp's record fits its ring");
 static_assert(kSW >= kGMax && kSW <= 8 && kMaxSplits <= 8 && kHeadDim == 32 * 4, "a warp finishes a head of eight parts at most");
 
-// The word, the four words, at this address of the same shared memory in another CTA of the cluster.
-__device__ __forceinline__ float ld_cluster_f32(const float* local, uint32_t rank) {
-  return __uint_as_float(ld_cluster(reinterpret_cast<const uint32_t*>(local), rank));
-}
-__device__ __forceinline__ float4 ld_cluster_f32x4(const float* local, uint32_t rank) {
+// The address of this shared memory in another CTA of the cluster; a store there.
+__device__ __forceinline__ uint32_t map_cluster(const float* local, uint32_t rank) {
   uint32_t at;
-  float4 v;
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_u32(local)), "r"(rank));
-  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(at) : "memory");
-  return v;
+  return at;
 }
+__device__ __forceinline__ void st_cluster_f32x4(uint32_t at, const float4& v) {
+  asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(at), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w) : "memory");
+}
+// The two halves of a barrier of the cluster's threads that orders no memory.
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.relaxed;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait;" ::: "memory"); }
 
 __global__ void __launch_bounds__(kSW * 32, kSelCtas) selected_kernel(const DecodeParams p, int splits) {
   constexpr int F = kFmtNvfp4, M = kScored;
@@ -1620,6 +1625,7 @@ __global__ void __launch_bounds__(kSW * 32, kSelCtas) selected_kernel(const Deco
   const int g = lane >> 2, t = lane & 3;
   const int pair = blockIdx.x / splits, rank = blockIdx.x - pair * splits;
   const int b = pair / p.hkv, h = pair - b * p.hkv;
+  if (splits > 1) cluster_arrive();
   after_earlier_kernels();
   const QRaw q = fetch_q<true>(p, pair, g, t);
   // the warp's part [w0, w0 + n) of a list of `listed` entries
@@ -1761,7 +1767,7 @@ __global__ void __launch_bounds__(kSW * 32, kSelCtas) selected_kernel(const Deco
         make_uint2(pack_bf16x2(o.x * r, o.y * r), pack_bf16x2(o.z * r, o.w * r));
     if (lane == 0) store_lse<M>(p, row, m, l);
   };
-  float* const cta = reinterpret_cast<float*>(smem + kOffCtaRecord);
+  float* const parts = reinterpret_cast<float*>(smem + kOffParts);
   if (warp < p.group) {
     // part k: warp k's record
     auto rec = [&](int k) { return reinterpret_cast<const float*>(smem + k * kStages * kStageBytes); };
@@ -1773,28 +1779,29 @@ __global__ void __launch_bounds__(kSW * 32, kSelCtas) selected_kernel(const Deco
     if (splits == 1) {
       put_out(warp, m, l, o);
     } else {
-      reinterpret_cast<float4*>(cta + warp * kHeadDim)[lane] = o;
-      if (lane == 0) {
-        cta[kOffM + warp] = m;
-        cta[kOffL + warp] = l;
-      }
+      // to the CTA that finishes the head
+      cluster_wait();  // every CTA has started
+      const uint32_t to = map_cluster(parts + (warp / splits * splits + rank) * kPartFloats, warp % splits);
+      st_cluster_f32x4(to + 16 * lane, o);
+      if (lane == 0) st_cluster_f32x4(to + 4 * kHeadDim, make_float4(m, l, 0.0f, 0.0f));
     }
+  } else if (splits > 1) {
+    cluster_wait();
   }
   if (splits > 1) {
     __syncwarp();
     cluster_sync();
-    // part k: CTA k's record; every splits-th head to a CTA
+    // part k: CTA k's; every splits-th head to a CTA
     const int head = rank + splits * warp;
     if (head < p.group) {
+      const float* const mine = parts + warp * splits * kPartFloats;
       const int k = lane < splits ? lane : 0;
       float m, l;
       float4 o;
-      merge(splits, ld_cluster_f32(cta + kOffM + head, k), ld_cluster_f32(cta + kOffL + head, k),
-            [&](int i) { return ld_cluster_f32x4(cta + head * kHeadDim + 4 * lane, i); }, m, l, o);
+      merge(splits, mine[k * kPartFloats + kHeadDim], mine[k * kPartFloats + kHeadDim + 1],
+            [&](int i) { return reinterpret_cast<const float4*>(mine + i * kPartFloats)[lane]; }, m, l, o);
       put_out(head, m, l, o);
     }
-    __syncwarp();
-    cluster_sync();  // no CTA leaves while another may still read its record
   }
 }
 

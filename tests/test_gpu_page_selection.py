@@ -324,6 +324,16 @@ def test_selected_decode_of_a_large_batch(cuda_lib, batch):
     run_attend(cache, o, table, lens, 8, random_lists(lens, 2, 9, 29), 30)
 
 
+@pytest.mark.parametrize("pairs,group", [(12, 7), (41, 5), (47, 8), (55, 3), (70, 7), (90, 8), (120, 6), (200, 8)])
+def test_selected_decode_at_every_number_of_parts(cuda_lib, pairs, group):
+    # 8, 7, .. 1 CTAs to a pair on this GPU: heads that do not divide among them, lists shorter than the warps
+    rng = np.random.default_rng(pairs)
+    lens = rng.integers(0, 900, pairs).tolist()
+    table, used = page_tables(lens, pairs + 1)
+    cache, o = random_cache(used, 1, pairs + 2)
+    run_attend(cache, o, table, lens, group, random_lists(lens, 1, 23, pairs + 3), pairs + 4)
+
+
 def test_lists_in_any_order_with_gaps(cuda_lib):
     lens = [400, 90, 50, 33]
     table, used = page_tables(lens, 31)
