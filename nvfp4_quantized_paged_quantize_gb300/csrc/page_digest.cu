@@ -11,6 +11,8 @@
 //
 // Both kernels cut the flattened list of their items evenly, over all warps (digests)
 // or blocks (scores).
+#include <climits>
+
 #include "nvfp4kv_device.cuh"
 #include "nvfp4kv_launch.h"
 
@@ -147,16 +149,17 @@ constexpr int kDgStages = 3;
 constexpr int kDgStageBytes = kPageDataBytes + kPageScaleBytes;
 static_assert(kOffKScale == kPageDataBytes, "the keys' scales follow the keys");
 
-// Starts the copy of a page-head's keys and scales (nothing for a null one) into a stage.
-__device__ __forceinline__ void fetch_keys(uint32_t stage, const uint8_t* ph, int lane) {
-  if (ph != nullptr) {
+// Starts the copy of a page-head's keys and scales (nothing if it is not there) into a
+// stage; both addresses are the lane's, 16 bytes from one lane to the next.
+__device__ __forceinline__ void fetch_keys(uint32_t stage, const uint8_t* src, bool there, int lane) {
+  if (there) {
     asm volatile(
         "{\n .reg .pred p;\n"
         " setp.lt.u32 p, %2, 8;\n"
         " cp.async.cg.shared.global [%0], [%1], 16;\n"
         " cp.async.cg.shared.global [%0+512], [%1+512], 16;\n"
         " @p cp.async.cg.shared.global [%0+1024], [%1+1024], 16;\n"
-        "}\n" ::"r"(stage + 16 * lane), "l"(ph + 16 * lane), "r"((uint32_t)lane)
+        "}\n" ::"r"(stage), "l"(src), "r"((uint32_t)lane)
         : "memory");
   }
   asm volatile("cp.async.commit_group;" ::: "memory");
@@ -254,44 +257,46 @@ __global__ void __launch_bounds__(kDgThreads, kDigestCtasPerSm) digest_kernel(co
     return max((L + kPage - 1) / kPage - from_page(b), 0) * p.hkv;
   });
   if (w.begin >= w.end) return;
-  // the next item to fetch: head h of page `page` of sequence b, which has `end` pages
+  // the next item to fetch: a head of page `page` of sequence b, which has `end` pages
   int b = w.b, L = seq_tokens(p, b, false), page = from_page(b), end = (L + kPage - 1) / kPage;
   const int i = w.begin - w.first;
-  page += i / p.hkv;
-  int h = i % p.hkv, id = -1;  // id: of `page`, read at its first head
-  bool known = false;
-  int fetched = w.begin;
+  page += i / p.hkv - 1;
+  int heads = 0, skip = i % p.hkv;  // heads left of the page; heads of the first page that are another warp's
+  int row = 0, valid = 0;           // its row of the pool (below 0: the page is not there), its tokens
+  const uint8_t* src = nullptr;
+  int left = w.end - w.begin;
   const uint8_t* const ring = rings[threadIdx.x >> 5];
-  const uint32_t ring_u32 = smem_u32(ring);
-  // starts the next item's copy; returns its row of the pool (-1 for none) and its valid tokens
+  const uint32_t ring_u32 = smem_u32(ring) + 16 * lane;
+  // starts the next item's copy; returns its row of the pool (below 0 for none) and its valid tokens
   auto fetch = [&](int stage) -> int2 {
-    if (fetched == w.end) {
-      fetch_keys(0, nullptr, lane);
+    if (left == 0) {
+      fetch_keys(0, nullptr, false, lane);
       return make_int2(-1, 0);
     }
-    ++fetched;
-    while (page >= end) {  // the next sequence that has any
-      ++b;
-      L = seq_tokens(p, b, false);
-      page = from_page(b);
-      end = (L + kPage - 1) / kPage;
-    }
-    if (!known) {
-      id = p.page_table[(long long)b * p.max_pages + page];
-      if (id < 0 || id >= p.num_pages) {
-        if (lane == 0) flag_error(p.status, NVFP4KV_DEVERR_PAGE);
-        id = -1;
-      }
-      known = true;
-    }
-    const int row = id < 0 ? -1 : id * p.hkv + h, valid = min(L - page * kPage, kPage);
-    fetch_keys(ring_u32 + stage * kDgStageBytes, row < 0 ? nullptr : p.pages + (long long)row * kPageHeadBytes, lane);
-    if (++h == p.hkv) {
-      h = 0;
+    --left;
+    if (heads == 0) {
       ++page;
-      known = false;
+      while (page >= end) {  // the next sequence that has any
+        ++b;
+        L = seq_tokens(p, b, false);
+        page = from_page(b);
+        end = (L + kPage - 1) / kPage;
+      }
+      const int id = p.page_table[(long long)b * p.max_pages + page];
+      const bool there = id >= 0 && id < p.num_pages;
+      if (!there && lane == 0) flag_error(p.status, NVFP4KV_DEVERR_PAGE);
+      heads = p.hkv - skip;
+      row = there ? id * p.hkv + skip : INT_MIN;
+      src = p.pages + (long long)max(row, 0) * kPageHeadBytes + 16 * lane;
+      valid = min(L - page * kPage, kPage);
+      skip = 0;
     }
-    return make_int2(row, valid);
+    fetch_keys(ring_u32 + stage * kDgStageBytes, src, row >= 0, lane);
+    const int2 r = make_int2(row, valid);
+    --heads;
+    ++row;
+    src += kPageHeadBytes;
+    return r;
   };
   static_assert(kDgStages == 3, "the items under way have names");
   int2 now = fetch(0), next = fetch(1);
