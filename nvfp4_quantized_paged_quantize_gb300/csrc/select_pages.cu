@@ -203,7 +203,9 @@ __global__ void __launch_bounds__(kThreads, kCtas) select_kernel(const SelectArg
   // or by the block: it has fewer than `left` keys above it, and with its equals at least that
   auto rank = [&](auto of) {
     each([&](float v) {
-      if (of(v)) s.few[atomicAdd(&s.few_count, 1u)] = order_key(v);
+      if (!of(v)) return;
+      const uint32_t at = atomicAdd(&s.few_count, 1u);
+      if (at < kFew) s.few[at] = order_key(v);  // (always, unless the scores change meanwhile)
     });
     const uint32_t* few = s.few;
     if constexpr (kCluster) {
@@ -215,7 +217,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) select_kernel(const SelectArg
         here = ld_cluster(&s.few_count, from);
         if (tid < before + here) break;
       }
-      if (from < ctas) s.all_few[tid] = ld_cluster(&s.few[tid - before], from);
+      if (from < ctas && tid < kFew) s.all_few[tid] = ld_cluster(&s.few[tid - before], from);
       few = s.all_few;
     }
     __syncthreads();
@@ -275,7 +277,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) select_kernel(const SelectArg
     });
     lo += bin << shift;
     found = true;
-    width = 1u << shift;
+    width = min(1u << shift, hi - lo + 1);  // the last piece ends with the part: keys behind it are counted already
     if (shift == 0) {  // one key
       cut = lo;
     } else if (count == left) {  // the whole part stays
