@@ -42,7 +42,9 @@ class PerDeviceOnce {
 
 // Launches a kernel, in clusters of `cluster` blocks, whose blocks may take the places of
 // those of the kernel ahead of it on the stream as these leave (a programmatic dependent; the
-// kernel itself waits for that one's end: after_earlier_kernels).  Calls in a row, with it
+// kernel itself waits for that one's end: after_earlier_kernels).  That end comes after the
+// end of everything before it only if that kernel has waited in its turn: every programmatic
+// dependent of the library does, whatever its inputs, in one block at least.  Calls in a row, with it
 // and without: page scores 10.6 and 12.3 us, selection 7.0 and 9.0, selected decode 12.2
 // and 14.3.  (With the next kernel's blocks let in from the start, they take the free
 // places of some SMs and then run there unevenly: 11.4, 7.4 and 12.6.)
