@@ -679,10 +679,12 @@ int nvfp4kv_page_digest(const nvfp4kv_cache* cache, const int32_t* page_table, i
 /* nvfp4kv_page_scores: for every page p of sequence b and each KV head,
  *     scores[b][hk][p] = softmax_scale * g_K * scale * max over the head's G query heads
  *                        of sum_d max(q_d hi_d, q_d lo_d)
- * which no token's softmax_scale * q . khat in the page exceeds (but for fp32's
- * rounding).  cache gives the pool's size and g_K; its pages are not read.
- *   q             device bf16 [batch][num_q_heads][head_dim], 16-byte aligned; G <= 8 (a
- *                 NaN or an infinity in it leaves its KV head's scores undefined)
+ * which no token's softmax_scale * q . khat in the page exceeds (but for the rounding of
+ * fp32, and that of values below 2^-28 of their head's largest one, to multiples of at
+ * most 2^-38 of it).  cache gives the pool's size and g_K; its pages are not read.
+ *   q             device bf16 [batch][num_q_heads][head_dim], 16-byte aligned, of any
+ *                 finite size; G <= 8 (a NaN or an infinity in it leaves its KV head's
+ *                 scores undefined)
  *   scores        device fp32 [batch][num_kv_heads][score_stride]; entries behind a
  *                 sequence's last page are left alone.  A longer sequence's pages from
  *                 score_stride on get none, with NVFP4KV_DEVERR_LENGTH

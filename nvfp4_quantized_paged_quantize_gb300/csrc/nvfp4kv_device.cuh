@@ -135,6 +135,22 @@ __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
   return r;
 }
 
+// Powers of two up and down = 1 / up with up * amax in [2^14, 2^15), so that f16 holds
+// values of up to amax times up; amax finite (below 2^-112: up = 2^126, the products
+// 2^-23 and more).  All steps are exact but f16's own.
+struct F16Range {
+  float up, down;
+};
+__device__ __forceinline__ F16Range f16_range(float amax) {
+  int e = 0;
+  if (amax > 0.0f) {
+    const int ex = (int)((__float_as_uint(amax) >> 23) & 0xFF) - 127;  // floor(log2 amax) for normals
+    e = 14 - ex;  // -113 and more
+    e = e > 126 ? 126 : e;
+  }
+  return F16Range{__uint_as_float((uint32_t)(e + 127) << 23), __uint_as_float((uint32_t)(127 - e) << 23)};
+}
+
 // Correctly rounded a / b from r = RN(1 / b): q0 = RN(a r), then Markstein's
 // correction RN(q0 + r RN(a - b q0)) (two FMAs).  Valid while b, 1 / b and
 // the quotient stay well inside the normal range; the caller checks.

@@ -347,12 +347,12 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   return r;
 }
 
-// The queries of a pair as B fragments, and what their heads' products are
-// multiplied with.  Lane (g, t) holds head g's dimensions 16 t .. 16 t + 15 and
+// The queries of a pair as B fragments, and the powers of two that their heads' products
+// are multiplied with.  Lane (g, t) holds head g's dimensions 16 t .. 16 t + 15 and
 // 64 + 16 t ..: the order in which a digest's 16-byte pieces bring them.
 struct Queries {
   uint32_t pos[8][2], neg[8][2];
-  float c0, c1;  // heads 2 t, 2 t + 1
+  float down0, down1;  // heads 2 t, 2 t + 1
 };
 
 __device__ __forceinline__ void load_queries(const ScoreArgs& p, int pair, int lane, Queries& q) {
@@ -379,20 +379,17 @@ __device__ __forceinline__ void load_queries(const ScoreArgs& p, int pair, int l
   for (int j = 0; j < 32; ++j) amax = fmaxf(amax, fabsf(v[j]));
   amax = fmaxf(amax, __shfl_xor_sync(kAll, amax, 1));
   amax = fmaxf(amax, __shfl_xor_sync(kAll, amax, 2));
-  int e = 0;
-  if (amax > 0.0f) e = min(max(14 - ((int)((__float_as_uint(amax) >> 23) & 0xFF) - 127), -100), 100);
-  const float pre = __uint_as_float((uint32_t)(e + 127) << 23), inv = __uint_as_float((uint32_t)(127 - e) << 23);
+  const F16Range r = f16_range(amax);
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    const float a = v[4 * i] * pre, b = v[4 * i + 1] * pre, c = v[4 * i + 2] * pre, d = v[4 * i + 3] * pre;
+    const float a = v[4 * i] * r.up, b = v[4 * i + 1] * r.up, c = v[4 * i + 2] * r.up, d = v[4 * i + 3] * r.up;
     q.pos[i][0] = pack_f16x2(fmaxf(a, 0.0f), fmaxf(b, 0.0f));
     q.pos[i][1] = pack_f16x2(fmaxf(c, 0.0f), fmaxf(d, 0.0f));
     q.neg[i][0] = pack_f16x2(fminf(a, 0.0f), fminf(b, 0.0f));
     q.neg[i][1] = pack_f16x2(fminf(c, 0.0f), fminf(d, 0.0f));
   }
-  const float c = p.score_scale * inv;
-  q.c0 = __shfl_sync(kAll, c, 8 * t);
-  q.c1 = __shfl_sync(kAll, c, 8 * t + 4);
+  q.down0 = __shfl_sync(kAll, r.down, 8 * t);
+  q.down1 = __shfl_sync(kAll, r.down, 8 * t + 4);
 }
 
 // How a block goes through a sequence's pages: `together` KV heads at once, one per
@@ -577,21 +574,27 @@ __global__ void __launch_bounds__(kScThreads, kScoreCtasPerSm) scores_kernel(con
                    e4m3x2_to_f16x2(e[m] >> 16), f[0], f[1]);
         }
       }
-      const int r = g + 8 * t;  // lanes t = 0 and 1 write pages g and g + 8
-      const float unit = t < 2 ? *reinterpret_cast<const float*>(rows + r * k.stride + kOffScale) : 0.0f;
+      const float u0 = *reinterpret_cast<const float*>(rows + g * k.stride + kOffScale);
+      const float u1 = *reinterpret_cast<const float*>(rows + (g + 8) * k.stride + kOffScale);
       __syncwarp();
       if (lane == 0) arrive(empty + 8 * stage);
-      // the largest over the group's heads, 2 t and 2 t + 1 in this lane
-      const float c00 = 2 * t < p.group ? c[0] * q.c0 : -INFINITY, c01 = 2 * t + 1 < p.group ? c[1] * q.c1 : -INFINITY;
-      const float c10 = 2 * t < p.group ? c[2] * q.c0 : -INFINITY, c11 = 2 * t + 1 < p.group ? c[3] * q.c1 : -INFINITY;
+      // A sum times its page's unit, the scale, and its head's power of two, in this order: sums in
+      // units lie within 2^-50 .. 2^36, so that no step leaves fp32's normal numbers before the score does.
+      // The largest over the group's heads, 2 t and 2 t + 1 in this lane.
+      const bool first = 2 * t < p.group, second = 2 * t + 1 < p.group;
+      const float c00 = first ? c[0] * u0 * p.score_scale * q.down0 : -INFINITY;
+      const float c01 = second ? c[1] * u0 * p.score_scale * q.down1 : -INFINITY;
+      const float c10 = first ? c[2] * u1 * p.score_scale * q.down0 : -INFINITY;
+      const float c11 = second ? c[3] * u1 * p.score_scale * q.down1 : -INFINITY;
       float m0 = fmaxf(c00, c01), m1 = fmaxf(c10, c11);
 #pragma unroll
       for (int off = 1; off < 4; off <<= 1) {
         m0 = fmaxf(m0, __shfl_xor_sync(kAll, m0, off));
         m1 = fmaxf(m1, __shfl_xor_sync(kAll, m1, off));
       }
+      const int r = g + 8 * t;  // lanes t = 0 and 1 write pages g and g + 8
       if (t < 2 && r < mine_pages)
-        p.scores[(long long)pair * p.score_stride + at.page + stream * kTile + r] = (there >> r & 1) ? (t ? m1 : m0) * unit : -INFINITY;
+        p.scores[(long long)pair * p.score_stride + at.page + stream * kTile + r] = (there >> r & 1) ? (t ? m1 : m0) : -INFINITY;
     } else if (lane == 0) {
       arrive(empty + 8 * stage);
     }
