@@ -616,24 +616,16 @@ __device__ __forceinline__ void load_q(const DecodeParams& p, const QRaw& raw, W
   for (int j = 0; j < 32; ++j) amax = fmaxf(amax, fabsf(qv[j]));
   amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 1));
   amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 2));
-  // prescale 2^e so that amax * 2^e lies in [2^14, 2^15); e clamped to +-100
-  int e = 0;
-  if (amax > 0.0f) {
-    const int ex = (int)((__float_as_uint(amax) >> 23) & 0xFF) - 127;  // floor(log2 amax) for normals
-    e = 14 - ex;
-    e = e > 100 ? 100 : (e < -100 ? -100 : e);
-  }
-  const float pre = __uint_as_float((uint32_t)(e + 127) << 23);
-  const float inv = __uint_as_float((uint32_t)(127 - e) << 23);
+  const F16Range r = f16_range(amax);
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    s.qf[i][0] = pack_f16x2(qv[4 * i] * pre, qv[4 * i + 1] * pre);
-    s.qf[i][1] = pack_f16x2(qv[4 * i + 2] * pre, qv[4 * i + 3] * pre);
+    s.qf[i][0] = pack_f16x2(qv[4 * i] * r.up, qv[4 * i + 1] * r.up);
+    s.qf[i][1] = pack_f16x2(qv[4 * i + 2] * r.up, qv[4 * i + 3] * r.up);
   }
-  const float c = p.score_scale * inv;  // score multiplier of head g
+  const float c = fminf(p.score_scale * r.down, FLT_MAX);  // score multiplier of head g; finite: it may meet a zero
   if constexpr ((M & kCapped) != 0) {
     // finite: it may meet a zero (and anything else it makes far larger than 1 either way)
-    const float x = fminf(p.cap_scale * inv, FLT_MAX);
+    const float x = fminf(p.cap_scale * r.down, FLT_MAX);
     s.x0 = __shfl_sync(0xFFFFFFFFu, x, (2 * t) * 4);
     s.x1 = __shfl_sync(0xFFFFFFFFu, x, (2 * t + 1) * 4);
     s.c0 = s.c1 = p.score_scale;

@@ -1,14 +1,15 @@
-"""Queries of every finite size: the page scores against their reference, with
-tolerances as step_util derives them."""
+"""Queries of every finite size: the page scores and the decodes against their
+references, with tolerances as step_util and scored_util derive them."""
 import numpy as np
 import pytest
 import torch
 
+import oracle
 import nvfp4_quantized_paged_quantize_gb300 as kv
-from gpu_util import dev, status_word
-from scored_util import SCALE, page_tables, random_cache, random_q, sequence_rows
+from gpu_util import dev, pool_host, status_word
+from scored_util import SCALE, check, page_tables, random_cache, random_q, sequence_rows
 from step_util import e4m3_values, score_ref
-from test_gpu_page_selection import guarded_digest
+from test_gpu_page_selection import attend_ref, guarded_digest, random_lists, run_attend
 
 pytestmark = pytest.mark.gpu
 
@@ -46,3 +47,43 @@ def test_scores(cuda_lib, size, gk, softmax_scale, small):
                 r = raw[table[b, p], h]
                 want, tol = score_ref(heads, e4m3_values(r[:128]), e4m3_values(r[128:256]), r[256:260].view(np.float32)[0], factor)
                 assert abs(want) < 2.0 ** 127 and abs(got[b, h, p] - want) <= tol, (b, h, p, got[b, h, p], want)
+
+
+# keys' scales that bring the scores back to ordinary size, where the softmax tells them apart
+@pytest.mark.parametrize("size,gk", [(2.0 ** 113, 2.0 ** -113), (2.0 ** 118, 2.0 ** -118), (2.0 ** 124, 2.0 ** -123), (2.0 ** -80, 2.0 ** 80),
+                                     (2.0 ** -100, 2.0 ** 100), (2.0 ** -118, 2.0 ** 118)])
+def test_decodes(cuda_lib, size, gk):
+    lens, hkv, group = [700, 40, 16], 2, 5
+    table, used = page_tables(lens, 53)
+    cache, o = random_cache(used, hkv, 54, gk=gk, gv=0.25)
+    run_attend(cache, o, table, lens, hkv * group, random_lists(lens, hkv, 9, 55), 56, size=size)
+    q, q64 = random_q((len(lens), hkv * group, 128), 56, size)
+    pt, sl = dev(table), dev(np.asarray(lens, np.int32))
+    ws = torch.zeros(kv.nvfp4kv_decode_workspace_size(cache, len(lens), hkv * group), dtype=torch.uint8, device="cuda")
+    out, scored = torch.empty(q.shape, device="cuda"), torch.empty_like(q)
+    lse = torch.empty(q.shape[:2], device="cuda")
+    kv.nvfp4kv_decode_attention(cache, q, out, pt, sl, SCALE, ws)
+    kv.nvfp4kv_decode_attention_scored(cache, q, scored, pt, sl, SCALE, ws, lse=lse)
+    got = [x.double().cpu().numpy() for x in (out, scored, lse)]
+    for b, n in enumerate(lens):
+        for i in range(hkv * group):
+            r = attend_ref(o, table[b], i // group, n, range(-(-n // 16)), q64[b, i])
+            for x in got[:2]:
+                check(x[b, i], r["out"], r["tol_out"], f"{b} {i}")
+            check(got[2][b, i], r["lse"], r["tol_lse"], f"lse {b} {i}")
+
+
+def test_keys_of_zeros(cuda_lib):
+    # a multiplier past fp32's largest number meets scores of zero: equal weights
+    table, used = page_tables([100], 57)
+    cache, o = random_cache(used, 1, 58, gk=2.0 ** 20)
+    cache.k_scale.zero_()
+    o = oracle.Cache(used, 1, 128, 16, 2.0 ** 20, 1.0, arrays=pool_host(cache))
+    run_attend(cache, o, table, [100], 8, random_lists([100], 1, 4, 59), 60, size=2.0 ** 120)
+    q, _ = random_q((1, 8, 128), 60, 2.0 ** 120)
+    out = torch.empty(q.shape, device="cuda")
+    ws = torch.zeros(kv.nvfp4kv_decode_workspace_size(cache, 1, 8), dtype=torch.uint8, device="cuda")
+    kv.nvfp4kv_decode_attention(cache, q, out, dev(table), dev(np.array([100], np.int32)), SCALE, ws)
+    r = attend_ref(o, table[0], 0, 100, range(7), np.zeros(128))
+    for i in range(8):
+        check(out[0, i].double().cpu().numpy(), r["out"], r["tol_out"], f"{i}")
