@@ -3,6 +3,7 @@
 // memory or synchronises; every launch goes to the caller's stream.
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <atomic>
 #include <cmath>
 #include <cstdint>
@@ -468,7 +469,7 @@ int nvfp4kv_plan_append(int32_t* page_table, int32_t max_pages_per_seq, const in
   if (batch < 0 || max_pages_per_seq <= 0 || free_capacity < 0 || num_pages <= 0 || max_tokens < 0)
     return NVFP4KV_ERR_INVALID_ARGUMENT;
   if ((int64_t)max_pages_per_seq * kPageSize >= (int64_t(1) << 31) || max_tokens >= (int64_t(1) << 31) - (1 << 18) ||
-      num_pages * kPageSize >= (int64_t(1) << 31) || batch >= (1 << 30) || free_capacity > (1 << 30))
+      num_pages >= (int64_t(1) << 31) / kPageSize || batch >= (1 << 30) || free_capacity > (1 << 30))
     return NVFP4KV_ERR_UNSUPPORTED;
   if (!free_count || !free_left || (free_capacity > 0 && !free_pages) || (max_tokens > 0 && !slot_mapping))
     return NVFP4KV_ERR_INVALID_ARGUMENT;
@@ -518,6 +519,9 @@ int nvfp4kv_norm_rope_append(const nvfp4kv_cache* cache, const void* q, int64_t 
       num_tokens >= (int64_t(1) << 31) / (num_q_heads > cache->num_kv_heads ? num_q_heads : cache->num_kv_heads) ||
       q_stride > most || q_out_stride > most || k_stride > most || v_stride > most || total_rows > most)
     return NVFP4KV_ERR_UNSUPPORTED;
+  // byte offsets of the last tokens' rows fit 62 bits
+  const int64_t longest = std::max(std::max(q_stride, q_out_stride), std::max(k_stride, v_stride));
+  if (longest > (int64_t(1) << 60) / num_tokens) return NVFP4KV_ERR_UNSUPPORTED;
   if (!q || !k || !v || !slot_mapping || !q_out || (how->rotary_dim > 0 && (!positions || !cos_sin)))
     return NVFP4KV_ERR_INVALID_ARGUMENT;
   if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(q_out, 16) || !aligned(cos_sin, 16) ||
