@@ -306,9 +306,9 @@ __device__ __forceinline__ HalfBlocks quantize_halves(const uint32_t (&w)[8], co
 #pragma unroll
     for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fabsf(f[i]));
     amax = fmaxf(amax, __shfl_xor_sync(kAll, amax, 1));
-    const BlockScale b = block_scale(amax, gs);
+    const BlockScale b = block_scale<true>(amax, gs);
     uint32_t c[1];
-    block_codes(f, b, c);
+    block_codes<true>(f, amax, b, c);
     q.codes[h] = c[0];
     q.sb[h] = b.sb;
   }

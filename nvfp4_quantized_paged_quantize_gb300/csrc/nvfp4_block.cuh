@@ -35,6 +35,15 @@ struct BlockScale {
   bool fast;    // den, 1 / den and every quotient well inside the normal range
 };
 
+__device__ __forceinline__ void set_reciprocal(BlockScale& b, float amax) {
+  b.rcp = __frcp_rn(b.den);
+  b.fast = b.den >= 0x1p-100f && b.den <= 0x1p+100f && __fmul_rn(amax, b.rcp) < 0x1p+64f;
+}
+
+// kEarly: with its reciprocal, else block_codes makes it once the block is known not to be
+// zeros.  Early, the appends with FP8 rows take 0.3 % and the normed one 0.7 % less time;
+// the plain append takes 0.2 % less without.
+template <bool kEarly>
 __device__ __forceinline__ BlockScale block_scale(float amax, const GlobalScale& s) {
   // the block scale's quotient: Markstein while the first product stays far
   // from overflow (a quotient below 2^-11 encodes as 0 either way)
@@ -43,14 +52,13 @@ __device__ __forceinline__ BlockScale block_scale(float amax, const GlobalScale&
   BlockScale b;
   b.sb = e4m3_from_f32(sq);
   b.den = __fmul_rn(e4m3_to_f32(b.sb), s.g);
-  b.rcp = __frcp_rn(b.den);
-  b.fast = b.den >= 0x1p-100f && b.den <= 0x1p+100f && __fmul_rn(amax, b.rcp) < 0x1p+64f;
+  if constexpr (kEarly) set_reciprocal(b, amax);
   return b;
 }
 
 // The codes of 8 kWords of the block's values, value i in nibble i % 8 of word i / 8.
-template <int kWords>
-__device__ __forceinline__ void block_codes(const float* f, const BlockScale& b, uint32_t (&c)[kWords]) {
+template <bool kEarly, int kWords>
+__device__ __forceinline__ void block_codes(const float* f, float amax, BlockScale b, uint32_t (&c)[kWords]) {
   if (b.den == 0.0f) {
     // signed zeros: code 8 for negative inputs
 #pragma unroll
@@ -61,6 +69,7 @@ __device__ __forceinline__ void block_codes(const float* f, const BlockScale& b,
     }
     return;
   }
+  if constexpr (!kEarly) set_reciprocal(b, amax);
   float y[8 * kWords];
   if (b.fast) {
     // a quotient that rounds to zero can come out as +0 for negative x;
@@ -84,13 +93,14 @@ struct BlockCodes {
   uint32_t sb;      // E4M3 block scale
 };
 
+template <bool kEarly>
 __device__ __forceinline__ BlockCodes quantize_block(const float (&f)[16], const GlobalScale& s) {
   float amax = 0.0f;
 #pragma unroll
   for (int i = 0; i < 16; ++i) amax = fmaxf(amax, fabsf(f[i]));
-  const BlockScale b = block_scale(amax, s);
+  const BlockScale b = block_scale<kEarly>(amax, s);
   uint32_t c[2];
-  block_codes(f, b, c);
+  block_codes<kEarly>(f, amax, b, c);
   return BlockCodes{c[0], c[1], b.sb};
 }
 

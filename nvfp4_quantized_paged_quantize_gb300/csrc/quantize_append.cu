@@ -158,7 +158,7 @@ __global__ void __launch_bounds__(kThreads) quantize_append_kernel(QuantParams p
     float f[16];
     unpack_bf16x8(ca, f);
     unpack_bf16x8(cb, f + 8);
-    const BlockCodes codes = quantize_block(f, gs);
+    const BlockCodes codes = quantize_block<kWs>(f, gs);
     const uint32_t lo = codes.lo, hi = codes.hi, sb = codes.sb;
     // V: the other token of the pair (lane ^ 8 holds the same block of it);
     // every lane takes part in the exchange
