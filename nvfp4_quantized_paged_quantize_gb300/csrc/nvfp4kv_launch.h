@@ -170,7 +170,7 @@ struct PlanArgs {
   int32_t free_capacity;
   const int32_t* free_count;
   int64_t num_pages;
-  int64_t max_tokens;  // < 2^31
+  int64_t max_tokens;  // < 2^31 - 2^18: a thread's 32-bit token counter steps past it by up to 128 * 1024
   int32_t* seq_lens;      // may be cached_lens
   int64_t* slot_mapping;  // [max_tokens]
   int32_t* positions;     // [max_tokens], or null

@@ -14,7 +14,7 @@
 // lengths or the free count are updated in place, the CTAs are one cluster, with a
 // barrier between reading and writing them.
 // Bound by latency: a launch, the loads of the lengths, the sums, and for each token
-// two dependent loads and its stores.  256 requests of one token each 2.9 us, 16 of
+// two dependent loads and its stores.  256 requests of one token each 3.1 us, 16 of
 // 820 to 2048 2.9, in a captured graph (one block of 1024 threads with 64-bit sums:
 // 6.9 and, in a cluster of eight, 8.9: the instructions of its SM).
 #include "nvfp4kv_device.cuh"
@@ -188,12 +188,12 @@ __global__ void __launch_bounds__(kThreads) plan_kernel(const PlanArgs p, int ct
 }  // namespace
 
 cudaError_t launch_plan_append(const PlanArgs& args, cudaStream_t stream) {
-  // few requests: small blocks, whose barriers cost less (256 requests of one token 3.3 us, with
-  // 1024 threads 3.9; 300 in two rounds 5.0 and 4.1)
+  // few requests: small blocks, whose barriers cost less (256 requests of one token 3.1 us, with
+  // 1024 threads 3.6, 16 of up to 2048 2.9 and 3.8; but 300, two rounds of small blocks, 4.8 and 3.9)
   const bool small = args.batch <= 256;
   const int threads = small ? 256 : 1024;
   const bool in_place = args.seq_lens == args.cached_lens || args.free_left == args.free_count;
-  // (16 requests of up to 2048 tokens over 128 blocks 3.4 us, over 8 9.3)
+  // (16 requests of up to 2048 tokens over 128 blocks 2.9 us, over 8 8.9)
   const int64_t want = (args.max_tokens + threads - 1) / threads, most = in_place ? kPlanMaxCluster : 128;
   const int ctas = (int)(want < 1 ? 1 : want < most ? want : most);
   return launch_overlapped(small ? plan_kernel<256> : plan_kernel<1024>, ctas, threads, 0, in_place ? ctas : 1, stream,
