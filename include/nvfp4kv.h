@@ -669,6 +669,8 @@ int nvfp4kv_norm_rope_append(const nvfp4kv_cache* cache, const void* q, int64_t 
  *                 aligned, by page id as the cache is; other pages' are left alone
  *   first_tokens  device int32 [batch], or NULL: from the start.  After an append, the
  *                 sequence's length before it: the page that it falls into is made anew
+ * A digest knows only of the tokens that were there when it was made: pages that another
+ * call rewrites (an eviction packs into fresh ones) want theirs made anew.
  * Two sequences that share pages write the same bytes, if both see them whole.
  * A page id outside the pool is skipped with NVFP4KV_DEVERR_PAGE; a length outside the
  * page table is clamped with NVFP4KV_DEVERR_LENGTH. */
