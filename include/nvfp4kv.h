@@ -643,7 +643,8 @@ typedef struct nvfp4kv_norm_rope {
  *                 must not reach into that of q, and its rows must not overlap those of k or v
  *   ws_rows       device int64 [num_tokens], or NULL: no workspace (total_rows, the scales,
  *                 ws_k and ws_v are then not looked at)
- * num_tokens < 2^30, heads <= 2^20, num_tokens * heads < 2^31.  Values up to 2^60 in size have exact norms.  Enqueues
+ * num_tokens < 2^30, heads <= 2^20, num_tokens * heads < 2^31, strides <= 2^40 and
+ * num_tokens * stride <= 2^60.  Values up to 2^60 in size have exact norms.  Enqueues
  * one kernel. */
 int nvfp4kv_norm_rope_append(const nvfp4kv_cache* cache, const void* q, int64_t q_stride, const void* k,
                              int64_t k_stride, const void* v, int64_t v_stride, int32_t num_q_heads,
